@@ -150,8 +150,8 @@ def prepare(case, seed):
             key[torch.arange(T, **dev)[None] >= lens[:, None]] = 2.0
             pos = pos.gather(1, key.argsort(1))
         s["positions"] = pos.contiguous()
-        s["score_out"] = torch.zeros(R, T, **dev)
-        s["positions_out"] = torch.zeros(R, T, dtype=torch.int32, **dev)
+        s["score_out"] = torch.rand(R, T, generator=g, **dev)
+        s["positions_out"] = torch.full((R, T), -1, dtype=torch.int32, **dev)
         s["lens_out"] = torch.zeros(R, dtype=torch.int32, **dev)
         s["moves"] = (torch.zeros(R, case["budget"], dtype=torch.int32, **dev),
                       torch.zeros(R, case["budget"], dtype=torch.int32, **dev),
@@ -247,6 +247,8 @@ def _plain_evict(s, c):
     for name in ("score", "positions"):
         out = s[name + "_out"]
         out[:, :B] = torch.where(stay, s[name].gather(1, take), out[:, :B])
+    # The places that the request gives up start from 0 for the next token there.
+    s["score_out"].copy_(torch.where((idx >= new_lens) & live, 0.0, s["score_out"]))
     table = s["block_table"].long()
     dst = table.gather(1, idx[:, :B] // page) * page + idx[:, :B] % page
     frm = table.gather(1, take // page) * page + take % page
@@ -291,7 +293,7 @@ def exact(case, seed):
 def _exact_evict(s, case):
     score, pos = s["score"].cpu().numpy().astype(np.float64), s["positions"].cpu().numpy()
     nxt, B = s["next_pos"].cpu().numpy(), case["budget"]
-    score_out, pos_out = np.zeros_like(score), np.zeros_like(pos)
+    score_out, pos_out = s["score_out"].cpu().numpy().astype(np.float64), s["positions_out"].cpu().numpy()
     lens, moved = np.zeros(case["rows"], np.int32), np.zeros(case["rows"], np.int32)
     for r, n in enumerate(_lens(case)):
         order = np.arange(n)
@@ -303,6 +305,7 @@ def _exact_evict(s, case):
             order[holes] = np.sort(kept[kept >= B])
             moved[r] = len(holes)
         lens[r] = len(order)
+        score_out[r, len(order):n] = 0.0
         score_out[r, :len(order)], pos_out[r, :len(order)] = score[r][order], pos[r][order]
     return [lens, moved, score_out, pos_out, None] + ([] if s["v_cache"] is None else [None])
 
@@ -311,12 +314,13 @@ def work(case):
     R, d, lens = case["rows"], case["d"], _lens(case)
     if case["op"] == "evict":
         row = case["kv_heads"] * d * 2 * (1 if case["mla"] else 2)
-        # Scores and positions read once, the kept ones written once; the
+        # Scores and positions read once, the kept ones written once, the given
+        # up scores cleared; the
         # moved rows (as many as kept tokens lie behind the budget, taken as
         # spread evenly over the context) read and written once.
         B = case["budget"]
         moved = sum(-(-(n - B) * B // n) for n in lens if n > B)
-        return {"bytes": sum(8 * n + 8 * min(n, B) for n in lens) + 2 * row * moved, "flops": 0.0}
+        return {"bytes": sum(8 * n + 8 * min(n, B) + 4 * max(0, n - B) for n in lens) + 2 * row * moved, "flops": 0.0}
     if case["window"]:
         lens = [min(n, case["window"] + case["sinks"]) for n in lens]
     elt = 1 if case["dtype"] == "e4m3" else 2
