@@ -51,6 +51,11 @@ typedef struct CUstream_st* hs_stream_t; /* identical to cudaStream_t */
 #define HS_ERR_BAD_INDEX 6    /* device: an index outside its buffer, skipped */
 #define HS_ERR_UNSUPPORTED 7  /* a shape no kernel here implements            */
 
+/* Element types of the paged-cache entry points (hs_paged_decode). */
+#define HS_BF16 0
+#define HS_FP16 1
+#define HS_E4M3 2 /* OCP FP8 E4M3 codes */
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char* hs_status_string(int status);
 
@@ -502,6 +507,68 @@ int hs_sparse_decode_fp8ds(const void* q, const void* kv8, int64_t row_bytes,
                            int32_t rows, int32_t cap, int32_t heads, float scale, void* out,
                            float* lse, void* workspace, int64_t workspace_bytes_given,
                            int32_t* status, hs_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * hs_paged_decode -- attention of one new token per request over EVERY cached
+ * token of the request, read in place through the block table: the dense
+ * counterpart of hs_sparse_decode ([PA] 1.3 addressing, 1.4 split over the
+ * cache's length and combine; [PT] 3.1 eqs. (4)-(6), 3.2 eq. (7)).
+ *
+ *   x_t = scale * k_scale[g] * (q . K_t),   w = softmax_t(x),
+ *   out = v_scale[g] * sum_t w_t V_t,       lse = log sum_t exp(x_t)
+ *
+ * q           [rows, heads, d] of q_dtype (HS_BF16 / HS_FP16), heads packed,
+ *             requests q_stride elements apart.
+ * k, v        caches of kv_dtype: element (page p, place o in the page, KV
+ *             head g, dim i) at p * page_stride + o * row_stride + g *
+ *             head_stride + i (elements).  HS_BF16 / HS_FP16: the type of q;
+ *             HS_E4M3: either type of q.  Bases 16-byte aligned, strides and
+ *             q_stride multiples of 16 bytes.
+ * block_table int32 [rows, bt_stride]: logical block -> page, the first
+ *             max_blocks entries of a row at most.  Only entries of blocks
+ *             that hold an attended token are read.
+ * seq_lens    int32 [rows]: tokens T of the request, the new one included.
+ *             T <= 0: an unused slot (out = 0, lse = -inf).
+ * max_len     host-side bound on T, <= max_blocks * page_size (it sizes the
+ *             workspace); a longer request is attended up to max_len and
+ *             reported as HS_ERR_BAD_INDEX in *status.
+ * k_scale, v_scale  fp32 [kv_heads] or NULL (= 1); HS_E4M3 only.
+ * window      > 0: only positions [max(0, T - window), T) and the first
+ *             num_sinks positions are attended; 0: all.
+ * score       fp32 [rows, score_stride >= max_len] or NULL: running scores,
+ *             score[t] := score_decay * score[t] + sum over heads of w_t for
+ *             t < T (weights of positions outside the window are 0; with
+ *             score_decay 0 the old value is not read).  score[t >= T] is
+ *             left as it was.
+ * out         [rows, heads, d] of q_dtype, fp32 accumulated, rounded to
+ *             nearest even.   lse fp32 [rows, heads] natural log, or NULL.
+ * workspace   device scratch, 256-byte aligned, of at least
+ *             hs_paged_decode_workspace_bytes(..) bytes; needs no contents on
+ *             entry and keeps none.  Calls that may overlap need their own.
+ * status      int32 device word or NULL: HS_ERR_BAD_INDEX if an attended
+ *             token's page lies outside [0, num_pages) (the token is skipped,
+ *             never read).
+ * Tokens past T and skipped tokens are not read.  A request whose logits are
+ * all -inf gives out = 0 and lse = -inf.  Results do not depend on timing.
+ * Supported: d 64, 128 or 256, any heads / kv_heads; others (and scales with
+ * 16-bit caches, or caches of another 16-bit type than q) return
+ * HS_ERR_UNSUPPORTED.  rows <= 4096 (HS_ERR_CAPACITY above, or when the
+ * workspace is missing or too small).
+ * ------------------------------------------------------------------------- */
+int64_t hs_paged_decode_workspace_bytes(int32_t rows, int32_t heads, int32_t kv_heads, int32_t d,
+                                        int32_t max_len, int32_t window, int32_t num_sinks,
+                                        int32_t with_score);
+
+int hs_paged_decode(const void* q, int64_t q_stride, int32_t q_dtype, const void* k, const void* v,
+                    int32_t kv_dtype, int64_t page_stride, int64_t row_stride,
+                    int64_t head_stride, int32_t num_pages, int32_t page_size,
+                    const int32_t* block_table, int64_t bt_stride, int32_t max_blocks,
+                    int32_t max_len, const int32_t* seq_lens, const float* k_scale,
+                    const float* v_scale, int32_t rows, int32_t heads, int32_t kv_heads, int32_t d,
+                    int32_t window, int32_t num_sinks, float scale, float* score,
+                    int64_t score_stride, float score_decay, void* out, float* lse,
+                    void* workspace, int64_t workspace_bytes, int32_t* status,
+                    hs_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * hs_wait_selftest -- no counterpart on the pages: a test of the bounded

@@ -68,6 +68,10 @@ _SIGS = {
                           _P, _P, _P], ctypes.c_int),
     "hs_sparse_decode_fp8ds": ([_P, _P, _I64, _I64, _P, _P, _I32, _I32, _I32, _F32, _P, _P, _P,
                                 _I64, _P, _P], ctypes.c_int),
+    "hs_paged_decode_workspace_bytes": ([_I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32], _I64),
+    "hs_paged_decode": ([_P, _I64, _I32, _P, _P, _I32, _I64, _I64, _I64, _I32, _I32, _P, _I64,
+                         _I32, _I32, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _F32, _P,
+                         _I64, _F32, _P, _P, _P, _I64, _P, _P], ctypes.c_int),
 }
 
 NOALLOC_WORKSPACE_BYTES = 8 * 1024 * 1024  # HS_NOALLOC_WORKSPACE_BYTES
@@ -525,4 +529,123 @@ def sparse_decode_noalloc(q, k_base, v_base, row_stride, kv_head_stride, num_kv_
     _call("hs_sparse_decode_noalloc", _ptr(q), _ptr(k_base), _ptr(v_base), row_stride,
           kv_head_stride, num_kv_rows, _ptr(kv_rows), _ptr(count), rows, cap, heads, kv_heads,
           d_qk, d_v, float(scale), _ptr(out), _ptr(lse), _ptr(status), _stream(stream))
+    return out, lse
+
+
+# ---------------------------------------------------------------------------
+_ELEMENT = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}  # HS_BF16, ..
+
+
+def _check_cache(k_cache, v_cache):
+    """Paged caches [num_pages, page_size, kv_heads, d], any strides with
+    contiguous rows (a [pages, heads, page, d] cache is passed transposed)."""
+    if k_cache.dim() != 4 or k_cache.stride(3) != 1:
+        raise ValueError("k_cache: [num_pages, page_size, kv_heads, d] with contiguous rows")
+    if not k_cache.is_cuda:
+        raise ValueError("k_cache: must be a CUDA tensor")
+    if v_cache is not None:
+        if v_cache.dtype != k_cache.dtype or v_cache.device != k_cache.device:
+            raise TypeError("v_cache: the type and device of k_cache")
+        if v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride():
+            raise ValueError("v_cache: the shape and strides of k_cache")
+
+
+def _cache_strides(c):
+    """Page, row and head strides in elements; 0 for a dimension of one entry
+    (its stride is never used and may be anything)."""
+    return tuple(st if n > 1 else 0 for st, n in zip(c.stride()[:3], c.shape[:3]))
+
+
+def _check_rows(t, dtype, name, device, rows, cols=None):
+    """A tensor of `rows` leading entries (and `cols` columns at least, rows a
+    stride apart) on `device`."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if t.shape[0] != rows or t.dim() != (1 if cols is None else 2):
+        raise ValueError(f"{name}: expected {rows} rows, got shape {tuple(t.shape)}")
+    if cols is None:
+        if t.numel() > 1 and t.stride(0) != 1:
+            raise ValueError(f"{name}: must be contiguous")
+    elif t.shape[1] < cols or (t.shape[1] > 1 and t.stride(1) != 1) or (
+            rows > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name}: needs {cols} contiguous columns, its rows apart")
+
+
+def _check_out(t, dtype, name, device, shape):
+    if t.dtype != dtype or t.device != device:
+        raise TypeError(f"{name}: expected {dtype} on {device}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {tuple(shape)}")
+
+
+def paged_decode_workspace_bytes(rows, heads, kv_heads, d, max_len, *, window=0, num_sinks=0,
+                                 with_score=False):
+    return int(lib().hs_paged_decode_workspace_bytes(rows, heads, kv_heads, d, max_len, window,
+                                                     num_sinks, 1 if with_score else 0))
+
+
+def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, *, window=0, num_sinks=0,
+                 max_len=None, k_scale=None, v_scale=None, score=None, score_decay=1.0, out=None,
+                 lse=None, workspace=None, status=None, stream=None):
+    """One new token's attention over every cached token (hs_paged_decode).
+
+    q [rows, heads, d] bf16 or fp16 (heads packed, rows may be strided);
+    k_cache, v_cache [num_pages, page_size, kv_heads, d] of q's type or
+    float8_e4m3fn (then k_scale, v_scale fp32 [kv_heads] or None), same
+    strides; block_table int32 [rows, blocks]; seq_lens int32 [rows]; max_len
+    bounds seq_lens (default: what block_table and score hold).  score fp32 [rows, >=
+    max_len]: running scores, updated in place with the tokens' attention
+    weights summed over the heads.  Returns (out [rows, heads, d] of q's type,
+    lse fp32 [rows, heads])."""
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"q: expected torch.bfloat16 or torch.float16, got {q.dtype}")
+    if not q.is_cuda or q.device.index != torch.cuda.current_device():
+        raise ValueError("q: must be on the current CUDA device")
+    _check_cache(k_cache, v_cache)
+    if v_cache is None:
+        raise ValueError("v_cache: needed")
+    if k_cache.dtype not in _ELEMENT:
+        raise TypeError(f"k_cache: unsupported {k_cache.dtype}")
+    rows, heads, d = q.shape
+    num_pages, page_size, kv_heads, dc = k_cache.shape
+    dev = q.device
+    if dc != d or k_cache.device != dev:
+        raise ValueError("k_cache: head size and device of q")
+    if rows and (q.stride(2) != 1 or q.stride(1) != d):
+        raise ValueError("q: heads must be packed")
+    _check_rows(block_table, torch.int32, "block_table", dev, rows, 0)
+    blocks = block_table.shape[1]
+    if max_len is None:
+        max_len = blocks * page_size
+        if score is not None and score.dim() == 2:
+            max_len = min(max_len, score.shape[1])
+    _check_rows(seq_lens, torch.int32, "seq_lens", dev, rows)
+    _check_rows(score, torch.float32, "score", dev, rows, max_len)
+    _check_rows(k_scale, torch.float32, "k_scale", dev, kv_heads)
+    _check_rows(v_scale, torch.float32, "v_scale", dev, kv_heads)
+    _check(status, torch.int32, "status")
+    if out is None:
+        out = torch.empty(rows, heads, d, dtype=q.dtype, device=dev)
+    else:
+        _check_out(out, q.dtype, "out", dev, (rows, heads, d))
+    if lse is None:
+        lse = torch.empty(rows, heads, dtype=torch.float32, device=dev)
+    else:
+        _check_out(lse, torch.float32, "lse", dev, (rows, heads))
+    ws = int(lib().hs_paged_decode_workspace_bytes(rows, heads, kv_heads, d, max_len, window,
+                                                   num_sinks, 0 if score is None else 1))
+    if workspace is None or workspace.numel() * workspace.element_size() < ws:
+        workspace = torch.empty(max(ws, 1), dtype=torch.uint8, device=dev)
+    ps, rs, hstr = _cache_strides(k_cache)
+    _call("hs_paged_decode", _ptr(q), q.stride(0) if rows > 1 else heads * d, _ELEMENT[q.dtype], _ptr(k_cache),
+          _ptr(v_cache), _ELEMENT[k_cache.dtype], ps, rs, hstr, num_pages, page_size,
+          _ptr(block_table), block_table.stride(0), blocks, max_len, _ptr(seq_lens),
+          _ptr(k_scale), _ptr(v_scale), rows, heads, kv_heads, d, window, num_sinks,
+          float(scale), _ptr(score), 0 if score is None else score.stride(0),
+          float(score_decay), _ptr(out), _ptr(lse), _ptr(workspace),
+          workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream))
     return out, lse
