@@ -571,6 +571,77 @@ int hs_paged_decode(const void* q, int64_t q_stride, int32_t q_dtype, const void
                     hs_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * hs_evict -- eviction to a budget by running attention scores (the `score`
+ * of hs_paged_decode; no counterpart on the pages).  Request r holds T =
+ * seq_lens[r] tokens in its places 0 .. T-1 (place i: block_table[r][i /
+ * page_size], i % page_size).  If T > budget it keeps `budget` of them, the
+ * first in the order
+ *   protected tokens, then higher score, then lower place,
+ * where a token is protected if its position is below num_sinks or at least
+ * next_pos[r] - recent.  Scores order as numbers, NaN below all.  Kept tokens
+ * below place `budget` stay where they are; the others move into the holes,
+ * the j-th such token (by place) into the j-th hole.  No source is a
+ * destination, so the moves may run in any order, and repeating them changes
+ * nothing.  The places from `budget` on are then free.
+ *
+ * hs_evict_select: which tokens stay, and the state that goes with them.
+ * score       fp32 [rows, score_stride].
+ * positions   int32 [rows, pos_stride]: position of the token in each place
+ *             (moved tokens stand out of order), or NULL: the place itself.
+ * next_pos    int32 [rows]: one more than the newest position, or NULL: T.
+ * max_len     host-side bound on T (strides are at least max_len); a longer
+ *             request counts as max_len tokens and is reported as
+ *             HS_ERR_BAD_INDEX in *status.  T <= 0: an unused slot.
+ * recent, num_sinks  recent + num_sinks <= budget.
+ * score_out   fp32 [rows, score_out_stride], may be `score`: the kept
+ *             tokens' scores at their new places; 0 in the places given up
+ *             ([budget, T)), so that a token written there starts from 0.
+ * positions_out  int32 [rows, pos_out_stride] or NULL, may be `positions`:
+ *             likewise; places given up are left as they were, except
+ *             nothing at or behind T is ever touched.
+ * lens_out    int32 [rows], may be `seq_lens`: min(T, budget).
+ * move_src, move_dst  int32 [rows, cap] places of the moves; only the first
+ *             move_count[r] are written.  cap >= min(budget, max_len -
+ *             budget) (HS_ERR_CAPACITY).   move_count int32 [rows].
+ * Out arrays must not overlap in arrays other than as stated.  Bit-exact and
+ * independent of thread scheduling.
+ *
+ * hs_evict_move: row move_src[r][j] -> move_dst[r][j] of a paged cache, every
+ * KV head (row_bytes each), for j < move_count[r].  Call it for each layer's
+ * caches that share the lists.
+ * k, v        caches (v NULL: one cache, as for latent rows); strides in
+ *             BYTES, multiples of 16 like row_bytes; 16-byte aligned.
+ * A move whose page lies outside [0, num_pages) is skipped and reported as
+ * HS_ERR_BAD_INDEX.  The pages written must not be shared with another
+ * request.
+ *
+ * hs_evict: hs_evict_select, then hs_evict_move with its lists.
+ * ------------------------------------------------------------------------- */
+int hs_evict_select(const float* score, int64_t score_stride, const int32_t* positions,
+                    int64_t pos_stride, const int32_t* seq_lens, const int32_t* next_pos,
+                    int32_t rows, int32_t max_len, int32_t budget, int32_t recent,
+                    int32_t num_sinks, float* score_out, int64_t score_out_stride,
+                    int32_t* positions_out, int64_t pos_out_stride, int32_t* lens_out,
+                    int32_t* move_src, int32_t* move_dst, int32_t* move_count, int32_t cap,
+                    int32_t* status, hs_stream_t stream);
+
+int hs_evict_move(void* k, void* v, int64_t page_stride, int64_t row_stride, int64_t head_stride,
+                  int32_t kv_heads, int32_t row_bytes, int32_t num_pages, int32_t page_size,
+                  const int32_t* block_table, int64_t bt_stride, int32_t max_blocks,
+                  const int32_t* move_src, const int32_t* move_dst, const int32_t* move_count,
+                  int32_t rows, int32_t cap, int32_t* status, hs_stream_t stream);
+
+int hs_evict(const float* score, int64_t score_stride, const int32_t* positions,
+             int64_t pos_stride, const int32_t* seq_lens, const int32_t* next_pos, int32_t rows,
+             int32_t max_len, int32_t budget, int32_t recent, int32_t num_sinks, float* score_out,
+             int64_t score_out_stride, int32_t* positions_out, int64_t pos_out_stride,
+             int32_t* lens_out, int32_t* move_src, int32_t* move_dst, int32_t* move_count,
+             int32_t cap, void* k, void* v, int64_t page_stride, int64_t row_stride,
+             int64_t head_stride, int32_t kv_heads, int32_t row_bytes, int32_t num_pages,
+             int32_t page_size, const int32_t* block_table, int64_t bt_stride, int32_t max_blocks,
+             int32_t* status, hs_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * hs_wait_selftest -- no counterpart on the pages: a test of the bounded
  * wait that every mbarrier wait of this library goes through (a wait that
  * cannot complete reports an error instead of hanging).  One CTA waits on an

@@ -72,6 +72,13 @@ _SIGS = {
     "hs_paged_decode": ([_P, _I64, _I32, _P, _P, _I32, _I64, _I64, _I64, _I32, _I32, _P, _I64,
                          _I32, _I32, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _F32, _P,
                          _I64, _F32, _P, _P, _P, _I64, _P, _P], ctypes.c_int),
+    "hs_evict_select": ([_P, _I64, _P, _I64, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _I64, _P,
+                         _I64, _P, _P, _P, _P, _I32, _P, _P], ctypes.c_int),
+    "hs_evict_move": ([_P, _P, _I64, _I64, _I64, _I32, _I32, _I32, _I32, _P, _I64, _I32, _P, _P,
+                       _P, _I32, _I32, _P, _P], ctypes.c_int),
+    "hs_evict": ([_P, _I64, _P, _I64, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _I64, _P, _I64,
+                  _P, _P, _P, _P, _I32, _P, _P, _I64, _I64, _I64, _I32, _I32, _I32, _I32, _P,
+                  _I64, _I32, _P, _P], ctypes.c_int),
 }
 
 NOALLOC_WORKSPACE_BYTES = 8 * 1024 * 1024  # HS_NOALLOC_WORKSPACE_BYTES
@@ -643,9 +650,111 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, *, window=0,
     ps, rs, hstr = _cache_strides(k_cache)
     _call("hs_paged_decode", _ptr(q), q.stride(0) if rows > 1 else heads * d, _ELEMENT[q.dtype], _ptr(k_cache),
           _ptr(v_cache), _ELEMENT[k_cache.dtype], ps, rs, hstr, num_pages, page_size,
-          _ptr(block_table), block_table.stride(0), blocks, max_len, _ptr(seq_lens),
+          _ptr(block_table), _row_stride(block_table), blocks, max_len, _ptr(seq_lens),
           _ptr(k_scale), _ptr(v_scale), rows, heads, kv_heads, d, window, num_sinks,
-          float(scale), _ptr(score), 0 if score is None else score.stride(0),
+          float(scale), _ptr(score), _row_stride(score),
           float(score_decay), _ptr(out), _ptr(lse), _ptr(workspace),
           workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream))
     return out, lse
+
+
+def _evict_args(score, seq_lens, budget, max_len, recent, num_sinks, positions, next_pos,
+                score_out, positions_out, lens_out, moves, status):
+    """Checked arguments of hs_evict_select, and what evict_select returns."""
+    if not score.is_cuda or score.device.index != torch.cuda.current_device():
+        raise ValueError("score: must be on the current CUDA device")
+    if score.dim() != 2:
+        raise ValueError("score: [rows, tokens]")
+    dev, rows = score.device, score.shape[0]
+    if max_len is None:
+        max_len = score.shape[1]
+    _check_rows(score, torch.float32, "score", dev, rows, max_len)
+    _check_rows(positions, torch.int32, "positions", dev, rows, max_len)
+    _check_rows(seq_lens, torch.int32, "seq_lens", dev, rows)
+    _check_rows(next_pos, torch.int32, "next_pos", dev, rows)
+    score_out = score if score_out is None else score_out
+    positions_out = positions if positions_out is None else positions_out
+    lens_out = seq_lens if lens_out is None else lens_out
+    _check_rows(score_out, torch.float32, "score_out", dev, rows, max_len)
+    _check_rows(positions_out, torch.int32, "positions_out", dev, rows, max_len)
+    _check_rows(lens_out, torch.int32, "lens_out", dev, rows)
+    if moves is None:
+        cap = max(0, min(budget, max_len - budget))
+        moves = (torch.empty(rows, cap, dtype=torch.int32, device=dev),
+                 torch.empty(rows, cap, dtype=torch.int32, device=dev),
+                 torch.empty(rows, dtype=torch.int32, device=dev))
+    src, dst, count = moves
+    cap = src.shape[1]
+    _check_out(src, torch.int32, "moves[0]", dev, (rows, cap))
+    _check_out(dst, torch.int32, "moves[1]", dev, (rows, cap))
+    _check_out(count, torch.int32, "moves[2]", dev, (rows,))
+    _check(status, torch.int32, "status")
+    args = (_ptr(score), _row_stride(score), _ptr(positions), _row_stride(positions),
+            _ptr(seq_lens), _ptr(next_pos), rows, max_len, budget, recent, num_sinks,
+            _ptr(score_out), _row_stride(score_out), _ptr(positions_out),
+            _row_stride(positions_out), _ptr(lens_out), _ptr(src), _ptr(dst), _ptr(count), cap)
+    return args, (score_out, positions_out, lens_out, moves)
+
+
+def _row_stride(t):
+    """Elements between the rows of a 2-D tensor (its width for a single row)."""
+    if t is None:
+        return 0
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _move_args(k_cache, v_cache, block_table, rows, device):
+    _check_cache(k_cache, v_cache)
+    if k_cache.device != device:
+        raise ValueError(f"k_cache: on {k_cache.device}, expected {device}")
+    _check_rows(block_table, torch.int32, "block_table", device, rows, 0)
+    num_pages, page_size, kv_heads, d = k_cache.shape
+    e = k_cache.element_size()
+    ps, rs, hstr = _cache_strides(k_cache)
+    return (_ptr(k_cache), _ptr(v_cache), ps * e, rs * e, hstr * e, kv_heads, d * e, num_pages,
+            page_size, _ptr(block_table), _row_stride(block_table), block_table.shape[1])
+
+
+def evict_select(score, seq_lens, budget, *, max_len=None, recent=0, num_sinks=0, positions=None,
+                 next_pos=None, score_out=None, positions_out=None, lens_out=None, moves=None,
+                 status=None, stream=None):
+    """Which tokens a request over its budget keeps (hs_evict_select).
+
+    score fp32 [rows, >= max_len]; seq_lens int32 [rows]; positions int32
+    [rows, >= max_len] or None; next_pos int32 [rows] or None; max_len
+    defaults to score's width.  score_out, positions_out and lens_out default
+    to the inputs (updated in place).  Returns (score_out, positions_out,
+    lens_out, (move_src, move_dst int32 [rows, cap], move_count int32
+    [rows]))."""
+    args, result = _evict_args(score, seq_lens, budget, max_len, recent, num_sinks, positions,
+                               next_pos, score_out, positions_out, lens_out, moves, status)
+    _call("hs_evict_select", *args, _ptr(status), _stream(stream))
+    return result
+
+
+def evict_move(moves, k_cache, v_cache, block_table, *, status=None, stream=None):
+    """Apply evict_select's moves to a paged cache [num_pages, page_size,
+    kv_heads, d] of any type (v_cache None: one cache) (hs_evict_move)."""
+    src, dst, count = moves
+    rows, cap = src.shape
+    dev = src.device
+    if not src.is_cuda or dev.index != torch.cuda.current_device():
+        raise ValueError("moves: must be on the current CUDA device")
+    _check_out(src, torch.int32, "moves[0]", dev, (rows, cap))
+    _check_out(dst, torch.int32, "moves[1]", dev, (rows, cap))
+    _check_out(count, torch.int32, "moves[2]", dev, (rows,))
+    _check(status, torch.int32, "status")
+    _call("hs_evict_move", *_move_args(k_cache, v_cache, block_table, rows, dev), _ptr(src),
+          _ptr(dst), _ptr(count), rows, cap, _ptr(status), _stream(stream))
+
+
+def evict(score, seq_lens, budget, k_cache, v_cache, block_table, *, max_len=None, recent=0,
+          num_sinks=0, positions=None, next_pos=None, score_out=None, positions_out=None,
+          lens_out=None, moves=None, status=None, stream=None):
+    """evict_select, then evict_move on one layer's caches (hs_evict); same
+    arguments and result as evict_select."""
+    args, result = _evict_args(score, seq_lens, budget, max_len, recent, num_sinks, positions,
+                               next_pos, score_out, positions_out, lens_out, moves, status)
+    _call("hs_evict", *args, *_move_args(k_cache, v_cache, block_table, score.shape[0],
+                                         score.device), _ptr(status), _stream(stream))
+    return result

@@ -46,3 +46,49 @@ def test_paged_decode_workspace_query():
     assert f(2, 8, 2, 128, 100000, window=64, num_sinks=4, with_score=True) < f(
         2, 8, 2, 128, 100000, with_score=True)
     assert f(-1, 8, 2, 128, 10) == -1 and f(1, 9, 2, 128, 10) == -1 and f(0, 8, 2, 128, 10) == 0
+
+
+SELECT = dict(score=P, score_stride=64, positions=None, pos_stride=0, lens=P, next_pos=None,
+              rows=2, max_len=64, budget=32, recent=4, sinks=2, score_out=P, score_out_stride=64,
+              positions_out=None, pos_out_stride=0, lens_out=P, src=P, dst=P, count=P, cap=32,
+              status=None, stream=None)
+MOVE = dict(k=P, v=None, page_stride=4096, row_stride=256, head_stride=128, kv_heads=2,
+            row_bytes=128, num_pages=4, page_size=16, table=P, bt_stride=4, max_blocks=4, src=P,
+            dst=P, count=P, rows=2, cap=32, status=None, stream=None)
+SELECT_BAD = [
+    (1, dict(rows=-1)), (1, dict(max_len=-1)), (1, dict(budget=0)), (1, dict(recent=-1)),
+    (1, dict(sinks=-1)), (1, dict(recent=31)), (1, dict(cap=-1)), (3, dict(cap=31)),
+    (1, dict(score=None)), (1, dict(lens=None)), (1, dict(score_out=None)),
+    (1, dict(lens_out=None)), (1, dict(src=None)), (1, dict(dst=None)), (1, dict(count=None)),
+    (1, dict(score_stride=63)), (1, dict(score_out_stride=63)),
+    (1, dict(positions=P, pos_stride=10)), (1, dict(positions_out=P, pos_out_stride=10)),
+    (1, dict(score_out_stride=80))]
+ODD2 = ctypes.c_void_p(P.value + 2)
+
+
+@pytest.mark.parametrize("code,kw", SELECT_BAD + [(2, dict(score=ODD2, score_out=ODD2)),
+                                                  (2, dict(lens=ODD2)), (0, dict(rows=0))])
+def test_evict_select_checks(code, kw):
+    assert hs.lib().hs_evict_select(*{**SELECT, **kw}.values()) == code
+
+
+MOVE_BAD = [
+    (1, dict(rows=-1)), (1, dict(kv_heads=0)), (1, dict(row_bytes=0)), (1, dict(page_size=0)),
+    (1, dict(num_pages=-1)), (1, dict(max_blocks=-1)), (1, dict(page_stride=-16)),
+    (1, dict(k=None)), (1, dict(table=None)), (1, dict(v=P)), (2, dict(row_bytes=100)),
+    (2, dict(head_stride=100)), (2, dict(row_stride=264)), (2, dict(k=ODD)), (2, dict(v=ODD)),
+    (1, dict(kv_heads=1 << 20, row_bytes=4096))]
+
+
+@pytest.mark.parametrize("code,kw", MOVE_BAD + [(1, dict(src=None)), (1, dict(count=None)),
+                                                (0, dict(rows=0)), (0, dict(cap=0))])
+def test_evict_move_checks(code, kw):
+    assert hs.lib().hs_evict_move(*{**MOVE, **kw}.values()) == code
+
+
+@pytest.mark.parametrize("code,kw", SELECT_BAD + MOVE_BAD + [(1, dict(max_blocks=3)),
+                                                             (0, dict(rows=0))])
+def test_evict_checks(code, kw):
+    a = {k: v for k, v in SELECT.items() if k not in ("status", "stream")}
+    b = {k: v for k, v in MOVE.items() if k not in ("src", "dst", "count", "rows", "cap")}
+    assert hs.lib().hs_evict(*{**a, **b, **kw}.values()) == code
