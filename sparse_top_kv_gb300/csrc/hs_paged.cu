@@ -1,11 +1,75 @@
 // hs_paged.cu -- hs_paged_decode: argument checks, workspace layout, the
 // merge of split contexts and the running attention scores.  The attention
 // kernel itself is in hs_paged_core.cuh.
+#include <cuda.h>
+
+#include <atomic>
+
 #include "hs_paged.cuh"
 
 namespace hs_paged {
 
+namespace tc {
+
+// The driver's tensor map encoder (a host-side function; no link to libcuda).
+using Encode = decltype(&cuTensorMapEncodeTiled);
+Encode encoder() {
+    static std::atomic<Encode> fn{nullptr};
+    Encode f = fn.load(std::memory_order_acquire);
+    if (f != nullptr) return f;
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult res = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &res) != cudaSuccess ||
+        res != cudaDriverEntryPointSuccess || p == nullptr) {
+        cudaGetLastError();
+        return nullptr;
+    }
+    f = reinterpret_cast<Encode>(p);
+    fn.store(f, std::memory_order_release);
+    return f;
+}
+
+int encode_map(CUtensorMap* m, int kv, const void* base, const PagedArgs& a, int d, int bt,
+               int hs_box) {
+    const Encode f = encoder();
+    if (f == nullptr) return HS_ERR_CUDA;
+    const cuuint64_t elt = kv == HS_E4M3 ? 1 : 2;
+    // A dimension of one entry may have any stride; the encoder wants a valid one.
+    const auto bytes = [&](int64_t stride, int64_t n) {
+        return n > 1 ? cuuint64_t(stride) * elt : cuuint64_t(d) * elt;
+    };
+    const cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(a.page_size), cuuint64_t(a.kv_heads),
+                                cuuint64_t(a.num_pages)};
+    const cuuint64_t strides[3] = {bytes(a.row_stride, a.page_size),
+                                   bytes(a.head_stride, a.kv_heads),
+                                   bytes(a.page_stride, a.num_pages)};
+    const cuuint32_t box[4] = {cuuint32_t(128 / elt), cuuint32_t(bt), cuuint32_t(hs_box), 1u};
+    const cuuint32_t one[4] = {1u, 1u, 1u, 1u};
+    const CUtensorMapDataType type = kv == HS_BF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                     : kv == HS_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                     : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const CUresult r =
+        f(m, type, 4, const_cast<void*>(base), dims, strides, box, one,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? HS_OK : HS_ERR_CUDA;
+}
+
+}  // namespace tc
+
 namespace {
+
+// The tensor-core kernel takes caches whose boxes of 16 tokens and more lie
+// inside a page and whose rows fill 128-byte blocks; others (small or odd
+// pages, E4M3 heads of 64 bytes, broadcast strides) run on warp-level MMAs.
+bool tensor_map_ok(const PagedArgs& a, int kv_dtype, int d) {
+    const int64_t most = int64_t(1) << 38;  // elements; the encoder takes strides below 2^40 bytes
+    return a.page_size % 16 == 0 && !(kv_dtype == HS_E4M3 && d == 64) && a.num_pages > 0 &&
+           (a.kv_heads == 1 || (a.head_stride > 0 && a.head_stride < most)) &&
+           (a.num_pages == 1 || (a.page_stride > 0 && a.page_stride < most)) &&
+           a.row_stride > 0 && a.row_stride < most;
+}
 
 constexpr int kMergeThreads = 256;
 constexpr int kScoreThreads = 128;
@@ -304,7 +368,11 @@ extern "C" int hs_paged_decode(const void* q, int64_t q_stride, int32_t q_dtype,
     a.ctas = w.ctas;
     a.status = status;
     int rc;
-    if (kv_dtype == HS_BF16) rc = launch_bf16(a, d, group, stream);
+    if (tensor_map_ok(a, kv_dtype, d)) {
+        if (kv_dtype == HS_BF16) rc = launch_tc_bf16(a, d, group, stream);
+        else if (kv_dtype == HS_FP16) rc = launch_tc_fp16(a, d, group, stream);
+        else rc = launch_tc_e4m3(a, d, group, stream);
+    } else if (kv_dtype == HS_BF16) rc = launch_bf16(a, d, group, stream);
     else if (kv_dtype == HS_FP16) rc = launch_fp16(a, d, group, stream);
     else rc = launch_e4m3(a, d, group, stream);
     if (rc != HS_OK) return rc;

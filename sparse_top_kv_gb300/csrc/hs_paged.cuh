@@ -87,5 +87,8 @@ __device__ __forceinline__ int run_of(const Plan& p, int64_t tile) {
 int launch_bf16(const PagedArgs& a, int d, int group, hs_stream_t stream);
 int launch_fp16(const PagedArgs& a, int d, int group, hs_stream_t stream);
 int launch_e4m3(const PagedArgs& a, int d, int group, hs_stream_t stream);
+int launch_tc_bf16(const PagedArgs& a, int d, int group, hs_stream_t stream);
+int launch_tc_fp16(const PagedArgs& a, int d, int group, hs_stream_t stream);
+int launch_tc_e4m3(const PagedArgs& a, int d, int group, hs_stream_t stream);
 
 }  // namespace hs_paged

@@ -1,0 +1,1054 @@
+// hs_paged_tc.cuh -- the attention kernel of hs_paged_decode on the 5th-
+// generation tensor cores, fed by TMA (included by one translation unit per
+// cache type; pages of a multiple of 16 tokens, rows of 128 bytes and more).
+//
+// Math, per request and query head h of KV head g, over the visible tokens:
+//   x_t = scale * k_scale_g * (q_h . K_t),  p_t = 2^((x_t - m) log2 e),
+//   l = sum p_t,  out_h = v_scale_g / l * sum p_t V_t,
+// as (m, l, sum) states, exact under merging (the rule of hs_merge_states).
+//
+// The operator reads every cached byte once and does 4 * (query heads per KV
+// head) flops with an element, so HBM bounds it; everything here serves to
+// keep TMA loads in flight without a pause.
+//  * A tile is 128 cache rows: hs KV heads x 128 / hs tokens, so that one TMA
+//    box takes all heads of a run of tokens and DRAM is read in long pieces
+//    (reading one head's 256 bytes of a token at a time measured half the
+//    rate).  Rows of a tile: [run of bt tokens][head][token of the run].
+//  * One elected lane per run issues the boxes into a K ring and a V ring in
+//    128-byte-swizzled blocks; the loads run ahead over the ends of units.
+//  * S^T[128 rows x queries] = K Q^T takes the queries of all hs heads as N;
+//    only the entries where the row's head is the query's own are used.  The
+//    rest is wasted work that the tensor cores have to spare.
+//  * Softmax: one thread per row, against a reference maximum that moves only
+//    when a logit exceeds it by 2^8 (a vote), so the common tile needs no
+//    reduction; exponent sums stay per thread until the unit ends.  A tile's
+//    softmax is one chain of dependent steps (1.9 us, longer than its loads),
+//    so two groups of four warps take the tiles in turn, each with its own
+//    maximum, sums and output accumulators, joined when the unit ends.
+//  * O^T[D x queries] += V^T P^T, V as an MN-major view of its tile, K = the
+//    16 (E4M3: 32) rows of one head, one accumulator per head.  P is carried
+//    as several parts in columns of their own: a bf16 or fp16 value and the
+//    rounding's remainder, so weights keep twice the operand's precision.
+//  * E4M3 caches are multiplied as they are (kind::f8f6f4): the query, scaled
+//    by a power of two, becomes three E4M3 parts (each the rounding of 16
+//    times the remainder before it), P four; each part has columns of its own
+//    and the parts are summed in fp32 with their weights 16^-i.
+// Every wait is bounded (HS_ERR_TIMEOUT in the status word on expiry).
+#pragma once
+
+#include <cuda.h>
+
+#include "hs_paged.cuh"
+#include "hs_pair.cuh"
+#include "hs_tcgen05.cuh"
+
+namespace hs_paged {
+namespace tc {
+
+enum Kind { kBf16 = 0, kFp16 = 1, kE4m3 = 2 };
+
+constexpr int kRows = 128;           // cache rows of a tile = M of the QK product
+constexpr int kBlk = kRows * 128;    // one block: 128 rows x 128 bytes
+constexpr int kSoftThreads = 128;    // one softmax group: a thread per row
+constexpr int kGroups = 2;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kQWarp = 10;
+constexpr int kQThreads = 64;
+constexpr int kThreads = 384;
+constexpr int kSoftBar = 1;          // named barriers of the groups: 1, 2
+constexpr int kBothBar = 3;          // and of both
+constexpr int kMaskRing = 16;        // tiles whose loaded runs are remembered
+constexpr float kThresh = 8.f;       // log2 headroom before O is rescaled
+constexpr int kTmemCols = 512;
+constexpr int kBarBytes = 8192;      // shared-memory budget of Bars
+
+// Two ways to cut a unit: all heads that a tile can hold (long DRAM pieces),
+// or one head per unit (small problems: more tokens per tile, fewer parts to
+// merge).  The kernel takes one by the amount of work it finds.
+struct TcArgs {
+    PagedArgs p;
+    int32_t hs[2], bt[2];
+    int32_t steps_for_wide;  // tiles per CTA from which the first way is taken
+    uint64_t timeout_ns;
+};
+
+template <int KV, int D, int GH>
+struct Cfg {
+    static constexpr bool kE4 = KV == kE4m3;
+    static constexpr int GM = 8 * GH;                    // query heads per KV head and unit
+    static constexpr int kElt = kE4 ? 1 : 2;
+    static constexpr int kBlkDims = 128 / kElt;          // dims of a block
+    static constexpr int kBlocks = D / kBlkDims;         // blocks of a K (or V) tile
+    static constexpr int kSubBlocks = kE4 ? 1 : (kBlocks < 2 ? 1 : 2);  // 128 dims of V
+    static constexpr int kSub = kSubBlocks * kBlk;       // one ring unit
+    static constexpr int kSubs = kBlocks / kSubBlocks;   // ring units of a tile
+    static constexpr int kQParts = kE4 ? 3 : 1;
+    static constexpr int kPParts = kE4 ? 4 : 2;
+    static constexpr int NH = GM * kQParts;              // query columns of a head
+    static constexpr int NP = GM * kPParts;              // output columns of a head
+    // P^T: K-major rows of 64 (E4M3: 128) cache rows; E4M3 tiles whose runs
+    // are 16 rows long hold two heads in a K step, each in rows of its own.
+    static constexpr int kPRows = kE4 ? 2 * NP : NP;
+    static constexpr int kPBytes = kPRows * kRows * kElt;
+    // Most heads of a tile: as many as leave the accumulators within TMEM and
+    // at least three units in each ring.
+    static constexpr int q_rows(int hs) { return hs * NH < 16 ? 16 : (hs * NH + 15) / 16 * 16; }
+    static constexpr int cols(int hs) { return 2 * q_rows(hs) + kGroups * kSubs * hs * NP; }
+    static constexpr int units(int hs) {
+        return (227 * 1024 - 1024 - kBarBytes - q_rows(hs) * D * kElt - 2 * kPBytes) / (2 * kSub);
+    }
+    static constexpr bool fits(int hs) { return cols(hs) <= kTmemCols && units(hs) >= 3; }
+    static constexpr int kHsMax = fits(8) ? 8 : fits(4) ? 4 : fits(2) ? 2 : 1;
+    static_assert(fits(kHsMax), "TMEM columns and ring units");
+    static constexpr int kQBytes = q_rows(kHsMax) * D * kElt;
+    static constexpr int kFit = units(kHsMax);
+    static constexpr int NS = kFit > 8 ? 8 : kFit;       // units of each ring
+    static constexpr int kKOff = 0;
+    static constexpr int kVOff = kKOff + NS * kSub;
+    static constexpr int kQOff = kVOff + NS * kSub;
+    static constexpr int kPOff = kQOff + kQBytes;
+    static constexpr int kBarOff = kPOff + 2 * kPBytes;
+};
+
+struct Bars {
+    uint64_t kfull[8], kempty[8], vfull[8], vempty[8];
+    uint64_t s_full[2], p_full[2], pv_done[2];
+    uint64_t q_full, q_empty, o_free, drain;
+    uint32_t tmem_base;
+    volatile int32_t abort;
+    int32_t start_row, start_tile;      // the run's first row and that row's first tile
+    int32_t scratch[32];
+    uint32_t loaded[kMaskRing];         // runs of a tile that were loaded
+    float red[kGroups][8][16];          // per 16 rows: maxima or sums
+    float alpha[kGroups][8][16];        // rescale factors, [head][query]
+    float ml[kGroups][8][16][2];        // epilogue: (m, l), [head][query]
+    float qscale[4][128];    // E4M3: factor of each query's logits, by segment
+};
+static_assert(sizeof(Bars) <= kBarBytes, "barrier block");
+
+// 4-D tensor map coordinates: dim, token of the page, KV head, page.
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int tok,
+                                         int head, int page, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(tok), "r"(head), "r"(page), "r"(hs::smem_u32(bar))
+        : "memory");
+}
+
+// Whether the phase with `parity` has completed (no wait).
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(hs::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+template <int KV>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                    uint32_t acc) {
+    if constexpr (KV == kE4m3)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+    else
+        hs::tc::mma_bf16(d, a, b, idesc, acc);
+}
+
+// Instruction descriptor: fp32 accumulators; types by kind (bf16 1, fp16 0,
+// E4M3 0); B K-major.
+template <int KV>
+__device__ __forceinline__ uint32_t idesc(int N, int a_mn_major) {
+    const uint32_t fmt = KV == kBf16 ? 1u : 0u;
+    return (1u << 4) | (fmt << 7) | (fmt << 10) | (uint32_t(a_mn_major) << 15) |
+           (uint32_t(N >> 3) << 17) | (uint32_t(kRows >> 4) << 24);
+}
+
+// Token tiles of a request: those of the sinks, then those of the window,
+// both on the grid of th tokens, so that boxes start on whole runs.
+struct Tiling {
+    int T, sc, w0, ns, tw0, n;
+};
+__device__ __forceinline__ Tiling tiling_of(const PagedArgs& a, int len, int th) {
+    Tiling v;
+    v.T = min(max(len, 0), a.max_len);
+    const int wc = a.window > 0 ? min(v.T, a.window) : v.T;
+    v.w0 = v.T - wc;
+    v.sc = a.window > 0 ? min(a.sinks, v.w0) : 0;
+    v.tw0 = v.w0 / th;
+    v.ns = min((v.sc + th - 1) / th, v.tw0);
+    v.n = max(1, v.ns + (v.T + th - 1) / th - v.tw0);
+    return v;
+}
+
+// Walks the tiles of a CTA's run; every role of the CTA walks alike.
+struct Cursor {
+    int row, chunk, tile, left;  // left: tiles of the run still to come, this one included
+    bool first;                  // this tile starts a segment (a unit, or the run)
+    Tiling v;
+};
+__device__ __forceinline__ void cursor_row(Cursor& c, const PagedArgs& a, int th) {
+    c.v = tiling_of(a, __ldg(a.seq_lens + c.row), th);
+}
+__device__ __forceinline__ Cursor cursor_at(const PagedArgs& a, const Plan& pl, int row,
+                                            int row_tile0, int64_t w, int64_t w1, int th) {
+    Cursor c;
+    c.row = row;
+    cursor_row(c, a, th);
+    const int64_t rel = w - int64_t(row_tile0) * pl.chunks;
+    c.chunk = int(rel / c.v.n);
+    c.tile = int(rel - int64_t(c.chunk) * c.v.n);
+    c.left = int(w1 - w);
+    c.first = true;
+    return c;
+}
+__device__ __forceinline__ bool last_of_segment(const Cursor& c) {
+    return c.left == 1 || c.tile == c.v.n - 1;
+}
+__device__ __forceinline__ void advance(Cursor& c, const PagedArgs& a, int chunks, int th) {
+    c.first = false;
+    --c.left;
+    if (++c.tile < c.v.n || c.left == 0) return;
+    c.tile = 0;
+    c.first = true;
+    if (++c.chunk < chunks) return;
+    c.chunk = 0;
+    ++c.row;
+    cursor_row(c, a, th);
+}
+__device__ __forceinline__ int tile_token(const Cursor& c, int th) {
+    return (c.tile < c.v.ns ? c.tile : c.tile - c.v.ns + c.v.tw0) * th;
+}
+__device__ __forceinline__ bool visible(const Tiling& v, int t) {
+    return t < v.T && (t < v.sc || t >= v.w0);
+}
+// Whether any of the tokens [t, t + n) is attended to.
+__device__ __forceinline__ bool any_visible(const Tiling& v, int t, int n) {
+    return t < v.T && (t < v.sc || t + n > v.w0);
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[N]) {
+    if constexpr (N == 8) {
+        hs::tc::tmem_ld8(addr, v);
+    } else if constexpr (N % 16 == 0) {
+#pragma unroll
+        for (int c = 0; c < N; c += 16) {
+            float t[16];
+            hs::tc::tmem_ld16(addr + c, t);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[c + i] = t[i];
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < N; c += 8) {
+            float t[8];
+            hs::tc::tmem_ld8(addr + c, t);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[c + i] = t[i];
+        }
+    }
+}
+
+__device__ __forceinline__ uint8_t to_e4m3(float x) {
+    return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float from_e4m3(uint8_t c) {
+    return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
+}
+
+template <int KV, int D, int GH>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUtensorMap kmap0,
+                const __grid_constant__ CUtensorMap vmap0,
+                const __grid_constant__ CUtensorMap kmap1,
+                const __grid_constant__ CUtensorMap vmap1) {
+    using C = Cfg<KV, D, GH>;
+    constexpr int GM = C::GM, NS = C::NS;
+    constexpr bool E4 = C::kE4;
+    const PagedArgs& a = ta.p;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Bars& B = *reinterpret_cast<Bars*>(smem + C::kBarOff);
+    const uint32_t sb = hs::smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint64_t tmo = ta.timeout_ns;
+    const volatile int* abort_flag = &B.abort;
+
+    hs::pdl_trigger();
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            hs::mbar_init(&B.kfull[i], 1);
+            hs::mbar_init(&B.kempty[i], 1);
+            hs::mbar_init(&B.vfull[i], 1);
+            hs::mbar_init(&B.vempty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            hs::mbar_init(&B.s_full[i], 1);
+            hs::mbar_init(&B.p_full[i], kSoftThreads);
+            hs::mbar_init(&B.pv_done[i], 1);
+        }
+        hs::mbar_init(&B.q_full, kQThreads);
+        hs::mbar_init(&B.q_empty, 1);
+        hs::mbar_init(&B.o_free, kGroups * kSoftThreads);
+        hs::mbar_init(&B.drain, 1);
+        B.abort = 0;
+        hs::fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        hs::tc::tmem_alloc(&B.tmem_base, kTmemCols);
+        hs::tc::tmem_relinquish();
+    }
+    // P's rows of the other head of a K step stay zero.
+    if constexpr (E4)
+        for (int i = tid; i < 2 * C::kPBytes / 16; i += kThreads)
+            reinterpret_cast<uint4*>(smem + C::kPOff)[i] = make_uint4(0u, 0u, 0u, 0u);
+    hs::pdl_wait();
+
+    // ---- The plan (the same in every CTA) ---------------------------------
+    const int group = a.heads / a.kv_heads;
+    const int gch = (group + GM - 1) / GM;
+    const int cta = blockIdx.x;
+    Plan pl;
+    int mode;
+    int64_t w0 = 0, w1 = 0;  // this CTA's run of tiles
+    {
+        int n0 = 0, n1 = 0;  // tiles of a chunk of heads, both ways
+        for (int r = tid; r < a.rows; r += kThreads) {
+            const int len = __ldg(a.seq_lens + r);
+            n0 += tiling_of(a, len, kRows / ta.hs[0]).n;
+            n1 += tiling_of(a, len, kRows / ta.hs[1]).n;
+            if (cta == 0 && len > a.max_len) hs::set_status(a.status, HS_ERR_BAD_INDEX);
+        }
+        int total0, total1;
+        hs::block_excl_scan(n0, B.scratch, &total0);
+        __syncthreads();
+        hs::block_excl_scan(n1, B.scratch, &total1);
+        const int64_t wide = int64_t(total0) * (a.kv_heads / ta.hs[0]) * gch;
+        mode = wide >= int64_t(a.ctas) * ta.steps_for_wide ? 0 : 1;
+        pl.hs = ta.hs[mode];
+        pl.chunks = a.kv_heads / pl.hs * gch;
+        pl.tiles = int64_t(mode == 0 ? total0 : total1) * pl.chunks;
+        pl.n = int(hs::max64(1, hs::min64(a.ctas, pl.tiles)));
+        if (cta < pl.n) {
+            w0 = run_begin(pl, cta);
+            w1 = run_begin(pl, cta + 1);
+        }
+        // The row that the run begins in; CTA 0 keeps every row's first tile
+        // for the merge.
+        int carry = 0;
+        for (int r0 = 0; r0 < a.rows; r0 += kThreads) {
+            const int r = r0 + tid;
+            const int n =
+                r < a.rows ? tiling_of(a, __ldg(a.seq_lens + r), kRows / pl.hs).n : 0;
+            __syncthreads();
+            int sum;
+            const int at = carry + hs::block_excl_scan(n, B.scratch, &sum);
+            if (r < a.rows) {
+                if (cta == 0) a.plan[8 + r] = at;
+                if (int64_t(at) * pl.chunks <= w0 && w0 < int64_t(at + n) * pl.chunks) {
+                    B.start_row = r;
+                    B.start_tile = at;
+                }
+            }
+            carry += sum;
+        }
+        if (cta == 0 && tid == 0) {
+            a.plan[8 + a.rows] = carry;
+            a.plan[0] = pl.hs;
+            a.plan[1] = pl.n;
+            a.plan[2] = pl.chunks;
+            a.plan[3] = GM;
+        }
+        hs::fence_proxy_async_shared();  // P's zeros, read by the tensor cores
+        hs::tc::fence_before_sync();
+        __syncthreads();
+        hs::tc::fence_after_sync();
+    }
+    const uint32_t tmem = B.tmem_base;
+    const int run = int(w1 - w0);
+    const int hsn = pl.hs, bt = ta.bt[mode];
+    // hs and bt are powers of two.
+    const int lhs = 31 - __clz(hsn), lbt = 31 - __clz(bt);
+    const int th = kRows >> lhs;     // tokens of a tile
+    const int nops = th >> lbt;      // runs (boxes) of a tile
+    const int chunks = pl.chunks;
+    const int nq = max(16, (hsn * C::NH + 15) / 16 * 16);  // N of the QK product
+    const uint32_t o_col = uint32_t(2 * nq);
+    const int ocols = hsn * C::NP;   // output columns of 128 dims
+
+    if (run <= 0) {
+        // Nothing to do: straight to the tear-down.
+    } else if (warp == kTmaWarp) {
+        // ------------------------------- loads -------------------------------
+        const CUtensorMap* kmap = mode == 0 ? &kmap0 : &kmap1;
+        const CUtensorMap* vmap = mode == 0 ? &vmap0 : &vmap1;
+        Cursor c = cursor_at(a, pl, B.start_row, B.start_tile, w0, w1, th);
+        bool ok = true, bad = false;
+        int kseq = 0, vseq = 0, t = 0;
+        // Lane i < nops: run i of the tile; its page is looked up a tile ahead.
+        auto lookup = [&](const Cursor& x, int& tok) {
+            tok = lane < nops ? tile_token(x, th) + lane * bt : 0;
+            const bool want = lane < nops && any_visible(x.v, tok, bt);
+            if (!want) return -2;
+            return __ldg(a.block_table + int64_t(x.row) * a.bt_stride + tok / a.page_size);
+        };
+        int tok_n, page_n = lookup(c, tok_n);
+        for (; ok;) {
+            const int tok = tok_n, page = page_n;
+            const int kvh0 = c.chunk / gch * hsn;
+            const bool more = c.left > 1;
+            advance(c, a, chunks, th);
+            if (more) page_n = lookup(c, tok_n);
+            const bool want = page >= 0 && page < a.num_pages;
+            if (page != -2 && !want) bad = true;
+            const uint32_t loaded = __ballot_sync(0xffffffffu, want);
+            const int boxes = __popc(loaded);
+            const uint32_t bytes = uint32_t(boxes) * uint32_t(hsn * bt) * 128u * C::kSubBlocks;
+            const int at = tok % a.page_size;
+            // Read by the softmax of this tile (its logits follow these
+            // loads), at most NS + 3 tiles behind.
+            if (lane == 0) B.loaded[t % kMaskRing] = loaded;
+            ++t;
+            auto fill = [&](uint64_t* full, uint64_t* empty, int off, const CUtensorMap* map,
+                            int& seq) {
+                for (int s = 0; s < C::kSubs; ++s, ++seq) {
+                    const int slot = seq % NS;
+                    if (!__all_sync(0xffffffffu,
+                                    hs::mbar_wait_bounded(&empty[slot], ((seq / NS) & 1) ^ 1, tmo,
+                                                          abort_flag)))
+                        return false;
+                    if (lane == 0) hs::mbar_arrive_expect_tx(&full[slot], bytes);
+                    __syncwarp();
+                    if (want) {
+                        const uint32_t dst = sb + off + slot * C::kSub + lane * hsn * bt * 128;
+#pragma unroll
+                        for (int b = 0; b < C::kSubBlocks; ++b)
+                            tma_load(dst + b * kBlk, map, (s * C::kSubBlocks + b) * C::kBlkDims,
+                                     at, kvh0, page, &full[slot]);
+                    }
+                }
+                return true;
+            };
+            ok = fill(B.kfull, B.kempty, C::kKOff, kmap, kseq) &&
+                 fill(B.vfull, B.vempty, C::kVOff, vmap, vseq);
+            if (!more) break;
+        }
+        if (!ok) {
+            hs::set_status(a.status, HS_ERR_TIMEOUT);
+            B.abort = 1;
+            // No copy may outlive the CTA: wait for every unit in flight.
+            for (int s = max(0, kseq - NS); s < kseq; ++s)
+                hs::mbar_wait_bounded(&B.kfull[s % NS], (s / NS) & 1, tmo, nullptr);
+            for (int s = max(0, vseq - NS); s < vseq; ++s)
+                hs::mbar_wait_bounded(&B.vfull[s % NS], (s / NS) & 1, tmo, nullptr);
+        }
+        if (bad) hs::set_status(a.status, HS_ERR_BAD_INDEX);
+    } else if (warp == kMmaWarp) {
+        // ------------------------------ products -----------------------------
+        if (lane == 0) {
+            constexpr int kStep = E4 ? 32 : 16;              // rows of a PV K step
+            constexpr int kSteps = kRows / kStep;
+            const uint32_t id_qk = idesc<KV>(nq, 0);
+            // E4M3, runs of 16 rows: a K step holds two heads, taken together.
+            const bool two = E4 && bt < kStep && hsn > 1;
+            const uint32_t id_pv = idesc<KV>(two ? 2 * C::NP : C::NP, 1);
+            // Descriptors of the first tiles; others are an offset (in units
+            // of 16 bytes) away.
+            const uint64_t k_desc = hs::tc::sdesc_sw128(sb + C::kKOff, 16, 1024);
+            const uint64_t q_desc = hs::tc::sdesc_sw128(sb + C::kQOff, 16, 1024);
+            const uint64_t v_desc = hs::tc::sdesc_sw128(sb + C::kVOff, kBlk, 1024);
+            const uint64_t p_desc = hs::tc::sdesc_sw128(sb + C::kPOff, 16, 1024);
+            // Output column of each K step's head, and the steps that hold a
+            // head's first rows.
+            uint32_t col[kSteps], starts = 0;
+#pragma unroll
+            for (int kk = 0; kk < kSteps; ++kk) {
+                const int r = kk * kStep;
+                col[kk] = uint32_t((r >> lbt) & (hsn - 1)) * C::NP;
+                if (r < (hsn << lbt) && (two || (r & (bt - 1)) == 0)) starts |= 1u << kk;
+            }
+            Cursor cq = cursor_at(a, pl, B.start_row, B.start_tile, w0, w1, th);
+            uint32_t first_mask = 0;  // bit t % 4: tile t starts a segment
+            int qseg = 0, oseg = 0, seg_t0 = 0;
+            auto issue_qk = [&](int t) -> bool {
+                if (cq.first) {
+                    if (!hs::mbar_wait_bounded(&B.q_full, qseg & 1, tmo, abort_flag)) return false;
+                    ++qseg;
+                }
+                first_mask = (first_mask & ~(1u << (t & 3))) | (uint32_t(cq.first) << (t & 3));
+                const uint32_t d = tmem + uint32_t((t & 1) * nq);
+                for (int s = 0; s < C::kSubs; ++s) {
+                    const int seq = t * C::kSubs + s, slot = seq % NS;
+                    if (!hs::mbar_wait_bounded(&B.kfull[slot], (seq / NS) & 1, tmo, abort_flag))
+                        return false;
+                    hs::tc::fence_after_sync();
+                    const uint64_t kd = k_desc + uint32_t(slot * (C::kSub >> 4));
+                    const uint64_t qd = q_desc + uint32_t(s * C::kSubBlocks * nq * 8);
+#pragma unroll
+                    for (int b = 0; b < C::kSubBlocks; ++b) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma<KV>(d, kd + uint32_t(b * (kBlk >> 4) + kk * 2),
+                                    qd + uint32_t(b * nq * 8 + kk * 2), id_qk,
+                                    (s | b | kk) ? 1u : 0u);
+                    }
+                    hs::tc::mma_commit(&B.kempty[slot]);
+                }
+                hs::tc::mma_commit(&B.s_full[t & 1]);
+                if (last_of_segment(cq)) hs::tc::mma_commit(&B.q_empty);
+                if (t + 1 < run) advance(cq, a, chunks, th);
+                return true;
+            };
+            auto issue_pv = [&](int t) -> bool {
+                if (!hs::mbar_wait_bounded(&B.p_full[t & 1], (t >> 1) & 1, tmo, abort_flag))
+                    return false;
+                if ((first_mask >> (t & 3)) & 1u) {
+                    // The epilogue of the segment before has read the output.
+                    if (oseg > 0 &&
+                        !hs::mbar_wait_bounded(&B.o_free, (oseg - 1) & 1, tmo, abort_flag))
+                        return false;
+                    ++oseg;
+                    seg_t0 = t;
+                }
+                // A group's first tile of the segment starts its output.
+                const uint32_t fresh = t - seg_t0 < kGroups ? starts : 0u;
+                const uint64_t pd = p_desc + uint32_t((t & 1) * (C::kPBytes >> 4));
+                for (int s = 0; s < C::kSubs; ++s) {
+                    const int seq = t * C::kSubs + s, slot = seq % NS;
+                    if (!hs::mbar_wait_bounded(&B.vfull[slot], (seq / NS) & 1, tmo, abort_flag))
+                        return false;
+                    hs::tc::fence_after_sync();
+                    const uint64_t vd = v_desc + uint32_t(slot * (C::kSub >> 4));
+                    const uint32_t d = tmem + o_col + uint32_t(((t & 1) * C::kSubs + s) * ocols);
+#pragma unroll
+                    for (int kk = 0; kk < kSteps; ++kk)
+                        mma<KV>(d + col[kk], vd + uint32_t(kk * kStep * 8),
+                                pd + uint32_t(E4 ? kk * 2 : (kk >> 2) * (C::NP * 8) + (kk & 3) * 2),
+                                id_pv, ((fresh >> kk) & 1u) ^ 1u);
+                    hs::tc::mma_commit(&B.vempty[slot]);
+                }
+                hs::tc::mma_commit(&B.pv_done[t & 1]);
+                return true;
+            };
+            // QK runs at most one tile ahead of PV (its S buffer); whichever
+            // has its operands goes first.
+            bool ok = issue_qk(0);
+            uint64_t since = 0;  // start of the wait for either
+            uint32_t polls = 0;
+            for (int t = 0, q = 1; t < run && ok;) {
+                if (q == run || q > t + 1) {
+                    ok = issue_pv(t++);
+                    continue;
+                }
+                const int ks = q * C::kSubs, vs = t * C::kSubs;
+                if (mbar_test(&B.kfull[ks % NS], (ks / NS) & 1)) {
+                    ok = issue_qk(q++);
+                } else if (mbar_test(&B.p_full[t & 1], (t >> 1) & 1) &&
+                           mbar_test(&B.vfull[vs % NS], (vs / NS) & 1)) {
+                    ok = issue_pv(t++);
+                } else {
+                    if (++polls % 64 == 0) {
+                        const uint64_t now = hs::global_timer_ns();
+                        if (since == 0) since = now;
+                        ok = B.abort == 0 && now - since <= tmo;
+                    }
+                    continue;
+                }
+                since = 0;
+            }
+            if (!ok) {
+                hs::set_status(a.status, HS_ERR_TIMEOUT);
+                B.abort = 1;
+            }
+            // Every product issued has completed before TMEM is freed.
+            hs::tc::mma_commit(&B.drain);
+            hs::mbar_wait_bounded(&B.drain, 0, tmo, nullptr);
+        }
+        __syncwarp();
+    } else if (warp >= kQWarp) {
+        // ------------------------------ queries ------------------------------
+        const int qt = tid - kQWarp * 32;
+        Cursor c = cursor_at(a, pl, B.start_row, B.start_tile, w0, w1, th);
+        bool ok = true;
+        for (int seg = 0; ok;) {
+            if (c.first) {
+                if (seg > 0 &&
+                    !__all_sync(0xffffffffu, hs::mbar_wait_bounded(&B.q_empty, (seg - 1) & 1, tmo,
+                                                                   abort_flag))) {
+                    ok = false;
+                    break;
+                }
+                const int kvh0 = c.chunk / gch * hsn, gc = c.chunk % gch;
+                const int Gc = min(GM, group - gc * GM);
+                const char* q = static_cast<const char*>(a.q) + int64_t(c.row) * a.q_stride * 2;
+                if constexpr (!E4) {
+                    constexpr int kCh = D / 8;  // 16-byte chunks of a query row
+                    for (int e = qt; e < nq * kCh; e += kQThreads) {
+                        const int n = e / kCh, ch = e % kCh;
+                        const int hl = n / GM, gi = n % GM;
+                        const bool in = hl < hsn && gi < Gc;
+                        const int h = (kvh0 + min(hl, hsn - 1)) * group + gc * GM + min(gi, Gc - 1);
+                        hs::tc::cp_async16(sb + C::kQOff + (ch >> 3) * uint32_t(nq) * 128 +
+                                               n * 128 + (((ch & 7) ^ (n & 7)) << 4),
+                                           q + int64_t(h) * D * 2 + ch * 16, in ? 16u : 0u);
+                    }
+                    hs::tc::cp_async_wait_all();
+                } else {
+                    // Lanes of 16 dims; D / 16 of them hold a row.
+                    constexpr int kL = D / 16;
+                    const int ch = qt % kL;
+                    for (int n0 = 0; n0 < hsn * GM; n0 += kQThreads / kL) {
+                        const int idx = n0 + qt / kL;  // (head, query) in order
+                        const int hl = idx / GM, gi = idx % GM;
+                        const bool slot_ok = hl < hsn;
+                        const bool in = slot_ok && gi < Gc;
+                        float x[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) x[i] = 0.f;
+                        if (in) {
+                            const int h = (kvh0 + hl) * group + gc * GM + gi;
+                            const uint4* p = reinterpret_cast<const uint4*>(
+                                q + (int64_t(h) * D + ch * 16) * 2);
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const uint4 u = __ldg(p + j);
+                                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const float2 f =
+                                        a.q_is_half
+                                            ? __half22float2(*reinterpret_cast<const __half2*>(&w[i]))
+                                            : __bfloat1622float2(
+                                                  *reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+                                    x[8 * j + 2 * i] = f.x;
+                                    x[8 * j + 2 * i + 1] = f.y;
+                                }
+                            }
+                        }
+                        float mx = 0.f;
+                        bool nan = false;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            mx = fmaxf(mx, fabsf(x[i]));
+                            nan |= !(fabsf(x[i]) < CUDART_INF_F);
+                        }
+#pragma unroll
+                        for (int o = kL / 2; o > 0; o >>= 1)
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                        // Largest magnitude to [2^7, 2^8).
+                        int e = 0;
+                        if (mx > 0.f && mx < CUDART_INF_F) e = 7 - ilogbf(mx);
+                        const float up = exp2f(float(max(e, -126) / 2));
+                        const float up2 = exp2f(float(max(e, -126) - max(e, -126) / 2));
+                        uint32_t code[3][4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) code[0][i] = code[1][i] = code[2][i] = 0u;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float r = x[i] * up * up2;
+#pragma unroll
+                            for (int k = 0; k < 3; ++k) {
+                                // A query that is not finite shows as NaN.
+                                const uint8_t cc = nan ? uint8_t(0x7f) : to_e4m3(r);
+                                code[k][i >> 2] |= uint32_t(cc) << (8 * (i & 3));
+                                r = (r - from_e4m3(cc)) * 16.f;
+                            }
+                        }
+                        if (slot_ok) {
+#pragma unroll
+                            for (int k = 0; k < 3; ++k) {
+                                const int n = hl * C::NH + k * GM + gi;
+                                *reinterpret_cast<uint4*>(
+                                    smem + C::kQOff + (ch >> 3) * nq * 128 + n * 128 +
+                                    (((ch & 7) ^ (n & 7)) << 4)) =
+                                    make_uint4(code[k][0], code[k][1], code[k][2], code[k][3]);
+                            }
+                            if (ch == 0) {
+                                float f = a.scale_log2 * exp2f(float(-max(e, -126) / 2)) *
+                                          exp2f(float(-(max(e, -126) - max(e, -126) / 2)));
+                                if (a.k_scale != nullptr) f *= __ldg(a.k_scale + kvh0 + hl);
+                                B.qscale[seg & 3][hl * GM + gi] = f;
+                            }
+                        }
+                    }
+                }
+                hs::fence_proxy_async_shared();
+                hs::mbar_arrive(&B.q_full);
+                ++seg;
+            }
+            if (c.left == 1) break;
+            advance(c, a, chunks, th);
+        }
+        if (!ok) {
+            hs::set_status(a.status, HS_ERR_TIMEOUT);
+            B.abort = 1;
+        }
+    } else {
+        // ------------------------- softmax and epilogue ------------------------
+        const int wg = warp >> 2;                // group: tiles t with t % 2 == wg
+        const int r = tid & 127;                 // row of the tile, and TMEM lane
+        const int run_r = r >> (lhs + lbt);      // its run
+        const int hl = (r >> lbt) & (hsn - 1);   // its head in the unit
+        const int rt = (run_r << lbt) + (r & (bt - 1));  // its token in the tile
+        const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+        // Heads of the warp's two half warps.
+        const int hA = ((warp & 3) * 32 >> lbt) & (hsn - 1);
+        const int hB = ((warp & 3) * 32 + 16 >> lbt) & (hsn - 1);
+        const uint32_t s_addr = tmem + lane_base + uint32_t(wg * nq);
+        const uint32_t o_addr = tmem + lane_base + o_col;
+        const uint32_t o_own = o_addr + uint32_t(wg * C::kSubs * ocols);
+        const uint32_t p_own = sb + C::kPOff + wg * C::kPBytes;
+        // This row's place in P^T: K-major rows of 128 bytes, 64 (E4M3: 128)
+        // cache rows each; E4M3 with two heads in a K step: each its own rows.
+        const int p_col = E4 ? r : (r & 63) * 2;
+        const uint32_t p_row =
+            p_own + (E4 ? (bt < 32 && hsn > 1 ? uint32_t(hl & 1) * (C::NP * 128) : 0u)
+                        : uint32_t(r >> 6) * (C::NP * 128)) + uint32_t(p_col & 15);
+        const uint32_t p_chunk = uint32_t(p_col >> 4);
+        auto put16 = [&](int n, uint16_t x) {
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(
+                             p_row + n * 128 + ((p_chunk ^ uint32_t(n & 7)) << 4)),
+                         "h"(x)
+                         : "memory");
+        };
+        auto put8 = [&](int n, uint32_t x) {
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"(
+                             p_row + n * 128 + ((p_chunk ^ uint32_t(n & 7)) << 4)),
+                         "r"(x)
+                         : "memory");
+        };
+        bool fail = false;
+        // A wait that gives up lets the CTA run to its end at once (every
+        // later wait sees the flag), so that all its barriers are met.
+        auto wait = [&](uint64_t* bar, int parity) {
+            if (!hs::mbar_wait_bounded(bar, uint32_t(parity), tmo, abort_flag)) {
+                fail = true;
+                B.abort = 1;
+            }
+            __syncwarp();
+        };
+        Cursor c = cursor_at(a, pl, B.start_row, B.start_tile, w0, w1, th);
+        for (int t = 0, seg = 0; t < run; ++seg) {
+            // ---- One segment: the tiles of one unit in this run ----------------
+            const int row = c.row;
+            const int kvh0 = c.chunk / gch * hsn, gc = c.chunk % gch;
+            const int Gc = min(GM, group - gc * GM);
+            const Tiling v = c.v;
+            const int tile0 = c.tile, n = min(c.left, v.n - tile0), t0 = t;
+            const bool whole = n == v.n;
+            const int slot = 2 * cta + (tile0 == 0 && t > 0 ? 1 : 0);
+            float mref[GM], l[GM];
+#pragma unroll
+            for (int i = 0; i < GM; ++i) {
+                mref[i] = -CUDART_INF_F;
+                l[i] = 0.f;
+            }
+            bool own = false;  // this group has had a tile of the segment
+            for (; t < t0 + n; ++t, advance(c, a, chunks, th)) {
+                if ((t & 1) != wg) continue;
+                const int tok = tile_token(c, th) + rt;
+                wait(&B.s_full[wg], (t >> 1) & 1);
+                hs::tc::fence_after_sync();
+                const bool seen = visible(v, tok);
+                const bool valid = seen && ((B.loaded[t % kMaskRing] >> run_r) & 1u);
+                float x[GM];
+#pragma unroll
+                for (int k = 0; k < C::kQParts; ++k) {
+                    float s[GM];
+                    tmem_ld<GM>(s_addr + hA * C::NH + k * GM, s);
+                    if (hB != hA) {
+                        float s2[GM];
+                        tmem_ld<GM>(s_addr + hB * C::NH + k * GM, s2);
+                        hs::tc::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < GM; ++i) s[i] = lane < 16 ? s[i] : s2[i];
+                    } else {
+                        hs::tc::tmem_wait_ld();
+                    }
+                    constexpr float kPart[3] = {1.f, 0.0625f, 0.00390625f};
+#pragma unroll
+                    for (int i = 0; i < GM; ++i)
+                        x[i] = k == 0 ? s[i] : fmaf(s[i], kPart[k], x[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < GM; ++i) {
+                    x[i] *= E4 ? B.qscale[seg & 3][hl * GM + i] : a.scale_log2;
+                    if (!valid) x[i] = -CUDART_INF_F;
+                }
+                if (a.logits != nullptr && seen) {
+                    const int i = tok < v.sc ? tok : tok - v.w0 + v.sc;
+                    float* lp = a.logits +
+                                (int64_t(row) * a.heads + (kvh0 + hl) * group + gc * GM) *
+                                    a.logit_stride + i;
+#pragma unroll
+                    for (int g = 0; g < GM; ++g)
+                        if (g < Gc) lp[g * a.logit_stride] = x[g];
+                }
+                bool grow = false;
+#pragma unroll
+                for (int i = 0; i < GM; ++i) grow |= i < Gc && x[i] > mref[i] + kThresh;
+                // The group's P buffer and output: its product before is done.
+                if (t >= kGroups) wait(&B.pv_done[wg], ((t - kGroups) >> 1) & 1);
+                if (hs::pair::named_sync_or(kSoftBar + wg, kSoftThreads, grow)) {
+                    // New reference maxima: the largest logits so far.
+#pragma unroll
+                    for (int i = 0; i < GM; ++i) {
+                        float mx = x[i];
+#pragma unroll
+                        for (int o = 8; o > 0; o >>= 1)
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                        if ((lane & 15) == 0) B.red[wg][r >> 4][i] = mx;
+                    }
+                    hs::pair::named_sync(kSoftBar + wg, kSoftThreads);
+#pragma unroll
+                    for (int i = 0; i < GM; ++i) {
+                        float mn = mref[i];
+                        for (int q = 0; q < 8; ++q)
+                            if (((q * 16 >> lbt) & (hsn - 1)) == hl) mn = fmaxf(mn, B.red[wg][q][i]);
+                        const float al = mn == mref[i] ? 1.f : exp2f(mref[i] - mn);
+                        l[i] *= al;
+                        mref[i] = mn;
+                        if (rt == 0) B.alpha[wg][hl][i] = al;
+                    }
+                    hs::pair::named_sync(kSoftBar + wg, kSoftThreads);
+                    if (own) {
+                        hs::tc::fence_after_sync();
+#pragma unroll 1
+                        for (int cb = 0; cb < C::kSubs * ocols; cb += 8) {
+                            float o[8];
+                            hs::tc::tmem_ld8(o_own + uint32_t(cb), o);
+                            hs::tc::tmem_wait_ld();
+                            const int oc = cb % ocols;
+                            const float* al = &B.alpha[wg][oc / C::NP][oc % GM];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) o[i] *= al[i];
+                            hs::tc::tmem_st8(o_own + uint32_t(cb), o);
+                        }
+                        hs::tc::tmem_wait_st();
+                    }
+                }
+                own = true;
+#pragma unroll
+                for (int i = 0; i < GM; ++i) {
+                    if (i >= Gc) break;
+                    // Without a finite logit so far: subtract 0, every weight
+                    // stays 0 (a NaN logit stays NaN).
+                    const float p = exp2f(x[i] - (mref[i] == -CUDART_INF_F ? 0.f : mref[i]));
+                    l[i] += p;
+                    if constexpr (KV == kBf16) {
+                        const __nv_bfloat16 hi = __float2bfloat16_rn(p);
+                        put16(i, __bfloat16_as_ushort(hi));
+                        put16(GM + i,
+                              __bfloat16_as_ushort(__float2bfloat16_rn(p - __bfloat162float(hi))));
+                    } else if constexpr (KV == kFp16) {
+                        const __half hi = __float2half_rn(p);
+                        put16(i, __half_as_ushort(hi));
+                        put16(GM + i, __half_as_ushort(__float2half_rn(p - __half2float(hi))));
+                    } else {
+                        float rem = p;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint8_t cc = to_e4m3(rem);
+                            put8(k * GM + i, cc);
+                            rem = (rem - from_e4m3(cc)) * 16.f;
+                        }
+                    }
+                }
+                // Rows that are not attended to hold anything (places behind
+                // the context, pages that were not loaded): their V becomes 0,
+                // so that the weight 0 times it is 0.
+                if (!valid) {
+                    for (int s = 0; s < C::kSubs; ++s) {
+                        const int seq = t * C::kSubs + s, at = seq % NS;
+                        if (!hs::mbar_wait_bounded(&B.vfull[at], (seq / NS) & 1, tmo, abort_flag)) {
+                            fail = true;
+                            B.abort = 1;
+                        }
+                        unsigned char* vr = smem + C::kVOff + at * C::kSub + r * 128;
+#pragma unroll
+                        for (int b = 0; b < C::kSubBlocks; ++b)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                reinterpret_cast<uint4*>(vr + b * kBlk)[(i + lane) & 7] =
+                                    make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                __syncwarp();
+                hs::fence_proxy_async_shared();
+                hs::tc::fence_before_sync();
+                hs::mbar_arrive(&B.p_full[wg]);
+            }
+
+            // ---- The segment's state: join the groups, write it -----------------
+            // The groups' last products of the segment.
+            if (own) {
+                const int tl = ((t - 1) & 1) == wg ? t - 1 : t - 2;
+                wait(&B.pv_done[wg], (tl >> 1) & 1);
+            }
+            hs::tc::fence_after_sync();
+#pragma unroll
+            for (int i = 0; i < GM; ++i) {
+                float s = l[i];
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                if ((lane & 15) == 0) B.red[wg][r >> 4][i] = s;
+            }
+            hs::pair::named_sync(kSoftBar + wg, kSoftThreads);
+            if (rt == 0) {
+#pragma unroll
+                for (int i = 0; i < GM; ++i) {
+                    float L = 0.f;
+                    for (int q = 0; q < 8; ++q)
+                        if (((q * 16 >> lbt) & (hsn - 1)) == hl) L += B.red[wg][q][i];
+                    B.ml[wg][hl][i][0] = mref[i];
+                    B.ml[wg][hl][i][1] = L;
+                }
+            }
+            hs::pair::named_sync(kBothBar, kGroups * kSoftThreads);
+            // A segment of one tile leaves the other group's output unwritten.
+            const bool has[2] = {n > 1 || (t0 & 1) == 0, n > 1 || (t0 & 1) == 1};
+            const bool bf = KV == kBf16 || (E4 && !a.q_is_half);
+            for (int sh = wg; sh < C::kSubs * hsn; sh += kGroups) {
+                const int s = sh / hsn, h = sh % hsn;
+                const int d = s * 128 + r;
+                const int kv = kvh0 + h;
+                const float vs = a.v_scale != nullptr ? __ldg(a.v_scale + kv) : 1.f;
+                const int64_t qh = int64_t(row) * a.heads + kv * group + gc * GM;
+                float O[GM];
+#pragma unroll
+                for (int i = 0; i < GM; ++i) O[i] = 0.f;
+#pragma unroll
+                for (int w = 0; w < kGroups; ++w) {
+                    if (!has[w]) continue;
+#pragma unroll
+                    for (int k = 0; k < C::kPParts; ++k) {
+                        float o[GM];
+                        tmem_ld<GM>(o_addr + uint32_t((w * C::kSubs + s) * ocols + h * C::NP +
+                                                      k * GM), o);
+                        hs::tc::tmem_wait_ld();
+                        constexpr float kPart[4] = {1.f, 0.0625f, 0.00390625f, 0.000244140625f};
+#pragma unroll
+                        for (int i = 0; i < GM; ++i) {
+                            const float M = fmaxf(B.ml[0][h][i][0], B.ml[1][h][i][0]);
+                            const float f =
+                                exp2f(B.ml[w][h][i][0] - (M == -CUDART_INF_F ? 0.f : M));
+                            O[i] = fmaf(o[i], E4 ? f * kPart[k] : f, O[i]);
+                        }
+                    }
+                }
+                if (d >= D) continue;
+#pragma unroll
+                for (int i = 0; i < GM; ++i) {
+                    if (i >= Gc) break;
+                    if (whole) {
+                        const float m0 = B.ml[0][h][i][0], m1 = B.ml[1][h][i][0];
+                        const float M = fmaxf(m0, m1), ref = M == -CUDART_INF_F ? 0.f : M;
+                        const float L =
+                            fmaf(exp2f(m0 - ref), B.ml[0][h][i][1],
+                                 exp2f(m1 - ref) * B.ml[1][h][i][1]);
+                        const float f = L == 0.f ? 0.f : O[i] / L * vs;
+                        if (bf)
+                            static_cast<__nv_bfloat16*>(a.out)[(qh + i) * D + d] =
+                                __float2bfloat16_rn(f);
+                        else
+                            static_cast<__half*>(a.out)[(qh + i) * D + d] = __float2half_rn(f);
+                    } else {
+                        a.part_o[(int64_t(slot) * a.unit_heads_max + h * GM + i) * D + d] = O[i];
+                    }
+                }
+            }
+            hs::tc::fence_before_sync();
+            hs::mbar_arrive(&B.o_free);
+            if (wg == 0)
+                for (int e = r; e < hsn * GM; e += kSoftThreads) {
+                    const int h = e / GM, i = e % GM;
+                    if (i >= Gc) continue;
+                    const float m0 = B.ml[0][h][i][0], m1 = B.ml[1][h][i][0];
+                    const float M = fmaxf(m0, m1), ref = M == -CUDART_INF_F ? 0.f : M;
+                    const float L = fmaf(exp2f(m0 - ref), B.ml[0][h][i][1],
+                                         exp2f(m1 - ref) * B.ml[1][h][i][1]);
+                    if (whole) {
+                        const int64_t qh =
+                            int64_t(row) * a.heads + (kvh0 + h) * group + gc * GM + i;
+                        const float lg = L == 0.f ? -CUDART_INF_F : M + log2f(L);
+                        if (a.lse != nullptr) a.lse[qh] = lg * kLn2;
+                        if (a.lse2 != nullptr) a.lse2[qh] = lg;
+                    } else {
+                        const int64_t k = int64_t(slot) * a.unit_heads_max + e;
+                        a.part_ml[2 * k] = M;
+                        a.part_ml[2 * k + 1] = L;
+                    }
+                }
+            // The states are read: the next segment may write its own.
+            hs::pair::named_sync(kBothBar, kGroups * kSoftThreads);
+        }
+        if (fail) hs::set_status(a.status, HS_ERR_TIMEOUT);
+    }
+    hs::tc::fence_before_sync();
+    __syncthreads();
+    hs::tc::fence_after_sync();
+    if (warp == kMmaWarp) hs::tc::tmem_dealloc(tmem, kTmemCols);
+}
+
+// Tensor map of a cache: dims (head dim, token of the page, KV head, page).
+int encode_map(CUtensorMap* m, int kv, const void* base, const PagedArgs& a, int d, int bt,
+               int hs_box);
+
+template <int KV, int D, int GH>
+int launch_one(const PagedArgs& a, hs_stream_t stream) {
+    using C = Cfg<KV, D, GH>;
+    TcArgs t{};
+    t.p = a;
+    int hs_max = 1;
+    while (hs_max < C::kHsMax && a.kv_heads % (2 * hs_max) == 0) hs_max *= 2;
+    const auto run_of_page = [&](int hs_) {
+        int bt = kRows / hs_;
+        while (a.page_size % bt) bt /= 2;
+        return bt;
+    };
+    t.hs[0] = hs_max;
+    t.bt[0] = run_of_page(hs_max);
+    t.hs[1] = 1;
+    t.bt[1] = run_of_page(1);
+    t.steps_for_wide = 4;
+    t.timeout_ns = hs::kWaitTimeoutNs;
+    CUtensorMap m[4];
+    for (int i = 0; i < 2; ++i) {
+        int rc = encode_map(&m[2 * i], KV, a.k, a, D, t.bt[i], t.hs[i]);
+        if (rc == HS_OK) rc = encode_map(&m[2 * i + 1], KV, a.v, a, D, t.bt[i], t.hs[i]);
+        if (rc != HS_OK) return rc;
+    }
+    auto kern = paged_tc_kernel<KV, D, GH>;
+    constexpr size_t smem = size_t(C::kBarOff) + sizeof(Bars) + 1024;
+    static_assert(smem <= 227 * 1024, "shared memory");
+    static int smem_set[64] = {};
+    const int rc =
+        hs_host::ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem, smem_set);
+    if (rc != HS_OK) return rc;
+    return hs_host::launch_pdl(kern, dim3(a.ctas), dim3(kThreads), smem, stream, t, m[0], m[1],
+                               m[2], m[3]);
+}
+
+template <int KV>
+int launch_kind(const PagedArgs& a, int d, int group, hs_stream_t stream) {
+    if constexpr (KV != kE4m3) {
+        if (d == 64)
+            return group <= 8 ? launch_one<KV, 64, 1>(a, stream)
+                              : launch_one<KV, 64, 2>(a, stream);
+    }
+    if (d == 128)
+        return group <= 8 ? launch_one<KV, 128, 1>(a, stream) : launch_one<KV, 128, 2>(a, stream);
+    return group <= 8 ? launch_one<KV, 256, 1>(a, stream) : launch_one<KV, 256, 2>(a, stream);
+}
+
+}  // namespace tc
+}  // namespace hs_paged
