@@ -75,19 +75,12 @@ constexpr int kMergeThreads = 256;
 constexpr int kScoreThreads = 128;
 constexpr int kScoreTokens = 4 * kScoreThreads;  // tokens of one scoring step
 
-__device__ __forceinline__ Plan load_plan(const PagedArgs& a) {
-    Plan p;
-    p.hs = a.plan[0];
-    p.n = a.plan[1];
-    p.chunks = a.plan[2];
-    p.tiles = int64_t(a.plan[8 + a.rows]) * p.chunks;
-    return p;
-}
-
 // Merge of the units whose tiles were dealt to several CTAs (the others were
 // written by their CTA): out = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p.
-// One block per (request, head); a warp reads every eighth partial row, so
-// all loads of a merge are in flight at once.
+// A block takes every gridDim.y-th head of a request; a warp reads every
+// eighth partial row, so all loads of a merge are in flight at once.  The
+// plan depends on seq_lens alone, which no longer changes once the attention
+// kernel lets this one start, so it is found while that kernel still runs.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) merge_units(const __grid_constant__ PagedArgs a,
                                                              int out_bf16) {
@@ -96,21 +89,48 @@ __global__ void __launch_bounds__(kMergeThreads) merge_units(const __grid_consta
     constexpr int PL = V4 > 32 ? V4 / 32 : 1;    // float4s of a lane
     __shared__ float wt[kMaxCtas];
     __shared__ float red[NW];
+    __shared__ int sums[NW][4];
     __shared__ float4 acc[NW][V4];
     hs::pdl_trigger();
-    hs::pdl_wait();
-    const Plan pl = load_plan(a);
-    const int GM = a.plan[3];
-    const int group = a.heads / a.kv_heads, gch = (group + GM - 1) / GM;
+    const int group = a.heads / a.kv_heads, gch = (group + a.gm - 1) / a.gm;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    for (int64_t qh = blockIdx.x; qh < int64_t(a.rows) * a.heads; qh += gridDim.x) {
-        const int row = int(qh / a.heads), h = int(qh % a.heads);
+    const int row = blockIdx.x;
+    int n[4] = {0, 0, 0, 0};  // tiles of all rows, and of those before this one, both ways
+    for (int r = tid; r < a.rows; r += kMergeThreads) {
+        const int len = a.seq_lens[r];
+        const int n0 = tiling_of(a, len, a.lth[0]).n, n1 = tiling_of(a, len, a.lth[1]).n;
+        n[0] += n0;
+        n[1] += n1;
+        if (r < row) {
+            n[2] += n0;
+            n[3] += n1;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) n[i] = __reduce_add_sync(0xffffffffu, n[i]);
+    if (lane == 0)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sums[warp][i] = n[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        n[i] = 0;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) n[i] += sums[w][i];
+    }
+    const int way = way_of(a, n[0]);
+    const Plan pl = plan_of(a, way, way == 0 ? n[0] : n[1]);
+    const int row_tiles = tiling_of(a, a.seq_lens[row], a.lth[way]).n;
+    const int first_tile = (way == 0 ? n[2] : n[3]) * a.chunks[way];
+    const int hs = a.hs[way];
+    hs::pdl_wait();
+    for (int h = blockIdx.y; h < a.heads; h += gridDim.y) {
         const int kvh = h / group, gi = h % group;
-        const int chunk = kvh / pl.hs * gch + gi / GM;
-        const int hu = (kvh % pl.hs) * GM + gi % GM;
-        const int p0 = a.plan[8 + row], nt = a.plan[9 + row] - p0;
-        const int64_t start = int64_t(p0) * pl.chunks + int64_t(chunk) * nt;
-        const int c0 = run_of(pl, start), c1 = run_of(pl, start + nt - 1);
+        const int64_t qh = int64_t(row) * a.heads + h;
+        const int chunk = kvh / hs * gch + gi / a.gm;
+        const int hu = (kvh % hs) * a.gm + gi % a.gm;
+        const int start = first_tile + chunk * row_tiles;
+        const int c0 = run_of(pl, start), c1 = run_of(pl, start + row_tiles - 1);
         if (c0 == c1) continue;
         const int parts = c1 - c0 + 1;
         // Only the first CTA's part can sit in its second slot.
@@ -200,15 +220,15 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const __grid_const
     hs::pdl_trigger();
     hs::pdl_wait();
     const int row = blockIdx.x / blocks_per_row, part = blockIdx.x % blocks_per_row;
-    const int T = min(max(a.seq_lens[row], 0), a.max_len);
-    const Visible vis = visible_of(a.seq_lens[row], a.max_len, a.window, a.sinks);
+    const Tiling vis = tiling_of(a, a.seq_lens[row], 0);
+    const int nvis = vis.T - vis.w0 + vis.sc;
     float* score = a.score + int64_t(row) * a.score_stride;
     const float* lse2 = a.lse2 + int64_t(row) * a.heads;
     // The visible tokens.
-    for (int64_t i0 = int64_t(part) * kScoreTokens; i0 < vis.n;
+    for (int64_t i0 = int64_t(part) * kScoreTokens; i0 < nvis;
          i0 += int64_t(blocks_per_row) * kScoreTokens) {
         const int i = int(i0) + 4 * threadIdx.x;
-        if (i >= vis.n) break;
+        if (i >= nvis) break;
         float w[4] = {0.f, 0.f, 0.f, 0.f};
         const float* x = a.logits + int64_t(row) * a.heads * a.logit_stride + i;
 #pragma unroll 8
@@ -224,7 +244,7 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const __grid_const
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if (i + j >= vis.n) break;
+            if (i + j >= nvis) break;
             const int t = i + j < vis.sc ? i + j : i + j - vis.sc + vis.w0;
             score[t] = a.decay == 0.f ? w[j] : fmaf(a.decay, score[t], w[j]);
         }
@@ -237,15 +257,15 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const __grid_const
 }
 
 struct Layout {
-    int64_t plan, lse2, ml, o, logits, total, logit_stride;
+    int64_t lse2, ml, o, logits, total, logit_stride;
     int32_t unit_heads, ctas;
 };
 
 int64_t up(int64_t x, int64_t q) { return (x + q - 1) / q * q; }
 
-// Workspace: the plan, the partial states (two slots per CTA: the unit that
-// its run begins in and the one that it ends in) and, for scored calls, the
-// log2 LSE and the logits.  Nothing in it survives a call.
+// Workspace: the partial states (two slots per CTA: the unit that its run
+// begins in and the one that it ends in) and, for scored calls, the log2 LSE
+// and the logits.  Nothing in it survives a call.
 Layout layout(int32_t rows, int32_t heads, int32_t kv_heads, int32_t d, int32_t max_len,
               int32_t window, int32_t sinks, bool scored) {
     Layout w;
@@ -263,7 +283,6 @@ Layout layout(int32_t rows, int32_t heads, int32_t kv_heads, int32_t d, int32_t 
         at += up(bytes, 256);
         return here;
     };
-    w.plan = take((8 + int64_t(rows) + 1) * 4);
     w.lse2 = take(scored ? int64_t(rows) * heads * 4 : 0);
     w.ml = take(int64_t(2) * w.ctas * w.unit_heads * 2 * 4);
     w.o = take(int64_t(2) * w.ctas * w.unit_heads * d * 4);
@@ -312,7 +331,10 @@ extern "C" int hs_paged_decode(const void* q, int64_t q_stride, int32_t q_dtype,
         (kv_dtype != HS_E4M3 && kv_dtype != q_dtype) ||
         (kv_dtype != HS_E4M3 && (k_scale != nullptr || v_scale != nullptr)))
         return HS_ERR_UNSUPPORTED;
-    if (rows > kMaxRows) return HS_ERR_CAPACITY;
+    // Tiles (of 16 tokens of a KV head at least) are counted in 31 bits.
+    if (rows > kMaxRows ||
+        int64_t(rows) * heads * (int64_t(max_len) / 16 + 2) >= (int64_t(1) << 31))
+        return HS_ERR_CAPACITY;
     if (rows == 0) return HS_OK;
     if (q == nullptr || k == nullptr || v == nullptr || seq_lens == nullptr || out == nullptr ||
         (block_table == nullptr && max_len > 0))
@@ -358,7 +380,6 @@ extern "C" int hs_paged_decode(const void* q, int64_t q_stride, int32_t q_dtype,
     a.score = score;
     a.score_stride = score_stride;
     a.decay = score_decay;
-    a.plan = reinterpret_cast<int32_t*>(ws + w.plan);
     a.lse2 = score != nullptr ? reinterpret_cast<float*>(ws + w.lse2) : nullptr;
     a.part_ml = reinterpret_cast<float*>(ws + w.ml);
     a.part_o = reinterpret_cast<float*>(ws + w.o);
@@ -376,9 +397,10 @@ extern "C" int hs_paged_decode(const void* q, int64_t q_stride, int32_t q_dtype,
     else if (kv_dtype == HS_FP16) rc = launch_fp16(a, d, group, stream);
     else rc = launch_e4m3(a, d, group, stream);
     if (rc != HS_OK) return rc;
-    const int blocks = int(hs::min64(int64_t(rows) * heads, 4 * int64_t(w.ctas)));
+    // A block per head where the blocks of a wave suffice, else several heads.
+    const int by = int(hs::max64(1, hs::min64(heads, 4 * int64_t(w.ctas) / rows)));
     const int bf = q_dtype == HS_BF16;
-    const dim3 mg(blocks), mt(kMergeThreads);
+    const dim3 mg{unsigned(rows), unsigned(by)}, mt{kMergeThreads};
     if (d == 64) rc = hs_host::launch_pdl(merge_units<64>, mg, mt, 0, stream, a, bf);
     else if (d == 128) rc = hs_host::launch_pdl(merge_units<128>, mg, mt, 0, stream, a, bf);
     else rc = hs_host::launch_pdl(merge_units<256>, mg, mt, 0, stream, a, bf);

@@ -37,8 +37,10 @@ struct PagedArgs {
     float* score;       // [rows, score_stride] or nullptr
     int64_t score_stride;
     float decay;
+    // The two ways to cut the call (below).
+    int32_t hs[2], lth[2], chunks[2], gm;
+    int64_t wide_tiles;  // tiles (way 0) from which way 0 is taken
     // Workspace.
-    int32_t* plan;      // [8] header, then prefix [rows + 1]
     float* lse2;        // [rows, heads] log2 units (scored calls)
     float* part_ml;     // [2 * ctas][unit heads][2]
     float* part_o;      // [2 * ctas][unit heads][D]
@@ -49,46 +51,184 @@ struct PagedArgs {
     int32_t* status;
 };
 
-// Tokens a request attends to: its last `window` (all without a window) and
-// the first `sinks` before them.  Index i of them is token
-// i < sc ? i : i - sc + w0.
-struct Visible {
-    int n, sc, w0;
+// How a call is cut into work.  A unit is one request x one chunk of its
+// heads (hs KV heads, up to gm query heads of each); its tokens are cut into
+// tiles of 2^lth.  The units' tiles, one after another, are dealt to the CTAs
+// in equal contiguous runs, so ragged batches load every SM alike and one
+// long context uses all of them.  There are two ways: units of as many heads
+// as a tile holds (way 0: long DRAM pieces), or of one (way 1: small calls,
+// fewer parts to merge); the kernels take one by the tiles that they find.
+
+// Token tiles of a request: those of the sinks, then those of the window,
+// both on the grid of 2^lth tokens.  Attended are the first sc tokens and
+// those from w0 on.
+struct Tiling {
+    int T, sc, w0, ns, tw0, n;
 };
-__device__ __forceinline__ Visible visible_of(int len, int max_len, int window, int sinks) {
-    const int T = min(max(len, 0), max_len);
-    Visible v;
-    const int wc = window > 0 ? min(T, window) : T;
-    v.w0 = T - wc;
-    v.sc = window > 0 ? min(sinks, v.w0) : 0;
-    v.n = wc + v.sc;
+__device__ __forceinline__ Tiling tiling_of(const PagedArgs& a, int len, int lth) {
+    Tiling v;
+    v.T = min(max(len, 0), a.max_len);
+    const int wc = a.window > 0 ? min(v.T, a.window) : v.T;
+    v.w0 = v.T - wc;
+    v.sc = a.window > 0 ? min(a.sinks, v.w0) : 0;
+    v.tw0 = v.w0 >> lth;
+    const int up = (1 << lth) - 1;
+    v.ns = min((v.sc + up) >> lth, v.tw0);
+    v.n = max(1, v.ns + ((v.T + up) >> lth) - v.tw0);
     return v;
 }
 
-// The plan, the same in every CTA.  A unit is one request x one chunk of its
-// heads (hs KV heads x up to GM query heads of each); its tokens are cut into
-// tiles of ts = warps / hs steps of 16.  The units' tiles, one after another,
-// are dealt to n CTAs in equal contiguous runs, so ragged batches load every
-// SM alike and one long context uses all of them.
-struct Plan {
-    int hs, n, chunks;
-    int64_t tiles;
+// Walks the tiles of a CTA's run; every role of the CTA walks alike.
+struct Cursor {
+    int row, chunk, tile, left;  // left: tiles of the run still to come, this one included
+    bool first;                  // this tile starts a segment (a unit, or the run)
+    Tiling v;
 };
-__device__ __forceinline__ int64_t run_begin(const Plan& p, int c) {
-    return p.tiles * c / p.n;
+__device__ __forceinline__ void cursor_row(Cursor& c, const PagedArgs& a, int lth) {
+    c.v = tiling_of(a, __ldg(a.seq_lens + c.row), lth);
 }
-__device__ __forceinline__ int run_of(const Plan& p, int64_t tile) {
-    int c = int(tile * p.n / p.tiles);
-    while (c > 0 && run_begin(p, c) > tile) --c;
+__device__ __forceinline__ bool last_of_segment(const Cursor& c) {
+    return c.left == 1 || c.tile == c.v.n - 1;
+}
+__device__ __forceinline__ void advance(Cursor& c, const PagedArgs& a, int chunks, int lth) {
+    c.first = false;
+    --c.left;
+    if (++c.tile < c.v.n || c.left == 0) return;
+    c.tile = 0;
+    c.first = true;
+    if (++c.chunk < chunks) return;
+    c.chunk = 0;
+    ++c.row;
+    cursor_row(c, a, lth);
+}
+__device__ __forceinline__ int tile_token(const Cursor& c, int lth) {
+    return (c.tile < c.v.ns ? c.tile : c.tile - c.v.ns + c.v.tw0) << lth;
+}
+__device__ __forceinline__ bool visible(const Tiling& v, int t) {
+    return t < v.T && (t < v.sc || t >= v.w0);
+}
+// Place of an attended token among them.
+__device__ __forceinline__ int visible_index(const Tiling& v, int t) {
+    return t < v.sc ? t : t - v.w0 + v.sc;
+}
+// Whether any of the tokens [t, t + n) is attended to.
+__device__ __forceinline__ bool any_visible(const Tiling& v, int t, int n) {
+    return t < v.T && (t < v.sc || t + n > v.w0);
+}
+
+// The runs of tiles of a call.
+struct Plan {
+    int tiles, n;   // tiles of the call, CTAs that share them
+    int per, rest;  // tiles / n, tiles % n
+};
+__device__ __forceinline__ Plan plan_of(const PagedArgs& a, int way, int total) {
+    Plan p;
+    p.tiles = total * a.chunks[way];
+    p.n = max(1, min(a.ctas, p.tiles));
+    p.per = p.tiles / p.n;
+    p.rest = p.tiles - p.per * p.n;
+    return p;
+}
+// floor(tiles c / n)
+__device__ __forceinline__ int run_begin(const Plan& p, int c) {
+    return p.per * c + p.rest * c / p.n;
+}
+__device__ __forceinline__ int run_of(const Plan& p, int tile) {
+    int c = min(p.n - 1, tile / max(1, p.per));
+    while (run_begin(p, c) > tile) --c;
     while (c + 1 < p.n && run_begin(p, c + 1) <= tile) ++c;
     return c;
 }
+__device__ __forceinline__ int way_of(const PagedArgs& a, int total0) {
+    return int64_t(total0) * a.chunks[0] >= a.wide_tiles ? 0 : 1;
+}
 
-int launch_bf16(const PagedArgs& a, int d, int group, hs_stream_t stream);
-int launch_fp16(const PagedArgs& a, int d, int group, hs_stream_t stream);
-int launch_e4m3(const PagedArgs& a, int d, int group, hs_stream_t stream);
-int launch_tc_bf16(const PagedArgs& a, int d, int group, hs_stream_t stream);
-int launch_tc_fp16(const PagedArgs& a, int d, int group, hs_stream_t stream);
-int launch_tc_e4m3(const PagedArgs& a, int d, int group, hs_stream_t stream);
+// One CTA's run: its tiles and where they begin.
+struct Run {
+    int way, chunks, w0, run, row, row_tile0;
+};
+// Called by all THREADS threads of the CTA; `scratch` and `first` (two ints)
+// in shared memory.
+template <int THREADS>
+__device__ __forceinline__ Run make_run(const PagedArgs& a, int cta, int32_t (*scratch)[32],
+                                        int32_t* first) {
+    const int tid = threadIdx.x;
+    int n0 = 0, n1 = 0;
+    for (int r = tid; r < a.rows; r += THREADS) {
+        const int len = __ldg(a.seq_lens + r);
+        n0 += tiling_of(a, len, a.lth[0]).n;
+        n1 += tiling_of(a, len, a.lth[1]).n;
+        if (cta == 0 && len > a.max_len) hs::set_status(a.status, HS_ERR_BAD_INDEX);
+    }
+    int total0, total1;
+    const int before0 = hs::block_excl_scan(n0, scratch[0], &total0);
+    const int before1 = hs::block_excl_scan(n1, scratch[1], &total1);
+    Run x;
+    x.way = way_of(a, total0);
+    x.chunks = a.chunks[x.way];
+    const Plan pl = plan_of(a, x.way, x.way == 0 ? total0 : total1);
+    x.w0 = cta < pl.n ? run_begin(pl, cta) : 0;
+    x.run = cta < pl.n ? run_begin(pl, cta + 1) - x.w0 : 0;
+    // The row that the run begins in.
+    auto place = [&](int r, int at, int n) {
+        if (at * x.chunks <= x.w0 && x.w0 < (at + n) * x.chunks) {
+            first[0] = r;
+            first[1] = at;
+        }
+    };
+    if (a.rows <= THREADS) {
+        if (tid < a.rows) place(tid, x.way == 0 ? before0 : before1, x.way == 0 ? n0 : n1);
+    } else {
+        int carry = 0;
+        for (int r0 = 0; r0 < a.rows; r0 += THREADS) {
+            const int r = r0 + tid;
+            const int n =
+                r < a.rows ? tiling_of(a, __ldg(a.seq_lens + r), a.lth[x.way]).n : 0;
+            __syncthreads();
+            int sum;
+            const int at = carry + hs::block_excl_scan(n, scratch[0], &sum);
+            if (r < a.rows) place(r, at, n);
+            carry += sum;
+        }
+    }
+    __syncthreads();
+    x.row = first[0];
+    x.row_tile0 = first[1];
+    return x;
+}
+__device__ __forceinline__ Cursor cursor_at(const PagedArgs& a, const Run& x) {
+    Cursor c;
+    c.row = x.row;
+    cursor_row(c, a, a.lth[x.way]);
+    const uint32_t rel = uint32_t(x.w0) - uint32_t(x.row_tile0) * uint32_t(x.chunks);
+    c.chunk = int(rel / uint32_t(c.v.n));
+    c.tile = int(rel) - c.chunk * c.v.n;
+    c.left = x.run;
+    c.first = true;
+    return c;
+}
+
+// Host: the two ways of a kernel whose tiles have tile_rows cache rows and at
+// most hs_max heads.
+inline void set_ways(PagedArgs& a, int hs_max, int tile_rows, int gm, int tiles_for_wide) {
+    const int gch = (a.heads / a.kv_heads + gm - 1) / gm;
+    int hs = 1;
+    while (hs < hs_max && a.kv_heads % (2 * hs) == 0) hs *= 2;
+    for (int way = 0; way < 2; ++way) {
+        a.hs[way] = way == 0 ? hs : 1;
+        a.lth[way] = 0;
+        while ((a.hs[way] << (a.lth[way] + 1)) <= tile_rows) ++a.lth[way];
+        a.chunks[way] = a.kv_heads / a.hs[way] * gch;
+    }
+    a.gm = gm;
+    a.wide_tiles = int64_t(a.ctas) * tiles_for_wide;
+}
+
+int launch_bf16(PagedArgs& a, int d, int group, hs_stream_t stream);
+int launch_fp16(PagedArgs& a, int d, int group, hs_stream_t stream);
+int launch_e4m3(PagedArgs& a, int d, int group, hs_stream_t stream);
+int launch_tc_bf16(PagedArgs& a, int d, int group, hs_stream_t stream);
+int launch_tc_fp16(PagedArgs& a, int d, int group, hs_stream_t stream);
+int launch_tc_e4m3(PagedArgs& a, int d, int group, hs_stream_t stream);
 
 }  // namespace hs_paged

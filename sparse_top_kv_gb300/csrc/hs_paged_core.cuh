@@ -26,6 +26,8 @@
 namespace hs_paged {
 namespace core {
 
+constexpr int kTilesForWide = 16;  // tiles per CTA from which units take several heads
+
 enum Kind { kBf16 = 0, kFp16 = 1, kE4m3 = 2 };
 
 template <int KV, int D, int GH_>
@@ -147,66 +149,21 @@ paged_kernel(const __grid_constant__ PagedArgs a) {
     extern __shared__ __align__(128) unsigned char smem[];
     unsigned char* body = smem;                                      // ring / reduction
     uint32_t* live_s = reinterpret_cast<uint32_t*>(smem + C::kBody);  // [NW][S]
-    int32_t* scratch = reinterpret_cast<int32_t*>(live_s + NW * S);   // [32]
-    int32_t* prefix = scratch + 32;                                  // [rows + 1]
+    __shared__ int32_t scratch[2][32];
+    __shared__ int32_t first[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
 
-    hs::pdl_trigger();
     hs::pdl_wait();
+    hs::pdl_trigger();
 
-    // ---- The plan -------------------------------------------------------
     const int group = a.heads / a.kv_heads;
     const int gch = (group + GM - 1) / GM;
-    Plan pl;
-    {
-        int mine = 0;
-        for (int r = tid; r < a.rows; r += C::kThreads) {
-            const int n = visible_of(a.seq_lens[r], a.max_len, a.window, a.sinks).n;
-            mine += max(1, (n + kKey - 1) / kKey);
-        }
-        int total;
-        hs::block_excl_scan(mine, scratch, &total);
-        int hs_max = 1;
-        while (hs_max < NW && a.kv_heads % (2 * hs_max) == 0) hs_max *= 2;
-        const int64_t steps = int64_t(total) * a.kv_heads * gch / NW;
-        pl.hs = steps >= int64_t(a.ctas) * 16 ? hs_max : 1;
-        const int ts = NW / pl.hs;
-        int carry = 0;
-        for (int r0 = 0; r0 < a.rows; r0 += C::kThreads) {
-            const int r = r0 + tid;
-            int tl = 0;
-            if (r < a.rows) {
-                const int len = a.seq_lens[r];
-                const int n = visible_of(len, a.max_len, a.window, a.sinks).n;
-                tl = max(1, (n + kKey * ts - 1) / (kKey * ts));
-                if (blockIdx.x == 0 && len > a.max_len) hs::set_status(a.status, HS_ERR_BAD_INDEX);
-            }
-            __syncthreads();
-            int sum;
-            const int ex = hs::block_excl_scan(tl, scratch, &sum);
-            if (r < a.rows) prefix[r] = carry + ex;
-            carry += sum;
-        }
-        if (tid == 0) prefix[a.rows] = carry;
-        pl.chunks = a.kv_heads / pl.hs * gch;
-        pl.tiles = int64_t(carry) * pl.chunks;
-        pl.n = int(hs::max64(1, hs::min64(a.ctas, pl.tiles / 2)));
-        __syncthreads();
-        if (blockIdx.x == 0) {
-            for (int r = tid; r <= a.rows; r += C::kThreads) a.plan[8 + r] = prefix[r];
-            if (tid == 0) {
-                a.plan[0] = pl.hs;
-                a.plan[1] = pl.n;
-                a.plan[2] = pl.chunks;
-                a.plan[3] = GM;
-            }
-        }
-    }
     const int cta = blockIdx.x;
-    if (cta >= pl.n) return;
-    const int hsn = pl.hs, ts = NW / hsn;
-    const int64_t w0 = run_begin(pl, cta), w1 = run_begin(pl, cta + 1);
+    const Run rn = make_run<C::kThreads>(a, cta, scratch, first);
+    if (rn.run <= 0) return;
+    const int way = rn.way, lth = a.lth[way];
+    const int hsn = a.hs[way], ts = NW / hsn;
     const int hl = warp % hsn, tg = warp / hsn;
     const uint32_t ring = hs::smem_u32(body) + uint32_t(warp) * (S * C::kStage);
     uint32_t* live_w = live_s + warp * S;
@@ -214,28 +171,18 @@ paged_kernel(const __grid_constant__ PagedArgs a) {
     const int mi = lane >> 3, r8 = lane & 7;
     bool bad = false;
 
-    for (int64_t w = w0; w < w1;) {
-        // ---- The unit that tile w belongs to ------------------------------
-        int lo = 0, hi = a.rows - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (int64_t(prefix[mid]) * pl.chunks <= w) lo = mid;
-            else hi = mid - 1;
-        }
-        const int row = lo;
-        const int row_tiles = prefix[row + 1] - prefix[row];
-        const int64_t rel = w - int64_t(prefix[row]) * pl.chunks;
-        const int chunk = int(rel / row_tiles);
-        const int tile0 = int(rel - int64_t(chunk) * row_tiles);
-        const int tile1 = int(hs::min64(row_tiles, tile0 + (w1 - w)));
-        const bool whole = tile0 == 0 && tile1 == row_tiles;
-        const int slot = 2 * cta + (tile0 == 0 && w != w0 ? 1 : 0);
-        w += tile1 - tile0;
-        const int kvh0 = chunk / gch * hsn, gc = chunk % gch;
+    Cursor c = cursor_at(a, rn);
+    for (bool begin = true; c.left > 0; begin = false) {
+        // ---- One segment: the tiles of one unit in this run ----------------
+        const int row = c.row;
+        const Tiling vis = c.v;
+        const int tile0 = c.tile, steps = min(c.left, vis.n - tile0);
+        const bool whole = steps == vis.n;
+        const int slot = 2 * cta + (tile0 == 0 && !begin ? 1 : 0);
+        const int kvh0 = c.chunk / gch * hsn, gc = c.chunk % gch;
         const int kvh = kvh0 + hl;
         const int Gc = min(GM, group - gc * GM);
         const int h0 = kvh * group + gc * GM;
-        const Visible vis = visible_of(a.seq_lens[row], a.max_len, a.window, a.sinks);
 
         // ---- Query fragments ---------------------------------------------
         uint32_t qa[D / 16][2 * GH];
@@ -312,13 +259,16 @@ paged_kernel(const __grid_constant__ PagedArgs a) {
         const int32_t* table = a.block_table + int64_t(row) * a.bt_stride;
         const char* kb = static_cast<const char*>(a.k) + int64_t(kvh) * a.head_stride * C::kElt;
         const char* vb = static_cast<const char*>(a.v) + int64_t(kvh) * a.head_stride * C::kElt;
-        const int steps = tile1 - tile0;
         // Lane l < 16 looks up token l of a step: its page one step before it
         // is needed.
-        auto token = [&](int j) {  // -1: outside the unit's tokens
-            const int i = ((tile0 + j) * ts + tg) * kKey + (lane & 15);
-            if (j >= steps || i >= vis.n) return -1;
-            return i < vis.sc ? i : i - vis.sc + vis.w0;
+        auto block_token = [&](int j) {  // first token of this warp's block of a step
+            Cursor x = c;
+            x.tile = tile0 + j;
+            return tile_token(x, lth) + tg * kKey;
+        };
+        auto token = [&](int j) {  // -1: not attended to
+            const int tok = block_token(j) + (lane & 15);
+            return j < steps && visible(vis, tok) ? tok : -1;
         };
         int tok_n = token(0);
         int page_n = tok_n >= 0 ? __ldg(table + tok_n / a.page_size) : -1;
@@ -408,10 +358,13 @@ paged_kernel(const __grid_constant__ PagedArgs a) {
                     x[i] = (mask >> key) & 1u ? x[i] * qs[hh] : -CUDART_INF_F;
                 }
                 if (a.logits != nullptr && g + 8 * hh < Gc) {
-                    const int i0 = ((tile0 + j) * ts + tg) * kKey + 2 * t;
-                    float* lp = a.logits + (int64_t(row) * a.heads + h0 + g + 8 * hh) * a.logit_stride + i0;
-                    if (i0 < vis.n) *reinterpret_cast<float2*>(lp) = make_float2(x[0], x[1]);
-                    if (i0 + 8 < vis.n) *reinterpret_cast<float2*>(lp + 8) = make_float2(x[2], x[3]);
+                    float* lp = a.logits +
+                                (int64_t(row) * a.heads + h0 + g + 8 * hh) * a.logit_stride;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int tok = block_token(j) + (i >> 1) * 8 + 2 * t + (i & 1);
+                        if (visible(vis, tok)) lp[visible_index(vis, tok)] = x[i];
+                    }
                 }
                 float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -560,15 +513,19 @@ paged_kernel(const __grid_constant__ PagedArgs a) {
             }
         }
         __syncthreads();  // the reduction's buffer becomes the next unit's ring
+        c.left -= steps - 1;
+        c.tile += steps - 1;
+        advance(c, a, rn.chunks, lth);
     }
     if (bad) hs::set_status(a.status, HS_ERR_BAD_INDEX);
 }
 
 template <int KV, int D, int GH>
-int launch_one(const PagedArgs& a, hs_stream_t stream) {
+int launch_one(PagedArgs& a, hs_stream_t stream) {
     using C = Cfg<KV, D, GH>;
     auto kern = paged_kernel<KV, D, GH>;
-    const size_t smem = C::kBody + C::kWarps * C::kStages * 4 + 32 * 4 + (size_t(a.rows) + 1) * 4;
+    set_ways(a, C::kWarps, C::kWarps * kKey, C::GM, kTilesForWide);
+    constexpr size_t smem = C::kBody + C::kWarps * C::kStages * 4;
     static int smem_set[64] = {};
     const int rc =
         hs_host::ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem, smem_set);
@@ -577,7 +534,7 @@ int launch_one(const PagedArgs& a, hs_stream_t stream) {
 }
 
 template <int KV>
-int launch_kind(const PagedArgs& a, int d, int group, hs_stream_t stream) {
+int launch_kind(PagedArgs& a, int d, int group, hs_stream_t stream) {
     if (group <= 8) {
         if (d == 64) return launch_one<KV, 64, 1>(a, stream);
         if (d == 128) return launch_one<KV, 128, 1>(a, stream);

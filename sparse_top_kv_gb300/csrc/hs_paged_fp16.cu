@@ -2,7 +2,7 @@
 #include "hs_paged_core.cuh"
 
 namespace hs_paged {
-int launch_fp16(const PagedArgs& a, int d, int group, hs_stream_t stream) {
+int launch_fp16(PagedArgs& a, int d, int group, hs_stream_t stream) {
     return core::launch_kind<core::kFp16>(a, d, group, stream);
 }
 }  // namespace hs_paged

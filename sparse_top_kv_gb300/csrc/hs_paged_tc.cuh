@@ -51,8 +51,7 @@ constexpr int kRows = 128;           // cache rows of a tile = M of the QK produ
 constexpr int kBlk = kRows * 128;    // one block: 128 rows x 128 bytes
 constexpr int kSoftThreads = 128;    // one softmax group: a thread per row
 constexpr int kGroups = 2;
-constexpr int kTmaWarp = 8, kMmaWarp = 9, kQWarp = 10;
-constexpr int kQThreads = 64;
+constexpr int kTmaWarp = 8, kQkWarp = 9, kPvWarp = 10, kQWarp = 11;
 constexpr int kThreads = 384;
 constexpr int kSoftBar = 1;          // named barriers of the groups: 1, 2
 constexpr int kBothBar = 3;          // and of both
@@ -60,14 +59,11 @@ constexpr int kMaskRing = 16;        // tiles whose loaded runs are remembered
 constexpr float kThresh = 8.f;       // log2 headroom before O is rescaled
 constexpr int kTmemCols = 512;
 constexpr int kBarBytes = 8192;      // shared-memory budget of Bars
+constexpr int kTilesForWide = 4;     // tiles per CTA from which units take several heads
 
-// Two ways to cut a unit: all heads that a tile can hold (long DRAM pieces),
-// or one head per unit (small problems: more tokens per tile, fewer parts to
-// merge).  The kernel takes one by the amount of work it finds.
 struct TcArgs {
     PagedArgs p;
-    int32_t hs[2], bt[2];
-    int32_t steps_for_wide;  // tiles per CTA from which the first way is taken
+    int32_t bt[2];
     uint64_t timeout_ns;
 };
 
@@ -112,15 +108,16 @@ struct Cfg {
 struct Bars {
     uint64_t kfull[8], kempty[8], vfull[8], vempty[8];
     uint64_t s_full[2], p_full[2], pv_done[2];
-    uint64_t q_full, q_empty, o_free, drain;
+    uint64_t q_full, q_empty, o_free, drain[2];
     uint32_t tmem_base;
     volatile int32_t abort;
-    int32_t start_row, start_tile;      // the run's first row and that row's first tile
-    int32_t scratch[32];
+    int32_t start_row[2];               // the run's first row and that row's first tile
+    int32_t scratch[2][32];
     uint32_t loaded[kMaskRing];         // runs of a tile that were loaded
-    float red[kGroups][8][16];          // per 16 rows: maxima or sums
+    alignas(16) float red[kGroups][8][16];  // per 16 rows: maxima or sums
     float alpha[kGroups][8][16];        // rescale factors, [head][query]
     float ml[kGroups][8][16][2];        // epilogue: (m, l), [head][query]
+    float weight[kGroups][8][16];       // and the groups' factors of the output
     float qscale[4][128];    // E4M3: factor of each query's logits, by segment
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barrier block");
@@ -171,69 +168,6 @@ __device__ __forceinline__ uint32_t idesc(int N, int a_mn_major) {
            (uint32_t(N >> 3) << 17) | (uint32_t(kRows >> 4) << 24);
 }
 
-// Token tiles of a request: those of the sinks, then those of the window,
-// both on the grid of th tokens, so that boxes start on whole runs.
-struct Tiling {
-    int T, sc, w0, ns, tw0, n;
-};
-__device__ __forceinline__ Tiling tiling_of(const PagedArgs& a, int len, int th) {
-    Tiling v;
-    v.T = min(max(len, 0), a.max_len);
-    const int wc = a.window > 0 ? min(v.T, a.window) : v.T;
-    v.w0 = v.T - wc;
-    v.sc = a.window > 0 ? min(a.sinks, v.w0) : 0;
-    v.tw0 = v.w0 / th;
-    v.ns = min((v.sc + th - 1) / th, v.tw0);
-    v.n = max(1, v.ns + (v.T + th - 1) / th - v.tw0);
-    return v;
-}
-
-// Walks the tiles of a CTA's run; every role of the CTA walks alike.
-struct Cursor {
-    int row, chunk, tile, left;  // left: tiles of the run still to come, this one included
-    bool first;                  // this tile starts a segment (a unit, or the run)
-    Tiling v;
-};
-__device__ __forceinline__ void cursor_row(Cursor& c, const PagedArgs& a, int th) {
-    c.v = tiling_of(a, __ldg(a.seq_lens + c.row), th);
-}
-__device__ __forceinline__ Cursor cursor_at(const PagedArgs& a, const Plan& pl, int row,
-                                            int row_tile0, int64_t w, int64_t w1, int th) {
-    Cursor c;
-    c.row = row;
-    cursor_row(c, a, th);
-    const int64_t rel = w - int64_t(row_tile0) * pl.chunks;
-    c.chunk = int(rel / c.v.n);
-    c.tile = int(rel - int64_t(c.chunk) * c.v.n);
-    c.left = int(w1 - w);
-    c.first = true;
-    return c;
-}
-__device__ __forceinline__ bool last_of_segment(const Cursor& c) {
-    return c.left == 1 || c.tile == c.v.n - 1;
-}
-__device__ __forceinline__ void advance(Cursor& c, const PagedArgs& a, int chunks, int th) {
-    c.first = false;
-    --c.left;
-    if (++c.tile < c.v.n || c.left == 0) return;
-    c.tile = 0;
-    c.first = true;
-    if (++c.chunk < chunks) return;
-    c.chunk = 0;
-    ++c.row;
-    cursor_row(c, a, th);
-}
-__device__ __forceinline__ int tile_token(const Cursor& c, int th) {
-    return (c.tile < c.v.ns ? c.tile : c.tile - c.v.ns + c.v.tw0) * th;
-}
-__device__ __forceinline__ bool visible(const Tiling& v, int t) {
-    return t < v.T && (t < v.sc || t >= v.w0);
-}
-// Whether any of the tokens [t, t + n) is attended to.
-__device__ __forceinline__ bool any_visible(const Tiling& v, int t, int n) {
-    return t < v.T && (t < v.sc || t + n > v.w0);
-}
-
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[N]) {
     if constexpr (N == 8) {
@@ -257,11 +191,22 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[N]) {
     }
 }
 
-__device__ __forceinline__ uint8_t to_e4m3(float x) {
-    return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+// Two fp32 values to E4M3 codes (the first in the low byte) and back.
+__device__ __forceinline__ uint32_t to_e4m3x2(float x, float y) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
 }
-__device__ __forceinline__ float from_e4m3(uint8_t c) {
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
+    return __half22float2(__half2(
+        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3)));
+}
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
+// 2^x (PTX ex2.approx.ftz: within 2 ulp; 0 below -126, where a weight no
+// longer counts against the sum's 1).
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 template <int KV, int D, int GH>
@@ -283,7 +228,6 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
     const uint64_t tmo = ta.timeout_ns;
     const volatile int* abort_flag = &B.abort;
 
-    hs::pdl_trigger();
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             hs::mbar_init(&B.kfull[i], 1);
@@ -296,14 +240,15 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
             hs::mbar_init(&B.p_full[i], kSoftThreads);
             hs::mbar_init(&B.pv_done[i], 1);
         }
-        hs::mbar_init(&B.q_full, kQThreads);
+        hs::mbar_init(&B.q_full, 32);
         hs::mbar_init(&B.q_empty, 1);
         hs::mbar_init(&B.o_free, kGroups * kSoftThreads);
-        hs::mbar_init(&B.drain, 1);
+        hs::mbar_init(&B.drain[0], 1);
+        hs::mbar_init(&B.drain[1], 1);
         B.abort = 0;
         hs::fence_mbar_init();
     }
-    if (warp == kMmaWarp) {
+    if (warp == kPvWarp) {
         hs::tc::tmem_alloc(&B.tmem_base, kTmemCols);
         hs::tc::tmem_relinquish();
     }
@@ -313,90 +258,40 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
             reinterpret_cast<uint4*>(smem + C::kPOff)[i] = make_uint4(0u, 0u, 0u, 0u);
     hs::pdl_wait();
 
-    // ---- The plan (the same in every CTA) ---------------------------------
+    hs::pdl_trigger();
+
     const int group = a.heads / a.kv_heads;
     const int gch = (group + GM - 1) / GM;
     const int cta = blockIdx.x;
-    Plan pl;
-    int mode;
-    int64_t w0 = 0, w1 = 0;  // this CTA's run of tiles
-    {
-        int n0 = 0, n1 = 0;  // tiles of a chunk of heads, both ways
-        for (int r = tid; r < a.rows; r += kThreads) {
-            const int len = __ldg(a.seq_lens + r);
-            n0 += tiling_of(a, len, kRows / ta.hs[0]).n;
-            n1 += tiling_of(a, len, kRows / ta.hs[1]).n;
-            if (cta == 0 && len > a.max_len) hs::set_status(a.status, HS_ERR_BAD_INDEX);
-        }
-        int total0, total1;
-        hs::block_excl_scan(n0, B.scratch, &total0);
-        __syncthreads();
-        hs::block_excl_scan(n1, B.scratch, &total1);
-        const int64_t wide = int64_t(total0) * (a.kv_heads / ta.hs[0]) * gch;
-        mode = wide >= int64_t(a.ctas) * ta.steps_for_wide ? 0 : 1;
-        pl.hs = ta.hs[mode];
-        pl.chunks = a.kv_heads / pl.hs * gch;
-        pl.tiles = int64_t(mode == 0 ? total0 : total1) * pl.chunks;
-        pl.n = int(hs::max64(1, hs::min64(a.ctas, pl.tiles)));
-        if (cta < pl.n) {
-            w0 = run_begin(pl, cta);
-            w1 = run_begin(pl, cta + 1);
-        }
-        // The row that the run begins in; CTA 0 keeps every row's first tile
-        // for the merge.
-        int carry = 0;
-        for (int r0 = 0; r0 < a.rows; r0 += kThreads) {
-            const int r = r0 + tid;
-            const int n =
-                r < a.rows ? tiling_of(a, __ldg(a.seq_lens + r), kRows / pl.hs).n : 0;
-            __syncthreads();
-            int sum;
-            const int at = carry + hs::block_excl_scan(n, B.scratch, &sum);
-            if (r < a.rows) {
-                if (cta == 0) a.plan[8 + r] = at;
-                if (int64_t(at) * pl.chunks <= w0 && w0 < int64_t(at + n) * pl.chunks) {
-                    B.start_row = r;
-                    B.start_tile = at;
-                }
-            }
-            carry += sum;
-        }
-        if (cta == 0 && tid == 0) {
-            a.plan[8 + a.rows] = carry;
-            a.plan[0] = pl.hs;
-            a.plan[1] = pl.n;
-            a.plan[2] = pl.chunks;
-            a.plan[3] = GM;
-        }
-        hs::fence_proxy_async_shared();  // P's zeros, read by the tensor cores
-        hs::tc::fence_before_sync();
-        __syncthreads();
-        hs::tc::fence_after_sync();
-    }
+    const Run rn = make_run<kThreads>(a, cta, B.scratch, B.start_row);
+    const int way = rn.way, chunks = rn.chunks, run = rn.run;
+    const Cursor start = cursor_at(a, rn);
+    hs::fence_proxy_async_shared();  // P's zeros, read by the tensor cores
+    hs::tc::fence_before_sync();
+    __syncthreads();
+    hs::tc::fence_after_sync();
     const uint32_t tmem = B.tmem_base;
-    const int run = int(w1 - w0);
-    const int hsn = pl.hs, bt = ta.bt[mode];
+    const int hsn = a.hs[way], bt = ta.bt[way];
     // hs and bt are powers of two.
     const int lhs = 31 - __clz(hsn), lbt = 31 - __clz(bt);
-    const int th = kRows >> lhs;     // tokens of a tile
-    const int nops = th >> lbt;      // runs (boxes) of a tile
-    const int chunks = pl.chunks;
+    const int lth = a.lth[way];          // log2 of the tokens of a tile
+    const int nops = 1 << (lth - lbt);   // runs (boxes) of a tile
     const int nq = max(16, (hsn * C::NH + 15) / 16 * 16);  // N of the QK product
     const uint32_t o_col = uint32_t(2 * nq);
-    const int ocols = hsn * C::NP;   // output columns of 128 dims
+    const int ocols = hsn * C::NP;       // output columns of 128 dims
 
     if (run <= 0) {
         // Nothing to do: straight to the tear-down.
     } else if (warp == kTmaWarp) {
         // ------------------------------- loads -------------------------------
-        const CUtensorMap* kmap = mode == 0 ? &kmap0 : &kmap1;
-        const CUtensorMap* vmap = mode == 0 ? &vmap0 : &vmap1;
-        Cursor c = cursor_at(a, pl, B.start_row, B.start_tile, w0, w1, th);
+        const CUtensorMap* kmap = way == 0 ? &kmap0 : &kmap1;
+        const CUtensorMap* vmap = way == 0 ? &vmap0 : &vmap1;
+        Cursor c = start;
         bool ok = true, bad = false;
         int kseq = 0, vseq = 0, t = 0;
         // Lane i < nops: run i of the tile; its page is looked up a tile ahead.
         auto lookup = [&](const Cursor& x, int& tok) {
-            tok = lane < nops ? tile_token(x, th) + lane * bt : 0;
+            tok = lane < nops ? tile_token(x, lth) + lane * bt : 0;
             const bool want = lane < nops && any_visible(x.v, tok, bt);
             if (!want) return -2;
             return __ldg(a.block_table + int64_t(x.row) * a.bt_stride + tok / a.page_size);
@@ -406,7 +301,7 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
             const int tok = tok_n, page = page_n;
             const int kvh0 = c.chunk / gch * hsn;
             const bool more = c.left > 1;
-            advance(c, a, chunks, th);
+            advance(c, a, chunks, lth);
             if (more) page_n = lookup(c, tok_n);
             const bool want = page >= 0 && page < a.num_pages;
             if (page != -2 && !want) bad = true;
@@ -452,44 +347,30 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
                 hs::mbar_wait_bounded(&B.vfull[s % NS], (s / NS) & 1, tmo, nullptr);
         }
         if (bad) hs::set_status(a.status, HS_ERR_BAD_INDEX);
-    } else if (warp == kMmaWarp) {
-        // ------------------------------ products -----------------------------
+    } else if (warp == kQkWarp) {
+        // ---------------------------- S^T = K Q^T -----------------------------
         if (lane == 0) {
-            constexpr int kStep = E4 ? 32 : 16;              // rows of a PV K step
-            constexpr int kSteps = kRows / kStep;
-            const uint32_t id_qk = idesc<KV>(nq, 0);
-            // E4M3, runs of 16 rows: a K step holds two heads, taken together.
-            const bool two = E4 && bt < kStep && hsn > 1;
-            const uint32_t id_pv = idesc<KV>(two ? 2 * C::NP : C::NP, 1);
-            // Descriptors of the first tiles; others are an offset (in units
+            const uint32_t id = idesc<KV>(nq, 0);
+            // Descriptors of the first tile; others are an offset (in units
             // of 16 bytes) away.
             const uint64_t k_desc = hs::tc::sdesc_sw128(sb + C::kKOff, 16, 1024);
             const uint64_t q_desc = hs::tc::sdesc_sw128(sb + C::kQOff, 16, 1024);
-            const uint64_t v_desc = hs::tc::sdesc_sw128(sb + C::kVOff, kBlk, 1024);
-            const uint64_t p_desc = hs::tc::sdesc_sw128(sb + C::kPOff, 16, 1024);
-            // Output column of each K step's head, and the steps that hold a
-            // head's first rows.
-            uint32_t col[kSteps], starts = 0;
-#pragma unroll
-            for (int kk = 0; kk < kSteps; ++kk) {
-                const int r = kk * kStep;
-                col[kk] = uint32_t((r >> lbt) & (hsn - 1)) * C::NP;
-                if (r < (hsn << lbt) && (two || (r & (bt - 1)) == 0)) starts |= 1u << kk;
-            }
-            Cursor cq = cursor_at(a, pl, B.start_row, B.start_tile, w0, w1, th);
-            uint32_t first_mask = 0;  // bit t % 4: tile t starts a segment
-            int qseg = 0, oseg = 0, seg_t0 = 0;
-            auto issue_qk = [&](int t) -> bool {
-                if (cq.first) {
-                    if (!hs::mbar_wait_bounded(&B.q_full, qseg & 1, tmo, abort_flag)) return false;
-                    ++qseg;
-                }
-                first_mask = (first_mask & ~(1u << (t & 3))) | (uint32_t(cq.first) << (t & 3));
+            Cursor c = start;
+            bool ok = true;
+            int slot = 0;
+            uint32_t phase = 0;
+            for (int t = 0, seg = 0; t < run; ++t) {
+                if (c.first)
+                    ok = ok && hs::mbar_wait_bounded(&B.q_full, seg++ & 1, tmo, abort_flag);
+                // The softmax of two tiles ago has read this S buffer.
+                if (t >= 2)
+                    ok = ok && hs::mbar_wait_bounded(&B.p_full[t & 1], ((t - 2) >> 1) & 1, tmo,
+                                                     abort_flag);
                 const uint32_t d = tmem + uint32_t((t & 1) * nq);
+#pragma unroll
                 for (int s = 0; s < C::kSubs; ++s) {
-                    const int seq = t * C::kSubs + s, slot = seq % NS;
-                    if (!hs::mbar_wait_bounded(&B.kfull[slot], (seq / NS) & 1, tmo, abort_flag))
-                        return false;
+                    ok = ok && hs::mbar_wait_bounded(&B.kfull[slot], phase, tmo, abort_flag);
+                    if (!ok) break;
                     hs::tc::fence_after_sync();
                     const uint64_t kd = k_desc + uint32_t(slot * (C::kSub >> 4));
                     const uint64_t qd = q_desc + uint32_t(s * C::kSubBlocks * nq * 8);
@@ -498,195 +379,206 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             mma<KV>(d, kd + uint32_t(b * (kBlk >> 4) + kk * 2),
-                                    qd + uint32_t(b * nq * 8 + kk * 2), id_qk,
+                                    qd + uint32_t(b * nq * 8 + kk * 2), id,
                                     (s | b | kk) ? 1u : 0u);
                     }
                     hs::tc::mma_commit(&B.kempty[slot]);
-                }
-                hs::tc::mma_commit(&B.s_full[t & 1]);
-                if (last_of_segment(cq)) hs::tc::mma_commit(&B.q_empty);
-                if (t + 1 < run) advance(cq, a, chunks, th);
-                return true;
-            };
-            auto issue_pv = [&](int t) -> bool {
-                if (!hs::mbar_wait_bounded(&B.p_full[t & 1], (t >> 1) & 1, tmo, abort_flag))
-                    return false;
-                if ((first_mask >> (t & 3)) & 1u) {
-                    // The epilogue of the segment before has read the output.
-                    if (oseg > 0 &&
-                        !hs::mbar_wait_bounded(&B.o_free, (oseg - 1) & 1, tmo, abort_flag))
-                        return false;
-                    ++oseg;
-                    seg_t0 = t;
-                }
-                // A group's first tile of the segment starts its output.
-                const uint32_t fresh = t - seg_t0 < kGroups ? starts : 0u;
-                const uint64_t pd = p_desc + uint32_t((t & 1) * (C::kPBytes >> 4));
-                for (int s = 0; s < C::kSubs; ++s) {
-                    const int seq = t * C::kSubs + s, slot = seq % NS;
-                    if (!hs::mbar_wait_bounded(&B.vfull[slot], (seq / NS) & 1, tmo, abort_flag))
-                        return false;
-                    hs::tc::fence_after_sync();
-                    const uint64_t vd = v_desc + uint32_t(slot * (C::kSub >> 4));
-                    const uint32_t d = tmem + o_col + uint32_t(((t & 1) * C::kSubs + s) * ocols);
-#pragma unroll
-                    for (int kk = 0; kk < kSteps; ++kk)
-                        mma<KV>(d + col[kk], vd + uint32_t(kk * kStep * 8),
-                                pd + uint32_t(E4 ? kk * 2 : (kk >> 2) * (C::NP * 8) + (kk & 3) * 2),
-                                id_pv, ((fresh >> kk) & 1u) ^ 1u);
-                    hs::tc::mma_commit(&B.vempty[slot]);
-                }
-                hs::tc::mma_commit(&B.pv_done[t & 1]);
-                return true;
-            };
-            // QK runs at most one tile ahead of PV (its S buffer); whichever
-            // has its operands goes first.
-            bool ok = issue_qk(0);
-            uint64_t since = 0;  // start of the wait for either
-            uint32_t polls = 0;
-            for (int t = 0, q = 1; t < run && ok;) {
-                if (q == run || q > t + 1) {
-                    ok = issue_pv(t++);
-                    continue;
-                }
-                const int ks = q * C::kSubs, vs = t * C::kSubs;
-                if (mbar_test(&B.kfull[ks % NS], (ks / NS) & 1)) {
-                    ok = issue_qk(q++);
-                } else if (mbar_test(&B.p_full[t & 1], (t >> 1) & 1) &&
-                           mbar_test(&B.vfull[vs % NS], (vs / NS) & 1)) {
-                    ok = issue_pv(t++);
-                } else {
-                    if (++polls % 64 == 0) {
-                        const uint64_t now = hs::global_timer_ns();
-                        if (since == 0) since = now;
-                        ok = B.abort == 0 && now - since <= tmo;
+                    if (++slot == NS) {
+                        slot = 0;
+                        phase ^= 1u;
                     }
-                    continue;
                 }
-                since = 0;
+                if (!ok) break;
+                hs::tc::mma_commit(&B.s_full[t & 1]);
+                if (last_of_segment(c)) hs::tc::mma_commit(&B.q_empty);
+                if (t + 1 < run) advance(c, a, chunks, lth);
             }
             if (!ok) {
                 hs::set_status(a.status, HS_ERR_TIMEOUT);
                 B.abort = 1;
             }
             // Every product issued has completed before TMEM is freed.
-            hs::tc::mma_commit(&B.drain);
-            hs::mbar_wait_bounded(&B.drain, 0, tmo, nullptr);
+            hs::tc::mma_commit(&B.drain[0]);
+            hs::mbar_wait_bounded(&B.drain[0], 0, tmo, nullptr);
         }
         __syncwarp();
-    } else if (warp >= kQWarp) {
-        // ------------------------------ queries ------------------------------
-        const int qt = tid - kQWarp * 32;
-        Cursor c = cursor_at(a, pl, B.start_row, B.start_tile, w0, w1, th);
-        bool ok = true;
-        for (int seg = 0; ok;) {
-            if (c.first) {
-                if (seg > 0 &&
-                    !__all_sync(0xffffffffu, hs::mbar_wait_bounded(&B.q_empty, (seg - 1) & 1, tmo,
-                                                                   abort_flag))) {
-                    ok = false;
-                    break;
-                }
-                const int kvh0 = c.chunk / gch * hsn, gc = c.chunk % gch;
-                const int Gc = min(GM, group - gc * GM);
-                const char* q = static_cast<const char*>(a.q) + int64_t(c.row) * a.q_stride * 2;
-                if constexpr (!E4) {
-                    constexpr int kCh = D / 8;  // 16-byte chunks of a query row
-                    for (int e = qt; e < nq * kCh; e += kQThreads) {
-                        const int n = e / kCh, ch = e % kCh;
-                        const int hl = n / GM, gi = n % GM;
-                        const bool in = hl < hsn && gi < Gc;
-                        const int h = (kvh0 + min(hl, hsn - 1)) * group + gc * GM + min(gi, Gc - 1);
-                        hs::tc::cp_async16(sb + C::kQOff + (ch >> 3) * uint32_t(nq) * 128 +
-                                               n * 128 + (((ch & 7) ^ (n & 7)) << 4),
-                                           q + int64_t(h) * D * 2 + ch * 16, in ? 16u : 0u);
-                    }
-                    hs::tc::cp_async_wait_all();
-                } else {
-                    // Lanes of 16 dims; D / 16 of them hold a row.
-                    constexpr int kL = D / 16;
-                    const int ch = qt % kL;
-                    for (int n0 = 0; n0 < hsn * GM; n0 += kQThreads / kL) {
-                        const int idx = n0 + qt / kL;  // (head, query) in order
-                        const int hl = idx / GM, gi = idx % GM;
-                        const bool slot_ok = hl < hsn;
-                        const bool in = slot_ok && gi < Gc;
-                        float x[16];
+    } else if (warp == kPvWarp) {
+        // -------------------------- O^T += V^T P^T -----------------------------
+        if (lane == 0) {
+            constexpr int kStep = E4 ? 32 : 16;  // rows of a K step
+            constexpr int kSteps = kRows / kStep;
+            // E4M3, runs of 16 rows: a K step holds two heads, taken together.
+            const bool two = E4 && bt < kStep && hsn > 1;
+            const uint32_t id = idesc<KV>(two ? 2 * C::NP : C::NP, 1);
+            const uint64_t v_desc = hs::tc::sdesc_sw128(sb + C::kVOff, kBlk, 1024);
+            const uint64_t p_desc = hs::tc::sdesc_sw128(sb + C::kPOff, 16, 1024);
+            // Output column of each K step's head, and the steps that hold a
+            // head's first rows.
+            uint32_t col[kSteps], starts = 0;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) x[i] = 0.f;
-                        if (in) {
-                            const int h = (kvh0 + hl) * group + gc * GM + gi;
-                            const uint4* p = reinterpret_cast<const uint4*>(
-                                q + (int64_t(h) * D + ch * 16) * 2);
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const uint4 u = __ldg(p + j);
-                                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const float2 f =
-                                        a.q_is_half
-                                            ? __half22float2(*reinterpret_cast<const __half2*>(&w[i]))
-                                            : __bfloat1622float2(
-                                                  *reinterpret_cast<const __nv_bfloat162*>(&w[i]));
-                                    x[8 * j + 2 * i] = f.x;
-                                    x[8 * j + 2 * i + 1] = f.y;
-                                }
-                            }
-                        }
-                        float mx = 0.f;
-                        bool nan = false;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            mx = fmaxf(mx, fabsf(x[i]));
-                            nan |= !(fabsf(x[i]) < CUDART_INF_F);
-                        }
-#pragma unroll
-                        for (int o = kL / 2; o > 0; o >>= 1)
-                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                        // Largest magnitude to [2^7, 2^8).
-                        int e = 0;
-                        if (mx > 0.f && mx < CUDART_INF_F) e = 7 - ilogbf(mx);
-                        const float up = exp2f(float(max(e, -126) / 2));
-                        const float up2 = exp2f(float(max(e, -126) - max(e, -126) / 2));
-                        uint32_t code[3][4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) code[0][i] = code[1][i] = code[2][i] = 0u;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float r = x[i] * up * up2;
-#pragma unroll
-                            for (int k = 0; k < 3; ++k) {
-                                // A query that is not finite shows as NaN.
-                                const uint8_t cc = nan ? uint8_t(0x7f) : to_e4m3(r);
-                                code[k][i >> 2] |= uint32_t(cc) << (8 * (i & 3));
-                                r = (r - from_e4m3(cc)) * 16.f;
-                            }
-                        }
-                        if (slot_ok) {
-#pragma unroll
-                            for (int k = 0; k < 3; ++k) {
-                                const int n = hl * C::NH + k * GM + gi;
-                                *reinterpret_cast<uint4*>(
-                                    smem + C::kQOff + (ch >> 3) * nq * 128 + n * 128 +
-                                    (((ch & 7) ^ (n & 7)) << 4)) =
-                                    make_uint4(code[k][0], code[k][1], code[k][2], code[k][3]);
-                            }
-                            if (ch == 0) {
-                                float f = a.scale_log2 * exp2f(float(-max(e, -126) / 2)) *
-                                          exp2f(float(-(max(e, -126) - max(e, -126) / 2)));
-                                if (a.k_scale != nullptr) f *= __ldg(a.k_scale + kvh0 + hl);
-                                B.qscale[seg & 3][hl * GM + gi] = f;
-                            }
-                        }
-                    }
-                }
-                hs::fence_proxy_async_shared();
-                hs::mbar_arrive(&B.q_full);
-                ++seg;
+            for (int kk = 0; kk < kSteps; ++kk) {
+                const int r = kk * kStep;
+                col[kk] = tmem + o_col + uint32_t((r >> lbt) & (hsn - 1)) * C::NP;
+                if (r < (hsn << lbt) && (two || (r & (bt - 1)) == 0)) starts |= 1u << kk;
             }
-            if (c.left == 1) break;
-            advance(c, a, chunks, th);
+            Cursor c = start;
+            bool ok = true;
+            int slot = 0, t0 = 0;
+            uint32_t phase = 0;
+            for (int t = 0, seg = 0; t < run; ++t) {
+                if (c.first) {
+                    // The epilogue of the segment before has read the output.
+                    if (seg > 0)
+                        ok = ok && hs::mbar_wait_bounded(&B.o_free, (seg - 1) & 1, tmo, abort_flag);
+                    ++seg;
+                    t0 = t;
+                }
+                ok = ok && hs::mbar_wait_bounded(&B.p_full[t & 1], (t >> 1) & 1, tmo, abort_flag);
+                // A group's first tile of the segment starts its output.
+                const uint32_t fresh = t - t0 < kGroups ? starts : 0u;
+                const uint64_t pd = p_desc + uint32_t((t & 1) * (C::kPBytes >> 4));
+#pragma unroll
+                for (int s = 0; s < C::kSubs; ++s) {
+                    ok = ok && hs::mbar_wait_bounded(&B.vfull[slot], phase, tmo, abort_flag);
+                    if (!ok) break;
+                    hs::tc::fence_after_sync();
+                    const uint64_t vd = v_desc + uint32_t(slot * (C::kSub >> 4));
+                    const uint32_t d = uint32_t(((t & 1) * C::kSubs + s) * ocols);
+#pragma unroll
+                    for (int kk = 0; kk < kSteps; ++kk)
+                        mma<KV>(d + col[kk], vd + uint32_t(kk * kStep * 8),
+                                pd + uint32_t(E4 ? kk * 2 : (kk >> 2) * (C::NP * 8) + (kk & 3) * 2),
+                                id, ((fresh >> kk) & 1u) ^ 1u);
+                    hs::tc::mma_commit(&B.vempty[slot]);
+                    if (++slot == NS) {
+                        slot = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                hs::tc::mma_commit(&B.pv_done[t & 1]);
+                if (t + 1 < run) advance(c, a, chunks, lth);
+            }
+            if (!ok) {
+                hs::set_status(a.status, HS_ERR_TIMEOUT);
+                B.abort = 1;
+            }
+            hs::tc::mma_commit(&B.drain[1]);
+            hs::mbar_wait_bounded(&B.drain[1], 0, tmo, nullptr);
+        }
+        __syncwarp();
+    } else if (warp == kQWarp) {
+        // ------------------------------ queries ------------------------------
+        Cursor c = start;
+        bool ok = true;
+        for (int seg = 0; c.left > 0; ++seg) {
+            if (seg > 0 && !__all_sync(0xffffffffu,
+                                       hs::mbar_wait_bounded(&B.q_empty, (seg - 1) & 1, tmo,
+                                                             abort_flag))) {
+                ok = false;
+                break;
+            }
+            const int kvh0 = c.chunk / gch * hsn, gc = c.chunk % gch;
+            const int Gc = min(GM, group - gc * GM);
+            const char* q = static_cast<const char*>(a.q) + int64_t(c.row) * a.q_stride * 2;
+            if constexpr (!E4) {
+                constexpr int kCh = D / 8;  // 16-byte chunks of a query row
+                for (int e = lane; e < nq * kCh; e += 32) {
+                    const int n = e / kCh, ch = e % kCh;
+                    const int hl = n / GM, gi = n % GM;
+                    const bool in = hl < hsn && gi < Gc;
+                    const int h = (kvh0 + min(hl, hsn - 1)) * group + gc * GM + min(gi, Gc - 1);
+                    hs::tc::cp_async16(sb + C::kQOff + (ch >> 3) * uint32_t(nq) * 128 + n * 128 +
+                                           (((ch & 7) ^ (n & 7)) << 4),
+                                       q + int64_t(h) * D * 2 + ch * 16, in ? 16u : 0u);
+                }
+                hs::tc::cp_async_wait_all();
+            } else {
+                // Lanes of 16 dims, D / 16 of them a row; the loads of all
+                // rows are in flight together.
+                constexpr int kL = D / 16, kIter = C::kHsMax * GM * kL / 32;
+                const int ch = lane % kL;
+                uint4 raw[kIter][2];
+#pragma unroll
+                for (int it = 0; it < kIter; ++it) {
+                    const int n = it * (32 / kL) + lane / kL, hl = n / GM, gi = n % GM;
+                    raw[it][0] = raw[it][1] = make_uint4(0u, 0u, 0u, 0u);
+                    if (hl < hsn && gi < Gc) {
+                        const uint4* p = reinterpret_cast<const uint4*>(
+                            q + (int64_t((kvh0 + hl) * group + gc * GM + gi) * D + ch * 16) * 2);
+                        raw[it][0] = __ldg(p);
+                        raw[it][1] = __ldg(p + 1);
+                    }
+                }
+#pragma unroll
+                for (int it = 0; it < kIter; ++it) {
+                    const int n = it * (32 / kL) + lane / kL, hl = n / GM, gi = n % GM;
+                    float x[16];
+                    const uint32_t w[8] = {raw[it][0].x, raw[it][0].y, raw[it][0].z, raw[it][0].w,
+                                           raw[it][1].x, raw[it][1].y, raw[it][1].z, raw[it][1].w};
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 f =
+                            a.q_is_half
+                                ? __half22float2(*reinterpret_cast<const __half2*>(&w[i]))
+                                : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+                        x[2 * i] = f.x;
+                        x[2 * i + 1] = f.y;
+                    }
+                    float mx = 0.f;
+                    bool odd = false;  // not finite: shows as NaN
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        mx = fmaxf(mx, fabsf(x[i]));
+                        odd |= !(fabsf(x[i]) < CUDART_INF_F);
+                    }
+#pragma unroll
+                    for (int o = kL / 2; o > 0; o >>= 1)
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    // Largest magnitude to [2^7, 2^8), by two factors (their
+                    // product may lie outside fp32's range).
+                    int e = 0;
+                    if (mx > 0.f && mx < CUDART_INF_F)
+                        e = max(7 - (int(__float_as_uint(mx) >> 23) - 127), -126);
+                    const int ea = e / 2, eb = e - ea;
+                    const float up = pow2(ea), up2 = pow2(eb);
+                    uint32_t code[3][4];
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        float r0 = x[i] * up * up2, r1 = x[i + 1] * up * up2;
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) {
+                            const uint32_t cc = odd ? 0x7f7fu : to_e4m3x2(r0, r1);
+                            const float2 f = from_e4m3x2(cc);
+                            code[k][i >> 2] =
+                                (i & 2) ? code[k][i >> 2] | (cc << 16) : cc;
+                            r0 = (r0 - f.x) * 16.f;
+                            r1 = (r1 - f.y) * 16.f;
+                        }
+                    }
+                    if (hl < hsn) {
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) {
+                            const int m = hl * C::NH + k * GM + gi;
+                            *reinterpret_cast<uint4*>(smem + C::kQOff + (ch >> 3) * nq * 128 +
+                                                      m * 128 + (((ch & 7) ^ (m & 7)) << 4)) =
+                                make_uint4(code[k][0], code[k][1], code[k][2], code[k][3]);
+                        }
+                        if (ch == 0) {
+                            float f = a.scale_log2 * pow2(-ea) * pow2(-eb);
+                            if (a.k_scale != nullptr) f *= __ldg(a.k_scale + kvh0 + hl);
+                            B.qscale[seg & 3][hl * GM + gi] = f;
+                        }
+                    }
+                }
+            }
+            hs::fence_proxy_async_shared();
+            hs::mbar_arrive(&B.q_full);
+            // On to the next segment.
+            const int n = min(c.left, c.v.n - c.tile);
+            c.left -= n - 1;
+            c.tile += n - 1;
+            advance(c, a, chunks, lth);
         }
         if (!ok) {
             hs::set_status(a.status, HS_ERR_TIMEOUT);
@@ -726,6 +618,11 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
                          "r"(x)
                          : "memory");
         };
+        // The j-th group of 16 rows that belong to this row's head, j < 8 / hs.
+        auto rows_of = [&](int j) {
+            const int lg = lbt - 4;  // log2 of the groups of a run
+            return ((((j >> lg) << lhs) + hl) << lg) + (j & ((1 << lg) - 1));
+        };
         bool fail = false;
         // A wait that gives up lets the CTA run to its end at once (every
         // later wait sees the flag), so that all its barriers are met.
@@ -736,7 +633,7 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
             }
             __syncwarp();
         };
-        Cursor c = cursor_at(a, pl, B.start_row, B.start_tile, w0, w1, th);
+        Cursor c = start;
         for (int t = 0, seg = 0; t < run; ++seg) {
             // ---- One segment: the tiles of one unit in this run ----------------
             const int row = c.row;
@@ -753,9 +650,9 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
                 l[i] = 0.f;
             }
             bool own = false;  // this group has had a tile of the segment
-            for (; t < t0 + n; ++t, advance(c, a, chunks, th)) {
+            for (; t < t0 + n; ++t, advance(c, a, chunks, lth)) {
                 if ((t & 1) != wg) continue;
-                const int tok = tile_token(c, th) + rt;
+                const int tok = tile_token(c, lth) + rt;
                 wait(&B.s_full[wg], (t >> 1) & 1);
                 hs::tc::fence_after_sync();
                 const bool seen = visible(v, tok);
@@ -785,7 +682,7 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
                     if (!valid) x[i] = -CUDART_INF_F;
                 }
                 if (a.logits != nullptr && seen) {
-                    const int i = tok < v.sc ? tok : tok - v.w0 + v.sc;
+                    const int i = visible_index(v, tok);
                     float* lp = a.logits +
                                 (int64_t(row) * a.heads + (kvh0 + hl) * group + gc * GM) *
                                     a.logit_stride + i;
@@ -793,34 +690,51 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
                     for (int g = 0; g < GM; ++g)
                         if (g < Gc) lp[g * a.logit_stride] = x[g];
                 }
-                bool grow = false;
+                bool grow = !own;
 #pragma unroll
                 for (int i = 0; i < GM; ++i) grow |= i < Gc && x[i] > mref[i] + kThresh;
                 // The group's P buffer and output: its product before is done.
                 if (t >= kGroups) wait(&B.pv_done[wg], ((t - kGroups) >> 1) & 1);
                 if (hs::pair::named_sync_or(kSoftBar + wg, kSoftThreads, grow)) {
                     // New reference maxima: the largest logits so far.
+                    float mx[GM];
 #pragma unroll
-                    for (int i = 0; i < GM; ++i) {
-                        float mx = x[i];
+                    for (int i = 0; i < GM; ++i) mx[i] = x[i];
 #pragma unroll
-                        for (int o = 8; o > 0; o >>= 1)
-                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                        if ((lane & 15) == 0) B.red[wg][r >> 4][i] = mx;
+                    for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+                        for (int i = 0; i < GM; ++i)
+                            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
+                    if (hsn < 8) {
+                        if ((lane & 15) == 0)
+#pragma unroll
+                            for (int i = 0; i < GM; i += 4)
+                                *reinterpret_cast<float4*>(&B.red[wg][r >> 4][i]) =
+                                    make_float4(mx[i], mx[i + 1], mx[i + 2], mx[i + 3]);
+                        hs::pair::named_sync(kSoftBar + wg, kSoftThreads);
+                        for (int j = 0; j < (8 >> lhs); ++j) {
+                            const float* q = B.red[wg][rows_of(j)];
+#pragma unroll
+                            for (int i = 0; i < GM; i += 4) {
+                                const float4 f = *reinterpret_cast<const float4*>(q + i);
+                                mx[i] = fmaxf(mx[i], f.x);
+                                mx[i + 1] = fmaxf(mx[i + 1], f.y);
+                                mx[i + 2] = fmaxf(mx[i + 2], f.z);
+                                mx[i + 3] = fmaxf(mx[i + 3], f.w);
+                            }
+                        }
                     }
-                    hs::pair::named_sync(kSoftBar + wg, kSoftThreads);
-#pragma unroll
-                    for (int i = 0; i < GM; ++i) {
-                        float mn = mref[i];
-                        for (int q = 0; q < 8; ++q)
-                            if (((q * 16 >> lbt) & (hsn - 1)) == hl) mn = fmaxf(mn, B.red[wg][q][i]);
-                        const float al = mn == mref[i] ? 1.f : exp2f(mref[i] - mn);
-                        l[i] *= al;
-                        mref[i] = mn;
-                        if (rt == 0) B.alpha[wg][hl][i] = al;
-                    }
-                    hs::pair::named_sync(kSoftBar + wg, kSoftThreads);
                     if (own) {
+                        // Rescale what has been summed.
+#pragma unroll
+                        for (int i = 0; i < GM; ++i) {
+                            const float mn = fmaxf(mref[i], mx[i]);
+                            const float al = mn == mref[i] ? 1.f : ex2(mref[i] - mn);
+                            l[i] *= al;
+                            mref[i] = mn;
+                            if (rt == 0) B.alpha[wg][hl][i] = al;
+                        }
+                        hs::pair::named_sync(kSoftBar + wg, kSoftThreads);
                         hs::tc::fence_after_sync();
 #pragma unroll 1
                         for (int cb = 0; cb < C::kSubs * ocols; cb += 8) {
@@ -834,32 +748,50 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
                             hs::tc::tmem_st8(o_own + uint32_t(cb), o);
                         }
                         hs::tc::tmem_wait_st();
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < GM; ++i) mref[i] = mx[i];
                     }
                 }
                 own = true;
 #pragma unroll
-                for (int i = 0; i < GM; ++i) {
+                for (int i = 0; i < GM; i += 2) {
                     if (i >= Gc) break;
                     // Without a finite logit so far: subtract 0, every weight
                     // stays 0 (a NaN logit stays NaN).
-                    const float p = exp2f(x[i] - (mref[i] == -CUDART_INF_F ? 0.f : mref[i]));
+                    const float p = ex2(x[i] - (mref[i] == -CUDART_INF_F ? 0.f : mref[i]));
+                    const float p2 =
+                        ex2(x[i + 1] - (mref[i + 1] == -CUDART_INF_F ? 0.f : mref[i + 1]));
                     l[i] += p;
+                    l[i + 1] += p2;
                     if constexpr (KV == kBf16) {
-                        const __nv_bfloat16 hi = __float2bfloat16_rn(p);
-                        put16(i, __bfloat16_as_ushort(hi));
-                        put16(GM + i,
-                              __bfloat16_as_ushort(__float2bfloat16_rn(p - __bfloat162float(hi))));
+                        const __nv_bfloat162 hi = __floats2bfloat162_rn(p, p2);
+                        const float2 f = __bfloat1622float2(hi);
+                        const __nv_bfloat162 lo = __floats2bfloat162_rn(p - f.x, p2 - f.y);
+                        put16(i, __bfloat16_as_ushort(hi.x));
+                        put16(i + 1, __bfloat16_as_ushort(hi.y));
+                        put16(GM + i, __bfloat16_as_ushort(lo.x));
+                        put16(GM + i + 1, __bfloat16_as_ushort(lo.y));
                     } else if constexpr (KV == kFp16) {
-                        const __half hi = __float2half_rn(p);
-                        put16(i, __half_as_ushort(hi));
-                        put16(GM + i, __half_as_ushort(__float2half_rn(p - __half2float(hi))));
+                        const __half2 hi = __floats2half2_rn(p, p2);
+                        const float2 f = __half22float2(hi);
+                        const __half2 lo = __floats2half2_rn(p - f.x, p2 - f.y);
+                        put16(i, __half_as_ushort(hi.x));
+                        put16(i + 1, __half_as_ushort(hi.y));
+                        put16(GM + i, __half_as_ushort(lo.x));
+                        put16(GM + i + 1, __half_as_ushort(lo.y));
                     } else {
-                        float rem = p;
+                        float r0 = p, r1 = p2;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const uint8_t cc = to_e4m3(rem);
+                            const uint32_t cc = to_e4m3x2(r0, r1);
                             put8(k * GM + i, cc);
-                            rem = (rem - from_e4m3(cc)) * 16.f;
+                            put8(k * GM + i + 1, cc >> 8);
+                            if (k < 3) {
+                                const float2 f = from_e4m3x2(cc);
+                                r0 = (r0 - f.x) * 16.f;
+                                r1 = (r1 - f.y) * 16.f;
+                            }
                         }
                     }
                 }
@@ -896,98 +828,98 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
             }
             hs::tc::fence_after_sync();
 #pragma unroll
-            for (int i = 0; i < GM; ++i) {
-                float s = l[i];
+            for (int o = 8; o > 0; o >>= 1)
 #pragma unroll
-                for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                if ((lane & 15) == 0) B.red[wg][r >> 4][i] = s;
-            }
-            hs::pair::named_sync(kSoftBar + wg, kSoftThreads);
-            if (rt == 0) {
+                for (int i = 0; i < GM; ++i) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+            if ((lane & 15) == 0)
 #pragma unroll
-                for (int i = 0; i < GM; ++i) {
-                    float L = 0.f;
-                    for (int q = 0; q < 8; ++q)
-                        if (((q * 16 >> lbt) & (hsn - 1)) == hl) L += B.red[wg][q][i];
-                    B.ml[wg][hl][i][0] = mref[i];
-                    B.ml[wg][hl][i][1] = L;
-                }
-            }
+                for (int i = 0; i < GM; i += 4)
+                    *reinterpret_cast<float4*>(&B.red[wg][r >> 4][i]) =
+                        make_float4(l[i], l[i + 1], l[i + 2], l[i + 3]);
+            if (rt == 0)
+#pragma unroll
+                for (int i = 0; i < GM; ++i) B.ml[wg][hl][i][0] = mref[i];
             hs::pair::named_sync(kBothBar, kGroups * kSoftThreads);
-            // A segment of one tile leaves the other group's output unwritten.
-            const bool has[2] = {n > 1 || (t0 & 1) == 0, n > 1 || (t0 & 1) == 1};
-            const bool bf = KV == kBf16 || (E4 && !a.q_is_half);
-            for (int sh = wg; sh < C::kSubs * hsn; sh += kGroups) {
-                const int s = sh / hsn, h = sh % hsn;
-                const int d = s * 128 + r;
-                const int kv = kvh0 + h;
-                const float vs = a.v_scale != nullptr ? __ldg(a.v_scale + kv) : 1.f;
-                const int64_t qh = int64_t(row) * a.heads + kv * group + gc * GM;
-                float O[GM];
-#pragma unroll
-                for (int i = 0; i < GM; ++i) O[i] = 0.f;
+            // A thread per query of the unit: both groups' sums, the unit's
+            // maximum, and the factors that join their outputs.
+            const int e = tid;
+            if (e < hsn * GM) {
+                const int h = e / GM, i = e % GM;
+                float lw[kGroups];
 #pragma unroll
                 for (int w = 0; w < kGroups; ++w) {
-                    if (!has[w]) continue;
-#pragma unroll
-                    for (int k = 0; k < C::kPParts; ++k) {
-                        float o[GM];
-                        tmem_ld<GM>(o_addr + uint32_t((w * C::kSubs + s) * ocols + h * C::NP +
-                                                      k * GM), o);
-                        hs::tc::tmem_wait_ld();
-                        constexpr float kPart[4] = {1.f, 0.0625f, 0.00390625f, 0.000244140625f};
-#pragma unroll
-                        for (int i = 0; i < GM; ++i) {
-                            const float M = fmaxf(B.ml[0][h][i][0], B.ml[1][h][i][0]);
-                            const float f =
-                                exp2f(B.ml[w][h][i][0] - (M == -CUDART_INF_F ? 0.f : M));
-                            O[i] = fmaf(o[i], E4 ? f * kPart[k] : f, O[i]);
-                        }
-                    }
+                    lw[w] = 0.f;
+                    const int lg = lbt - 4;
+                    for (int j = 0; j < (8 >> lhs); ++j)
+                        lw[w] += B.red[w][((((j >> lg) << lhs) + h) << lg) + (j & ((1 << lg) - 1))][i];
                 }
-                if (d >= D) continue;
-#pragma unroll
-                for (int i = 0; i < GM; ++i) {
-                    if (i >= Gc) break;
-                    if (whole) {
-                        const float m0 = B.ml[0][h][i][0], m1 = B.ml[1][h][i][0];
-                        const float M = fmaxf(m0, m1), ref = M == -CUDART_INF_F ? 0.f : M;
-                        const float L =
-                            fmaf(exp2f(m0 - ref), B.ml[0][h][i][1],
-                                 exp2f(m1 - ref) * B.ml[1][h][i][1]);
-                        const float f = L == 0.f ? 0.f : O[i] / L * vs;
-                        if (bf)
-                            static_cast<__nv_bfloat16*>(a.out)[(qh + i) * D + d] =
-                                __float2bfloat16_rn(f);
-                        else
-                            static_cast<__half*>(a.out)[(qh + i) * D + d] = __float2half_rn(f);
-                    } else {
-                        a.part_o[(int64_t(slot) * a.unit_heads_max + h * GM + i) * D + d] = O[i];
-                    }
-                }
-            }
-            hs::tc::fence_before_sync();
-            hs::mbar_arrive(&B.o_free);
-            if (wg == 0)
-                for (int e = r; e < hsn * GM; e += kSoftThreads) {
-                    const int h = e / GM, i = e % GM;
-                    if (i >= Gc) continue;
-                    const float m0 = B.ml[0][h][i][0], m1 = B.ml[1][h][i][0];
-                    const float M = fmaxf(m0, m1), ref = M == -CUDART_INF_F ? 0.f : M;
-                    const float L = fmaf(exp2f(m0 - ref), B.ml[0][h][i][1],
-                                         exp2f(m1 - ref) * B.ml[1][h][i][1]);
+                const float m0 = B.ml[0][h][i][0], m1 = B.ml[1][h][i][0];
+                const float M = fmaxf(m0, m1), ref = M == -CUDART_INF_F ? 0.f : M;
+                const float f0 = exp2f(m0 - ref), f1 = exp2f(m1 - ref);
+                const float L = fmaf(f0, lw[0], f1 * lw[1]);
+                float inv = 1.f;
+                if (i < Gc) {
                     if (whole) {
                         const int64_t qh =
                             int64_t(row) * a.heads + (kvh0 + h) * group + gc * GM + i;
                         const float lg = L == 0.f ? -CUDART_INF_F : M + log2f(L);
                         if (a.lse != nullptr) a.lse[qh] = lg * kLn2;
                         if (a.lse2 != nullptr) a.lse2[qh] = lg;
+                        inv = L == 0.f ? 0.f : 1.f / L;
+                        if (a.v_scale != nullptr) inv *= __ldg(a.v_scale + kvh0 + h);
                     } else {
                         const int64_t k = int64_t(slot) * a.unit_heads_max + e;
                         a.part_ml[2 * k] = M;
                         a.part_ml[2 * k + 1] = L;
                     }
                 }
+                B.weight[0][h][i] = f0 * inv;
+                B.weight[1][h][i] = f1 * inv;
+            }
+            hs::pair::named_sync(kBothBar, kGroups * kSoftThreads);
+            // A segment of one tile leaves the other group's output unwritten.
+            const bool has0 = n > 1 || (t0 & 1) == 0, has1 = n > 1 || (t0 & 1) == 1;
+            const bool bf = KV == kBf16 || (E4 && !a.q_is_half);
+            for (int sh = wg; sh < (C::kSubs << lhs); sh += kGroups) {
+                const int s = sh >> lhs, h = sh & (hsn - 1);
+                const int d = s * 128 + r;
+                float O[GM];
+#pragma unroll
+                for (int i = 0; i < GM; ++i) O[i] = 0.f;
+#pragma unroll
+                for (int w = 0; w < kGroups; ++w) {
+                    if (!(w == 0 ? has0 : has1)) continue;
+                    float o[C::NP];
+                    tmem_ld<C::NP>(o_addr + uint32_t((w * C::kSubs + s) * ocols + h * C::NP), o);
+                    hs::tc::tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < GM; ++i) {
+                        float v;
+                        if constexpr (E4)
+                            v = fmaf(fmaf(fmaf(o[3 * GM + i], 0.0625f, o[2 * GM + i]), 0.0625f,
+                                          o[GM + i]), 0.0625f, o[i]);
+                        else
+                            v = o[i] + o[GM + i];
+                        O[i] = fmaf(v, B.weight[w][h][i], O[i]);
+                    }
+                }
+                if (d >= D) continue;
+                const int64_t qh = int64_t(row) * a.heads + (kvh0 + h) * group + gc * GM;
+                const int64_t at = whole ? qh * D + d
+                                         : (int64_t(slot) * a.unit_heads_max + h * GM) * D + d;
+#pragma unroll
+                for (int i = 0; i < GM; ++i) {
+                    if (i >= Gc) break;
+                    if (!whole)
+                        a.part_o[at + i * D] = O[i];
+                    else if (bf)
+                        static_cast<__nv_bfloat16*>(a.out)[at + i * D] = __float2bfloat16_rn(O[i]);
+                    else
+                        static_cast<__half*>(a.out)[at + i * D] = __float2half_rn(O[i]);
+                }
+            }
+            hs::tc::fence_before_sync();
+            hs::mbar_arrive(&B.o_free);
             // The states are read: the next segment may write its own.
             hs::pair::named_sync(kBothBar, kGroups * kSoftThreads);
         }
@@ -996,7 +928,7 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
     hs::tc::fence_before_sync();
     __syncthreads();
     hs::tc::fence_after_sync();
-    if (warp == kMmaWarp) hs::tc::tmem_dealloc(tmem, kTmemCols);
+    if (warp == kPvWarp) hs::tc::tmem_dealloc(tmem, kTmemCols);
 }
 
 // Tensor map of a cache: dims (head dim, token of the page, KV head, page).
@@ -1004,27 +936,21 @@ int encode_map(CUtensorMap* m, int kv, const void* base, const PagedArgs& a, int
                int hs_box);
 
 template <int KV, int D, int GH>
-int launch_one(const PagedArgs& a, hs_stream_t stream) {
+int launch_one(PagedArgs& a, hs_stream_t stream) {
     using C = Cfg<KV, D, GH>;
+    constexpr int GM = C::GM;
     TcArgs t{};
+    set_ways(a, C::kHsMax, kRows, GM, kTilesForWide);
     t.p = a;
-    int hs_max = 1;
-    while (hs_max < C::kHsMax && a.kv_heads % (2 * hs_max) == 0) hs_max *= 2;
-    const auto run_of_page = [&](int hs_) {
-        int bt = kRows / hs_;
-        while (a.page_size % bt) bt /= 2;
-        return bt;
-    };
-    t.hs[0] = hs_max;
-    t.bt[0] = run_of_page(hs_max);
-    t.hs[1] = 1;
-    t.bt[1] = run_of_page(1);
-    t.steps_for_wide = 4;
+    for (int i = 0; i < 2; ++i) {
+        t.bt[i] = kRows / a.hs[i];
+        while (a.page_size % t.bt[i]) t.bt[i] /= 2;
+    }
     t.timeout_ns = hs::kWaitTimeoutNs;
     CUtensorMap m[4];
     for (int i = 0; i < 2; ++i) {
-        int rc = encode_map(&m[2 * i], KV, a.k, a, D, t.bt[i], t.hs[i]);
-        if (rc == HS_OK) rc = encode_map(&m[2 * i + 1], KV, a.v, a, D, t.bt[i], t.hs[i]);
+        int rc = encode_map(&m[2 * i], KV, a.k, a, D, t.bt[i], a.hs[i]);
+        if (rc == HS_OK) rc = encode_map(&m[2 * i + 1], KV, a.v, a, D, t.bt[i], a.hs[i]);
         if (rc != HS_OK) return rc;
     }
     auto kern = paged_tc_kernel<KV, D, GH>;
@@ -1039,7 +965,7 @@ int launch_one(const PagedArgs& a, hs_stream_t stream) {
 }
 
 template <int KV>
-int launch_kind(const PagedArgs& a, int d, int group, hs_stream_t stream) {
+int launch_kind(PagedArgs& a, int d, int group, hs_stream_t stream) {
     if constexpr (KV != kE4m3) {
         if (d == 64)
             return group <= 8 ? launch_one<KV, 64, 1>(a, stream)

@@ -2,7 +2,7 @@
 #include "hs_paged_tc.cuh"
 
 namespace hs_paged {
-int launch_tc_fp16(const PagedArgs& a, int d, int group, hs_stream_t stream) {
+int launch_tc_fp16(PagedArgs& a, int d, int group, hs_stream_t stream) {
     return tc::launch_kind<tc::kFp16>(a, d, group, stream);
 }
 }  // namespace hs_paged
