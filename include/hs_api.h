@@ -554,7 +554,8 @@ int hs_sparse_decode_fp8ds(const void* q, const void* kv8, int64_t row_bytes,
  * Supported: d 64, 128 or 256, any heads / kv_heads; others (and scales with
  * 16-bit caches, or caches of another 16-bit type than q) return
  * HS_ERR_UNSUPPORTED.  rows <= 4096 and rows * heads * max_len / 16 < 2^31
- * (HS_ERR_CAPACITY above, or when the workspace is missing or too small).
+ * (HS_ERR_CAPACITY above, or when the workspace is missing or too small; the
+ * workspace query gives -1 for sizes that are refused).
  * ------------------------------------------------------------------------- */
 int64_t hs_paged_decode_workspace_bytes(int32_t rows, int32_t heads, int32_t kv_heads, int32_t d,
                                         int32_t max_len, int32_t window, int32_t num_sinks,

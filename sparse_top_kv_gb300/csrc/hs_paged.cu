@@ -72,29 +72,18 @@ bool tensor_map_ok(const PagedArgs& a, int kv_dtype, int d) {
 }
 
 constexpr int kMergeThreads = 256;
-constexpr int kScoreThreads = 128;
-constexpr int kScoreTokens = 4 * kScoreThreads;  // tokens of one scoring step
+constexpr int kMergeWarps = kMergeThreads / 32;
+constexpr int kHeadChunk = 256;  // heads whose LSE a scoring block holds at a time
 
-// Merge of the units whose tiles were dealt to several CTAs (the others were
-// written by their CTA): out = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p.
-// A block takes every gridDim.y-th head of a request; a warp reads every
-// eighth partial row, so all loads of a merge are in flight at once.  The
-// plan depends on seq_lens alone, which no longer changes once the attention
-// kernel lets this one start, so it is found while that kernel still runs.
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads) merge_units(const __grid_constant__ PagedArgs a,
-                                                             int out_bf16) {
-    constexpr int NW = kMergeThreads / 32;
-    constexpr int V4 = D / 4;                    // float4s of a row
-    constexpr int PL = V4 > 32 ? V4 / 32 : 1;    // float4s of a lane
-    __shared__ float wt[kMaxCtas];
-    __shared__ float red[NW];
-    __shared__ int sums[NW][4];
-    __shared__ float4 acc[NW][V4];
-    hs::pdl_trigger();
-    const int group = a.heads / a.kv_heads, gch = (group + a.gm - 1) / a.gm;
+// Where the units of one request lie in the call's runs of tiles.
+struct RowPlan {
+    Plan pl;
+    int way, row_tiles, first_tile;
+};
+// Called by every thread of the block.
+__device__ __forceinline__ RowPlan row_plan(const PagedArgs& a, int row) {
+    __shared__ int sums[kMergeWarps][4];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int row = blockIdx.x;
     int n[4] = {0, 0, 0, 0};  // tiles of all rows, and of those before this one, both ways
     for (int r = tid; r < a.rows; r += kMergeThreads) {
         const int len = a.seq_lens[r];
@@ -116,65 +105,94 @@ __global__ void __launch_bounds__(kMergeThreads) merge_units(const __grid_consta
     for (int i = 0; i < 4; ++i) {
         n[i] = 0;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) n[i] += sums[w][i];
+        for (int w = 0; w < kMergeWarps; ++w) n[i] += sums[w][i];
     }
-    const int way = way_of(a, n[0]);
-    const Plan pl = plan_of(a, way, way == 0 ? n[0] : n[1]);
-    const int row_tiles = tiling_of(a, a.seq_lens[row], a.lth[way]).n;
-    const int first_tile = (way == 0 ? n[2] : n[3]) * a.chunks[way];
-    const int hs = a.hs[way];
-    hs::pdl_wait();
-    for (int h = blockIdx.y; h < a.heads; h += gridDim.y) {
-        const int kvh = h / group, gi = h % group;
+    RowPlan p;
+    p.way = way_of(a, n[0]);
+    p.pl = plan_of(a, p.way, p.way == 0 ? n[0] : n[1]);
+    p.row_tiles = tiling_of(a, a.seq_lens[row], a.lth[p.way]).n;
+    p.first_tile = (p.way == 0 ? n[2] : n[3]) * a.chunks[p.way];
+    return p;
+}
+// The parts that a query head's unit was dealt to: part p (one per CTA) of the
+// head is entry at(p) of the partial states.
+struct Parts {
+    int n;
+    int64_t first, rest;
+    int64_t step;
+    __device__ __forceinline__ int64_t at(int p) const { return p == 0 ? first : rest + p * step; }
+};
+__device__ __forceinline__ Parts parts_of(const PagedArgs& a, const RowPlan& r, int h) {
+    const int group = a.heads / a.kv_heads, gch = (group + a.gm - 1) / a.gm;
+    const int hs = a.hs[r.way], kvh = h / group, gi = h % group;
+    const int hu = (kvh % hs) * a.gm + gi % a.gm;
+    const int start = r.first_tile + (kvh / hs * gch + gi / a.gm) * r.row_tiles;
+    const int c0 = run_of(r.pl, start), c1 = run_of(r.pl, start + r.row_tiles - 1);
+    Parts p;
+    p.n = c1 - c0 + 1;
+    p.step = 2 * int64_t(a.unit_heads_max);
+    p.rest = c0 * p.step + hu;
+    // Only the first CTA's part can sit in its second slot.
+    p.first = p.rest + (start > run_begin(r.pl, c0) ? a.unit_heads_max : 0);
+    return p;
+}
+
+// Merge of the units whose tiles were dealt to several CTAs (the others were
+// written by their CTA): out = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p.
+// A warp reads every eighth partial row, so all loads of a head's merge are
+// in flight at once.
+template <int D>
+__device__ __forceinline__ void merge_heads(const PagedArgs& a, const RowPlan& plan, int row,
+                                            int h0, int step, int out_bf16) {
+    constexpr int NW = kMergeWarps;
+    constexpr int V4 = D / 4;                    // float4s of a row
+    constexpr int PL = V4 > 32 ? V4 / 32 : 1;    // float4s of a lane
+    __shared__ float wt[kMaxCtas];
+    __shared__ float red[2][NW];
+    __shared__ float4 acc[NW][V4];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    for (int h = h0; h < a.heads; h += step) {
+        const Parts parts = parts_of(a, plan, h);
+        if (parts.n == 1) continue;
         const int64_t qh = int64_t(row) * a.heads + h;
-        const int chunk = kvh / hs * gch + gi / a.gm;
-        const int hu = (kvh % hs) * a.gm + gi % a.gm;
-        const int start = first_tile + chunk * row_tiles;
-        const int c0 = run_of(pl, start), c1 = run_of(pl, start + row_tiles - 1);
-        if (c0 == c1) continue;
-        const int parts = c1 - c0 + 1;
-        // Only the first CTA's part can sit in its second slot.
-        const int64_t first =
-            int64_t(2 * c0 + (start > run_begin(pl, c0) ? 1 : 0)) * a.unit_heads_max + hu;
-        auto part = [&](int p) {
-            return p == 0 ? first : int64_t(2 * (c0 + p)) * a.unit_heads_max + hu;
-        };
-        float m[(kMaxCtas + kMergeThreads - 1) / kMergeThreads];
+        float2 ml[kMaxCtas / kMergeThreads];
         float M = -CUDART_INF_F;
 #pragma unroll
         for (int i = 0; i < kMaxCtas / kMergeThreads; ++i) {
             const int p = tid + i * kMergeThreads;
-            m[i] = p < parts ? __ldcg(a.part_ml + 2 * part(p)) : -CUDART_INF_F;
-            M = fmaxf(M, m[i]);
+            ml[i] = p < parts.n
+                        ? __ldcg(reinterpret_cast<const float2*>(a.part_ml) + parts.at(p))
+                        : make_float2(-CUDART_INF_F, 0.f);
+            M = fmaxf(M, ml[i].x);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        if (lane == 0) red[warp] = M;
+        if (lane == 0) red[0][warp] = M;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < NW; ++i) M = fmaxf(M, red[i]);
+        for (int i = 0; i < NW; ++i) M = fmaxf(M, red[0][i]);
         const float ref = M == -CUDART_INF_F ? 0.f : M;
         float L = 0.f;
 #pragma unroll
         for (int i = 0; i < kMaxCtas / kMergeThreads; ++i) {
             const int p = tid + i * kMergeThreads;
-            if (p < parts) {
-                const float w = exp2f(m[i] - ref);
+            if (p < parts.n) {
+                const float w = exp2f(ml[i].x - ref);
                 wt[p] = w;
-                L = fmaf(w, __ldcg(a.part_ml + 2 * part(p) + 1), L);
+                L = fmaf(w, ml[i].y, L);
             }
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        if (lane == 0) red[1][warp] = L;
         __syncthreads();
-        if (lane == 0) red[warp] = L;
         float4 s[PL];
 #pragma unroll
         for (int i = 0; i < PL; ++i) s[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int p = warp; p < parts; p += NW) {
+        for (int p = warp; p < parts.n; p += NW) {
             const float w = wt[p];
-            const float4* po = reinterpret_cast<const float4*>(a.part_o + part(p) * D);
+            const float4* po = reinterpret_cast<const float4*>(a.part_o + parts.at(p) * D);
 #pragma unroll
             for (int i = 0; i < PL; ++i) {
                 const int c = lane + 32 * i;
@@ -193,67 +211,103 @@ __global__ void __launch_bounds__(kMergeThreads) merge_units(const __grid_consta
         __syncthreads();
         L = 0.f;
 #pragma unroll
-        for (int i = 0; i < NW; ++i) L += red[i];
+        for (int i = 0; i < NW; ++i) L += red[1][i];
+        const float vs = a.v_scale != nullptr ? __ldg(a.v_scale + h / (a.heads / a.kv_heads)) : 1.f;
         for (int d = tid; d < D; d += kMergeThreads) {
             float O = 0.f;
 #pragma unroll
             for (int i = 0; i < NW; ++i) O += reinterpret_cast<const float*>(acc[i])[d];
-            float r = L == 0.f ? 0.f : O / L;
-            if (a.v_scale != nullptr) r *= __ldg(a.v_scale + kvh);
+            const float r = L == 0.f ? 0.f : O / L * vs;
             if (out_bf16) static_cast<__nv_bfloat16*>(a.out)[qh * D + d] = __float2bfloat16_rn(r);
             else static_cast<__half*>(a.out)[qh * D + d] = __float2half_rn(r);
         }
-        if (tid == 0) {
-            const float lg = L == 0.f ? -CUDART_INF_F : M + log2f(L);
-            if (a.lse != nullptr) a.lse[qh] = lg * kLn2;
-            if (a.lse2 != nullptr) a.lse2[qh] = lg;
-        }
+        if (tid == 0 && a.lse != nullptr)
+            a.lse[qh] = L == 0.f ? -CUDART_INF_F : (M + log2f(L)) * kLn2;
         __syncthreads();
     }
 }
 
-// score[r][t] := decay * score[r][t] + sum_h 2^(x[r][h][t] - lse2[r][h]), the
-// heads in order; tokens outside the window only decay.  Four tokens a
-// thread, so that a warp reads 512 contiguous bytes of a head's logits.
-__global__ void __launch_bounds__(kScoreThreads) score_kernel(const __grid_constant__ PagedArgs a,
-                                                              int blocks_per_row) {
-    hs::pdl_trigger();
-    hs::pdl_wait();
-    const int row = blockIdx.x / blocks_per_row, part = blockIdx.x % blocks_per_row;
+// score[r][t] := decay * score[r][t] + sum_h 2^(x[r][h][t] - LSE[r][h]), the
+// heads in order; tokens outside the window only decay.  A thread per token,
+// sixteen heads' logits in flight; the heads' LSE first, a warp per head over
+// its parts, so that this needs no merge to have finished.
+__device__ __forceinline__ void score_tokens(const PagedArgs& a, const RowPlan& plan, int row,
+                                             int part, int blocks) {
+    __shared__ float lse2[kHeadChunk];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Tiling vis = tiling_of(a, a.seq_lens[row], 0);
     const int nvis = vis.T - vis.w0 + vis.sc;
     float* score = a.score + int64_t(row) * a.score_stride;
-    const float* lse2 = a.lse2 + int64_t(row) * a.heads;
-    // The visible tokens.
-    for (int64_t i0 = int64_t(part) * kScoreTokens; i0 < nvis;
-         i0 += int64_t(blocks_per_row) * kScoreTokens) {
-        const int i = int(i0) + 4 * threadIdx.x;
-        if (i >= nvis) break;
-        float w[4] = {0.f, 0.f, 0.f, 0.f};
-        const float* x = a.logits + int64_t(row) * a.heads * a.logit_stride + i;
-#pragma unroll 8
-        for (int h = 0; h < a.heads; ++h) {
-            const float ls = __ldg(lse2 + h);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(x + h * a.logit_stride));
-            // A head without any weight (LSE = -inf) adds nothing.
-            const float ref = ls == -CUDART_INF_F ? 0.f : ls;
-            w[0] += exp2f(v.x - ref);
-            w[1] += exp2f(v.y - ref);
-            w[2] += exp2f(v.z - ref);
-            w[3] += exp2f(v.w - ref);
-        }
+    for (int64_t i0 = int64_t(part) * kMergeThreads; i0 < nvis;
+         i0 += int64_t(blocks) * kMergeThreads) {
+        const int i = int(i0) + tid;
+        float w = 0.f;
+        for (int hc = 0; hc < a.heads; hc += kHeadChunk) {
+            const int nh = min(kHeadChunk, a.heads - hc);
+            if (a.heads > kHeadChunk || i0 == int64_t(part) * kMergeThreads) {
+                __syncthreads();
+                for (int h = warp; h < nh; h += kMergeWarps) {
+                    const Parts parts = parts_of(a, plan, hc + h);
+                    float M = -CUDART_INF_F, L = 0.f;
+                    if (parts.n == 1) {
+                        M = __ldcg(a.lse2 + int64_t(row) * a.heads + hc + h);
+                        L = lane == 0 ? 1.f : 0.f;
+                    } else {
+                        for (int p = lane; p < parts.n; p += 32) {
+                            const float2 ml =
+                                __ldcg(reinterpret_cast<const float2*>(a.part_ml) + parts.at(p));
+                            const float m = fmaxf(M, ml.x), ref = m == -CUDART_INF_F ? 0.f : m;
+                            L = fmaf(L, exp2f(M - ref), ml.y * exp2f(ml.x - ref));
+                            M = m;
+                        }
+                        const float own = M;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (i + j >= nvis) break;
-            const int t = i + j < vis.sc ? i + j : i + j - vis.sc + vis.w0;
-            score[t] = a.decay == 0.f ? w[j] : fmaf(a.decay, score[t], w[j]);
+                        for (int o = 16; o > 0; o >>= 1)
+                            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+                        L *= exp2f(own - (M == -CUDART_INF_F ? 0.f : M));
+                    }
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+                    // A head without any weight adds nothing: subtract 0.
+                    const float lg = L == 0.f ? -CUDART_INF_F : M + log2f(L);
+                    if (lane == 0) lse2[h] = lg == -CUDART_INF_F ? 0.f : lg;
+                }
+                __syncthreads();
+            }
+            if (i < nvis) {
+                const float* x =
+                    a.logits + (int64_t(row) * a.heads + hc) * a.logit_stride + i;
+#pragma unroll 16
+                for (int h = 0; h < nh; ++h)
+                    w += exp2f(__ldcg(x + h * a.logit_stride) - lse2[h]);
+            }
+        }
+        if (i < nvis) {
+            const int t = i < vis.sc ? i : i - vis.sc + vis.w0;
+            score[t] = a.decay == 0.f ? w : fmaf(a.decay, score[t], w);
         }
     }
     // Tokens between the sinks and the window.
     if (a.decay != 1.f)
-        for (int64_t t = vis.sc + int64_t(part) * kScoreThreads + threadIdx.x; t < vis.w0;
-             t += int64_t(blocks_per_row) * kScoreThreads)
+        for (int64_t t = vis.sc + int64_t(part) * kMergeThreads + tid; t < vis.w0;
+             t += int64_t(blocks) * kMergeThreads)
             score[t] = a.decay == 0.f ? 0.f : a.decay * score[t];
+}
+
+// What follows the attention: blocks (row, y < merges) join the parts of every
+// merges-th head of a request, the others score its tokens.  The plan depends
+// on seq_lens alone, which no longer changes once the attention kernel lets
+// this one start, so it is found while that kernel still runs.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) finish_kernel(const __grid_constant__ PagedArgs a,
+                                                               int merges, int out_bf16) {
+    hs::pdl_trigger();
+    const RowPlan plan = row_plan(a, blockIdx.x);
+    hs::pdl_wait();
+    if (int(blockIdx.y) < merges)
+        merge_heads<D>(a, plan, blockIdx.x, blockIdx.y, merges, out_bf16);
+    else
+        score_tokens(a, plan, blockIdx.x, blockIdx.y - merges, gridDim.y - merges);
 }
 
 struct Layout {
@@ -291,6 +345,12 @@ Layout layout(int32_t rows, int32_t heads, int32_t kv_heads, int32_t d, int32_t 
     return w;
 }
 
+// Tiles (of 16 tokens of a KV head at least) are counted in 31 bits.
+bool too_large(int32_t rows, int32_t heads, int32_t max_len) {
+    return rows > kMaxRows ||
+           int64_t(rows) * heads * (int64_t(max_len) / 16 + 2) >= (int64_t(1) << 31);
+}
+
 bool bad_shape(int32_t rows, int32_t heads, int32_t kv_heads, int32_t d, int32_t max_len,
                int32_t window, int32_t sinks) {
     return rows < 0 || heads <= 0 || kv_heads <= 0 || heads % kv_heads != 0 || d <= 0 ||
@@ -305,7 +365,9 @@ using namespace hs_paged;
 extern "C" int64_t hs_paged_decode_workspace_bytes(int32_t rows, int32_t heads, int32_t kv_heads,
                                                    int32_t d, int32_t max_len, int32_t window,
                                                    int32_t num_sinks, int32_t with_score) {
-    if (bad_shape(rows, heads, kv_heads, d, max_len, window, num_sinks)) return -1;
+    if (bad_shape(rows, heads, kv_heads, d, max_len, window, num_sinks) ||
+        too_large(rows, heads, max_len))
+        return -1;
     if (rows == 0) return 0;
     return layout(rows, heads, kv_heads, d, max_len, window, num_sinks, with_score != 0).total;
 }
@@ -331,10 +393,7 @@ extern "C" int hs_paged_decode(const void* q, int64_t q_stride, int32_t q_dtype,
         (kv_dtype != HS_E4M3 && kv_dtype != q_dtype) ||
         (kv_dtype != HS_E4M3 && (k_scale != nullptr || v_scale != nullptr)))
         return HS_ERR_UNSUPPORTED;
-    // Tiles (of 16 tokens of a KV head at least) are counted in 31 bits.
-    if (rows > kMaxRows ||
-        int64_t(rows) * heads * (int64_t(max_len) / 16 + 2) >= (int64_t(1) << 31))
-        return HS_ERR_CAPACITY;
+    if (too_large(rows, heads, max_len)) return HS_ERR_CAPACITY;
     if (rows == 0) return HS_OK;
     if (q == nullptr || k == nullptr || v == nullptr || seq_lens == nullptr || out == nullptr ||
         (block_table == nullptr && max_len > 0))
@@ -397,17 +456,17 @@ extern "C" int hs_paged_decode(const void* q, int64_t q_stride, int32_t q_dtype,
     else if (kv_dtype == HS_FP16) rc = launch_fp16(a, d, group, stream);
     else rc = launch_e4m3(a, d, group, stream);
     if (rc != HS_OK) return rc;
-    // A block per head where the blocks of a wave suffice, else several heads.
-    const int by = int(hs::max64(1, hs::min64(heads, 4 * int64_t(w.ctas) / rows)));
+    // Merging: a block per head where a few waves hold them, else several
+    // heads a block.  Scoring: a block per step of tokens, likewise.
+    const int64_t wave = 8 * int64_t(w.ctas);
+    const int merges = int(hs::max64(1, hs::min64(heads, wave / 2 / rows)));
+    const int64_t steps = (int64_t(max_len) + kMergeThreads - 1) / kMergeThreads;
+    const int scores =
+        score == nullptr ? 0 : int(hs::max64(1, hs::min64(steps, 2 * wave / rows)));
     const int bf = q_dtype == HS_BF16;
-    const dim3 mg{unsigned(rows), unsigned(by)}, mt{kMergeThreads};
-    if (d == 64) rc = hs_host::launch_pdl(merge_units<64>, mg, mt, 0, stream, a, bf);
-    else if (d == 128) rc = hs_host::launch_pdl(merge_units<128>, mg, mt, 0, stream, a, bf);
-    else rc = hs_host::launch_pdl(merge_units<256>, mg, mt, 0, stream, a, bf);
-    if (rc != HS_OK || score == nullptr) return rc;
-    // Enough blocks per request for its longest context, within a few waves.
-    const int64_t most = hs::max64(1, (int64_t(max_len) + kScoreTokens - 1) / kScoreTokens);
-    const int per_row = int(hs::min64(most, hs::max64(1, 16 * int64_t(w.ctas) / rows)));
-    return hs_host::launch_pdl(score_kernel, dim3(unsigned(rows) * unsigned(per_row)),
-                               dim3(kScoreThreads), 0, stream, a, per_row);
+    const dim3 grid{unsigned(rows), unsigned(merges + scores)}, block{kMergeThreads};
+    if (d == 64) return hs_host::launch_pdl(finish_kernel<64>, grid, block, 0, stream, a, merges, bf);
+    if (d == 128)
+        return hs_host::launch_pdl(finish_kernel<128>, grid, block, 0, stream, a, merges, bf);
+    return hs_host::launch_pdl(finish_kernel<256>, grid, block, 0, stream, a, merges, bf);
 }

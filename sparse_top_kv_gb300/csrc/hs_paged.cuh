@@ -147,54 +147,52 @@ __device__ __forceinline__ int way_of(const PagedArgs& a, int total0) {
 struct Run {
     int way, chunks, w0, run, row, row_tile0;
 };
-// Called by all THREADS threads of the CTA; `scratch` and `first` (two ints)
-// in shared memory.
-template <int THREADS>
-__device__ __forceinline__ Run make_run(const PagedArgs& a, int cta, int32_t (*scratch)[32],
-                                        int32_t* first) {
-    const int tid = threadIdx.x;
+// Every warp finds it for itself: a lane per request, a few dozen shuffles and
+// no barrier, so each role starts as soon as the lengths have arrived.
+__device__ __forceinline__ Run make_run(const PagedArgs& a, int cta) {
+    constexpr uint32_t kAll = 0xffffffffu;
+    const int lane = threadIdx.x & 31;
     int n0 = 0, n1 = 0;
-    for (int r = tid; r < a.rows; r += THREADS) {
+#pragma unroll 4
+    for (int r = lane; r < a.rows; r += 32) {
         const int len = __ldg(a.seq_lens + r);
         n0 += tiling_of(a, len, a.lth[0]).n;
         n1 += tiling_of(a, len, a.lth[1]).n;
-        if (cta == 0 && len > a.max_len) hs::set_status(a.status, HS_ERR_BAD_INDEX);
     }
-    int total0, total1;
-    const int before0 = hs::block_excl_scan(n0, scratch[0], &total0);
-    const int before1 = hs::block_excl_scan(n1, scratch[1], &total1);
+    const int mine0 = n0, mine1 = n1;
+    n0 = __reduce_add_sync(kAll, n0);
+    n1 = __reduce_add_sync(kAll, n1);
     Run x;
-    x.way = way_of(a, total0);
+    x.way = way_of(a, n0);
     x.chunks = a.chunks[x.way];
-    const Plan pl = plan_of(a, x.way, x.way == 0 ? total0 : total1);
+    const Plan pl = plan_of(a, x.way, x.way == 0 ? n0 : n1);
     x.w0 = cta < pl.n ? run_begin(pl, cta) : 0;
     x.run = cta < pl.n ? run_begin(pl, cta + 1) - x.w0 : 0;
-    // The row that the run begins in.
-    auto place = [&](int r, int at, int n) {
-        if (at * x.chunks <= x.w0 && x.w0 < (at + n) * x.chunks) {
-            first[0] = r;
-            first[1] = at;
-        }
-    };
-    if (a.rows <= THREADS) {
-        if (tid < a.rows) place(tid, x.way == 0 ? before0 : before1, x.way == 0 ? n0 : n1);
-    } else {
-        int carry = 0;
-        for (int r0 = 0; r0 < a.rows; r0 += THREADS) {
-            const int r = r0 + tid;
-            const int n =
-                r < a.rows ? tiling_of(a, __ldg(a.seq_lens + r), a.lth[x.way]).n : 0;
-            __syncthreads();
-            int sum;
-            const int at = carry + hs::block_excl_scan(n, scratch[0], &sum);
-            if (r < a.rows) place(r, at, n);
-            carry += sum;
-        }
+    // The row that the run begins in: the last whose first tile is at or
+    // before it (every row has a tile).
+    x.row = 0;
+    x.row_tile0 = 0;
+    for (int r0 = 0, carry = 0; r0 < a.rows; r0 += 32) {
+        const int r = r0 + lane;
+        int n = 0;
+        if (a.rows <= 32) n = x.way == 0 ? mine0 : mine1;
+        else if (r < a.rows) n = tiling_of(a, __ldg(a.seq_lens + r), a.lth[x.way]).n;
+        const int incl = carry + hs::warp_incl_scan(n);
+        const uint32_t before =
+            __ballot_sync(kAll, r < a.rows && int64_t(incl - n) * x.chunks <= x.w0);
+        if (before == 0) break;
+        const int last = 31 - __clz(before);
+        x.row = r0 + last;
+        x.row_tile0 = __shfl_sync(kAll, incl - n, last);
+        if (last < 31) break;
+        carry = __shfl_sync(kAll, incl, 31);
     }
-    __syncthreads();
-    x.row = first[0];
-    x.row_tile0 = first[1];
     return x;
+}
+// A length past max_len is reported once.
+__device__ __forceinline__ void report_lengths(const PagedArgs& a) {
+    for (int r = threadIdx.x; r < a.rows; r += blockDim.x)
+        if (a.seq_lens[r] > a.max_len) hs::set_status(a.status, HS_ERR_BAD_INDEX);
 }
 __device__ __forceinline__ Cursor cursor_at(const PagedArgs& a, const Run& x) {
     Cursor c;

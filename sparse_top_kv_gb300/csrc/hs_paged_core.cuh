@@ -149,8 +149,6 @@ paged_kernel(const __grid_constant__ PagedArgs a) {
     extern __shared__ __align__(128) unsigned char smem[];
     unsigned char* body = smem;                                      // ring / reduction
     uint32_t* live_s = reinterpret_cast<uint32_t*>(smem + C::kBody);  // [NW][S]
-    __shared__ int32_t scratch[2][32];
-    __shared__ int32_t first[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
 
@@ -160,7 +158,8 @@ paged_kernel(const __grid_constant__ PagedArgs a) {
     const int group = a.heads / a.kv_heads;
     const int gch = (group + GM - 1) / GM;
     const int cta = blockIdx.x;
-    const Run rn = make_run<C::kThreads>(a, cta, scratch, first);
+    const Run rn = make_run(a, cta);
+    if (cta == 0) report_lengths(a);
     if (rn.run <= 0) return;
     const int way = rn.way, lth = a.lth[way];
     const int hsn = a.hs[way], ts = NW / hsn;

@@ -30,8 +30,9 @@
 //    as several parts in columns of their own: a bf16 or fp16 value and the
 //    rounding's remainder, so weights keep twice the operand's precision.
 //  * E4M3 caches are multiplied as they are (kind::f8f6f4): the query, scaled
-//    by a power of two, becomes three E4M3 parts (each the rounding of 16
-//    times the remainder before it), P four; each part has columns of its own
+//    by a power of two, becomes several E4M3 parts (each the rounding of 16
+//    times the remainder before it: two hold the 8 bits of a bf16 query,
+//    three the 11 of an fp16 one), P four; each part has columns of its own
 //    and the parts are summed in fp32 with their weights 16^-i.
 // Every wait is bounded (HS_ERR_TIMEOUT in the status word on expiry).
 #pragma once
@@ -67,7 +68,8 @@ struct TcArgs {
     uint64_t timeout_ns;
 };
 
-template <int KV, int D, int GH>
+// QP: E4M3 parts of the query.
+template <int KV, int D, int GH, int QP>
 struct Cfg {
     static constexpr bool kE4 = KV == kE4m3;
     static constexpr int GM = 8 * GH;                    // query heads per KV head and unit
@@ -77,7 +79,7 @@ struct Cfg {
     static constexpr int kSubBlocks = kE4 ? 1 : (kBlocks < 2 ? 1 : 2);  // 128 dims of V
     static constexpr int kSub = kSubBlocks * kBlk;       // one ring unit
     static constexpr int kSubs = kBlocks / kSubBlocks;   // ring units of a tile
-    static constexpr int kQParts = kE4 ? 3 : 1;
+    static constexpr int kQParts = kE4 ? QP : 1;
     static constexpr int kPParts = kE4 ? 4 : 2;
     static constexpr int NH = GM * kQParts;              // query columns of a head
     static constexpr int NP = GM * kPParts;              // output columns of a head
@@ -111,8 +113,6 @@ struct Bars {
     uint64_t q_full, q_empty, o_free, drain[2];
     uint32_t tmem_base;
     volatile int32_t abort;
-    int32_t start_row[2];               // the run's first row and that row's first tile
-    int32_t scratch[2][32];
     uint32_t loaded[kMaskRing];         // runs of a tile that were loaded
     alignas(16) float red[kGroups][8][16];  // per 16 rows: maxima or sums
     float alpha[kGroups][8][16];        // rescale factors, [head][query]
@@ -209,13 +209,13 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-template <int KV, int D, int GH>
+template <int KV, int D, int GH, int QP>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUtensorMap kmap0,
                 const __grid_constant__ CUtensorMap vmap0,
                 const __grid_constant__ CUtensorMap kmap1,
                 const __grid_constant__ CUtensorMap vmap1) {
-    using C = Cfg<KV, D, GH>;
+    using C = Cfg<KV, D, GH, QP>;
     constexpr int GM = C::GM, NS = C::NS;
     constexpr bool E4 = C::kE4;
     const PagedArgs& a = ta.p;
@@ -256,20 +256,20 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
     if constexpr (E4)
         for (int i = tid; i < 2 * C::kPBytes / 16; i += kThreads)
             reinterpret_cast<uint4*>(smem + C::kPOff)[i] = make_uint4(0u, 0u, 0u, 0u);
+    hs::fence_proxy_async_shared();  // P's zeros, read by the tensor cores
+    hs::tc::fence_before_sync();
+    __syncthreads();
+    hs::tc::fence_after_sync();
     hs::pdl_wait();
-
     hs::pdl_trigger();
 
     const int group = a.heads / a.kv_heads;
     const int gch = (group + GM - 1) / GM;
     const int cta = blockIdx.x;
-    const Run rn = make_run<kThreads>(a, cta, B.scratch, B.start_row);
+    const Run rn = make_run(a, cta);
     const int way = rn.way, chunks = rn.chunks, run = rn.run;
     const Cursor start = cursor_at(a, rn);
-    hs::fence_proxy_async_shared();  // P's zeros, read by the tensor cores
-    hs::tc::fence_before_sync();
-    __syncthreads();
-    hs::tc::fence_after_sync();
+    if (cta == 0) report_lengths(a);
     const uint32_t tmem = B.tmem_base;
     const int hsn = a.hs[way], bt = ta.bt[way];
     // hs and bt are powers of two.
@@ -542,12 +542,18 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
                         e = max(7 - (int(__float_as_uint(mx) >> 23) - 127), -126);
                     const int ea = e / 2, eb = e - ea;
                     const float up = pow2(ea), up2 = pow2(eb);
-                    uint32_t code[3][4];
+                    // Rows without a query (the same for the whole warp where
+                    // its rows are all of one kind) are zero.
+                    uint32_t code[QP][4];
+#pragma unroll
+                    for (int k = 0; k < QP; ++k)
+                        code[k][0] = code[k][1] = code[k][2] = code[k][3] = 0u;
+                    if (__any_sync(0xffffffffu, mx > 0.f || odd)) {
 #pragma unroll
                     for (int i = 0; i < 16; i += 2) {
                         float r0 = x[i] * up * up2, r1 = x[i + 1] * up * up2;
 #pragma unroll
-                        for (int k = 0; k < 3; ++k) {
+                        for (int k = 0; k < QP; ++k) {
                             const uint32_t cc = odd ? 0x7f7fu : to_e4m3x2(r0, r1);
                             const float2 f = from_e4m3x2(cc);
                             code[k][i >> 2] =
@@ -556,9 +562,10 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
                             r1 = (r1 - f.y) * 16.f;
                         }
                     }
+                    }
                     if (hl < hsn) {
 #pragma unroll
-                        for (int k = 0; k < 3; ++k) {
+                        for (int k = 0; k < QP; ++k) {
                             const int m = hl * C::NH + k * GM + gi;
                             *reinterpret_cast<uint4*>(smem + C::kQOff + (ch >> 3) * nq * 128 +
                                                       m * 128 + (((ch & 7) ^ (m & 7)) << 4)) =
@@ -935,9 +942,9 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
 int encode_map(CUtensorMap* m, int kv, const void* base, const PagedArgs& a, int d, int bt,
                int hs_box);
 
-template <int KV, int D, int GH>
+template <int KV, int D, int GH, int QP>
 int launch_one(PagedArgs& a, hs_stream_t stream) {
-    using C = Cfg<KV, D, GH>;
+    using C = Cfg<KV, D, GH, QP>;
     constexpr int GM = C::GM;
     TcArgs t{};
     set_ways(a, C::kHsMax, kRows, GM, kTilesForWide);
@@ -953,7 +960,7 @@ int launch_one(PagedArgs& a, hs_stream_t stream) {
         if (rc == HS_OK) rc = encode_map(&m[2 * i + 1], KV, a.v, a, D, t.bt[i], a.hs[i]);
         if (rc != HS_OK) return rc;
     }
-    auto kern = paged_tc_kernel<KV, D, GH>;
+    auto kern = paged_tc_kernel<KV, D, GH, QP>;
     constexpr size_t smem = size_t(C::kBarOff) + sizeof(Bars) + 1024;
     static_assert(smem <= 227 * 1024, "shared memory");
     static int smem_set[64] = {};
@@ -964,16 +971,18 @@ int launch_one(PagedArgs& a, hs_stream_t stream) {
                                m[2], m[3]);
 }
 
-template <int KV>
+template <int KV, int QP>
 int launch_kind(PagedArgs& a, int d, int group, hs_stream_t stream) {
     if constexpr (KV != kE4m3) {
         if (d == 64)
-            return group <= 8 ? launch_one<KV, 64, 1>(a, stream)
-                              : launch_one<KV, 64, 2>(a, stream);
+            return group <= 8 ? launch_one<KV, 64, 1, QP>(a, stream)
+                              : launch_one<KV, 64, 2, QP>(a, stream);
     }
     if (d == 128)
-        return group <= 8 ? launch_one<KV, 128, 1>(a, stream) : launch_one<KV, 128, 2>(a, stream);
-    return group <= 8 ? launch_one<KV, 256, 1>(a, stream) : launch_one<KV, 256, 2>(a, stream);
+        return group <= 8 ? launch_one<KV, 128, 1, QP>(a, stream)
+                          : launch_one<KV, 128, 2, QP>(a, stream);
+    return group <= 8 ? launch_one<KV, 256, 1, QP>(a, stream)
+                      : launch_one<KV, 256, 2, QP>(a, stream);
 }
 
 }  // namespace tc

@@ -3,6 +3,6 @@
 
 namespace hs_paged {
 int launch_tc_fp16(PagedArgs& a, int d, int group, hs_stream_t stream) {
-    return tc::launch_kind<tc::kFp16>(a, d, group, stream);
+    return tc::launch_kind<tc::kFp16, 1>(a, d, group, stream);
 }
 }  // namespace hs_paged

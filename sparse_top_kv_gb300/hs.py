@@ -125,6 +125,13 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _raw_stream(device, stream=None):
+    """As _stream, as an int, for the current stream of `device` (an index)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
 def _call(name, *args):
     rc = getattr(lib(), name)(*args)
     if rc != HS_OK:
@@ -540,16 +547,20 @@ def sparse_decode_noalloc(q, k_base, v_base, row_stride, kv_head_stride, num_kv_
 
 
 # ---------------------------------------------------------------------------
+# Paged caches.  These calls are short next to their argument checks, so each
+# argument is first compared with what it should be in one expression; the
+# checkers below, which say what is wrong, run where that fails.
 _ELEMENT = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}  # HS_BF16, ..
+_I, _F = torch.int32, torch.float32
 
 
-def _check_cache(k_cache, v_cache):
+def _check_cache(k_cache, v_cache, device):
     """Paged caches [num_pages, page_size, kv_heads, d], any strides with
     contiguous rows (a [pages, heads, page, d] cache is passed transposed)."""
     if k_cache.dim() != 4 or k_cache.stride(3) != 1:
         raise ValueError("k_cache: [num_pages, page_size, kv_heads, d] with contiguous rows")
-    if not k_cache.is_cuda:
-        raise ValueError("k_cache: must be a CUDA tensor")
+    if k_cache.get_device() != device:
+        raise ValueError(f"k_cache: on {k_cache.device}, expected cuda:{device}")
     if v_cache is not None:
         if v_cache.dtype != k_cache.dtype or v_cache.device != k_cache.device:
             raise TypeError("v_cache: the type and device of k_cache")
@@ -557,22 +568,14 @@ def _check_cache(k_cache, v_cache):
             raise ValueError("v_cache: the shape and strides of k_cache")
 
 
-def _cache_strides(c):
-    """Page, row and head strides in elements; 0 for a dimension of one entry
-    (its stride is never used and may be anything)."""
-    return tuple(st if n > 1 else 0 for st, n in zip(c.stride()[:3], c.shape[:3]))
-
-
 def _check_rows(t, dtype, name, device, rows, cols=None):
     """A tensor of `rows` leading entries (and `cols` columns at least, rows a
-    stride apart) on `device`."""
-    if t is None:
-        return
+    stride apart) on CUDA device `device`."""
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    if t.shape[0] != rows or t.dim() != (1 if cols is None else 2):
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{device}")
+    if t.dim() != (1 if cols is None else 2) or t.shape[0] != rows:
         raise ValueError(f"{name}: expected {rows} rows, got shape {tuple(t.shape)}")
     if cols is None:
         if t.numel() > 1 and t.stride(0) != 1:
@@ -582,11 +585,59 @@ def _check_rows(t, dtype, name, device, rows, cols=None):
         raise ValueError(f"{name}: needs {cols} contiguous columns, its rows apart")
 
 
-def _check_out(t, dtype, name, device, shape):
-    if t.dtype != dtype or t.device != device:
-        raise TypeError(f"{name}: expected {dtype} on {device}")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+def _vector(t, dtype, name, device, n):
+    """Address of a contiguous 1-D tensor of n entries, or None."""
+    if t is None:
+        return None
+    if (t.dtype is not dtype or t.get_device() != device or t.shape != (n,)
+            or not t.is_contiguous()):
+        _check_rows(t, dtype, name, device, n)
+    return t.data_ptr()
+
+
+def _matrix(t, dtype, name, device, rows, cols):
+    """(address, elements between rows) of a 2-D tensor of at least `cols`
+    columns, or (None, 0)."""
+    if t is None:
+        return None, 0
+    shape, stride = t.shape, t.stride()
+    if (t.dtype is not dtype or t.get_device() != device or len(shape) != 2 or shape[0] != rows
+            or shape[1] < cols or stride[1] != 1 or stride[0] < shape[1]):
+        _check_rows(t, dtype, name, device, rows, cols)
+    return t.data_ptr(), stride[0] if rows > 1 else shape[1]
+
+
+def _output(t, dtype, name, device, shape):
+    """Address of a contiguous tensor of exactly this shape."""
+    if (t.dtype is not dtype or t.get_device() != device or t.shape != shape
+            or not t.is_contiguous()):
+        if t.dtype != dtype or t.get_device() != device:
+            raise TypeError(f"{name}: expected {dtype} on cuda:{device}")
         raise ValueError(f"{name}: expected contiguous {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _status_ptr(status):
+    if status is None:
+        return None
+    if status.dtype is not _I or not status.is_cuda:
+        _check(status, _I, "status")
+        return _ptr(status)
+    return status.data_ptr()
+
+
+def _cache_strides(c, unit):
+    """Page, row and head strides in elements times `unit`; 0 for a dimension
+    of one entry (its stride is never used and may be anything)."""
+    (p, r, h, _), (np_, nr, nh, _) = c.stride(), c.shape
+    return p * unit if np_ > 1 else 0, r * unit if nr > 1 else 0, h * unit if nh > 1 else 0
+
+
+def _current_device(t, name):
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name}: must be on the current CUDA device")
+    return dev
 
 
 def paged_decode_workspace_bytes(rows, heads, kv_heads, d, max_len, *, window=0, num_sinks=0,
@@ -604,115 +655,128 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, *, window=0,
     k_cache, v_cache [num_pages, page_size, kv_heads, d] of q's type or
     float8_e4m3fn (then k_scale, v_scale fp32 [kv_heads] or None), same
     strides; block_table int32 [rows, blocks]; seq_lens int32 [rows]; max_len
-    bounds seq_lens (default: what block_table and score hold).  score fp32 [rows, >=
-    max_len]: running scores, updated in place with the tokens' attention
-    weights summed over the heads.  Returns (out [rows, heads, d] of q's type,
-    lse fp32 [rows, heads])."""
-    if q.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"q: expected torch.bfloat16 or torch.float16, got {q.dtype}")
-    if not q.is_cuda or q.device.index != torch.cuda.current_device():
-        raise ValueError("q: must be on the current CUDA device")
-    _check_cache(k_cache, v_cache)
+    bounds seq_lens (default: what block_table and score hold).  score fp32
+    [rows, >= max_len]: running scores, updated in place with the tokens'
+    attention weights summed over the heads.  workspace: a CUDA tensor, used
+    if it is large enough (paged_decode_workspace_bytes).  Returns (out [rows,
+    heads, d] of q's type, lse fp32 [rows, heads])."""
+    dev = _current_device(q, "q")
+    qt, kt = q.dtype, k_cache.dtype
+    if qt is not torch.bfloat16 and qt is not torch.float16:
+        raise TypeError(f"q: expected torch.bfloat16 or torch.float16, got {qt}")
+    if kt not in _ELEMENT:
+        raise TypeError(f"k_cache: unsupported {kt}")
     if v_cache is None:
         raise ValueError("v_cache: needed")
-    if k_cache.dtype not in _ELEMENT:
-        raise TypeError(f"k_cache: unsupported {k_cache.dtype}")
-    rows, heads, d = q.shape
-    num_pages, page_size, kv_heads, dc = k_cache.shape
-    dev = q.device
-    if dc != d or k_cache.device != dev:
-        raise ValueError("k_cache: head size and device of q")
-    if rows and (q.stride(2) != 1 or q.stride(1) != d):
+    qshape, qstride, kshape, kstride = q.shape, q.stride(), k_cache.shape, k_cache.stride()
+    if (len(kshape) != 4 or kstride[3] != 1 or k_cache.get_device() != dev
+            or v_cache.dtype is not kt or v_cache.shape != kshape or v_cache.stride() != kstride
+            or v_cache.get_device() != dev):
+        _check_cache(k_cache, v_cache, dev)
+    rows, heads, d = qshape
+    num_pages, page_size, kv_heads, dc = kshape
+    if dc != d:
+        raise ValueError("k_cache: head size of q")
+    if rows and (qstride[2] != 1 or qstride[1] != d):
         raise ValueError("q: heads must be packed")
-    _check_rows(block_table, torch.int32, "block_table", dev, rows, 0)
+    table, table_stride = _matrix(block_table, _I, "block_table", dev, rows, 0)
     blocks = block_table.shape[1]
     if max_len is None:
         max_len = blocks * page_size
         if score is not None and score.dim() == 2:
             max_len = min(max_len, score.shape[1])
-    _check_rows(seq_lens, torch.int32, "seq_lens", dev, rows)
-    _check_rows(score, torch.float32, "score", dev, rows, max_len)
-    _check_rows(k_scale, torch.float32, "k_scale", dev, kv_heads)
-    _check_rows(v_scale, torch.float32, "v_scale", dev, kv_heads)
-    _check(status, torch.int32, "status")
+    lens = _vector(seq_lens, _I, "seq_lens", dev, rows)
+    score_ptr, score_stride = _matrix(score, _F, "score", dev, rows, max_len)
+    k_scale_ptr = _vector(k_scale, _F, "k_scale", dev, kv_heads)
+    v_scale_ptr = _vector(v_scale, _F, "v_scale", dev, kv_heads)
     if out is None:
-        out = torch.empty(rows, heads, d, dtype=q.dtype, device=dev)
-    else:
-        _check_out(out, q.dtype, "out", dev, (rows, heads, d))
+        out = torch.empty(rows, heads, d, dtype=qt, device=q.device)
     if lse is None:
-        lse = torch.empty(rows, heads, dtype=torch.float32, device=dev)
-    else:
-        _check_out(lse, torch.float32, "lse", dev, (rows, heads))
-    ws = int(lib().hs_paged_decode_workspace_bytes(rows, heads, kv_heads, d, max_len, window,
-                                                   num_sinks, 0 if score is None else 1))
-    if workspace is None or workspace.numel() * workspace.element_size() < ws:
-        workspace = torch.empty(max(ws, 1), dtype=torch.uint8, device=dev)
-    ps, rs, hstr = _cache_strides(k_cache)
-    _call("hs_paged_decode", _ptr(q), q.stride(0) if rows > 1 else heads * d, _ELEMENT[q.dtype], _ptr(k_cache),
-          _ptr(v_cache), _ELEMENT[k_cache.dtype], ps, rs, hstr, num_pages, page_size,
-          _ptr(block_table), _row_stride(block_table), blocks, max_len, _ptr(seq_lens),
-          _ptr(k_scale), _ptr(v_scale), rows, heads, kv_heads, d, window, num_sinks,
-          float(scale), _ptr(score), _row_stride(score),
-          float(score_decay), _ptr(out), _ptr(lse), _ptr(workspace),
-          workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream))
+        lse = torch.empty(rows, heads, dtype=_F, device=q.device)
+    out_ptr = _output(out, qt, "out", dev, qshape)
+    lse_ptr = _output(lse, _F, "lse", dev, (rows, heads))
+    ps, rs, hstr = _cache_strides(k_cache, 1)
+    call = lib().hs_paged_decode
+    for again in (False, True):
+        ws, ws_bytes = None, 0
+        if workspace is not None:
+            if workspace.get_device() != dev:
+                raise ValueError("workspace: must be on q's device")
+            ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        rc = call(q.data_ptr(), qstride[0] if rows > 1 else heads * d, _ELEMENT[qt],
+                  k_cache.data_ptr(), v_cache.data_ptr(), _ELEMENT[kt], ps, rs, hstr, num_pages,
+                  page_size, table, table_stride, blocks, max_len, lens, k_scale_ptr, v_scale_ptr,
+                  rows, heads, kv_heads, d, window, num_sinks, scale, score_ptr, score_stride,
+                  score_decay, out_ptr, lse_ptr, ws, ws_bytes, _status_ptr(status),
+                  _raw_stream(dev, stream))
+        if rc != 3 or again:
+            break
+        # HS_ERR_CAPACITY: the workspace is missing or too small.
+        n = paged_decode_workspace_bytes(rows, heads, kv_heads, d, max_len, window=window,
+                                         num_sinks=num_sinks, with_score=score is not None)
+        if n < 0:
+            break
+        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+    if rc != HS_OK:
+        raise HSError("hs_paged_decode", rc)
     return out, lse
 
 
 def _evict_args(score, seq_lens, budget, max_len, recent, num_sinks, positions, next_pos,
-                score_out, positions_out, lens_out, moves, status):
-    """Checked arguments of hs_evict_select, and what evict_select returns."""
-    if not score.is_cuda or score.device.index != torch.cuda.current_device():
-        raise ValueError("score: must be on the current CUDA device")
+                score_out, positions_out, lens_out, moves):
+    """Device, checked arguments of hs_evict_select, and what evict_select
+    returns."""
+    dev = _current_device(score, "score")
     if score.dim() != 2:
         raise ValueError("score: [rows, tokens]")
-    dev, rows = score.device, score.shape[0]
+    rows, width = score.shape
     if max_len is None:
-        max_len = score.shape[1]
-    _check_rows(score, torch.float32, "score", dev, rows, max_len)
-    _check_rows(positions, torch.int32, "positions", dev, rows, max_len)
-    _check_rows(seq_lens, torch.int32, "seq_lens", dev, rows)
-    _check_rows(next_pos, torch.int32, "next_pos", dev, rows)
-    score_out = score if score_out is None else score_out
-    positions_out = positions if positions_out is None else positions_out
-    lens_out = seq_lens if lens_out is None else lens_out
-    _check_rows(score_out, torch.float32, "score_out", dev, rows, max_len)
-    _check_rows(positions_out, torch.int32, "positions_out", dev, rows, max_len)
-    _check_rows(lens_out, torch.int32, "lens_out", dev, rows)
+        max_len = width
+    score_ptr, score_stride = _matrix(score, _F, "score", dev, rows, max_len)
+    pos_ptr, pos_stride = _matrix(positions, _I, "positions", dev, rows, max_len)
+    lens_ptr = _vector(seq_lens, _I, "seq_lens", dev, rows)
+    next_ptr = _vector(next_pos, _I, "next_pos", dev, rows)
+    if score_out is None:
+        score_out, so_ptr, so_stride = score, score_ptr, score_stride
+    else:
+        so_ptr, so_stride = _matrix(score_out, _F, "score_out", dev, rows, max_len)
+    if positions_out is None:
+        positions_out, po_ptr, po_stride = positions, pos_ptr, pos_stride
+    else:
+        po_ptr, po_stride = _matrix(positions_out, _I, "positions_out", dev, rows, max_len)
+    if lens_out is None:
+        lens_out, lo_ptr = seq_lens, lens_ptr
+    else:
+        lo_ptr = _vector(lens_out, _I, "lens_out", dev, rows)
     if moves is None:
         cap = max(0, min(budget, max_len - budget))
-        moves = (torch.empty(rows, cap, dtype=torch.int32, device=dev),
-                 torch.empty(rows, cap, dtype=torch.int32, device=dev),
-                 torch.empty(rows, dtype=torch.int32, device=dev))
+        i32 = dict(dtype=_I, device=score.device)
+        moves = (torch.empty(rows, cap, **i32), torch.empty(rows, cap, **i32),
+                 torch.empty(rows, **i32))
     src, dst, count = moves
-    cap = src.shape[1]
-    _check_out(src, torch.int32, "moves[0]", dev, (rows, cap))
-    _check_out(dst, torch.int32, "moves[1]", dev, (rows, cap))
-    _check_out(count, torch.int32, "moves[2]", dev, (rows,))
-    _check(status, torch.int32, "status")
-    args = (_ptr(score), _row_stride(score), _ptr(positions), _row_stride(positions),
-            _ptr(seq_lens), _ptr(next_pos), rows, max_len, budget, recent, num_sinks,
-            _ptr(score_out), _row_stride(score_out), _ptr(positions_out),
-            _row_stride(positions_out), _ptr(lens_out), _ptr(src), _ptr(dst), _ptr(count), cap)
-    return args, (score_out, positions_out, lens_out, moves)
+    shape = src.shape
+    if len(shape) != 2 or shape[0] != rows:
+        raise ValueError(f"moves[0]: expected {rows} rows, got shape {tuple(shape)}")
+    args = (score_ptr, score_stride, pos_ptr, pos_stride, lens_ptr, next_ptr, rows, max_len,
+            budget, recent, num_sinks, so_ptr, so_stride, po_ptr, po_stride, lo_ptr,
+            _output(src, _I, "moves[0]", dev, shape), _output(dst, _I, "moves[1]", dev, shape),
+            _vector(count, _I, "moves[2]", dev, rows), shape[1])
+    return dev, args, (score_out, positions_out, lens_out, moves)
 
 
-def _row_stride(t):
-    """Elements between the rows of a 2-D tensor (its width for a single row)."""
-    if t is None:
-        return 0
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _move_args(k_cache, v_cache, block_table, rows, device):
-    _check_cache(k_cache, v_cache)
-    if k_cache.device != device:
-        raise ValueError(f"k_cache: on {k_cache.device}, expected {device}")
-    _check_rows(block_table, torch.int32, "block_table", device, rows, 0)
-    num_pages, page_size, kv_heads, d = k_cache.shape
+def _move_args(k_cache, v_cache, block_table, rows, dev):
+    shape, stride = k_cache.shape, k_cache.stride()
+    if (len(shape) != 4 or stride[3] != 1 or k_cache.get_device() != dev
+            or v_cache is not None and (v_cache.dtype is not k_cache.dtype
+                                        or v_cache.shape != shape or v_cache.stride() != stride
+                                        or v_cache.get_device() != dev)):
+        _check_cache(k_cache, v_cache, dev)
+    table, table_stride = _matrix(block_table, _I, "block_table", dev, rows, 0)
+    num_pages, page_size, kv_heads, d = shape
     e = k_cache.element_size()
-    ps, rs, hstr = _cache_strides(k_cache)
-    return (_ptr(k_cache), _ptr(v_cache), ps * e, rs * e, hstr * e, kv_heads, d * e, num_pages,
-            page_size, _ptr(block_table), _row_stride(block_table), block_table.shape[1])
+    ps, rs, hstr = _cache_strides(k_cache, e)
+    return (k_cache.data_ptr(), None if v_cache is None else v_cache.data_ptr(), ps, rs, hstr,
+            kv_heads, d * e, num_pages, page_size, table, table_stride, block_table.shape[1])
 
 
 def evict_select(score, seq_lens, budget, *, max_len=None, recent=0, num_sinks=0, positions=None,
@@ -726,9 +790,12 @@ def evict_select(score, seq_lens, budget, *, max_len=None, recent=0, num_sinks=0
     to the inputs (updated in place).  Returns (score_out, positions_out,
     lens_out, (move_src, move_dst int32 [rows, cap], move_count int32
     [rows]))."""
-    args, result = _evict_args(score, seq_lens, budget, max_len, recent, num_sinks, positions,
-                               next_pos, score_out, positions_out, lens_out, moves, status)
-    _call("hs_evict_select", *args, _ptr(status), _stream(stream))
+    dev, args, result = _evict_args(score, seq_lens, budget, max_len, recent, num_sinks,
+                                    positions, next_pos, score_out, positions_out, lens_out,
+                                    moves)
+    rc = lib().hs_evict_select(*args, _status_ptr(status), _raw_stream(dev, stream))
+    if rc != HS_OK:
+        raise HSError("hs_evict_select", rc)
     return result
 
 
@@ -736,16 +803,17 @@ def evict_move(moves, k_cache, v_cache, block_table, *, status=None, stream=None
     """Apply evict_select's moves to a paged cache [num_pages, page_size,
     kv_heads, d] of any type (v_cache None: one cache) (hs_evict_move)."""
     src, dst, count = moves
-    rows, cap = src.shape
-    dev = src.device
-    if not src.is_cuda or dev.index != torch.cuda.current_device():
-        raise ValueError("moves: must be on the current CUDA device")
-    _check_out(src, torch.int32, "moves[0]", dev, (rows, cap))
-    _check_out(dst, torch.int32, "moves[1]", dev, (rows, cap))
-    _check_out(count, torch.int32, "moves[2]", dev, (rows,))
-    _check(status, torch.int32, "status")
-    _call("hs_evict_move", *_move_args(k_cache, v_cache, block_table, rows, dev), _ptr(src),
-          _ptr(dst), _ptr(count), rows, cap, _ptr(status), _stream(stream))
+    dev = _current_device(src, "moves")
+    shape = src.shape
+    if len(shape) != 2:
+        raise ValueError("moves[0]: [rows, cap]")
+    rows, cap = shape
+    lists = (_output(src, _I, "moves[0]", dev, shape), _output(dst, _I, "moves[1]", dev, shape),
+             _vector(count, _I, "moves[2]", dev, rows))
+    rc = lib().hs_evict_move(*_move_args(k_cache, v_cache, block_table, rows, dev), *lists, rows,
+                             cap, _status_ptr(status), _raw_stream(dev, stream))
+    if rc != HS_OK:
+        raise HSError("hs_evict_move", rc)
 
 
 def evict(score, seq_lens, budget, k_cache, v_cache, block_table, *, max_len=None, recent=0,
@@ -753,8 +821,11 @@ def evict(score, seq_lens, budget, k_cache, v_cache, block_table, *, max_len=Non
           lens_out=None, moves=None, status=None, stream=None):
     """evict_select, then evict_move on one layer's caches (hs_evict); same
     arguments and result as evict_select."""
-    args, result = _evict_args(score, seq_lens, budget, max_len, recent, num_sinks, positions,
-                               next_pos, score_out, positions_out, lens_out, moves, status)
-    _call("hs_evict", *args, *_move_args(k_cache, v_cache, block_table, score.shape[0],
-                                         score.device), _ptr(status), _stream(stream))
+    dev, args, result = _evict_args(score, seq_lens, budget, max_len, recent, num_sinks,
+                                    positions, next_pos, score_out, positions_out, lens_out,
+                                    moves)
+    rc = lib().hs_evict(*args, *_move_args(k_cache, v_cache, block_table, score.shape[0], dev),
+                        _status_ptr(status), _raw_stream(dev, stream))
+    if rc != HS_OK:
+        raise HSError("hs_evict", rc)
     return result

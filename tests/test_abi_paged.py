@@ -31,7 +31,8 @@ def decode(**kw):
     (2, dict(q=ODD)), (2, dict(k=ODD)), (2, dict(v=ODD)), (2, dict(out=ODD)),
     (2, dict(q_stride=1028)), (2, dict(row_stride=260)), (2, dict(head_stride=4)),
     (2, dict(page_stride=4100)), (2, dict(kv_dtype=2, row_stride=264)), (2, dict(ws=ODD)),
-    (3, dict()), (3, dict(rows=4097)), (3, dict(ws=P, ws_bytes=100)),
+    (3, dict()), (3, dict(rows=4097)),
+    (3, dict(rows=4096, heads=128, max_blocks=1 << 20, max_len=1 << 24)), (3, dict(ws=P, ws_bytes=100)),
     (7, dict(d=96)), (7, dict(kv_dtype=1)), (7, dict(q_dtype=1)), (7, dict(k_scale=P)),
     (7, dict(v_scale=P)), (0, dict(rows=0))])
 def test_paged_decode_checks(code, kw):
@@ -45,7 +46,8 @@ def test_paged_decode_workspace_query():
     # A window bounds the logits that a scored call keeps.
     assert f(2, 8, 2, 128, 100000, window=64, num_sinks=4, with_score=True) < f(
         2, 8, 2, 128, 100000, with_score=True)
-    assert f(-1, 8, 2, 128, 10) == -1 and f(1, 9, 2, 128, 10) == -1 and f(0, 8, 2, 128, 10) == 0
+    assert f(-1, 8, 2, 128, 10) == -1 and f(1, 9, 2, 128, 10) == -1 and f(
+        4097, 8, 2, 128, 10) == -1 and f(0, 8, 2, 128, 10) == 0
 
 
 SELECT = dict(score=P, score_stride=64, positions=None, pos_stride=0, lens=P, next_pos=None,
