@@ -276,3 +276,51 @@ def test_refusals(change, error):
         v = v[:4]
     with pytest.raises(error):
         hs.evict(score, lens, budget, k, v, table, **kw)
+
+
+@pytest.mark.parametrize("budget,over", [(1024, 8), (5, 8), (2048, 1), (4100, 8), (1, 3)])
+@pytest.mark.parametrize("fill", ["random", "equal", "nan"])
+def test_a_few_tokens_over(budget, over, fill):
+    """Requests at most a few tokens over the budget (a decode step's case)."""
+    W = budget + over
+    g = torch.Generator().manual_seed(W)
+    lens = [W, budget, budget + 1, 0, max(1, budget - 3), W - 1, W]
+    score = torch.rand(len(lens), W, generator=g)
+    if fill == "equal":
+        score[:] = -1.0
+    elif fill == "nan":
+        score[torch.rand(len(lens), W, generator=g) < 0.5] = float("nan")
+    positions = torch.stack([torch.randperm(W, generator=g) * 3 for _ in lens]).to(torch.int32)
+    for in_place in (True, False):
+        check(score, lens, budget, in_place=in_place)
+        check(score, lens, budget, recent=budget // 2, sinks=budget // 4, in_place=in_place,
+              positions=positions, next_pos=[3 * W + 1] * len(lens))
+
+
+@pytest.mark.parametrize("layout", ["packed", "heads_first", "single"])
+def test_a_few_tokens_over_moves(layout):
+    R, B, W, page = 6, 40, 48, 16
+    k, v = caches(R * 3 + 1, page, 3, 64, torch.bfloat16)
+    if layout == "heads_first":
+        k, v = (x.transpose(1, 2).contiguous().transpose(1, 2) for x in (k, v))
+    if layout == "single":
+        v = None
+    g = torch.Generator().manual_seed(5)
+    table = torch.randperm(R * 3, generator=g).view(R, 3).to(torch.int32).cuda()
+    table[4, 2] = 99  # a bad page: its rows are skipped and reported
+    score = torch.rand(R, W, generator=g).cuda()
+    score[4, 40:] = 9.0
+    lens = torch.tensor([48, 41, 40, 0, 48, 45], dtype=torch.int32, device="cuda")
+    old = [None if c is None else c.contiguous().clone() for c in (k, v)]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    src, dst, cnt = (m.cpu() for m in hs.evict(score, lens, B, k, v, table, status=status)[3])
+    assert int(status) == 6 and cnt.tolist()[2:4] == [0, 0] and cnt[4] == 8
+    tab = table.cpu()
+    for c, was in zip((k, v), old):
+        if c is None:
+            continue
+        want = was.clone()
+        for r in (0, 1, 5):
+            for s, t in zip(src[r, :cnt[r]].tolist(), dst[r, :cnt[r]].tolist()):
+                want[tab[r, t // page].long(), t % page] = was[tab[r, s // page].long(), s % page]
+        assert same_bits(c, want)
