@@ -591,8 +591,8 @@ int hs_paged_decode(const void* q, int64_t q_stride, int32_t q_dtype, const void
  * positions   int32 [rows, pos_stride]: position of the token in each place
  *             (moved tokens stand out of order), or NULL: the place itself.
  * next_pos    int32 [rows]: one more than the newest position, or NULL: T.
- * max_len     host-side bound on T (strides are at least max_len); a longer
- *             request counts as max_len tokens and is reported as
+ * max_len     host-side bound on T (strides are at least max_len; up to 2^30,
+ *             HS_ERR_CAPACITY above); a longer request counts as max_len tokens and is reported as
  *             HS_ERR_BAD_INDEX in *status.  T <= 0: an unused slot.
  * recent, num_sinks  recent + num_sinks <= budget.
  * score_out   fp32 [rows, score_out_stride], may be `score`: the kept

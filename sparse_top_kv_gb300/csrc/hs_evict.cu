@@ -14,15 +14,18 @@
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kDigit = 11;          // bits of a key decided in one pass
 constexpr int kBins = 1 << kDigit;
 constexpr int kCopies = 4;          // counters of a bin, by lane
-constexpr int kBinsPerThread = kBins / kThreads;
+static_assert(kBins == 2 * kThreads, "two bins a thread");
 constexpr int kMaxCluster = 8;
 constexpr int kCacheKeys = 40960;   // keys of a CTA's slice that shared memory keeps
-constexpr int kSliceMin = 4096;     // tokens a CTA of a cluster should have at least
+// Tokens a CTA of a cluster should have at least: below that the cluster's
+// barriers and remote loads cost what the shorter slice saves (32 requests of
+// 32 K tokens: 16.3 us at 8192 and 4096, 18.9 at 16384, 26.1 at 32768).
+constexpr int kSliceMin = 8192;
 constexpr int kTrimThreads = 1024;
 constexpr int kTrimKeys = 16;       // keys a thread of the trimming kernel holds
 constexpr int kTrimMost = 8;        // tokens that it evicts at most
@@ -70,6 +73,14 @@ __device__ __forceinline__ uint32_t peer_addr(const int* p, uint32_t rank) {
                  : "r"(hs::smem_u32(p)), "r"(rank));
     return addr;
 }
+__device__ __forceinline__ int2 peer_load2(const int* p, uint32_t rank) {
+    int2 v;
+    asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];"
+                 : "=r"(v.x), "=r"(v.y)
+                 : "r"(peer_addr(p, rank))
+                 : "memory");
+    return v;
+}
 __device__ __forceinline__ int4 peer_load4(const int* p, uint32_t rank) {
     int4 v;
     asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
@@ -111,8 +122,6 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int slice, int cached) 
 
     hs::pdl_trigger();
     hs::pdl_wait();
-    const int len = a.seq_lens[row];
-    const int T = min(max(len, 0), a.max_len), B = a.budget;
     const float* score = a.score + int64_t(row) * a.score_stride;
     const int32_t* pos = a.positions ? a.positions + int64_t(row) * a.pos_stride : nullptr;
     float* score_out = a.score_out + int64_t(row) * a.score_out_stride;
@@ -120,6 +129,23 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int slice, int cached) 
         a.positions_out ? a.positions_out + int64_t(row) * a.pos_out_stride : nullptr;
     const bool copy_score = a.score_out != a.score;
     const bool copy_pos = pos_out != nullptr && a.positions_out != a.positions;
+    // The first scores and positions are read along with the length (rows
+    // hold max_len entries; those past the length are not used).
+    constexpr int U = 8;
+    float x[U];
+    int32_t p[U];
+    {
+        const int e = min(a.max_len, int(rank) * slice + slice);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = int(rank) * slice + tid + u * kThreads;
+            x[u] = i < e ? score[i] : 0.f;
+            p[u] = pos != nullptr && i < e ? pos[i] : i;
+        }
+    }
+    const int len = a.seq_lens[row];
+    const int next = a.next_pos ? a.next_pos[row] : 0;
+    const int T = min(max(len, 0), a.max_len), B = a.budget;
     const int s0 = min(T, int(rank) * slice), s1 = min(T, s0 + slice);
     if (len > a.max_len && rank == 0 && tid == 0) hs::set_status(a.status, HS_ERR_BAD_INDEX);
 
@@ -135,22 +161,10 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int slice, int cached) 
         }
         return;
     }
-    const int newest = a.next_pos ? a.next_pos[row] : T;
-    const int64_t from = int64_t(newest) - a.recent;  // positions from here on are protected
+    const int64_t from = int64_t(a.next_pos ? next : T) - a.recent;  // positions from here on are protected
     auto make_key = [&](int i) {
         const int p = pos ? pos[i] : i;
         return order_key(score[i], p < a.sinks || p >= from);
-    };
-    // As make_key, and copies what stands below the budget on the way (a hole
-    // among it is overwritten by the row that moves there).
-    auto first_key = [&](int i) {
-        const float x = score[i];
-        const int p = pos ? pos[i] : i;
-        if (i < B) {
-            if (copy_score) score_out[i] = x;
-            if (copy_pos) pos_out[i] = p;
-        }
-        return order_key(x, p < a.sinks || p >= from);
     };
     auto key_at = [&](int i) { return cached ? keys[i - s0] : make_key(i); };
 
@@ -166,20 +180,29 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int slice, int cached) 
         __syncthreads();
         int* column = hist + (lane & (kCopies - 1)) * kBins;
         if (pass == 0) {
-            constexpr int U = 8;
+            // All loads of a batch ahead of its stores (the outputs may be the
+            // inputs, so the compiler keeps their order).  What stands below
+            // the budget is copied on the way: a hole among it is overwritten
+            // by the row that moves there.
             for (int i0 = s0 + tid; i0 < s1; i0 += U * kThreads) {
-                uint32_t k[U];
+                if (i0 >= int(rank) * slice + U * kThreads) {
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int i = i0 + u * kThreads;
-                    k[u] = i < s1 ? first_key(i) : 0u;
+                    for (int u = 0; u < U; ++u) {
+                        const int i = i0 + u * kThreads;
+                        x[u] = i < s1 ? score[i] : 0.f;
+                        p[u] = pos != nullptr && i < s1 ? pos[i] : i;
+                    }
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const int i = i0 + u * kThreads;
-                    if (i < s1) {
-                        if (cached) keys[i - s0] = k[u];
-                        atomicAdd(column + (k[u] >> 21), 1);
+                    if (i >= s1) break;
+                    const uint32_t k = order_key(x[u], p[u] < a.sinks || p[u] >= from);
+                    if (cached) keys[i - s0] = k;
+                    atomicAdd(column + (k >> 21), 1);
+                    if (i < B) {
+                        if (copy_score) score_out[i] = x[u];
+                        if (copy_pos) pos_out[i] = p[u];
                     }
                 }
             }
@@ -192,44 +215,35 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int slice, int cached) 
             }
         }
         __syncthreads();
-        // A thread sums four neighbouring bins; the cluster's counts of a pass
+        // A thread sums two neighbouring bins; the cluster's counts of a pass
         // are read before those of the next but one are written.
         int* mine = counts + (pass & 1) * kBins;
-        {
-            int4 n = make_int4(0, 0, 0, 0);
+        const int b0 = kBins - 2 * (tid + 1);  // from the largest digit down
+        int2 n = make_int2(0, 0);
 #pragma unroll
-            for (int c = 0; c < kCopies; ++c) {
-                const int4 x = reinterpret_cast<const int4*>(hist + c * kBins)[tid];
-                n.x += x.x;
-                n.y += x.y;
-                n.z += x.z;
-                n.w += x.w;
-            }
-            reinterpret_cast<int4*>(mine)[tid] = n;
-        }
-        cluster_sync();
-        // Counts of the whole request, from the largest digit down.
-        const int b0 = kBins - kBinsPerThread * (tid + 1);
-        int4 n = make_int4(0, 0, 0, 0);
-#pragma unroll 8
-        for (uint32_t c = 0; c < ncta; ++c) {
-            const int4 x = peer_load4(mine + b0, c);
+        for (int c = 0; c < kCopies; ++c) {
+            const int2 x = *reinterpret_cast<const int2*>(hist + c * kBins + b0);
             n.x += x.x;
             n.y += x.y;
-            n.z += x.z;
-            n.w += x.w;
+        }
+        if (ncta > 1) {
+            *reinterpret_cast<int2*>(mine + b0) = n;
+            cluster_sync();
+            n = make_int2(0, 0);
+            for (uint32_t c = 0; c < ncta; ++c) {
+                const int2 x = peer_load2(mine + b0, c);
+                n.x += x.x;
+                n.y += x.y;
+            }
         }
         int sum;
-        int before = hs::block_excl_scan((n.x + n.y) + (n.z + n.w), scratch, &sum);
-        const int v[4] = {n.w, n.z, n.y, n.x};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (before < need && need <= before + v[j]) {
-                pick[0] = b0 + 3 - j;
-                pick[1] = need - before;
-                pick[2] = need == before + v[j];
-            }
-            before += v[j];
+        const int before = hs::block_excl_scan(n.x + n.y, scratch, &sum);
+        if (before < need && need <= before + n.y + n.x) {
+            const bool low = need > before + n.y;  // the lower of the two bins
+            const int upto = before + n.y + (low ? n.x : 0);
+            pick[0] = low ? b0 : b0 + 1;
+            pick[1] = need - (low ? before + n.y : before);
+            pick[2] = need == upto;
         }
         __syncthreads();
         prefix |= uint32_t(pick[0]) << shift;
@@ -247,6 +261,7 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int slice, int cached) 
     const int per_warp = ((slice + kWarps - 1) / kWarps + 31) / 32 * 32;
     const int w0 = min(s1, s0 + warp * per_warp), w1 = min(s1, w0 + per_warp);
     int gt = 0, eq = 0, gt_low = 0, eq_low = 0;
+#pragma unroll 4
     for (int i0 = w0; i0 < w1; i0 += 32) {
         const int i = i0 + lane;
         const uint32_t k = i < w1 ? key_at(i) : 0u;
@@ -287,6 +302,7 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int slice, int cached) 
     int32_t* msrc = a.move_src + int64_t(row) * a.cap;
     int32_t* mdst = a.move_dst + int64_t(row) * a.cap;
     const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 4
     for (int i0 = w0; i0 < w1; i0 += 32) {
         const int i = i0 + lane;
         const bool in = i < w1;
@@ -348,9 +364,10 @@ __device__ __forceinline__ int64_t place_of(const MoveArgs& a, const int32_t* ta
 
 // A warp takes up to 32 moves at a time, a lane looking up one of them (the
 // offsets go to shared memory), and copies their rows of all caches as one
-// run of 16-byte pieces, a piece per lane and eight in flight.
+// run of 16-byte pieces, a piece per lane and four in flight (four CTAs an SM:
+// 8 in flight or 6 CTAs measured 10 % slower, the registers spill).
 constexpr int kMoveWarps = 8;
-constexpr int kMoveFlight = 8;
+constexpr int kMoveFlight = 4;
 __global__ void __launch_bounds__(kMoveWarps * 32, 4)
 evict_move_kernel(const __grid_constant__ MoveArgs a, int ctas_per_row) {
     __shared__ longlong2 offs[kMoveWarps][32];
@@ -450,17 +467,30 @@ evict_trim_kernel(const __grid_constant__ EvictArgs a, const __grid_constant__ M
     // one among them is overwritten or zeroed below.
     unsigned long long k[kTrimKeys];
 #pragma unroll
-    for (int u = 0; u < kTrimKeys; ++u) {
-        const int i = tid + u * kTrimThreads;
-        k[u] = ~0ull;
-        if (u * kTrimThreads < T && i < T) {
-            const float x = score[i];
-            const int p = pos ? pos[i] : i;
-            k[u] = (static_cast<unsigned long long>(order_key(x, p < a.sinks || p >= from)) << 32) |
-                   uint32_t(~i);
-            if (i < B) {
-                if (copy_score) score_out[i] = x;
-                if (copy_pos) pos_out[i] = p;
+    for (int u0 = 0; u0 < kTrimKeys; u0 += 4) {
+        if (u0 * kTrimThreads >= T) {
+            k[u0] = k[u0 + 1] = k[u0 + 2] = k[u0 + 3] = ~0ull;
+            continue;
+        }
+        // Four loads ahead of their stores (the outputs may be the inputs).
+        float x[4];
+        int32_t p[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = tid + (u0 + u) * kTrimThreads;
+            x[u] = i < T ? score[i] : 0.f;
+            p[u] = pos != nullptr && i < T ? pos[i] : i;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = tid + (u0 + u) * kTrimThreads;
+            const bool keep = p[u] < a.sinks || p[u] >= from;
+            k[u0 + u] = i < T ? (static_cast<unsigned long long>(order_key(x[u], keep)) << 32) |
+                                    uint32_t(~i)
+                              : ~0ull;
+            if (i < min(T, B)) {
+                if (copy_score) score_out[i] = x[u];
+                if (copy_pos) pos_out[i] = p[u];
             }
         }
     }
@@ -557,7 +587,8 @@ int check_select(const EvictArgs& a) {
     if (a.rows < 0 || a.max_len < 0 || a.budget <= 0 || a.recent < 0 || a.sinks < 0 ||
         int64_t(a.recent) + a.sinks > a.budget || a.cap < 0)
         return HS_ERR_INVALID_ARG;
-    // A request moves at most this many rows.
+    // Places are counted in 31 bits; a request moves at most this many rows.
+    if (a.max_len > (1 << 30)) return HS_ERR_CAPACITY;
     if (a.cap < hs::min64(a.budget, hs::max64(0, int64_t(a.max_len) - a.budget)))
         return HS_ERR_CAPACITY;
     if (a.rows == 0) return HS_OK;

@@ -101,6 +101,13 @@ __device__ __forceinline__ void advance(Cursor& c, const PagedArgs& a, int chunk
     ++c.row;
     cursor_row(c, a, lth);
 }
+// On to the run's next segment (left = 0: there is none).
+__device__ __forceinline__ void next_segment(Cursor& c, const PagedArgs& a, int chunks, int lth) {
+    const int n = min(c.left, c.v.n - c.tile);
+    c.left -= n - 1;
+    c.tile += n - 1;
+    advance(c, a, chunks, lth);
+}
 __device__ __forceinline__ int tile_token(const Cursor& c, int lth) {
     return (c.tile < c.v.ns ? c.tile : c.tile - c.v.ns + c.v.tw0) << lth;
 }

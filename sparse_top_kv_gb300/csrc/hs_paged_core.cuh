@@ -512,9 +512,7 @@ paged_kernel(const __grid_constant__ PagedArgs a) {
             }
         }
         __syncthreads();  // the reduction's buffer becomes the next unit's ring
-        c.left -= steps - 1;
-        c.tile += steps - 1;
-        advance(c, a, rn.chunks, lth);
+        next_segment(c, a, rn.chunks, lth);
     }
     if (bad) hs::set_status(a.status, HS_ERR_BAD_INDEX);
 }

@@ -80,6 +80,7 @@ struct Cfg {
     static constexpr int kSub = kSubBlocks * kBlk;       // one ring unit
     static constexpr int kSubs = kBlocks / kSubBlocks;   // ring units of a tile
     static constexpr int kQParts = kE4 ? QP : 1;
+    static constexpr int kQBufs = kE4 ? 2 : 1;  // the E4M3 parts take time to make
     static constexpr int kPParts = kE4 ? 4 : 2;
     static constexpr int NH = GM * kQParts;              // query columns of a head
     static constexpr int NP = GM * kPParts;              // output columns of a head
@@ -92,7 +93,8 @@ struct Cfg {
     static constexpr int q_rows(int hs) { return hs * NH < 16 ? 16 : (hs * NH + 15) / 16 * 16; }
     static constexpr int cols(int hs) { return 2 * q_rows(hs) + kGroups * kSubs * hs * NP; }
     static constexpr int units(int hs) {
-        return (227 * 1024 - 1024 - kBarBytes - q_rows(hs) * D * kElt - 2 * kPBytes) / (2 * kSub);
+        return (227 * 1024 - 1024 - kBarBytes - kQBufs * q_rows(hs) * D * kElt - 2 * kPBytes) /
+               (2 * kSub);
     }
     static constexpr bool fits(int hs) { return cols(hs) <= kTmemCols && units(hs) >= 3; }
     static constexpr int kHsMax = fits(8) ? 8 : fits(4) ? 4 : fits(2) ? 2 : 1;
@@ -103,14 +105,14 @@ struct Cfg {
     static constexpr int kKOff = 0;
     static constexpr int kVOff = kKOff + NS * kSub;
     static constexpr int kQOff = kVOff + NS * kSub;
-    static constexpr int kPOff = kQOff + kQBytes;
+    static constexpr int kPOff = kQOff + kQBufs * kQBytes;
     static constexpr int kBarOff = kPOff + 2 * kPBytes;
 };
 
 struct Bars {
     uint64_t kfull[8], kempty[8], vfull[8], vempty[8];
     uint64_t s_full[2], p_full[2], pv_done[2];
-    uint64_t q_full, q_empty, o_free, drain[2];
+    uint64_t q_full[2], q_empty, o_free, drain[2];
     uint32_t tmem_base;
     volatile int32_t abort;
     uint32_t loaded[kMaskRing];         // runs of a tile that were loaded
@@ -209,6 +211,82 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// E4M3 parts of the queries of a segment: step `it` makes 512 / D rows (head
+// hl, query gi) of the unit, a lane 16 dims of one.  A function of its own, so
+// that its two callers share the instructions.
+template <int D, int GH, int QP>
+__device__ __noinline__ void query_parts(const PagedArgs& a, Bars& B, unsigned char* qbuf, int nq,
+                                         int hsn, int row, int chunk, int seg, int it) {
+    constexpr int GM = 8 * GH, NH = GM * QP, kL = D / 16;
+    const int lane = threadIdx.x & 31;
+    const int group = a.heads / a.kv_heads, gch = (group + GM - 1) / GM;
+    const int kvh0 = chunk / gch * hsn, gc = chunk % gch;
+    const int Gc = min(GM, group - gc * GM);
+    const int ch = lane % kL, n = it * (32 / kL) + lane / kL, hl = n / GM, gi = n % GM;
+    uint4 raw[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+    if (gi < Gc) {
+        const uint4* p = reinterpret_cast<const uint4*>(
+            static_cast<const char*>(a.q) +
+            (int64_t(row) * a.q_stride + int64_t((kvh0 + hl) * group + gc * GM + gi) * D +
+             ch * 16) * 2);
+        raw[0] = __ldg(p);
+        raw[1] = __ldg(p + 1);
+    }
+    float x[16];
+    const uint32_t w[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w,
+                           raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 f = QP == 3 ? __half22float2(*reinterpret_cast<const __half2*>(&w[i]))
+                                 : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+    float mx = 0.f;
+    bool odd = false;  // not finite: shows as NaN
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        mx = fmaxf(mx, fabsf(x[i]));
+        odd |= !(fabsf(x[i]) < CUDART_INF_F);
+    }
+#pragma unroll
+    for (int o = kL / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    // Largest magnitude to [2^7, 2^8), by two factors (their product may lie
+    // outside fp32's range).
+    int e = 0;
+    if (mx > 0.f && mx < CUDART_INF_F)
+        e = max(7 - (int(__float_as_uint(mx) >> 23) - 127), -126);
+    const int ea = e / 2, eb = e - ea;
+    const float up = pow2(ea), up2 = pow2(eb);
+    uint32_t code[QP][4];
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+        float r0 = x[i] * up * up2, r1 = x[i + 1] * up * up2;
+#pragma unroll
+        for (int k = 0; k < QP; ++k) {
+            const uint32_t cc = odd ? 0x7f7fu : to_e4m3x2(r0, r1);
+            code[k][i >> 2] = (i & 2) ? code[k][i >> 2] | (cc << 16) : cc;
+            if (k + 1 < QP) {
+                const float2 f = from_e4m3x2(cc);
+                r0 = (r0 - f.x) * 16.f;
+                r1 = (r1 - f.y) * 16.f;
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < QP; ++k) {
+        const int m = hl * NH + k * GM + gi;
+        *reinterpret_cast<uint4*>(qbuf + (ch >> 3) * nq * 128 + m * 128 +
+                                  (((ch & 7) ^ (m & 7)) << 4)) =
+            make_uint4(code[k][0], code[k][1], code[k][2], code[k][3]);
+    }
+    if (ch == 0) {
+        float f = a.scale_log2 * pow2(-ea) * pow2(-eb);
+        if (a.k_scale != nullptr) f *= __ldg(a.k_scale + kvh0 + hl);
+        B.qscale[seg & 3][hl * GM + gi] = f;
+    }
+}
+
 template <int KV, int D, int GH, int QP>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUtensorMap kmap0,
@@ -240,7 +318,9 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
             hs::mbar_init(&B.p_full[i], kSoftThreads);
             hs::mbar_init(&B.pv_done[i], 1);
         }
-        hs::mbar_init(&B.q_full, 32);
+        for (int i = 0; i < C::kQBufs; ++i) {
+            hs::mbar_init(&B.q_full[i], E4 ? kGroups * kSoftThreads : 32);
+        }
         hs::mbar_init(&B.q_empty, 1);
         hs::mbar_init(&B.o_free, kGroups * kSoftThreads);
         hs::mbar_init(&B.drain[0], 1);
@@ -252,11 +332,14 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
         hs::tc::tmem_alloc(&B.tmem_base, kTmemCols);
         hs::tc::tmem_relinquish();
     }
-    // P's rows of the other head of a K step stay zero.
-    if constexpr (E4)
-        for (int i = tid; i < 2 * C::kPBytes / 16; i += kThreads)
-            reinterpret_cast<uint4*>(smem + C::kPOff)[i] = make_uint4(0u, 0u, 0u, 0u);
-    hs::fence_proxy_async_shared();  // P's zeros, read by the tensor cores
+    // P's rows of the other head of a K step stay zero, and so do the rows of
+    // queries that a unit does not have.
+    if constexpr (E4) {
+        constexpr int kBytes = C::kBarOff - C::kQOff;
+        for (int i = tid; i < kBytes / 16; i += kThreads)
+            reinterpret_cast<uint4*>(smem + C::kQOff)[i] = make_uint4(0u, 0u, 0u, 0u);
+        hs::fence_proxy_async_shared();
+    }
     hs::tc::fence_before_sync();
     __syncthreads();
     hs::tc::fence_after_sync();
@@ -357,11 +440,15 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
             const uint64_t q_desc = hs::tc::sdesc_sw128(sb + C::kQOff, 16, 1024);
             Cursor c = start;
             bool ok = true;
-            int slot = 0;
+            int slot = 0, qb = 0;
             uint32_t phase = 0;
             for (int t = 0, seg = 0; t < run; ++t) {
-                if (c.first)
-                    ok = ok && hs::mbar_wait_bounded(&B.q_full, seg++ & 1, tmo, abort_flag);
+                if (c.first) {
+                    qb = seg % C::kQBufs;
+                    ok = ok && hs::mbar_wait_bounded(&B.q_full[qb], (seg / C::kQBufs) & 1, tmo,
+                                                     abort_flag);
+                    ++seg;
+                }
                 // The softmax of two tiles ago has read this S buffer.
                 if (t >= 2)
                     ok = ok && hs::mbar_wait_bounded(&B.p_full[t & 1], ((t - 2) >> 1) & 1, tmo,
@@ -373,7 +460,8 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
                     if (!ok) break;
                     hs::tc::fence_after_sync();
                     const uint64_t kd = k_desc + uint32_t(slot * (C::kSub >> 4));
-                    const uint64_t qd = q_desc + uint32_t(s * C::kSubBlocks * nq * 8);
+                    const uint64_t qd =
+                        q_desc + uint32_t(qb * (C::kQBytes >> 4) + s * C::kSubBlocks * nq * 8);
 #pragma unroll
                     for (int b = 0; b < C::kSubBlocks; ++b) {
 #pragma unroll
@@ -390,7 +478,7 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
                 }
                 if (!ok) break;
                 hs::tc::mma_commit(&B.s_full[t & 1]);
-                if (last_of_segment(c)) hs::tc::mma_commit(&B.q_empty);
+                if (!E4 && last_of_segment(c)) hs::tc::mma_commit(&B.q_empty);
                 if (t + 1 < run) advance(c, a, chunks, lth);
             }
             if (!ok) {
@@ -468,20 +556,20 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
         }
         __syncwarp();
     } else if (warp == kQWarp) {
-        // ------------------------------ queries ------------------------------
-        Cursor c = start;
-        bool ok = true;
-        for (int seg = 0; c.left > 0; ++seg) {
-            if (seg > 0 && !__all_sync(0xffffffffu,
-                                       hs::mbar_wait_bounded(&B.q_empty, (seg - 1) & 1, tmo,
-                                                             abort_flag))) {
-                ok = false;
-                break;
-            }
-            const int kvh0 = c.chunk / gch * hsn, gc = c.chunk % gch;
-            const int Gc = min(GM, group - gc * GM);
-            const char* q = static_cast<const char*>(a.q) + int64_t(c.row) * a.q_stride * 2;
-            if constexpr (!E4) {
+        // ------------------- queries (E4M3: the softmax warps) -------------------
+        if constexpr (!E4) {
+            Cursor c = start;
+            bool ok = true;
+            for (int seg = 0; c.left > 0; ++seg) {
+                if (seg > 0 && !__all_sync(0xffffffffu,
+                                           hs::mbar_wait_bounded(&B.q_empty, (seg - 1) & 1, tmo,
+                                                                 abort_flag))) {
+                    ok = false;
+                    break;
+                }
+                const int kvh0 = c.chunk / gch * hsn, gc = c.chunk % gch;
+                const int Gc = min(GM, group - gc * GM);
+                const char* q = static_cast<const char*>(a.q) + int64_t(c.row) * a.q_stride * 2;
                 constexpr int kCh = D / 8;  // 16-byte chunks of a query row
                 for (int e = lane; e < nq * kCh; e += 32) {
                     const int n = e / kCh, ch = e % kCh;
@@ -493,103 +581,14 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
                                        q + int64_t(h) * D * 2 + ch * 16, in ? 16u : 0u);
                 }
                 hs::tc::cp_async_wait_all();
-            } else {
-                // Lanes of 16 dims, D / 16 of them a row; the loads of all
-                // rows are in flight together.
-                constexpr int kL = D / 16, kIter = C::kHsMax * GM * kL / 32;
-                const int ch = lane % kL;
-                uint4 raw[kIter][2];
-#pragma unroll
-                for (int it = 0; it < kIter; ++it) {
-                    const int n = it * (32 / kL) + lane / kL, hl = n / GM, gi = n % GM;
-                    raw[it][0] = raw[it][1] = make_uint4(0u, 0u, 0u, 0u);
-                    if (hl < hsn && gi < Gc) {
-                        const uint4* p = reinterpret_cast<const uint4*>(
-                            q + (int64_t((kvh0 + hl) * group + gc * GM + gi) * D + ch * 16) * 2);
-                        raw[it][0] = __ldg(p);
-                        raw[it][1] = __ldg(p + 1);
-                    }
-                }
-#pragma unroll
-                for (int it = 0; it < kIter; ++it) {
-                    const int n = it * (32 / kL) + lane / kL, hl = n / GM, gi = n % GM;
-                    float x[16];
-                    const uint32_t w[8] = {raw[it][0].x, raw[it][0].y, raw[it][0].z, raw[it][0].w,
-                                           raw[it][1].x, raw[it][1].y, raw[it][1].z, raw[it][1].w};
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 f =
-                            a.q_is_half
-                                ? __half22float2(*reinterpret_cast<const __half2*>(&w[i]))
-                                : __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
-                        x[2 * i] = f.x;
-                        x[2 * i + 1] = f.y;
-                    }
-                    float mx = 0.f;
-                    bool odd = false;  // not finite: shows as NaN
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        mx = fmaxf(mx, fabsf(x[i]));
-                        odd |= !(fabsf(x[i]) < CUDART_INF_F);
-                    }
-#pragma unroll
-                    for (int o = kL / 2; o > 0; o >>= 1)
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                    // Largest magnitude to [2^7, 2^8), by two factors (their
-                    // product may lie outside fp32's range).
-                    int e = 0;
-                    if (mx > 0.f && mx < CUDART_INF_F)
-                        e = max(7 - (int(__float_as_uint(mx) >> 23) - 127), -126);
-                    const int ea = e / 2, eb = e - ea;
-                    const float up = pow2(ea), up2 = pow2(eb);
-                    // Rows without a query (the same for the whole warp where
-                    // its rows are all of one kind) are zero.
-                    uint32_t code[QP][4];
-#pragma unroll
-                    for (int k = 0; k < QP; ++k)
-                        code[k][0] = code[k][1] = code[k][2] = code[k][3] = 0u;
-                    if (__any_sync(0xffffffffu, mx > 0.f || odd)) {
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        float r0 = x[i] * up * up2, r1 = x[i + 1] * up * up2;
-#pragma unroll
-                        for (int k = 0; k < QP; ++k) {
-                            const uint32_t cc = odd ? 0x7f7fu : to_e4m3x2(r0, r1);
-                            const float2 f = from_e4m3x2(cc);
-                            code[k][i >> 2] =
-                                (i & 2) ? code[k][i >> 2] | (cc << 16) : cc;
-                            r0 = (r0 - f.x) * 16.f;
-                            r1 = (r1 - f.y) * 16.f;
-                        }
-                    }
-                    }
-                    if (hl < hsn) {
-#pragma unroll
-                        for (int k = 0; k < QP; ++k) {
-                            const int m = hl * C::NH + k * GM + gi;
-                            *reinterpret_cast<uint4*>(smem + C::kQOff + (ch >> 3) * nq * 128 +
-                                                      m * 128 + (((ch & 7) ^ (m & 7)) << 4)) =
-                                make_uint4(code[k][0], code[k][1], code[k][2], code[k][3]);
-                        }
-                        if (ch == 0) {
-                            float f = a.scale_log2 * pow2(-ea) * pow2(-eb);
-                            if (a.k_scale != nullptr) f *= __ldg(a.k_scale + kvh0 + hl);
-                            B.qscale[seg & 3][hl * GM + gi] = f;
-                        }
-                    }
-                }
+                hs::fence_proxy_async_shared();
+                hs::mbar_arrive(&B.q_full[0]);
+                next_segment(c, a, chunks, lth);
             }
-            hs::fence_proxy_async_shared();
-            hs::mbar_arrive(&B.q_full);
-            // On to the next segment.
-            const int n = min(c.left, c.v.n - c.tile);
-            c.left -= n - 1;
-            c.tile += n - 1;
-            advance(c, a, chunks, lth);
-        }
-        if (!ok) {
-            hs::set_status(a.status, HS_ERR_TIMEOUT);
-            B.abort = 1;
+            if (!ok) {
+                hs::set_status(a.status, HS_ERR_TIMEOUT);
+                B.abort = 1;
+            }
         }
     } else {
         // ------------------------- softmax and epilogue ------------------------
@@ -641,6 +640,22 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
             __syncwarp();
         };
         Cursor c = start;
+        // E4M3: the parts of a segment's queries, a step of rows per warp.  The
+        // buffer's last reader, the segment before last, is done by then.
+        auto make_parts = [&](const Cursor& x, int seg) {
+            if constexpr (E4) {
+                const int Gc = min(GM, group - x.chunk % gch * GM);
+                constexpr int kStepRows = 512 / D;
+                for (int it = warp; it * kStepRows < hsn * GM; it += kGroups * 4)
+                    if (it * kStepRows % GM < Gc)
+                        query_parts<D, GH, QP>(a, B, smem + C::kQOff + (seg & 1) * C::kQBytes, nq,
+                                               hsn, x.row, x.chunk, seg, it);
+                __syncwarp();
+                hs::fence_proxy_async_shared();
+                hs::mbar_arrive(&B.q_full[seg & 1]);
+            }
+        };
+        make_parts(c, 0);
         for (int t = 0, seg = 0; t < run; ++seg) {
             // ---- One segment: the tiles of one unit in this run ----------------
             const int row = c.row;
@@ -649,6 +664,11 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
             const Tiling v = c.v;
             const int tile0 = c.tile, n = min(c.left, v.n - tile0), t0 = t;
             const bool whole = n == v.n;
+            if (E4 && c.left > n) {
+                Cursor x = c;
+                next_segment(x, a, chunks, lth);
+                make_parts(x, seg + 1);
+            }
             const int slot = 2 * cta + (tile0 == 0 && t > 0 ? 1 : 0);
             float mref[GM], l[GM];
 #pragma unroll

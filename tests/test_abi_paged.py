@@ -60,6 +60,7 @@ MOVE = dict(k=P, v=None, page_stride=4096, row_stride=256, head_stride=128, kv_h
 SELECT_BAD = [
     (1, dict(rows=-1)), (1, dict(max_len=-1)), (1, dict(budget=0)), (1, dict(recent=-1)),
     (1, dict(sinks=-1)), (1, dict(recent=31)), (1, dict(cap=-1)), (3, dict(cap=31)),
+    (3, dict(max_len=(1 << 30) + 1)),
     (1, dict(score=None)), (1, dict(lens=None)), (1, dict(score_out=None)),
     (1, dict(lens_out=None)), (1, dict(src=None)), (1, dict(dst=None)), (1, dict(count=None)),
     (1, dict(score_stride=63)), (1, dict(score_out_stride=63)),
