@@ -127,8 +127,9 @@ __device__ __forceinline__ Parts parts_of(const PagedArgs& a, const RowPlan& r, 
     const int hs = a.hs[r.way], kvh = h / group, gi = h % group;
     const int hu = (kvh % hs) * a.gm + gi % a.gm;
     const int start = r.first_tile + (kvh / hs * gch + gi / a.gm) * r.row_tiles;
+    Parts p{};
+    if (r.row_tiles == 0) return p;  // a request without tokens
     const int c0 = run_of(r.pl, start), c1 = run_of(r.pl, start + r.row_tiles - 1);
-    Parts p;
     p.n = c1 - c0 + 1;
     p.step = 2 * int64_t(a.unit_heads_max);
     p.rest = c0 * p.step + hu;
@@ -139,105 +140,168 @@ __device__ __forceinline__ Parts parts_of(const PagedArgs& a, const RowPlan& r, 
 
 // Merge of the units whose tiles were dealt to several CTAs (the others were
 // written by their CTA): out = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p.
-// A warp reads every eighth partial row, so all loads of a head's merge are
-// in flight at once.
+// A warp's share is the parts first, first + step, ..: a lane per part for the
+// maxima and sums, then the partial rows, eight in flight.
 template <int D>
-__device__ __forceinline__ void merge_heads(const PagedArgs& a, const RowPlan& plan, int row,
-                                            int h0, int step, int out_bf16) {
-    constexpr int NW = kMergeWarps;
-    constexpr int V4 = D / 4;                    // float4s of a row
-    constexpr int PL = V4 > 32 ? V4 / 32 : 1;    // float4s of a lane
-    __shared__ float wt[kMaxCtas];
-    __shared__ float red[2][NW];
-    __shared__ float4 acc[NW][V4];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    for (int h = h0; h < a.heads; h += step) {
-        const Parts parts = parts_of(a, plan, h);
-        if (parts.n == 1) continue;
-        const int64_t qh = int64_t(row) * a.heads + h;
-        float2 ml[kMaxCtas / kMergeThreads];
-        float M = -CUDART_INF_F;
+struct MergeState {
+    static constexpr int V4 = D / 4;                  // float4s of a row
+    static constexpr int PL = V4 > 32 ? V4 / 32 : 1;  // float4s of a lane
+    float m, l;
+    float4 o[PL];
+};
+template <int D>
+__device__ __forceinline__ MergeState<D> merge_share(const PagedArgs& a, const Parts& parts,
+                                                     int first, int step) {
+    using S = MergeState<D>;
+    const int lane = threadIdx.x & 31;
+    S s;
+    s.m = -CUDART_INF_F;
+    s.l = 0.f;
 #pragma unroll
-        for (int i = 0; i < kMaxCtas / kMergeThreads; ++i) {
-            const int p = tid + i * kMergeThreads;
-            ml[i] = p < parts.n
-                        ? __ldcg(reinterpret_cast<const float2*>(a.part_ml) + parts.at(p))
-                        : make_float2(-CUDART_INF_F, 0.f);
-            M = fmaxf(M, ml[i].x);
-        }
+    for (int i = 0; i < S::PL; ++i) s.o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = first; p0 < parts.n; p0 += 32 * step) {
+        const int p = p0 + lane * step;
+        const float2 ml = p < parts.n
+                              ? __ldcg(reinterpret_cast<const float2*>(a.part_ml) + parts.at(p))
+                              : make_float2(-CUDART_INF_F, 0.f);
+        float mx = fmaxf(s.m, ml.x);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        if (lane == 0) red[0][warp] = M;
-        __syncthreads();
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float ref = mx == -CUDART_INF_F ? 0.f : mx;
+        const float keep = exp2f(s.m - ref), w = exp2f(ml.x - ref);
+        float l = w * ml.y;
 #pragma unroll
-        for (int i = 0; i < NW; ++i) M = fmaxf(M, red[0][i]);
-        const float ref = M == -CUDART_INF_F ? 0.f : M;
-        float L = 0.f;
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        s.l = fmaf(s.l, keep, l);
+        s.m = mx;
+        if (p0 != first) {
 #pragma unroll
-        for (int i = 0; i < kMaxCtas / kMergeThreads; ++i) {
-            const int p = tid + i * kMergeThreads;
-            if (p < parts.n) {
-                const float w = exp2f(ml[i].x - ref);
-                wt[p] = w;
-                L = fmaf(w, ml[i].y, L);
+            for (int i = 0; i < S::PL; ++i) {
+                s.o[i].x *= keep;
+                s.o[i].y *= keep;
+                s.o[i].z *= keep;
+                s.o[i].w *= keep;
             }
         }
+        const int n = min(32, (parts.n - p0 + step - 1) / step);
+#pragma unroll 8
+        for (int k = 0; k < n; ++k) {
+            const float f = __shfl_sync(0xffffffffu, w, k);
+            const float4* po =
+                reinterpret_cast<const float4*>(a.part_o + parts.at(p0 + k * step) * D);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-        if (lane == 0) red[1][warp] = L;
-        __syncthreads();
-        float4 s[PL];
-#pragma unroll
-        for (int i = 0; i < PL; ++i) s[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int p = warp; p < parts.n; p += NW) {
-            const float w = wt[p];
-            const float4* po = reinterpret_cast<const float4*>(a.part_o + parts.at(p) * D);
-#pragma unroll
-            for (int i = 0; i < PL; ++i) {
-                const int c = lane + 32 * i;
-                if (c < V4) {
-                    const float4 x = __ldcg(po + c);
-                    s[i].x = fmaf(w, x.x, s[i].x);
-                    s[i].y = fmaf(w, x.y, s[i].y);
-                    s[i].z = fmaf(w, x.z, s[i].z);
-                    s[i].w = fmaf(w, x.w, s[i].w);
+            for (int i = 0; i < S::PL; ++i) {
+                if (S::V4 >= 32 || lane < S::V4) {
+                    const float4 x = __ldcg(po + lane + 32 * i);
+                    s.o[i].x = fmaf(f, x.x, s.o[i].x);
+                    s.o[i].y = fmaf(f, x.y, s.o[i].y);
+                    s.o[i].z = fmaf(f, x.z, s.o[i].z);
+                    s.o[i].w = fmaf(f, x.w, s.o[i].w);
                 }
             }
         }
-#pragma unroll
-        for (int i = 0; i < PL; ++i)
-            if (lane + 32 * i < V4) acc[warp][lane + 32 * i] = s[i];
-        __syncthreads();
-        L = 0.f;
-#pragma unroll
-        for (int i = 0; i < NW; ++i) L += red[1][i];
-        const float vs = a.v_scale != nullptr ? __ldg(a.v_scale + h / (a.heads / a.kv_heads)) : 1.f;
-        for (int d = tid; d < D; d += kMergeThreads) {
-            float O = 0.f;
-#pragma unroll
-            for (int i = 0; i < NW; ++i) O += reinterpret_cast<const float*>(acc[i])[d];
-            const float r = L == 0.f ? 0.f : O / L * vs;
-            if (out_bf16) static_cast<__nv_bfloat16*>(a.out)[qh * D + d] = __float2bfloat16_rn(r);
-            else static_cast<__half*>(a.out)[qh * D + d] = __float2half_rn(r);
-        }
-        if (tid == 0 && a.lse != nullptr)
-            a.lse[qh] = L == 0.f ? -CUDART_INF_F : (M + log2f(L)) * kLn2;
-        __syncthreads();
     }
+    return s;
+}
+
+// One warp writes a head's merged state.
+template <int D>
+__device__ __forceinline__ void write_head(const PagedArgs& a, int64_t qh, int kvh,
+                                           const MergeState<D>& s, int out_bf16) {
+    using S = MergeState<D>;
+    const int lane = threadIdx.x & 31;
+    float f = s.l == 0.f ? 0.f : 1.f / s.l;
+    if (a.v_scale != nullptr && s.l != 0.f) f *= __ldg(a.v_scale + kvh);
+#pragma unroll
+    for (int i = 0; i < S::PL; ++i) {
+        if (S::V4 < 32 && lane >= S::V4) break;
+        const float4 x = s.o[i];
+        const int64_t at = qh * D + 4 * (lane + 32 * i);
+        if (out_bf16) {
+            __nv_bfloat162 y[2] = {__floats2bfloat162_rn(x.x * f, x.y * f),
+                                   __floats2bfloat162_rn(x.z * f, x.w * f)};
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
+                *reinterpret_cast<const uint2*>(y);
+        } else {
+            __half2 y[2] = {__floats2half2_rn(x.x * f, x.y * f),
+                            __floats2half2_rn(x.z * f, x.w * f)};
+            *reinterpret_cast<uint2*>(static_cast<__half*>(a.out) + at) =
+                *reinterpret_cast<const uint2*>(y);
+        }
+    }
+    if (lane == 0 && a.lse != nullptr)
+        a.lse[qh] = s.l == 0.f ? -CUDART_INF_F : (s.m + log2f(s.l)) * kLn2;
+}
+
+// A block takes 8 / wp heads of a request, wp warps (1, 2, 4 or 8) to a head.
+template <int D>
+__device__ __forceinline__ void merge_heads(const PagedArgs& a, const RowPlan& plan, int row,
+                                            int part, int wp, int out_bf16) {
+    using S = MergeState<D>;
+    __shared__ float2 ml_s[kMergeWarps];
+    __shared__ float4 o_s[kMergeWarps][S::V4];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = part * (kMergeWarps / wp) + warp / wp;
+    Parts parts{};
+    if (h < a.heads) parts = parts_of(a, plan, h);
+    // A request without a token has no part: zeros.
+    const bool mine = h < a.heads && parts.n != 1;
+    hs::pdl_wait();
+    S s = merge_share<D>(a, parts.n > 1 ? parts : Parts{}, warp % wp, wp);
+    if (wp > 1 && parts.n > 1) {
+        if (lane == 0) ml_s[warp] = make_float2(s.m, s.l);
+#pragma unroll
+        for (int j = 0; j < S::PL; ++j)
+            if (S::V4 >= 32 || lane < S::V4) o_s[warp][lane + 32 * j] = s.o[j];
+    }
+    if (wp > 1) __syncthreads();
+    if (!mine || warp % wp != 0) return;
+    if (wp > 1 && parts.n > 1) {
+        float M = s.m;
+        for (int w = 1; w < wp; ++w) M = fmaxf(M, ml_s[warp + w].x);
+        const float ref = M == -CUDART_INF_F ? 0.f : M;
+        const float own = exp2f(s.m - ref);
+        s.l *= own;
+#pragma unroll
+        for (int j = 0; j < S::PL; ++j) {
+            s.o[j].x *= own;
+            s.o[j].y *= own;
+            s.o[j].z *= own;
+            s.o[j].w *= own;
+        }
+        for (int w = 1; w < wp; ++w) {
+            const float f = exp2f(ml_s[warp + w].x - ref);
+            s.l = fmaf(f, ml_s[warp + w].y, s.l);
+#pragma unroll
+            for (int j = 0; j < S::PL; ++j) {
+                if (S::V4 < 32 && lane >= S::V4) break;
+                const float4 x = o_s[warp + w][lane + 32 * j];
+                s.o[j].x = fmaf(f, x.x, s.o[j].x);
+                s.o[j].y = fmaf(f, x.y, s.o[j].y);
+                s.o[j].z = fmaf(f, x.z, s.o[j].z);
+                s.o[j].w = fmaf(f, x.w, s.o[j].w);
+            }
+        }
+        s.m = M;
+    }
+    write_head<D>(a, int64_t(row) * a.heads + h, h / (a.heads / a.kv_heads), s, out_bf16);
 }
 
 // score[r][t] := decay * score[r][t] + sum_h 2^(x[r][h][t] - LSE[r][h]), the
 // heads in order; tokens outside the window only decay.  A thread per token,
-// sixteen heads' logits in flight; the heads' LSE first, a warp per head over
-// its parts, so that this needs no merge to have finished.
+// sixteen heads' logits in flight; the heads' LSE first, eight lanes to a
+// head over its parts, so that this needs no merge to have finished.
 __device__ __forceinline__ void score_tokens(const PagedArgs& a, const RowPlan& plan, int row,
                                              int part, int blocks) {
     __shared__ float lse2[kHeadChunk];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int kLanes = 8, kAtOnce = kMergeThreads / kLanes;  // lanes of a head, heads at once
+    const int tid = threadIdx.x;
     const Tiling vis = tiling_of(a, a.seq_lens[row], 0);
     const int nvis = vis.T - vis.w0 + vis.sc;
     float* score = a.score + int64_t(row) * a.score_stride;
+    Parts ahead{};  // of this thread's first head
+    if (tid / kLanes < a.heads && plan.row_tiles > 0) ahead = parts_of(a, plan, tid / kLanes);
+    hs::pdl_wait();
     for (int64_t i0 = int64_t(part) * kMergeThreads; i0 < nvis;
          i0 += int64_t(blocks) * kMergeThreads) {
         const int i = int(i0) + tid;
@@ -246,31 +310,38 @@ __device__ __forceinline__ void score_tokens(const PagedArgs& a, const RowPlan& 
             const int nh = min(kHeadChunk, a.heads - hc);
             if (a.heads > kHeadChunk || i0 == int64_t(part) * kMergeThreads) {
                 __syncthreads();
-                for (int h = warp; h < nh; h += kMergeWarps) {
-                    const Parts parts = parts_of(a, plan, hc + h);
+                for (int h0 = 0; h0 < nh; h0 += kAtOnce) {
+                    const int h = h0 + tid / kLanes, l = tid % kLanes;
                     float M = -CUDART_INF_F, L = 0.f;
-                    if (parts.n == 1) {
-                        M = __ldcg(a.lse2 + int64_t(row) * a.heads + hc + h);
-                        L = lane == 0 ? 1.f : 0.f;
-                    } else {
-                        for (int p = lane; p < parts.n; p += 32) {
-                            const float2 ml =
-                                __ldcg(reinterpret_cast<const float2*>(a.part_ml) + parts.at(p));
-                            const float m = fmaxf(M, ml.x), ref = m == -CUDART_INF_F ? 0.f : m;
-                            L = fmaf(L, exp2f(M - ref), ml.y * exp2f(ml.x - ref));
-                            M = m;
+                    if (h < nh) {
+                        const Parts parts =
+                            h0 == 0 && hc == 0 ? ahead : parts_of(a, plan, hc + h);
+                        if (parts.n == 1) {
+                            M = __ldcg(a.lse2 + int64_t(row) * a.heads + hc + h);
+                            L = l == 0 ? 1.f : 0.f;
+                        } else {
+#pragma unroll 4
+                            for (int p = l; p < parts.n; p += kLanes) {
+                                const float2 ml = __ldcg(
+                                    reinterpret_cast<const float2*>(a.part_ml) + parts.at(p));
+                                const float m = fmaxf(M, ml.x);
+                                const float ref = m == -CUDART_INF_F ? 0.f : m;
+                                L = fmaf(L, exp2f(M - ref), ml.y * exp2f(ml.x - ref));
+                                M = m;
+                            }
                         }
-                        const float own = M;
-#pragma unroll
-                        for (int o = 16; o > 0; o >>= 1)
-                            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-                        L *= exp2f(own - (M == -CUDART_INF_F ? 0.f : M));
                     }
+                    const float own = M;
 #pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+                    for (int o = kLanes / 2; o > 0; o >>= 1)
+                        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+                    L *= exp2f(own - (M == -CUDART_INF_F ? 0.f : M));
+#pragma unroll
+                    for (int o = kLanes / 2; o > 0; o >>= 1)
+                        L += __shfl_xor_sync(0xffffffffu, L, o);
                     // A head without any weight adds nothing: subtract 0.
                     const float lg = L == 0.f ? -CUDART_INF_F : M + log2f(L);
-                    if (lane == 0) lse2[h] = lg == -CUDART_INF_F ? 0.f : lg;
+                    if (l == 0 && h < nh) lse2[h] = lg == -CUDART_INF_F ? 0.f : lg;
                 }
                 __syncthreads();
             }
@@ -294,18 +365,17 @@ __device__ __forceinline__ void score_tokens(const PagedArgs& a, const RowPlan& 
             score[t] = a.decay == 0.f ? 0.f : a.decay * score[t];
 }
 
-// What follows the attention: blocks (row, y < merges) join the parts of every
-// merges-th head of a request, the others score its tokens.  The plan depends
+// What follows the attention: block (row, y) with y < merges joins the parts
+// of some heads of a request, the others score its tokens.  The plan depends
 // on seq_lens alone, which no longer changes once the attention kernel lets
 // this one start, so it is found while that kernel still runs.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) finish_kernel(const __grid_constant__ PagedArgs a,
-                                                               int merges, int out_bf16) {
+                                                               int merges, int wp, int out_bf16) {
     hs::pdl_trigger();
     const RowPlan plan = row_plan(a, blockIdx.x);
-    hs::pdl_wait();
     if (int(blockIdx.y) < merges)
-        merge_heads<D>(a, plan, blockIdx.x, blockIdx.y, merges, out_bf16);
+        merge_heads<D>(a, plan, blockIdx.x, blockIdx.y, wp, out_bf16);
     else
         score_tokens(a, plan, blockIdx.x, blockIdx.y - merges, gridDim.y - merges);
 }
@@ -456,17 +526,23 @@ extern "C" int hs_paged_decode(const void* q, int64_t q_stride, int32_t q_dtype,
     else if (kv_dtype == HS_FP16) rc = launch_fp16(a, d, group, stream);
     else rc = launch_e4m3(a, d, group, stream);
     if (rc != HS_OK) return rc;
-    // Merging: a block per head where a few waves hold them, else several
-    // heads a block.  Scoring: a block per step of tokens, likewise.
-    const int64_t wave = 8 * int64_t(w.ctas);
-    const int merges = int(hs::max64(1, hs::min64(heads, wave / 2 / rows)));
+    // Merging: as many warps to a head as leave all blocks in one wave (one
+    // context over all SMs has 152 parts a head).  Scoring: a block per step of
+    // tokens where a few waves hold them, else several steps a block.
+    int wp = kMergeWarps;
+    while (wp > 1 && int64_t(rows) * heads * wp > 4 * int64_t(w.ctas) * kMergeWarps) wp /= 2;
+    const int merges = (heads * wp + kMergeWarps - 1) / kMergeWarps;
     const int64_t steps = (int64_t(max_len) + kMergeThreads - 1) / kMergeThreads;
     const int scores =
-        score == nullptr ? 0 : int(hs::max64(1, hs::min64(steps, 2 * wave / rows)));
+        score == nullptr ? 0
+                         : int(hs::max64(1, hs::min64(steps, 16 * int64_t(w.ctas) / rows)));
     const int bf = q_dtype == HS_BF16;
     const dim3 grid{unsigned(rows), unsigned(merges + scores)}, block{kMergeThreads};
-    if (d == 64) return hs_host::launch_pdl(finish_kernel<64>, grid, block, 0, stream, a, merges, bf);
+    if (d == 64) return hs_host::launch_pdl(finish_kernel<64>, grid, block, 0, stream, a, merges, wp,
+                                   bf);
     if (d == 128)
-        return hs_host::launch_pdl(finish_kernel<128>, grid, block, 0, stream, a, merges, bf);
-    return hs_host::launch_pdl(finish_kernel<256>, grid, block, 0, stream, a, merges, bf);
+        return hs_host::launch_pdl(finish_kernel<128>, grid, block, 0, stream, a, merges, wp,
+                                   bf);
+    return hs_host::launch_pdl(finish_kernel<256>, grid, block, 0, stream, a, merges, wp,
+                                   bf);
 }

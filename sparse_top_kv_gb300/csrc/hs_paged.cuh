@@ -74,7 +74,7 @@ __device__ __forceinline__ Tiling tiling_of(const PagedArgs& a, int len, int lth
     v.tw0 = v.w0 >> lth;
     const int up = (1 << lth) - 1;
     v.ns = min((v.sc + up) >> lth, v.tw0);
-    v.n = max(1, v.ns + ((v.T + up) >> lth) - v.tw0);
+    v.n = v.ns + ((v.T + up) >> lth) - v.tw0;  // 0: no token (the merge writes zeros)
     return v;
 }
 
@@ -98,8 +98,10 @@ __device__ __forceinline__ void advance(Cursor& c, const PagedArgs& a, int chunk
     c.first = true;
     if (++c.chunk < chunks) return;
     c.chunk = 0;
-    ++c.row;
-    cursor_row(c, a, lth);
+    do {  // the next request with a token; there is one, as left > 0
+        ++c.row;
+        cursor_row(c, a, lth);
+    } while (c.v.n == 0 && c.row + 1 < a.rows);
 }
 // On to the run's next segment (left = 0: there is none).
 __device__ __forceinline__ void next_segment(Cursor& c, const PagedArgs& a, int chunks, int lth) {
@@ -176,7 +178,7 @@ __device__ __forceinline__ Run make_run(const PagedArgs& a, int cta) {
     x.w0 = cta < pl.n ? run_begin(pl, cta) : 0;
     x.run = cta < pl.n ? run_begin(pl, cta + 1) - x.w0 : 0;
     // The row that the run begins in: the last whose first tile is at or
-    // before it (every row has a tile).
+    // before it (rows without tiles share theirs with the next row).
     x.row = 0;
     x.row_tile0 = 0;
     for (int r0 = 0, carry = 0; r0 < a.rows; r0 += 32) {
@@ -206,7 +208,7 @@ __device__ __forceinline__ Cursor cursor_at(const PagedArgs& a, const Run& x) {
     c.row = x.row;
     cursor_row(c, a, a.lth[x.way]);
     const uint32_t rel = uint32_t(x.w0) - uint32_t(x.row_tile0) * uint32_t(x.chunks);
-    c.chunk = int(rel / uint32_t(c.v.n));
+    c.chunk = int(rel / uint32_t(max(1, c.v.n)));
     c.tile = int(rel) - c.chunk * c.v.n;
     c.left = x.run;
     c.first = true;

@@ -493,7 +493,7 @@ paged_kernel(const __grid_constant__ PagedArgs a) {
             if (whole) {
                 const int64_t qh = int64_t(row) * a.heads + kv * group + gc * GM + hg;
                 float r = L == 0.f ? 0.f : O / L;
-                if (a.v_scale != nullptr) r *= __ldg(a.v_scale + kv);
+                if (a.v_scale != nullptr && L != 0.f) r *= __ldg(a.v_scale + kv);
                 const bool bf = KV == kBf16 || (KV == kE4m3 && !a.q_is_half);
                 if (bf) static_cast<__nv_bfloat16*>(a.out)[qh * D + d] = __float2bfloat16_rn(r);
                 else static_cast<__half*>(a.out)[qh * D + d] = __float2half_rn(r);

@@ -893,7 +893,7 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
                         if (a.lse != nullptr) a.lse[qh] = lg * kLn2;
                         if (a.lse2 != nullptr) a.lse2[qh] = lg;
                         inv = L == 0.f ? 0.f : 1.f / L;
-                        if (a.v_scale != nullptr) inv *= __ldg(a.v_scale + kvh0 + h);
+                        if (a.v_scale != nullptr && L != 0.f) inv *= __ldg(a.v_scale + kvh0 + h);
                     } else {
                         const int64_t k = int64_t(slot) * a.unit_heads_max + e;
                         a.part_ml[2 * k] = M;
