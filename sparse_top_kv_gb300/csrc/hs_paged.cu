@@ -80,38 +80,33 @@ struct RowPlan {
     Plan pl;
     int way, row_tiles, first_tile;
 };
-// Called by every thread of the block.
+// Found by every warp for itself (a lane per request, no barrier).
 __device__ __forceinline__ RowPlan row_plan(const PagedArgs& a, int row) {
-    __shared__ int sums[kMergeWarps][4];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int n[4] = {0, 0, 0, 0};  // tiles of all rows, and of those before this one, both ways
-    for (int r = tid; r < a.rows; r += kMergeThreads) {
+    constexpr uint32_t kAll = 0xffffffffu;
+    const int lane = threadIdx.x & 31;
+    int n0 = 0, n1 = 0, b0 = 0, b1 = 0, own0 = 0, own1 = 0;
+#pragma unroll 4
+    for (int r = lane; r < a.rows; r += 32) {
         const int len = a.seq_lens[r];
-        const int n0 = tiling_of(a, len, a.lth[0]).n, n1 = tiling_of(a, len, a.lth[1]).n;
-        n[0] += n0;
-        n[1] += n1;
+        const int t0 = tiling_of(a, len, a.lth[0]).n, t1 = tiling_of(a, len, a.lth[1]).n;
+        n0 += t0;
+        n1 += t1;
         if (r < row) {
-            n[2] += n0;
-            n[3] += n1;
+            b0 += t0;
+            b1 += t1;
+        }
+        if (r == row) {
+            own0 = t0;
+            own1 = t1;
         }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) n[i] = __reduce_add_sync(0xffffffffu, n[i]);
-    if (lane == 0)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sums[warp][i] = n[i];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        n[i] = 0;
-#pragma unroll
-        for (int w = 0; w < kMergeWarps; ++w) n[i] += sums[w][i];
-    }
+    n0 = __reduce_add_sync(kAll, n0);
     RowPlan p;
-    p.way = way_of(a, n[0]);
-    p.pl = plan_of(a, p.way, p.way == 0 ? n[0] : n[1]);
-    p.row_tiles = tiling_of(a, a.seq_lens[row], a.lth[p.way]).n;
-    p.first_tile = (p.way == 0 ? n[2] : n[3]) * a.chunks[p.way];
+    p.way = way_of(a, n0);
+    const bool narrow = p.way != 0;
+    p.pl = plan_of(a, p.way, narrow ? __reduce_add_sync(kAll, n1) : n0);
+    p.row_tiles = __shfl_sync(kAll, narrow ? own1 : own0, row & 31);
+    p.first_tile = __reduce_add_sync(kAll, narrow ? b1 : b0) * a.chunks[p.way];
     return p;
 }
 // The parts that a query head's unit was dealt to: part p (one per CTA) of the
@@ -123,10 +118,12 @@ struct Parts {
     __device__ __forceinline__ int64_t at(int p) const { return p == 0 ? first : rest + p * step; }
 };
 __device__ __forceinline__ Parts parts_of(const PagedArgs& a, const RowPlan& r, int h) {
-    const int group = a.heads / a.kv_heads, gch = (group + a.gm - 1) / a.gm;
-    const int hs = a.hs[r.way], kvh = h / group, gi = h % group;
-    const int hu = (kvh % hs) * a.gm + gi % a.gm;
-    const int start = r.first_tile + (kvh / hs * gch + gi / a.gm) * r.row_tiles;
+    // hs and gm are powers of two.
+    const int lhs = 31 - __clz(a.hs[r.way]), lgm = 31 - __clz(a.gm);
+    const int group = a.group, gch = (group + a.gm - 1) >> lgm;
+    const int kvh = div_small(h, group), gi = h - kvh * group;
+    const int hu = ((kvh & (a.hs[r.way] - 1)) << lgm) + (gi & (a.gm - 1));
+    const int start = r.first_tile + ((kvh >> lhs) * gch + (gi >> lgm)) * r.row_tiles;
     Parts p{};
     if (r.row_tiles == 0) return p;  // a request without tokens
     const int c0 = run_of(r.pl, start), c1 = run_of(r.pl, start + r.row_tiles - 1);
@@ -141,7 +138,8 @@ __device__ __forceinline__ Parts parts_of(const PagedArgs& a, const RowPlan& r, 
 // Merge of the units whose tiles were dealt to several CTAs (the others were
 // written by their CTA): out = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p.
 // A warp's share is the parts first, first + step, ..: a lane per part for the
-// maxima and sums, then the partial rows, eight in flight.
+// maxima and sums, then the partial rows, many in
+// flight.
 template <int D>
 struct MergeState {
     static constexpr int V4 = D / 4;                  // float4s of a row
@@ -184,7 +182,7 @@ __device__ __forceinline__ MergeState<D> merge_share(const PagedArgs& a, const P
             }
         }
         const int n = min(32, (parts.n - p0 + step - 1) / step);
-#pragma unroll 8
+#pragma unroll (S::PL == 1 ? 16 : 8)
         for (int k = 0; k < n; ++k) {
             const float f = __shfl_sync(0xffffffffu, w, k);
             const float4* po =
@@ -284,7 +282,7 @@ __device__ __forceinline__ void merge_heads(const PagedArgs& a, const RowPlan& p
         }
         s.m = M;
     }
-    write_head<D>(a, int64_t(row) * a.heads + h, h / (a.heads / a.kv_heads), s, out_bf16);
+    write_head<D>(a, int64_t(row) * a.heads + h, div_small(h, a.group), s, out_bf16);
 }
 
 // score[r][t] := decay * score[r][t] + sum_h 2^(x[r][h][t] - LSE[r][h]), the
@@ -497,6 +495,7 @@ extern "C" int hs_paged_decode(const void* q, int64_t q_stride, int32_t q_dtype,
     a.rows = rows;
     a.heads = heads;
     a.kv_heads = kv_heads;
+    a.group = group;
     a.num_pages = num_pages;
     a.page_size = page_size;
     a.max_len = max_len;
@@ -526,11 +525,20 @@ extern "C" int hs_paged_decode(const void* q, int64_t q_stride, int32_t q_dtype,
     else if (kv_dtype == HS_FP16) rc = launch_fp16(a, d, group, stream);
     else rc = launch_e4m3(a, d, group, stream);
     if (rc != HS_OK) return rc;
-    // Merging: as many warps to a head as leave all blocks in one wave (one
-    // context over all SMs has 152 parts a head).  Scoring: a block per step of
-    // tokens where a few waves hold them, else several steps a block.
-    int wp = kMergeWarps;
-    while (wp > 1 && int64_t(rows) * heads * wp > 4 * int64_t(w.ctas) * kMergeWarps) wp /= 2;
+    // Merging: about half as many warps to a head as its unit has parts (one
+    // context over all SMs has 152), within a few blocks an SM.  The kernel
+    // chose between the two ways by the lengths; here their bound decides.
+    // Scoring: a block per step of tokens where a few waves hold them, else
+    // several steps a block.
+    const int64_t vis = window > 0 ? hs::min64(max_len, int64_t(window) + num_sinks) : max_len;
+    const auto tiles = [&](int way) { return (vis >> a.lth[way]) + 3; };
+    const int way = rows * a.chunks[0] * tiles(0) < a.wide_tiles ? 1 : 0;
+    const int64_t parts =
+        hs::min64(tiles(way), w.ctas / hs::max64(1, int64_t(rows) * a.chunks[way]) + 2);
+    int wp = 1;
+    while (wp < kMergeWarps && 2 * wp <= parts &&
+           int64_t(rows) * heads * 2 * wp <= 4 * int64_t(w.ctas) * kMergeWarps)
+        wp *= 2;
     const int merges = (heads * wp + kMergeWarps - 1) / kMergeWarps;
     const int64_t steps = (int64_t(max_len) + kMergeThreads - 1) / kMergeThreads;
     const int scores =

@@ -29,7 +29,7 @@ struct PagedArgs {
     const int32_t* seq_lens;
     const float* k_scale;  // [kv_heads] or nullptr (E4M3)
     const float* v_scale;
-    int32_t rows, heads, kv_heads, num_pages, page_size, max_len, window, sinks;
+    int32_t rows, heads, kv_heads, group, num_pages, page_size, max_len, window, sinks;
     int32_t q_is_half;  // E4M3 caches: the query is fp16 (else bf16)
     float scale_log2;   // scale * log2(e)
     void* out;          // [rows, heads, D]
@@ -125,6 +125,16 @@ __device__ __forceinline__ bool any_visible(const Tiling& v, int t, int n) {
     return t < v.T && (t < v.sc || t + n > v.w0);
 }
 
+// floor(x / d) for 0 <= x < 2^23, by a float estimate and one correction (an
+// integer division is a routine of many instructions).
+__device__ __forceinline__ int div_small(int x, int d) {
+    int q = __float2int_rz(__fdividef(float(x), float(d)));
+    const int r = x - q * d;
+    if (r < 0) --q;
+    if (r >= d) ++q;
+    return q;
+}
+
 // The runs of tiles of a call.
 struct Plan {
     int tiles, n;   // tiles of the call, CTAs that share them
@@ -138,12 +148,12 @@ __device__ __forceinline__ Plan plan_of(const PagedArgs& a, int way, int total) 
     p.rest = p.tiles - p.per * p.n;
     return p;
 }
-// floor(tiles c / n)
+// floor(tiles c / n); rest, c <= n <= kMaxCtas
 __device__ __forceinline__ int run_begin(const Plan& p, int c) {
-    return p.per * c + p.rest * c / p.n;
+    return p.per * c + div_small(p.rest * c, p.n);
 }
 __device__ __forceinline__ int run_of(const Plan& p, int tile) {
-    int c = min(p.n - 1, tile / max(1, p.per));
+    int c = min(p.n - 1, __float2int_rz(float(tile) * __fdividef(float(p.n), float(p.tiles))));
     while (run_begin(p, c) > tile) --c;
     while (c + 1 < p.n && run_begin(p, c + 1) <= tile) ++c;
     return c;
