@@ -481,3 +481,120 @@ class MultiLayerHiSparse:
     # the two attention passes (index_copy_ is torch's).
     def launches_per_step(self):
         return 1 + 5 * len(self.layers)
+
+
+class BudgetedDecoder:
+    """Decoding with the whole cache on the device, kept to a budget: every
+    request attends to all tokens that it still holds (hs_paged_decode), whose
+    attention weights add up in running scores, and gives up the lowest-scored
+    ones past its budget (hs_evict).  One layer, `num_reqs` fixed places for
+    requests of K and V rows [kv_heads, d], page tables fixed at set-up.
+
+    A request's place i holds the token at position `positions[r, i]`; the rows
+    carry their position themselves (rotated keys), so moved rows stand in any
+    order.  Kept in any case: positions below `num_sinks` and the newest
+    `recent` ones.  `capacity` (default budget + 1) bounds the tokens between
+    two steps: a prompt longer than the budget needs as much."""
+
+    def __init__(self, *, num_reqs, heads, kv_heads, d, page_size, budget, scale, recent=0,
+                 num_sinks=0, capacity=None, score_decay=1.0, dtype=torch.bfloat16,
+                 device="cuda"):
+        capacity = budget + 1 if capacity is None else capacity
+        if capacity <= budget:
+            raise ValueError("capacity: more than the budget, for the new token")
+        self.device = torch.device(device)
+        dev = self.device
+        self.num_reqs, self.heads, self.kv_heads, self.d = num_reqs, heads, kv_heads, d
+        self.page_size, self.budget, self.scale = page_size, budget, scale
+        self.recent, self.num_sinks, self.score_decay = recent, num_sinks, score_decay
+        self.capacity = capacity
+        R = num_reqs
+        blocks = -(-capacity // page_size)
+        self.num_pages = R * blocks + 1  # the last page takes the rows of inactive places
+        shape = (self.num_pages, page_size, kv_heads, d)
+        self.k_cache = torch.zeros(shape, dtype=dtype, device=dev)
+        self.v_cache = torch.zeros(shape, dtype=dtype, device=dev)
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.block_table = torch.arange(R * blocks, **i32).view(R, blocks)
+        self.seq_lens = torch.zeros(R, **i32)
+        self.next_pos = torch.zeros(R, **i32)
+        self.positions = torch.zeros(R, capacity, **i32)
+        self.score = torch.zeros(R, capacity, dtype=torch.float32, device=dev)
+        cap = min(budget, capacity - budget)
+        self.moves = (torch.zeros(R, cap, **i32), torch.zeros(R, cap, **i32),
+                      torch.zeros(R, **i32))
+        self.status = torch.zeros(1, **i32)
+        self.row_req = torch.arange(R, **i32)
+        self.out = torch.empty(R, heads, d, dtype=dtype, device=dev)
+        self.lse = torch.empty(R, heads, dtype=torch.float32, device=dev)
+        self.workspace = torch.empty(hs.paged_decode_workspace_bytes(
+            R, heads, kv_heads, d, capacity, with_score=True), dtype=torch.uint8, device=dev)
+        self.graph = None
+
+    def start(self, r, k, v):
+        """Begin a request in place r with its prompt's rows k, v [tokens,
+        kv_heads, d] (at most capacity - 1 tokens, so that the first step's
+        token has room)."""
+        n = k.shape[0]
+        if not 0 < n < self.capacity:
+            raise ValueError(f"prompt: 1 to {self.capacity - 1} tokens")
+        t = torch.arange(n, device=self.device)
+        page = self.block_table[r].long()[t // self.page_size]
+        for cache, rows in ((self.k_cache, k), (self.v_cache, v)):
+            cache[page, t % self.page_size] = rows.to(cache)
+        self.positions[r, :n] = t.to(torch.int32)
+        self.score[r].zero_()
+        self.seq_lens[r] = n
+        self.next_pos[r] = n
+
+    def stop(self, r):
+        """Free place r."""
+        self.seq_lens[r] = 0
+        self.next_pos[r] = 0
+
+    def step(self, q, k_new, v_new):
+        """One token of every active request: q [R, heads, d], its K and V rows
+        k_new, v_new [R, kv_heads, d].  Evicts what is past the budget, appends
+        the rows, attends, and adds the weights to the scores.  Returns (out
+        [R, heads, d], lse fp32 [R, heads]); inactive places give 0 and -inf."""
+        hs.evict(self.score, self.seq_lens, self.budget, self.k_cache, self.v_cache,
+                 self.block_table, max_len=self.capacity, recent=self.recent,
+                 num_sinks=self.num_sinks, positions=self.positions, next_pos=self.next_pos,
+                 moves=self.moves, status=self.status)
+        # The model's KV write of the new token (stand-in), at place seq_lens.
+        active = (self.seq_lens > 0).to(torch.int32)
+        place = self.seq_lens.clone()
+        self.seq_lens += active
+        slot = hs.normalize_indices(place.view(-1, 1), self.row_req, self.seq_lens,
+                                    self.block_table, self.page_size,
+                                    num_pages=self.num_pages)[1].view(-1)
+        slot = torch.where(active > 0, slot, (self.num_pages - 1) * self.page_size).long()
+        self.k_cache.view(-1, self.kv_heads, self.d).index_copy_(0, slot, k_new)
+        self.v_cache.view(-1, self.kv_heads, self.d).index_copy_(0, slot, v_new)
+        self.positions.scatter_(1, place.long().view(-1, 1), self.next_pos.view(-1, 1))
+        self.next_pos += active
+        return hs.paged_decode(q, self.k_cache, self.v_cache, self.block_table, self.seq_lens,
+                               self.scale, max_len=self.capacity, score=self.score,
+                               score_decay=self.score_decay, out=self.out, lse=self.lse,
+                               workspace=self.workspace, status=self.status)
+
+    def capture(self):
+        """Capture one step over static inputs (self.graph_q, graph_k, graph_v)
+        as a CUDA graph, which `replay` fills and runs.  The state is left as
+        it is.  Run at least one eager step first."""
+        opt = dict(dtype=self.k_cache.dtype, device=self.device)
+        self.graph_q = torch.zeros(self.num_reqs, self.heads, self.d, **opt)
+        self.graph_k = torch.zeros(self.num_reqs, self.kv_heads, self.d, **opt)
+        self.graph_v = torch.zeros_like(self.graph_k)
+        self.graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(self.graph):
+            self.step(self.graph_q, self.graph_k, self.graph_v)
+        return self.graph
+
+    def replay(self, q, k_new, v_new):
+        """One step through the captured graph."""
+        self.graph_q.copy_(q, non_blocking=True)
+        self.graph_k.copy_(k_new, non_blocking=True)
+        self.graph_v.copy_(v_new, non_blocking=True)
+        self.graph.replay()
+        return self.out, self.lse
