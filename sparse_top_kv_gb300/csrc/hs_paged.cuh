@@ -30,6 +30,7 @@ struct PagedArgs {
     const float* k_scale;  // [kv_heads] or nullptr (E4M3)
     const float* v_scale;
     int32_t rows, heads, kv_heads, group, num_pages, page_size, max_len, window, sinks;
+    int32_t page_shift;   // log2 of page_size, or -1
     int32_t q_is_half;  // E4M3 caches: the query is fp16 (else bf16)
     float scale_log2;   // scale * log2(e)
     void* out;          // [rows, heads, D]
@@ -115,6 +116,10 @@ __device__ __forceinline__ int tile_token(const Cursor& c, int lth) {
 }
 __device__ __forceinline__ bool visible(const Tiling& v, int t) {
     return t < v.T && (t < v.sc || t >= v.w0);
+}
+// Block of the page table that holds token t.
+__device__ __forceinline__ int block_of(const PagedArgs& a, int t) {
+    return a.page_shift >= 0 ? t >> a.page_shift : t / a.page_size;
 }
 // Place of an attended token among them.
 __device__ __forceinline__ int visible_index(const Tiling& v, int t) {

@@ -270,16 +270,16 @@ paged_kernel(const __grid_constant__ PagedArgs a) {
             return j < steps && visible(vis, tok) ? tok : -1;
         };
         int tok_n = token(0);
-        int page_n = tok_n >= 0 ? __ldg(table + tok_n / a.page_size) : -1;
+        int page_n = tok_n >= 0 ? __ldg(table + block_of(a, tok_n)) : -1;
         auto issue = [&](int j) {
             const int tok = tok_n;
             int page = page_n;
             tok_n = token(j + 1);
-            page_n = tok_n >= 0 ? __ldg(table + tok_n / a.page_size) : -1;
+            page_n = tok_n >= 0 ? __ldg(table + block_of(a, tok_n)) : -1;
             if (page >= a.num_pages || (tok >= 0 && page < 0)) bad = true;
             const bool ok = tok >= 0 && page >= 0 && page < a.num_pages;
             const int64_t off =
-                ok ? (int64_t(page) * a.page_stride + int64_t(tok % a.page_size) * a.row_stride) *
+                ok ? (int64_t(page) * a.page_stride + int64_t(tok - block_of(a, tok) * a.page_size) * a.row_stride) *
                          C::kElt
                    : -1;
             const uint32_t mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;

@@ -328,6 +328,10 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
         B.abort = 0;
         hs::fence_mbar_init();
     }
+    if (warp == kTmaWarp && lane < 4) {
+        const CUtensorMap* m = lane == 0 ? &kmap0 : lane == 1 ? &vmap0 : lane == 2 ? &kmap1 : &vmap1;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+    }
     if (warp == kPvWarp) {
         hs::tc::tmem_alloc(&B.tmem_base, kTmemCols);
         hs::tc::tmem_relinquish();
@@ -377,7 +381,7 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
             tok = lane < nops ? tile_token(x, lth) + lane * bt : 0;
             const bool want = lane < nops && any_visible(x.v, tok, bt);
             if (!want) return -2;
-            return __ldg(a.block_table + int64_t(x.row) * a.bt_stride + tok / a.page_size);
+            return __ldg(a.block_table + int64_t(x.row) * a.bt_stride + block_of(a, tok));
         };
         int tok_n, page_n = lookup(c, tok_n);
         for (; ok;) {
@@ -391,7 +395,7 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
             const uint32_t loaded = __ballot_sync(0xffffffffu, want);
             const int boxes = __popc(loaded);
             const uint32_t bytes = uint32_t(boxes) * uint32_t(hsn * bt) * 128u * C::kSubBlocks;
-            const int at = tok % a.page_size;
+            const int at = tok - block_of(a, tok) * a.page_size;
             // Read by the softmax of this tile (its logits follow these
             // loads), at most NS + 3 tiles behind.
             if (lane == 0) B.loaded[t % kMaskRing] = loaded;
