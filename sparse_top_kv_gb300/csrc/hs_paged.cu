@@ -78,7 +78,7 @@ constexpr int kHeadChunk = 256;  // heads whose LSE a scoring block holds at a t
 // Where the units of one request lie in the call's runs of tiles.
 struct RowPlan {
     Plan pl;
-    int way, row_tiles, first_tile;
+    int way, row_tiles, first_place;
 };
 // Found by every warp for itself (a lane per request, no barrier).
 __device__ __forceinline__ RowPlan row_plan(const PagedArgs& a, int row) {
@@ -89,11 +89,11 @@ __device__ __forceinline__ RowPlan row_plan(const PagedArgs& a, int row) {
     for (int r = lane; r < a.rows; r += 32) {
         const int len = a.seq_lens[r];
         const int t0 = tiling_of(a, len, a.lth[0]).n, t1 = tiling_of(a, len, a.lth[1]).n;
-        n0 += t0;
-        n1 += t1;
+        n0 += places(a, t0);
+        n1 += places(a, t1);
         if (r < row) {
-            b0 += t0;
-            b1 += t1;
+            b0 += places(a, t0);
+            b1 += places(a, t1);
         }
         if (r == row) {
             own0 = t0;
@@ -106,7 +106,7 @@ __device__ __forceinline__ RowPlan row_plan(const PagedArgs& a, int row) {
     const bool narrow = p.way != 0;
     p.pl = plan_of(a, p.way, narrow ? __reduce_add_sync(kAll, n1) : n0);
     p.row_tiles = __shfl_sync(kAll, narrow ? own1 : own0, row & 31);
-    p.first_tile = __reduce_add_sync(kAll, narrow ? b1 : b0) * a.chunks[p.way];
+    p.first_place = __reduce_add_sync(kAll, narrow ? b1 : b0) * a.chunks[p.way];
     return p;
 }
 // The parts that a query head's unit was dealt to: part p (one per CTA) of the
@@ -123,10 +123,12 @@ __device__ __forceinline__ Parts parts_of(const PagedArgs& a, const RowPlan& r, 
     const int group = a.group, gch = (group + a.gm - 1) >> lgm;
     const int kvh = div_small(h, group), gi = h - kvh * group;
     const int hu = ((kvh & (a.hs[r.way] - 1)) << lgm) + (gi & (a.gm - 1));
-    const int start = r.first_tile + ((kvh >> lhs) * gch + (gi >> lgm)) * r.row_tiles;
+    const int start =
+        r.first_place + ((kvh >> lhs) * gch + (gi >> lgm)) * places(a, r.row_tiles);
     Parts p{};
     if (r.row_tiles == 0) return p;  // a request without tokens
-    const int c0 = run_of(r.pl, start), c1 = run_of(r.pl, start + r.row_tiles - 1);
+    const int c0 = run_of(r.pl, start + a.extra);
+    const int c1 = run_of(r.pl, start + a.extra + r.row_tiles - 1);
     p.n = c1 - c0 + 1;
     p.step = 2 * int64_t(a.unit_heads_max);
     p.rest = c0 * p.step + hu;
@@ -430,7 +432,7 @@ Layout layout(int32_t rows, int32_t heads, int32_t kv_heads, int32_t d, int32_t 
 // Tiles (of 16 tokens of a KV head at least) are counted in 31 bits.
 bool too_large(int32_t rows, int32_t heads, int32_t max_len) {
     return rows > kMaxRows ||
-           int64_t(rows) * heads * (int64_t(max_len) / 16 + 2) >= (int64_t(1) << 31);
+           int64_t(rows) * heads * (int64_t(max_len) / 16 + 16) >= (int64_t(1) << 31);
 }
 
 bool bad_shape(int32_t rows, int32_t heads, int32_t kv_heads, int32_t d, int32_t max_len,
@@ -548,7 +550,7 @@ extern "C" int hs_paged_decode(const void* q, int64_t q_stride, int32_t q_dtype,
     // Scoring: a block per step of tokens where a few waves hold them, else
     // several steps a block.
     const int64_t vis = window > 0 ? hs::min64(max_len, int64_t(window) + num_sinks) : max_len;
-    const auto tiles = [&](int way) { return (vis >> a.lth[way]) + 3; };
+    const auto tiles = [&](int way) { return (vis >> a.lth[way]) + 3 + a.extra; };
     const int way = rows * a.chunks[0] * tiles(0) < a.wide_tiles ? 1 : 0;
     const int64_t parts =
         hs::min64(tiles(way), w.ctas / hs::max64(1, int64_t(rows) * a.chunks[way]) + 2);

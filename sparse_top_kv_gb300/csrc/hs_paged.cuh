@@ -39,7 +39,7 @@ struct PagedArgs {
     int64_t score_stride;
     float decay;
     // The two ways to cut the call (below).
-    int32_t hs[2], lth[2], chunks[2], gm;
+    int32_t hs[2], lth[2], chunks[2], gm, extra;
     int64_t wide_tiles;  // tiles (way 0) from which way 0 is taken
     // Workspace.
     float* lse2;        // [rows, heads] log2 units (scored calls)
@@ -56,7 +56,10 @@ struct PagedArgs {
 // heads (hs KV heads, up to gm query heads of each); its tokens are cut into
 // tiles of 2^lth.  The units' tiles, one after another, are dealt to the CTAs
 // in equal contiguous runs, so ragged batches load every SM alike and one
-// long context uses all of them.  There are two ways: units of as many heads
+// long context uses all of them.  Starting and ending a unit takes as long as
+// a few tiles; each unit has that many places without work (`extra`) ahead of
+// its tiles, so that a run of many short units holds fewer tiles (64 ragged
+// E4M3 requests: the slowest CTA 85 us, 95 without).  There are two ways: units of as many heads
 // as a tile holds (way 0: long DRAM pieces), or of one (way 1: small calls,
 // fewer parts to merge); the kernels take one by the tiles that they find.
 
@@ -140,11 +143,13 @@ __device__ __forceinline__ int div_small(int x, int d) {
     return q;
 }
 
-// The runs of tiles of a call.
+// The runs of a call: places (tiles and extras) dealt to CTAs.
 struct Plan {
-    int tiles, n;   // tiles of the call, CTAs that share them
+    int tiles, n;   // places of the call, CTAs that share them
     int per, rest;  // tiles / n, tiles % n
 };
+// Places of one chunk of heads of a request with n tiles.
+__device__ __forceinline__ int places(const PagedArgs& a, int n) { return n > 0 ? n + a.extra : 0; }
 __device__ __forceinline__ Plan plan_of(const PagedArgs& a, int way, int total) {
     Plan p;
     p.tiles = total * a.chunks[way];
@@ -167,50 +172,70 @@ __device__ __forceinline__ int way_of(const PagedArgs& a, int total0) {
     return int64_t(total0) * a.chunks[0] >= a.wide_tiles ? 0 : 1;
 }
 
-// One CTA's run: its tiles and where they begin.
+// One CTA's run: `run` tiles from `tile` of chunk `chunk` of request `row` on.
 struct Run {
-    int way, chunks, w0, run, row, row_tile0;
+    int way, chunks, run, row, chunk, tile;
 };
 // Every warp finds it for itself: a lane per request, a few dozen shuffles and
 // no barrier, so each role starts as soon as the lengths have arrived.
 __device__ __forceinline__ Run make_run(const PagedArgs& a, int cta) {
     constexpr uint32_t kAll = 0xffffffffu;
     const int lane = threadIdx.x & 31;
-    int n0 = 0, n1 = 0;
+    int t0 = 0, t1 = 0, n0 = 0, n1 = 0;  // tiles of one request; places of this lane's
 #pragma unroll 4
     for (int r = lane; r < a.rows; r += 32) {
         const int len = __ldg(a.seq_lens + r);
-        n0 += tiling_of(a, len, a.lth[0]).n;
-        n1 += tiling_of(a, len, a.lth[1]).n;
+        t0 = tiling_of(a, len, a.lth[0]).n;
+        t1 = tiling_of(a, len, a.lth[1]).n;
+        n0 += places(a, t0);
+        n1 += places(a, t1);
     }
-    const int mine0 = n0, mine1 = n1;
     n0 = __reduce_add_sync(kAll, n0);
-    n1 = __reduce_add_sync(kAll, n1);
     Run x;
     x.way = way_of(a, n0);
+    const bool narrow = x.way != 0;
     x.chunks = a.chunks[x.way];
-    const Plan pl = plan_of(a, x.way, x.way == 0 ? n0 : n1);
-    x.w0 = cta < pl.n ? run_begin(pl, cta) : 0;
-    x.run = cta < pl.n ? run_begin(pl, cta + 1) - x.w0 : 0;
-    // The row that the run begins in: the last whose first tile is at or
-    // before it (rows without tiles share theirs with the next row).
-    x.row = 0;
-    x.row_tile0 = 0;
-    for (int r0 = 0, carry = 0; r0 < a.rows; r0 += 32) {
+    const Plan pl = plan_of(a, x.way, narrow ? __reduce_add_sync(kAll, n1) : n0);
+    const int v0 = cta < pl.n ? run_begin(pl, cta) : pl.tiles;
+    const int v1 = cta < pl.n ? run_begin(pl, cta + 1) : pl.tiles;
+    // The requests that places v0 and v1 lie in (the last whose first place is
+    // at or before them; requests without tiles share theirs with the next),
+    // and how many tiles come before each place.
+    x.row = x.chunk = x.tile = 0;
+    int before0 = 0, before1 = 0;
+    for (int r0 = 0, tiles = 0, place = 0; r0 < a.rows; r0 += 32) {
         const int r = r0 + lane;
-        int n = 0;
-        if (a.rows <= 32) n = x.way == 0 ? mine0 : mine1;
-        else if (r < a.rows) n = tiling_of(a, __ldg(a.seq_lens + r), a.lth[x.way]).n;
-        const int incl = carry + hs::warp_incl_scan(n);
-        const uint32_t before =
-            __ballot_sync(kAll, r < a.rows && int64_t(incl - n) * x.chunks <= x.w0);
-        if (before == 0) break;
-        const int last = 31 - __clz(before);
-        x.row = r0 + last;
-        x.row_tile0 = __shfl_sync(kAll, incl - n, last);
-        if (last < 31) break;
-        carry = __shfl_sync(kAll, incl, 31);
+        int n = narrow ? t1 : t0;
+        if (a.rows > 32)
+            n = r < a.rows ? tiling_of(a, __ldg(a.seq_lens + r), a.lth[x.way]).n : 0;
+        else if (r >= a.rows)
+            n = 0;
+        const int np = places(a, n);
+        const int at = place + hs::warp_incl_scan(np) - np;      // places before request r
+        const int tl = tiles + hs::warp_incl_scan(n) - n;        // tiles before it
+        const bool in = r < a.rows;
+        const uint32_t m0 = __ballot_sync(kAll, in && at * x.chunks <= v0);
+        const uint32_t m1 = __ballot_sync(kAll, in && at * x.chunks <= v1);
+        auto find = [&](uint32_t m, int v, int& chunk, int& tile) {
+            const int last = 31 - __clz(m);
+            const int f_at = __shfl_sync(kAll, at, last), f_tl = __shfl_sync(kAll, tl, last);
+            const int f_n = __shfl_sync(kAll, n, last), f_p = __shfl_sync(kAll, np, last);
+            const uint32_t rel = uint32_t(v - f_at * x.chunks);
+            chunk = f_p > 0 ? min(int(rel / uint32_t(f_p)), x.chunks) : 0;
+            tile = chunk < x.chunks ? max(0, int(rel) - chunk * f_p - a.extra) : 0;
+            return f_tl * x.chunks + chunk * f_n + tile;
+        };
+        int c1, i1;
+        if (m0 != 0) {
+            before0 = find(m0, v0, x.chunk, x.tile);
+            x.row = r0 + 31 - __clz(m0);
+        }
+        if (m1 != 0) before1 = find(m1, v1, c1, i1);
+        tiles = __shfl_sync(kAll, tl + n, 31);
+        place = __shfl_sync(kAll, at + np, 31);
+        if (place * x.chunks > v1) break;
     }
+    x.run = before1 - before0;
     return x;
 }
 // A length past max_len is reported once.
@@ -222,9 +247,8 @@ __device__ __forceinline__ Cursor cursor_at(const PagedArgs& a, const Run& x) {
     Cursor c;
     c.row = x.row;
     cursor_row(c, a, a.lth[x.way]);
-    const uint32_t rel = uint32_t(x.w0) - uint32_t(x.row_tile0) * uint32_t(x.chunks);
-    c.chunk = int(rel / uint32_t(max(1, c.v.n)));
-    c.tile = int(rel) - c.chunk * c.v.n;
+    c.chunk = x.chunk;
+    c.tile = x.tile;
     c.left = x.run;
     c.first = true;
     return c;
@@ -232,7 +256,8 @@ __device__ __forceinline__ Cursor cursor_at(const PagedArgs& a, const Run& x) {
 
 // Host: the two ways of a kernel whose tiles have tile_rows cache rows and at
 // most hs_max heads.
-inline void set_ways(PagedArgs& a, int hs_max, int tile_rows, int gm, int tiles_for_wide) {
+inline void set_ways(PagedArgs& a, int hs_max, int tile_rows, int gm, int tiles_for_wide,
+                     int extra) {
     const int gch = (a.heads / a.kv_heads + gm - 1) / gm;
     int hs = 1;
     while (hs < hs_max && a.kv_heads % (2 * hs) == 0) hs *= 2;
@@ -243,6 +268,7 @@ inline void set_ways(PagedArgs& a, int hs_max, int tile_rows, int gm, int tiles_
         a.chunks[way] = a.kv_heads / a.hs[way] * gch;
     }
     a.gm = gm;
+    a.extra = extra;
     a.wide_tiles = int64_t(a.ctas) * tiles_for_wide;
 }
 

@@ -521,7 +521,7 @@ template <int KV, int D, int GH>
 int launch_one(PagedArgs& a, hs_stream_t stream) {
     using C = Cfg<KV, D, GH>;
     auto kern = paged_kernel<KV, D, GH>;
-    set_ways(a, C::kWarps, C::kWarps * kKey, C::GM, kTilesForWide);
+    set_ways(a, C::kWarps, C::kWarps * kKey, C::GM, kTilesForWide, 1);
     constexpr size_t smem = C::kBody + C::kWarps * C::kStages * 4;
     static int smem_set[64] = {};
     const int rc =

@@ -102,6 +102,8 @@ struct Cfg {
     static constexpr int kQBytes = q_rows(kHsMax) * D * kElt;
     static constexpr int kFit = units(kHsMax);
     static constexpr int NS = kFit > 8 ? 8 : kFit;       // units of each ring
+    // A unit's start and end in tiles: 2.6 us at an SM's share of the bandwidth.
+    static constexpr int kExtra = 2 * kSubs * kSub > 98304 ? 1 : 131072 / (2 * kSubs * kSub);
     static constexpr int kKOff = 0;
     static constexpr int kVOff = kKOff + NS * kSub;
     static constexpr int kQOff = kVOff + NS * kSub;
@@ -971,7 +973,7 @@ int launch_one(PagedArgs& a, hs_stream_t stream) {
     using C = Cfg<KV, D, GH, QP>;
     constexpr int GM = C::GM;
     TcArgs t{};
-    set_ways(a, C::kHsMax, kRows, GM, kTilesForWide);
+    set_ways(a, C::kHsMax, kRows, GM, kTilesForWide, C::kExtra);
     t.p = a;
     for (int i = 0; i < 2; ++i) {
         t.bt[i] = kRows / a.hs[i];

@@ -325,3 +325,33 @@ def test_refusals(change, error):
         kw["k_scale"] = torch.ones(2, device="cuda")
     with pytest.raises(error):
         hs.paged_decode(q, k, v, table, lens, 1.0, **kw)
+
+
+@pytest.mark.parametrize("rows,most,page", [(33, 900, 16), (70, 5000, 16), (400, 150, 16),
+                                            (1100, 40, 16), (70, 700, 12)])
+def test_many_requests(rows, most, page):
+    """More requests than a warp has lanes, empty ones among them, first and
+    last, and runs of CTAs that span several."""
+    g = torch.Generator().manual_seed(rows)
+    lens = torch.randint(0, most, (rows,), generator=g)
+    lens[torch.rand(rows, generator=g) < 0.3] = 0
+    lens[0] = lens[-1] = lens[-2] = 0
+    lens[rows // 2] = most
+    s = make(lens.tolist(), 8, 4, 64, page, seed=rows, poison=True)
+    score = torch.zeros(rows, s["table"].shape[1] * page, device="cuda")
+    *_, status = run_and_check(s, score=score)
+    assert status == 0
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(288, 32), (600, 8), (257, 257)])
+def test_many_heads(heads, kv_heads):
+    s = make([300, 1, 0, 77], heads, kv_heads, 64, 16, seed=heads)
+    score = torch.rand(4, s["table"].shape[1] * 16, device="cuda")
+    run_and_check(s, score=score, decay=0.5)
+
+
+def test_nothing_cached():
+    s = make([0, 0, -5], 8, 2, 128, 16)
+    score = torch.full((3, 16), 4.0, device="cuda")
+    out, lse, status = run_and_check(s, score=score)
+    assert status == 0 and not out.any() and (lse == -math.inf).all() and (score == 4.0).all()
