@@ -551,7 +551,8 @@ extern "C" int hs_paged_decode(const void* q, int64_t q_stride, int32_t q_dtype,
     // several steps a block.
     const int64_t vis = window > 0 ? hs::min64(max_len, int64_t(window) + num_sinks) : max_len;
     const auto tiles = [&](int way) { return (vis >> a.lth[way]) + 3 + a.extra; };
-    const int way = rows * a.chunks[0] * tiles(0) < a.wide_tiles ? 1 : 0;
+    const int64_t most = rows * a.chunks[0] * tiles(0);
+    const int way = most < a.wide_from || most >= a.wide_to ? 1 : 0;
     const int64_t parts =
         hs::min64(tiles(way), w.ctas / hs::max64(1, int64_t(rows) * a.chunks[way]) + 2);
     int wp = 1;

@@ -40,7 +40,7 @@ struct PagedArgs {
     float decay;
     // The two ways to cut the call (below).
     int32_t hs[2], lth[2], chunks[2], gm, extra;
-    int64_t wide_tiles;  // tiles (way 0) from which way 0 is taken
+    int64_t wide_from, wide_to;  // places (way 0) between which way 0 is taken
     // Workspace.
     float* lse2;        // [rows, heads] log2 units (scored calls)
     float* part_ml;     // [2 * ctas][unit heads][2]
@@ -169,7 +169,8 @@ __device__ __forceinline__ int run_of(const Plan& p, int tile) {
     return c;
 }
 __device__ __forceinline__ int way_of(const PagedArgs& a, int total0) {
-    return int64_t(total0) * a.chunks[0] >= a.wide_tiles ? 0 : 1;
+    const int64_t n = int64_t(total0) * a.chunks[0];
+    return n >= a.wide_from && n < a.wide_to ? 0 : 1;
 }
 
 // One CTA's run: `run` tiles from `tile` of chunk `chunk` of request `row` on.
@@ -269,7 +270,8 @@ inline void set_ways(PagedArgs& a, int hs_max, int tile_rows, int gm, int tiles_
     }
     a.gm = gm;
     a.extra = extra;
-    a.wide_tiles = int64_t(a.ctas) * tiles_for_wide;
+    a.wide_from = int64_t(a.ctas) * tiles_for_wide;
+    a.wide_to = INT64_MAX;
 }
 
 int launch_bf16(PagedArgs& a, int d, int group, hs_stream_t stream);

@@ -12,8 +12,9 @@
 // keep TMA loads in flight without a pause.
 //  * A tile is 128 cache rows: hs KV heads x 128 / hs tokens, so that one TMA
 //    box takes all heads of a run of tokens and DRAM is read in long pieces
-//    (reading one head's 256 bytes of a token at a time measured half the
-//    rate).  Rows of a tile: [run of bt tokens][head][token of the run].
+//    (one head's row at a time: 351 instead of 336 us over a bf16 batch of up
+//    to 64 K tokens, 122 instead of 88 over E4M3 rows of 128 bytes).  Rows of
+//    a tile: [run of bt tokens][head][token of the run].
 //  * One elected lane per run issues the boxes into a K ring and a V ring in
 //    128-byte-swizzled blocks; the loads run ahead over the ends of units.
 //  * S^T[128 rows x queries] = K Q^T takes the queries of all hs heads as N;
@@ -22,9 +23,12 @@
 //  * Softmax: one thread per row, against a reference maximum that moves only
 //    when a logit exceeds it by 2^8 (a vote), so the common tile needs no
 //    reduction; exponent sums stay per thread until the unit ends.  A tile's
-//    softmax is one chain of dependent steps (1.9 us, longer than its loads),
-//    so two groups of four warps take the tiles in turn, each with its own
-//    maximum, sums and output accumulators, joined when the unit ends.
+//    softmax is one chain of dependent steps (0.6 us, E4M3 0.75 us, as long as
+//    the tile's loads), so two groups of four warps take the tiles in turn,
+//    each with its own maximum, sums and output accumulators, joined when the
+//    unit ends.
+//  * QK and PV are issued by a warp each: one thread issuing both was the
+//    bound at first (16 products a tile at 80 to 100 cycles each).
 //  * O^T[D x queries] += V^T P^T, V as an MN-major view of its tile, K = the
 //    16 (E4M3: 32) rows of one head, one accumulator per head.  P is carried
 //    as several parts in columns of their own: a bf16 or fp16 value and the
@@ -60,7 +64,18 @@ constexpr int kMaskRing = 16;        // tiles whose loaded runs are remembered
 constexpr float kThresh = 8.f;       // log2 headroom before O is rescaled
 constexpr int kTmemCols = 512;
 constexpr int kBarBytes = 8192;      // shared-memory budget of Bars
-constexpr int kTilesForWide = 4;     // tiles per CTA from which units take several heads
+// Places per CTA from which units take several heads.  32/8 heads of 128, bf16,
+// us with all heads / one head to a unit: one request of 1 K tokens 10.8 / 10.8,
+// 4 K 14.2 / 12.8, 16 K 18.1 / 20.0, eight of 1 K 14.6 / 16.8, of 2 K 17.1 /
+// 21.7, 32 of 512 17.9 / 23.3.
+constexpr int kTilesForWide = 2;
+// A long 16-bit context or two alone on the GPU is cut by single heads again:
+// the 256-byte pieces of a head cost little there, and a head's merge joins a
+// few parts instead of 152 (us, all heads / one: 24 K tokens 25.8 / 26.5, 32 K
+// 34.6 / 31.1, 128 K 93.1 / 90.2, two of 32 K 52.5 / 51.4, four 90.7 / 91.3).
+// E4M3 heads are 128-byte pieces: never (64 requests of up to 8 K 88 / 122).
+constexpr int kWideAlone = 2;        // requests x chunks of heads
+constexpr int kTilesAlone = 12;      // places per CTA
 
 struct TcArgs {
     PagedArgs p;
@@ -974,6 +989,8 @@ int launch_one(PagedArgs& a, hs_stream_t stream) {
     constexpr int GM = C::GM;
     TcArgs t{};
     set_ways(a, C::kHsMax, kRows, GM, kTilesForWide, C::kExtra);
+    if (C::kElt == 2 && a.rows * a.chunks[0] <= kWideAlone)
+        a.wide_to = int64_t(a.ctas) * kTilesAlone;
     t.p = a;
     for (int i = 0; i < 2; ++i) {
         t.bt[i] = kRows / a.hs[i];
