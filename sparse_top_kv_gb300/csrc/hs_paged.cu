@@ -549,12 +549,11 @@ extern "C" int hs_paged_decode(const void* q, int64_t q_stride, int32_t q_dtype,
     // chose between the two ways by the lengths; here their bound decides.
     // Scoring: a block per step of tokens where a few waves hold them, else
     // several steps a block.
-    const int64_t vis = window > 0 ? hs::min64(max_len, int64_t(window) + num_sinks) : max_len;
-    const auto tiles = [&](int way) { return (vis >> a.lth[way]) + 3 + a.extra; };
-    const int64_t most = rows * a.chunks[0] * tiles(0);
+    const int64_t most = most_places(a);
     const int way = most < a.wide_from || most >= a.wide_to ? 1 : 0;
-    const int64_t parts =
-        hs::min64(tiles(way), w.ctas / hs::max64(1, int64_t(rows) * a.chunks[way]) + 2);
+    const int64_t units = int64_t(rows) * a.chunks[way];
+    const int64_t parts = hs::min64(most_places(a, way) / hs::max64(1, units),
+                                    w.ctas / hs::max64(1, units) + 2);
     int wp = 1;
     while (wp < kMergeWarps && 2 * wp <= parts &&
            int64_t(rows) * heads * 2 * wp <= 4 * int64_t(w.ctas) * kMergeWarps)

@@ -274,6 +274,12 @@ inline void set_ways(PagedArgs& a, int hs_max, int tile_rows, int gm, int tiles_
     a.wide_to = INT64_MAX;
 }
 
+// Host: at most this many places in way `way`, by the bound on the lengths.
+inline int64_t most_places(const PagedArgs& a, int way = 0) {
+    const int64_t vis = a.window > 0 ? hs::min64(a.max_len, int64_t(a.window) + a.sinks) : a.max_len;
+    return int64_t(a.rows) * a.chunks[way] * ((vis >> a.lth[way]) + 3 + a.extra);
+}
+
 int launch_bf16(PagedArgs& a, int d, int group, hs_stream_t stream);
 int launch_fp16(PagedArgs& a, int d, int group, hs_stream_t stream);
 int launch_e4m3(PagedArgs& a, int d, int group, hs_stream_t stream);

@@ -991,18 +991,28 @@ int launch_one(PagedArgs& a, hs_stream_t stream) {
     set_ways(a, C::kHsMax, kRows, GM, kTilesForWide, C::kExtra);
     if (C::kElt == 2 && a.rows * a.chunks[0] <= kWideAlone)
         a.wide_to = int64_t(a.ctas) * kTilesAlone;
-    t.p = a;
     for (int i = 0; i < 2; ++i) {
         t.bt[i] = kRows / a.hs[i];
         while (a.page_size % t.bt[i]) t.bt[i] /= 2;
     }
     t.timeout_ns = hs::kWaitTimeoutNs;
+    // Small calls surely take way 1: two descriptors instead of four.
+    const bool both = a.hs[0] != 1 && most_places(a) >= a.wide_from;
     CUtensorMap m[4];
-    for (int i = 0; i < 2; ++i) {
+    for (int i = both ? 0 : 1; i < 2; ++i) {
         int rc = encode_map(&m[2 * i], KV, a.k, a, D, t.bt[i], a.hs[i]);
         if (rc == HS_OK) rc = encode_map(&m[2 * i + 1], KV, a.v, a, D, t.bt[i], a.hs[i]);
         if (rc != HS_OK) return rc;
     }
+    if (!both) {
+        m[0] = m[2];
+        m[1] = m[3];
+        t.bt[0] = t.bt[1];
+        a.hs[0] = a.hs[1];
+        a.lth[0] = a.lth[1];
+        a.chunks[0] = a.chunks[1];
+    }
+    t.p = a;
     auto kern = paged_tc_kernel<KV, D, GH, QP>;
     constexpr size_t smem = size_t(C::kBarOff) + sizeof(Bars) + 1024;
     static_assert(smem <= 227 * 1024, "shared memory");

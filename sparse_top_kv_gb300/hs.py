@@ -600,11 +600,12 @@ def _matrix(t, dtype, name, device, rows, cols):
     columns, or (None, 0)."""
     if t is None:
         return None, 0
-    shape, stride = t.shape, t.stride()
-    if (t.dtype is not dtype or t.get_device() != device or len(shape) != 2 or shape[0] != rows
-            or shape[1] < cols or stride[1] != 1 or stride[0] < shape[1]):
-        _check_rows(t, dtype, name, device, rows, cols)
-    return t.data_ptr(), stride[0] if rows > 1 else shape[1]
+    shape = t.shape
+    if (t.dtype is dtype and t.get_device() == device and len(shape) == 2 and shape[0] == rows
+            and shape[1] >= cols and t.is_contiguous()):
+        return t.data_ptr(), shape[1]
+    _check_rows(t, dtype, name, device, rows, cols)
+    return t.data_ptr(), t.stride(0) if rows > 1 else shape[1]
 
 
 def _output(t, dtype, name, device, shape):
@@ -660,7 +661,9 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, *, window=0,
     attention weights summed over the heads.  workspace: a CUDA tensor, used
     if it is large enough (paged_decode_workspace_bytes).  Returns (out [rows,
     heads, d] of q's type, lse fp32 [rows, heads])."""
-    dev = _current_device(q, "q")
+    dev = q.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError("q: must be on the current CUDA device")
     qt, kt = q.dtype, k_cache.dtype
     if qt is not torch.bfloat16 and qt is not torch.float16:
         raise TypeError(f"q: expected torch.bfloat16 or torch.float16, got {qt}")
@@ -668,7 +671,7 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, *, window=0,
         raise TypeError(f"k_cache: unsupported {kt}")
     if v_cache is None:
         raise ValueError("v_cache: needed")
-    qshape, qstride, kshape, kstride = q.shape, q.stride(), k_cache.shape, k_cache.stride()
+    qshape, kshape, kstride, tshape = q.shape, k_cache.shape, k_cache.stride(), block_table.shape
     if (len(kshape) != 4 or kstride[3] != 1 or k_cache.get_device() != dev
             or v_cache.dtype is not kt or v_cache.shape != kshape or v_cache.stride() != kstride
             or v_cache.get_device() != dev):
@@ -677,37 +680,57 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, *, window=0,
     num_pages, page_size, kv_heads, dc = kshape
     if dc != d:
         raise ValueError("k_cache: head size of q")
-    if rows and (qstride[2] != 1 or qstride[1] != d):
-        raise ValueError("q: heads must be packed")
-    table, table_stride = _matrix(block_table, _I, "block_table", dev, rows, 0)
-    blocks = block_table.shape[1]
+    if q.is_contiguous():
+        q_stride = heads * d
+    else:
+        q_stride, *rest = q.stride()
+        if rest != [d, 1]:
+            raise ValueError("q: heads must be packed")
+    if (block_table.dtype is not _I or seq_lens.dtype is not _I
+            or block_table.get_device() != dev or seq_lens.get_device() != dev
+            or seq_lens.shape != (rows,) or len(tshape) != 2 or tshape[0] != rows
+            or not seq_lens.is_contiguous() or not block_table.is_contiguous()):
+        _check_rows(block_table, _I, "block_table", dev, rows, 0)
+        _check_rows(seq_lens, _I, "seq_lens", dev, rows)
+    blocks = tshape[1]
     if max_len is None:
         max_len = blocks * page_size
         if score is not None and score.dim() == 2:
             max_len = min(max_len, score.shape[1])
-    lens = _vector(seq_lens, _I, "seq_lens", dev, rows)
-    score_ptr, score_stride = _matrix(score, _F, "score", dev, rows, max_len)
-    k_scale_ptr = _vector(k_scale, _F, "k_scale", dev, kv_heads)
-    v_scale_ptr = _vector(v_scale, _F, "v_scale", dev, kv_heads)
+    score_ptr, score_stride, k_scale_ptr, v_scale_ptr = None, 0, None, None
+    if score is not None:
+        score_ptr, score_stride = _matrix(score, _F, "score", dev, rows, max_len)
+    if k_scale is not None:
+        k_scale_ptr = _vector(k_scale, _F, "k_scale", dev, kv_heads)
+    if v_scale is not None:
+        v_scale_ptr = _vector(v_scale, _F, "v_scale", dev, kv_heads)
     if out is None:
         out = torch.empty(rows, heads, d, dtype=qt, device=q.device)
+    elif (out.dtype is not qt or out.get_device() != dev or out.shape != qshape
+          or not out.is_contiguous()):
+        _output(out, qt, "out", dev, qshape)
     if lse is None:
         lse = torch.empty(rows, heads, dtype=_F, device=q.device)
-    out_ptr = _output(out, qt, "out", dev, qshape)
-    lse_ptr = _output(lse, _F, "lse", dev, (rows, heads))
-    ps, rs, hstr = _cache_strides(k_cache, 1)
+    elif (lse.dtype is not _F or lse.get_device() != dev or lse.shape != (rows, heads)
+          or not lse.is_contiguous()):
+        _output(lse, _F, "lse", dev, (rows, heads))
+    # A dimension of one entry may have any stride: it is never used.
+    ps, rs, hstr, _ = kstride
+    if num_pages <= 1 or page_size <= 1 or kv_heads <= 1:
+        ps, rs, hstr = _cache_strides(k_cache, 1)
     call = lib().hs_paged_decode
     for again in (False, True):
         ws, ws_bytes = None, 0
         if workspace is not None:
             if workspace.get_device() != dev:
                 raise ValueError("workspace: must be on q's device")
-            ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        rc = call(q.data_ptr(), qstride[0] if rows > 1 else heads * d, _ELEMENT[qt],
-                  k_cache.data_ptr(), v_cache.data_ptr(), _ELEMENT[kt], ps, rs, hstr, num_pages,
-                  page_size, table, table_stride, blocks, max_len, lens, k_scale_ptr, v_scale_ptr,
-                  rows, heads, kv_heads, d, window, num_sinks, scale, score_ptr, score_stride,
-                  score_decay, out_ptr, lse_ptr, ws, ws_bytes, _status_ptr(status),
+            ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
+        rc = call(q.data_ptr(), q_stride, _ELEMENT[qt], k_cache.data_ptr(), v_cache.data_ptr(),
+                  _ELEMENT[kt], ps, rs, hstr, num_pages, page_size, block_table.data_ptr(),
+                  block_table.stride(0) if rows > 1 else blocks, blocks, max_len,
+                  seq_lens.data_ptr(), k_scale_ptr, v_scale_ptr, rows, heads, kv_heads, d, window,
+                  num_sinks, scale, score_ptr, score_stride, score_decay, out.data_ptr(),
+                  lse.data_ptr(), ws, ws_bytes, None if status is None else _status_ptr(status),
                   _raw_stream(dev, stream))
         if rc != 3 or again:
             break
