@@ -550,10 +550,12 @@ int hs_sparse_decode_fp8ds(const void* q, const void* kv8, int64_t row_bytes,
  *             never read).
  * What stands in places past T, outside the window or skipped has no effect,
  * NaN included.  A request whose logits are all -inf gives out = 0 and lse =
- * -inf.  Results do not depend on timing.
+ * -inf; entries of attended tokens that are not finite give outputs of their
+ * own head that are not finite (an infinite V entry NaN).  Results do not depend on timing.
  * Supported: d 64, 128 or 256, any heads / kv_heads; others (and scales with
  * 16-bit caches, or caches of another 16-bit type than q) return
- * HS_ERR_UNSUPPORTED.  rows <= 4096 and rows * heads * max_len / 16 < 2^31
+ * HS_ERR_UNSUPPORTED.  rows <= 4096, max_len <= 2^30 and about
+ * rows * heads * max_len / 16 < 2^31
  * (HS_ERR_CAPACITY above, or when the workspace is missing or too small; the
  * workspace query gives -1 for sizes that are refused).
  * ------------------------------------------------------------------------- */

@@ -431,7 +431,7 @@ Layout layout(int32_t rows, int32_t heads, int32_t kv_heads, int32_t d, int32_t 
 
 // Tiles (of 16 tokens of a KV head at least) are counted in 31 bits.
 bool too_large(int32_t rows, int32_t heads, int32_t max_len) {
-    return rows > kMaxRows ||
+    return rows > kMaxRows || max_len > (1 << 30) ||
            int64_t(rows) * heads * (int64_t(max_len) / 16 + 16) >= (int64_t(1) << 31);
 }
 

@@ -14,7 +14,8 @@
 //    box takes all heads of a run of tokens and DRAM is read in long pieces
 //    (one head's row at a time: 351 instead of 336 us over a bf16 batch of up
 //    to 64 K tokens, 122 instead of 88 over E4M3 rows of 128 bytes).  Rows of
-//    a tile: [run of bt tokens][head][token of the run].
+//    a tile: [run of bt tokens][head][token of the run], so that a K step of
+//    PV holds one head (E4M3 pages of 16: a box per head, [head][token]).
 //  * One elected lane per run issues the boxes into a K ring and a V ring in
 //    128-byte-swizzled blocks; the loads run ahead over the ends of units.
 //  * S^T[128 rows x queries] = K Q^T takes the queries of all hs heads as N;
@@ -79,7 +80,8 @@ constexpr int kTilesAlone = 12;      // places per CTA
 
 struct TcArgs {
     PagedArgs p;
-    int32_t bt[2];
+    int32_t bt[2];     // tokens of a run (a box): they lie in one page
+    int32_t split[2];  // runs shorter than a K step of PV: one box per head
     uint64_t timeout_ns;
 };
 
@@ -99,10 +101,8 @@ struct Cfg {
     static constexpr int kPParts = kE4 ? 4 : 2;
     static constexpr int NH = GM * kQParts;              // query columns of a head
     static constexpr int NP = GM * kPParts;              // output columns of a head
-    // P^T: K-major rows of 64 (E4M3: 128) cache rows; E4M3 tiles whose runs
-    // are 16 rows long hold two heads in a K step, each in rows of its own.
-    static constexpr int kPRows = kE4 ? 2 * NP : NP;
-    static constexpr int kPBytes = kPRows * kRows * kElt;
+    static constexpr int kStep = 32 / kElt;              // rows of a PV K step
+    static constexpr int kPBytes = NP * kRows * kElt;    // P^T: rows of 64 (E4M3: 128) cache rows
     // Most heads of a tile: as many as leave the accumulators within TMEM and
     // at least three units in each ring.
     static constexpr int q_rows(int hs) { return hs * NH < 16 ? 16 : (hs * NH + 15) / 16 * 16; }
@@ -353,10 +353,9 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
         hs::tc::tmem_alloc(&B.tmem_base, kTmemCols);
         hs::tc::tmem_relinquish();
     }
-    // P's rows of the other head of a K step stay zero, and so do the rows of
-    // queries that a unit does not have.
+    // The rows of queries that a unit does not have stay zero.
     if constexpr (E4) {
-        constexpr int kBytes = C::kBarOff - C::kQOff;
+        constexpr int kBytes = C::kPOff - C::kQOff;
         for (int i = tid; i < kBytes / 16; i += kThreads)
             reinterpret_cast<uint4*>(smem + C::kQOff)[i] = make_uint4(0u, 0u, 0u, 0u);
         hs::fence_proxy_async_shared();
@@ -379,7 +378,9 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
     // hs and bt are powers of two.
     const int lhs = 31 - __clz(hsn), lbt = 31 - __clz(bt);
     const int lth = a.lth[way];          // log2 of the tokens of a tile
-    const int nops = 1 << (lth - lbt);   // runs (boxes) of a tile
+    const int runs = 1 << (lth - lbt);   // runs of a tile
+    const bool split = ta.split[way] != 0;
+    const int lrow = split ? lth : lbt;  // log2 of a head's neighbouring rows
     const int nq = max(16, (hsn * C::NH + 15) / 16 * 16);  // N of the QK product
     const uint32_t o_col = uint32_t(2 * nq);
     const int ocols = hsn * C::NP;       // output columns of 128 dims
@@ -393,25 +394,29 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
         Cursor c = start;
         bool ok = true, bad = false;
         int kseq = 0, vseq = 0, t = 0;
-        // Lane i < nops: run i of the tile; its page is looked up a tile ahead.
+        // Lane i: run i % runs of the tile (and head i / runs, if the boxes are
+        // split); its page is looked up a tile ahead.
+        const int run_i = lane & (runs - 1), head_i = lane >> (lth - lbt);
+        const bool lane_in = head_i < (split ? hsn : 1);
+        const uint32_t lane_row =
+            split ? uint32_t((head_i << lth) + (run_i << lbt)) : uint32_t(run_i << (lhs + lbt));
+        const uint32_t box = uint32_t(split ? bt : hsn * bt) * 128u;  // bytes of a block's box
         auto lookup = [&](const Cursor& x, int& tok) {
-            tok = lane < nops ? tile_token(x, lth) + lane * bt : 0;
-            const bool want = lane < nops && any_visible(x.v, tok, bt);
-            if (!want) return -2;
+            tok = tile_token(x, lth) + (run_i << lbt);
+            if (!lane_in || !any_visible(x.v, tok, bt)) return -2;
             return __ldg(a.block_table + int64_t(x.row) * a.bt_stride + block_of(a, tok));
         };
         int tok_n, page_n = lookup(c, tok_n);
         for (; ok;) {
             const int tok = tok_n, page = page_n;
-            const int kvh0 = c.chunk / gch * hsn;
+            const int head0 = c.chunk / gch * hsn + (split ? head_i : 0);
             const bool more = c.left > 1;
             advance(c, a, chunks, lth);
             if (more) page_n = lookup(c, tok_n);
             const bool want = page >= 0 && page < a.num_pages;
             if (page != -2 && !want) bad = true;
             const uint32_t loaded = __ballot_sync(0xffffffffu, want);
-            const int boxes = __popc(loaded);
-            const uint32_t bytes = uint32_t(boxes) * uint32_t(hsn * bt) * 128u * C::kSubBlocks;
+            const uint32_t bytes = uint32_t(__popc(loaded)) * box * C::kSubBlocks;
             const int at = tok - block_of(a, tok) * a.page_size;
             // Read by the softmax of this tile (its logits follow these
             // loads), at most NS + 3 tiles behind.
@@ -428,11 +433,11 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
                     if (lane == 0) hs::mbar_arrive_expect_tx(&full[slot], bytes);
                     __syncwarp();
                     if (want) {
-                        const uint32_t dst = sb + off + slot * C::kSub + lane * hsn * bt * 128;
+                        const uint32_t dst = sb + off + slot * C::kSub + lane_row * 128;
 #pragma unroll
                         for (int b = 0; b < C::kSubBlocks; ++b)
                             tma_load(dst + b * kBlk, map, (s * C::kSubBlocks + b) * C::kBlkDims,
-                                     at, kvh0, page, &full[slot]);
+                                     at, head0, page, &full[slot]);
                     }
                 }
                 return true;
@@ -514,11 +519,8 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
     } else if (warp == kPvWarp) {
         // -------------------------- O^T += V^T P^T -----------------------------
         if (lane == 0) {
-            constexpr int kStep = E4 ? 32 : 16;  // rows of a K step
-            constexpr int kSteps = kRows / kStep;
-            // E4M3, runs of 16 rows: a K step holds two heads, taken together.
-            const bool two = E4 && bt < kStep && hsn > 1;
-            const uint32_t id = idesc<KV>(two ? 2 * C::NP : C::NP, 1);
+            constexpr int kStep = C::kStep, kSteps = kRows / kStep;
+            const uint32_t id = idesc<KV>(C::NP, 1);
             const uint64_t v_desc = hs::tc::sdesc_sw128(sb + C::kVOff, kBlk, 1024);
             const uint64_t p_desc = hs::tc::sdesc_sw128(sb + C::kPOff, 16, 1024);
             // Output column of each K step's head, and the steps that hold a
@@ -527,8 +529,8 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
 #pragma unroll
             for (int kk = 0; kk < kSteps; ++kk) {
                 const int r = kk * kStep;
-                col[kk] = tmem + o_col + uint32_t((r >> lbt) & (hsn - 1)) * C::NP;
-                if (r < (hsn << lbt) && (two || (r & (bt - 1)) == 0)) starts |= 1u << kk;
+                col[kk] = tmem + o_col + uint32_t((r >> lrow) & (hsn - 1)) * C::NP;
+                if (r < (hsn << lrow) && (r & ((1 << lrow) - 1)) == 0) starts |= 1u << kk;
             }
             Cursor c = start;
             bool ok = true;
@@ -615,23 +617,22 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
         // ------------------------- softmax and epilogue ------------------------
         const int wg = warp >> 2;                // group: tiles t with t % 2 == wg
         const int r = tid & 127;                 // row of the tile, and TMEM lane
-        const int run_r = r >> (lhs + lbt);      // its run
-        const int hl = (r >> lbt) & (hsn - 1);   // its head in the unit
-        const int rt = (run_r << lbt) + (r & (bt - 1));  // its token in the tile
+        const int hl = (r >> lrow) & (hsn - 1);  // its head in the unit
+        const int rt = (r >> (lhs + lrow) << lrow) + (r & ((1 << lrow) - 1));  // its token
+        const int run_r = rt >> lbt;             // and that token's run
         const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
         // Heads of the warp's two half warps.
-        const int hA = ((warp & 3) * 32 >> lbt) & (hsn - 1);
-        const int hB = ((warp & 3) * 32 + 16 >> lbt) & (hsn - 1);
+        const int hA = ((warp & 3) * 32 >> lrow) & (hsn - 1);
+        const int hB = ((warp & 3) * 32 + 16 >> lrow) & (hsn - 1);
         const uint32_t s_addr = tmem + lane_base + uint32_t(wg * nq);
         const uint32_t o_addr = tmem + lane_base + o_col;
         const uint32_t o_own = o_addr + uint32_t(wg * C::kSubs * ocols);
         const uint32_t p_own = sb + C::kPOff + wg * C::kPBytes;
         // This row's place in P^T: K-major rows of 128 bytes, 64 (E4M3: 128)
-        // cache rows each; E4M3 with two heads in a K step: each its own rows.
+        // cache rows each.
         const int p_col = E4 ? r : (r & 63) * 2;
         const uint32_t p_row =
-            p_own + (E4 ? (bt < 32 && hsn > 1 ? uint32_t(hl & 1) * (C::NP * 128) : 0u)
-                        : uint32_t(r >> 6) * (C::NP * 128)) + uint32_t(p_col & 15);
+            p_own + (E4 ? 0u : uint32_t(r >> 6) * (C::NP * 128)) + uint32_t(p_col & 15);
         const uint32_t p_chunk = uint32_t(p_col >> 4);
         auto put16 = [&](int n, uint16_t x) {
             asm volatile("st.shared.u16 [%0], %1;" ::"r"(
@@ -647,7 +648,7 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
         };
         // The j-th group of 16 rows that belong to this row's head, j < 8 / hs.
         auto rows_of = [&](int j) {
-            const int lg = lbt - 4;  // log2 of the groups of a run
+            const int lg = lrow - 4;  // log2 of a head's neighbouring groups
             return ((((j >> lg) << lhs) + hl) << lg) + (j & ((1 << lg) - 1));
         };
         bool fail = false;
@@ -897,7 +898,7 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
 #pragma unroll
                 for (int w = 0; w < kGroups; ++w) {
                     lw[w] = 0.f;
-                    const int lg = lbt - 4;
+                    const int lg = lrow - 4;
                     for (int j = 0; j < (8 >> lhs); ++j)
                         lw[w] += B.red[w][((((j >> lg) << lhs) + h) << lg) + (j & ((1 << lg) - 1))][i];
                 }
@@ -994,20 +995,22 @@ int launch_one(PagedArgs& a, hs_stream_t stream) {
     for (int i = 0; i < 2; ++i) {
         t.bt[i] = kRows / a.hs[i];
         while (a.page_size % t.bt[i]) t.bt[i] /= 2;
+        t.split[i] = a.hs[i] > 1 && t.bt[i] < C::kStep;
     }
     t.timeout_ns = hs::kWaitTimeoutNs;
     // Small calls surely take way 1: two descriptors instead of four.
     const bool both = a.hs[0] != 1 && most_places(a) >= a.wide_from;
     CUtensorMap m[4];
     for (int i = both ? 0 : 1; i < 2; ++i) {
-        int rc = encode_map(&m[2 * i], KV, a.k, a, D, t.bt[i], a.hs[i]);
-        if (rc == HS_OK) rc = encode_map(&m[2 * i + 1], KV, a.v, a, D, t.bt[i], a.hs[i]);
+        int rc = encode_map(&m[2 * i], KV, a.k, a, D, t.bt[i], t.split[i] ? 1 : a.hs[i]);
+        if (rc == HS_OK) rc = encode_map(&m[2 * i + 1], KV, a.v, a, D, t.bt[i], t.split[i] ? 1 : a.hs[i]);
         if (rc != HS_OK) return rc;
     }
     if (!both) {
         m[0] = m[2];
         m[1] = m[3];
         t.bt[0] = t.bt[1];
+        t.split[0] = t.split[1];
         a.hs[0] = a.hs[1];
         a.lth[0] = a.lth[1];
         a.chunks[0] = a.chunks[1];

@@ -355,3 +355,41 @@ def test_nothing_cached():
     score = torch.full((3, 16), 4.0, device="cuda")
     out, lse, status = run_and_check(s, score=score)
     assert status == 0 and not out.any() and (lse == -math.inf).all() and (score == 4.0).all()
+
+
+@pytest.mark.parametrize("page", [16, 32, 48, 64, 7])
+@pytest.mark.parametrize("kind,d", [("e4m3", 128), ("e4m3", 256), ("bf16", 128), ("fp16", 64)])
+def test_what_is_not_attended_has_no_effect(kind, d, page):
+    """NaN behind the contexts and in unused pages, at every way of cutting a
+    call (few and many tiles)."""
+    for lens in ([33, 1, 100], [3000, 47, 0, 2500, 1777, 900, 31, 4000]):
+        s = make(lens, 16, 4, d, page, kind=kind, seed=page + d, poison=True)
+        *_, status = run_and_check(s)
+        assert status == 0
+
+
+@pytest.mark.parametrize("page", [16, 32, 5])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_a_nan_stays_in_its_head(kind, page):
+    for lens in ([40, 300], [4000, 2000, 3000, 1500, 2500, 3500]):
+        s = make(lens, 16, 8, 128, page, kind=kind, seed=page)
+        want, want_lse, _ = run_and_check(s)
+        at = s["table"][1, 17 // page].long(), 17 % page
+        s["v"][at[0], at[1], 3] = math.nan
+        s["k"][at[0], at[1], 6] = math.nan
+        out, lse, _ = run_and_check_nonfinite_scaled(s)
+        heads = torch.ones(16, dtype=torch.bool, device="cuda")
+        heads[6:8] = heads[12:14] = False
+        assert torch.isnan(out[1, 6:8]).all() and torch.isnan(out[1, 12:14]).all()
+        assert torch.equal(out[1, heads], want[1, heads])
+        assert torch.equal(lse[1, :12], want_lse[1, :12]) and torch.isnan(lse[1, 12:14]).all()
+        rest = [r for r in range(len(lens)) if r != 1]
+        assert torch.equal(out[rest], want[rest]) and torch.equal(lse[rest], want_lse[rest])
+
+
+def run_and_check_nonfinite_scaled(s):
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = hs.paged_decode(s["q"], s["k"], s["v"], s["table"], s["lens"], s["scale"],
+                               k_scale=s["scales"][0], v_scale=s["scales"][1], status=status)
+    torch.cuda.synchronize()
+    return out, lse, int(status.item())
