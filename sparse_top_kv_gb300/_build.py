@@ -1,10 +1,13 @@
 """Build libhs.so (the C ABI of include/hs_api.h) from csrc/*.cu with nvcc for
 sm_103a.  One nvcc process per translation unit, run in parallel, then one
-link.  Output: sparse_top_kv_gb300/_build/libhs.so (git-ignored, in-tree)."""
+link.  Output: sparse_top_kv_gb300/_build/libhs.so (git-ignored, in-tree), and
+beside it the Python extension of the hot calls (csrc/hs_binding.cpp) where
+Python's headers are installed."""
 import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -12,6 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libhs.so")
+BINDING = os.path.join(OUT_DIR, "_hs_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I" + INCLUDE, "-I" + CSRC]
@@ -37,7 +41,9 @@ def _deps_mtime():
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+    done = [LIB] + ([BINDING] if _python_include() else [])
+    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= _deps_mtime()
+                         for p in done):
         return LIB
     cc = nvcc()
     objs = []
@@ -60,7 +66,28 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{res.stderr}")
     os.replace(tmp, LIB)
+    _build_binding()
     return LIB
+
+
+def _python_include():
+    """Folder of Python.h, or None."""
+    inc = sysconfig.get_paths()["include"]
+    return inc if os.path.exists(os.path.join(inc, "Python.h")) and shutil.which("g++") else None
+
+
+def _build_binding():
+    inc = _python_include()
+    if inc is None:
+        return
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I" + inc, "-I" + INCLUDE,
+           os.path.join(CSRC, "hs_binding.cpp"), "-o", tmp, "-L" + OUT_DIR, "-l:libhs.so",
+           "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on hs_binding.cpp:\n{res.stderr}")
+    os.replace(tmp, BINDING)
 
 
 if __name__ == "__main__":

@@ -6,12 +6,16 @@ CUDA stream.  Every step of the path runs in the CUDA kernels of libhs.so;
 there is no CPU fallback.  If the library cannot be loaded this module raises.
 """
 import ctypes
+import importlib.machinery
+import importlib.util
+import os
 
 import torch
 
 from . import _build
 
 _lib = None
+_binding = None  # the hot calls' extension module (csrc/hs_binding.cpp), if built
 
 HS_OK = 0
 STATUS_NAMES = {0: "HS_OK", 1: "HS_ERR_INVALID_ARG", 2: "HS_ERR_MISALIGNED", 3: "HS_ERR_CAPACITY",
@@ -101,7 +105,20 @@ def lib():
             f.argtypes = args
             f.restype = res
         _lib = L
+        _load_binding()
     return _lib
+
+
+def _load_binding():
+    global _binding
+    if not os.path.exists(_build.BINDING):
+        return
+    loader = importlib.machinery.ExtensionFileLoader("_hs_binding", _build.BINDING)
+    mod = importlib.util.module_from_spec(
+        importlib.util.spec_from_loader("_hs_binding", loader))
+    loader.exec_module(mod)
+    mod.setup(torch.bfloat16, torch.float16, torch.float8_e4m3fn, torch.float32, torch.int32)
+    _binding = mod
 
 
 def _ptr(t):
@@ -547,9 +564,11 @@ def sparse_decode_noalloc(q, k_base, v_base, row_stride, kv_head_stride, num_kv_
 
 
 # ---------------------------------------------------------------------------
-# Paged caches.  These calls are short next to their argument checks, so each
-# argument is first compared with what it should be in one expression; the
-# checkers below, which say what is wrong, run where that fails.
+# Paged caches.  These calls are short next to their argument checks.  The
+# common case (contiguous tensors, everything given) is checked and called by
+# the extension module, which returns None for any other; then each argument is
+# compared with what it should be in one expression, and the checkers below,
+# which say what is wrong, run where that fails.
 _ELEMENT = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}  # HS_BF16, ..
 _I, _F = torch.int32, torch.float32
 
@@ -661,8 +680,17 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, *, window=0,
     attention weights summed over the heads.  workspace: a CUDA tensor, used
     if it is large enough (paged_decode_workspace_bytes).  Returns (out [rows,
     heads, d] of q's type, lse fp32 [rows, heads])."""
-    dev = q.get_device()
-    if dev < 0 or dev != torch._C._cuda_getDevice():
+    dev = torch._C._cuda_getDevice()
+    if _binding is not None:
+        rc = _binding.paged_decode(dev, _raw_stream(dev, stream), q, k_cache, v_cache,
+                                   block_table, seq_lens, scale, window, num_sinks, max_len,
+                                   k_scale, v_scale, score, score_decay, out, lse, workspace,
+                                   status)
+        if rc is not None:
+            if rc != HS_OK:
+                raise HSError("hs_paged_decode", rc)
+            return out, lse
+    if q.get_device() != dev:
         raise ValueError("q: must be on the current CUDA device")
     qt, kt = q.dtype, k_cache.dtype
     if qt is not torch.bfloat16 and qt is not torch.float16:
@@ -697,6 +725,8 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, *, window=0,
         max_len = blocks * page_size
         if score is not None and score.dim() == 2:
             max_len = min(max_len, score.shape[1])
+    if not 0 <= max_len < 1 << 31:
+        raise ValueError("max_len: 0 to 2^31 - 1")
     score_ptr, score_stride, k_scale_ptr, v_scale_ptr = None, 0, None, None
     if score is not None:
         score_ptr, score_stride = _matrix(score, _F, "score", dev, rows, max_len)
@@ -844,6 +874,17 @@ def evict(score, seq_lens, budget, k_cache, v_cache, block_table, *, max_len=Non
           lens_out=None, moves=None, status=None, stream=None):
     """evict_select, then evict_move on one layer's caches (hs_evict); same
     arguments and result as evict_select."""
+    if _binding is not None:
+        dev = torch._C._cuda_getDevice()
+        rc = _binding.evict(dev, _raw_stream(dev, stream), score, seq_lens, budget, k_cache,
+                            v_cache, block_table, max_len, recent, num_sinks, positions, next_pos,
+                            score_out, positions_out, lens_out, moves, status)
+        if rc is not None:
+            if rc != HS_OK:
+                raise HSError("hs_evict", rc)
+            return (score if score_out is None else score_out,
+                    positions if positions_out is None else positions_out,
+                    seq_lens if lens_out is None else lens_out, moves)
     dev, args, result = _evict_args(score, seq_lens, budget, max_len, recent, num_sinks,
                                     positions, next_pos, score_out, positions_out, lens_out,
                                     moves)

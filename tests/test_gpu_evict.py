@@ -324,3 +324,49 @@ def test_a_few_tokens_over_moves(layout):
             for s, t in zip(src[r, :cnt[r]].tolist(), dst[r, :cnt[r]].tolist()):
                 want[tab[r, t // page].long(), t % page] = was[tab[r, s // page].long(), s % page]
         assert same_bits(c, want)
+
+
+@pytest.mark.parametrize("given", ["all", "least"])
+def test_extension_and_general_path_agree(given, monkeypatch):
+    hs.lib()
+    if hs._binding is None:
+        pytest.skip("Python headers were not there at build time")
+    taken = []
+
+    class Spy:
+        def evict(self, *a):
+            taken.append(binding.evict(*a))
+            return taken[-1]
+
+    binding = hs._binding
+    R, W, B, page = 5, 96, 40, 16
+    g = torch.Generator().manual_seed(8)
+    first = torch.rand(R, W, generator=g)
+    table = torch.randperm(R * 6, generator=g).view(R, 6).to(torch.int32).cuda()
+    base = caches(R * 6, page, 2, 64, torch.bfloat16)
+    got = []
+    for mod in (Spy(), None):
+        monkeypatch.setattr(hs, "_binding", mod)
+        k, v = (c.clone() for c in base)
+        score = first.cuda()
+        lens = torch.tensor([96, 41, 40, 0, 70], dtype=torch.int32, device="cuda")
+        moves = tuple(torch.zeros(*s, dtype=torch.int32, device="cuda")
+                      for s in ((R, B), (R, B), (R,)))
+        kw = {}
+        if given == "all":
+            kw = dict(max_len=W, recent=5, num_sinks=2, score_out=torch.ones(R, W, device="cuda"),
+                      positions=torch.arange(W, dtype=torch.int32, device="cuda").repeat(R, 1),
+                      next_pos=lens.clone(), lens_out=torch.empty_like(lens),
+                      positions_out=torch.zeros(R, W, dtype=torch.int32, device="cuda"),
+                      status=torch.zeros(1, dtype=torch.int32, device="cuda"))
+        r = hs.evict(score, lens, B, k, v, table, moves=moves, **kw)
+        torch.cuda.synchronize()
+        got.append([x for x in (*r[:3], *moves, k, v) if x is not None])
+        assert r[0] is kw.get("score_out", score) and r[2] is kw.get("lens_out", lens)
+    assert taken == [0]
+    for a, b in zip(*got):
+        assert same_bits(a, b)
+    monkeypatch.setattr(hs, "_binding", Spy())
+    with pytest.raises(hs.HSError):
+        hs.evict(first.cuda(), lens, 0, k, v, table, moves=moves)
+    assert taken[-1] == 1

@@ -393,3 +393,59 @@ def run_and_check_nonfinite_scaled(s):
                                k_scale=s["scales"][0], v_scale=s["scales"][1], status=status)
     torch.cuda.synchronize()
     return out, lse, int(status.item())
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("scored", [False, True])
+def test_extension_and_general_path_agree(kind, scored, monkeypatch):
+    """The extension module's common case and the general path of the binding
+    make the same call; what the extension does not take is refused as before."""
+    hs.lib()
+    if hs._binding is None:
+        pytest.skip("Python headers were not there at build time")
+    taken = []
+
+    class Spy:
+        def paged_decode(self, *a):
+            taken.append(binding.paged_decode(*a))
+            return taken[-1]
+
+    binding = hs._binding
+    s = make([100, 7, 0, 333], 8, 2, 128, 16, kind=kind, seed=3)
+    n = s["table"].shape[1] * 16
+    ws = torch.empty(hs.paged_decode_workspace_bytes(4, 8, 2, 128, n, window=50, num_sinks=4,
+                                                     with_score=True),
+                     dtype=torch.uint8, device="cuda")
+    got = []
+    for mod in (Spy(), None):
+        monkeypatch.setattr(hs, "_binding", mod)
+        score = torch.full((4, n - 3), 0.5, device="cuda") if scored else None
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = torch.empty_like(s["q"])
+        lse = torch.empty(4, 8, device="cuda")
+        r = hs.paged_decode(s["q"], s["k"], s["v"], s["table"], s["lens"], s["scale"], window=50,
+                            num_sinks=4, k_scale=s["scales"][0], v_scale=s["scales"][1],
+                            score=score, score_decay=0.25, out=out, lse=lse, workspace=ws,
+                            status=status)
+        torch.cuda.synchronize()
+        assert r[0] is out and r[1] is lse and int(status) == 0
+        got.append((out, lse) + ((score,) if scored else ()))
+    assert taken == [0]
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    # Left to the general path: a workspace that is too small, a strided query.
+    monkeypatch.setattr(hs, "_binding", Spy())
+    small = torch.empty(256, dtype=torch.uint8, device="cuda")
+    wide = torch.empty(4, 8 * 128 + 8, dtype=s["q"].dtype, device="cuda")
+    wide[:, :8 * 128] = s["q"].view(4, -1)
+    for q, w in ((s["q"], small), (wide[:, :8 * 128].unflatten(1, (8, 128)), ws)):
+        out = torch.empty_like(s["q"])
+        hs.paged_decode(q, s["k"], s["v"], s["table"], s["lens"], s["scale"], window=50,
+                        num_sinks=4, k_scale=s["scales"][0], v_scale=s["scales"][1], out=out,
+                        lse=torch.empty(4, 8, device="cuda"), workspace=w)
+        assert taken[-1] is None and torch.equal(out, got[0][0])
+    with pytest.raises(hs.HSError):  # an error of the C call through the extension
+        hs.paged_decode(s["q"], s["k"], s["v"], s["table"], s["lens"], s["scale"], window=-1,
+                        k_scale=s["scales"][0], v_scale=s["scales"][1], out=out,
+                        lse=torch.empty(4, 8, device="cuda"), workspace=ws)
+    assert taken[-1] == 1
