@@ -551,13 +551,16 @@ int hs_sparse_decode_fp8ds(const void* q, const void* kv8, int64_t row_bytes,
  * What stands in places past T, outside the window or skipped has no effect,
  * NaN included.  A request whose logits are all -inf gives out = 0 and lse =
  * -inf; entries of attended tokens that are not finite give outputs of their
- * own head that are not finite (an infinite V entry NaN).  Results do not depend on timing.
+ * own head that are not finite (an infinite V entry NaN).  Results do not
+ * depend on timing.  out must not overlap an input.  A process's first call of
+ * a kind (types, d, group size) loads its kernel: make it before a stream
+ * capture.
  * Supported: d 64, 128 or 256, any heads / kv_heads; others (and scales with
  * 16-bit caches, or caches of another 16-bit type than q) return
- * HS_ERR_UNSUPPORTED.  rows <= 4096, max_len <= 2^30 and about
- * rows * heads * max_len / 16 < 2^31
- * (HS_ERR_CAPACITY above, or when the workspace is missing or too small; the
- * workspace query gives -1 for sizes that are refused).
+ * HS_ERR_UNSUPPORTED.  rows <= 4096, heads <= 65536, max_len <= 2^30 and about
+ * rows * heads * max_len / 16 < 2^31 (HS_ERR_CAPACITY above, or when the
+ * workspace is missing or too small; the workspace query gives -1 for sizes
+ * that are refused).
  * ------------------------------------------------------------------------- */
 int64_t hs_paged_decode_workspace_bytes(int32_t rows, int32_t heads, int32_t kv_heads, int32_t d,
                                         int32_t max_len, int32_t window, int32_t num_sinks,
@@ -594,8 +597,9 @@ int hs_paged_decode(const void* q, int64_t q_stride, int32_t q_dtype, const void
  *             (moved tokens stand out of order), or NULL: the place itself.
  * next_pos    int32 [rows]: one more than the newest position, or NULL: T.
  * max_len     host-side bound on T (strides are at least max_len; up to 2^30,
- *             HS_ERR_CAPACITY above); a longer request counts as max_len tokens and is reported as
- *             HS_ERR_BAD_INDEX in *status.  T <= 0: an unused slot.
+ *             HS_ERR_CAPACITY above); a longer request counts as max_len
+ *             tokens and is reported as HS_ERR_BAD_INDEX in *status.  T <= 0:
+ *             an unused slot.
  * recent, num_sinks  recent + num_sinks <= budget.
  * score_out   fp32 [rows, score_out_stride], may be `score`: the kept
  *             tokens' scores at their new places; 0 in the places given up

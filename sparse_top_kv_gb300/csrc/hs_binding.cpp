@@ -1,8 +1,8 @@
 // hs_binding.cpp -- the usual calls of the paged-cache entry points from
 // Python without the interpreter in between: a decode step's kernel runs for
 // ten microseconds, and checking and converting thirty arguments in Python and
-// ctypes took as long again (13.4 us a call of hs_paged_decode, 9.0 here; hs_evict
-// 14.2 and 7.9).
+// ctypes took as long again (13.4 us a call of hs_paged_decode, 9.0 here;
+// hs_evict 14.2 and 7.9).
 //
 // Each function looks at its tensors through their Python attributes (no torch
 // headers) and makes the C call if everything is as in the common case: right
@@ -58,6 +58,7 @@ bool as_float(PyObject* o, float* out) {
 // Contiguous tensor on `device` with at most four dimensions.
 Tensor look(PyObject* t, int64_t device) {
     Tensor x;
+    if (PyErr_Occurred()) return x;  // an earlier look failed: on to general()
     PyObject* o = PyObject_GetAttr(t, s_dtype);
     if (o == nullptr) return x;
     x.dtype = o;  // a singleton that outlives the call

@@ -429,9 +429,10 @@ Layout layout(int32_t rows, int32_t heads, int32_t kv_heads, int32_t d, int32_t 
     return w;
 }
 
-// Tiles (of 16 tokens of a KV head at least) are counted in 31 bits.
+// Tiles (of 16 tokens of a KV head at least) are counted in 31 bits; the
+// finishing kernel's grid has a block for up to eight heads in its y dimension.
 bool too_large(int32_t rows, int32_t heads, int32_t max_len) {
-    return rows > kMaxRows || max_len > (1 << 30) ||
+    return rows > kMaxRows || heads > kMaxHeads || max_len > (1 << 30) ||
            int64_t(rows) * heads * (int64_t(max_len) / 16 + 16) >= (int64_t(1) << 31);
 }
 

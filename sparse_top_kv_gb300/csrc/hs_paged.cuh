@@ -14,6 +14,7 @@
 namespace hs_paged {
 
 constexpr int kKey = 16;           // cached tokens per warp step
+constexpr int kMaxHeads = 65536;
 constexpr int kMaxRows = 4096;     // requests of one call (their plan sits in shared memory)
 constexpr int kMaxCtas = 1024;     // most CTAs of the attention kernel
 constexpr float kLog2e = 1.4426950408889634f;

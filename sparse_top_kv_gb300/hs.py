@@ -653,6 +653,21 @@ def _cache_strides(c, unit):
     return p * unit if np_ > 1 else 0, r * unit if nr > 1 else 0, h * unit if nh > 1 else 0
 
 
+def _check_i32(**values):
+    """Host integers that the C call takes as int32 (ctypes would wrap them)."""
+    for name, v in values.items():
+        if not -1 << 31 <= v < 1 << 31:
+            raise ValueError(f"{name}: {v} is out of range")
+
+
+def _used_on(stream, *tensors):
+    """Tensors made here and used on a stream other than the current one: the
+    allocator must not hand their memory out before that stream is done."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
 def _current_device(t, name):
     dev = t.get_device()
     if dev < 0 or dev != torch._C._cuda_getDevice():
@@ -662,6 +677,8 @@ def _current_device(t, name):
 
 def paged_decode_workspace_bytes(rows, heads, kv_heads, d, max_len, *, window=0, num_sinks=0,
                                  with_score=False):
+    _check_i32(rows=rows, heads=heads, kv_heads=kv_heads, d=d, max_len=max_len, window=window,
+               num_sinks=num_sinks)
     return int(lib().hs_paged_decode_workspace_bytes(rows, heads, kv_heads, d, max_len, window,
                                                      num_sinks, 1 if with_score else 0))
 
@@ -727,6 +744,7 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, *, window=0,
             max_len = min(max_len, score.shape[1])
     if not 0 <= max_len < 1 << 31:
         raise ValueError("max_len: 0 to 2^31 - 1")
+    _check_i32(window=window, num_sinks=num_sinks)
     score_ptr, score_stride, k_scale_ptr, v_scale_ptr = None, 0, None, None
     if score is not None:
         score_ptr, score_stride = _matrix(score, _F, "score", dev, rows, max_len)
@@ -736,11 +754,13 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, *, window=0,
         v_scale_ptr = _vector(v_scale, _F, "v_scale", dev, kv_heads)
     if out is None:
         out = torch.empty(rows, heads, d, dtype=qt, device=q.device)
+        _used_on(stream, out)
     elif (out.dtype is not qt or out.get_device() != dev or out.shape != qshape
           or not out.is_contiguous()):
         _output(out, qt, "out", dev, qshape)
     if lse is None:
         lse = torch.empty(rows, heads, dtype=_F, device=q.device)
+        _used_on(stream, lse)
     elif (lse.dtype is not _F or lse.get_device() != dev or lse.shape != (rows, heads)
           or not lse.is_contiguous()):
         _output(lse, _F, "lse", dev, (rows, heads))
@@ -770,13 +790,14 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, *, window=0,
         if n < 0:
             break
         workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+        _used_on(stream, workspace)
     if rc != HS_OK:
         raise HSError("hs_paged_decode", rc)
     return out, lse
 
 
 def _evict_args(score, seq_lens, budget, max_len, recent, num_sinks, positions, next_pos,
-                score_out, positions_out, lens_out, moves):
+                score_out, positions_out, lens_out, moves, stream):
     """Device, checked arguments of hs_evict_select, and what evict_select
     returns."""
     dev = _current_device(score, "score")
@@ -785,6 +806,7 @@ def _evict_args(score, seq_lens, budget, max_len, recent, num_sinks, positions, 
     rows, width = score.shape
     if max_len is None:
         max_len = width
+    _check_i32(max_len=max_len, budget=budget, recent=recent, num_sinks=num_sinks)
     score_ptr, score_stride = _matrix(score, _F, "score", dev, rows, max_len)
     pos_ptr, pos_stride = _matrix(positions, _I, "positions", dev, rows, max_len)
     lens_ptr = _vector(seq_lens, _I, "seq_lens", dev, rows)
@@ -806,6 +828,7 @@ def _evict_args(score, seq_lens, budget, max_len, recent, num_sinks, positions, 
         i32 = dict(dtype=_I, device=score.device)
         moves = (torch.empty(rows, cap, **i32), torch.empty(rows, cap, **i32),
                  torch.empty(rows, **i32))
+        _used_on(stream, *moves)
     src, dst, count = moves
     shape = src.shape
     if len(shape) != 2 or shape[0] != rows:
@@ -845,7 +868,7 @@ def evict_select(score, seq_lens, budget, *, max_len=None, recent=0, num_sinks=0
     [rows]))."""
     dev, args, result = _evict_args(score, seq_lens, budget, max_len, recent, num_sinks,
                                     positions, next_pos, score_out, positions_out, lens_out,
-                                    moves)
+                                    moves, stream)
     rc = lib().hs_evict_select(*args, _status_ptr(status), _raw_stream(dev, stream))
     if rc != HS_OK:
         raise HSError("hs_evict_select", rc)
@@ -887,7 +910,7 @@ def evict(score, seq_lens, budget, k_cache, v_cache, block_table, *, max_len=Non
                     seq_lens if lens_out is None else lens_out, moves)
     dev, args, result = _evict_args(score, seq_lens, budget, max_len, recent, num_sinks,
                                     positions, next_pos, score_out, positions_out, lens_out,
-                                    moves)
+                                    moves, stream)
     rc = lib().hs_evict(*args, *_move_args(k_cache, v_cache, block_table, score.shape[0], dev),
                         _status_ptr(status), _raw_stream(dev, stream))
     if rc != HS_OK:

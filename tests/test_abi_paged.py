@@ -95,3 +95,19 @@ def test_evict_checks(code, kw):
     a = {k: v for k, v in SELECT.items() if k not in ("status", "stream")}
     b = {k: v for k, v in MOVE.items() if k not in ("src", "dst", "count", "rows", "cap")}
     assert hs.lib().hs_evict(*{**a, **b, **kw}.values()) == code
+
+
+def test_paged_decode_head_limit():
+    kw = dict(heads=65537, kv_heads=1, ws=P, ws_bytes=1 << 60)
+    assert decode(**kw) == 3
+    assert hs.paged_decode_workspace_bytes(2, 65537, 1, 128, 64) == -1
+    assert hs.paged_decode_workspace_bytes(2, 65536, 1, 128, 64) > 0
+
+
+@pytest.mark.parametrize("kw", [dict(window=1 << 32), dict(num_sinks=1 << 31),
+                                dict(max_len=(1 << 32) + 5), dict(rows=-(1 << 31) - 1)])
+def test_sizes_past_32_bits_are_refused(kw):
+    """ctypes would wrap them around."""
+    with pytest.raises(ValueError):
+        hs.paged_decode_workspace_bytes(**{**dict(rows=2, heads=8, kv_heads=2, d=128,
+                                                  max_len=64), **kw})

@@ -370,3 +370,42 @@ def test_extension_and_general_path_agree(given, monkeypatch):
     with pytest.raises(hs.HSError):
         hs.evict(first.cuda(), lens, 0, k, v, table, moves=moves)
     assert taken[-1] == 1
+
+
+@pytest.mark.parametrize("kw", [dict(budget=(1 << 32) + 8), dict(recent=1 << 32),
+                                dict(num_sinks=1 << 31), dict(max_len=(1 << 32) + 16)])
+def test_sizes_past_32_bits_are_refused(kw):
+    score = torch.zeros(2, 64, device="cuda")
+    lens = torch.tensor([64, 3], dtype=torch.int32, device="cuda")
+    k, v = caches(8, 16, 2, 64, torch.bfloat16)
+    table = torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4)
+    kw = {**dict(budget=16), **kw}
+    budget = kw.pop("budget")
+    with pytest.raises(ValueError):
+        hs.evict(score, lens, budget, k, v, table, **kw)
+    with pytest.raises(ValueError):
+        hs.evict_select(score, lens, budget, **kw)
+
+
+def test_memory_of_a_call_on_another_stream():
+    """The move lists that a call makes for itself are not handed out again
+    while the other stream still works with them."""
+    R, W, B = 4, 256, 64
+    g = torch.Generator().manual_seed(9)
+    score, (k, v) = torch.rand(R, W, generator=g).cuda(), caches(R * 16, 16, 2, 64, torch.bfloat16)
+    table = torch.arange(R * 16, dtype=torch.int32, device="cuda").view(R, 16)
+    results = []
+    for stream in (None, torch.cuda.Stream()):
+        s, kc, vc = score.clone(), k.clone(), v.clone()
+        lens = torch.full((R,), W, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                torch.cuda._sleep(40_000_000)
+        hs.evict(s, lens, B, kc, vc, table, stream=stream)
+        junk = [torch.full((R, B), -1, dtype=torch.int32, device="cuda") for _ in range(6)]
+        torch.cuda.synchronize()
+        results.append((s, lens, kc, vc))
+        assert len(junk) == 6
+    for a, b in zip(*results):
+        assert same_bits(a, b)

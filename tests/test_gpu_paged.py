@@ -449,3 +449,33 @@ def test_extension_and_general_path_agree(kind, scored, monkeypatch):
                         k_scale=s["scales"][0], v_scale=s["scales"][1], out=out,
                         lse=torch.empty(4, 8, device="cuda"), workspace=ws)
     assert taken[-1] == 1
+
+
+@pytest.mark.parametrize("kw", [dict(window=1 << 32), dict(num_sinks=(1 << 32) + 4)])
+def test_sizes_past_32_bits_are_refused(kw):
+    s = make([20, 30], 8, 2, 64, 16)
+    with pytest.raises(ValueError):
+        hs.paged_decode(s["q"], s["k"], s["v"], s["table"], s["lens"], s["scale"], **kw)
+
+
+def test_memory_of_a_call_on_another_stream():
+    """The workspace that a call makes for itself is not handed out again while
+    the other stream still works with it."""
+    s = make([3000, 1, 777, 20000], 32, 8, 128, 16, seed=6)
+    args = (s["q"], s["k"], s["v"], s["table"], s["lens"], s["scale"])
+    want, want_lse = hs.paged_decode(*args)
+    n = hs.paged_decode_workspace_bytes(4, 32, 8, 128, s["table"].shape[1] * 16)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(40_000_000)
+    out, lse = hs.paged_decode(*args, stream=side)
+    junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse) and len(junk) == 3
+
+
+def test_largest_head_count():
+    # Shapes near the limit on heads: the grid of the finishing kernel.
+    s = make([40, 0], 65536, 8192, 64, 16)
+    run_and_check(s)
