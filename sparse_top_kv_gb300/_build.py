@@ -59,14 +59,21 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(compile_one, _sources()))
+        binding = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{res.stderr}")
     os.replace(tmp, LIB)
-    _build_binding()
+    if binding is not None:
+        tmp = BINDING + f".tmp{os.getpid()}"
+        _gcc("-shared", binding, "-o", tmp, "-L" + OUT_DIR, "-l:libhs.so",
+             "-L" + os.path.join(_torch(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+             "-Wl,-rpath,$ORIGIN")
+        os.replace(tmp, BINDING)
     return LIB
 
 
@@ -76,18 +83,26 @@ def _python_include():
     return inc if os.path.exists(os.path.join(inc, "Python.h")) and shutil.which("g++") else None
 
 
-def _build_binding():
-    inc = _python_include()
-    if inc is None:
-        return
-    tmp = BINDING + f".tmp{os.getpid()}"
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I" + inc, "-I" + INCLUDE,
-           os.path.join(CSRC, "hs_binding.cpp"), "-o", tmp, "-L" + OUT_DIR, "-l:libhs.so",
-           "-Wl,-rpath,$ORIGIN"]
-    res = subprocess.run(cmd, capture_output=True, text=True)
+def _torch():
+    import torch
+    return os.path.dirname(torch.__file__)
+
+
+def _gcc(*args):
+    res = subprocess.run(["g++", *args], capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"g++ failed on hs_binding.cpp:\n{res.stderr}")
-    os.replace(tmp, BINDING)
+
+
+def _compile_binding():
+    inc = _python_include()
+    if inc is None:
+        return None
+    obj = os.path.join(OUT_DIR, "hs_binding.o")
+    _gcc("-O2", "-std=c++17", "-fPIC", "-I" + inc, "-I" + INCLUDE,
+         "-I" + os.path.join(_torch(), "include"), "-c", os.path.join(CSRC, "hs_binding.cpp"),
+         "-o", obj)
+    return obj
 
 
 if __name__ == "__main__":

@@ -1,18 +1,18 @@
 // hs_binding.cpp -- the usual calls of the paged-cache entry points from
 // Python without the interpreter in between: a decode step's kernel runs for
 // ten microseconds, and checking and converting thirty arguments in Python and
-// ctypes took as long again (13.4 us a call of hs_paged_decode, 9.0 here;
-// hs_evict 14.2 and 7.9).
+// ctypes took as long again (13.4 us a call of hs_paged_decode, 5.5 here;
+// hs_evict 14.2 and 3.7).
 //
-// Each function looks at its tensors through their Python attributes (no torch
-// headers) and makes the C call if everything is as in the common case: right
-// types and shapes, contiguous, on the given device.  Where anything is not, it
-// returns None without having done anything, and hs.py goes through its own
-// checks, which say what is wrong or take the general way (strided tensors, a
-// workspace to allocate).
+// Each function looks at its tensors and makes the C call if everything is as
+// in the common case: right types and shapes, contiguous, on the given device.
+// Where anything is not, it returns None without having done anything, and
+// hs.py goes through its own checks, which say what is wrong or take the
+// general way (strided tensors, a workspace to allocate).
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <stdint.h>
+#include <torch/csrc/autograd/python_variable.h>
 
 #include <initializer_list>
 
@@ -20,15 +20,14 @@
 
 namespace {
 
-PyObject *s_dtype, *s_shape, *s_get_device, *s_is_contiguous, *s_data_ptr, *s_nbytes;
-PyObject *t_bf16, *t_fp16, *t_e4m3, *t_f32, *t_i32;  // torch dtypes
-
-// One tensor's facts; `ok` false where an attribute is missing (no tensor).
+// One tensor's facts; `ok` only for a contiguous CUDA tensor on the device asked
+// for, with at most four dimensions.
 struct Tensor {
-    PyObject* dtype = nullptr;  // borrowed from the dtype singletons
+    at::ScalarType dtype = at::ScalarType::Undefined;
     int64_t dim[4] = {0, 0, 0, 0};
     int ndim = 0;
     void* ptr = nullptr;
+    int64_t bytes = 0;
     bool ok = false;
 };
 
@@ -55,44 +54,28 @@ bool as_float(PyObject* o, float* out) {
     return true;
 }
 
-// Contiguous tensor on `device` with at most four dimensions.
-Tensor look(PyObject* t, int64_t device) {
+Tensor look(PyObject* o, int64_t device) {
     Tensor x;
-    if (PyErr_Occurred()) return x;  // an earlier look failed: on to general()
-    PyObject* o = PyObject_GetAttr(t, s_dtype);
-    if (o == nullptr) return x;
-    x.dtype = o;  // a singleton that outlives the call
-    Py_DECREF(o);
-    o = PyObject_GetAttr(t, s_shape);
-    if (o == nullptr) return x;
-    bool good = PyTuple_Check(o) && PyTuple_GET_SIZE(o) <= 4;
-    if (good) {
-        x.ndim = int(PyTuple_GET_SIZE(o));
-        for (int i = 0; i < x.ndim && good; ++i) good = as_int(PyTuple_GET_ITEM(o, i), &x.dim[i]);
+    if (!THPVariable_Check(o)) return x;
+    try {
+        const at::Tensor& t = THPVariable_Unpack(o);
+        if (!t.is_cuda() || t.get_device() != device || t.dim() > 4 || !t.is_contiguous())
+            return x;
+        x.dtype = t.scalar_type();
+        x.ndim = int(t.dim());
+        for (int i = 0; i < x.ndim; ++i) x.dim[i] = t.size(i);
+        x.ptr = t.data_ptr();
+        x.bytes = int64_t(t.nbytes());
+        x.ok = true;
+    } catch (const std::exception&) {  // no storage of its own, symbolic sizes
     }
-    Py_DECREF(o);
-    if (!good) return x;
-    o = PyObject_CallMethodNoArgs(t, s_get_device);
-    int64_t v = -1;
-    good = as_int(o, &v) && v == device;
-    Py_XDECREF(o);
-    if (!good) return x;
-    o = PyObject_CallMethodNoArgs(t, s_is_contiguous);
-    good = o == Py_True;
-    Py_XDECREF(o);
-    if (!good) return x;
-    o = PyObject_CallMethodNoArgs(t, s_data_ptr);
-    if (o == nullptr) return x;
-    x.ptr = PyLong_AsVoidPtr(o);
-    Py_DECREF(o);
-    x.ok = !PyErr_Occurred();
     return x;
 }
 
-bool vector(const Tensor& t, PyObject* dtype, int64_t n) {
+bool vector(const Tensor& t, at::ScalarType dtype, int64_t n) {
     return t.ok && t.dtype == dtype && t.ndim == 1 && t.dim[0] == n;
 }
-bool matrix(const Tensor& t, PyObject* dtype, int64_t rows, int64_t cols) {
+bool matrix(const Tensor& t, at::ScalarType dtype, int64_t rows, int64_t cols) {
     return t.ok && t.dtype == dtype && t.ndim == 2 && t.dim[0] == rows && t.dim[1] >= cols;
 }
 bool same_shape(const Tensor& a, const Tensor& b) {
@@ -108,8 +91,8 @@ PyObject* general() {
     Py_RETURN_NONE;
 }
 
-int element(PyObject* dtype) {
-    return dtype == t_bf16 ? HS_BF16 : dtype == t_fp16 ? HS_FP16 : dtype == t_e4m3 ? HS_E4M3 : -1;
+int element(at::ScalarType dtype) {
+    return dtype == at::kBFloat16 ? HS_BF16 : dtype == at::kHalf ? HS_FP16 : dtype == at::kFloat8_e4m3fn ? HS_E4M3 : -1;
 }
 
 // paged_decode(device, stream, q, k_cache, v_cache, block_table, seq_lens,
@@ -135,8 +118,8 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
             if (t->dim[i] > INT32_MAX) return general();
     const int64_t rows = q.dim[0], heads = q.dim[1], d = q.dim[2];
     const int64_t pages = k.dim[0], page = k.dim[1], kvh = k.dim[2];
-    if (!matrix(table, t_i32, rows, 0) || !vector(lens, t_i32, rows) || !out.ok ||
-        out.dtype != q.dtype || !same_shape(out, q) || !matrix(lse, t_f32, rows, heads) ||
+    if (!matrix(table, at::kInt, rows, 0) || !vector(lens, at::kInt, rows) || !out.ok ||
+        out.dtype != q.dtype || !same_shape(out, q) || !matrix(lse, at::kFloat, rows, heads) ||
         lse.dim[1] != heads || !ws.ok)
         return general();
     const int64_t blocks = table.dim[1];
@@ -144,7 +127,7 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Tensor score, ks, vs;
     if (a[13] != Py_None) {
         score = look(a[13], device);
-        if (!matrix(score, t_f32, rows, 0)) return general();
+        if (!matrix(score, at::kFloat, rows, 0)) return general();
         if (score.dim[1] < max_len) max_len = score.dim[1];
     }
     if (a[10] != Py_None && !as_int(a[10], &max_len)) return general();
@@ -152,23 +135,18 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
         return general();
     if (a[11] != Py_None) {
         ks = look(a[11], device);
-        if (!vector(ks, t_f32, kvh)) return general();
+        if (!vector(ks, at::kFloat, kvh)) return general();
     }
     if (a[12] != Py_None) {
         vs = look(a[12], device);
-        if (!vector(vs, t_f32, kvh)) return general();
+        if (!vector(vs, at::kFloat, kvh)) return general();
     }
     void* status = nullptr;
     if (a[18] != Py_None) {
         const Tensor s = look(a[18], device);
-        if (!s.ok || s.dtype != t_i32) return general();
+        if (!s.ok || s.dtype != at::kInt) return general();
         status = s.ptr;
     }
-    PyObject* o = PyObject_GetAttr(a[17], s_nbytes);
-    int64_t ws_bytes = 0;
-    const bool good = as_int(o, &ws_bytes);
-    Py_XDECREF(o);
-    if (!good) return general();
     const int rc = hs_paged_decode(
         q.ptr, heads * d, qe, k.ptr, v.ptr, ke, pages > 1 ? page * kvh * d : 0,
         page > 1 ? kvh * d : 0, kvh > 1 ? d : 0, int32_t(pages), int32_t(page),
@@ -176,7 +154,7 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
         static_cast<const int32_t*>(lens.ptr), static_cast<const float*>(ks.ptr),
         static_cast<const float*>(vs.ptr), int32_t(rows), int32_t(heads), int32_t(kvh), int32_t(d),
         window, sinks, scale, static_cast<float*>(score.ptr), score.ok ? score.dim[1] : 0, decay,
-        out.ptr, static_cast<float*>(lse.ptr), ws.ptr, ws_bytes, static_cast<int32_t*>(status),
+        out.ptr, static_cast<float*>(lse.ptr), ws.ptr, ws.bytes, static_cast<int32_t*>(status),
         reinterpret_cast<hs_stream_t>(stream));
     if (rc == HS_ERR_CAPACITY) return general();  // a larger workspace is wanted
     return PyLong_FromLong(rc);
@@ -194,42 +172,42 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
         !PyTuple_CheckExact(a[16]) || PyTuple_GET_SIZE(a[16]) != 3)
         return general();
     const Tensor score = look(a[2], device), lens = look(a[3], device);
-    if (!score.ok || score.ndim != 2 || score.dtype != t_f32 || score.dim[0] > INT32_MAX ||
+    if (!score.ok || score.ndim != 2 || score.dtype != at::kFloat || score.dim[0] > INT32_MAX ||
         score.dim[1] > INT32_MAX)
         return general();
     const int64_t rows = score.dim[0];
     max_len = score.dim[1];
     if (a[8] != Py_None && !as_int(a[8], &max_len)) return general();
-    if (max_len < 0 || max_len > score.dim[1] || !vector(lens, t_i32, rows)) return general();
+    if (max_len < 0 || max_len > score.dim[1] || !vector(lens, at::kInt, rows)) return general();
     Tensor pos, next, so = score, po, lo = lens;
     if (a[11] != Py_None) {
         pos = look(a[11], device);
-        if (!matrix(pos, t_i32, rows, max_len)) return general();
+        if (!matrix(pos, at::kInt, rows, max_len)) return general();
     }
     po = pos;
     if (a[12] != Py_None) {
         next = look(a[12], device);
-        if (!vector(next, t_i32, rows)) return general();
+        if (!vector(next, at::kInt, rows)) return general();
     }
     if (a[13] != Py_None) {
         so = look(a[13], device);
-        if (!matrix(so, t_f32, rows, max_len)) return general();
+        if (!matrix(so, at::kFloat, rows, max_len)) return general();
     }
     if (a[14] != Py_None) {
         po = look(a[14], device);
-        if (!matrix(po, t_i32, rows, max_len)) return general();
+        if (!matrix(po, at::kInt, rows, max_len)) return general();
     }
     if (a[15] != Py_None) {
         lo = look(a[15], device);
-        if (!vector(lo, t_i32, rows)) return general();
+        if (!vector(lo, at::kInt, rows)) return general();
     }
     const Tensor src = look(PyTuple_GET_ITEM(a[16], 0), device);
     const Tensor dst = look(PyTuple_GET_ITEM(a[16], 1), device);
     const Tensor count = look(PyTuple_GET_ITEM(a[16], 2), device);
     const Tensor k = look(a[5], device), table = look(a[7], device);
-    if (!matrix(src, t_i32, rows, 0) || src.dim[1] > INT32_MAX || !matrix(dst, t_i32, rows, 0) ||
-        dst.dim[1] != src.dim[1] || !vector(count, t_i32, rows) || !k.ok || k.ndim != 4 ||
-        !matrix(table, t_i32, rows, 0))
+    if (!matrix(src, at::kInt, rows, 0) || src.dim[1] > INT32_MAX || !matrix(dst, at::kInt, rows, 0) ||
+        dst.dim[1] != src.dim[1] || !vector(count, at::kInt, rows) || !k.ok || k.ndim != 4 ||
+        !matrix(table, at::kInt, rows, 0))
         return general();
     Tensor v;
     if (a[6] != Py_None) {
@@ -238,7 +216,7 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     int64_t e;
     if (element(k.dtype) >= 0) {
-        e = k.dtype == t_e4m3 ? 1 : 2;
+        e = k.dtype == at::kFloat8_e4m3fn ? 1 : 2;
     } else {
         return general();
     }
@@ -249,7 +227,7 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* status = nullptr;
     if (a[17] != Py_None) {
         const Tensor s = look(a[17], device);
-        if (!s.ok || s.dtype != t_i32) return general();
+        if (!s.ok || s.dtype != at::kInt) return general();
         status = s.ptr;
     }
     const int rc = hs_evict(
@@ -266,20 +244,6 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return PyLong_FromLong(rc);
 }
 
-// setup(bfloat16, float16, float8_e4m3fn, float32, int32): torch's dtypes.
-PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (n != 5) {
-        PyErr_SetString(PyExc_TypeError, "setup: five dtypes");
-        return nullptr;
-    }
-    PyObject** to[5] = {&t_bf16, &t_fp16, &t_e4m3, &t_f32, &t_i32};
-    for (int i = 0; i < 5; ++i) {
-        Py_INCREF(a[i]);
-        *to[i] = a[i];
-    }
-    Py_RETURN_NONE;
-}
-
 template <typename F>
 PyCFunction fast(F f) {
     return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
@@ -287,19 +251,10 @@ PyCFunction fast(F f) {
 
 PyMethodDef methods[] = {{"paged_decode", fast(paged_decode), METH_FASTCALL, nullptr},
                          {"evict", fast(evict), METH_FASTCALL, nullptr},
-                         {"setup", fast(setup), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_hs_binding", nullptr, -1, methods,
                       nullptr,               nullptr,       nullptr, nullptr};
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__hs_binding() {
-    s_dtype = PyUnicode_InternFromString("dtype");
-    s_shape = PyUnicode_InternFromString("shape");
-    s_get_device = PyUnicode_InternFromString("get_device");
-    s_is_contiguous = PyUnicode_InternFromString("is_contiguous");
-    s_data_ptr = PyUnicode_InternFromString("data_ptr");
-    s_nbytes = PyUnicode_InternFromString("nbytes");
-    return PyModule_Create(&module);
-}
+PyMODINIT_FUNC PyInit__hs_binding() { return PyModule_Create(&module); }

@@ -117,7 +117,6 @@ def _load_binding():
     mod = importlib.util.module_from_spec(
         importlib.util.spec_from_loader("_hs_binding", loader))
     loader.exec_module(mod)
-    mod.setup(torch.bfloat16, torch.float16, torch.float8_e4m3fn, torch.float32, torch.int32)
     _binding = mod
 
 
