@@ -530,7 +530,8 @@ int hs_sparse_decode_fp8ds(const void* q, const void* kv8, int64_t row_bytes,
  * seq_lens    int32 [rows]: tokens T of the request, the new one included.
  *             T <= 0: an unused slot (out = 0, lse = -inf).
  * max_len     host-side bound on T, <= max_blocks * page_size (it sizes the
- *             workspace); a longer request is attended up to max_len and
+ *             workspace, and a tight one lets small calls take a shorter way,
+ *             so that results may differ in their last bits); a longer request is attended up to max_len and
  *             reported as HS_ERR_BAD_INDEX in *status.
  * k_scale, v_scale  fp32 [kv_heads] or NULL (= 1); HS_E4M3 only.
  * window      > 0: only positions [max(0, T - window), T) and the first

@@ -85,6 +85,7 @@ __device__ __forceinline__ RowPlan row_plan(const PagedArgs& a, int row) {
     constexpr uint32_t kAll = 0xffffffffu;
     const int lane = threadIdx.x & 31;
     int n0 = 0, n1 = 0, b0 = 0, b1 = 0, own0 = 0, own1 = 0;
+    if (a.cl > 0) return RowPlan{};  // nothing to merge
 #pragma unroll 4
     for (int r = lane; r < a.rows; r += 32) {
         const int len = a.seq_lens[r];
@@ -118,6 +119,7 @@ struct Parts {
     __device__ __forceinline__ int64_t at(int p) const { return p == 0 ? first : rest + p * step; }
 };
 __device__ __forceinline__ Parts parts_of(const PagedArgs& a, const RowPlan& r, int h) {
+    if (a.cl > 0) return Parts{1, 0, 0, 0};
     // hs and gm are powers of two.
     const int lhs = 31 - __clz(a.hs[r.way]), lgm = 31 - __clz(a.gm);
     const int group = a.group, gch = (group + a.gm - 1) >> lgm;
@@ -314,7 +316,7 @@ __device__ __forceinline__ void score_tokens(const PagedArgs& a, const RowPlan& 
     const int nvis = vis.T - vis.w0 + vis.sc;
     float* score = a.score + int64_t(row) * a.score_stride;
     Parts ahead{};  // of this thread's first head
-    if (tid / kLanes < a.heads && plan.row_tiles > 0) ahead = parts_of(a, plan, tid / kLanes);
+    if (tid / kLanes < a.heads && (plan.row_tiles > 0 || a.cl > 0)) ahead = parts_of(a, plan, tid / kLanes);
     hs::pdl_wait();
     for (int64_t i0 = int64_t(part) * kMergeThreads; i0 < nvis;
          i0 += int64_t(blocks) * kMergeThreads) {
@@ -544,7 +546,7 @@ extern "C" int hs_paged_decode(const void* q, int64_t q_stride, int32_t q_dtype,
     } else if (kv_dtype == HS_BF16) rc = launch_bf16(a, d, group, stream);
     else if (kv_dtype == HS_FP16) rc = launch_fp16(a, d, group, stream);
     else rc = launch_e4m3(a, d, group, stream);
-    if (rc != HS_OK) return rc;
+    if (rc != HS_OK || (a.cl > 0 && score == nullptr)) return rc;
     // Merging: about half as many warps to a head as its unit has parts (one
     // context over all SMs has 152), within a few blocks an SM.  The kernel
     // chose between the two ways by the lengths; here their bound decides.
@@ -559,7 +561,7 @@ extern "C" int hs_paged_decode(const void* q, int64_t q_stride, int32_t q_dtype,
     while (wp < kMergeWarps && 2 * wp <= parts &&
            int64_t(rows) * heads * 2 * wp <= 4 * int64_t(w.ctas) * kMergeWarps)
         wp *= 2;
-    const int merges = (heads * wp + kMergeWarps - 1) / kMergeWarps;
+    const int merges = a.cl > 0 ? 0 : (heads * wp + kMergeWarps - 1) / kMergeWarps;
     const int64_t steps = (int64_t(max_len) + kMergeThreads - 1) / kMergeThreads;
     const int scores =
         score == nullptr ? 0

@@ -42,6 +42,7 @@ struct PagedArgs {
     // The two ways to cut the call (below).
     int32_t hs[2], lth[2], chunks[2], gm, extra;
     int64_t wide_from, wide_to;  // places (way 0) between which way 0 is taken
+    int32_t cl;  // > 0: a cluster of cl CTAs per unit (way 1) in place of the deal of tiles
     // Workspace.
     float* lse2;        // [rows, heads] log2 units (scored calls)
     float* part_ml;     // [2 * ctas][unit heads][2]
@@ -60,9 +61,11 @@ struct PagedArgs {
 // long context uses all of them.  Starting and ending a unit takes as long as
 // a few tiles; each unit has that many places without work (`extra`) ahead of
 // its tiles, so that a run of many short units holds fewer tiles (64 ragged
-// E4M3 requests: the slowest CTA 85 us, 95 without).  There are two ways: units of as many heads
-// as a tile holds (way 0: long DRAM pieces), or of one (way 1: small calls,
+// E4M3 requests: the slowest CTA 85 us, 95 without).  There are two ways: units
+// of as many heads as a tile holds (way 0: long DRAM pieces), or of one (way 1: small calls,
 // fewer parts to merge); the kernels take one by the tiles that they find.
+// Calls that are surely small are not dealt: each unit has a cluster of CTAs
+// to itself, which join their parts through distributed shared memory.
 
 // Token tiles of a request: those of the sinks, then those of the window,
 // both on the grid of 2^lth tokens.  Attended are the first sc tokens and
@@ -240,6 +243,18 @@ __device__ __forceinline__ Run make_run(const PagedArgs& a, int cta) {
     x.run = before1 - before0;
     return x;
 }
+// The run of a CTA that shares its unit with the other CTAs of its cluster.
+__device__ __forceinline__ Run unit_run(const PagedArgs& a, int unit, int rank) {
+    Run x;
+    x.way = 1;
+    x.chunks = a.chunks[1];
+    x.row = unit / x.chunks;
+    x.chunk = unit - x.row * x.chunks;
+    const int n = tiling_of(a, __ldg(a.seq_lens + x.row), a.lth[1]).n;
+    x.tile = n * rank / a.cl;
+    x.run = n * (rank + 1) / a.cl - x.tile;
+    return x;
+}
 // A length past max_len is reported once.
 __device__ __forceinline__ void report_lengths(const PagedArgs& a) {
     for (int r = threadIdx.x; r < a.rows; r += blockDim.x)
@@ -273,6 +288,15 @@ inline void set_ways(PagedArgs& a, int hs_max, int tile_rows, int gm, int tiles_
     a.extra = extra;
     a.wide_from = int64_t(a.ctas) * tiles_for_wide;
     a.wide_to = INT64_MAX;
+}
+
+// Host: at most this many tiles in one unit of way `way`, by the bound on the
+// lengths.
+inline int64_t most_tiles(const PagedArgs& a, int way) {
+    const int64_t up = (int64_t(1) << a.lth[way]) - 1;
+    const int64_t all = (a.max_len + up) >> a.lth[way];
+    if (a.window == 0) return all;
+    return hs::min64(all, ((a.sinks + up) >> a.lth[way]) + ((a.window + up) >> a.lth[way]) + 1);
 }
 
 // Host: at most this many places in way `way`, by the bound on the lengths.

@@ -65,7 +65,8 @@ constexpr int kMaskRing = 16;        // tiles whose loaded runs are remembered
 constexpr float kThresh = 8.f;       // log2 headroom before O is rescaled
 constexpr int kTmemCols = 512;
 constexpr int kBarBytes = 8192;      // shared-memory budget of Bars
-// Places per CTA from which units take several heads.  32/8 heads of 128, bf16,
+// Places per CTA from which the units of a deal take several heads (the
+// shorter calls here are dealt where their bound on the lengths is long).  32/8 heads of 128, bf16,
 // us with all heads / one head to a unit: one request of 1 K tokens 10.8 / 10.8,
 // 4 K 14.2 / 12.8, 16 K 18.1 / 20.0, eight of 1 K 14.6 / 16.8, of 2 K 17.1 /
 // 21.7, 32 of 512 17.9 / 23.3.
@@ -77,6 +78,22 @@ constexpr int kTilesForWide = 2;
 // E4M3 heads are 128-byte pieces: never (64 requests of up to 8 K 88 / 122).
 constexpr int kWideAlone = 2;        // requests x chunks of heads
 constexpr int kTilesAlone = 12;      // places per CTA
+
+constexpr int kMaxCluster = 8;  // the largest portable cluster
+constexpr int kMaxUnit = 64;    // queries of a unit
+
+__device__ __forceinline__ float2 peer_load2(uint32_t addr, int rank) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                 : "=f"(v.x), "=f"(v.y)
+                 : "r"(hs::pair::mapa(addr, uint32_t(rank)))
+                 : "memory");
+    return v;
+}
+
+// Tiles of a CTA whose cluster takes a unit, at most, and their bytes.
+constexpr int kTilesOfUnit = 8;
+constexpr int kUnitBytes = 512 * 1024;
 
 struct TcArgs {
     PagedArgs p;
@@ -124,6 +141,7 @@ struct Cfg {
     static constexpr int kQOff = kVOff + NS * kSub;
     static constexpr int kPOff = kQOff + kQBufs * kQBytes;
     static constexpr int kBarOff = kPOff + 2 * kPBytes;
+    static_assert(kHsMax * GM <= kMaxUnit && kHsMax * GM * D * 4 <= kQOff, "a cluster's parts");
 };
 
 struct Bars {
@@ -132,6 +150,7 @@ struct Bars {
     uint64_t q_full[2], q_empty, o_free, drain[2];
     uint32_t tmem_base;
     volatile int32_t abort;
+    float2 join_ml[kMaxUnit];           // [head, query] the cluster's CTAs read each other's
     uint32_t loaded[kMaskRing];         // runs of a tile that were loaded
     alignas(16) float red[kGroups][8][16];  // per 16 rows: maxima or sums
     float alpha[kGroups][8][16];        // rescale factors, [head][query]
@@ -369,7 +388,8 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
     const int group = a.heads / a.kv_heads;
     const int gch = (group + GM - 1) / GM;
     const int cta = blockIdx.x;
-    const Run rn = make_run(a, cta);
+    const int cl = a.cl, rank = cl > 1 ? int(hs::pair::cta_rank()) : 0;
+    const Run rn = cl > 0 ? unit_run(a, cl > 1 ? cta / cl : cta, rank) : make_run(a, cta);
     const int way = rn.way, chunks = rn.chunks, run = rn.run;
     const Cursor start = cursor_at(a, rn);
     if (cta == 0) report_lengths(a);
@@ -685,7 +705,7 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
             const int Gc = min(GM, group - gc * GM);
             const Tiling v = c.v;
             const int tile0 = c.tile, n = min(c.left, v.n - tile0), t0 = t;
-            const bool whole = n == v.n;
+            const bool whole = n == v.n && cl <= 1;
             if (E4 && c.left > n) {
                 Cursor x = c;
                 next_segment(x, a, chunks, lth);
@@ -916,6 +936,8 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
                         if (a.lse2 != nullptr) a.lse2[qh] = lg;
                         inv = L == 0.f ? 0.f : 1.f / L;
                         if (a.v_scale != nullptr && L != 0.f) inv *= __ldg(a.v_scale + kvh0 + h);
+                    } else if (cl > 0) {
+                        B.join_ml[h * GM + i] = make_float2(M, L);
                     } else {
                         const int64_t k = int64_t(slot) * a.unit_heads_max + e;
                         a.part_ml[2 * k] = M;
@@ -926,6 +948,8 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
                 B.weight[1][h][i] = f1 * inv;
             }
             hs::pair::named_sync(kBothBar, kGroups * kSoftThreads);
+            // A CTA of a cluster has one segment: its rings are free by now.
+            float* joined = reinterpret_cast<float*>(smem);
             // A segment of one tile leaves the other group's output unwritten.
             const bool has0 = n > 1 || (t0 & 1) == 0, has1 = n > 1 || (t0 & 1) == 1;
             const bool bf = KV == kBf16 || (E4 && !a.q_is_half);
@@ -959,7 +983,9 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
 #pragma unroll
                 for (int i = 0; i < GM; ++i) {
                     if (i >= Gc) break;
-                    if (!whole)
+                    if (cl > 1)
+                        joined[(h * GM + i) * D + d] = O[i];
+                    else if (!whole)
                         a.part_o[at + i * D] = O[i];
                     else if (bf)
                         static_cast<__nv_bfloat16*>(a.out)[at + i * D] = __float2bfloat16_rn(O[i]);
@@ -978,11 +1004,126 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
     __syncthreads();
     hs::tc::fence_after_sync();
     if (warp == kPvWarp) hs::tc::tmem_dealloc(tmem, kTmemCols);
+    if (cl > 1 || (cl == 1 && run == 0)) {
+        // The cluster joins its parts, each CTA some pairs of dims; a request
+        // without a token has none: zeros.
+        if (cl > 1) hs::pair::cluster_sync();
+        const int kvh0 = start.chunk / gch * hsn, gc = start.chunk % gch, tiles = start.v.n;
+        const int Gc = min(GM, group - gc * GM);
+        const int64_t qh0 = int64_t(start.row) * a.heads + kvh0 * group + gc * GM;
+        const int pairs = hsn * Gc * (D / 2), share = (pairs + cl - 1) / cl;
+        const int end = min(pairs, (rank + 1) * share);
+        const uint32_t ml_at = hs::smem_u32(B.join_ml), o_at = hs::smem_u32(smem);
+        for (int p = rank * share + tid; p < end; p += kThreads) {
+            const int d = p % (D / 2) * 2, h = p / (D / 2) / Gc, i = p / (D / 2) - h * Gc;
+            const int e = h * GM + i;
+            float2 ml[kMaxCluster], o[kMaxCluster];
+#pragma unroll
+            for (int c = 0; c < kMaxCluster; ++c) {
+                ml[c] = make_float2(-CUDART_INF_F, 0.f);
+                o[c] = make_float2(0.f, 0.f);
+                // (CTAs without a tile have written nothing.)
+                if (c < cl && tiles * (c + 1) / cl > tiles * c / cl) {
+                    ml[c] = peer_load2(ml_at + e * 8, c);
+                    o[c] = peer_load2(o_at + (e * D + d) * 4, c);
+                }
+            }
+            float M = -CUDART_INF_F, L = 0.f;
+#pragma unroll
+            for (int c = 0; c < kMaxCluster; ++c) M = fmaxf(M, ml[c].x);
+            const float ref = M == -CUDART_INF_F ? 0.f : M;
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int c = 0; c < kMaxCluster; ++c) {
+                const float f = exp2f(ml[c].x - ref);
+                L = fmaf(f, ml[c].y, L);
+                sum.x = fmaf(f, o[c].x, sum.x);
+                sum.y = fmaf(f, o[c].y, sum.y);
+            }
+            float inv = L == 0.f ? 0.f : 1.f / L;
+            if (a.v_scale != nullptr && L != 0.f) inv *= __ldg(a.v_scale + kvh0 + h);
+            const int64_t qh = qh0 + h * group + i;
+            sum.x *= inv;
+            sum.y *= inv;
+            if (KV == kBf16 || (E4 && !a.q_is_half))
+                reinterpret_cast<__nv_bfloat162*>(a.out)[(qh * D + d) / 2] =
+                    __floats2bfloat162_rn(sum.x, sum.y);
+            else
+                reinterpret_cast<__half2*>(a.out)[(qh * D + d) / 2] =
+                    __floats2half2_rn(sum.x, sum.y);
+            if (d == 0) {
+                const float lg = L == 0.f ? -CUDART_INF_F : M + log2f(L);
+                if (a.lse != nullptr) a.lse[qh] = lg * kLn2;
+                if (a.lse2 != nullptr) a.lse2[qh] = lg;
+            }
+        }
+        if (cl > 1) hs::pair::cluster_sync();  // no CTA ends while its parts are read
+    }
 }
 
 // Tensor map of a cache: dims (head dim, token of the page, KV head, page).
 int encode_map(CUtensorMap* m, int kv, const void* base, const PagedArgs& a, int d, int bt,
                int hs_box);
+
+inline cudaLaunchConfig_t cluster_config(cudaLaunchAttribute (&attr)[2], int units, int cl,
+                                         size_t smem) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(cl);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(units) * unsigned(cl));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cfg;
+}
+
+// Sets a.cl, and returns the way whose units clusters take (1 where none do).
+// Clusters take the units where all of them fit the GPU at once and the bound
+// on the lengths leaves each CTA few tiles; then nothing is dealt, merged or
+// launched behind (us, dealt / by clusters: one request of 128 tokens 8.1 /
+// 6.2, 1 K 10.7 / 8.8, 4 K 13.9 / 11.6, 8 K 19.1 / 14.9; 16 requests of 128
+// 11.0 / 7.9, of 1 K 22.9 / 18.2; 64 of 64 16.3 / 10.3; 16 with a window of
+// 256 14.0 / 9.4).  With more tiles a ragged batch would wait for its longest
+// request (24 of up to 5001 tokens and 256-wide heads: 38.3 / 33.5 where all
+// are that long, but 21.7 dealt where they are half of it on average).
+inline int cluster_way(PagedArgs& a, const void* kern, size_t smem, int tile_bytes,
+                       int (&resident)[64][kMaxCluster + 1]) {
+    int dev = 0;
+    a.cl = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+    const int64_t few = hs::min64(kTilesOfUnit, kUnitBytes / tile_bytes);
+    for (int way = 1; way >= 0 && a.cl == 0; --way) {
+        const int64_t units = int64_t(a.rows) * a.chunks[way], tiles = most_tiles(a, way);
+        if (units > a.ctas || tiles > few * kMaxCluster) continue;
+        int64_t best = INT64_MAX;
+        for (int cl = 1; cl <= kMaxCluster && units * cl <= a.ctas; ++cl) {
+            // In halves of a tile's time: a join takes as long as 2.5 tiles,
+            // or 4.5 where the unit has several heads.
+            const int64_t each = hs::max64(1, (tiles + cl - 1) / cl);
+            const int64_t cost = 2 * each + (cl == 1 ? 0 : a.hs[way] == 1 ? 5 : 9);
+            if (each > few || cost >= best) continue;
+            int& fit = resident[dev][cl];
+            if (cl > 1 && fit == 0) {
+                cudaLaunchAttribute attr[2];
+                const cudaLaunchConfig_t cfg = cluster_config(attr, 1, cl, smem);
+                if (cudaOccupancyMaxActiveClusters(&fit, kern, &cfg) != cudaSuccess || fit < 1) {
+                    cudaGetLastError();
+                    fit = -1;
+                }
+            }
+            if (cl > 1 && units > fit) continue;
+            best = cost;
+            a.cl = cl;
+        }
+        if (a.cl > 0) return way;
+    }
+    return 1;
+}
 
 template <int KV, int D, int GH, int QP>
 int launch_one(PagedArgs& a, hs_stream_t stream) {
@@ -998,33 +1139,49 @@ int launch_one(PagedArgs& a, hs_stream_t stream) {
         t.split[i] = a.hs[i] > 1 && t.bt[i] < C::kStep;
     }
     t.timeout_ns = hs::kWaitTimeoutNs;
-    // Small calls surely take way 1: two descriptors instead of four.
-    const bool both = a.hs[0] != 1 && most_places(a) >= a.wide_from;
-    CUtensorMap m[4];
-    for (int i = both ? 0 : 1; i < 2; ++i) {
-        int rc = encode_map(&m[2 * i], KV, a.k, a, D, t.bt[i], t.split[i] ? 1 : a.hs[i]);
-        if (rc == HS_OK) rc = encode_map(&m[2 * i + 1], KV, a.v, a, D, t.bt[i], t.split[i] ? 1 : a.hs[i]);
-        if (rc != HS_OK) return rc;
-    }
-    if (!both) {
-        m[0] = m[2];
-        m[1] = m[3];
-        t.bt[0] = t.bt[1];
-        t.split[0] = t.split[1];
-        a.hs[0] = a.hs[1];
-        a.lth[0] = a.lth[1];
-        a.chunks[0] = a.chunks[1];
-    }
-    t.p = a;
     auto kern = paged_tc_kernel<KV, D, GH, QP>;
     constexpr size_t smem = size_t(C::kBarOff) + sizeof(Bars) + 1024;
     static_assert(smem <= 227 * 1024, "shared memory");
     static int smem_set[64] = {};
-    const int rc =
-        hs_host::ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem, smem_set);
+    int rc = hs_host::ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem, smem_set);
     if (rc != HS_OK) return rc;
-    return hs_host::launch_pdl(kern, dim3(a.ctas), dim3(kThreads), smem, stream, t, m[0], m[1],
-                               m[2], m[3]);
+    static int resident[64][kMaxCluster + 1] = {};
+    const int only = cluster_way(a, reinterpret_cast<const void*>(kern), smem,
+                                 2 * C::kSubs * C::kSub, resident);
+    // Small calls surely take one way: two descriptors instead of four.
+    const bool both = a.cl == 0 && a.hs[0] != 1 && most_places(a) >= a.wide_from;
+    CUtensorMap m[4];
+    for (int i = 0; i < 2; ++i) {
+        if (!both && i != only) continue;
+        rc = encode_map(&m[2 * i], KV, a.k, a, D, t.bt[i], t.split[i] ? 1 : a.hs[i]);
+        if (rc == HS_OK)
+            rc = encode_map(&m[2 * i + 1], KV, a.v, a, D, t.bt[i], t.split[i] ? 1 : a.hs[i]);
+        if (rc != HS_OK) return rc;
+    }
+    if (!both) {
+        const int other = 1 - only;
+        m[2 * other] = m[2 * only];
+        m[2 * other + 1] = m[2 * only + 1];
+        t.bt[other] = t.bt[only];
+        t.split[other] = t.split[only];
+        a.hs[other] = a.hs[only];
+        a.lth[other] = a.lth[only];
+        a.chunks[other] = a.chunks[only];
+    }
+    t.p = a;
+    if (a.cl <= 1) {
+        const int ctas = a.cl == 0 ? a.ctas : a.rows * a.chunks[1];
+        return hs_host::launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, stream, t, m[0], m[1],
+                                   m[2], m[3]);
+    }
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = cluster_config(attr, a.rows * a.chunks[1], a.cl, smem);
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    if (cudaLaunchKernelEx(&cfg, kern, t, m[0], m[1], m[2], m[3]) != cudaSuccess) {
+        cudaGetLastError();
+        return HS_ERR_CUDA;
+    }
+    return HS_OK;
 }
 
 template <int KV, int QP>

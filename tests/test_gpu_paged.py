@@ -479,3 +479,73 @@ def test_largest_head_count():
     # Shapes near the limit on heads: the grid of the finishing kernel.
     s = make([40, 0], 65536, 8192, 64, 16)
     run_and_check(s)
+
+
+def long_bound(s, tokens=20000):
+    """The same requests in a table that could hold `tokens` each: the bound on
+    the lengths decides how a call is cut."""
+    page = s["k"].shape[1]
+    pad = max(0, -(-tokens // page) - s["table"].shape[1])
+    s["table"] = torch.nn.functional.pad(s["table"], (0, pad), value=-1)
+    return s
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("heads,kv_heads", [(1, 1), (32, 8), (15, 3), (16, 1), (40, 1)])
+def test_short_requests_under_a_long_bound(kind, d, heads, kv_heads):
+    s = long_bound(make([1, 15, 16, 17, 130, 0, 333], heads, kv_heads, d, 16, kind=kind,
+                        seed=d + heads, poison=kind != "e4m3"))
+    *_, status = run_and_check(s)
+    assert status == 0
+
+
+@pytest.mark.parametrize("page", [16, 48, 64, 256])
+@pytest.mark.parametrize("lens", [[1], [2, 1], [0, 0], [129, 4097, 7], list(range(1, 70))])
+def test_pages_under_a_long_bound(page, lens):
+    s = long_bound(make(lens, 8, 2, 64, page, seed=page + len(lens), poison=True))
+    score = torch.rand(len(lens), s["table"].shape[1] * page, device="cuda")
+    *_, status = run_and_check(s, score=score)
+    assert status == 0
+
+
+@pytest.mark.parametrize("kind,heads,kv_heads,d", [
+    ("bf16", 32, 8, 128), ("fp16", 12, 12, 64), ("e4m3", 32, 8, 128), ("bf16", 16, 1, 256),
+    ("e4m3", 16, 1, 256), ("bf16", 48, 4, 64), ("fp16", 24, 1, 128)])
+@pytest.mark.parametrize("lens", [
+    [100], [300], [511], [1000], [1025], [4000], [8192], [500, 0, 3], [0, 900, 0, 128, 127],
+    [130] * 12, [7, 256, 0, 64, 200, 0] * 5, [90, 0, 128, 1] * 16, [33] * 128])
+def test_units_of_clusters(kind, heads, kv_heads, d, lens):
+    """Short bounds: every unit has CTAs of its own, one or a cluster (some
+    without a tile), with one KV head or several."""
+    s = make(lens, heads, kv_heads, d, 16, kind=kind, seed=len(lens) + d, poison=kind != "e4m3")
+    n = s["table"].shape[1] * 16
+    out, lse, status = run_and_check(s)
+    score = torch.rand(len(lens), n, device="cuda")
+    out2, lse2, status2 = run_and_check(s, score=score, decay=0.5)
+    assert status == status2 == 0
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("rows,window,sinks", [(1, 700, 4), (3, 130, 0), (18, 256, 4),
+                                               (40, 20, 17), (70, 64, 4)])
+def test_windows_of_clusters(rows, window, sinks):
+    g = torch.Generator().manual_seed(rows)
+    lens = torch.randint(0, 3000, (rows,), generator=g)
+    lens[0] = 2999
+    s = make(lens.tolist(), 32, 8, 128, 16, seed=rows)
+    score = torch.rand(rows, s["table"].shape[1] * 16, device="cuda")
+    run_and_check(s, window=window, sinks=sinks)
+    *_, status = run_and_check(s, window=window, sinks=sinks, score=score)
+    assert status == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_clusters_skip_bad_pages(kind):
+    """A CTA of a cluster whose pages are all bad has no token to add."""
+    s = make([600, 600, 40], 8, 2, 128, 16, kind=kind, seed=4)
+    s["table"][0, 8:16] = -1
+    s["table"][1, :] = s["k"].shape[0]
+    s["table"][2, 1] = 1 << 30
+    out, lse, status = run_and_check(s)
+    assert status == 6 and not out[1].any() and (lse[1] == -math.inf).all()
