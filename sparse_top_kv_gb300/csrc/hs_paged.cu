@@ -71,6 +71,24 @@ bool tensor_map_ok(const PagedArgs& a, int kv_dtype, int d) {
            a.row_stride > 0 && a.row_stride < most;
 }
 
+// Small calls of few requests with few query heads on a KV head run on the
+// warp-level kernel: it starts and ends a unit sooner than the tcgen05 kernel,
+// which is ahead where more is streamed, where more query heads share a row,
+// and where a cluster's CTAs have very few tiles each.  us, tcgen05 / warps,
+// 32/8 heads of 128: one request of 2 K tokens 10.6 / 8.9, 16 K 24.6 / 19.6,
+// eight of up to 4 K 18.5 / 16.4, eight of 16 K 88.3 / 92.1, 16 of up to 1 K
+// 17.7 / 14.6, 32 of up to 2 K 32.9 / 36.3, 16 of 256 9.1 / 12.0; 64/8 heads:
+// one request of 1 K 9.2 / 9.9; 12/12 heads of 64: eight of 1 K 13.6 / 11.8, of
+// 8 K 40.8 / 43.8.
+constexpr int kWarpRows = 16, kWarpGroup = 4;
+constexpr int kWarpTiles = 28;  // tiles of 128 tokens of a KV head per CTA, at most
+bool by_warps(const PagedArgs& a, int kv_dtype, int d) {
+    if (kv_dtype == HS_E4M3 || d > 128 || a.group > kWarpGroup || a.rows > kWarpRows) return false;
+    const int64_t units = int64_t(a.rows) * a.kv_heads, tiles = most_tiles(a, 7);
+    const bool clusters = units <= a.ctas && tiles <= (units > 64 ? 4 : 3);
+    return !clusters && units * tiles <= int64_t(a.ctas) * kWarpTiles;
+}
+
 constexpr int kMergeThreads = 256;
 constexpr int kMergeWarps = kMergeThreads / 32;
 constexpr int kHeadChunk = 256;  // heads whose LSE a scoring block holds at a time
@@ -539,7 +557,7 @@ extern "C" int hs_paged_decode(const void* q, int64_t q_stride, int32_t q_dtype,
     a.ctas = w.ctas;
     a.status = status;
     int rc;
-    if (tensor_map_ok(a, kv_dtype, d)) {
+    if (tensor_map_ok(a, kv_dtype, d) && !by_warps(a, kv_dtype, d)) {
         if (kv_dtype == HS_BF16) rc = launch_tc_bf16(a, d, group, stream);
         else if (kv_dtype == HS_FP16) rc = launch_tc_fp16(a, d, group, stream);
         else rc = launch_tc_e4m3(a, d, group, stream);

@@ -290,13 +290,13 @@ inline void set_ways(PagedArgs& a, int hs_max, int tile_rows, int gm, int tiles_
     a.wide_to = INT64_MAX;
 }
 
-// Host: at most this many tiles in one unit of way `way`, by the bound on the
-// lengths.
-inline int64_t most_tiles(const PagedArgs& a, int way) {
-    const int64_t up = (int64_t(1) << a.lth[way]) - 1;
-    const int64_t all = (a.max_len + up) >> a.lth[way];
+// Host: at most this many tiles of 2^lth tokens in one unit, by the bound on
+// the lengths.
+inline int64_t most_tiles(const PagedArgs& a, int lth) {
+    const int64_t up = (int64_t(1) << lth) - 1;
+    const int64_t all = (a.max_len + up) >> lth;
     if (a.window == 0) return all;
-    return hs::min64(all, ((a.sinks + up) >> a.lth[way]) + ((a.window + up) >> a.lth[way]) + 1);
+    return hs::min64(all, ((a.sinks + up) >> lth) + ((a.window + up) >> lth) + 1);
 }
 
 // Host: at most this many places in way `way`, by the bound on the lengths.

@@ -1,5 +1,10 @@
-// hs_paged_core.cuh -- the attention kernel of hs_paged_decode for one cache
-// type (included by one translation unit per type).
+// hs_paged_core.cuh -- the warp-level attention kernel of hs_paged_decode for
+// one cache type (included by one translation unit per type): small calls of
+// few requests, and caches that tensor maps or the tcgen05 kernel do not take
+// (pages that are no multiple of 16 tokens, broadcast strides, E4M3 heads of
+// 64).  Bound by latency in small calls (one request of 1 K tokens, 32/8 heads
+// of 128: 5 us, and 3.4 for the merge), by HBM in large ones (64 requests of
+// 8 K: 321 us, 6.7 TB/s).
 //
 // Math, per request and query head h of KV head g, over the visible tokens:
 //   x_t = scale * k_scale_g * (q_h . K_t),  m = max_t x_t,
@@ -26,7 +31,14 @@
 namespace hs_paged {
 namespace core {
 
-constexpr int kTilesForWide = 16;  // tiles per CTA from which units take several heads
+// Places per CTA from which units take several heads.  us with one head / several:
+// 64 requests of 2 K tokens (27 places) 89.3 / 94.2, one of 128 K 86.8 / 91.8, 64
+// of 32 K (430 places) 1269 / 1227; E4M3 heads of 64, 64 requests of 4 K (64
+// places) 108 / 92.
+constexpr int kTilesForWide = 64;
+// Places that a unit's start and end count for (us at 0 / 1 / 4: eight requests
+// of 1 K tokens 16.4 / 15.1 / 15.9, 64 of 510 38.7 / 35.5 / 37.4).
+constexpr int kExtra = 1;
 
 enum Kind { kBf16 = 0, kFp16 = 1, kE4m3 = 2 };
 
@@ -521,7 +533,7 @@ template <int KV, int D, int GH>
 int launch_one(PagedArgs& a, hs_stream_t stream) {
     using C = Cfg<KV, D, GH>;
     auto kern = paged_kernel<KV, D, GH>;
-    set_ways(a, C::kWarps, C::kWarps * kKey, C::GM, kTilesForWide, 1);
+    set_ways(a, C::kWarps, C::kWarps * kKey, C::GM, kTilesForWide, kExtra);
     constexpr size_t smem = C::kBody + C::kWarps * C::kStages * 4;
     static int smem_set[64] = {};
     const int rc =

@@ -1098,7 +1098,7 @@ inline int cluster_way(PagedArgs& a, const void* kern, size_t smem, int tile_byt
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
     const int64_t few = hs::min64(kTilesOfUnit, kUnitBytes / tile_bytes);
     for (int way = 1; way >= 0 && a.cl == 0; --way) {
-        const int64_t units = int64_t(a.rows) * a.chunks[way], tiles = most_tiles(a, way);
+        const int64_t units = int64_t(a.rows) * a.chunks[way], tiles = most_tiles(a, a.lth[way]);
         if (units > a.ctas || tiles > few * kMaxCluster) continue;
         int64_t best = INT64_MAX;
         for (int cl = 1; cl <= kMaxCluster && units * cl <= a.ctas; ++cl) {

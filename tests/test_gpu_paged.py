@@ -481,7 +481,7 @@ def test_largest_head_count():
     run_and_check(s)
 
 
-def long_bound(s, tokens=20000):
+def long_bound(s, tokens=200000):
     """The same requests in a table that could hold `tokens` each: the bound on
     the lengths decides how a call is cut."""
     page = s["k"].shape[1]
