@@ -147,7 +147,9 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (!s.ok || s.dtype != at::kInt) return general();
         status = s.ptr;
     }
-    const int rc = hs_paged_decode(
+    int rc;
+    Py_BEGIN_ALLOW_THREADS  // a launch may wait for room in its stream
+    rc = hs_paged_decode(
         q.ptr, heads * d, qe, k.ptr, v.ptr, ke, pages > 1 ? page * kvh * d : 0,
         page > 1 ? kvh * d : 0, kvh > 1 ? d : 0, int32_t(pages), int32_t(page),
         static_cast<const int32_t*>(table.ptr), blocks, int32_t(blocks), int32_t(max_len),
@@ -156,6 +158,7 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
         window, sinks, scale, static_cast<float*>(score.ptr), score.ok ? score.dim[1] : 0, decay,
         out.ptr, static_cast<float*>(lse.ptr), ws.ptr, ws.bytes, static_cast<int32_t*>(status),
         reinterpret_cast<hs_stream_t>(stream));
+    Py_END_ALLOW_THREADS
     if (rc == HS_ERR_CAPACITY) return general();  // a larger workspace is wanted
     return PyLong_FromLong(rc);
 }
@@ -230,7 +233,9 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (!s.ok || s.dtype != at::kInt) return general();
         status = s.ptr;
     }
-    const int rc = hs_evict(
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = hs_evict(
         static_cast<const float*>(score.ptr), score.dim[1], static_cast<const int32_t*>(pos.ptr),
         pos.ok ? pos.dim[1] : 0, static_cast<const int32_t*>(lens.ptr),
         static_cast<const int32_t*>(next.ptr), int32_t(rows), int32_t(max_len), budget, recent,
@@ -241,6 +246,7 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
         kvh > 1 ? row : 0, int32_t(kvh), int32_t(row), int32_t(pages), int32_t(page),
         static_cast<const int32_t*>(table.ptr), table.dim[1], int32_t(table.dim[1]),
         static_cast<int32_t*>(status), reinterpret_cast<hs_stream_t>(stream));
+    Py_END_ALLOW_THREADS
     return PyLong_FromLong(rc);
 }
 
