@@ -107,7 +107,7 @@ __device__ __forceinline__ uint32_t order_key(float s, bool keep) {
 // again.  Then each warp walks its part of the slice in order: what is kept
 // before an index gives the rank of a hole or of a moving row.
 __global__ void __launch_bounds__(kThreads)
-evict_select_kernel(const __grid_constant__ EvictArgs a, int slice, int cached) {
+evict_select_kernel(const __grid_constant__ EvictArgs a, int slice, int cached, int state) {
     extern __shared__ __align__(16) unsigned char smem[];
     int* hist = reinterpret_cast<int*>(smem);              // [kCopies][kBins]
     int* counts = hist + kCopies * kBins;                  // [2][kBins], read by the cluster
@@ -326,6 +326,11 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int slice, int cached) 
     }
     // The lists are complete (and every CTA has read the request's state).
     cluster_sync();
+    if (rank == 0 && tid == 0) {
+        a.lens_out[row] = B;
+        a.move_count[row] = moves;
+    }
+    if (!state) return;  // the kernel that moves the rows moves these too
     for (int j = int(rank) * kThreads + tid; j < moves; j += int(ncta) * kThreads) {
         const int s = __ldcg(msrc + j), d = __ldcg(mdst + j);
         const float x = score[s];
@@ -333,11 +338,6 @@ evict_select_kernel(const __grid_constant__ EvictArgs a, int slice, int cached) 
         score_out[d] = x;
         if (pos_out != nullptr) pos_out[d] = pos ? pos[s] : s;
     }
-    if (rank == 0 && tid == 0) {
-        a.lens_out[row] = B;
-        a.move_count[row] = moves;
-    }
-    cluster_sync();  // no CTA ends while a peer may still read its shared memory
 }
 
 struct MoveArgs {
@@ -351,6 +351,12 @@ struct MoveArgs {
     const int32_t* dst;
     const int32_t* count;
     int32_t* status;
+    // Scores and positions that move along, or nullptr.
+    const float* score;
+    float* score_out;
+    const int32_t* positions;
+    int32_t* positions_out;
+    int64_t score_stride, score_out_stride, pos_stride, pos_out_stride;
 };
 
 // Byte offset of a request's place in the caches, or -1 (a bad page).
@@ -388,10 +394,18 @@ evict_move_kernel(const __grid_constant__ MoveArgs a, int ctas_per_row) {
     bool bad = false;
     for (int j0 = (part * kMoveWarps + warp) * batch; j0 < n; j0 += warps * batch) {
         const int m = min(n - j0, batch);
+        int s = 0, d = 0, p = 0;
+        float sc = 0.f;
         if (lane < m) {
+            s = __ldcg(src + j0 + lane);
+            d = __ldcg(dst + j0 + lane);
+            if (a.score_out != nullptr) {
+                sc = a.score[row * a.score_stride + s];
+                p = a.positions != nullptr ? a.positions[row * a.pos_stride + s] : s;
+            }
             longlong2 o;
-            o.x = place_of(a, table, __ldcg(src + j0 + lane));
-            o.y = place_of(a, table, __ldcg(dst + j0 + lane));
+            o.x = place_of(a, table, s);
+            o.y = place_of(a, table, d);
             if (o.x < 0 || o.y < 0) {
                 bad = true;
                 o.x = -1;
@@ -431,6 +445,11 @@ evict_move_kernel(const __grid_constant__ MoveArgs a, int ctas_per_row) {
 #pragma unroll
             for (int u = 0; u < kMoveFlight; ++u)
                 if (to[u] != nullptr) *reinterpret_cast<uint4*>(to[u]) = r[u];
+        }
+        if (lane < m && a.score_out != nullptr) {
+            a.score_out[row * a.score_out_stride + s] = 0.f;
+            a.score_out[row * a.score_out_stride + d] = sc;
+            if (a.positions_out != nullptr) a.positions_out[row * a.pos_out_stride + d] = p;
         }
         __syncwarp();  // the offsets are read
     }
@@ -618,7 +637,7 @@ int check_select(const EvictArgs& a) {
 
 // Whether every request is within a few tokens of the budget and small enough
 // for the trimming kernel (64 requests of 2049 tokens: one launch instead of
-// two, a third of the time).
+// two, 5.4 us instead of 16.8).
 bool trims(const EvictArgs& a) {
     return int64_t(a.max_len) - a.budget <= kTrimMost && a.max_len <= kTrimThreads * kTrimKeys;
 }
@@ -628,7 +647,8 @@ int launch_trim(const EvictArgs& a, const MoveArgs& m, hs_stream_t stream) {
                                stream, a, m);
 }
 
-int launch_select(const EvictArgs& a, hs_stream_t stream) {
+// state: whether the scores and positions move here or with the rows.
+int launch_select(const EvictArgs& a, bool state, hs_stream_t stream) {
     // As many CTAs per request as the GPU has free, each with a slice worth
     // a cluster barrier.
     const int64_t sms = hs_host::num_sms();
@@ -658,7 +678,8 @@ int launch_select(const EvictArgs& a, hs_stream_t stream) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, evict_select_kernel, a, slice, cached) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, evict_select_kernel, a, slice, cached, int(state)) !=
+        cudaSuccess) {
         cudaGetLastError();
         return HS_ERR_CUDA;
     }
@@ -710,7 +731,8 @@ MoveArgs move_args(void* k, void* v, int64_t page_stride, int64_t row_stride, in
                    int32_t cap, int32_t* status) {
     return MoveArgs{static_cast<unsigned char*>(k), static_cast<unsigned char*>(v), page_stride,
                     row_stride, head_stride, kv_heads, row_bytes, num_pages, page_size, rows,
-                    max_blocks, cap, block_table, bt_stride, src, dst, count, status};
+                    max_blocks, cap, block_table, bt_stride, src, dst, count, status,
+                    nullptr, nullptr, nullptr, nullptr, 0, 0, 0, 0};
 }
 
 }  // namespace
@@ -729,7 +751,7 @@ extern "C" int hs_evict_select(const float* score, int64_t score_stride, const i
                                     move_src, move_dst, move_count, cap, status);
     const int rc = check_select(a);
     if (rc != HS_OK || rows == 0) return rc;
-    return trims(a) ? launch_trim(a, MoveArgs{}, stream) : launch_select(a, stream);
+    return trims(a) ? launch_trim(a, MoveArgs{}, stream) : launch_select(a, true, stream);
 }
 
 extern "C" int hs_evict_move(void* k, void* v, int64_t page_stride, int64_t row_stride,
@@ -760,14 +782,25 @@ extern "C" int hs_evict(const float* score, int64_t score_stride, const int32_t*
                                     rows, max_len, budget, recent, num_sinks, score_out,
                                     score_out_stride, positions_out, pos_out_stride, lens_out,
                                     move_src, move_dst, move_count, cap, status);
-    const MoveArgs m = move_args(k, v, page_stride, row_stride, head_stride, kv_heads, row_bytes,
-                                 num_pages, page_size, block_table, bt_stride, max_blocks,
-                                 move_src, move_dst, move_count, rows, cap, status);
+    MoveArgs m = move_args(k, v, page_stride, row_stride, head_stride, kv_heads, row_bytes,
+                           num_pages, page_size, block_table, bt_stride, max_blocks,
+                           move_src, move_dst, move_count, rows, cap, status);
     int rc = check_select(a);
     if (rc == HS_OK) rc = check_move(m);
     if (rc == HS_OK && int64_t(max_blocks) * page_size < max_len) rc = HS_ERR_INVALID_ARG;
     if (rc != HS_OK || rows == 0) return rc;
     if (trims(a)) return launch_trim(a, m, stream);
-    rc = launch_select(a, stream);
+    // The scores and positions of the rows that move go with them, so that the
+    // selection, during which nothing else runs, is shorter (32 latent contexts
+    // of 32 K tokens 39.5 us instead of 40.5).
+    m.score = score;
+    m.score_out = score_out;
+    m.positions = positions;
+    m.positions_out = positions_out;
+    m.score_stride = score_stride;
+    m.score_out_stride = score_out_stride;
+    m.pos_stride = pos_stride;
+    m.pos_out_stride = pos_out_stride;
+    rc = launch_select(a, false, stream);
     return rc != HS_OK ? rc : launch_move(m, stream);
 }

@@ -409,3 +409,40 @@ def test_memory_of_a_call_on_another_stream():
         assert len(junk) == 6
     for a, b in zip(*results):
         assert same_bits(a, b)
+
+
+@pytest.mark.parametrize("given", ["none", "positions", "outputs"])
+@pytest.mark.parametrize("lens,budget", [([300, 64, 65, 0, 200, 128], 64), ([5000], 1000),
+                                         ([20000, 9000, 40000], 2048), ([900] * 40, 450)])
+def test_both_steps_in_one_call(lens, budget, given):
+    """hs_evict moves scores and positions along with the rows; hs_evict_select
+    moves them itself."""
+    R, W, page = len(lens), max(lens) + 3, 16
+    g = torch.Generator().manual_seed(R + budget)
+    blocks = -(-W // page)
+    score = torch.rand(R, W, generator=g)
+    score[:, ::7] = score[:, 1:2]
+    pos = torch.stack([torch.randperm(W, generator=g) for _ in range(R)]).to(torch.int32)
+    k, v = caches(R * blocks, page, 2, 64, torch.bfloat16)
+    table = torch.randperm(R * blocks, generator=g).to(torch.int32).view(R, blocks).cuda()
+    results = []
+    for split in (False, True):
+        s, kc, vc = score.cuda(), k.clone(), v.clone()
+        ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        kw = dict(recent=20, num_sinks=3)
+        if given != "none":
+            kw.update(positions=pos.cuda(),
+                      next_pos=torch.full((R,), W, dtype=torch.int32, device="cuda"))
+        if given == "outputs":
+            kw.update(score_out=torch.full_like(s, 5.0), lens_out=torch.full_like(ln, -7),
+                      positions_out=torch.full((R, W), -3, dtype=torch.int32, device="cuda"))
+        if split:
+            so, po, lo, moves = hs.evict_select(s, ln, budget, **kw)
+            hs.evict_move(moves, kc, vc, table)
+        else:
+            so, po, lo, moves = hs.evict(s, ln, budget, kc, vc, table, **kw)
+        torch.cuda.synchronize()
+        results.append([s, so, lo, moves[2], kc, vc] + ([] if po is None else [po]))
+    assert int(results[0][3].sum()) > 0
+    for a, b in zip(*results):
+        assert same_bits(a, b)
