@@ -870,7 +870,16 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
                 if (!valid) {
                     for (int s = 0; s < C::kSubs; ++s) {
                         const int seq = t * C::kSubs + s, at = seq % NS;
-                        if (!hs::mbar_wait_bounded(&B.vfull[at], (seq / NS) & 1, tmo, abort_flag)) {
+                        // A parity tells two neighbouring phases apart: the
+                        // unit's load before this one has to be known to be
+                        // complete.  pv_done says so up to tile t - 2; a unit
+                        // that tile t - 1 used last is waited for.
+                        bool full = true;
+                        if (NS < 2 * C::kSubs && s >= NS - C::kSubs && seq >= NS)
+                            full = hs::mbar_wait_bounded(&B.vempty[at], (seq / NS - 1) & 1, tmo,
+                                                         abort_flag);
+                        if (!full ||
+                            !hs::mbar_wait_bounded(&B.vfull[at], (seq / NS) & 1, tmo, abort_flag)) {
                             fail = true;
                             B.abort = 1;
                         }

@@ -549,3 +549,20 @@ def test_clusters_skip_bad_pages(kind):
     s["table"][2, 1] = 1 << 30
     out, lse, status = run_and_check(s)
     assert status == 6 and not out[1].any() and (lse[1] == -math.inf).all()
+
+
+@pytest.mark.parametrize("kind,d,heads,kv_heads", [("fp16", 256, 16, 16), ("bf16", 256, 16, 1),
+                                                   ("bf16", 128, 32, 8), ("fp16", 64, 8, 8)])
+@pytest.mark.parametrize("page", [16, 128])
+def test_partial_tiles_many_times(kind, d, heads, kv_heads, page):
+    """NaN behind the contexts: a tile's unused rows are cleared after they
+    have been loaded and before they are multiplied, however the loads of
+    neighbouring tiles fall."""
+    g = torch.Generator().manual_seed(d)
+    lens = torch.randint(0, 964, (64,), generator=g)
+    lens[torch.rand(64, generator=g) < 0.3] = 963
+    s = long_bound(make(lens.tolist(), heads, kv_heads, d, page, kind=kind, seed=d, poison=True))
+    want, want_lse, _ = run_and_check(s)
+    for _ in range(60):
+        out, lse = hs.paged_decode(s["q"], s["k"], s["v"], s["table"], s["lens"], s["scale"])
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
