@@ -566,3 +566,30 @@ def test_partial_tiles_many_times(kind, d, heads, kv_heads, page):
     for _ in range(60):
         out, lse = hs.paged_decode(s["q"], s["k"], s["v"], s["table"], s["lens"], s["scale"])
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+def test_calls_on_two_streams_at_once():
+    """Each with its own workspace: dealt calls, clusters and the warp-level
+    kernel side by side."""
+    shapes = [long_bound(make([3000, 5, 777, 9000], 32, 8, 128, 16, seed=1)),
+              make([260] * 16, 64, 8, 128, 16, seed=2), make([1500, 40, 3], 32, 8, 128, 16, seed=3)]
+    wants, spaces = [], []
+    for s in shapes:
+        wants.append(run_and_check(s)[:2])
+        n = hs.paged_decode_workspace_bytes(*s["q"].shape[:2], s["k"].shape[2], 128,
+                                            s["table"].shape[1] * 16)
+        spaces.append([torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(2)])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[[] for _ in shapes] for _ in streams]
+    torch.cuda.synchronize()
+    for it in range(30):
+        for j, stream in enumerate(streams):
+            i = (it + j) % len(shapes)
+            s = shapes[i]
+            with torch.cuda.stream(stream):
+                outs[j][i].append(hs.paged_decode(s["q"], s["k"], s["v"], s["table"], s["lens"],
+                                                  s["scale"], workspace=spaces[i][j]))
+    torch.cuda.synchronize()
+    for per_stream in outs:
+        for (want, want_lse), got in zip(wants, per_stream):
+            assert all(torch.equal(o, want) and torch.equal(l, want_lse) for o, l in got)
