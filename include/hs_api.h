@@ -553,9 +553,7 @@ int hs_sparse_decode_fp8ds(const void* q, const void* kv8, int64_t row_bytes,
  * NaN included.  A request whose logits are all -inf gives out = 0 and lse =
  * -inf; entries of attended tokens that are not finite give outputs of their
  * own head that are not finite (an infinite V entry NaN).  Results do not
- * depend on timing.  out must not overlap an input.  A process's first call of
- * a kind (types, d, group size) loads its kernel: make it before a stream
- * capture.
+ * depend on timing.  out must not overlap an input.
  * Supported: d 64, 128 or 256, any heads / kv_heads; others (and scales with
  * 16-bit caches, or caches of another 16-bit type than q) return
  * HS_ERR_UNSUPPORTED.  rows <= 4096, heads <= 65536, max_len <= 2^30 and about

@@ -3,8 +3,8 @@
 // few requests, and caches that tensor maps or the tcgen05 kernel do not take
 // (pages that are no multiple of 16 tokens, broadcast strides, E4M3 heads of
 // 64).  Bound by latency in small calls (one request of 1 K tokens, 32/8 heads
-// of 128: 5 us, and 3.4 for the merge), by HBM in large ones (64 requests of
-// 8 K: 321 us, 6.7 TB/s).
+// of 128: 8.4 us with the merge), by HBM in large ones (64 requests of 8 K in
+// pages of 12: 321 us, 6.7 TB/s).
 //
 // Math, per request and query head h of KV head g, over the visible tokens:
 //   x_t = scale * k_scale_g * (q_h . K_t),  m = max_t x_t,
