@@ -502,6 +502,10 @@ class BudgetedDecoder:
         capacity = budget + 1 if capacity is None else capacity
         if capacity <= budget:
             raise ValueError("capacity: more than the budget, for the new token")
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"dtype: torch.bfloat16 or torch.float16, got {dtype}")
+        if recent < 0 or num_sinks < 0 or recent + num_sinks > budget:
+            raise ValueError("recent, num_sinks: within the budget")
         self.device = torch.device(device)
         dev = self.device
         self.num_reqs, self.heads, self.kv_heads, self.d = num_reqs, heads, kv_heads, d

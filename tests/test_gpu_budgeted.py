@@ -90,3 +90,13 @@ def test_refusals():
     for n in (0, 17):
         with pytest.raises(ValueError):
             dec.start(0, torch.zeros(n, 2, 64), torch.zeros(n, 2, 64))
+
+
+@pytest.mark.parametrize("kw,error", [(dict(dtype=torch.float8_e4m3fn), TypeError),
+                                      (dict(dtype=torch.float32), TypeError),
+                                      (dict(recent=30, num_sinks=4), ValueError),
+                                      (dict(recent=-1), ValueError)])
+def test_refused_at_set_up(kw, error):
+    with pytest.raises(error):
+        BudgetedDecoder(num_reqs=2, heads=4, kv_heads=2, d=64, page_size=16, budget=32,
+                        scale=0.1, **kw)
