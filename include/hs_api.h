@@ -543,6 +543,9 @@ int hs_sparse_decode_fp8ds(const void* q, const void* kv8, int64_t row_bytes,
  *             left as it was.
  * out         [rows, heads, d] of q_dtype, fp32 accumulated, rounded to
  *             nearest even.   lse fp32 [rows, heads] natural log, or NULL.
+ *             A weight enters the sum within 2^-16 of itself; with fp16 and
+ *             E4M3 caches, where that is more, within the smaller of 2^-10
+ *             of itself and 2^-35 of the largest, or within 2^-40 of that.
  * workspace   device scratch, 256-byte aligned, of at least
  *             hs_paged_decode_workspace_bytes(..) bytes; needs no contents on
  *             entry and keeps none.  Calls that may overlap need their own.

@@ -22,8 +22,11 @@
 // rounded part and the rounding's remainder, so the weights keep twice the
 // operand's precision: up to 8 query heads leave rows 8..15 of the fragment
 // free and the remainder rides there at no cost; 9..16 heads take a second
-// product.  E4M3 codes are widened exactly to fp16 (the query row is scaled
-// by a power of two into fp16's range, undone on the logits).
+// product.  fp16 weights are scaled by 2^15, so that they lose 2^-40 of the
+// largest and not 2^-25 (a remainder in rows of its own by 2^12 more: 2^-52);
+// bf16 has fp32's exponents.  E4M3 codes are widened exactly to fp16 (the
+// query row is scaled by a power of two into fp16's range, undone on the
+// logits).
 #pragma once
 
 #include "hs_paged.cuh"
@@ -158,6 +161,8 @@ paged_kernel(const __grid_constant__ PagedArgs a) {
     constexpr bool BF = KV == kBf16;
     constexpr int NW = C::kWarps, S = C::kStages, GM = C::GM;
     constexpr int NT = D / 8;
+    // Scales of the weights' two parts (the second's relative to the first's).
+    constexpr float kP = BF ? 1.f : 32768.f, kLo = BF || GH == 2 ? 1.f : 4096.f;
     extern __shared__ __align__(128) unsigned char smem[];
     unsigned char* body = smem;                                      // ring / reduction
     uint32_t* live_s = reinterpret_cast<uint32_t*>(smem + C::kBody);  // [NW][S]
@@ -393,9 +398,10 @@ paged_kernel(const __grid_constant__ PagedArgs a) {
                 grow |= alpha[hh] != 1.f;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    ph[hh][i] = pack<BF>(p[2 * i], p[2 * i + 1]);
+                    const float x0 = p[2 * i] * kP, x1 = p[2 * i + 1] * kP;
+                    ph[hh][i] = pack<BF>(x0, x1);
                     const float2 f = unpack<BF>(ph[hh][i]);
-                    plo[hh][i] = pack<BF>(p[2 * i] - f.x, p[2 * i + 1] - f.y);
+                    plo[hh][i] = pack<BF>((x0 - f.x) * kLo, (x1 - f.y) * kLo);
                 }
             }
             if (__any_sync(0xffffffffu, grow)) {
@@ -461,6 +467,10 @@ paged_kernel(const __grid_constant__ PagedArgs a) {
         __syncthreads();  // the ring becomes the reduction's buffer
         float* so = reinterpret_cast<float*>(body);  // [NW][GM][D]
         float* sml = so + NW * GM * D;               // [NW][GM][2]
+        // A head's sum from its two rows of a fragment, or its one.
+        auto sum = [&](const float (&c)[4], int hh, int j) {
+            return (GH == 1 ? fmaf(c[2 + j], 1.f / kLo, c[j]) : c[2 * hh + j]) * (1.f / kP);
+        };
 #pragma unroll
         for (int hh = 0; hh < GH; ++hh) {
             if (g + 8 * hh < Gc) {
@@ -468,18 +478,15 @@ paged_kernel(const __grid_constant__ PagedArgs a) {
                 if constexpr (KV != kE4m3) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        const float x = GH == 1 ? o[n][0] + o[n][2] : o[n][2 * hh];
-                        const float y = GH == 1 ? o[n][1] + o[n][3] : o[n][2 * hh + 1];
-                        *reinterpret_cast<float2*>(dst + n * 8 + 2 * t) = make_float2(x, y);
+                        *reinterpret_cast<float2*>(dst + n * 8 + 2 * t) =
+                            make_float2(sum(o[n], hh, 0), sum(o[n], hh, 1));
                     }
                 } else {
 #pragma unroll
                     for (int n = 0; n < NT; n += 2) {
-                        const float x = GH == 1 ? o[n][0] + o[n][2] : o[n][2 * hh];
-                        const float z = GH == 1 ? o[n][1] + o[n][3] : o[n][2 * hh + 1];
-                        const float y = GH == 1 ? o[n + 1][0] + o[n + 1][2] : o[n + 1][2 * hh];
-                        const float u = GH == 1 ? o[n + 1][1] + o[n + 1][3] : o[n + 1][2 * hh + 1];
-                        *reinterpret_cast<float4*>(dst + n * 8 + 4 * t) = make_float4(x, y, z, u);
+                        *reinterpret_cast<float4*>(dst + n * 8 + 4 * t) =
+                            make_float4(sum(o[n], hh, 0), sum(o[n + 1], hh, 0),
+                                        sum(o[n], hh, 1), sum(o[n + 1], hh, 1));
                     }
                 }
                 if (t == 0) {

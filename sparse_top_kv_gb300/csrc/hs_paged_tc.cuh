@@ -32,13 +32,16 @@
 //    bound at first (16 products a tile at 80 to 100 cycles each).
 //  * O^T[D x queries] += V^T P^T, V as an MN-major view of its tile, K = the
 //    16 (E4M3: 32) rows of one head, one accumulator per head.  P is carried
-//    as several parts in columns of their own: a bf16 or fp16 value and the
-//    rounding's remainder, so weights keep twice the operand's precision.
+//    as several parts in columns of their own: two bf16 or fp16 ones, six E4M3
+//    ones, scaled so that small weights keep their bits too (Cfg::up): behind
+//    an attention sink without a value they are all of the output.
 //  * E4M3 caches are multiplied as they are (kind::f8f6f4): the query, scaled
 //    by a power of two, becomes several E4M3 parts (each the rounding of 16
 //    times the remainder before it: two hold the 8 bits of a bf16 query,
-//    three the 11 of an fp16 one), P four; each part has columns of its own
-//    and the parts are summed in fp32 with their weights 16^-i.
+//    three the 11 of an fp16 one, down to about 2^-14 and 2^-15 of its row's
+//    largest element; smaller ones are off by 2^-22 and 2^-26 of that); each
+//    part has columns of its own and the parts are summed in fp32 with their
+//    weights 16^-i.
 // Every wait is bounded (HS_ERR_TIMEOUT in the status word on expiry).
 #pragma once
 
@@ -64,7 +67,7 @@ constexpr int kBothBar = 3;          // and of both
 constexpr int kMaskRing = 16;        // tiles whose loaded runs are remembered
 constexpr float kThresh = 8.f;       // log2 headroom before O is rescaled
 constexpr int kTmemCols = 512;
-constexpr int kBarBytes = 8192;      // shared-memory budget of Bars
+constexpr int kBarBytes = 5120;      // shared-memory budget of Bars
 // Places per CTA from which the units of a deal take several heads (the
 // shorter calls here are dealt where their bound on the lengths is long).  32/8 heads of 128, bf16,
 // us with all heads / one head to a unit: one request of 1 K tokens 10.8 / 10.8,
@@ -115,7 +118,23 @@ struct Cfg {
     static constexpr int kSubs = kBlocks / kSubBlocks;   // ring units of a tile
     static constexpr int kQParts = kE4 ? QP : 1;
     static constexpr int kQBufs = kE4 ? 2 : 1;  // the E4M3 parts take time to make
-    static constexpr int kPParts = kE4 ? 4 : 2;
+    static constexpr int kPParts = kE4 ? 6 : 2;
+    // Weights p <= 2^kThresh are carried as parts c_i of the operand's type, p =
+    // sum c_i / s_i: each the rounding of s_i times what the parts before it leave,
+    // with s_0 = up(-1) and s_(i+1) = s_i up(i).
+    //  bf16: has fp32's exponents; two parts keep p to 2^-17.
+    //  fp16: s_0 brings the largest p to 2^15, the remainder has a scale of its
+    //    own: p to 2^-23, and to 2^-44 in all (below 2^-25 without the scales).
+    //  E4M3: 4 bits and a sign each, so s_i grows by 2^5: the first four keep p
+    //    >= 2^-6 to 2^-19 and leave 2^-25 of smaller ones.  The last two start
+    //    there (large weights' remainders saturate in them, which does no harm):
+    //    p to 2^-35, or 2^-10 of itself below 2^-25, down to 2^-48.  (64 requests
+    //    of up to 8 K tokens: 90.4 us, 89.0 with four parts 2^4 apart, which lose
+    //    p < 2^-22.)
+    static constexpr float up(int i) {
+        return kE4 ? (i < 0 ? 1.f : i == 3 ? 262144.f : 32.f)
+                   : KV == kFp16 ? (i < 0 ? 128.f : 4096.f) : 1.f;
+    }
     static constexpr int NH = GM * kQParts;              // query columns of a head
     static constexpr int NP = GM * kPParts;              // output columns of a head
     static constexpr int kStep = 32 / kElt;              // rows of a PV K step
@@ -153,10 +172,11 @@ struct Bars {
     float2 join_ml[kMaxUnit];           // [head, query] the cluster's CTAs read each other's
     uint32_t loaded[kMaskRing];         // runs of a tile that were loaded
     alignas(16) float red[kGroups][8][16];  // per 16 rows: maxima or sums
-    float alpha[kGroups][8][16];        // rescale factors, [head][query]
-    float ml[kGroups][8][16][2];        // epilogue: (m, l), [head][query]
-    float weight[kGroups][8][16];       // and the groups' factors of the output
-    float qscale[4][128];    // E4M3: factor of each query's logits, by segment
+    // By head * GM + query:
+    float alpha[kGroups][kMaxUnit];     // rescale factors
+    float m[kGroups][kMaxUnit];         // epilogue: the groups' references
+    float weight[kGroups][kMaxUnit];    // and their factors of the output
+    float qscale[4][kMaxUnit];          // E4M3: factor of each query's logits, by segment
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barrier block");
 
@@ -801,7 +821,7 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
                             const float al = mn == mref[i] ? 1.f : ex2(mref[i] - mn);
                             l[i] *= al;
                             mref[i] = mn;
-                            if (rt == 0) B.alpha[wg][hl][i] = al;
+                            if (rt == 0) B.alpha[wg][hl * GM + i] = al;
                         }
                         hs::pair::named_sync(kSoftBar + wg, kSoftThreads);
                         hs::tc::fence_after_sync();
@@ -811,7 +831,7 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
                             hs::tc::tmem_ld8(o_own + uint32_t(cb), o);
                             hs::tc::tmem_wait_ld();
                             const int oc = cb % ocols;
-                            const float* al = &B.alpha[wg][oc / C::NP][oc % GM];
+                            const float* al = &B.alpha[wg][oc / C::NP * GM + oc % GM];
 #pragma unroll
                             for (int i = 0; i < 8; ++i) o[i] *= al[i];
                             hs::tc::tmem_st8(o_own + uint32_t(cb), o);
@@ -833,35 +853,28 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
                         ex2(x[i + 1] - (mref[i + 1] == -CUDART_INF_F ? 0.f : mref[i + 1]));
                     l[i] += p;
                     l[i + 1] += p2;
-                    if constexpr (KV == kBf16) {
-                        const __nv_bfloat162 hi = __floats2bfloat162_rn(p, p2);
-                        const float2 f = __bfloat1622float2(hi);
-                        const __nv_bfloat162 lo = __floats2bfloat162_rn(p - f.x, p2 - f.y);
-                        put16(i, __bfloat16_as_ushort(hi.x));
-                        put16(i + 1, __bfloat16_as_ushort(hi.y));
-                        put16(GM + i, __bfloat16_as_ushort(lo.x));
-                        put16(GM + i + 1, __bfloat16_as_ushort(lo.y));
-                    } else if constexpr (KV == kFp16) {
-                        const __half2 hi = __floats2half2_rn(p, p2);
-                        const float2 f = __half22float2(hi);
-                        const __half2 lo = __floats2half2_rn(p - f.x, p2 - f.y);
-                        put16(i, __half_as_ushort(hi.x));
-                        put16(i + 1, __half_as_ushort(hi.y));
-                        put16(GM + i, __half_as_ushort(lo.x));
-                        put16(GM + i + 1, __half_as_ushort(lo.y));
-                    } else {
-                        float r0 = p, r1 = p2;
+                    float r0 = p * C::up(-1), r1 = p2 * C::up(-1);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t cc = to_e4m3x2(r0, r1);
-                            put8(k * GM + i, cc);
-                            put8(k * GM + i + 1, cc >> 8);
-                            if (k < 3) {
-                                const float2 f = from_e4m3x2(cc);
-                                r0 = (r0 - f.x) * 16.f;
-                                r1 = (r1 - f.y) * 16.f;
-                            }
+                    for (int k = 0; k < C::kPParts; ++k) {
+                        float2 f;
+                        if constexpr (KV == kBf16) {
+                            const __nv_bfloat162 c = __floats2bfloat162_rn(r0, r1);
+                            f = __bfloat1622float2(c);
+                            put16(k * GM + i, __bfloat16_as_ushort(c.x));
+                            put16(k * GM + i + 1, __bfloat16_as_ushort(c.y));
+                        } else if constexpr (KV == kFp16) {
+                            const __half2 c = __floats2half2_rn(r0, r1);
+                            f = __half22float2(c);
+                            put16(k * GM + i, __half_as_ushort(c.x));
+                            put16(k * GM + i + 1, __half_as_ushort(c.y));
+                        } else {
+                            const uint32_t c = to_e4m3x2(r0, r1);
+                            f = from_e4m3x2(c);
+                            put8(k * GM + i, c);
+                            put8(k * GM + i + 1, c >> 8);
                         }
+                        r0 = (r0 - f.x) * C::up(k);
+                        r1 = (r1 - f.y) * C::up(k);
                     }
                 }
                 // Rows that are not attended to hold anything (places behind
@@ -916,7 +929,7 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
                         make_float4(l[i], l[i + 1], l[i + 2], l[i + 3]);
             if (rt == 0)
 #pragma unroll
-                for (int i = 0; i < GM; ++i) B.ml[wg][hl][i][0] = mref[i];
+                for (int i = 0; i < GM; ++i) B.m[wg][hl * GM + i] = mref[i];
             hs::pair::named_sync(kBothBar, kGroups * kSoftThreads);
             // A thread per query of the unit: both groups' sums, the unit's
             // maximum, and the factors that join their outputs.
@@ -931,7 +944,7 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
                     for (int j = 0; j < (8 >> lhs); ++j)
                         lw[w] += B.red[w][((((j >> lg) << lhs) + h) << lg) + (j & ((1 << lg) - 1))][i];
                 }
-                const float m0 = B.ml[0][h][i][0], m1 = B.ml[1][h][i][0];
+                const float m0 = B.m[0][e], m1 = B.m[1][e];
                 const float M = fmaxf(m0, m1), ref = M == -CUDART_INF_F ? 0.f : M;
                 const float f0 = exp2f(m0 - ref), f1 = exp2f(m1 - ref);
                 const float L = fmaf(f0, lw[0], f1 * lw[1]);
@@ -953,8 +966,9 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
                         a.part_ml[2 * k + 1] = L;
                     }
                 }
-                B.weight[0][h][i] = f0 * inv;
-                B.weight[1][h][i] = f1 * inv;
+                inv *= 1.f / C::up(-1);
+                B.weight[0][e] = f0 * inv;
+                B.weight[1][e] = f1 * inv;
             }
             hs::pair::named_sync(kBothBar, kGroups * kSoftThreads);
             // A CTA of a cluster has one segment: its rings are free by now.
@@ -971,19 +985,26 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
 #pragma unroll
                 for (int w = 0; w < kGroups; ++w) {
                     if (!(w == 0 ? has0 : has1)) continue;
-                    float o[C::NP];
-                    tmem_ld<C::NP>(o_addr + uint32_t((w * C::kSubs + s) * ocols + h * C::NP), o);
-                    hs::tc::tmem_wait_ld();
+                    // The parts from the last to the first, a few at a time.
+                    constexpr int kAt = C::NP <= 48 ? C::kPParts : C::kPParts / 2;
+                    float sum[GM];
 #pragma unroll
-                    for (int i = 0; i < GM; ++i) {
-                        float v;
-                        if constexpr (E4)
-                            v = fmaf(fmaf(fmaf(o[3 * GM + i], 0.0625f, o[2 * GM + i]), 0.0625f,
-                                          o[GM + i]), 0.0625f, o[i]);
-                        else
-                            v = o[i] + o[GM + i];
-                        O[i] = fmaf(v, B.weight[w][h][i], O[i]);
+                    for (int k0 = C::kPParts - kAt; k0 >= 0; k0 -= kAt) {
+                        float o[kAt * GM];
+                        tmem_ld<kAt * GM>(o_addr + uint32_t((w * C::kSubs + s) * ocols + h * C::NP +
+                                                            k0 * GM), o);
+                        hs::tc::tmem_wait_ld();
+#pragma unroll
+                        for (int k = kAt - 1; k >= 0; --k)
+#pragma unroll
+                            for (int i = 0; i < GM; ++i)
+                                sum[i] = k0 + k + 1 == C::kPParts
+                                             ? o[k * GM + i]
+                                             : fmaf(sum[i], 1.f / C::up(k0 + k), o[k * GM + i]);
                     }
+#pragma unroll
+                    for (int i = 0; i < GM; ++i)
+                        O[i] = fmaf(sum[i], B.weight[w][h * GM + i], O[i]);
                 }
                 if (d >= D) continue;
                 const int64_t qh = int64_t(row) * a.heads + (kvh0 + h) * group + gc * GM;
