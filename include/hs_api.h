@@ -587,7 +587,8 @@ int hs_paged_decode(const void* q, int64_t q_stride, int32_t q_dtype, const void
  * first in the order
  *   protected tokens, then higher score, then lower place,
  * where a token is protected if its position is below num_sinks or at least
- * next_pos[r] - recent.  Scores order as numbers, NaN below all.  Kept tokens
+ * next_pos[r] - recent (these may be more than the budget; then some go, by
+ * score).  Scores order as numbers, NaN below all.  Kept tokens
  * below place `budget` stay where they are; the others move into the holes,
  * the j-th such token (by place) into the j-th hole.  No source is a
  * destination, so the moves may run in any order, and repeating them changes
