@@ -182,13 +182,18 @@ __device__ __forceinline__ int block_excl_scan(int v, int* scratch, int* total) 
 // ----------------------------------------------------------------------------
 // Programmatic dependent launch (PTX griddepcontrol).  Every kernel of the
 // library lets its dependents start launching (pdl_trigger) at once, except
-// the fp8 row reconstruction, which does so when it is done, and
-// the kernels on the decode step's critical path are launched with
-// programmatic stream serialization, so each may start while its stream
-// predecessor still runs.  Rule kept by every such kernel: before pdl_wait
-// it writes no global memory and reads only inputs that no kernel of this
-// library writes (the query); pdl_wait returns once the predecessor grid has
-// completed and its writes are visible (at once when there is none).
+// the fp8 row reconstruction, which does so when it is done, and the paged
+// attention kernels, which do so after their own pdl_wait.  The kernels on
+// the decode step's critical path are launched with programmatic stream
+// serialization, so each may start while its stream predecessor still runs.
+// Rule kept by every such kernel: before pdl_wait it writes no global memory
+// and reads only inputs that no kernel of this library writes (the query), or
+// that its predecessor has already waited for (the lengths of a paged decode,
+// in its finishing kernel); pdl_wait returns once the predecessor grid has
+// completed and its writes are visible (at once when there is none).  What a
+// predecessor may write is read with plain loads: the read-only path (__ldg)
+// is for data that stays as it is as long as the kernel runs, and the kernel
+// may have started before the predecessor wrote.
 __device__ __forceinline__ void pdl_trigger() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

@@ -377,7 +377,7 @@ struct MoveArgs {
 __device__ __forceinline__ int64_t place_of(const MoveArgs& a, const int32_t* table, int i) {
     const int b = i / a.page_size;
     if (i < 0 || b >= a.max_blocks) return -1;
-    const int page = __ldg(table + b);
+    const int page = table[b];
     if (page < 0 || page >= a.num_pages) return -1;
     return page * a.page_stride + (i - b * a.page_size) * a.row_stride;
 }

@@ -245,7 +245,7 @@ __device__ __forceinline__ void write_head(const PagedArgs& a, int64_t qh, int k
     using S = MergeState<D>;
     const int lane = threadIdx.x & 31;
     float f = s.l == 0.f ? 0.f : 1.f / s.l;
-    if (a.v_scale != nullptr && s.l != 0.f) f *= __ldg(a.v_scale + kvh);
+    if (a.v_scale != nullptr && s.l != 0.f) f *= a.v_scale[kvh];
 #pragma unroll
     for (int i = 0; i < S::PL; ++i) {
         if (S::V4 < 32 && lane >= S::V4) break;

@@ -93,7 +93,7 @@ struct Cursor {
     Tiling v;
 };
 __device__ __forceinline__ void cursor_row(Cursor& c, const PagedArgs& a, int lth) {
-    c.v = tiling_of(a, __ldg(a.seq_lens + c.row), lth);
+    c.v = tiling_of(a, a.seq_lens[c.row], lth);
 }
 __device__ __forceinline__ bool last_of_segment(const Cursor& c) {
     return c.left == 1 || c.tile == c.v.n - 1;
@@ -189,7 +189,7 @@ __device__ __forceinline__ Run make_run(const PagedArgs& a, int cta) {
     int t0 = 0, t1 = 0, n0 = 0, n1 = 0;  // tiles of one request; places of this lane's
 #pragma unroll 4
     for (int r = lane; r < a.rows; r += 32) {
-        const int len = __ldg(a.seq_lens + r);
+        const int len = a.seq_lens[r];
         t0 = tiling_of(a, len, a.lth[0]).n;
         t1 = tiling_of(a, len, a.lth[1]).n;
         n0 += places(a, t0);
@@ -212,7 +212,7 @@ __device__ __forceinline__ Run make_run(const PagedArgs& a, int cta) {
         const int r = r0 + lane;
         int n = narrow ? t1 : t0;
         if (a.rows > 32)
-            n = r < a.rows ? tiling_of(a, __ldg(a.seq_lens + r), a.lth[x.way]).n : 0;
+            n = r < a.rows ? tiling_of(a, a.seq_lens[r], a.lth[x.way]).n : 0;
         else if (r >= a.rows)
             n = 0;
         const int np = places(a, n);
@@ -250,7 +250,7 @@ __device__ __forceinline__ Run unit_run(const PagedArgs& a, int unit, int rank) 
     x.chunks = a.chunks[1];
     x.row = unit / x.chunks;
     x.chunk = unit - x.row * x.chunks;
-    const int n = tiling_of(a, __ldg(a.seq_lens + x.row), a.lth[1]).n;
+    const int n = tiling_of(a, a.seq_lens[x.row], a.lth[1]).n;
     x.tile = n * rank / a.cl;
     x.run = n * (rank + 1) / a.cl - x.tile;
     return x;

@@ -204,7 +204,7 @@ paged_kernel(const __grid_constant__ PagedArgs a) {
         uint32_t qa[D / 16][2 * GH];
         float qs[GH];  // factor of the row's logits, log2 units
         {
-            const float ksc = a.k_scale != nullptr ? __ldg(a.k_scale + kvh) : 1.f;
+            const float ksc = a.k_scale != nullptr ? a.k_scale[kvh] : 1.f;
 #pragma unroll
             for (int hh = 0; hh < GH; ++hh) {
                 const int hr = g + 8 * hh;
@@ -219,11 +219,11 @@ paged_kernel(const __grid_constant__ PagedArgs a) {
                     // meet (below), the same on both sides of the product.
                     if constexpr (KV != kE4m3) {
                         const uint32_t* p = reinterpret_cast<const uint32_t*>(qp + ks * 16);
-                        qa[ks][hh] = hr < Gc ? __ldg(p + t) : 0u;
-                        qa[ks][GH + hh] = hr < Gc ? __ldg(p + 4 + t) : 0u;
+                        qa[ks][hh] = hr < Gc ? p[t] : 0u;
+                        qa[ks][GH + hh] = hr < Gc ? p[4 + t] : 0u;
                     } else {
                         const int d0 = (ks >> 2) * 64 + t * 16 + (ks & 3) * 4;
-                        const uint2 u = hr < Gc ? __ldg(reinterpret_cast<const uint2*>(qp + d0))
+                        const uint2 u = hr < Gc ? *reinterpret_cast<const uint2*>(qp + d0)
                                                 : make_uint2(0u, 0u);
                         qa[ks][hh] = u.x;
                         qa[ks][GH + hh] = u.y;
@@ -287,12 +287,12 @@ paged_kernel(const __grid_constant__ PagedArgs a) {
             return j < steps && visible(vis, tok) ? tok : -1;
         };
         int tok_n = token(0);
-        int page_n = tok_n >= 0 ? __ldg(table + block_of(a, tok_n)) : -1;
+        int page_n = tok_n >= 0 ? table[block_of(a, tok_n)] : -1;
         auto issue = [&](int j) {
             const int tok = tok_n;
             int page = page_n;
             tok_n = token(j + 1);
-            page_n = tok_n >= 0 ? __ldg(table + block_of(a, tok_n)) : -1;
+            page_n = tok_n >= 0 ? table[block_of(a, tok_n)] : -1;
             if (page >= a.num_pages || (tok >= 0 && page < 0)) bad = true;
             const bool ok = tok >= 0 && page >= 0 && page < a.num_pages;
             const int64_t off =
@@ -512,7 +512,7 @@ paged_kernel(const __grid_constant__ PagedArgs a) {
             if (whole) {
                 const int64_t qh = int64_t(row) * a.heads + kv * group + gc * GM + hg;
                 float r = L == 0.f ? 0.f : O / L;
-                if (a.v_scale != nullptr && L != 0.f) r *= __ldg(a.v_scale + kv);
+                if (a.v_scale != nullptr && L != 0.f) r *= a.v_scale[kv];
                 const bool bf = KV == kBf16 || (KV == kE4m3 && !a.q_is_half);
                 if (bf) static_cast<__nv_bfloat16*>(a.out)[qh * D + d] = __float2bfloat16_rn(r);
                 else static_cast<__half*>(a.out)[qh * D + d] = __float2half_rn(r);

@@ -285,8 +285,8 @@ __device__ __noinline__ void query_parts(const PagedArgs& a, Bars& B, unsigned c
             static_cast<const char*>(a.q) +
             (int64_t(row) * a.q_stride + int64_t((kvh0 + hl) * group + gc * GM + gi) * D +
              ch * 16) * 2);
-        raw[0] = __ldg(p);
-        raw[1] = __ldg(p + 1);
+        raw[0] = *p;
+        raw[1] = p[1];
     }
     float x[16];
     const uint32_t w[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w,
@@ -338,7 +338,7 @@ __device__ __noinline__ void query_parts(const PagedArgs& a, Bars& B, unsigned c
     }
     if (ch == 0) {
         float f = a.scale_log2 * pow2(-ea) * pow2(-eb);
-        if (a.k_scale != nullptr) f *= __ldg(a.k_scale + kvh0 + hl);
+        if (a.k_scale != nullptr) f *= a.k_scale[kvh0 + hl];
         B.qscale[seg & 3][hl * GM + gi] = f;
     }
 }
@@ -444,7 +444,7 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
         auto lookup = [&](const Cursor& x, int& tok) {
             tok = tile_token(x, lth) + (run_i << lbt);
             if (!lane_in || !any_visible(x.v, tok, bt)) return -2;
-            return __ldg(a.block_table + int64_t(x.row) * a.bt_stride + block_of(a, tok));
+            return a.block_table[int64_t(x.row) * a.bt_stride + block_of(a, tok)];
         };
         int tok_n, page_n = lookup(c, tok_n);
         for (; ok;) {
@@ -957,7 +957,7 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
                         if (a.lse != nullptr) a.lse[qh] = lg * kLn2;
                         if (a.lse2 != nullptr) a.lse2[qh] = lg;
                         inv = L == 0.f ? 0.f : 1.f / L;
-                        if (a.v_scale != nullptr && L != 0.f) inv *= __ldg(a.v_scale + kvh0 + h);
+                        if (a.v_scale != nullptr && L != 0.f) inv *= a.v_scale[kvh0 + h];
                     } else if (cl > 0) {
                         B.join_ml[h * GM + i] = make_float2(M, L);
                     } else {
@@ -1071,7 +1071,7 @@ paged_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUten
                 sum.y = fmaf(f, o[c].y, sum.y);
             }
             float inv = L == 0.f ? 0.f : 1.f / L;
-            if (a.v_scale != nullptr && L != 0.f) inv *= __ldg(a.v_scale + kvh0 + h);
+            if (a.v_scale != nullptr && L != 0.f) inv *= a.v_scale[kvh0 + h];
             const int64_t qh = qh0 + h * group + i;
             sum.x *= inv;
             sum.y *= inv;
