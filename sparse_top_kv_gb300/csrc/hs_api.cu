@@ -1,6 +1,7 @@
 // hs_api.cu -- host-side helpers of the C ABI (status strings, pinned host
 // pointers, device properties).
 #include "hs_common.cuh"
+#include "hs_shared.h"
 
 extern "C" const char* hs_status_string(int status) {
     switch (status) {
@@ -78,32 +79,35 @@ int num_sms() {
     static int cache[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 1;
-    if (dev >= 0 && dev < 64 && cache[dev] > 0) return cache[dev];
-    int n = 1;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-        n = 1;
-    if (dev >= 0 && dev < 64) cache[dev] = n;
-    return n;
+    const auto ask = [dev] {
+        int n = 1;
+        return cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
+                       n > 0
+                   ? n
+                   : 1;
+    };
+    return dev >= 0 && dev < 64 ? ask_once(&cache[dev], ask) : ask();
 }
 
 int ensure_dynamic_smem(const void* func, size_t bytes, int* cache) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return HS_ERR_CUDA;
-    if (dev >= 0 && dev < 64 && cache[dev] >= int(bytes)) return HS_OK;
-    cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, func) != cudaSuccess) return HS_ERR_CUDA;
-    int optin = 0;
-    if (cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) !=
-        cudaSuccess)
-        return HS_ERR_CUDA;
-    if (bytes + fa.sharedSizeBytes > size_t(optin)) return HS_ERR_CAPACITY;
-    // Without the opt-in, static + dynamic shared memory must fit 48 KB.
-    if (bytes + fa.sharedSizeBytes > 48 * 1024 &&
-        cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes)) !=
+    int none = 0;
+    return raise_limit(dev >= 0 && dev < 64 ? &cache[dev] : &none, int(bytes), [&](int n) -> int {
+        cudaFuncAttributes fa;
+        if (cudaFuncGetAttributes(&fa, func) != cudaSuccess) return HS_ERR_CUDA;
+        int optin = 0;
+        if (cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) !=
             cudaSuccess)
-        return HS_ERR_CUDA;
-    if (dev >= 0 && dev < 64) cache[dev] = int(bytes);
-    return HS_OK;
+            return HS_ERR_CUDA;
+        if (n + fa.sharedSizeBytes > size_t(optin)) return HS_ERR_CAPACITY;
+        // Without the opt-in, static + dynamic shared memory must fit 48 KB.
+        if (n + fa.sharedSizeBytes > 48 * 1024 &&
+            cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, n) !=
+                cudaSuccess)
+            return HS_ERR_CUDA;
+        return HS_OK;
+    });
 }
 
 }  // namespace hs_host

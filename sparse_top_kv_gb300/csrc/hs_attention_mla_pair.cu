@@ -49,6 +49,7 @@
 
 #include "hs_attention_internal.cuh"
 #include "hs_pair.cuh"
+#include "hs_shared.h"
 #include "hs_tcgen05.cuh"
 
 namespace hs_attn {
@@ -943,8 +944,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kThreads, 1)
 namespace {
 int g_smem_set2[64] = {};
 int g_smem_set4[64] = {};
-int g_clusters4[64];
-bool g_clusters4_init = false;
+int g_clusters4[64] = {};  // resident clusters of four, plus one
 }  // namespace
 
 bool mla_pair_cluster_merge(int rows, int splits) {
@@ -953,11 +953,7 @@ bool mla_pair_cluster_merge(int rows, int splits) {
     // waits for the other pair of the cluster).
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
-    if (!g_clusters4_init) {
-        for (int i = 0; i < 64; ++i) g_clusters4[i] = -1;
-        g_clusters4_init = true;
-    }
-    if (g_clusters4[dev] < 0) {
+    const auto ask = [] {
         int n = 0;
         if (hs_host::ensure_dynamic_smem(reinterpret_cast<const void*>(mla_pair_kernel<4>),
                                          size_t(kSmemBytes), g_smem_set4) == HS_OK) {
@@ -970,9 +966,9 @@ bool mla_pair_cluster_merge(int rows, int splits) {
                 n = 0;
             }
         }
-        g_clusters4[dev] = n;
-    }
-    return rows <= g_clusters4[dev];
+        return n + 1;
+    };
+    return rows < hs_host::ask_once(&g_clusters4[dev], ask);
 }
 
 int launch_mla_pair(const MlaArgs& a, int pairs, hs_stream_t stream) {

@@ -29,6 +29,7 @@
 
 #include "hs_common.cuh"
 #include "hs_fp8.cuh"
+#include "hs_shared.h"
 
 namespace {
 
@@ -115,17 +116,15 @@ __global__ void __launch_bounds__(kThreads, 3) fp8ds_gather_kernel(const GatherA
 
 int gather_ctas_per_sm() {
     static int per_sm = 0;
-    if (per_sm == 0) {
+    return hs_host::ask_once(&per_sm, [] {
         int n = 0;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fp8ds_gather_kernel, kThreads, 0) !=
-                cudaSuccess ||
-            n <= 0) {
-            cudaGetLastError();
-            n = 1;
-        }
-        per_sm = n;
-    }
-    return per_sm;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fp8ds_gather_kernel, kThreads, 0) ==
+                cudaSuccess &&
+            n > 0)
+            return n;
+        cudaGetLastError();
+        return 1;
+    });
 }
 
 int64_t align256(int64_t x) { return (x + 255) & ~int64_t(255); }

@@ -49,6 +49,7 @@
 
 #include "hs_paged.cuh"
 #include "hs_pair.cuh"
+#include "hs_shared.h"
 #include "hs_tcgen05.cuh"
 
 namespace hs_paged {
@@ -1137,16 +1138,16 @@ inline int cluster_way(PagedArgs& a, const void* kern, size_t smem, int tile_byt
             const int64_t each = hs::max64(1, (tiles + cl - 1) / cl);
             const int64_t cost = 2 * each + (cl == 1 ? 0 : a.hs[way] == 1 ? 5 : 9);
             if (each > few || cost >= best) continue;
-            int& fit = resident[dev][cl];
-            if (cl > 1 && fit == 0) {
+            const auto ask = [&] {
+                int n = 0;
                 cudaLaunchAttribute attr[2];
                 const cudaLaunchConfig_t cfg = cluster_config(attr, 1, cl, smem);
-                if (cudaOccupancyMaxActiveClusters(&fit, kern, &cfg) != cudaSuccess || fit < 1) {
-                    cudaGetLastError();
-                    fit = -1;
-                }
-            }
-            if (cl > 1 && units > fit) continue;
+                if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0)
+                    return n;
+                cudaGetLastError();
+                return -1;
+            };
+            if (cl > 1 && units > hs_host::ask_once(&resident[dev][cl], ask)) continue;
             best = cost;
             a.cl = cl;
         }
