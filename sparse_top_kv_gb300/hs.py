@@ -165,6 +165,12 @@ def _check(t, dtype, name, cuda=True):
         raise ValueError(f"{name}: must be a CUDA tensor or pinned host memory")
 
 
+def _check_workspace(t):
+    """Scratch is one run of bytes: numel elements from the tensor's start."""
+    if t is not None and not t.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
+
+
 def wait_selftest(mode, timeout_ns, *, stream=None):
     """Bounded-wait self-test (hs_wait_selftest); returns (status, elapsed_ns)."""
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
@@ -391,6 +397,7 @@ def sparse_decode(q, k_base, v_base, row_stride, kv_head_stride, num_kv_rows, kv
     if lse is None:
         lse = torch.empty(rows, heads, dtype=torch.float32, device=q.device)
     ws = sparse_decode_workspace_bytes(rows, heads, kv_heads, cap, d_qk, d_v)
+    _check_workspace(workspace)
     if ws > 0 and (workspace is None or workspace.numel() * workspace.element_size() < ws):
         workspace = torch.empty(ws, dtype=torch.uint8, device=q.device)
     _call("hs_sparse_decode", _ptr(q), _ptr(k_base), _ptr(v_base), row_stride, kv_head_stride,
@@ -466,6 +473,7 @@ def sparse_decode_fp8ds(q, kv8, kv_rows, count, scale, *, out=None, lse=None, wo
     if lse is None:
         lse = torch.empty(rows, heads, dtype=torch.float32, device=q.device)
     ws = sparse_decode_fp8ds_workspace_bytes(rows, heads, cap)
+    _check_workspace(workspace)
     if workspace is None or workspace.numel() * workspace.element_size() < ws:
         workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=q.device)
     _call("hs_sparse_decode_fp8ds", _ptr(q), _ptr(kv8), kv8.shape[1], kv8.shape[0],
@@ -693,9 +701,10 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, *, window=0,
     strides; block_table int32 [rows, blocks]; seq_lens int32 [rows]; max_len
     bounds seq_lens (default: what block_table and score hold).  score fp32
     [rows, >= max_len]: running scores, updated in place with the tokens'
-    attention weights summed over the heads.  workspace: a CUDA tensor, used
-    if it is large enough (paged_decode_workspace_bytes).  Returns (out [rows,
-    heads, d] of q's type, lse fp32 [rows, heads])."""
+    attention weights summed over the heads.  workspace: a contiguous CUDA
+    tensor, used if it is large enough (paged_decode_workspace_bytes).  Returns
+    (out [rows, heads, d] of q's type, lse fp32 [rows, heads]).  A call with out,
+    lse and workspace given takes the shortest way through the binding."""
     dev = torch._C._cuda_getDevice()
     if _binding is not None:
         rc = _binding.paged_decode(dev, _raw_stream(dev, stream), q, k_cache, v_cache,
@@ -773,6 +782,7 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, *, window=0,
         if workspace is not None:
             if workspace.get_device() != dev:
                 raise ValueError("workspace: must be on q's device")
+            _check_workspace(workspace)
             ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
         rc = call(q.data_ptr(), q_stride, _ELEMENT[qt], k_cache.data_ptr(), v_cache.data_ptr(),
                   _ELEMENT[kt], ps, rs, hstr, num_pages, page_size, block_table.data_ptr(),
