@@ -144,7 +144,7 @@ PyObject* paged_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* status = nullptr;
     if (a[18] != Py_None) {
         const Tensor s = look(a[18], device);
-        if (!s.ok || s.dtype != at::kInt) return general();
+        if (!s.ok || s.dtype != at::kInt || s.bytes < 4) return general();
         status = s.ptr;
     }
     int rc;
@@ -230,7 +230,7 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* status = nullptr;
     if (a[17] != Py_None) {
         const Tensor s = look(a[17], device);
-        if (!s.ok || s.dtype != at::kInt) return general();
+        if (!s.ok || s.dtype != at::kInt || s.bytes < 4) return general();
         status = s.ptr;
     }
     int rc;

@@ -644,11 +644,16 @@ def _output(t, dtype, name, device, shape):
     return t.data_ptr()
 
 
-def _status_ptr(status):
+def _status_ptr(status, device):
+    """Address of a status word on CUDA device `device` or in pinned host memory."""
     if status is None:
         return None
-    if status.dtype is not _I or not status.is_cuda:
+    if status.numel() < 1:
+        raise ValueError("status: needs a word")
+    if status.dtype is not _I or status.get_device() != device:
         _check(status, _I, "status")
+        if status.is_cuda:
+            raise ValueError(f"status: on {status.device}, expected cuda:{device}")
         return _ptr(status)
     return status.data_ptr()
 
@@ -789,7 +794,7 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, *, window=0,
                   block_table.stride(0) if rows > 1 else blocks, blocks, max_len,
                   seq_lens.data_ptr(), k_scale_ptr, v_scale_ptr, rows, heads, kv_heads, d, window,
                   num_sinks, scale, score_ptr, score_stride, score_decay, out.data_ptr(),
-                  lse.data_ptr(), ws, ws_bytes, None if status is None else _status_ptr(status),
+                  lse.data_ptr(), ws, ws_bytes, None if status is None else _status_ptr(status, dev),
                   _raw_stream(dev, stream))
         if rc != 3 or again:
             break
@@ -878,7 +883,7 @@ def evict_select(score, seq_lens, budget, *, max_len=None, recent=0, num_sinks=0
     dev, args, result = _evict_args(score, seq_lens, budget, max_len, recent, num_sinks,
                                     positions, next_pos, score_out, positions_out, lens_out,
                                     moves, stream)
-    rc = lib().hs_evict_select(*args, _status_ptr(status), _raw_stream(dev, stream))
+    rc = lib().hs_evict_select(*args, _status_ptr(status, dev), _raw_stream(dev, stream))
     if rc != HS_OK:
         raise HSError("hs_evict_select", rc)
     return result
@@ -896,7 +901,7 @@ def evict_move(moves, k_cache, v_cache, block_table, *, status=None, stream=None
     lists = (_output(src, _I, "moves[0]", dev, shape), _output(dst, _I, "moves[1]", dev, shape),
              _vector(count, _I, "moves[2]", dev, rows))
     rc = lib().hs_evict_move(*_move_args(k_cache, v_cache, block_table, rows, dev), *lists, rows,
-                             cap, _status_ptr(status), _raw_stream(dev, stream))
+                             cap, _status_ptr(status, dev), _raw_stream(dev, stream))
     if rc != HS_OK:
         raise HSError("hs_evict_move", rc)
 
@@ -921,7 +926,7 @@ def evict(score, seq_lens, budget, k_cache, v_cache, block_table, *, max_len=Non
                                     positions, next_pos, score_out, positions_out, lens_out,
                                     moves, stream)
     rc = lib().hs_evict(*args, *_move_args(k_cache, v_cache, block_table, score.shape[0], dev),
-                        _status_ptr(status), _raw_stream(dev, stream))
+                        _status_ptr(status, dev), _raw_stream(dev, stream))
     if rc != HS_OK:
         raise HSError("hs_evict", rc)
     return result
