@@ -535,10 +535,17 @@ class BudgetedDecoder:
             R, heads, kv_heads, d, capacity, with_score=True), dtype=torch.uint8, device=dev)
         self.graph = None
 
-    def start(self, r, k, v):
+    def start(self, r, k, v, *, score=None, q=None):
         """Begin a request in place r with its prompt's rows k, v [tokens,
         kv_heads, d] (at most capacity - 1 tokens, so that the first step's
-        token has room)."""
+        token has room).
+
+        The first step cuts a prompt longer than the budget by the scores that
+        it finds.  `score` fp32 [tokens] gives them; `q` [queries, heads, d] are
+        the queries of the prompt's last tokens, whose attention to the tokens
+        up to their own is added, as `step` does for a new token.  With neither
+        all scores are 0: the protected tokens stay, and the first of the
+        others."""
         n = k.shape[0]
         if not 0 < n < self.capacity:
             raise ValueError(f"prompt: 1 to {self.capacity - 1} tokens")
@@ -548,8 +555,30 @@ class BudgetedDecoder:
             cache[page, t % self.page_size] = rows.to(cache)
         self.positions[r, :n] = t.to(torch.int32)
         self.score[r].zero_()
+        if score is not None:
+            self.score[r, :n] = score
+        if q is not None:
+            self._score_prompt(r, n, q)
         self.seq_lens[r] = n
         self.next_pos[r] = n
+
+    def _score_prompt(self, r, n, q, at_once=64):
+        """score[r] := decay * score[r] + weights, query by query; `at_once` of
+        them are requests of one call, which share the pages."""
+        total = self.score[r, :n]
+        for i in range(0, q.shape[0], at_once):
+            part = q[i:i + at_once]
+            c = part.shape[0]
+            last = n - q.shape[0] + i + 1  # tokens up to the first query's own
+            lens = torch.arange(last, last + c, dtype=torch.int32, device=self.device)
+            w = torch.zeros(c, n, dtype=torch.float32, device=self.device)
+            hs.paged_decode(part, self.k_cache, self.v_cache,
+                            self.block_table[r].expand(c, -1).contiguous(), lens, self.scale,
+                            max_len=n, score=w)
+            if self.score_decay != 1.0:
+                w *= self.score_decay ** torch.arange(c - 1, -1, -1, device=self.device)[:, None]
+                total *= self.score_decay ** c
+            total += w.sum(0)
 
     def stop(self, r):
         """Free place r."""
