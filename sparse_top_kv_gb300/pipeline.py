@@ -504,6 +504,8 @@ class BudgetedDecoder:
             raise ValueError("capacity: more than the budget, for the new token")
         if dtype not in (torch.bfloat16, torch.float16):
             raise TypeError(f"dtype: torch.bfloat16 or torch.float16, got {dtype}")
+        if budget < 1:
+            raise ValueError("budget: at least one token")
         if recent < 0 or num_sinks < 0 or recent + num_sinks > budget:
             raise ValueError("recent, num_sinks: within the budget")
         self.device = torch.device(device)
@@ -549,6 +551,15 @@ class BudgetedDecoder:
         n = k.shape[0]
         if not 0 < n < self.capacity:
             raise ValueError(f"prompt: 1 to {self.capacity - 1} tokens")
+        self._check_shape("k", k, n, self.kv_heads, self.d)
+        self._check_shape("v", v, n, self.kv_heads, self.d)
+        if score is not None:
+            self._check_shape("score", score, n)
+        if q is not None:
+            if not 0 < q.shape[0] <= n:
+                raise ValueError(f"q: 1 to {n} queries")
+            self._check_shape("q", q, q.shape[0], self.heads, self.d)
+            q = q.to(self.k_cache)
         t = torch.arange(n, device=self.device)
         page = self.block_table[r].long()[t // self.page_size]
         for cache, rows in ((self.k_cache, k), (self.v_cache, v)):
@@ -580,6 +591,16 @@ class BudgetedDecoder:
                 total *= self.score_decay ** c
             total += w.sum(0)
 
+    def _check_shape(self, name, t, *shape):
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name}: expected {shape}, got {tuple(t.shape)}")
+
+    def _check_rows(self, q, k_new, v_new):
+        R = self.num_reqs
+        self._check_shape("q", q, R, self.heads, self.d)
+        self._check_shape("k_new", k_new, R, self.kv_heads, self.d)
+        self._check_shape("v_new", v_new, R, self.kv_heads, self.d)
+
     def stop(self, r):
         """Free place r."""
         self.seq_lens[r] = 0
@@ -589,7 +610,16 @@ class BudgetedDecoder:
         """One token of every active request: q [R, heads, d], its K and V rows
         k_new, v_new [R, kv_heads, d].  Evicts what is past the budget, appends
         the rows, attends, and adds the weights to the scores.  Returns (out
-        [R, heads, d], lse fp32 [R, heads]); inactive places give 0 and -inf."""
+        [R, heads, d], lse fp32 [R, heads]); inactive places give 0 and -inf.
+        A call that is refused leaves the state as it was."""
+        self._check_rows(q, k_new, v_new)
+        for name, t in (("q", q), ("k_new", k_new), ("v_new", v_new)):
+            if t.dtype != self.k_cache.dtype:
+                raise TypeError(f"{name}: expected {self.k_cache.dtype}, got {t.dtype}")
+            if t.device != self.k_cache.device:
+                raise ValueError(f"{name}: on {t.device}, expected {self.k_cache.device}")
+        if not q.is_contiguous() and q.stride()[1:] != (self.d, 1):
+            raise ValueError("q: heads must be packed")
         hs.evict(self.score, self.seq_lens, self.budget, self.k_cache, self.v_cache,
                  self.block_table, max_len=self.capacity, recent=self.recent,
                  num_sinks=self.num_sinks, positions=self.positions, next_pos=self.next_pos,
@@ -626,6 +656,9 @@ class BudgetedDecoder:
 
     def replay(self, q, k_new, v_new):
         """One step through the captured graph."""
+        if self.graph is None:
+            raise ValueError("replay: capture a step first")
+        self._check_rows(q, k_new, v_new)
         self.graph_q.copy_(q, non_blocking=True)
         self.graph_k.copy_(k_new, non_blocking=True)
         self.graph_v.copy_(v_new, non_blocking=True)
