@@ -9,6 +9,7 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import warnings
 
 import torch
 
@@ -111,12 +112,17 @@ def lib():
 
 def _load_binding():
     global _binding
-    if not os.path.exists(_build.BINDING):
+    path = _build.binding_path()
+    if path is None or not os.path.exists(path):
         return
-    loader = importlib.machinery.ExtensionFileLoader("_hs_binding", _build.BINDING)
-    mod = importlib.util.module_from_spec(
-        importlib.util.spec_from_loader("_hs_binding", loader))
-    loader.exec_module(mod)
+    loader = importlib.machinery.ExtensionFileLoader("_hs_binding", path)
+    try:
+        mod = importlib.util.module_from_spec(
+            importlib.util.spec_from_loader("_hs_binding", loader))
+        loader.exec_module(mod)
+    except ImportError as e:  # every call has its way through ctypes
+        warnings.warn(f"the extension of the hot calls does not load: {e}")
+        return
     _binding = mod
 
 
