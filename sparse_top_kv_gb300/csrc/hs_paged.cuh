@@ -92,9 +92,6 @@ struct Cursor {
     bool first;                  // this tile starts a segment (a unit, or the run)
     Tiling v;
 };
-__device__ __forceinline__ void cursor_row(Cursor& c, const PagedArgs& a, int lth) {
-    c.v = tiling_of(a, a.seq_lens[c.row], lth);
-}
 __device__ __forceinline__ bool last_of_segment(const Cursor& c) {
     return c.left == 1 || c.tile == c.v.n - 1;
 }
@@ -108,7 +105,7 @@ __device__ __forceinline__ void advance(Cursor& c, const PagedArgs& a, int chunk
     c.chunk = 0;
     do {  // the next request with a token; there is one, as left > 0
         ++c.row;
-        cursor_row(c, a, lth);
+        c.v = tiling_of(a, a.seq_lens[c.row], lth);
     } while (c.v.n == 0 && c.row + 1 < a.rows);
 }
 // On to the run's next segment (left = 0: there is none).
@@ -180,16 +177,18 @@ __device__ __forceinline__ int way_of(const PagedArgs& a, int total0) {
 // One CTA's run: `run` tiles from `tile` of chunk `chunk` of request `row` on.
 struct Run {
     int way, chunks, run, row, chunk, tile;
+    int len;  // of that request
 };
 // Every warp finds it for itself: a lane per request, a few dozen shuffles and
 // no barrier, so each role starts as soon as the lengths have arrived.
 __device__ __forceinline__ Run make_run(const PagedArgs& a, int cta) {
     constexpr uint32_t kAll = 0xffffffffu;
     const int lane = threadIdx.x & 31;
-    int t0 = 0, t1 = 0, n0 = 0, n1 = 0;  // tiles of one request; places of this lane's
+    int len = 0, t0 = 0, t1 = 0;  // one request's length and tiles
+    int n0 = 0, n1 = 0;           // places of this lane's
 #pragma unroll 4
     for (int r = lane; r < a.rows; r += 32) {
-        const int len = a.seq_lens[r];
+        len = a.seq_lens[r];
         t0 = tiling_of(a, len, a.lth[0]).n;
         t1 = tiling_of(a, len, a.lth[1]).n;
         n0 += places(a, t0);
@@ -206,15 +205,17 @@ __device__ __forceinline__ Run make_run(const PagedArgs& a, int cta) {
     // The requests that places v0 and v1 lie in (the last whose first place is
     // at or before them; requests without tiles share theirs with the next),
     // and how many tiles come before each place.
-    x.row = x.chunk = x.tile = 0;
+    x.row = x.chunk = x.tile = x.len = 0;
     int before0 = 0, before1 = 0;
     for (int r0 = 0, tiles = 0, place = 0; r0 < a.rows; r0 += 32) {
         const int r = r0 + lane;
         int n = narrow ? t1 : t0;
-        if (a.rows > 32)
-            n = r < a.rows ? tiling_of(a, a.seq_lens[r], a.lth[x.way]).n : 0;
-        else if (r >= a.rows)
+        if (a.rows > 32) {
+            len = r < a.rows ? a.seq_lens[r] : 0;
+            n = tiling_of(a, len, a.lth[x.way]).n;
+        } else if (r >= a.rows) {
             n = 0;
+        }
         const int np = places(a, n);
         const int at = place + hs::warp_incl_scan(np) - np;      // places before request r
         const int tl = tiles + hs::warp_incl_scan(n) - n;        // tiles before it
@@ -234,6 +235,7 @@ __device__ __forceinline__ Run make_run(const PagedArgs& a, int cta) {
         if (m0 != 0) {
             before0 = find(m0, v0, x.chunk, x.tile);
             x.row = r0 + 31 - __clz(m0);
+            x.len = __shfl_sync(kAll, len, 31 - __clz(m0));
         }
         if (m1 != 0) before1 = find(m1, v1, c1, i1);
         tiles = __shfl_sync(kAll, tl + n, 31);
@@ -250,7 +252,8 @@ __device__ __forceinline__ Run unit_run(const PagedArgs& a, int unit, int rank) 
     x.chunks = a.chunks[1];
     x.row = unit / x.chunks;
     x.chunk = unit - x.row * x.chunks;
-    const int n = tiling_of(a, a.seq_lens[x.row], a.lth[1]).n;
+    x.len = a.seq_lens[x.row];
+    const int n = tiling_of(a, x.len, a.lth[1]).n;
     x.tile = n * rank / a.cl;
     x.run = n * (rank + 1) / a.cl - x.tile;
     return x;
@@ -263,7 +266,7 @@ __device__ __forceinline__ void report_lengths(const PagedArgs& a) {
 __device__ __forceinline__ Cursor cursor_at(const PagedArgs& a, const Run& x) {
     Cursor c;
     c.row = x.row;
-    cursor_row(c, a, a.lth[x.way]);
+    c.v = tiling_of(a, x.len, a.lth[x.way]);
     c.chunk = x.chunk;
     c.tile = x.tile;
     c.left = x.run;
