@@ -626,7 +626,8 @@ int hs_paged_decode(const void* q, int64_t q_stride, int32_t q_dtype, const void
  * HS_ERR_BAD_INDEX.  The pages written must not be shared with another
  * request.
  *
- * hs_evict: hs_evict_select, then hs_evict_move with its lists.
+ * hs_evict: hs_evict_select, then hs_evict_move with its lists (one launch for
+ * all where max_len is at most 8 above the budget and at most 16384).
  * ------------------------------------------------------------------------- */
 int hs_evict_select(const float* score, int64_t score_stride, const int32_t* positions,
                     int64_t pos_stride, const int32_t* seq_lens, const int32_t* next_pos,

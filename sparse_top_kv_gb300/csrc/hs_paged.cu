@@ -73,8 +73,10 @@ bool tensor_map_ok(const PagedArgs& a, int kv_dtype, int d) {
 
 // Small calls of few requests with few query heads on a KV head run on the
 // warp-level kernel: it starts and ends a unit sooner than the tcgen05 kernel,
-// which is ahead where more is streamed, where more query heads share a row,
-// and where a cluster's CTAs have very few tiles each.  us, tcgen05 / warps,
+// which is ahead where more is streamed and where a cluster's CTAs have very
+// few tiles each (and mostly where more query heads share a row; but one to
+// eight requests of 2 K to 16 K with 64/8 heads are up to 41 % faster by warps:
+// 8 K 19.5 / 13.8).  us in captured graphs, tcgen05 / warps,
 // 32/8 heads of 128: one request of 2 K tokens 10.6 / 8.9, 16 K 24.6 / 19.6,
 // eight of up to 4 K 18.5 / 16.4, eight of 16 K 88.3 / 92.1, 16 of up to 1 K
 // 17.7 / 14.6, 32 of up to 2 K 32.9 / 36.3, 16 of 256 9.1 / 12.0; 64/8 heads:

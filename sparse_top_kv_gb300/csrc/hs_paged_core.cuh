@@ -3,7 +3,7 @@
 // few requests, and caches that tensor maps or the tcgen05 kernel do not take
 // (pages that are no multiple of 16 tokens, broadcast strides, E4M3 heads of
 // 64).  Bound by latency in small calls (one request of 1 K tokens, 32/8 heads
-// of 128: 8.4 us with the merge), by HBM in large ones (64 requests of 8 K in
+// of 128: 8.5 us with the merge), by HBM in large ones (64 requests of 8 K in
 // pages of 12: 321 us, 6.7 TB/s).
 //
 // Math, per request and query head h of KV head g, over the visible tokens:

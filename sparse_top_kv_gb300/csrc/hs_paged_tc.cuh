@@ -13,7 +13,8 @@
 //  * A tile is 128 cache rows: hs KV heads x 128 / hs tokens, so that one TMA
 //    box takes all heads of a run of tokens and DRAM is read in long pieces
 //    (one head's row at a time: 351 instead of 336 us over a bf16 batch of up
-//    to 64 K tokens, 122 instead of 88 over E4M3 rows of 128 bytes).  Rows of
+//    to 64 K tokens, 122 instead of 88 over E4M3 rows of 128 bytes, both
+//    before their weights had six parts).  Rows of
 //    a tile: [run of bt tokens][head][token of the run], so that a K step of
 //    PV holds one head (E4M3 pages of 16: a box per head, [head][token]).
 //  * One elected lane per run issues the boxes into a K ring and a V ring in
@@ -79,7 +80,8 @@ constexpr int kTilesForWide = 2;
 // the 256-byte pieces of a head cost little there, and a head's merge joins a
 // few parts instead of 152 (us, all heads / one: 24 K tokens 25.8 / 26.5, 32 K
 // 34.6 / 31.1, 128 K 93.1 / 90.2, two of 32 K 52.5 / 51.4, four 90.7 / 91.3).
-// E4M3 heads are 128-byte pieces: never (64 requests of up to 8 K 88 / 122).
+// E4M3 heads are 128-byte pieces: never (64 requests of up to 8 K 88 / 122, with
+// four parts to a weight).
 constexpr int kWideAlone = 2;        // requests x chunks of heads
 constexpr int kTilesAlone = 12;      // places per CTA
 
