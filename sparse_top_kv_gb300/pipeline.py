@@ -559,7 +559,7 @@ class BudgetedDecoder:
             if not 0 < q.shape[0] <= n:
                 raise ValueError(f"q: 1 to {n} queries")
             self._check_shape("q", q, q.shape[0], self.heads, self.d)
-            q = q.to(self.k_cache)
+            q = q.to(self.k_cache).contiguous()
         t = torch.arange(n, device=self.device)
         page = self.block_table[r].long()[t // self.page_size]
         for cache, rows in ((self.k_cache, k), (self.v_cache, v)):

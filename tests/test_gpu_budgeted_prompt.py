@@ -77,6 +77,17 @@ def test_scores_of_the_last_queries(n, queries, decay):
         assert queries > 1 or n // 2 in now
 
 
+def test_queries_of_any_layout():
+    g = torch.Generator(device="cuda").manual_seed(4)
+    k, v, q = rows(g, 60, 2, 64), rows(g, 60, 2, 64), rows(g, 9, 8, 64)
+    found = []
+    for x in (q, q.transpose(1, 2).contiguous().transpose(1, 2), q.float().cpu()):
+        dec = decoder()
+        dec.start(0, k, v, q=x)
+        found.append(dec.score)
+    assert all(torch.equal(x, found[0]) for x in found)
+
+
 def test_without_scores_the_first_places_stay():
     g = torch.Generator(device="cuda").manual_seed(3)
     dec = decoder()
