@@ -506,6 +506,10 @@ class BudgetedDecoder:
             raise TypeError(f"dtype: torch.bfloat16 or torch.float16, got {dtype}")
         if budget < 1:
             raise ValueError("budget: at least one token")
+        if d not in (64, 128, 256) or kv_heads < 1 or heads < 1 or heads % kv_heads:
+            raise ValueError("d: 64, 128 or 256; heads: a multiple of kv_heads")
+        if num_reqs < 1 or page_size < 1:
+            raise ValueError("num_reqs, page_size: at least one")
         if recent < 0 or num_sinks < 0 or recent + num_sinks > budget:
             raise ValueError("recent, num_sinks: within the budget")
         self.device = torch.device(device)

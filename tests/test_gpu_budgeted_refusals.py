@@ -9,9 +9,11 @@ from sparse_top_kv_gb300.pipeline import BudgetedDecoder
 SHAPE = dict(num_reqs=3, heads=8, kv_heads=2, d=64, page_size=16, budget=16, capacity=40, scale=0.1)
 
 
-def test_budget_without_a_token():
+@pytest.mark.parametrize("bad", [dict(budget=0), dict(d=96), dict(heads=7), dict(kv_heads=0),
+                                 dict(num_reqs=0), dict(page_size=0)])
+def test_set_up(bad):
     with pytest.raises(ValueError):
-        BudgetedDecoder(**{**SHAPE, "budget": 0})
+        BudgetedDecoder(**{**SHAPE, **bad})
 
 
 def state(dec):
