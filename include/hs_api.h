@@ -654,6 +654,142 @@ int hs_evict(const float* score, int64_t score_stride, const int32_t* positions,
              int32_t* status, hs_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Several new tokens of a request in one step (a prompt's chunk, guessed
+ * tokens to be verified, one token): hs_paged_extend makes room for them,
+ * hs_rope_append writes their rows, hs_paged_prefill attends.  The step's
+ * tokens stand one request after another; those of request r are
+ * [cu_new[r], cu_new[r + 1]).  No counterpart on the pages beyond the slot
+ * formula ([HS], as for S1) and [PT] 3.1.
+ *
+ * hs_paged_extend -- requests grow by new tokens or give tokens up; pages of
+ * page_size tokens come from and go to a ring of free ones.
+ * new_lens    int32 [rows]: n > 0: tokens to be added; n < 0: the last -n
+ *             tokens (at most all) are given up, and with them the pages that
+ *             hold none any more; 0: nothing.
+ * seq_lens    int32 [rows]: tokens T held (a negative one counts as 0).
+ * block_table int32 [rows, bt_stride], max_blocks entries of a row at most:
+ *             entries of fresh blocks are written, the others left (those
+ *             behind a request's last block mean nothing).
+ * free_ring   int32 [num_pages]: free pages are entries ring_pos[0] ..
+ *             ring_pos[1] - 1, modulo num_pages.  Pages are taken at the front,
+ *             in the order of the requests and of their blocks, and given back
+ *             at the end likewise; a page given back is not taken in the same
+ *             call.  It never holds a page twice as long as tables do not.
+ * ring_pos    int64 [2]; ring_out int64 [2], may be ring_pos.
+ * A request is served if its row of the table has room (max_blocks), its new
+ * tokens lie below max_tokens, and its pages and those asked for by the
+ * requests before it are in the ring together; one that needs no page does not
+ * wait for the ring.  A request that is not served keeps its tokens, its new
+ * tokens have no slot, and HS_ERR_CAPACITY is reported in *status.
+ * lens_out    int32 [rows], may be seq_lens: tokens held afterwards.
+ * attend_lens int32 [rows]: the same for a served request with new tokens, else
+ *             0 (the seq_lens of hs_paged_prefill).
+ * cu_new      int32 [rows + 1]: sums of the tokens asked for (served or not),
+ *             at most max_tokens.
+ * slot, row_req, positions  int32 [max_tokens], by token: block_table[r][t /
+ *             page_size] * page_size + t % page_size, r and t; -1 for tokens
+ *             of requests that are not served and behind the last request.
+ * A ring that cannot be (ends out of order, more pages than num_pages), a
+ * length past the table and a page outside [0, num_pages) leave the request as
+ * it is and are reported as HS_ERR_BAD_INDEX.  Out arrays must not overlap in
+ * arrays other than as stated.  Bit-exact and independent of thread scheduling.
+ * HS_ERR_CAPACITY: rows > 4096, num_pages, max_tokens or max_blocks * page_size
+ * > 2^30, num_pages * page_size >= 2^31.
+ * ------------------------------------------------------------------------- */
+int hs_paged_extend(const int32_t* new_lens, const int32_t* seq_lens, int32_t* block_table,
+                    int64_t bt_stride, int32_t rows, int32_t max_blocks, int32_t* free_ring,
+                    int32_t num_pages, const int64_t* ring_pos, int32_t page_size,
+                    int32_t max_tokens, int32_t* lens_out, int32_t* attend_lens,
+                    int64_t* ring_out, int32_t* cu_new, int32_t* slot, int32_t* row_req,
+                    int32_t* positions, int32_t* status, hs_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * hs_rope_append -- rotary positions on the queries and keys of tokens, and the
+ * rotated keys and the values into their slots of a paged cache.
+ *
+ *   (x_a, x_b) -> mscale (x_a cos - x_b sin, x_a sin + x_b cos),
+ *   angle = 2 pi p turns[i] / 2^64
+ *
+ * for pair i < rot / 2 of a head at position p: elements (i, i + rot / 2), or,
+ * interleaved, (2 i, 2 i + 1).  Elements from rot on stay as they are.
+ * q           [tokens, heads, d] of `dtype` (HS_BF16 / HS_FP16), heads packed,
+ *             tokens q_stride elements apart; NULL: none.  q_out likewise, of
+ *             the same type; may be q.
+ * k, v        [tokens, kv_heads, d] likewise; both NULL: no cache is written.
+ * positions   int32 [tokens]; a token with a negative one is left out: its rows
+ *             of q_out stay as they were and nothing is written for it.
+ * slot        int32 [tokens]: place page * page_size + o in the cache; < 0: the
+ *             token's rows are not stored.  A slot past num_pages * page_size is
+ *             skipped and reported as HS_ERR_BAD_INDEX in *status.  Slots of
+ *             different tokens must differ.
+ * turns       int64 [rot / 2]: turns per position (frequency / 2 pi) times 2^64.
+ *             The product with the position wraps at whole turns, so that far
+ *             positions lose nothing.
+ * k_cache, v_cache  of kv_dtype (that of k, or HS_E4M3): element (page, place
+ *             o, head g, dim i) at page * page_stride + o * row_stride + g *
+ *             head_stride + i.  Other places stay as they were.
+ * k_scale, v_scale  fp32 [kv_heads] or NULL (= 1); HS_E4M3 only: stored is the
+ *             row divided by its head's scale, saturating at +-448 (NaN stays).
+ * Computed in fp32 and rounded once, to nearest even.  16-byte aligned bases,
+ * strides multiples of 16 bytes.  d a multiple of 8 up to 1024, rot even;
+ * others HS_ERR_UNSUPPORTED.
+ * ------------------------------------------------------------------------- */
+int hs_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                   const void* v, int64_t v_stride, int32_t dtype, int32_t tokens, int32_t heads,
+                   int32_t kv_heads, int32_t d, const int32_t* positions, const int32_t* slot,
+                   const int64_t* turns, int32_t rot, int32_t interleaved, float mscale,
+                   void* q_out, int64_t q_out_stride, void* k_cache, void* v_cache,
+                   int32_t kv_dtype, int64_t page_stride, int64_t row_stride,
+                   int64_t head_stride, int32_t num_pages, int32_t page_size,
+                   const float* k_scale, const float* v_scale, int32_t* status,
+                   hs_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * hs_paged_prefill -- attention of several new tokens per request, causally,
+ * over the request's cached tokens, the new ones among them: hs_paged_decode
+ * for chunks.  Query i of request r's n = cu_new[r + 1] - cu_new[r] stands at
+ * position p = T - n + i and attends to the tokens t <= p; with a window, to
+ * those with t > p - window or t < num_sinks.
+ *
+ * q           [tokens, heads, d] of q_dtype, heads packed, tokens q_stride
+ *             elements apart.
+ * cu_new      int32 [rows + 1]: not descending; entries outside [0, tokens] and
+ *             descending ones are clipped and reported as HS_ERR_BAD_INDEX.
+ *             q and out rows outside [cu_new[0], cu_new[rows]) are neither
+ *             read nor written.
+ * seq_lens    int32 [rows]: T, the request's cached tokens with the new ones.
+ *             Queries before position 0 (T < n) give out = 0, lse = -inf.
+ * out         [tokens, heads, d] of q_dtype, packed; lse fp32 [tokens, heads]
+ *             or NULL.
+ * The other arguments as for hs_paged_decode, workspace and status included;
+ * a token counts as attended to where any query of the step attends to it.
+ * What stands in places that a query does not attend to has no effect on it,
+ * NaN and infinities included; attended entries that are not finite give
+ * outputs of their own head that are not finite.
+ * Weights are rounded to the type of the products: relative to a query's
+ * largest weight, with 16-bit floats of 8 bits (bf16 caches) or of 11 bits
+ * (fp16 and E4M3 caches, where those below 2^-24 keep 2^-35).  Results do not
+ * depend on timing.
+ * Supported: d 64, 128 or 256, at most 128 query heads on a KV head; others
+ * HS_ERR_UNSUPPORTED.  rows <= 4096, heads <= 65536, max_len <= 2^30 and tokens
+ * <= 2^24 (HS_ERR_CAPACITY above, or when the workspace is missing or too
+ * small; the query gives -1 for sizes that are refused).
+ * ------------------------------------------------------------------------- */
+int64_t hs_paged_prefill_workspace_bytes(int32_t tokens, int32_t rows, int32_t heads,
+                                         int32_t kv_heads, int32_t d, int32_t max_len,
+                                         int32_t window, int32_t num_sinks);
+
+int hs_paged_prefill(const void* q, int64_t q_stride, int32_t q_dtype, int32_t tokens,
+                     const void* k, const void* v, int32_t kv_dtype, int64_t page_stride,
+                     int64_t row_stride, int64_t head_stride, int32_t num_pages,
+                     int32_t page_size, const int32_t* block_table, int64_t bt_stride,
+                     int32_t max_blocks, int32_t max_len, const int32_t* cu_new,
+                     const int32_t* seq_lens, const float* k_scale, const float* v_scale,
+                     int32_t rows, int32_t heads, int32_t kv_heads, int32_t d, int32_t window,
+                     int32_t num_sinks, float scale, void* out, float* lse, void* workspace,
+                     int64_t workspace_bytes, int32_t* status, hs_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * hs_wait_selftest -- no counterpart on the pages: a test of the bounded
  * wait that every mbarrier wait of this library goes through (a wait that
  * cannot complete reports an error instead of hanging).  One CTA waits on an

@@ -8,6 +8,7 @@ there is no CPU fallback.  If the library cannot be loaded this module raises.
 import ctypes
 import importlib.machinery
 import importlib.util
+import math
 import os
 import warnings
 
@@ -84,6 +85,15 @@ _SIGS = {
     "hs_evict": ([_P, _I64, _P, _I64, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _I64, _P, _I64,
                   _P, _P, _P, _P, _I32, _P, _P, _I64, _I64, _I64, _I32, _I32, _I32, _I32, _P,
                   _I64, _I32, _P, _P], ctypes.c_int),
+    "hs_paged_extend": ([_P, _P, _P, _I64, _I32, _I32, _P, _I32, _P, _I32, _I32, _P, _P, _P, _P,
+                         _P, _P, _P, _P, _P], ctypes.c_int),
+    "hs_rope_append": ([_P, _I64, _P, _I64, _P, _I64, _I32, _I32, _I32, _I32, _I32, _P, _P, _P,
+                        _I32, _I32, _F32, _P, _I64, _P, _P, _I32, _I64, _I64, _I64, _I32, _I32,
+                        _P, _P, _P, _P], ctypes.c_int),
+    "hs_paged_prefill_workspace_bytes": ([_I32] * 8, _I64),
+    "hs_paged_prefill": ([_P, _I64, _I32, _I32, _P, _P, _I32, _I64, _I64, _I64, _I32, _I32, _P,
+                          _I64, _I32, _I32, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32,
+                          _F32, _P, _P, _P, _I64, _P, _P], ctypes.c_int),
 }
 
 NOALLOC_WORKSPACE_BYTES = 8 * 1024 * 1024  # HS_NOALLOC_WORKSPACE_BYTES
@@ -936,3 +946,266 @@ def evict(score, seq_lens, budget, k_cache, v_cache, block_table, *, max_len=Non
     if rc != HS_OK:
         raise HSError("hs_evict", rc)
     return result
+
+
+def _token_rows(t, name, device, dtype=None, shape=None):
+    """(address, elements from token to token) of rows [tokens, heads, d] whose
+    heads are packed; tokens may be strided."""
+    if t.dtype not in (torch.bfloat16, torch.float16) or dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype or 'torch.bfloat16 or torch.float16'}, got "
+                        f"{t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: must be on the current CUDA device")
+    if t.dim() != 3 or shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: expected {'[tokens, heads, d]' if shape is None else shape}, "
+                         f"got {tuple(t.shape)}")
+    n, heads, d = t.shape
+    if t.numel() and (t.stride(2) != 1 or heads > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: heads must be packed")
+    return t.data_ptr(), t.stride(0) if n > 1 else heads * d
+
+
+def paged_extend(new_lens, seq_lens, block_table, free_ring, ring_pos, page_size, max_tokens, *,
+                 lens_out=None, attend_lens=None, ring_out=None, cu_new=None, slot=None,
+                 row_req=None, positions=None, status=None, stream=None):
+    """Requests grow by new_lens tokens or give tokens up (hs_paged_extend).
+
+    new_lens, seq_lens int32 [rows]; block_table int32 [rows, blocks], updated in
+    place; free_ring int32 [num_pages] and ring_pos int64 [2]: the free pages are
+    entries ring_pos[0] to ring_pos[1] - 1 modulo num_pages; max_tokens bounds
+    the step's tokens.  lens_out and ring_out default to the inputs (updated in
+    place).  Returns (lens_out, attend_lens, cu_new int32 [rows + 1], slot,
+    row_req, positions int32 [max_tokens])."""
+    if not isinstance(max_tokens, int):
+        raise TypeError("max_tokens: an int")
+    _check_i32(page_size=page_size, max_tokens=max_tokens)
+    if max_tokens < 0:
+        raise ValueError("max_tokens: not negative")
+    dev = _current_device(new_lens, "new_lens")
+    if new_lens.dim() != 1 or block_table.dim() != 2 or free_ring.dim() != 1:
+        raise ValueError("new_lens: [rows]; block_table: [rows, blocks]; free_ring: [num_pages]")
+    rows, pages = new_lens.shape[0], free_ring.shape[0]
+    i64 = torch.int64
+    given = lens_out, attend_lens, ring_out, cu_new, slot, row_req, positions
+    opt = dict(dtype=_I, device=new_lens.device)
+    if lens_out is None:
+        lens_out = seq_lens
+    if ring_out is None:
+        ring_out = ring_pos
+    if attend_lens is None:
+        attend_lens = torch.empty(rows, **opt)
+    if cu_new is None:
+        cu_new = torch.empty(rows + 1, **opt)
+    slot, row_req, positions = (torch.empty(max_tokens, **opt) if t is None else t
+                                for t in (slot, row_req, positions))
+    _used_on(stream, *(t for t, g in zip((lens_out, attend_lens, ring_out, cu_new, slot, row_req,
+                                          positions), given)
+                       if g is None and t is not seq_lens and t is not ring_pos))
+    table, table_stride = _matrix(block_table, _I, "block_table", dev, rows, 0)
+    rc = lib().hs_paged_extend(
+        _vector(new_lens, _I, "new_lens", dev, rows), _vector(seq_lens, _I, "seq_lens", dev, rows),
+        table, table_stride, rows, block_table.shape[1],
+        _vector(free_ring, _I, "free_ring", dev, pages), pages,
+        _vector(ring_pos, i64, "ring_pos", dev, 2), page_size, max_tokens,
+        _vector(lens_out, _I, "lens_out", dev, rows),
+        _vector(attend_lens, _I, "attend_lens", dev, rows),
+        _vector(ring_out, i64, "ring_out", dev, 2), _vector(cu_new, _I, "cu_new", dev, rows + 1),
+        _vector(slot, _I, "slot", dev, max_tokens),
+        _vector(row_req, _I, "row_req", dev, max_tokens),
+        _vector(positions, _I, "positions", dev, max_tokens), _status_ptr(status, dev),
+        _raw_stream(dev, stream))
+    if rc != HS_OK:
+        raise HSError("hs_paged_extend", rc)
+    return lens_out, attend_lens, cu_new, slot, row_req, positions
+
+
+def rope_frequencies(rot, base=10000.0, *, scaling=None, factor=1.0, original_len=None,
+                     slow_turns=1.0, fast_turns=32.0):
+    """Frequencies (float64 [rot / 2], radians per position) of rotary positions
+    over `rot` dims, base^(-2 i / rot), and the factor for rope_append's mscale.
+
+    scaling "linear": positions divided by `factor`; "ntk": the base grown so
+    that the slowest pair turns `factor` times slower and the fastest stays;
+    "yarn": pairs that turn fewer than `slow_turns` times over `original_len`
+    tokens are slowed by `factor`, those that turn more than `fast_turns` times
+    not at all, linearly between, and attention sharpened by 0.1 ln(factor) + 1."""
+    if rot < 0 or rot % 2:
+        raise ValueError("rot: even, not negative")
+    if factor <= 0 or base <= 0:
+        raise ValueError("factor, base: positive")
+    if scaling == "ntk" and rot > 2:
+        base = base * factor ** (rot / (rot - 2))
+    inv = base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / max(rot, 1))
+    if scaling in (None, "ntk"):
+        return inv, 1.0
+    if scaling == "linear":
+        return inv / factor, 1.0
+    if scaling != "yarn":
+        raise ValueError(f"scaling: None, 'linear', 'ntk' or 'yarn', got {scaling!r}")
+    if original_len is None or original_len <= 0 or not slow_turns < fast_turns:
+        raise ValueError("yarn: needs original_len > 0 and slow_turns < fast_turns")
+    turns = original_len * inv / (2 * math.pi)
+    keep = ((turns - slow_turns) / (fast_turns - slow_turns)).clamp(0, 1)
+    return inv * keep + inv / factor * (1 - keep), max(1.0, 0.1 * math.log(factor) + 1.0)
+
+
+def rope_turns(inv_freq, device="cuda"):
+    """The table that rope_append takes: frequencies [rot / 2] in radians per
+    position as int64 turns per position times 2^64."""
+    x = inv_freq.to("cpu", torch.float64) / (2 * math.pi)
+    x = x - torch.floor(x)
+    x = torch.where(x >= 0.5, x - 1.0, x)  # whole turns do not count; int64 is signed
+    return (x * 2.0 ** 64).to(torch.int64).to(device)
+
+
+def rope_append(q, k, v, positions, slot, turns, k_cache, v_cache, *, interleaved=False,
+                mscale=1.0, k_scale=None, v_scale=None, q_out=None, status=None, stream=None):
+    """Rotary positions on q and k, and the rotated k and v into their slots of a
+    paged cache (hs_rope_append).
+
+    q [tokens, heads, d], k, v [tokens, kv_heads, d] bf16 or fp16, heads packed,
+    tokens may be strided (parts of one projection's rows); positions, slot int32
+    [tokens] (as paged_extend gives them); turns int64 [rot / 2] of rope_turns;
+    caches [num_pages, page_size, kv_heads, d] of k's type or float8_e4m3fn (then
+    k_scale, v_scale fp32 [kv_heads] or None).  q_out defaults to a new tensor
+    and may be q; rows of tokens without a position are left as they are
+    (undefined in a new tensor).  q None: only the cache is written; k, v, slot
+    and the caches None: only q.
+    Returns q_out."""
+    dev = _current_device(positions, "positions")
+    if q is None and k is None:
+        raise ValueError("q, k: at least one")
+    shape = (k if q is None else q).shape
+    if len(shape) != 3:
+        raise ValueError("q, k: [tokens, heads, d]")
+    n, heads, d = shape
+    heads, kv_heads = 0 if q is None else heads, 0
+    dtype = (k if q is None else q).dtype
+    q_ptr, q_stride, qo_ptr, qo_stride, k_ptr, k_stride, v_ptr, v_stride = (None, 0) * 4
+    if q is not None:
+        q_ptr, q_stride = _token_rows(q, "q", dev)
+        if q_out is None:
+            q_out = torch.empty(n, heads, d, dtype=dtype, device=q.device)
+            _used_on(stream, q_out)
+        qo_ptr, qo_stride = _token_rows(q_out, "q_out", dev, dtype, q.shape)
+    elif q_out is not None:
+        raise ValueError("q_out: needs q")
+    if (k is None) != (v is None) or (k is None) != (k_cache is None) or (
+            (k is None) != (v_cache is None)) or (k is None) != (slot is None):
+        raise ValueError("k, v, slot and the caches: all or none")
+    kc = vc = None
+    ps = rs = hstr = pages = page_size = 0
+    kt = _ELEMENT.get(dtype)
+    if k is not None:
+        kv_heads = k.shape[1] if k.dim() == 3 else 0
+        k_ptr, k_stride = _token_rows(k, "k", dev, dtype, torch.Size((n, kv_heads, d)))
+        v_ptr, v_stride = _token_rows(v, "v", dev, dtype, k.shape)
+        if k_cache.dtype not in _ELEMENT:
+            raise TypeError(f"k_cache: unsupported {k_cache.dtype}")
+        _check_cache(k_cache, v_cache, dev)
+        pages, page_size, gc, dc = k_cache.shape
+        if (gc, dc) != (kv_heads, d):
+            raise ValueError("k_cache: heads and head size of k")
+        kt = _ELEMENT[k_cache.dtype]
+        kc, vc = k_cache.data_ptr(), v_cache.data_ptr()
+        ps, rs, hstr = _cache_strides(k_cache, 1)
+    if turns.dim() != 1:
+        raise ValueError("turns: [rot / 2]")
+    if not isinstance(interleaved, (bool, int)):
+        raise TypeError("interleaved: a bool")
+    rc = lib().hs_rope_append(
+        q_ptr, q_stride, k_ptr, k_stride, v_ptr, v_stride, _ELEMENT[dtype], n, heads, kv_heads, d,
+        _vector(positions, _I, "positions", dev, n),
+        None if slot is None else _vector(slot, _I, "slot", dev, n),
+        _vector(turns, torch.int64, "turns", dev, turns.shape[0]), 2 * turns.shape[0],
+        1 if interleaved else 0, mscale, qo_ptr, qo_stride, kc, vc, kt, ps, rs, hstr, pages,
+        page_size, _vector(k_scale, _F, "k_scale", dev, kv_heads),
+        _vector(v_scale, _F, "v_scale", dev, kv_heads), _status_ptr(status, dev),
+        _raw_stream(dev, stream))
+    if rc != HS_OK:
+        raise HSError("hs_rope_append", rc)
+    return q_out
+
+
+def paged_prefill_workspace_bytes(tokens, rows, heads, kv_heads, d, max_len, *, window=0,
+                                  num_sinks=0):
+    _check_i32(tokens=tokens, rows=rows, heads=heads, kv_heads=kv_heads, d=d, max_len=max_len,
+               window=window, num_sinks=num_sinks)
+    return int(lib().hs_paged_prefill_workspace_bytes(tokens, rows, heads, kv_heads, d, max_len,
+                                                      window, num_sinks))
+
+
+def paged_prefill(q, k_cache, v_cache, block_table, cu_new, seq_lens, scale, *, window=0,
+                  num_sinks=0, max_len=None, k_scale=None, v_scale=None, out=None, lse=None,
+                  workspace=None, status=None, stream=None):
+    """Several new tokens' attention, causally, over every cached token of their
+    request, their own among them (hs_paged_prefill).
+
+    q [tokens, heads, d] bf16 or fp16 (heads packed, tokens may be strided), the
+    requests' tokens one after another: cu_new int32 [rows + 1] says where;
+    seq_lens int32 [rows]: cached tokens, the new ones included (paged_extend's
+    attend_lens).  Caches, block_table, scales, max_len, window, workspace and
+    status as for paged_decode.  Returns (out [tokens, heads, d] of q's type, lse
+    fp32 [tokens, heads]); rows of q of no request are left as they are (zeros in
+    tensors made here)."""
+    dev = _current_device(q, "q")
+    q_ptr, q_stride = _token_rows(q, "q", dev)
+    if k_cache.dtype not in _ELEMENT:
+        raise TypeError(f"k_cache: unsupported {k_cache.dtype}")
+    if v_cache is None:
+        raise ValueError("v_cache: needed")
+    _check_cache(k_cache, v_cache, dev)
+    n, heads, d = q.shape
+    num_pages, page_size, kv_heads, dc = k_cache.shape
+    if dc != d:
+        raise ValueError("k_cache: head size of q")
+    if seq_lens.dim() != 1 or block_table.dim() != 2:
+        raise ValueError("seq_lens: [rows]; block_table: [rows, blocks]")
+    rows = seq_lens.shape[0]
+    table, table_stride = _matrix(block_table, _I, "block_table", dev, rows, 0)
+    blocks = block_table.shape[1]
+    if max_len is None:
+        max_len = blocks * page_size
+    if not 0 <= max_len < 1 << 31:
+        raise ValueError("max_len: 0 to 2^31 - 1")
+    _check_i32(window=window, num_sinks=num_sinks)
+    lens = (_vector(cu_new, _I, "cu_new", dev, rows + 1),
+            _vector(seq_lens, _I, "seq_lens", dev, rows))
+    scales = (_vector(k_scale, _F, "k_scale", dev, kv_heads),
+              _vector(v_scale, _F, "v_scale", dev, kv_heads))
+    made = []
+    if out is None:
+        made.append(out := torch.empty(n, heads, d, dtype=q.dtype, device=q.device))
+    if lse is None:
+        made.append(lse := torch.empty(n, heads, dtype=_F, device=q.device))
+    _used_on(stream, *made)
+    with torch.cuda.stream(stream):  # the call's own: the kernel follows
+        for t in made:
+            t.zero_()
+    out_ptr = _output(out, q.dtype, "out", dev, q.shape)
+    lse_ptr = _output(lse, _F, "lse", dev, q.shape[:2])
+    strides = _cache_strides(k_cache, 1)
+    for again in (False, True):
+        ws, ws_bytes = None, 0
+        if workspace is not None:
+            if workspace.get_device() != dev:
+                raise ValueError("workspace: must be on q's device")
+            _check_workspace(workspace)
+            ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
+        rc = lib().hs_paged_prefill(
+            q_ptr, q_stride, _ELEMENT[q.dtype], n, k_cache.data_ptr(), v_cache.data_ptr(),
+            _ELEMENT[k_cache.dtype], *strides, num_pages, page_size, table, table_stride, blocks,
+            max_len, *lens, *scales, rows, heads, kv_heads, d, window, num_sinks, scale, out_ptr,
+            lse_ptr, ws, ws_bytes, _status_ptr(status, dev), _raw_stream(dev, stream))
+        if rc != 3 or again:
+            break
+        # HS_ERR_CAPACITY: the workspace is missing or too small.
+        need = paged_prefill_workspace_bytes(n, rows, heads, kv_heads, d, max_len, window=window,
+                                             num_sinks=num_sinks)
+        if need < 0:
+            break
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        _used_on(stream, workspace)
+    if rc != HS_OK:
+        raise HSError("hs_paged_prefill", rc)
+    return out, lse
