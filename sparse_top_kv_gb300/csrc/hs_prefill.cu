@@ -1,91 +1,148 @@
-// hs_prefill.cu -- hs_paged_prefill: argument checks and the attention of a
-// chunk of new tokens over a paged cache.
+// hs_prefill.cu -- hs_paged_prefill: argument checks, workspace layout and the
+// merge of units that several CTAs shared.  The attention kernel itself is in
+// hs_prefill_tc.cuh.
+#include <cuda.h>
+
 #include <type_traits>
 
 #include "hs_prefill.cuh"
 
+namespace hs_paged {
+namespace tc {
+int encode_map(CUtensorMap* m, int kv, const void* base, const PagedArgs& a, int d, int bt,
+               int hs_box);
+}  // namespace tc
+}  // namespace hs_paged
+
 namespace hs_prefill {
+
+int launch_bf16(const PrefillArgs& a, int d, int bt, hs_stream_t stream);
+int launch_fp16(const PrefillArgs& a, int d, int bt, hs_stream_t stream);
+int launch_e4m3(const PrefillArgs& a, int d, int bt, hs_stream_t stream);
+
+namespace tc {
+int encode_map(CUtensorMap* m, const void* base, const PrefillArgs& a, int kv_dtype, int d,
+               int bt) {
+    hs_paged::PagedArgs p{};  // what the decode's maps depend on
+    p.page_stride = a.page_stride;
+    p.row_stride = a.row_stride;
+    p.head_stride = a.head_stride;
+    p.num_pages = a.num_pages;
+    p.page_size = a.page_size;
+    p.kv_heads = a.kv_heads;
+    return hs_paged::tc::encode_map(m, kv_dtype, base, p, d, bt, 1);
+}
+}  // namespace tc
+
 namespace {
 
-template <typename T>
-__device__ __forceinline__ float widen(T x) {
-    return float(x);
+// Tokens of a TMA box, or 0 where threads have to load: pages without runs of
+// 16 tokens, broadcast strides.  (E4M3 rows are converted by threads.)
+int box_tokens(const PrefillArgs& a, int kv_dtype) {
+    const int64_t most = int64_t(1) << 38;  // elements; the encoder takes strides below 2^40 bytes
+    if (kv_dtype == HS_E4M3 || a.page_size % 16 != 0 || a.num_pages <= 0 ||
+        (a.kv_heads > 1 && (a.head_stride <= 0 || a.head_stride >= most)) ||
+        (a.num_pages > 1 && (a.page_stride <= 0 || a.page_stride >= most)) || a.row_stride <= 0 ||
+        a.row_stride >= most)
+        return 0;
+    int bt = kTile;
+    while (a.page_size % bt) bt /= 2;
+    return bt;
 }
 
-// A warp per (new token, query head): a lane holds d / 32 elements of the query
-// and of the sum, keys one after another with a running maximum.
-template <typename Q, typename K, int D>
-__global__ void __launch_bounds__(256) simple_kernel(const __grid_constant__ PrefillArgs a) {
-    constexpr int N = D / 32;
+constexpr int kMergeThreads = 256;
+constexpr int kMergeSlices = 8;
+
+// Joins the parts of a shared unit: out = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p -
+// M) l_p.  Block (c, y): some rows of the unit whose first part CTA c had; a
+// warp per row.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ PrefillArgs a,
+                                                              int out_bf16) {
+    constexpr int V = D / 32;  // elements of a lane
     hs::pdl_wait();
     hs::pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    const int64_t unit = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int token = int(unit / a.heads), h = int(unit % a.heads);
-    if (blockIdx.x == 0)
-        for (int r = threadIdx.x; r < a.rows; r += blockDim.x) {
-            const int c0 = a.cu_new[r], c1 = a.cu_new[r + 1];
-            if (a.seq_lens[r] > a.max_len || c0 < 0 || c1 < c0 || c1 > a.tokens)
-                hs::set_status(a.status, HS_ERR_BAD_INDEX);
+    const int c = blockIdx.x, lane = threadIdx.x & 31;
+    const SharedUnit u = a.shared[c];
+    if (!u.valid) return;
+    for (int j = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5); j < a.unit_rows;
+         j += kMergeSlices * (kMergeThreads / 32)) {
+        const int w = j / kTile, r = j % kTile, tok = r / a.group, hd = r - tok * a.group;
+        if (tok >= a.tq || w * a.tq + tok >= u.tokens) continue;
+        float M = -CUDART_INF_F, L = 0.f, o[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = 0.f;
+        int64_t at = run_begin(u.total, a.ctas, c) - u.start;
+        int64_t slot = 2 * c + (at > 0 ? 0 : 1);
+        int i0 = tile_at(at, u.cost, u.tiles);
+        for (int p = c; i0 < u.tiles && p < a.ctas; ++p, slot = 2 * p) {
+            at = run_begin(u.total, a.ctas, p + 1) - u.start;
+            const int i1 = tile_at(at, u.cost, u.tiles);
+            if (i1 > i0) {
+                const int64_t k = slot * a.unit_rows + j;
+                const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + k);
+                float x[V];
+#pragma unroll
+                for (int i = 0; i < V; i += 2) {
+                    const float2 y = __ldcg(reinterpret_cast<const float2*>(a.part_o + k * D) +
+                                            i / 2 * 32 + lane);
+                    x[i] = y.x;
+                    x[i + 1] = y.y;
+                }
+                const float m = fmaxf(M, ml.x), ref = m == -CUDART_INF_F ? 0.f : m;
+                const float keep = exp2f(M - ref), f = exp2f(ml.x - ref);
+                M = m;
+                L = fmaf(L, keep, f * ml.y);
+#pragma unroll
+                for (int i = 0; i < V; ++i) o[i] = fmaf(o[i], keep, f * x[i]);
+            }
+            i0 = i1;
         }
-    if (token >= a.tokens || a.rows == 0) return;
-    int lo = 0, hi = a.rows;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (a.cu_new[mid] <= token) lo = mid;
-        else hi = mid;
-    }
-    const Request x = request_of(a, lo);
-    if (token < x.first || token >= x.first + x.n) return;
-    const int g = h / a.group, pos = x.T - x.n + (token - x.first);
-    const Q* q = static_cast<const Q*>(a.q) + token * a.q_stride + int64_t(h) * D + lane * N;
-    float qf[N], o[N];
-    const float scale = a.scale_log2 * (a.k_scale != nullptr ? a.k_scale[g] : 1.f);
+        float f = L == 0.f ? 0.f : 1.f / L;
+        if (a.v_scale != nullptr && L != 0.f) f *= a.v_scale[u.kvh];
+        const int64_t qh = int64_t(u.first + w * a.tq + tok) * a.heads + u.kvh * a.group + hd;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        qf[i] = widen(q[i]) * scale;
-        o[i] = 0.f;
-    }
-    float m = -CUDART_INF_F, l = 0.f;
-    bool bad = false;
-    for (int t = 0; t <= pos; ++t) {
-        if (a.window > 0 && t <= pos - a.window && t >= a.sinks) {
-            t = pos - a.window;
-            continue;
+        for (int i = 0; i < V; i += 2) {
+            const float x = L == 0.f ? 0.f : o[i] * f, y = L == 0.f ? 0.f : o[i + 1] * f;
+            const int64_t e = qh * (D / 2) + i / 2 * 32 + lane;
+            if (out_bf16)
+                static_cast<__nv_bfloat162*>(a.out)[e] = __floats2bfloat162_rn(x, y);
+            else
+                static_cast<__half2*>(a.out)[e] = __floats2half2_rn(x, y);
         }
-        const int b = block_of(a, t), page = a.block_table[lo * a.bt_stride + b];
-        if (page < 0 || page >= a.num_pages) {
-            bad = true;
-            continue;
-        }
-        const int64_t at = page * a.page_stride + (t - b * a.page_size) * a.row_stride +
-                           g * a.head_stride + lane * N;
-        const K* k = static_cast<const K*>(a.k) + at;
-        const K* v = static_cast<const K*>(a.v) + at;
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) s = fmaf(qf[i], widen(k[i]), s);
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        const float mn = fmaxf(m, s), ref = mn == -CUDART_INF_F ? 0.f : mn;
-        const float keep = exp2f(m - ref), p = exp2f(s - ref);
-        m = mn;
-        l = fmaf(l, keep, p);
-#pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = fmaf(p, widen(v[i]), o[i] * keep);
+        if (lane == 0 && a.lse != nullptr)
+            a.lse[qh] = L == 0.f ? -CUDART_INF_F : (M + log2f(L)) * kLn2;
     }
-    if (bad) hs::set_status(a.status, HS_ERR_BAD_INDEX);
-    const float f = l == 0.f ? 0.f : (a.v_scale != nullptr ? a.v_scale[g] : 1.f) / l;
-    const int64_t at = int64_t(token) * a.heads + h;
-    Q* out = static_cast<Q*>(a.out) + at * D + lane * N;
-#pragma unroll
-    for (int i = 0; i < N; ++i) out[i] = Q(l == 0.f ? 0.f : o[i] * f);
-    if (lane == 0 && a.lse != nullptr)
-        a.lse[at] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
+}
+
+struct Layout {
+    int64_t ml, o, shared, total;
+    int32_t unit_rows, ctas;
+};
+
+// Workspace: the partial states (two slots per CTA) and the shared units.
+// Nothing in it survives a call.
+Layout layout(int32_t d) {
+    Layout w;
+    w.unit_rows = d == 256 ? kTile : 2 * kTile;
+    w.ctas = int32_t(hs::min64(kMaxCtas, hs_host::num_sms()));
+    int64_t at = 0;
+    const auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    w.ml = take(int64_t(2) * w.ctas * w.unit_rows * 2 * 4);
+    w.o = take(int64_t(2) * w.ctas * w.unit_rows * d * 4);
+    w.shared = take(int64_t(w.ctas) * sizeof(SharedUnit));
+    w.total = at;
+    return w;
 }
 
 bool too_large(int32_t tokens, int32_t rows, int32_t heads, int32_t max_len) {
-    return rows > kMaxRows || heads > kMaxHeads || max_len > (1 << 30) || tokens > (1 << 24);
+    // The places of a call are counted in 63 bits, those of a block in 31.
+    return rows > kMaxRows || heads > kMaxHeads || max_len > (1 << 30) || tokens > (1 << 24) ||
+           (int64_t(tokens) + rows) * heads >= int64_t(1) << 31;
 }
 
 bool bad_shape(int32_t tokens, int32_t rows, int32_t heads, int32_t kv_heads, int32_t d,
@@ -105,7 +162,7 @@ extern "C" int64_t hs_paged_prefill_workspace_bytes(int32_t tokens, int32_t rows
     if (bad_shape(tokens, rows, heads, kv_heads, d, max_len, window, num_sinks) ||
         too_large(tokens, rows, heads, max_len))
         return -1;
-    return 0;
+    return rows == 0 || tokens == 0 ? 0 : layout(d).total;
 }
 
 extern "C" int hs_paged_prefill(const void* q, int64_t q_stride, int32_t q_dtype, int32_t tokens,
@@ -168,26 +225,32 @@ extern "C" int hs_paged_prefill(const void* q, int64_t q_stride, int32_t q_dtype
     for (int i = 0; i < 31; ++i)
         if (page_size == (1 << i)) a.page_shift = i;
     a.max_len = max_len;
-    a.window = window;
-    a.sinks = num_sinks;
     a.scale_log2 = scale * kLog2e;
     a.out = out;
     a.lse = lse;
     a.status = status;
-    (void)workspace;
-    (void)workspace_bytes;
-    const dim3 grid{unsigned((int64_t(tokens) * heads + 7) / 8)};
-    const auto launch = [&](auto qt, auto kt) {
-        using Q = decltype(qt);
-        using K = decltype(kt);
-        if (d == 64)
-            return hs_host::launch_pdl(simple_kernel<Q, K, 64>, grid, dim3(256), 0, stream, a);
-        if (d == 128)
-            return hs_host::launch_pdl(simple_kernel<Q, K, 128>, grid, dim3(256), 0, stream, a);
-        return hs_host::launch_pdl(simple_kernel<Q, K, 256>, grid, dim3(256), 0, stream, a);
-    };
-    if (kv_dtype == HS_BF16) return launch(__nv_bfloat16{}, __nv_bfloat16{});
-    if (kv_dtype == HS_FP16) return launch(__half{}, __half{});
-    return q_dtype == HS_FP16 ? launch(__half{}, __nv_fp8_e4m3{})
-                              : launch(__nv_bfloat16{}, __nv_fp8_e4m3{});
+    a.q_is_half = q_dtype == HS_FP16;
+    // Longer ones than any context see as much.
+    a.window = int32_t(hs::min64(window, 1 << 30));
+    a.sinks = int32_t(hs::min64(num_sinks, 1 << 30));
+    const Layout w = layout(d);
+    if (workspace == nullptr || workspace_bytes < w.total) return HS_ERR_CAPACITY;
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    a.tq = kTile / a.group;
+    a.tb = a.tq * (w.unit_rows / kTile);
+    a.ctas = w.ctas;
+    a.part_ml = reinterpret_cast<float*>(ws + w.ml);
+    a.part_o = reinterpret_cast<float*>(ws + w.o);
+    a.shared = reinterpret_cast<SharedUnit*>(ws + w.shared);
+    a.unit_rows = w.unit_rows;
+    const int bt = box_tokens(a, kv_dtype);
+    const int rc = kv_dtype == HS_BF16   ? launch_bf16(a, d, bt, stream)
+                   : kv_dtype == HS_FP16 ? launch_fp16(a, d, bt, stream)
+                                         : launch_e4m3(a, d, bt, stream);
+    if (rc != HS_OK) return rc;
+    const dim3 grid{unsigned(a.ctas), kMergeSlices}, block{kMergeThreads};
+    const int bf = q_dtype == HS_BF16;
+    if (d == 64) return hs_host::launch_pdl(merge_kernel<64>, grid, block, 0, stream, a, bf);
+    if (d == 128) return hs_host::launch_pdl(merge_kernel<128>, grid, block, 0, stream, a, bf);
+    return hs_host::launch_pdl(merge_kernel<256>, grid, block, 0, stream, a, bf);
 }

@@ -1,5 +1,6 @@
-// hs_prefill.cuh -- hs_paged_prefill: arguments shared by the dispatcher
-// (hs_prefill.cu) and the attention kernel.
+// hs_prefill.cuh -- hs_paged_prefill: arguments and work plan shared by the
+// dispatcher with its merge kernel (hs_prefill.cu) and the attention kernel
+// (hs_prefill_tc.cuh, one translation unit per cache type).
 #pragma once
 
 #include "hs_paged.cuh"
@@ -10,6 +11,20 @@ using hs_paged::kLn2;
 using hs_paged::kLog2e;
 using hs_paged::kMaxHeads;
 using hs_paged::kMaxRows;
+
+constexpr int kTile = 128;      // query rows and cached tokens of a tile
+constexpr int kMaxCtas = 1024;  // most CTAs of the attention kernel
+// Places (tokens' time) that a unit takes besides its tokens: its queries'
+// loads, the first product and the output.
+constexpr int kExtra = 256;
+
+// A unit whose tokens several CTAs share, written by the CTA of its first part.
+struct SharedUnit {
+    int64_t start, total;  // its first place, and the places of the call
+    int32_t cost, tiles;   // its places and tiles
+    int32_t first, tokens; // its new tokens
+    int32_t kvh, valid;    // 0: this CTA has no first part
+};
 
 struct PrefillArgs {
     const void* q;  // [tokens, heads, D], tokens q_stride elements apart
@@ -24,11 +39,30 @@ struct PrefillArgs {
     const float* v_scale;
     int32_t tokens, rows, heads, kv_heads, group, num_pages, page_size, max_len, window, sinks;
     int32_t page_shift;  // log2 of page_size, or -1
+    int32_t q_is_half;   // E4M3 caches: the query is fp16 (else bf16)
     float scale_log2;    // scale * log2(e)
     void* out;           // [tokens, heads, D]
     float* lse;          // [tokens, heads] or nullptr
+    int32_t tq;          // new tokens of a query tile: 128 / group
+    int32_t tb;          // and of a unit: one or two query tiles
+    int32_t ctas;
+    // Workspace: two partial states per CTA (of the units that its run begins
+    // and ends in) and the shared units.
+    float* part_ml;      // [2 * ctas][unit rows][2]
+    float* part_o;       // [2 * ctas][unit rows][D]
+    SharedUnit* shared;  // [ctas]
+    int32_t unit_rows;   // 128 or 256
     int32_t* status;
 };
+
+// How a call is cut into work.  A unit is one KV head x one block of a
+// request's new tokens: one or two query tiles, each 128 rows of (token, query
+// head of the KV head).  Units stand one after another (requests, their KV
+// heads, their blocks), each over as many places as cached tokens it sees and
+// kExtra more, and the places are dealt to the CTAs in equal contiguous runs;
+// a unit whose places several CTAs got is cut at tiles of 128 cached tokens
+// and merged.  So ragged batches, causal blocks of growing length and one
+// long context load every SM alike.
 
 // Where request r's new tokens stand, and its cached tokens.
 struct Request {
@@ -43,6 +77,34 @@ __device__ __forceinline__ Request request_of(const PrefillArgs& a, int r) {
 }
 __device__ __forceinline__ int block_of(const PrefillArgs& a, int t) {
     return a.page_shift >= 0 ? t >> a.page_shift : t / a.page_size;
+}
+__device__ __forceinline__ int blocks_of(const PrefillArgs& a, int n) {
+    return (n + a.tb - 1) / a.tb;
+}
+// Places of the first b blocks of a request, in closed form: block i sees up to
+// position base + (i + 1) tb and, with a window, from base + i tb + 1 - window
+// on (the grid of tiles, the sinks and a last block that is not full do not
+// count).
+__device__ __forceinline__ int64_t places(const PrefillArgs& a, const Request& x, int b) {
+    const int64_t base = max(x.T - x.n, 0), tb = a.tb, n = b;
+    int64_t sum = n * (kExtra + base) + tb * (n * (n + 1) / 2);
+    if (a.window > 0) {
+        const int64_t c0 = base + 1 - a.window;
+        const int64_t i0 = c0 > 0 ? 0 : -c0 / tb + 1;  // the first block that starts behind 0
+        if (n > i0) sum -= (n - i0) * c0 + tb * (n * (n - 1) / 2 - i0 * (i0 - 1) / 2);
+    }
+    return sum;
+}
+__device__ __forceinline__ int64_t places_of(const PrefillArgs& a, const Request& x) {
+    return x.n > 0 ? places(a, x, blocks_of(a, x.n)) * a.kv_heads : 0;
+}
+__device__ __forceinline__ int64_t run_begin(int64_t total, int ctas, int c) {
+    const int64_t per = total / ctas, rest = total - per * ctas;
+    return per * c + rest * c / ctas;
+}
+// The tile that place `at` of a unit stands for.
+__device__ __forceinline__ int tile_at(int64_t at, int cost, int tiles) {
+    return at <= 0 ? 0 : at >= cost ? tiles : int(at * tiles / cost);
 }
 
 }  // namespace hs_prefill

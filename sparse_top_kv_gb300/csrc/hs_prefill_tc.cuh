@@ -1,0 +1,1167 @@
+// hs_prefill_tc.cuh -- the attention kernel of hs_paged_prefill on the 5th-
+// generation tensor cores (included by one translation unit per cache type).
+//
+// Math, per new token i and query head h of KV head g, over the cached tokens t
+// that the token's position attends to:
+//   x_t = scale * k_scale_g * (q . K_t),  p_t = 2^((x_t - m) log2 e),
+//   l = sum p_t,  out = v_scale_g / l * sum p_t V_t,
+// as (m, l, sum) states, exact under merging (the rule of hs_merge_states).
+//
+// 4 d flops per (query, token) and head: the tensor cores bound long chunks, HBM
+// and latency few tokens.
+//  * A query tile is 128 rows of (new token, query head of the KV head), so that
+//    a K tile of 128 cached tokens serves every head that shares it, and the
+//    causal edge is 128 / group tokens wide.  Two query tiles share the K and V
+//    tiles (heads of 256: one), and the tensor cores work on one while the other
+//    is in its softmax.
+//  * S[queries x tokens] = Q K^T from shared memory into TMEM; P goes back into
+//    the S columns as the A operand of O += P V, V an MN-major view of its tile.
+//    A thread per query row: no shuffle in the softmax, and P, O and the
+//    statistics of a row never leave their lane.
+//  * Softmax against a reference maximum that moves only when a logit exceeds it
+//    by 2^kThresh, so that O is rescaled a few times a unit.
+//  * P is rounded once to the type of V's products: bf16, or fp16 raised by
+//    2^kShift, so that weights down to 2^-25 of the reference keep 11 bits and
+//    smaller ones 2^-36 of it.  The sums l are of unrounded weights, in fp32.
+//  * E4M3 caches become fp16 in shared memory (exact), bf16 queries fp16 of
+//    their row's largest magnitude 2^14 (elements down to 2^-28 of it exact).
+//  * Loads: 16-bit caches whose pages hold runs of 16 tokens by TMA; others and
+//    E4M3 by 128 threads, a batch of loads ahead of the stores.
+//  * Entries of V that are not finite must not meet a weight of 0.  Where some
+//    query of the unit does not see some token of a tile, rows that no query
+//    sees become 0, and rows with entries that are not finite too; those are
+//    added to the queries that do see them, one by one.
+// Every wait is bounded (HS_ERR_TIMEOUT in the status word on expiry).
+#pragma once
+
+#include <cuda.h>
+
+#include "hs_pair.cuh"
+#include "hs_prefill.cuh"
+#include "hs_shared.h"
+#include "hs_tcgen05.cuh"
+
+namespace hs_prefill {
+namespace tc {
+
+enum Kind { kBf16 = 0, kFp16 = 1, kE4m3 = 2 };
+
+constexpr int kThreads = 512;
+constexpr int kMmaWarp = 8;    // 9 to 11: queries
+constexpr int kQWarps = 3;
+constexpr int kLoadWarp = 12;  // TMA: 13 to 15 check V; else all four load
+constexpr int kCheckWarps = 3;
+constexpr int kLoadBar = 1;    // named barrier of the loading threads
+constexpr int kBlk = kTile * 128;  // 128 rows x 128 bytes
+constexpr int kRing = 16;      // tiles whose loaded tokens are remembered
+constexpr int kTmemCols = 512;
+constexpr int kSegRing = 4;    // units whose query scales are remembered
+
+struct TcArgs {
+    PrefillArgs p;
+    int32_t bt;  // tokens of a run (a TMA box): they lie in one page
+    uint64_t timeout_ns;
+};
+
+template <int KV, int D, bool TMA>
+struct Cfg {
+    static constexpr bool kE4 = KV == kE4m3;
+    static constexpr int NQ = D == 256 ? 1 : 2;            // query tiles of a unit
+    static constexpr int NB = D == 256 ? 2 : 1;            // S buffers of each
+    static constexpr int kDims = D < 128 ? D : 128;        // dims of a ring unit
+    static constexpr int kSubs = D / kDims;                // ring units of a tile
+    static constexpr int kUnit = kTile * kDims * 2;
+    static constexpr int kQTile = kTile * D * 2;
+    static constexpr int NS = D == 64 ? 10 : TMA ? 5 : 4;  // ring units
+    static constexpr int kQOff = 0;
+    static constexpr int kRingOff = NQ * kQTile;
+    static constexpr int kBarOff = kRingOff + NS * kUnit;
+    static constexpr uint32_t kOCol = 256;                 // TMEM: S (and P), then O
+    static constexpr uint32_t kOCols = D == 64 ? 64 : 128; // columns of an O tile (D = 256: two)
+    static constexpr float kThresh = KV == kBf16 ? 8.f : 4.f;
+    static constexpr float kShift = KV == kBf16 ? 0.f : 11.f;
+};
+
+struct Bars {
+    uint64_t full[10], ready[10], empty[10];
+    uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], o_free[2], pv_done, drain;
+    int64_t place0, place1, total, start;  // the run, and where its first unit starts
+    int32_t row, kvh, block;               // its first unit
+    uint32_t tmem_base;
+    volatile int32_t abort;
+    volatile int32_t keep[2];              // O holds something before the first product
+    alignas(16) uint32_t loaded[kRing][4]; // tokens of a tile that were loaded
+    alignas(16) uint32_t odd[kRing][2][4]; // rows of V that were taken out, by ring unit
+};
+struct BarsLdg : Bars {
+    int64_t offset[2][kTile];              // rows of a tile in the cache, -1: none
+};
+struct BarsE4 : BarsLdg {
+    float qscale[kSegRing][2 * kTile];
+};
+template <bool TMA, bool E4>
+struct BarsOf {
+    using T = Bars;
+};
+template <>
+struct BarsOf<false, false> {
+    using T = BarsLdg;
+};
+template <>
+struct BarsOf<false, true> {
+    using T = BarsE4;
+};
+
+// One unit's share of a run.
+struct Seg {
+    int row, kvh, block;
+    Request x;
+    int64_t start;   // its first place
+    int cost, nt;    // its places and tiles
+    int i0, i1;      // this run's tiles
+    int p0, m;       // position of its first query, and its tokens
+    int ns, tw;      // tiles of the sinks; the first tile of the rest
+    bool begins;     // the run holds the unit's first place
+};
+__device__ __forceinline__ int token_of(const Seg& s, int i) {
+    return (i < s.ns ? i : i - s.ns + s.tw) * kTile;
+}
+__device__ __forceinline__ void shape(const PrefillArgs& a, Seg& s, int64_t place0,
+                                      int64_t place1) {
+    s.m = min(a.tb, s.x.n - s.block * a.tb);
+    s.p0 = s.x.T - s.x.n + s.block * a.tb;
+    const int hi = max(0, s.p0 + s.m);  // tokens up to the last query's own
+    const int lo = a.window > 0 ? max(0, s.p0 + 1 - a.window) : 0;
+    s.tw = min(lo, hi) / kTile;
+    const int sc = a.window > 0 ? min(a.sinks, lo) : 0;
+    s.ns = min((sc + kTile - 1) / kTile, s.tw);
+    s.nt = s.ns + (hi + kTile - 1) / kTile - s.tw;
+    s.cost = int(places(a, s.x, s.block + 1) - places(a, s.x, s.block));
+    s.i0 = tile_at(place0 - s.start, s.cost, s.nt);
+    s.i1 = tile_at(place1 - s.start, s.cost, s.nt);
+    s.begins = place0 <= s.start;
+}
+// The run's first unit, or none (false).
+__device__ __forceinline__ bool first_seg(const PrefillArgs& a, const Bars& B, Seg& s) {
+    if (B.place0 >= B.place1) return false;
+    s.row = B.row;
+    s.kvh = B.kvh;
+    s.block = B.block;
+    s.start = B.start;
+    s.x = request_of(a, s.row);
+    shape(a, s, B.place0, B.place1);
+    return true;
+}
+__device__ __forceinline__ bool next_seg(const PrefillArgs& a, const Bars& B, Seg& s) {
+    s.start += s.cost;
+    if (s.start >= B.place1) return false;
+    if (++s.block >= blocks_of(a, s.x.n)) {
+        s.block = 0;
+        if (++s.kvh >= a.kv_heads) {
+            s.kvh = 0;
+            do {  // the next request with a new token; there is one
+                if (++s.row >= a.rows) return false;
+                s.x = request_of(a, s.row);
+            } while (s.x.n == 0);
+        }
+    }
+    shape(a, s, B.place0, B.place1);
+    return true;
+}
+// Whether any query of the unit sees token t.
+__device__ __forceinline__ bool any_sees(const PrefillArgs& a, const Seg& s, int t) {
+    return t < s.p0 + s.m && (a.window == 0 || t > s.p0 - a.window || t < a.sinks);
+}
+// Whether any of them sees any of the tokens [t, t + n).
+__device__ __forceinline__ bool any_sees(const PrefillArgs& a, const Seg& s, int t, int n) {
+    return t < s.p0 + s.m && (a.window == 0 || t + n - 1 > s.p0 - a.window || t < a.sinks);
+}
+// Whether every query of the unit sees every token of the tile from t on.
+__device__ __forceinline__ bool all_see(const PrefillArgs& a, const Seg& s, int t) {
+    return t + kTile - 1 <= s.p0 &&
+           (a.window == 0 || t > s.p0 + s.m - 1 - a.window || t + kTile <= a.sinks);
+}
+
+// The run of this CTA: its places, and the unit that they begin in.  All
+// threads; ends with a barrier.
+__device__ __forceinline__ void make_plan(const PrefillArgs& a, Bars& B, int64_t* sums) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int kWarps = kThreads / 32;
+    // Inclusive sum over the block; *all receives the total.
+    const auto scan = [&](int64_t v, int64_t* all) {
+        const int64_t own = v;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t o = __shfl_up_sync(0xffffffffu, v, d);
+            if (lane >= d) v += o;
+        }
+        __syncthreads();
+        if (lane == 31) sums[warp] = v;
+        __syncthreads();
+        int64_t before = 0, total = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) before += sums[w];
+            total += sums[w];
+        }
+        *all = total;
+        return before + v - own;
+    };
+    int64_t total = 0, at = 0, own = 0;
+    Request x{};
+    for (int r0 = 0; r0 < a.rows; r0 += kThreads) {
+        own = 0;
+        if (r0 + tid < a.rows) {
+            x = request_of(a, r0 + tid);
+            own = places_of(a, x);
+        }
+        int64_t all;
+        at = scan(own, &all);
+        total += all;
+    }
+    const int64_t p0 = run_begin(total, a.ctas, blockIdx.x);
+    const int64_t p1 = run_begin(total, a.ctas, blockIdx.x + 1);
+    int64_t base = 0;
+    for (int r0 = 0; r0 < a.rows; r0 += kThreads) {
+        if (a.rows > kThreads) {
+            own = 0;
+            if (r0 + tid < a.rows) {
+                x = request_of(a, r0 + tid);
+                own = places_of(a, x);
+            }
+            int64_t all;
+            at = base + scan(own, &all);
+            base += all;
+        }
+        if (own > 0 && p0 >= at && p0 < at + own) {
+            const int64_t each = own / a.kv_heads;
+            const int kvh = int((p0 - at) / each);
+            const int64_t rel = p0 - at - kvh * each;
+            int lo = 0, hi = blocks_of(a, x.n);
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (places(a, x, mid) <= rel) lo = mid;
+                else hi = mid;
+            }
+            B.row = r0 + tid;
+            B.kvh = kvh;
+            B.block = lo;
+            B.start = at + kvh * each + places(a, x, lo);
+        }
+    }
+    if (tid == 0) {
+        B.place0 = p0;
+        B.place1 = p1;
+        B.total = total;
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int tok,
+                                         int head, int page, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(tok), "r"(head), "r"(page), "r"(hs::smem_u32(bar))
+        : "memory");
+}
+// D(tmem) (+)= A(tmem) B(smem desc), 16-bit in, f32 accumulate.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// kind::f16, fp32 accumulators, A K-major (or in TMEM), M = 128.
+template <int KV>
+__host__ __device__ constexpr uint32_t idesc(int N, int b_mn_major) {
+    return (1u << 4) | ((KV == kBf16 ? 1u : 0u) << 7) | ((KV == kBf16 ? 1u : 0u) << 10) |
+           (uint32_t(b_mn_major) << 16) | (uint32_t(N >> 3) << 17) | (uint32_t(kTile >> 4) << 24);
+}
+
+// 32 lanes x 32 columns of 32 bit.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+        "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
+    return r;
+}
+template <int N>
+__device__ __forceinline__ void set_max_regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_max_regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// 2^x (PTX ex2.approx.ftz: within 2 ulp; 0 below -126, where a weight no longer
+// counts against the sum's 1).
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+template <int KV>
+__device__ __forceinline__ uint32_t pack(float x, float y) {
+    if constexpr (KV == kBf16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
+// The low n bits (n outside [0, 32] as the nearest).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t c) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3);
+    return uint32_t(h.x) | (uint32_t(h.y) << 16);
+}
+// Whether any of the 16 bytes' entries is not finite.
+template <int KV>
+__device__ __forceinline__ bool not_finite(const uint4& w) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (KV == kE4m3) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) any |= ((u[i] >> j) & 0x7fu) == 0x7fu;
+        } else {
+            constexpr uint32_t e = KV == kBf16 ? 0x7f80u : 0x7c00u;
+            any |= (u[i] & e) == e || ((u[i] >> 16) & e) == e;
+        }
+    }
+    return any;
+}
+// Element i of a cache row as fp32.
+template <int KV>
+__device__ __forceinline__ float element(const void* row, int i) {
+    if constexpr (KV == kBf16) return __bfloat162float(static_cast<const __nv_bfloat16*>(row)[i]);
+    else if constexpr (KV == kFp16) return __half2float(static_cast<const __half*>(row)[i]);
+    else return float(static_cast<const __nv_fp8_e4m3*>(row)[i]);
+}
+
+template <int KV, int D, bool TMA>
+__global__ void __launch_bounds__(kThreads, 1)
+prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap) {
+    using C = Cfg<KV, D, TMA>;
+    constexpr int NQ = C::NQ, NS = C::NS, kSubs = C::kSubs;
+    constexpr bool E4 = C::kE4;
+    using BarsT = typename BarsOf<TMA, E4>::T;
+    const PrefillArgs& a = ta.p;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    BarsT& B = *reinterpret_cast<BarsT*>(smem + C::kBarOff);
+    const uint32_t sb = hs::smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint64_t tmo = ta.timeout_ns;
+    const volatile int* abort_flag = &B.abort;
+
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            hs::mbar_init(&B.full[i], TMA ? 1 : kTile);
+            hs::mbar_init(&B.ready[i], TMA ? kCheckWarps : kTile);
+            hs::mbar_init(&B.empty[i], 1);
+        }
+        hs::mbar_init(&B.q_full, kQWarps * 32);
+        hs::mbar_init(&B.q_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            hs::mbar_init(&B.s_full[i], 1);
+            hs::mbar_init(&B.p_full[i], kTile);
+            hs::mbar_init(&B.o_full[i], 1);
+            hs::mbar_init(&B.o_free[i], kTile);
+        }
+        hs::mbar_init(&B.pv_done, 1);
+        hs::mbar_init(&B.drain, 1);
+        B.abort = 0;
+        hs::fence_mbar_init();
+    }
+    if (TMA && warp == kLoadWarp && lane < 2)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &kmap : &vmap) : "memory");
+    if (warp == kMmaWarp) {
+        hs::tc::tmem_alloc(&B.tmem_base, kTmemCols);
+        hs::tc::tmem_relinquish();
+    }
+    hs::tc::fence_before_sync();
+    __syncthreads();
+    hs::tc::fence_after_sync();
+    hs::pdl_wait();
+    hs::pdl_trigger();
+    if (blockIdx.x == 0)
+        for (int r = tid; r < a.rows; r += kThreads) {
+            const int c0 = a.cu_new[r], c1 = a.cu_new[r + 1];
+            if (a.seq_lens[r] > a.max_len || c0 < 0 || c1 < c0 || c1 > a.tokens)
+                hs::set_status(a.status, HS_ERR_BAD_INDEX);
+        }
+    make_plan(a, B, reinterpret_cast<int64_t*>(smem));
+    const uint32_t tmem = B.tmem_base;
+    const auto give_up = [&] {
+        hs::set_status(a.status, HS_ERR_TIMEOUT);
+        B.abort = 1;
+    };
+    const auto wait = [&](uint64_t* bar, int parity) {
+        return hs::mbar_wait_bounded(bar, uint32_t(parity & 1), tmo, abort_flag);
+    };
+    // Ring unit s of the CTA's tile t: first those of K, then those of V.
+    const auto unit_of = [](int t, bool v, int s) { return (2 * t + (v ? 1 : 0)) * kSubs + s; };
+    // Barriers that complete once per unit of V (`ready`), or of K (`full`, where
+    // threads load), count those alone.
+    const auto turn_of = [](int t, int s) { return t * kSubs + s; };
+    Seg s;
+
+    if (warp < 8) {
+        // ------------------------- softmax and output -------------------------
+        set_max_regs_up<192>();
+        const int w = warp >> 2;   // query tile (NQ = 1: only 0 works)
+        const int r = tid & 127;   // row of the tile, and TMEM lane
+        const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+        const int tok = r / a.group, hd = r - tok * a.group;  // its new token and query head
+        const uint32_t o_addr = tmem + lanes + C::kOCol + uint32_t(NQ == 2 ? w * 128 : 0);
+        const bool bf = KV == kBf16 || (E4 && !a.q_is_half);
+        bool ok = w < NQ;
+        int t = 0, mine = 0, units = 0;  // the CTA's tiles, this tile's, units with tiles
+        int segs = 0;                    // this query tile's units
+        bool head = false;               // the run ends in the first part of a shared unit
+        for (bool more = ok && first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
+            const int n = s.i1 - s.i0;
+            const bool live = tok < a.tq && w * a.tq + tok < s.m;
+            const int64_t qh = int64_t(s.x.first + s.block * a.tb + w * a.tq + tok) * a.heads +
+                               s.kvh * a.group + hd;
+            if (n == 0) {
+                if (s.nt == 0 && s.begins && live) {
+                    // Nothing is attended to: zeros.
+                    for (int i = 0; i < D / 8; ++i)
+                        reinterpret_cast<uint4*>(a.out)[qh * (D / 8) + i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (a.lse != nullptr) a.lse[qh] = -CUDART_INF_F;
+                }
+                continue;
+            }
+            const bool whole = s.i0 == 0 && s.i1 == s.nt;
+            if (w == 0 && tid == 0 && !whole && s.i0 == 0) {
+                head = true;
+                SharedUnit u;
+                u.start = s.start;
+                u.total = B.total;
+                u.cost = s.cost;
+                u.tiles = s.nt;
+                u.first = s.x.first + s.block * a.tb;
+                u.tokens = s.m;
+                u.kvh = s.kvh;
+                u.valid = 1;
+                a.shared[blockIdx.x] = u;
+            }
+            const int useg = units++;
+            if (w * a.tq >= s.m) {  // the second tile of a unit that has one
+                t += n;
+                continue;
+            }
+            // The row's position; rows without a query see what the last does.
+            const int pos = s.p0 + min(w * a.tq + tok, s.m - 1);
+            float scl = a.scale_log2;
+            float off = -CUDART_INF_F, l0 = 0.f, l1 = 0.f;  // reference - kShift, sums
+            for (int i = s.i0; i < s.i1; ++i, ++t, ++mine) {
+                const int x = NQ == 2 ? w : mine & 1;
+                const int ph = NQ == 2 ? mine : mine >> 1;
+                const uint32_t s_addr = tmem + lanes + uint32_t(x * 128);
+                ok = __all_sync(0xffffffffu, wait(&B.s_full[x], ph));
+                if (!ok) break;
+                hs::tc::fence_after_sync();
+                float v[128];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, v + c * 32);
+                if (i == s.i0) {
+                    // (0 would turn masked places into NaN; 2^-126 does not show.)
+                    if constexpr (E4) {
+                        scl *= B.qscale[useg & (kSegRing - 1)][w * kTile + r];
+                        if (a.k_scale != nullptr) scl *= a.k_scale[s.kvh];
+                    }
+                    if (scl == 0.f) scl = 1.17549435e-38f;
+                }
+                // What this row sees of the tile.
+                const int t0 = token_of(s, i);
+                const uint4 ld = *reinterpret_cast<const uint4*>(B.loaded[t & (kRing - 1)]);
+                const uint32_t lw[4] = {ld.x, ld.y, ld.z, ld.w};
+                const bool part = !all_see(a, s, t0) || (ld.x & ld.y & ld.z & ld.w) != 0xffffffffu;
+                uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+                hs::tc::tmem_wait_ld();
+                if (scl < 0.f) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) v[c] = -v[c];
+                }
+                const float as = fabsf(scl);
+                if (part) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int b = t0 + 32 * j;
+                        vis[j] = low_bits(pos + 1 - b) & lw[j];
+                        if (a.window > 0)
+                            vis[j] &= ~low_bits(pos - a.window + 1 - b) | low_bits(a.sinks - b);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (!((vis[j] >> c) & 1u)) v[32 * j + c] = -CUDART_INF_F;
+                    }
+                }
+                float mx[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+                for (int c = 4; c < 128; c += 4)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], v[c + j]);
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * as;
+                // The reference moves up to the maximum where that is far above.
+                const bool grow = top - C::kShift > off + C::kThresh || (off == -CUDART_INF_F && top > off);
+                if (i == s.i0) {
+                    if (grow) off = top - C::kShift;
+                } else if (__any_sync(0xffffffffu, grow)) {
+                    const float to = grow ? top - C::kShift : off;
+                    const float al = grow ? (off == -CUDART_INF_F ? 0.f : ex2(off - to)) : 1.f;
+                    off = to;
+                    l0 *= al;
+                    l1 *= al;
+                    // The products into O so far are done (two tiles: S of this
+                    // one was issued behind them).
+                    if (NQ == 1) {
+                        ok = __all_sync(0xffffffffu, wait(&B.pv_done, mine - 1));
+                        if (!ok) break;
+                        hs::tc::fence_after_sync();
+                    }
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        float o[16];
+                        hs::tc::tmem_ld16(o_addr + uint32_t(c), o);
+                        hs::tc::tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[j] *= al;
+                        hs::tc::tmem_st16(o_addr + uint32_t(c), o);
+                    }
+                }
+                // Without a finite logit so far: subtract 0, every weight is 0
+                // (a NaN logit stays NaN).
+                const float ref = off == -CUDART_INF_F ? 0.f : off;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float pa = ex2(fmaf(v[32 * c + 2 * j], as, -ref));
+                        const float pb = ex2(fmaf(v[32 * c + 2 * j + 1], as, -ref));
+                        l0 += pa;
+                        l1 += pb;
+                        pk[j] = pack<KV>(pa, pb);
+                    }
+                    tmem_st16u(s_addr + c * 16, pk);
+                }
+                hs::tc::tmem_wait_st();
+                if (part) {
+                    // Rows of V that were taken out.
+                    uint32_t any = 0;
+                    for (int u = 0; u < kSubs && ok; ++u) {
+                        const int q = turn_of(t, u);
+                        ok = __all_sync(0xffffffffu, wait(&B.ready[q % NS], q / NS));
+                        const uint4 o = *reinterpret_cast<const uint4*>(B.odd[t & (kRing - 1)][u]);
+                        any |= o.x | o.y | o.z | o.w;
+                    }
+                    if (!ok) break;
+                    if (i == s.i0) B.keep[w] = any != 0;
+                    if (any != 0) {
+                        if (NQ == 1 && i != s.i0) {
+                            ok = __all_sync(0xffffffffu, wait(&B.pv_done, mine - 1));
+                            if (!ok) break;
+                            hs::tc::fence_after_sync();
+                        }
+                        const float zero[16] = {};
+                        if (i == s.i0)
+                            for (int c = 0; c < D; c += 16) hs::tc::tmem_st16(o_addr + uint32_t(c), zero);
+                        hs::tc::tmem_wait_st();
+                        for (int j = 0; j < kTile; ++j) {
+                            const uint32_t pw = tmem_ld1(s_addr + uint32_t(j >> 1));
+                            hs::tc::tmem_wait_ld();
+                            const uint32_t h = (j & 1) ? pw >> 16 : pw & 0xffffu;
+                            const float p = KV == kBf16 ? __uint_as_float(h << 16)
+                                                        : __half2float(__ushort_as_half(uint16_t(h)));
+                            const uint32_t vw = j < 32 ? vis[0] : j < 64 ? vis[1] : j < 96 ? vis[2] : vis[3];
+                            const bool sees = (vw >> (j & 31)) & 1u;
+                            for (int u = 0; u < kSubs; ++u) {
+                                if (!((B.odd[t & (kRing - 1)][u][j >> 5] >> (j & 31)) & 1u)) continue;
+                                const int tk = t0 + j, b = block_of(a, tk);
+                                const int64_t page = a.block_table[s.row * a.bt_stride + b];
+                                const void* row = static_cast<const char*>(a.v) +
+                                    (page * a.page_stride + int64_t(tk - b * a.page_size) * a.row_stride +
+                                     s.kvh * a.head_stride) * (E4 ? 1 : 2);
+                                for (int c = u * C::kDims; c < (u + 1) * C::kDims; c += 16) {
+                                    float o[16];
+                                    hs::tc::tmem_ld16(o_addr + uint32_t(c), o);
+                                    hs::tc::tmem_wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e)
+                                        if (sees) o[e] = fmaf(p, element<KV>(row, c + e), o[e]);
+                                    hs::tc::tmem_st16(o_addr + uint32_t(c), o);
+                                    hs::tc::tmem_wait_st();
+                                }
+                            }
+                        }
+                    }
+                } else if (i == s.i0) {
+                    B.keep[w] = 0;
+                }
+                hs::tc::fence_before_sync();
+                hs::mbar_arrive(&B.p_full[x]);
+            }
+            if (!ok) break;
+            // ---- The unit's state ---------------------------------------------
+            ok = __all_sync(0xffffffffu, wait(&B.o_full[w], segs));
+            if (!ok) break;
+            ++segs;
+            hs::tc::fence_after_sync();
+            const float l = l0 + l1;
+            const float lg = l == 0.f ? -CUDART_INF_F : off + log2f(l);
+            float f = 1.f;
+            if (whole) {
+                f = l == 0.f ? 0.f : 1.f / l;
+                if (a.v_scale != nullptr && l != 0.f) f *= a.v_scale[s.kvh];
+                if (live && a.lse != nullptr) a.lse[qh] = lg * kLn2;
+            }
+            const int64_t slot = int64_t(2 * blockIdx.x + (s.start < B.place0 ? 0 : 1)) * a.unit_rows +
+                                 w * kTile + r;
+            if (!whole && live) {
+                a.part_ml[2 * slot] = off;
+                a.part_ml[2 * slot + 1] = l;
+            }
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                float o[32];
+                tmem_ld32(o_addr + uint32_t(c), o);
+                hs::tc::tmem_wait_ld();
+                if (!live) continue;
+                if (!whole) {
+                    float4* po = reinterpret_cast<float4*>(a.part_o + slot * D + c);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        po[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    continue;
+                }
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = l == 0.f ? 0.f : o[j] * f;
+                uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + qh * D + c);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t y[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        y[e] = bf ? pack<kBf16>(o[8 * j + 2 * e], o[8 * j + 2 * e + 1])
+                                  : pack<kFp16>(o[8 * j + 2 * e], o[8 * j + 2 * e + 1]);
+                    out[j] = make_uint4(y[0], y[1], y[2], y[3]);
+                }
+            }
+            hs::tc::fence_before_sync();
+            hs::mbar_arrive(&B.o_free[w]);
+        }
+        if (w < NQ && !ok) give_up();
+        if (tid == 0 && !head) a.shared[blockIdx.x].valid = 0;
+    } else if (warp < kLoadWarp) {
+        set_max_regs_down<40>();
+        if (warp == kMmaWarp) {
+            // ------------------------------ products ----------------------------
+            if (lane == 0) {
+                constexpr uint32_t id_qk = idesc<KV>(kTile, 0), id_pv = idesc<KV>(C::kDims, 1);
+                const uint64_t q_desc = hs::tc::sdesc_sw128(sb + C::kQOff, 16, 1024);
+                const uint64_t k_desc = hs::tc::sdesc_sw128(sb + C::kRingOff, 16, 1024);
+                const uint64_t v_desc = hs::tc::sdesc_sw128(sb + C::kRingOff, kBlk, 1024);
+                bool ok = true;
+                int t = 0, segs = 0, done[2] = {0, 0}, had[2] = {0, 0};
+                // S of query tile (or buffer) x from the K tile in the ring.
+                const auto qk = [&](int t, int x, int tile) {
+#pragma unroll
+                    for (int u = 0; u < kSubs; ++u) {
+                        const uint32_t at = uint32_t(unit_of(t, false, u) % NS * (C::kUnit >> 4));
+#pragma unroll
+                        for (int k = 0; k < C::kDims / 16; ++k) {
+                            const int b = u * (C::kDims / 64) + k / 4;
+                            hs::tc::mma_bf16(tmem + uint32_t(x * 128),
+                                             q_desc + uint32_t(tile * (C::kQTile >> 4) + b * (kBlk >> 4) + (k & 3) * 2),
+                                             k_desc + at + uint32_t(k / 4 * (kBlk >> 4) + (k & 3) * 2),
+                                             id_qk, (u | k) ? 1u : 0u);
+                        }
+                    }
+                };
+                const auto wait_k = [&](int t) {
+                    for (int u = 0; u < kSubs; ++u) {
+                        const int q = TMA ? unit_of(t, false, u) : turn_of(t, u);
+                        ok = ok && wait(&B.full[q % NS], q / NS);
+                    }
+                    hs::tc::fence_after_sync();
+                };
+                const auto wait_v = [&](int t) {
+                    for (int u = 0; u < kSubs; ++u) {
+                        const int q = turn_of(t, u);
+                        ok = ok && wait(&B.ready[q % NS], q / NS);
+                    }
+                    hs::tc::fence_after_sync();
+                };
+                const auto free_units = [&](int t, bool v) {
+                    for (int u = 0; u < kSubs; ++u) hs::tc::mma_commit(&B.empty[unit_of(t, v, u) % NS]);
+                };
+                const auto pv = [&](int t, int x, int tile, bool fresh) {
+#pragma unroll
+                    for (int u = 0; u < kSubs; ++u) {
+                        const uint32_t at = uint32_t(unit_of(t, true, u) % NS * (C::kUnit >> 4));
+#pragma unroll
+                        for (int k = 0; k < kTile / 16; ++k)
+                            mma_ts(tmem + C::kOCol + uint32_t(tile * 128 + u * 128),
+                                   tmem + uint32_t(x * 128 + k * 8), v_desc + at + uint32_t(k * 128),
+                                   id_pv, fresh && k == 0 ? 0u : 1u);
+                    }
+                };
+                for (bool more = first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
+                    const int n = s.i1 - s.i0;
+                    if (n == 0) continue;
+                    const int tiles = NQ == 2 && s.m > a.tq ? 2 : 1;
+                    ok = ok && wait(&B.q_full, segs);
+                    ++segs;
+                    wait_k(t);
+                    if (!ok) break;
+                    if (NQ == 2) {
+                        for (int x = 0; x < tiles; ++x) {
+                            qk(t, x, x);
+                            hs::tc::mma_commit(&B.s_full[x]);
+                        }
+                    } else {
+                        qk(t, t & 1, 0);
+                        hs::tc::mma_commit(&B.s_full[t & 1]);
+                    }
+                    free_units(t, false);
+                    if (n == 1) hs::tc::mma_commit(&B.q_empty);
+                    for (int i = 0; i < n && ok; ++i, ++t) {
+                        const bool next = i + 1 < n;
+                        if (NQ == 1 && next) {
+                            wait_k(t + 1);
+                            if (!ok) break;
+                            qk(t + 1, (t + 1) & 1, 0);
+                            hs::tc::mma_commit(&B.s_full[(t + 1) & 1]);
+                            free_units(t + 1, false);
+                            if (i + 2 == n) hs::tc::mma_commit(&B.q_empty);
+                        }
+                        for (int tile = 0; tile < tiles && ok; ++tile) {
+                            const int x = NQ == 2 ? tile : t & 1;
+                            const int ph = NQ == 2 ? done[tile] : t >> 1;
+                            // The output before has been read.
+                            if (i == 0 && had[tile] > 0) ok = wait(&B.o_free[tile], had[tile] - 1);
+                            ok = ok && wait(&B.p_full[x], ph);
+                            if (tile == 0) wait_v(t);
+                            hs::tc::fence_after_sync();
+                            if (!ok) break;
+                            pv(t, x, tile, i == 0 && B.keep[tile] == 0);
+                            ++done[tile];
+                            if (NQ == 1) hs::tc::mma_commit(&B.pv_done);
+                            if (tile == tiles - 1) free_units(t, true);
+                            if (!next) {
+                                hs::tc::mma_commit(&B.o_full[tile]);
+                                ++had[tile];
+                            } else if (NQ == 2) {
+                                if (tile == 0) wait_k(t + 1);
+                                if (!ok) break;
+                                qk(t + 1, x, tile);
+                                hs::tc::mma_commit(&B.s_full[x]);
+                                if (tile == tiles - 1) {
+                                    free_units(t + 1, false);
+                                    if (i + 2 == n) hs::tc::mma_commit(&B.q_empty);
+                                }
+                            }
+                        }
+                    }
+                }
+                if (!ok) give_up();
+                // Every product issued has completed before TMEM is freed.
+                hs::tc::mma_commit(&B.drain);
+                hs::mbar_wait_bounded(&B.drain, 0, tmo, nullptr);
+            }
+            __syncwarp();
+        } else {
+            // ------------------------------- queries ----------------------------
+            const int qw = warp - kMmaWarp - 1, qt = qw * 32 + lane;
+            bool ok = true;
+            int segs = 0;
+            for (bool more = first_seg(a, B, s); more; more = next_seg(a, B, s)) {
+                if (s.i1 == s.i0) continue;
+                if (segs > 0 && !__all_sync(0xffffffffu, wait(&B.q_empty, segs - 1))) {
+                    ok = false;
+                    break;
+                }
+                const int64_t first = s.x.first + s.block * a.tb;
+                const char* q = static_cast<const char*>(a.q) + int64_t(s.kvh) * a.group * D * 2;
+                constexpr int kCh = D / 8;  // 16-byte chunks of a row
+                if constexpr (!E4) {
+                    for (int e = qt; e < NQ * kTile * kCh; e += kQWarps * 32) {
+                        const int n = e / kCh, ch = e % kCh, w = n / kTile, r = n % kTile;
+                        const int tok = r / a.group, hd = r - tok * a.group;
+                        const bool in = tok < a.tq && w * a.tq + tok < s.m;
+                        const int64_t at = in ? (first + w * a.tq + tok) * a.q_stride + hd * D + ch * 8 : 0;
+                        hs::tc::cp_async16(sb + C::kQOff + w * C::kQTile + (ch >> 3) * kBlk + r * 128 +
+                                               (((ch & 7) ^ (r & 7)) << 4),
+                                           q + at * 2, in ? 16u : 0u);
+                    }
+                    hs::tc::cp_async_wait_all();
+                } else {
+                    // A row per D / 8 lanes.
+                    constexpr int kRows = 32 / kCh;
+                    const int ch = lane % kCh;
+                    for (int n = qw * kRows + lane / kCh; n < NQ * kTile; n += kQWarps * kRows) {
+                        const int w = n / kTile, r = n % kTile;
+                        const int tok = r / a.group, hd = r - tok * a.group;
+                        const bool in = tok < a.tq && w * a.tq + tok < s.m;
+                        uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+                        if (in)
+                            raw = *reinterpret_cast<const uint4*>(
+                                q + ((first + w * a.tq + tok) * a.q_stride + hd * D + ch * 8) * 2);
+                        float scale = 1.f;
+                        if (!a.q_is_half) {
+                            uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+                            float f[8], mx = 0.f;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u[i]));
+                                f[2 * i] = y.x;
+                                f[2 * i + 1] = y.y;
+                                mx = fmaxf(mx, fmaxf(fabsf(y.x), fabsf(y.y)));
+                            }
+#pragma unroll
+                            for (int o = kCh / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                            // Largest magnitude to [2^14, 2^15), by two factors
+                            // (their product may lie outside fp32's range).
+                            int e = 0;
+                            if (mx > 0.f && mx < CUDART_INF_F)
+                                e = max(14 - (int(__float_as_uint(mx) >> 23) - 127), -126);
+                            const int ea = e / 2, eb = e - ea;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                u[i] = pack<kFp16>(f[2 * i] * pow2(ea) * pow2(eb),
+                                                   f[2 * i + 1] * pow2(ea) * pow2(eb));
+                            raw = make_uint4(u[0], u[1], u[2], u[3]);
+                            scale = pow2(-ea) * pow2(-eb);
+                        }
+                        *reinterpret_cast<uint4*>(smem + C::kQOff + w * C::kQTile + (ch >> 3) * kBlk + r * 128 +
+                                                  (((ch & 7) ^ (r & 7)) << 4)) = raw;
+                        if (ch == 0) B.qscale[segs & (kSegRing - 1)][n] = scale;
+                    }
+                }
+                hs::fence_proxy_async_shared();
+                hs::mbar_arrive(&B.q_full);
+                ++segs;
+            }
+            if (!ok) give_up();
+        }
+    } else if constexpr (TMA) {
+        set_max_regs_down<88>();
+        const int runs = kTile / ta.bt;  // a power of two up to 8
+        if (warp == kLoadWarp) {
+            // -------------------------------- loads -----------------------------
+            bool ok = true, bad = false;
+            int t = 0, seq = 0;
+            const uint32_t box = uint32_t(ta.bt) * 128u;
+            for (bool more = first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
+                for (int i = s.i0; i < s.i1 && ok; ++i, ++t) {
+                    // Lane i: run i of the tile.
+                    const int tok = token_of(s, i) + lane * ta.bt;
+                    const int b = block_of(a, tok);
+                    const bool wants = lane < runs && any_sees(a, s, tok, ta.bt);
+                    const int page = wants ? a.block_table[s.row * a.bt_stride + b] : -1;
+                    const bool want = wants && page >= 0 && page < a.num_pages;
+                    if (wants && !want) bad = true;
+                    const uint32_t got = __ballot_sync(0xffffffffu, want);
+                    if (lane < 4) {
+                        uint32_t bits = 0;
+                        if (ta.bt >= 32) {
+                            bits = (got >> (lane * 32 / ta.bt)) & 1u ? 0xffffffffu : 0u;
+                        } else {  // 16
+                            if ((got >> (2 * lane)) & 1u) bits |= 0xffffu;
+                            if ((got >> (2 * lane + 1)) & 1u) bits |= 0xffff0000u;
+                        }
+                        B.loaded[t & (kRing - 1)][lane] = bits;
+                    }
+                    __syncwarp();
+                    const uint32_t bytes = uint32_t(__popc(got)) * box * (C::kDims / 64);
+                    const int at = tok - b * a.page_size;
+                    for (int u = 0; u < 2 * kSubs; ++u, ++seq) {
+                        const int slot = seq % NS;
+                        ok = __all_sync(0xffffffffu, wait(&B.empty[slot], seq / NS + 1));
+                        if (!ok) break;
+                        if (lane == 0) hs::mbar_arrive_expect_tx(&B.full[slot], bytes);
+                        __syncwarp();
+                        if (want) {
+                            const uint32_t dst = sb + C::kRingOff + slot * C::kUnit + lane * box;
+#pragma unroll
+                            for (int c = 0; c < C::kDims / 64; ++c)
+                                tma_load(dst + c * kBlk, u < kSubs ? &kmap : &vmap,
+                                         u % kSubs * C::kDims + c * 64, at, s.kvh, page, &B.full[slot]);
+                        }
+                    }
+                }
+            }
+            if (!ok) {
+                give_up();
+                // No copy may outlive the CTA: wait for every unit in flight.
+                for (int q = max(0, seq - NS); q < seq; ++q)
+                    hs::mbar_wait_bounded(&B.full[q % NS], (q / NS) & 1, tmo, nullptr);
+            }
+            if (bad) hs::set_status(a.status, HS_ERR_BAD_INDEX);
+        } else {
+            // ------------------------------ rows of V ---------------------------
+            const int cw = warp - kLoadWarp - 1;
+            bool ok = true;
+            int t = 0;
+            for (bool more = first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
+                for (int i = s.i0; i < s.i1 && ok; ++i, ++t) {
+                    const int t0 = token_of(s, i);
+                    for (int u = 0; u < kSubs; ++u) {
+                        const int q = unit_of(t, true, u);
+                        ok = __all_sync(0xffffffffu, wait(&B.full[q % NS], q / NS));
+                        if (!ok) break;
+                        const uint4 ld = *reinterpret_cast<const uint4*>(B.loaded[t & (kRing - 1)]);
+                        if (!all_see(a, s, t0) || (ld.x & ld.y & ld.z & ld.w) != 0xffffffffu) {
+                            for (int j = cw; j < 4; j += kCheckWarps) {
+                                const int r = j * 32 + lane;
+                                const bool in = any_sees(a, s, t0 + r) &&
+                                                ((B.loaded[t & (kRing - 1)][j] >> lane) & 1u);
+                                unsigned char* row = smem + C::kRingOff + q % NS * C::kUnit + r * 128;
+                                bool odd = false;
+                                if (in)
+                                    for (int c = 0; c < C::kDims / 8; ++c)
+                                        odd |= not_finite<KV>(*reinterpret_cast<const uint4*>(
+                                            row + (c >> 3) * kBlk + (((c + lane) & 7) << 4)));
+                                const uint32_t all = __ballot_sync(0xffffffffu, odd);
+                                if (lane == 0) B.odd[t & (kRing - 1)][u][j] = all;
+                                if (!in || odd)
+                                    for (int c = 0; c < C::kDims / 8; ++c)
+                                        *reinterpret_cast<uint4*>(row + (c >> 3) * kBlk + (((c + lane) & 7) << 4)) =
+                                            make_uint4(0u, 0u, 0u, 0u);
+                            }
+                            hs::fence_proxy_async_shared();
+                        }
+                        __syncwarp();
+                        if (lane == 0) hs::mbar_arrive(&B.ready[turn_of(t, u) % NS]);
+                    }
+                }
+            }
+            if (!ok) give_up();
+        }
+    } else {
+        // ------------------- loads by threads, and rows of V --------------------
+        set_max_regs_down<88>();
+        constexpr int kElt = E4 ? 1 : 2, kPer = 16 / kElt;  // elements of 16 bytes
+        constexpr int kCh = D / kPer;                       // 16-byte chunks of a row
+        constexpr int kStep = kTile / kCh;                  // rows of a pass
+        constexpr int kPass = kCh < 8 ? kCh : 8;            // passes of a batch
+        constexpr int kBatch = kPass * kStep, kBatches = kTile / kBatch;
+        const int lt = tid - kLoadWarp * 32, ch = lt % kCh, r0 = lt / kCh;
+        bool ok = true, bad = false;
+        int t = 0;
+        uint4 buf[2][kPass];
+        const auto rows_of = [&](int t, int i) {
+            // Row lt of the tile: where it lies in the cache.
+            const int tok = token_of(s, i) + lt, b = block_of(a, tok);
+            int64_t at = -1;
+            if (any_sees(a, s, tok)) {
+                const int64_t page = a.block_table[s.row * a.bt_stride + b];
+                if (page >= 0 && page < a.num_pages)
+                    at = page * a.page_stride + int64_t(tok - b * a.page_size) * a.row_stride +
+                         s.kvh * a.head_stride;
+                else
+                    bad = true;
+            }
+            B.offset[t & 1][lt] = at;
+            const uint32_t got = __ballot_sync(0xffffffffu, at >= 0);
+            if (lane == 0) {
+                B.loaded[t & (kRing - 1)][lt >> 5] = got;
+                B.odd[t & (kRing - 1)][0][lt >> 5] = 0;
+                B.odd[t & (kRing - 1)][1][lt >> 5] = 0;
+            }
+            hs::pair::named_sync(kLoadBar, kTile);
+        };
+        const auto load = [&](int t, bool v, int batch, uint4 (&x)[kPass]) {
+            const char* base = static_cast<const char*>(v ? a.v : a.k) + ch * 16;
+#pragma unroll
+            for (int j = 0; j < kPass; ++j) {
+                const int64_t at = B.offset[t & 1][batch * kBatch + j * kStep + r0];
+                x[j] = at >= 0 ? *reinterpret_cast<const uint4*>(base + at * kElt)
+                               : make_uint4(0u, 0u, 0u, 0u);
+            }
+        };
+        const auto store = [&](int t, bool v, int batch, uint4 (&x)[kPass], bool part) {
+#pragma unroll
+            for (int j = 0; j < kPass; ++j) {
+                const int r = batch * kBatch + j * kStep + r0;
+                if (v && part) {
+                    // A row's chunks lie in neighbouring lanes of one warp.
+                    const uint32_t odd = __ballot_sync(0xffffffffu, not_finite<KV>(x[j]));
+                    const uint32_t mine = (kCh == 32 ? 0xffffffffu : ((1u << (kCh & 31)) - 1u) << (lane / kCh * kCh));
+                    if (odd & mine) {
+                        x[j] = make_uint4(0u, 0u, 0u, 0u);
+                        if (ch == 0)
+                            for (int u = 0; u < kSubs; ++u)
+                                atomicOr(&B.odd[t & (kRing - 1)][u][r >> 5], 1u << (r & 31));
+                    }
+                }
+                const int c0 = E4 ? 2 * ch : ch;  // its first chunk of eight 16-bit elements
+                const int u = c0 * 8 / C::kDims, cb = c0 - u * (C::kDims / 8);
+                unsigned char* dst = smem + C::kRingOff + unit_of(t, v, u) % NS * C::kUnit +
+                                     (cb >> 3) * kBlk + r * 128;
+                if constexpr (E4) {
+                    uint4 y, z;
+                    y.x = e4m3x2_to_half2(x[j].x & 0xffffu);
+                    y.y = e4m3x2_to_half2(x[j].x >> 16);
+                    y.z = e4m3x2_to_half2(x[j].y & 0xffffu);
+                    y.w = e4m3x2_to_half2(x[j].y >> 16);
+                    z.x = e4m3x2_to_half2(x[j].z & 0xffffu);
+                    z.y = e4m3x2_to_half2(x[j].z >> 16);
+                    z.z = e4m3x2_to_half2(x[j].w & 0xffffu);
+                    z.w = e4m3x2_to_half2(x[j].w >> 16);
+                    *reinterpret_cast<uint4*>(dst + (((cb & 7) ^ (r & 7)) << 4)) = y;
+                    *reinterpret_cast<uint4*>(dst + ((((cb & 7) + 1) ^ (r & 7)) << 4)) = z;
+                } else {
+                    *reinterpret_cast<uint4*>(dst + (((cb & 7) ^ (r & 7)) << 4)) = x[j];
+                }
+            }
+        };
+        const auto wait_empty = [&](int t, bool v) {
+            bool fine = true;
+            for (int u = 0; u < kSubs; ++u) {
+                const int q = unit_of(t, v, u);
+                fine = fine && wait(&B.empty[q % NS], q / NS + 1);
+            }
+            // All or none go on: they meet at a barrier.
+            return !hs::pair::named_sync_or(kLoadBar, kTile, !fine);
+        };
+        const auto arrive = [&](int t, bool v) {
+            hs::fence_proxy_async_shared();
+            for (int u = 0; u < kSubs; ++u) {
+                const int q = turn_of(t, u);
+                hs::mbar_arrive(v ? &B.ready[q % NS] : &B.full[q % NS]);
+            }
+        };
+        for (bool more = first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
+            if (s.i0 == s.i1) continue;
+            rows_of(t, s.i0);
+            load(t, false, 0, buf[0]);
+            for (int i = s.i0; i < s.i1 && ok; ++i, ++t) {
+                const uint4 ld = *reinterpret_cast<const uint4*>(B.loaded[t & (kRing - 1)]);
+                const bool part = !all_see(a, s, token_of(s, i)) ||
+                                  (ld.x & ld.y & ld.z & ld.w) != 0xffffffffu;
+                // Batches of K, then of V; each is loaded while the one before
+                // it is stored.
+#pragma unroll
+                for (int j = 0; j < 2 * kBatches; ++j) {
+                    const bool v = j >= kBatches;
+                    if (j % kBatches == 0 && ok) ok = wait_empty(t, v);
+                    if (j + 1 < 2 * kBatches) {
+                        load(t, j + 1 >= kBatches, (j + 1) % kBatches, buf[(j + 1) & 1]);
+                    } else if (i + 1 < s.i1) {
+                        rows_of(t + 1, i + 1);
+                        load(t + 1, false, 0, buf[0]);
+                    }
+                    if (ok) {
+                        store(t, v, j % kBatches, buf[j & 1], part);
+                        if ((j + 1) % kBatches == 0) arrive(t, v);
+                    }
+                }
+            }
+        }
+        if (!ok) give_up();
+        if (bad) hs::set_status(a.status, HS_ERR_BAD_INDEX);
+    }
+    hs::tc::fence_before_sync();
+    __syncthreads();
+    hs::tc::fence_after_sync();
+    if (warp == kMmaWarp) hs::tc::tmem_dealloc(tmem, kTmemCols);
+}
+
+// Tensor map of a cache: dims (head dim, token of the page, KV head, page).
+int encode_map(CUtensorMap* m, const void* base, const PrefillArgs& a, int kv_dtype, int d, int bt);
+
+template <int KV, int D, bool TMA>
+int launch_one(const PrefillArgs& a, int bt, hs_stream_t stream) {
+    using C = Cfg<KV, D, TMA>;
+    TcArgs t{};
+    t.p = a;
+    t.bt = bt;
+    t.timeout_ns = hs::kWaitTimeoutNs;
+    auto kern = prefill_tc_kernel<KV, D, TMA>;
+    constexpr size_t smem = size_t(C::kBarOff) + sizeof(typename BarsOf<TMA, C::kE4>::T) + 1024;
+    static_assert(smem <= 227 * 1024, "shared memory");
+    static int smem_set[64] = {};
+    int rc = hs_host::ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem, smem_set);
+    if (rc != HS_OK) return rc;
+    // The warps' register shares (setmaxnreg) add up to what 128 a thread give.
+    static int regs[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return HS_ERR_CUDA;
+    const auto ask = [&] {
+        cudaFuncAttributes fa;
+        if (cudaFuncGetAttributes(&fa, kern) == cudaSuccess) return fa.numRegs;
+        cudaGetLastError();
+        return -1;
+    };
+    if (hs_host::ask_once(&regs[dev], ask) != 65536 / kThreads) return HS_ERR_UNSUPPORTED;
+    CUtensorMap k{}, v{};
+    if (TMA) {
+        rc = encode_map(&k, a.k, a, KV, D, bt);
+        if (rc == HS_OK) rc = encode_map(&v, a.v, a, KV, D, bt);
+        if (rc != HS_OK) return rc;
+    }
+    return hs_host::launch_pdl(kern, dim3(unsigned(a.ctas)), dim3(kThreads), smem, stream, t, k, v);
+}
+
+// bt: tokens of a TMA box, or 0: threads load.
+template <int KV>
+int launch_kind(const PrefillArgs& a, int d, int bt, hs_stream_t stream) {
+    if constexpr (KV != kE4m3) {
+        if (bt > 0) {
+            if (d == 64) return launch_one<KV, 64, true>(a, bt, stream);
+            if (d == 128) return launch_one<KV, 128, true>(a, bt, stream);
+            return launch_one<KV, 256, true>(a, bt, stream);
+        }
+    }
+    if (d == 64) return launch_one<KV, 64, false>(a, 0, stream);
+    if (d == 128) return launch_one<KV, 128, false>(a, 0, stream);
+    return launch_one<KV, 256, false>(a, 0, stream);
+}
+
+}  // namespace tc
+
+int launch_bf16(const PrefillArgs& a, int d, int bt, hs_stream_t stream);
+int launch_fp16(const PrefillArgs& a, int d, int bt, hs_stream_t stream);
+int launch_e4m3(const PrefillArgs& a, int d, int bt, hs_stream_t stream);
+
+}  // namespace hs_prefill
