@@ -2,7 +2,8 @@
 // Python without the interpreter in between: a decode step's kernel runs for
 // ten microseconds, and checking and converting thirty arguments in Python and
 // ctypes took as long again (13.4 us a call of hs_paged_decode, 5.5 here;
-// hs_evict 14.2 and 3.7).
+// hs_evict 14.2 and 3.7).  So did those of a step of several new tokens
+// (hs_paged_extend, hs_rope_append, hs_paged_prefill).
 //
 // Each function looks at its tensors and makes the C call if everything is as
 // in the common case: right types and shapes, contiguous, on the given device.
@@ -72,6 +73,47 @@ Tensor look(PyObject* o, int64_t device) {
     return x;
 }
 
+// Rows [tokens, heads, d] whose heads are packed; tokens may be strided.
+struct Rows {
+    at::ScalarType dtype = at::ScalarType::Undefined;
+    int64_t n = 0, heads = 0, d = 0, stride = 0;
+    void* ptr = nullptr;
+    bool ok = false;
+};
+
+Rows look_rows(PyObject* o, int64_t device) {
+    Rows x;
+    if (!THPVariable_Check(o)) return x;
+    try {
+        const at::Tensor& t = THPVariable_Unpack(o);
+        if (!t.is_cuda() || t.get_device() != device || t.dim() != 3) return x;
+        x.dtype = t.scalar_type();
+        x.n = t.size(0);
+        x.heads = t.size(1);
+        x.d = t.size(2);
+        if (x.n > INT32_MAX || x.heads > INT32_MAX || x.d > INT32_MAX || t.stride(2) != 1 ||
+            (x.heads > 1 && t.stride(1) != x.d))
+            return x;
+        x.stride = x.n > 1 ? t.stride(0) : x.heads * x.d;
+        x.ptr = t.data_ptr();
+        x.ok = x.dtype == at::kBFloat16 || x.dtype == at::kHalf;
+    } catch (const std::exception&) {
+    }
+    return x;
+}
+
+// A paged cache pair [pages, page_size, kv_heads, d].
+struct Cache {
+    Tensor k, v;
+    int64_t page_stride = 0, row_stride = 0, head_stride = 0;
+    int element = -1;
+};
+
+bool look_cache(PyObject* k, PyObject* v, int64_t device, Cache* c);
+
+// An optional status word: false where the common case does not apply.
+bool look_status(PyObject* o, int64_t device, int32_t** out);
+
 bool vector(const Tensor& t, at::ScalarType dtype, int64_t n) {
     return t.ok && t.dtype == dtype && t.ndim == 1 && t.dim[0] == n;
 }
@@ -93,6 +135,171 @@ PyObject* general() {
 
 int element(at::ScalarType dtype) {
     return dtype == at::kBFloat16 ? HS_BF16 : dtype == at::kHalf ? HS_FP16 : dtype == at::kFloat8_e4m3fn ? HS_E4M3 : -1;
+}
+
+bool look_cache(PyObject* k, PyObject* v, int64_t device, Cache* c) {
+    c->k = look(k, device);
+    c->v = look(v, device);
+    c->element = c->k.ok ? element(c->k.dtype) : -1;
+    if (c->element < 0 || c->k.ndim != 4 || !c->v.ok || c->v.dtype != c->k.dtype ||
+        !same_shape(c->k, c->v))
+        return false;
+    const int64_t* n = c->k.dim;
+    for (int i = 0; i < 4; ++i)
+        if (n[i] > INT32_MAX) return false;
+    c->page_stride = n[0] > 1 ? n[1] * n[2] * n[3] : 0;
+    c->row_stride = n[1] > 1 ? n[2] * n[3] : 0;
+    c->head_stride = n[2] > 1 ? n[3] : 0;
+    return true;
+}
+
+bool look_status(PyObject* o, int64_t device, int32_t** out) {
+    *out = nullptr;
+    if (o == Py_None) return true;
+    const Tensor s = look(o, device);
+    if (!s.ok || s.dtype != at::kInt || s.bytes < 4) return false;
+    *out = static_cast<int32_t*>(s.ptr);
+    return true;
+}
+
+// An optional fp32 vector of n entries.
+bool look_scale(PyObject* o, int64_t device, int64_t n, const float** out) {
+    *out = nullptr;
+    if (o == Py_None) return true;
+    const Tensor s = look(o, device);
+    if (!vector(s, at::kFloat, n)) return false;
+    *out = static_cast<const float*>(s.ptr);
+    return true;
+}
+
+template <typename T>
+T* as(const Tensor& t) {
+    return static_cast<T*>(t.ptr);
+}
+
+// paged_extend(device, stream, new_lens, seq_lens, block_table, free_ring,
+// ring_pos, page_size, max_tokens, lens_out, attend_lens, ring_out, cu_new, slot,
+// row_req, positions, status): the arguments of hs.paged_extend; lens_out and
+// ring_out may be None.
+PyObject* paged_extend(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    int64_t device, stream;
+    int32_t page_size, max_tokens;
+    int32_t* status;
+    if (n != 17 || !as_int(a[0], &device) || device < 0 || !as_int(a[1], &stream) ||
+        !as_i32(a[7], &page_size) || !as_i32(a[8], &max_tokens) || max_tokens < 0)
+        return general();
+    const Tensor fresh = look(a[2], device), lens = look(a[3], device);
+    const Tensor table = look(a[4], device), ring = look(a[5], device), pos = look(a[6], device);
+    if (!fresh.ok || fresh.ndim != 1 || fresh.dtype != at::kInt || fresh.dim[0] > INT32_MAX)
+        return general();
+    const int64_t rows = fresh.dim[0];
+    if (!vector(lens, at::kInt, rows) || !matrix(table, at::kInt, rows, 0) ||
+        table.dim[1] > INT32_MAX || !ring.ok || ring.ndim != 1 || ring.dtype != at::kInt ||
+        ring.dim[0] > INT32_MAX || !vector(pos, at::kLong, 2))
+        return general();
+    const Tensor lens_out = a[9] == Py_None ? lens : look(a[9], device);
+    const Tensor attend = look(a[10], device);
+    const Tensor ring_out = a[11] == Py_None ? pos : look(a[11], device);
+    const Tensor cu = look(a[12], device), slot = look(a[13], device);
+    const Tensor row = look(a[14], device), at = look(a[15], device);
+    if (!vector(lens_out, at::kInt, rows) || !vector(attend, at::kInt, rows) ||
+        !vector(ring_out, at::kLong, 2) || !vector(cu, at::kInt, rows + 1) ||
+        !vector(slot, at::kInt, max_tokens) || !vector(row, at::kInt, max_tokens) ||
+        !vector(at, at::kInt, max_tokens) || !look_status(a[16], device, &status))
+        return general();
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = hs_paged_extend(as<const int32_t>(fresh), as<const int32_t>(lens), as<int32_t>(table),
+                         table.dim[1], int32_t(rows), int32_t(table.dim[1]), as<int32_t>(ring),
+                         int32_t(ring.dim[0]), as<const int64_t>(pos), page_size, max_tokens,
+                         as<int32_t>(lens_out), as<int32_t>(attend), as<int64_t>(ring_out),
+                         as<int32_t>(cu), as<int32_t>(slot), as<int32_t>(row), as<int32_t>(at),
+                         status, reinterpret_cast<hs_stream_t>(stream));
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+// rope_append(device, stream, q, k, v, positions, slot, turns, k_cache, v_cache,
+// interleaved, mscale, k_scale, v_scale, q_out, status): the arguments of
+// hs.rope_append with everything given but the scales and status.
+PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    int64_t device, stream;
+    float mscale;
+    const float *ks, *vs;
+    int32_t* status;
+    Cache c;
+    if (n != 16 || !as_int(a[0], &device) || device < 0 || !as_int(a[1], &stream) ||
+        !PyBool_Check(a[10]) || !as_float(a[11], &mscale))
+        return general();
+    const Rows q = look_rows(a[2], device), k = look_rows(a[3], device), v = look_rows(a[4], device);
+    const Rows out = look_rows(a[14], device);
+    const Tensor pos = look(a[5], device), slot = look(a[6], device), turns = look(a[7], device);
+    if (!q.ok || !k.ok || !v.ok || !out.ok || k.dtype != q.dtype || v.dtype != q.dtype ||
+        out.dtype != q.dtype || k.n != q.n || v.n != q.n || out.n != q.n || k.d != q.d ||
+        v.d != q.d || out.d != q.d || v.heads != k.heads || out.heads != q.heads ||
+        !vector(pos, at::kInt, q.n) || !vector(slot, at::kInt, q.n) || !turns.ok ||
+        turns.ndim != 1 || turns.dtype != at::kLong || turns.dim[0] > INT32_MAX / 2 ||
+        !look_cache(a[8], a[9], device, &c) || c.k.dim[2] != k.heads || c.k.dim[3] != q.d ||
+        !look_scale(a[12], device, k.heads, &ks) || !look_scale(a[13], device, k.heads, &vs) ||
+        !look_status(a[15], device, &status))
+        return general();
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = hs_rope_append(q.ptr, q.stride, k.ptr, k.stride, v.ptr, v.stride, element(q.dtype),
+                        int32_t(q.n), int32_t(q.heads), int32_t(k.heads), int32_t(q.d),
+                        as<const int32_t>(pos), as<const int32_t>(slot), as<const int64_t>(turns),
+                        int32_t(2 * turns.dim[0]), a[10] == Py_True, mscale, out.ptr, out.stride,
+                        c.k.ptr, c.v.ptr, c.element, c.page_stride, c.row_stride, c.head_stride,
+                        int32_t(c.k.dim[0]), int32_t(c.k.dim[1]), ks, vs, status,
+                        reinterpret_cast<hs_stream_t>(stream));
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+// paged_prefill(device, stream, q, k_cache, v_cache, block_table, cu_new,
+// seq_lens, scale, window, num_sinks, max_len, k_scale, v_scale, out, lse,
+// workspace, status)
+PyObject* paged_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    int64_t device, stream;
+    int32_t window, sinks;
+    float scale;
+    const float *ks, *vs;
+    int32_t* status;
+    Cache c;
+    if (n != 18 || !as_int(a[0], &device) || device < 0 || !as_int(a[1], &stream) ||
+        !as_float(a[8], &scale) || !as_i32(a[9], &window) || !as_i32(a[10], &sinks) ||
+        a[14] == Py_None || a[15] == Py_None || a[16] == Py_None)
+        return general();
+    const Rows q = look_rows(a[2], device);
+    const Tensor table = look(a[5], device), cu = look(a[6], device), lens = look(a[7], device);
+    const Tensor out = look(a[14], device), lse = look(a[15], device), ws = look(a[16], device);
+    if (!q.ok || !look_cache(a[3], a[4], device, &c) || c.k.dim[3] != q.d || !lens.ok ||
+        lens.ndim != 1 || lens.dtype != at::kInt || lens.dim[0] > INT32_MAX)
+        return general();
+    const int64_t rows = lens.dim[0];
+    if (!matrix(table, at::kInt, rows, 0) || table.dim[1] > INT32_MAX ||
+        !vector(cu, at::kInt, rows + 1) || !out.ok || out.dtype != q.dtype || out.ndim != 3 ||
+        out.dim[0] != q.n || out.dim[1] != q.heads || out.dim[2] != q.d ||
+        !matrix(lse, at::kFloat, q.n, q.heads) || lse.dim[1] != q.heads || !ws.ok ||
+        !look_scale(a[12], device, c.k.dim[2], &ks) || !look_scale(a[13], device, c.k.dim[2], &vs) ||
+        !look_status(a[17], device, &status))
+        return general();
+    int64_t max_len = table.dim[1] * c.k.dim[1];
+    if (a[11] != Py_None && !as_int(a[11], &max_len)) return general();
+    if (max_len < 0 || max_len > INT32_MAX) return general();
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = hs_paged_prefill(q.ptr, q.stride, element(q.dtype), int32_t(q.n), c.k.ptr, c.v.ptr,
+                          c.element, c.page_stride, c.row_stride, c.head_stride,
+                          int32_t(c.k.dim[0]), int32_t(c.k.dim[1]), as<const int32_t>(table),
+                          table.dim[1], int32_t(table.dim[1]), int32_t(max_len),
+                          as<const int32_t>(cu), as<const int32_t>(lens), ks, vs, int32_t(rows),
+                          int32_t(q.heads), int32_t(c.k.dim[2]), int32_t(q.d), window, sinks, scale,
+                          out.ptr, as<float>(lse), ws.ptr, ws.bytes, status,
+                          reinterpret_cast<hs_stream_t>(stream));
+    Py_END_ALLOW_THREADS
+    if (rc == HS_ERR_CAPACITY) return general();  // a larger workspace is wanted
+    return PyLong_FromLong(rc);
 }
 
 // paged_decode(device, stream, q, k_cache, v_cache, block_table, seq_lens,
@@ -257,6 +464,9 @@ PyCFunction fast(F f) {
 
 PyMethodDef methods[] = {{"paged_decode", fast(paged_decode), METH_FASTCALL, nullptr},
                          {"evict", fast(evict), METH_FASTCALL, nullptr},
+                         {"paged_extend", fast(paged_extend), METH_FASTCALL, nullptr},
+                         {"rope_append", fast(rope_append), METH_FASTCALL, nullptr},
+                         {"paged_prefill", fast(paged_prefill), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_hs_binding", nullptr, -1, methods,
                       nullptr,               nullptr,       nullptr, nullptr};

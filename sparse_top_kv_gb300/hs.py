@@ -976,6 +976,16 @@ def paged_extend(new_lens, seq_lens, block_table, free_ring, ring_pos, page_size
     the step's tokens.  lens_out and ring_out default to the inputs (updated in
     place).  Returns (lens_out, attend_lens, cu_new int32 [rows + 1], slot,
     row_req, positions int32 [max_tokens])."""
+    if _binding is not None:
+        dev = torch._C._cuda_getDevice()
+        rc = _binding.paged_extend(dev, _raw_stream(dev, stream), new_lens, seq_lens, block_table,
+                                   free_ring, ring_pos, page_size, max_tokens, lens_out,
+                                   attend_lens, ring_out, cu_new, slot, row_req, positions, status)
+        if rc is not None:
+            if rc != HS_OK:
+                raise HSError("hs_paged_extend", rc)
+            return (seq_lens if lens_out is None else lens_out, attend_lens, cu_new, slot, row_req,
+                    positions)
     if not isinstance(max_tokens, int):
         raise TypeError("max_tokens: an int")
     _check_i32(page_size=page_size, max_tokens=max_tokens)
@@ -1072,6 +1082,15 @@ def rope_append(q, k, v, positions, slot, turns, k_cache, v_cache, *, interleave
     (undefined in a new tensor).  q None: only the cache is written; k, v, slot
     and the caches None: only q.
     Returns q_out."""
+    if _binding is not None:
+        dev = torch._C._cuda_getDevice()
+        rc = _binding.rope_append(dev, _raw_stream(dev, stream), q, k, v, positions, slot, turns,
+                                  k_cache, v_cache, interleaved, mscale, k_scale, v_scale, q_out,
+                                  status)
+        if rc is not None:
+            if rc != HS_OK:
+                raise HSError("hs_rope_append", rc)
+            return q_out
     dev = _current_device(positions, "positions")
     if q is None and k is None:
         raise ValueError("q, k: at least one")
@@ -1148,6 +1167,15 @@ def paged_prefill(q, k_cache, v_cache, block_table, cu_new, seq_lens, scale, *, 
     status as for paged_decode.  Returns (out [tokens, heads, d] of q's type, lse
     fp32 [tokens, heads]); rows of q of no request are left as they are (zeros in
     tensors made here)."""
+    if _binding is not None:
+        dev = torch._C._cuda_getDevice()
+        rc = _binding.paged_prefill(dev, _raw_stream(dev, stream), q, k_cache, v_cache,
+                                    block_table, cu_new, seq_lens, scale, window, num_sinks,
+                                    max_len, k_scale, v_scale, out, lse, workspace, status)
+        if rc is not None:
+            if rc != HS_OK:
+                raise HSError("hs_paged_prefill", rc)
+            return out, lse
     dev = _current_device(q, "q")
     q_ptr, q_stride = _token_rows(q, "q", dev)
     if k_cache.dtype not in _ELEMENT:
