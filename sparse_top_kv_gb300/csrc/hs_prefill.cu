@@ -9,6 +9,8 @@
 
 namespace hs_paged {
 namespace tc {
+using Encode = decltype(&cuTensorMapEncodeTiled);
+Encode encoder();
 int encode_map(CUtensorMap* m, int kv, const void* base, const PagedArgs& a, int d, int bt,
                int hs_box);
 }  // namespace tc
@@ -32,6 +34,21 @@ int encode_map(CUtensorMap* m, const void* base, const PrefillArgs& a, int kv_dt
     p.kv_heads = a.kv_heads;
     return hs_paged::tc::encode_map(m, kv_dtype, base, p, d, bt, 1);
 }
+int encode_q_map(CUtensorMap* m, const PrefillArgs& a, int dtype, int d) {
+    const hs_paged::tc::Encode f = hs_paged::tc::encoder();
+    if (f == nullptr) return HS_ERR_CUDA;
+    const cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(a.heads), cuuint64_t(a.tokens)};
+    const cuuint64_t strides[2] = {
+        cuuint64_t(d) * 2,
+        a.tokens > 1 ? cuuint64_t(a.q_stride) * 2 : cuuint64_t(a.heads) * d * 2};
+    const cuuint32_t box[3] = {64u, cuuint32_t(a.group), cuuint32_t(a.tq)};
+    const cuuint32_t one[3] = {1u, 1u, 1u};
+    const CUresult r = f(m, dtype == HS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                         3, const_cast<void*>(a.q), dims, strides, box, one,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? HS_OK : HS_ERR_CUDA;
+}
 }  // namespace tc
 
 namespace {
@@ -43,76 +60,115 @@ int box_tokens(const PrefillArgs& a, int kv_dtype) {
     if (kv_dtype == HS_E4M3 || a.page_size % 16 != 0 || a.num_pages <= 0 ||
         (a.kv_heads > 1 && (a.head_stride <= 0 || a.head_stride >= most)) ||
         (a.num_pages > 1 && (a.page_stride <= 0 || a.page_stride >= most)) || a.row_stride <= 0 ||
-        a.row_stride >= most)
+        a.row_stride >= most || (a.tokens > 1 && (a.q_stride <= 0 || a.q_stride >= most)))
         return 0;
     int bt = kTile;
     while (a.page_size % bt) bt /= 2;
     return bt;
 }
 
-constexpr int kMergeThreads = 256;
-constexpr int kMergeSlices = 8;
+constexpr int kMergeThreads = 128;
+constexpr int kMergeDims = 16;  // dims of a block
 
 // Joins the parts of a shared unit: out = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p -
-// M) l_p.  Block (c, y): some rows of the unit whose first part CTA c had; a
-// warp per row.
+// M) l_p.  Block (c, y): 16 dims of 128 rows of the unit whose first part CTA c
+// had; a thread per row, as the partial states lie.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_constant__ PrefillArgs a,
                                                               int out_bf16) {
-    constexpr int V = D / 32;  // elements of a lane
+    constexpr int kParts = D / kMergeDims;
+    __shared__ int slots[kMaxCtas];
+    __shared__ int count;
     hs::pdl_wait();
     hs::pdl_trigger();
-    const int c = blockIdx.x, lane = threadIdx.x & 31;
+    const int c = blockIdx.x;
     const SharedUnit u = a.shared[c];
     if (!u.valid) return;
-    for (int j = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5); j < a.unit_rows;
-         j += kMergeSlices * (kMergeThreads / 32)) {
-        const int w = j / kTile, r = j % kTile, tok = r / a.group, hd = r - tok * a.group;
-        if (tok >= a.tq || w * a.tq + tok >= u.tokens) continue;
-        float M = -CUDART_INF_F, L = 0.f, o[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = 0.f;
-        int64_t at = run_begin(u.total, a.ctas, c) - u.start;
-        int64_t slot = 2 * c + (at > 0 ? 0 : 1);
-        int i0 = tile_at(at, u.cost, u.tiles);
-        for (int p = c; i0 < u.tiles && p < a.ctas; ++p, slot = 2 * p) {
-            at = run_begin(u.total, a.ctas, p + 1) - u.start;
-            const int i1 = tile_at(at, u.cost, u.tiles);
-            if (i1 > i0) {
-                const int64_t k = slot * a.unit_rows + j;
-                const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + k);
-                float x[V];
-#pragma unroll
-                for (int i = 0; i < V; i += 2) {
-                    const float2 y = __ldcg(reinterpret_cast<const float2*>(a.part_o + k * D) +
-                                            i / 2 * 32 + lane);
-                    x[i] = y.x;
-                    x[i + 1] = y.y;
-                }
-                const float m = fmaxf(M, ml.x), ref = m == -CUDART_INF_F ? 0.f : m;
-                const float keep = exp2f(M - ref), f = exp2f(ml.x - ref);
-                M = m;
-                L = fmaf(L, keep, f * ml.y);
-#pragma unroll
-                for (int i = 0; i < V; ++i) o[i] = fmaf(o[i], keep, f * x[i]);
+    // The slots of the unit's parts, in order; CTAs without a tile have none.
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int n = 0;
+        for (int c0 = c;; c0 += 32) {
+            const int p = c0 + lane;
+            int slot = -1, i1 = 0;
+            if (p < a.ctas) {
+                const int64_t at = run_begin(u.per, u.rest, a.ctas, p) - u.start;
+                const int i0 = tile_at(at, u.cost, u.tiles);
+                i1 = tile_at(run_begin(u.per, u.rest, a.ctas, p + 1) - u.start, u.cost, u.tiles);
+                if (i1 > i0) slot = 2 * p + (at > 0 ? 0 : 1);
             }
-            i0 = i1;
+            const uint32_t has = __ballot_sync(0xffffffffu, slot >= 0);
+            if (slot >= 0) slots[n + __popc(has & ((1u << lane) - 1u))] = slot;
+            n += __popc(has);
+            if (__any_sync(0xffffffffu, i1 == u.tiles || p + 1 >= a.ctas)) break;
         }
-        float f = L == 0.f ? 0.f : 1.f / L;
-        if (a.v_scale != nullptr && L != 0.f) f *= a.v_scale[u.kvh];
-        const int64_t qh = int64_t(u.first + w * a.tq + tok) * a.heads + u.kvh * a.group + hd;
-#pragma unroll
-        for (int i = 0; i < V; i += 2) {
-            const float x = L == 0.f ? 0.f : o[i] * f, y = L == 0.f ? 0.f : o[i + 1] * f;
-            const int64_t e = qh * (D / 2) + i / 2 * 32 + lane;
-            if (out_bf16)
-                static_cast<__nv_bfloat162*>(a.out)[e] = __floats2bfloat162_rn(x, y);
-            else
-                static_cast<__half2*>(a.out)[e] = __floats2half2_rn(x, y);
-        }
-        if (lane == 0 && a.lse != nullptr)
-            a.lse[qh] = L == 0.f ? -CUDART_INF_F : (M + log2f(L)) * kLn2;
+        if (lane == 0) count = n;
     }
+    __syncthreads();
+    const int n = count, w = blockIdx.y / kParts, part = blockIdx.y % kParts, r = threadIdx.x;
+    const int tok = r / a.group, hd = r - tok * a.group;
+    if (tok >= a.tq || w * a.tq + tok >= u.tokens) return;
+    const int j = w * kTile + r;
+    float M = -CUDART_INF_F, L = 0.f;
+    float o[kMergeDims];
+#pragma unroll
+    for (int i = 0; i < kMergeDims; ++i) o[i] = 0.f;
+    const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + j;
+    const float4* po = reinterpret_cast<const float4*>(a.part_o) +
+                       int64_t(part * (kMergeDims / 4)) * a.unit_rows + j;
+    constexpr int kAhead = 4;  // parts in flight
+    for (int p0 = 0; p0 < n; p0 += kAhead) {
+        float2 s[kAhead];
+        float4 x[kAhead][kMergeDims / 4];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            s[k] = make_float2(-CUDART_INF_F, 0.f);
+            if (p0 + k >= n) continue;
+            const int64_t slot = slots[p0 + k];
+            s[k] = __ldcg(ml + slot * a.unit_rows);
+#pragma unroll
+            for (int i = 0; i < kMergeDims / 4; ++i)
+                x[k][i] = __ldcg(po + (slot * (D / 4) + i) * a.unit_rows);
+        }
+        float m = M;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) m = fmaxf(m, s[k].x);
+        const float ref = m == -CUDART_INF_F ? 0.f : m, keep = exp2f(M - ref);
+        M = m;
+        L *= keep;
+#pragma unroll
+        for (int i = 0; i < kMergeDims; ++i) o[i] *= keep;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (p0 + k >= n) break;
+            const float f = exp2f(s[k].x - ref);
+            L = fmaf(f, s[k].y, L);
+#pragma unroll
+            for (int i = 0; i < kMergeDims / 4; ++i) {
+                o[4 * i] = fmaf(f, x[k][i].x, o[4 * i]);
+                o[4 * i + 1] = fmaf(f, x[k][i].y, o[4 * i + 1]);
+                o[4 * i + 2] = fmaf(f, x[k][i].z, o[4 * i + 2]);
+                o[4 * i + 3] = fmaf(f, x[k][i].w, o[4 * i + 3]);
+            }
+        }
+    }
+    float f = L == 0.f ? 0.f : 1.f / L;
+    if (a.v_scale != nullptr && L != 0.f) f *= a.v_scale[u.kvh];
+    const int64_t qh = int64_t(u.first + w * a.tq + tok) * a.heads + u.kvh * a.group + hd;
+    uint32_t y[kMergeDims / 2];
+#pragma unroll
+    for (int i = 0; i < kMergeDims / 2; ++i) {
+        const float p = L == 0.f ? 0.f : o[2 * i] * f, q = L == 0.f ? 0.f : o[2 * i + 1] * f;
+        const __nv_bfloat162 yb = __floats2bfloat162_rn(p, q);
+        const __half2 yh = __floats2half2_rn(p, q);
+        y[i] = out_bf16 ? *reinterpret_cast<const uint32_t*>(&yb)
+                        : *reinterpret_cast<const uint32_t*>(&yh);
+    }
+    uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + qh * D + part * kMergeDims);
+    out[0] = make_uint4(y[0], y[1], y[2], y[3]);
+    out[1] = make_uint4(y[4], y[5], y[6], y[7]);
+    if (part == 0 && a.lse != nullptr)
+        a.lse[qh] = L == 0.f ? -CUDART_INF_F : (M + log2f(L)) * kLn2;
 }
 
 struct Layout {
@@ -248,7 +304,7 @@ extern "C" int hs_paged_prefill(const void* q, int64_t q_stride, int32_t q_dtype
                    : kv_dtype == HS_FP16 ? launch_fp16(a, d, bt, stream)
                                          : launch_e4m3(a, d, bt, stream);
     if (rc != HS_OK) return rc;
-    const dim3 grid{unsigned(a.ctas), kMergeSlices}, block{kMergeThreads};
+    const dim3 grid{unsigned(a.ctas), unsigned(w.unit_rows / kTile * (d / kMergeDims))}, block{kMergeThreads};
     const int bf = q_dtype == HS_BF16;
     if (d == 64) return hs_host::launch_pdl(merge_kernel<64>, grid, block, 0, stream, a, bf);
     if (d == 128) return hs_host::launch_pdl(merge_kernel<128>, grid, block, 0, stream, a, bf);

@@ -20,10 +20,11 @@ constexpr int kExtra = 256;
 
 // A unit whose tokens several CTAs share, written by the CTA of its first part.
 struct SharedUnit {
-    int64_t start, total;  // its first place, and the places of the call
-    int32_t cost, tiles;   // its places and tiles
-    int32_t first, tokens; // its new tokens
-    int32_t kvh, valid;    // 0: this CTA has no first part
+    int64_t start, per;     // its first place, and the places of a run
+    int32_t rest;           // (places left over)
+    int32_t cost, tiles;    // its places and tiles
+    int32_t first, tokens;  // its new tokens
+    int32_t kvh, valid;     // 0: this CTA has no first part
 };
 
 struct PrefillArgs {
@@ -49,7 +50,7 @@ struct PrefillArgs {
     // Workspace: two partial states per CTA (of the units that its run begins
     // and ends in) and the shared units.
     float* part_ml;      // [2 * ctas][unit rows][2]
-    float* part_o;       // [2 * ctas][unit rows][D]
+    float* part_o;       // [2 * ctas][D / 4][unit rows][4]
     SharedUnit* shared;  // [ctas]
     int32_t unit_rows;   // 128 or 256
     int32_t* status;
@@ -90,7 +91,7 @@ __device__ __forceinline__ int64_t places(const PrefillArgs& a, const Request& x
     int64_t sum = n * (kExtra + base) + tb * (n * (n + 1) / 2);
     if (a.window > 0) {
         const int64_t c0 = base + 1 - a.window;
-        const int64_t i0 = c0 > 0 ? 0 : -c0 / tb + 1;  // the first block that starts behind 0
+        const int64_t i0 = c0 > 0 ? 0 : int(-c0) / a.tb + 1;  // the first block that starts behind 0
         if (n > i0) sum -= (n - i0) * c0 + tb * (n * (n - 1) / 2 - i0 * (i0 - 1) / 2);
     }
     return sum;
@@ -98,8 +99,14 @@ __device__ __forceinline__ int64_t places(const PrefillArgs& a, const Request& x
 __device__ __forceinline__ int64_t places_of(const PrefillArgs& a, const Request& x) {
     return x.n > 0 ? places(a, x, blocks_of(a, x.n)) * a.kv_heads : 0;
 }
-__device__ __forceinline__ int64_t run_begin(int64_t total, int ctas, int c) {
-    const int64_t per = total / ctas, rest = total - per * ctas;
+// Places of one block.
+__device__ __forceinline__ int cost_of(const PrefillArgs& a, const Request& x, int b) {
+    const int base = max(x.T - x.n, 0);
+    const int lo = a.window > 0 ? max(0, base + b * a.tb + 1 - a.window) : 0;
+    return kExtra + base + (b + 1) * a.tb - lo;
+}
+// First place of CTA c's run: floor(total c / ctas).
+__device__ __forceinline__ int64_t run_begin(int64_t per, int rest, int ctas, int c) {
     return per * c + rest * c / ctas;
 }
 // The tile that place `at` of a unit stands for.

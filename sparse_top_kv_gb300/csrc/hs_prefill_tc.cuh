@@ -47,8 +47,9 @@ namespace tc {
 enum Kind { kBf16 = 0, kFp16 = 1, kE4m3 = 2 };
 
 constexpr int kThreads = 512;
-constexpr int kMmaWarp = 8;    // 9 to 11: queries
-constexpr int kQWarps = 3;
+constexpr int kQkWarp = 8, kPvWarp = 9;
+constexpr int kQWarp = 10;     // and 11: queries
+constexpr int kQWarps = 2;
 constexpr int kLoadWarp = 12;  // TMA: 13 to 15 check V; else all four load
 constexpr int kCheckWarps = 3;
 constexpr int kLoadBar = 1;    // named barrier of the loading threads
@@ -76,21 +77,28 @@ struct Cfg {
     static constexpr int kQOff = 0;
     static constexpr int kRingOff = NQ * kQTile;
     static constexpr int kBarOff = kRingOff + NS * kUnit;
-    static constexpr uint32_t kOCol = 256;                 // TMEM: S (and P), then O
-    static constexpr uint32_t kOCols = D == 64 ? 64 : 128; // columns of an O tile (D = 256: two)
+    // TMEM columns.  Two query tiles: one S for both, a P of each, an O of each.
+    // One: two S buffers, whose first half P takes, and O.
+    static constexpr uint32_t kPCol = 128, kOCol = 256;
+    // Registers of a thread, by warpgroup: 2 * soft + products + loads = 512.
+    static constexpr int kSoftRegs = TMA ? 184 : 168, kMmaRegs = 72, kLoadRegs = TMA ? 72 : 104;
+    static_assert(2 * kSoftRegs + kMmaRegs + kLoadRegs == 65536 / 128, "register shares");
     static constexpr float kThresh = KV == kBf16 ? 8.f : 4.f;
     static constexpr float kShift = KV == kBf16 ? 0.f : 11.f;
 };
 
 struct Bars {
-    uint64_t full[10], ready[10], empty[10];
-    uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], o_free[2], pv_done, drain;
-    int64_t place0, place1, total, start;  // the run, and where its first unit starts
-    int32_t row, kvh, block;               // its first unit
+    uint64_t kfull[10], vfull[10], ready[10], empty[10];
+    uint64_t q_full, q_empty, s_full[2], s_free, p_full[2], pv_done[2], o_free[2], drain[2];
+    int64_t place0, place1, start;  // the run, and where its first unit starts
+    int64_t per;                    // the call's places: per * ctas + rest
+    int32_t rest;
+    int32_t row, kvh, block;        // the run's first unit
     uint32_t tmem_base;
     volatile int32_t abort;
     volatile int32_t keep[2];              // O holds something before the first product
     alignas(16) uint32_t loaded[kRing][4]; // tokens of a tile that were loaded
+    int2 tile[kRing];                      // its first token; whether some query does not see all of it
     alignas(16) uint32_t odd[kRing][2][4]; // rows of V that were taken out, by ring unit
 };
 struct BarsLdg : Bars {
@@ -136,7 +144,7 @@ __device__ __forceinline__ void shape(const PrefillArgs& a, Seg& s, int64_t plac
     const int sc = a.window > 0 ? min(a.sinks, lo) : 0;
     s.ns = min((sc + kTile - 1) / kTile, s.tw);
     s.nt = s.ns + (hi + kTile - 1) / kTile - s.tw;
-    s.cost = int(places(a, s.x, s.block + 1) - places(a, s.x, s.block));
+    s.cost = cost_of(a, s.x, s.block);
     s.i0 = tile_at(place0 - s.start, s.cost, s.nt);
     s.i1 = tile_at(place1 - s.start, s.cost, s.nt);
     s.begins = place0 <= s.start;
@@ -219,8 +227,10 @@ __device__ __forceinline__ void make_plan(const PrefillArgs& a, Bars& B, int64_t
         at = scan(own, &all);
         total += all;
     }
-    const int64_t p0 = run_begin(total, a.ctas, blockIdx.x);
-    const int64_t p1 = run_begin(total, a.ctas, blockIdx.x + 1);
+    const int64_t per = total / a.ctas;
+    const int rest = int(total - per * a.ctas);
+    const int64_t p0 = run_begin(per, rest, a.ctas, blockIdx.x);
+    const int64_t p1 = run_begin(per, rest, a.ctas, blockIdx.x + 1);
     int64_t base = 0;
     for (int r0 = 0; r0 < a.rows; r0 += kThreads) {
         if (a.rows > kThreads) {
@@ -252,7 +262,8 @@ __device__ __forceinline__ void make_plan(const PrefillArgs& a, Bars& B, int64_t
     if (tid == 0) {
         B.place0 = p0;
         B.place1 = p1;
-        B.total = total;
+        B.per = per;
+        B.rest = rest;
     }
     __syncthreads();
 }
@@ -265,14 +276,55 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
         "l"(map), "r"(x), "r"(tok), "r"(head), "r"(page), "r"(hs::smem_u32(bar))
         : "memory");
 }
-// D(tmem) (+)= A(tmem) B(smem desc), 16-bit in, f32 accumulate.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t acc) {
+__device__ __forceinline__ void tma_load_q(uint32_t dst, const CUtensorMap* map, int x, int head,
+                                           int token, uint64_t* bar) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(head), "r"(token), "r"(hs::smem_u32(bar))
+        : "memory");
+}
+// Products and commits are issued by the whole warp, converged, for one elected
+// lane, four products to a statement: with a lane of its own in a branch, the
+// operands' way to uniform registers made each product 110 cycles' work, twice
+// what the tensor cores take for it.
+// D(tmem) (+)= A(smem desc) B(smem desc), four K steps of 16 (32 bytes apart).
+__device__ __forceinline__ void mma_ss4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, t, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.u32 t, 0, 0;\n\t"
+        "add.u64 a1, %1, 2;\n\tadd.u64 a2, %1, 4;\n\tadd.u64 a3, %1, 6;\n\t"
+        "add.u64 b1, %2, 2;\n\tadd.u64 b2, %2, 4;\n\tadd.u64 b3, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// D(tmem) (+)= A(tmem) B(smem desc, 16 rows of 128 bytes a K step), four steps.
+__device__ __forceinline__ void mma_ts4(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, t, e;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.u32 t, 0, 0;\n\t"
+        "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
+        "add.u64 b1, %2, 128;\n\tadd.u64 b2, %2, 256;\n\tadd.u64 b3, %2, 384;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            hs::smem_u32(bar))
         : "memory");
 }
 // kind::f16, fp32 accumulators, A K-major (or in TMEM), M = 128.
@@ -329,6 +381,32 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Pairs of fp32.
+__device__ __forceinline__ uint64_t pair_of(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 split(uint64_t p) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 template <int KV>
 __device__ __forceinline__ uint32_t pack(float x, float y) {
     if constexpr (KV == kBf16) {
@@ -375,7 +453,8 @@ __device__ __forceinline__ float element(const void* row, int i) {
 
 template <int KV, int D, bool TMA>
 __global__ void __launch_bounds__(kThreads, 1)
-prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUtensorMap kmap,
+prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUtensorMap qmap,
+                  const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap) {
     using C = Cfg<KV, D, TMA>;
     constexpr int NQ = C::NQ, NS = C::NS, kSubs = C::kSubs;
@@ -393,26 +472,28 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
 
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
-            hs::mbar_init(&B.full[i], TMA ? 1 : kTile);
+            hs::mbar_init(&B.kfull[i], TMA ? 1 : kTile);
+            hs::mbar_init(&B.vfull[i], 1);
             hs::mbar_init(&B.ready[i], TMA ? kCheckWarps : kTile);
             hs::mbar_init(&B.empty[i], 1);
         }
-        hs::mbar_init(&B.q_full, kQWarps * 32);
+        hs::mbar_init(&B.q_full, TMA ? 1 : kQWarps * 32);
         hs::mbar_init(&B.q_empty, 1);
+        hs::mbar_init(&B.s_free, kTile);
         for (int i = 0; i < 2; ++i) {
             hs::mbar_init(&B.s_full[i], 1);
             hs::mbar_init(&B.p_full[i], kTile);
-            hs::mbar_init(&B.o_full[i], 1);
+            hs::mbar_init(&B.pv_done[i], 1);
             hs::mbar_init(&B.o_free[i], kTile);
+            hs::mbar_init(&B.drain[i], 1);
         }
-        hs::mbar_init(&B.pv_done, 1);
-        hs::mbar_init(&B.drain, 1);
         B.abort = 0;
         hs::fence_mbar_init();
     }
-    if (TMA && warp == kLoadWarp && lane < 2)
-        asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &kmap : &vmap) : "memory");
-    if (warp == kMmaWarp) {
+    if (TMA && warp == kLoadWarp && lane < 3)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &kmap : lane == 1 ? &vmap : &qmap)
+                     : "memory");
+    if (warp == kQkWarp) {
         hs::tc::tmem_alloc(&B.tmem_base, kTmemCols);
         hs::tc::tmem_relinquish();
     }
@@ -438,14 +519,15 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
     };
     // Ring unit s of the CTA's tile t: first those of K, then those of V.
     const auto unit_of = [](int t, bool v, int s) { return (2 * t + (v ? 1 : 0)) * kSubs + s; };
-    // Barriers that complete once per unit of V (`ready`), or of K (`full`, where
-    // threads load), count those alone.
+    // The barriers of K's units and of V's count those alone: loads may land in
+    // another order than they were issued in, and a parity tells only neighbouring
+    // phases apart, so who waits has to have seen the phase before.
     const auto turn_of = [](int t, int s) { return t * kSubs + s; };
     Seg s;
 
     if (warp < 8) {
         // ------------------------- softmax and output -------------------------
-        set_max_regs_up<192>();
+        set_max_regs_up<C::kSoftRegs>();
         const int w = warp >> 2;   // query tile (NQ = 1: only 0 works)
         const int r = tid & 127;   // row of the tile, and TMEM lane
         const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
@@ -453,8 +535,11 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
         const uint32_t o_addr = tmem + lanes + C::kOCol + uint32_t(NQ == 2 ? w * 128 : 0);
         const bool bf = KV == kBf16 || (E4 && !a.q_is_half);
         bool ok = w < NQ;
+        // The product of this tile's k-th P is done.
+        const auto pv_wait = [&](int k) {
+            return NQ == 2 ? wait(&B.pv_done[w], k) : wait(&B.pv_done[k & 1], k >> 1);
+        };
         int t = 0, mine = 0, units = 0;  // the CTA's tiles, this tile's, units with tiles
-        int segs = 0;                    // this query tile's units
         bool head = false;               // the run ends in the first part of a shared unit
         for (bool more = ok && first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
             const int n = s.i1 - s.i0;
@@ -475,7 +560,8 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
                 head = true;
                 SharedUnit u;
                 u.start = s.start;
-                u.total = B.total;
+                u.per = B.per;
+                u.rest = B.rest;
                 u.cost = s.cost;
                 u.tiles = s.nt;
                 u.first = s.x.first + s.block * a.tb;
@@ -492,18 +578,22 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
             // The row's position; rows without a query see what the last does.
             const int pos = s.p0 + min(w * a.tq + tok, s.m - 1);
             float scl = a.scale_log2;
-            float off = -CUDART_INF_F, l0 = 0.f, l1 = 0.f;  // reference - kShift, sums
-            for (int i = s.i0; i < s.i1; ++i, ++t, ++mine) {
+            float off = -CUDART_INF_F;      // reference - kShift
+            uint64_t l0 = 0, l1 = 0;        // sums, in pairs
+            bool first = true;
+            const int last = mine + n;
+            for (; mine < last; ++t, ++mine, first = false) {
                 const int x = NQ == 2 ? w : mine & 1;
                 const int ph = NQ == 2 ? mine : mine >> 1;
-                const uint32_t s_addr = tmem + lanes + uint32_t(x * 128);
+                const uint32_t s_addr = tmem + lanes + uint32_t(NQ == 2 ? 0 : x * 128);
+                const uint32_t p_addr = NQ == 2 ? tmem + lanes + C::kPCol + uint32_t(w * 64) : s_addr;
                 ok = __all_sync(0xffffffffu, wait(&B.s_full[x], ph));
                 if (!ok) break;
                 hs::tc::fence_after_sync();
                 float v[128];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, v + c * 32);
-                if (i == s.i0) {
+                if (first) {
                     // (0 would turn masked places into NaN; 2^-126 does not show.)
                     if constexpr (E4) {
                         scl *= B.qscale[useg & (kSegRing - 1)][w * kTile + r];
@@ -511,23 +601,27 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
                     }
                     if (scl == 0.f) scl = 1.17549435e-38f;
                 }
-                // What this row sees of the tile.
-                const int t0 = token_of(s, i);
-                const uint4 ld = *reinterpret_cast<const uint4*>(B.loaded[t & (kRing - 1)]);
-                const uint32_t lw[4] = {ld.x, ld.y, ld.z, ld.w};
-                const bool part = !all_see(a, s, t0) || (ld.x & ld.y & ld.z & ld.w) != 0xffffffffu;
+                const bool part = B.tile[t & (kRing - 1)].y != 0;
+                const float as = fabsf(scl);
                 uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
                 hs::tc::tmem_wait_ld();
+                if (NQ == 2) {
+                    hs::tc::fence_before_sync();
+                    hs::mbar_arrive(&B.s_free);
+                }
                 if (scl < 0.f) {
 #pragma unroll
                     for (int c = 0; c < 128; ++c) v[c] = -v[c];
                 }
-                const float as = fabsf(scl);
                 if (part) {
+                    // What this row sees of the tile.
+                    const uint4 ld = *reinterpret_cast<const uint4*>(B.loaded[t & (kRing - 1)]);
+                    const int t0 = B.tile[t & (kRing - 1)].x;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int b = t0 + 32 * j;
-                        vis[j] = low_bits(pos + 1 - b) & lw[j];
+                        const uint32_t lw = j == 0 ? ld.x : j == 1 ? ld.y : j == 2 ? ld.z : ld.w;
+                        vis[j] = low_bits(pos + 1 - b) & lw;
                         if (a.window > 0)
                             vis[j] &= ~low_bits(pos - a.window + 1 - b) | low_bits(a.sinks - b);
 #pragma unroll
@@ -535,27 +629,53 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
                             if (!((vis[j] >> c) & 1u)) v[32 * j + c] = -CUDART_INF_F;
                     }
                 }
-                float mx[4] = {v[0], v[1], v[2], v[3]};
+                uint64_t as2, ref2, s0 = 0, s1 = 0;
+                const auto refer = [&] {
+                    // Without a finite logit so far: subtract 0, every weight is
+                    // 0 (a NaN logit stays NaN).
+                    const float ref = off == -CUDART_INF_F ? 0.f : off;
+                    as2 = pair_of(as, as);
+                    ref2 = pair_of(-ref, -ref);
+                };
+                const auto weigh = [&](int c) {  // columns [32 c, 32 c + 32)
+                    uint32_t pk[16];
 #pragma unroll
-                for (int c = 4; c < 128; c += 4)
+                    for (int j = 0; j < 16; j += 2) {
+                        const int e = 32 * c + 2 * j;
+                        const float2 y = split(fma2(pair_of(v[e], v[e + 1]), as2, ref2));
+                        const float2 z = split(fma2(pair_of(v[e + 2], v[e + 3]), as2, ref2));
+                        const float2 p = make_float2(ex2(y.x), ex2(y.y)), q = make_float2(ex2(z.x), ex2(z.y));
+                        s0 = add2(s0, pair_of(p.x, p.y));
+                        s1 = add2(s1, pair_of(q.x, q.y));
+                        pk[j] = pack<KV>(p.x, p.y);
+                        pk[j + 1] = pack<KV>(q.x, q.y);
+                    }
+                    tmem_st16u(p_addr + c * 16, pk);
+                };
+                // The reference moves up to the maximum where that is far above;
+                // what has been summed is scaled down.
+                const auto raise = [&] {
+                    float mx[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], v[c + j]);
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * as;
-                // The reference moves up to the maximum where that is far above.
-                const bool grow = top - C::kShift > off + C::kThresh || (off == -CUDART_INF_F && top > off);
-                if (i == s.i0) {
-                    if (grow) off = top - C::kShift;
-                } else if (__any_sync(0xffffffffu, grow)) {
-                    const float to = grow ? top - C::kShift : off;
+                    for (int c = 4; c < 124; c += 8)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) mx[j] = max3(mx[j], v[c + 2 * j], v[c + 2 * j + 1]);
+                    mx[0] = max3(mx[0], v[124], v[125]);
+                    mx[1] = max3(mx[1], v[126], v[127]);
+                    const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * as - C::kShift;
+                    const bool grow = top > off + C::kThresh || (off == -CUDART_INF_F && top > off);
+                    if (first) {
+                        if (grow) off = top;
+                        return false;
+                    }
+                    if (!__any_sync(0xffffffffu, grow)) return false;
+                    const float to = grow ? top : off;
                     const float al = grow ? (off == -CUDART_INF_F ? 0.f : ex2(off - to)) : 1.f;
                     off = to;
-                    l0 *= al;
-                    l1 *= al;
-                    // The products into O so far are done (two tiles: S of this
-                    // one was issued behind them).
+                    l0 = fma2(l0, pair_of(al, al), 0);
+                    l1 = fma2(l1, pair_of(al, al), 0);
                     if (NQ == 1) {
-                        ok = __all_sync(0xffffffffu, wait(&B.pv_done, mine - 1));
-                        if (!ok) break;
+                        ok = __all_sync(0xffffffffu, pv_wait(mine - 1));
                         hs::tc::fence_after_sync();
                     }
 #pragma unroll 1
@@ -567,23 +687,31 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
                         for (int j = 0; j < 16; ++j) o[j] *= al;
                         hs::tc::tmem_st16(o_addr + uint32_t(c), o);
                     }
+                    return true;
+                };
+                // The products of the tile before have read P and are in O.
+                if (NQ == 2 && mine > 0) {
+                    ok = __all_sync(0xffffffffu, pv_wait(mine - 1));
+                    hs::tc::fence_after_sync();
                 }
-                // Without a finite logit so far: subtract 0, every weight is 0
-                // (a NaN logit stays NaN).
-                const float ref = off == -CUDART_INF_F ? 0.f : off;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float pa = ex2(fmaf(v[32 * c + 2 * j], as, -ref));
-                        const float pb = ex2(fmaf(v[32 * c + 2 * j + 1], as, -ref));
-                        l0 += pa;
-                        l1 += pb;
-                        pk[j] = pack<KV>(pa, pb);
-                    }
-                    tmem_st16u(s_addr + c * 16, pk);
+                // Mostly the reference stays: the weights are made while the
+                // maximum is found, and the first half again where it moved.
+                const bool ahead = !part && !first && scl > 0.f;
+                if (!ahead) raise();
+                refer();
+                weigh(0);
+                weigh(1);
+                if (ahead && raise()) {
+                    refer();
+                    s0 = s1 = 0;
+                    weigh(0);
+                    weigh(1);
                 }
+                if (!ok) break;
+                weigh(2);
+                weigh(3);
+                l0 = add2(l0, s0);
+                l1 = add2(l1, s1);
                 hs::tc::tmem_wait_st();
                 if (part) {
                     // Rows of V that were taken out.
@@ -595,19 +723,19 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
                         any |= o.x | o.y | o.z | o.w;
                     }
                     if (!ok) break;
-                    if (i == s.i0) B.keep[w] = any != 0;
+                    if (first) B.keep[w] = any != 0;
                     if (any != 0) {
-                        if (NQ == 1 && i != s.i0) {
-                            ok = __all_sync(0xffffffffu, wait(&B.pv_done, mine - 1));
+                        if (NQ == 1 && !first) {
+                            ok = __all_sync(0xffffffffu, pv_wait(mine - 1));
                             if (!ok) break;
                             hs::tc::fence_after_sync();
                         }
                         const float zero[16] = {};
-                        if (i == s.i0)
+                        if (first)
                             for (int c = 0; c < D; c += 16) hs::tc::tmem_st16(o_addr + uint32_t(c), zero);
                         hs::tc::tmem_wait_st();
                         for (int j = 0; j < kTile; ++j) {
-                            const uint32_t pw = tmem_ld1(s_addr + uint32_t(j >> 1));
+                            const uint32_t pw = tmem_ld1(p_addr + uint32_t(j >> 1));
                             hs::tc::tmem_wait_ld();
                             const uint32_t h = (j & 1) ? pw >> 16 : pw & 0xffffu;
                             const float p = KV == kBf16 ? __uint_as_float(h << 16)
@@ -616,7 +744,7 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
                             const bool sees = (vw >> (j & 31)) & 1u;
                             for (int u = 0; u < kSubs; ++u) {
                                 if (!((B.odd[t & (kRing - 1)][u][j >> 5] >> (j & 31)) & 1u)) continue;
-                                const int tk = t0 + j, b = block_of(a, tk);
+                                const int tk = B.tile[t & (kRing - 1)].x + j, b = block_of(a, tk);
                                 const int64_t page = a.block_table[s.row * a.bt_stride + b];
                                 const void* row = static_cast<const char*>(a.v) +
                                     (page * a.page_stride + int64_t(tk - b * a.page_size) * a.row_stride +
@@ -634,7 +762,7 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
                             }
                         }
                     }
-                } else if (i == s.i0) {
+                } else if (first) {
                     B.keep[w] = 0;
                 }
                 hs::tc::fence_before_sync();
@@ -642,11 +770,11 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
             }
             if (!ok) break;
             // ---- The unit's state ---------------------------------------------
-            ok = __all_sync(0xffffffffu, wait(&B.o_full[w], segs));
+            ok = __all_sync(0xffffffffu, pv_wait(mine - 1));
             if (!ok) break;
-            ++segs;
             hs::tc::fence_after_sync();
-            const float l = l0 + l1;
+            const float2 ls = split(add2(l0, l1));
+            const float l = ls.x + ls.y;
             const float lg = l == 0.f ? -CUDART_INF_F : off + log2f(l);
             float f = 1.f;
             if (whole) {
@@ -654,36 +782,63 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
                 if (a.v_scale != nullptr && l != 0.f) f *= a.v_scale[s.kvh];
                 if (live && a.lse != nullptr) a.lse[qh] = lg * kLn2;
             }
-            const int64_t slot = int64_t(2 * blockIdx.x + (s.start < B.place0 ? 0 : 1)) * a.unit_rows +
-                                 w * kTile + r;
-            if (!whole && live) {
-                a.part_ml[2 * slot] = off;
-                a.part_ml[2 * slot + 1] = l;
-            }
+            const int64_t slot0 = 2 * int(blockIdx.x) + (s.start < B.place0 ? 0 : 1);
+            if (!whole && live)
+                reinterpret_cast<float2*>(a.part_ml)[slot0 * a.unit_rows + w * kTile + r] =
+                    make_float2(off, l);
+            // Lanes of the warp's rows that have a query, and where they go.
+            const int64_t to = live ? qh * D : -1;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float o[32];
                 tmem_ld32(o_addr + uint32_t(c), o);
                 hs::tc::tmem_wait_ld();
-                if (!live) continue;
                 if (!whole) {
-                    float4* po = reinterpret_cast<float4*>(a.part_o + slot * D + c);
+                    // [4 dims][row]: neighbouring lanes, neighbouring addresses.
+                    float4* po = reinterpret_cast<float4*>(a.part_o) +
+                                 ((slot0 * (D / 4) + c / 4) * a.unit_rows + w * kTile + r);
+                    if (live)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        po[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                        for (int j = 0; j < 8; ++j)
+                            po[j * a.unit_rows] =
+                                make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                     continue;
                 }
 #pragma unroll
                 for (int j = 0; j < 32; ++j) o[j] = l == 0.f ? 0.f : o[j] * f;
-                uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + qh * D + c);
+                // Four lanes exchange 16-byte pieces of their rows, so that they
+                // write 64 neighbouring bytes of one row at a time (16 bytes of
+                // 32 rows at a time took 4 us a unit).
+                uint32_t y[4][4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t y[4];
+                for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        y[e] = bf ? pack<kBf16>(o[8 * j + 2 * e], o[8 * j + 2 * e + 1])
-                                  : pack<kFp16>(o[8 * j + 2 * e], o[8 * j + 2 * e + 1]);
-                    out[j] = make_uint4(y[0], y[1], y[2], y[3]);
+                        y[j][e] = bf ? pack<kBf16>(o[8 * j + 2 * e], o[8 * j + 2 * e + 1])
+                                     : pack<kFp16>(o[8 * j + 2 * e], o[8 * j + 2 * e + 1]);
+                const int b = lane & 3;
+                // got[k]: piece b of the row of the quad's lane b ^ k.
+                uint32_t got[4][4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int j = b ^ k;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t give = j == 0 ? y[0][e] : j == 1 ? y[1][e] : j == 2 ? y[2][e] : y[3][e];
+                        got[k][e] = k == 0 ? give : __shfl_xor_sync(0xffffffffu, give, k);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int j = b ^ k;
+                    const int64_t row = __shfl_sync(0xffffffffu, to, (lane & ~3) + k);
+                    uint32_t z[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        z[e] = j == 0 ? got[0][e] : j == 1 ? got[1][e] : j == 2 ? got[2][e] : got[3][e];
+                    if (row >= 0)
+                        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row + c + b * 8) =
+                            make_uint4(z[0], z[1], z[2], z[3]);
                 }
             }
             hs::tc::fence_before_sync();
@@ -692,127 +847,139 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
         if (w < NQ && !ok) give_up();
         if (tid == 0 && !head) a.shared[blockIdx.x].valid = 0;
     } else if (warp < kLoadWarp) {
-        set_max_regs_down<40>();
-        if (warp == kMmaWarp) {
-            // ------------------------------ products ----------------------------
-            if (lane == 0) {
-                constexpr uint32_t id_qk = idesc<KV>(kTile, 0), id_pv = idesc<KV>(C::kDims, 1);
-                const uint64_t q_desc = hs::tc::sdesc_sw128(sb + C::kQOff, 16, 1024);
-                const uint64_t k_desc = hs::tc::sdesc_sw128(sb + C::kRingOff, 16, 1024);
-                const uint64_t v_desc = hs::tc::sdesc_sw128(sb + C::kRingOff, kBlk, 1024);
-                bool ok = true;
-                int t = 0, segs = 0, done[2] = {0, 0}, had[2] = {0, 0};
-                // S of query tile (or buffer) x from the K tile in the ring.
-                const auto qk = [&](int t, int x, int tile) {
+        set_max_regs_down<C::kMmaRegs>();
+        // Products and commits are the bound of a warp that issues them all (3600
+        // cycles for a pair of tiles whose products take 2048): one issues QK,
+        // one PV.  Two query tiles share S, whose softmax begins by taking it into
+        // registers, and have a P each: the QK of one runs ahead of the PV of the
+        // other, and a tile has the time of both tiles' products for its softmax.
+        // (With S and P of a tile in the same columns QK has to wait for PV and
+        // the softmax is on the products' path.)
+        bool ok = true;
+        const auto all_wait = [&](uint64_t* bar, int parity) {
+            ok = ok && __all_sync(0xffffffffu, wait(bar, parity));
+        };
+        if (warp == kQkWarp) {
+            // ------------------------------- S = Q K^T ---------------------------
+            constexpr uint32_t id = idesc<KV>(kTile, 0);
+            const uint64_t q_desc = hs::tc::sdesc_sw128(sb + C::kQOff, 16, 1024);
+            const uint64_t k_desc = hs::tc::sdesc_sw128(sb + C::kRingOff, 16, 1024);
+            int t = 0, segs = 0, n_qk = 0;
+            for (bool more = first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
+                const int n = s.i1 - s.i0;
+                if (n == 0) continue;
+                const int tiles = NQ == 2 && a.tq < s.m ? 2 : 1;
+                all_wait(&B.q_full, segs++);
+                for (int i = 0; i < n && ok; ++i, ++t) {
+                    uint32_t at[kSubs];
 #pragma unroll
                     for (int u = 0; u < kSubs; ++u) {
-                        const uint32_t at = uint32_t(unit_of(t, false, u) % NS * (C::kUnit >> 4));
-#pragma unroll
-                        for (int k = 0; k < C::kDims / 16; ++k) {
-                            const int b = u * (C::kDims / 64) + k / 4;
-                            hs::tc::mma_bf16(tmem + uint32_t(x * 128),
-                                             q_desc + uint32_t(tile * (C::kQTile >> 4) + b * (kBlk >> 4) + (k & 3) * 2),
-                                             k_desc + at + uint32_t(k / 4 * (kBlk >> 4) + (k & 3) * 2),
-                                             id_qk, (u | k) ? 1u : 0u);
+                        const int k = turn_of(t, u);
+                        at[u] = uint32_t(unit_of(t, false, u) % NS * (C::kUnit >> 4));
+                        all_wait(&B.kfull[k % NS], k / NS);
+                    }
+                    for (int w = 0; w < tiles; ++w, ++n_qk) {
+                        const int x = NQ == 2 ? 0 : t & 1;
+                        // The last softmax has taken S, or the last product of
+                        // this buffer's P is done.
+                        if (NQ == 2) {
+                            if (n_qk > 0) all_wait(&B.s_free, n_qk - 1);
+                        } else if (t >= 2) {
+                            all_wait(&B.pv_done[x], (t - 2) >> 1);
                         }
+                        hs::tc::fence_after_sync();
+                        if (!ok) break;
+#pragma unroll
+                        for (int u = 0; u < kSubs; ++u)
+#pragma unroll
+                            for (int b = 0; b < C::kDims / 64; ++b)
+                                mma_ss4(tmem + uint32_t(x * 128),
+                                        q_desc + uint32_t(w * (C::kQTile >> 4) +
+                                                          (u * (C::kDims / 64) + b) * (kBlk >> 4)),
+                                        k_desc + at[u] + uint32_t(b * (kBlk >> 4)), id,
+                                        (u | b) ? 1u : 0u);
+                        commit(&B.s_full[NQ == 2 ? w : x]);
                     }
-                };
-                const auto wait_k = [&](int t) {
-                    for (int u = 0; u < kSubs; ++u) {
-                        const int q = TMA ? unit_of(t, false, u) : turn_of(t, u);
-                        ok = ok && wait(&B.full[q % NS], q / NS);
-                    }
-                    hs::tc::fence_after_sync();
-                };
-                const auto wait_v = [&](int t) {
+                    if (!ok) break;
+#pragma unroll
+                    for (int u = 0; u < kSubs; ++u) commit(&B.empty[unit_of(t, false, u) % NS]);
+                    if (i + 1 == n) commit(&B.q_empty);
+                }
+            }
+        } else if (warp == kPvWarp) {
+            // ------------------------------- O += P V ----------------------------
+            constexpr uint32_t id = idesc<KV>(C::kDims, 1);
+            const uint64_t v_desc = hs::tc::sdesc_sw128(sb + C::kRingOff, kBlk, 1024);
+            int t = 0, done0 = 0, done1 = 0, had0 = 0, had1 = 0;
+            for (bool more = first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
+                const int n = s.i1 - s.i0;
+                if (n == 0) continue;
+                const int tiles = NQ == 2 && a.tq < s.m ? 2 : 1;
+                // The outputs before have been read.
+                if (had0 > 0) all_wait(&B.o_free[0], had0 - 1);
+                if (tiles == 2 && had1 > 0) all_wait(&B.o_free[1], had1 - 1);
+                ++had0;
+                if (tiles == 2) ++had1;
+                for (int i = 0; i < n && ok; ++i, ++t) {
+                    uint32_t at[kSubs];
+#pragma unroll
                     for (int u = 0; u < kSubs; ++u) {
                         const int q = turn_of(t, u);
-                        ok = ok && wait(&B.ready[q % NS], q / NS);
+                        at[u] = uint32_t(unit_of(t, true, u) % NS * (C::kUnit >> 4));
+                        all_wait(&B.ready[q % NS], q / NS);
                     }
-                    hs::tc::fence_after_sync();
-                };
-                const auto free_units = [&](int t, bool v) {
-                    for (int u = 0; u < kSubs; ++u) hs::tc::mma_commit(&B.empty[unit_of(t, v, u) % NS]);
-                };
-                const auto pv = [&](int t, int x, int tile, bool fresh) {
+                    for (int w = 0; w < tiles; ++w) {
+                        const int x = NQ == 2 ? w : t & 1;
+                        all_wait(&B.p_full[x], NQ == 2 ? (w == 0 ? done0 : done1) : t >> 1);
+                        hs::tc::fence_after_sync();
+                        if (!ok) break;
+                        const bool fresh = i == 0 && B.keep[w] == 0;
+                        const uint32_t p_col =
+                            tmem + (NQ == 2 ? C::kPCol + uint32_t(w * 64) : uint32_t(x * 128));
 #pragma unroll
-                    for (int u = 0; u < kSubs; ++u) {
-                        const uint32_t at = uint32_t(unit_of(t, true, u) % NS * (C::kUnit >> 4));
+                        for (int u = 0; u < kSubs; ++u)
 #pragma unroll
-                        for (int k = 0; k < kTile / 16; ++k)
-                            mma_ts(tmem + C::kOCol + uint32_t(tile * 128 + u * 128),
-                                   tmem + uint32_t(x * 128 + k * 8), v_desc + at + uint32_t(k * 128),
-                                   id_pv, fresh && k == 0 ? 0u : 1u);
+                            for (int h = 0; h < 2; ++h)
+                                mma_ts4(tmem + C::kOCol + uint32_t((w + u) * 128), p_col + uint32_t(h * 32),
+                                        v_desc + at[u] + uint32_t(h * 512), id,
+                                        fresh && h == 0 ? 0u : 1u);
+                        commit(&B.pv_done[x]);
+                        if (w == 0) ++done0;
+                        else ++done1;
                     }
-                };
-                for (bool more = first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
-                    const int n = s.i1 - s.i0;
-                    if (n == 0) continue;
-                    const int tiles = NQ == 2 && s.m > a.tq ? 2 : 1;
-                    ok = ok && wait(&B.q_full, segs);
-                    ++segs;
-                    wait_k(t);
                     if (!ok) break;
-                    if (NQ == 2) {
-                        for (int x = 0; x < tiles; ++x) {
-                            qk(t, x, x);
-                            hs::tc::mma_commit(&B.s_full[x]);
-                        }
-                    } else {
-                        qk(t, t & 1, 0);
-                        hs::tc::mma_commit(&B.s_full[t & 1]);
-                    }
-                    free_units(t, false);
-                    if (n == 1) hs::tc::mma_commit(&B.q_empty);
-                    for (int i = 0; i < n && ok; ++i, ++t) {
-                        const bool next = i + 1 < n;
-                        if (NQ == 1 && next) {
-                            wait_k(t + 1);
-                            if (!ok) break;
-                            qk(t + 1, (t + 1) & 1, 0);
-                            hs::tc::mma_commit(&B.s_full[(t + 1) & 1]);
-                            free_units(t + 1, false);
-                            if (i + 2 == n) hs::tc::mma_commit(&B.q_empty);
-                        }
-                        for (int tile = 0; tile < tiles && ok; ++tile) {
-                            const int x = NQ == 2 ? tile : t & 1;
-                            const int ph = NQ == 2 ? done[tile] : t >> 1;
-                            // The output before has been read.
-                            if (i == 0 && had[tile] > 0) ok = wait(&B.o_free[tile], had[tile] - 1);
-                            ok = ok && wait(&B.p_full[x], ph);
-                            if (tile == 0) wait_v(t);
-                            hs::tc::fence_after_sync();
-                            if (!ok) break;
-                            pv(t, x, tile, i == 0 && B.keep[tile] == 0);
-                            ++done[tile];
-                            if (NQ == 1) hs::tc::mma_commit(&B.pv_done);
-                            if (tile == tiles - 1) free_units(t, true);
-                            if (!next) {
-                                hs::tc::mma_commit(&B.o_full[tile]);
-                                ++had[tile];
-                            } else if (NQ == 2) {
-                                if (tile == 0) wait_k(t + 1);
-                                if (!ok) break;
-                                qk(t + 1, x, tile);
-                                hs::tc::mma_commit(&B.s_full[x]);
-                                if (tile == tiles - 1) {
-                                    free_units(t + 1, false);
-                                    if (i + 2 == n) hs::tc::mma_commit(&B.q_empty);
-                                }
-                            }
-                        }
-                    }
+#pragma unroll
+                    for (int u = 0; u < kSubs; ++u) commit(&B.empty[unit_of(t, true, u) % NS]);
                 }
-                if (!ok) give_up();
-                // Every product issued has completed before TMEM is freed.
-                hs::tc::mma_commit(&B.drain);
-                hs::mbar_wait_bounded(&B.drain, 0, tmo, nullptr);
             }
-            __syncwarp();
-        } else {
+        } else if (TMA && warp == kQWarp) {
             // ------------------------------- queries ----------------------------
-            const int qw = warp - kMmaWarp - 1, qt = qw * 32 + lane;
-            bool ok = true;
+            // A box takes the heads of a KV head for a tile's tokens: its rows
+            // are the tile's.  (Tokens of other requests behind a unit's own
+            // land in rows that are not written.)
+            int segs = 0;
+            const uint32_t bytes = uint32_t(a.tq * a.group) * 128u;
+            for (bool more = first_seg(a, B, s); more; more = next_seg(a, B, s)) {
+                if (s.i1 == s.i0) continue;
+                ok = segs == 0 || __all_sync(0xffffffffu, wait(&B.q_empty, segs - 1));
+                if (!ok) break;
+                if (lane == 0) {
+                    const int tiles = s.m > a.tq ? 2 : 1;
+                    hs::mbar_arrive_expect_tx(&B.q_full, bytes * (D / 64) * tiles);
+                    for (int w = 0; w < tiles; ++w)
+                        for (int c = 0; c < D / 64; ++c)
+                            tma_load_q(sb + C::kQOff + w * C::kQTile + c * kBlk, &qmap, c * 64,
+                                       s.kvh * a.group, s.x.first + s.block * a.tb + w * a.tq,
+                                       &B.q_full);
+                }
+                __syncwarp();
+                ++segs;
+            }
+            // No copy may outlive the CTA.
+            if (segs > 0) hs::mbar_wait_bounded(&B.q_full, (segs - 1) & 1, tmo, nullptr);
+        } else if (!TMA && warp >= kQWarp) {
+            // ------------------------------- queries ----------------------------
+            const int qw = warp - kQWarp, qt = qw * 32 + lane;
             int segs = 0;
             for (bool more = first_seg(a, B, s); more; more = next_seg(a, B, s)) {
                 if (s.i1 == s.i0) continue;
@@ -823,10 +990,27 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
                 const int64_t first = s.x.first + s.block * a.tb;
                 const char* q = static_cast<const char*>(a.q) + int64_t(s.kvh) * a.group * D * 2;
                 constexpr int kCh = D / 8;  // 16-byte chunks of a row
+                // (A quotient by a division a row took 7 us a unit.)
+                constexpr int kRowStep = kQWarps * 32 / kCh;
+                const int hstep = kRowStep % a.group, tstep = kRowStep / a.group;
+                const int row0 = E4 ? qw * (32 / kCh) + lane / kCh : qt / kCh;
+                int tok = row0 / a.group, hd = row0 - tok * a.group;
+                const int tok0 = tok, hd0 = hd;
+                const auto next_row = [&](int n) {
+                    hd += hstep;
+                    tok += tstep;
+                    if (hd >= a.group) {
+                        hd -= a.group;
+                        ++tok;
+                    }
+                    if (NQ == 2 && n == kTile) {  // the second tile starts over
+                        tok = tok0;
+                        hd = hd0;
+                    }
+                };
                 if constexpr (!E4) {
-                    for (int e = qt; e < NQ * kTile * kCh; e += kQWarps * 32) {
-                        const int n = e / kCh, ch = e % kCh, w = n / kTile, r = n % kTile;
-                        const int tok = r / a.group, hd = r - tok * a.group;
+                    for (int n = row0; n < NQ * kTile; n += kRowStep, next_row(n - row0)) {
+                        const int ch = qt % kCh, w = n / kTile, r = n % kTile;
                         const bool in = tok < a.tq && w * a.tq + tok < s.m;
                         const int64_t at = in ? (first + w * a.tq + tok) * a.q_stride + hd * D + ch * 8 : 0;
                         hs::tc::cp_async16(sb + C::kQOff + w * C::kQTile + (ch >> 3) * kBlk + r * 128 +
@@ -836,11 +1020,10 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
                     hs::tc::cp_async_wait_all();
                 } else {
                     // A row per D / 8 lanes.
-                    constexpr int kRows = 32 / kCh;
                     const int ch = lane % kCh;
-                    for (int n = qw * kRows + lane / kCh; n < NQ * kTile; n += kQWarps * kRows) {
+#pragma unroll 4
+                    for (int n = row0; n < NQ * kTile; n += kRowStep, next_row(n - row0)) {
                         const int w = n / kTile, r = n % kTile;
-                        const int tok = r / a.group, hd = r - tok * a.group;
                         const bool in = tok < a.tq && w * a.tq + tok < s.m;
                         uint4 raw = make_uint4(0u, 0u, 0u, 0u);
                         if (in)
@@ -881,10 +1064,17 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
                 hs::mbar_arrive(&B.q_full);
                 ++segs;
             }
-            if (!ok) give_up();
+        }
+        if (!ok) give_up();
+        if (warp <= kPvWarp) {
+            // Every product issued has completed before TMEM is freed.
+            __syncwarp();
+            commit(&B.drain[warp - kQkWarp]);
+            hs::mbar_wait_bounded(&B.drain[warp - kQkWarp], 0, tmo, nullptr);
+            __syncwarp();
         }
     } else if constexpr (TMA) {
-        set_max_regs_down<88>();
+        set_max_regs_down<C::kLoadRegs>();
         const int runs = kTile / ta.bt;  // a power of two up to 8
         if (warp == kLoadWarp) {
             // -------------------------------- loads -----------------------------
@@ -911,6 +1101,10 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
                         }
                         B.loaded[t & (kRing - 1)][lane] = bits;
                     }
+                    if (lane == 4) {
+                        const int t0 = token_of(s, i);
+                        B.tile[t & (kRing - 1)] = make_int2(t0, !all_see(a, s, t0) || got != low_bits(runs));
+                    }
                     __syncwarp();
                     const uint32_t bytes = uint32_t(__popc(got)) * box * (C::kDims / 64);
                     const int at = tok - b * a.page_size;
@@ -918,14 +1112,16 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
                         const int slot = seq % NS;
                         ok = __all_sync(0xffffffffu, wait(&B.empty[slot], seq / NS + 1));
                         if (!ok) break;
-                        if (lane == 0) hs::mbar_arrive_expect_tx(&B.full[slot], bytes);
+                        const int turn = turn_of(t, u % kSubs) % NS;
+                        uint64_t* full = u < kSubs ? &B.kfull[turn] : &B.vfull[turn];
+                        if (lane == 0) hs::mbar_arrive_expect_tx(full, bytes);
                         __syncwarp();
                         if (want) {
                             const uint32_t dst = sb + C::kRingOff + slot * C::kUnit + lane * box;
 #pragma unroll
                             for (int c = 0; c < C::kDims / 64; ++c)
                                 tma_load(dst + c * kBlk, u < kSubs ? &kmap : &vmap,
-                                         u % kSubs * C::kDims + c * 64, at, s.kvh, page, &B.full[slot]);
+                                         u % kSubs * C::kDims + c * 64, at, s.kvh, page, full);
                         }
                     }
                 }
@@ -933,8 +1129,11 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
             if (!ok) {
                 give_up();
                 // No copy may outlive the CTA: wait for every unit in flight.
-                for (int q = max(0, seq - NS); q < seq; ++q)
-                    hs::mbar_wait_bounded(&B.full[q % NS], (q / NS) & 1, tmo, nullptr);
+                for (int q = max(0, seq - NS); q < seq; ++q) {
+                    const int u = q % (2 * kSubs), turn = turn_of(q / (2 * kSubs), u % kSubs);
+                    hs::mbar_wait_bounded(u < kSubs ? &B.kfull[turn % NS] : &B.vfull[turn % NS],
+                                          (turn / NS) & 1, tmo, nullptr);
+                }
             }
             if (bad) hs::set_status(a.status, HS_ERR_BAD_INDEX);
         } else {
@@ -946,11 +1145,10 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
                 for (int i = s.i0; i < s.i1 && ok; ++i, ++t) {
                     const int t0 = token_of(s, i);
                     for (int u = 0; u < kSubs; ++u) {
-                        const int q = unit_of(t, true, u);
-                        ok = __all_sync(0xffffffffu, wait(&B.full[q % NS], q / NS));
+                        const int q = unit_of(t, true, u), turn = turn_of(t, u);
+                        ok = __all_sync(0xffffffffu, wait(&B.vfull[turn % NS], turn / NS));
                         if (!ok) break;
-                        const uint4 ld = *reinterpret_cast<const uint4*>(B.loaded[t & (kRing - 1)]);
-                        if (!all_see(a, s, t0) || (ld.x & ld.y & ld.z & ld.w) != 0xffffffffu) {
+                        if (B.tile[t & (kRing - 1)].y != 0) {
                             for (int j = cw; j < 4; j += kCheckWarps) {
                                 const int r = j * 32 + lane;
                                 const bool in = any_sees(a, s, t0 + r) &&
@@ -971,7 +1169,7 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
                             hs::fence_proxy_async_shared();
                         }
                         __syncwarp();
-                        if (lane == 0) hs::mbar_arrive(&B.ready[turn_of(t, u) % NS]);
+                        if (lane == 0) hs::mbar_arrive(&B.ready[turn % NS]);
                     }
                 }
             }
@@ -979,7 +1177,7 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
         }
     } else {
         // ------------------- loads by threads, and rows of V --------------------
-        set_max_regs_down<88>();
+        set_max_regs_down<C::kLoadRegs>();
         constexpr int kElt = E4 ? 1 : 2, kPer = 16 / kElt;  // elements of 16 bytes
         constexpr int kCh = D / kPer;                       // 16-byte chunks of a row
         constexpr int kStep = kTile / kCh;                  // rows of a pass
@@ -1068,7 +1266,7 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
             hs::fence_proxy_async_shared();
             for (int u = 0; u < kSubs; ++u) {
                 const int q = turn_of(t, u);
-                hs::mbar_arrive(v ? &B.ready[q % NS] : &B.full[q % NS]);
+                hs::mbar_arrive(v ? &B.ready[q % NS] : &B.kfull[q % NS]);
             }
         };
         for (bool more = first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
@@ -1079,6 +1277,7 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
                 const uint4 ld = *reinterpret_cast<const uint4*>(B.loaded[t & (kRing - 1)]);
                 const bool part = !all_see(a, s, token_of(s, i)) ||
                                   (ld.x & ld.y & ld.z & ld.w) != 0xffffffffu;
+                if (lt == 0) B.tile[t & (kRing - 1)] = make_int2(token_of(s, i), part);
                 // Batches of K, then of V; each is loaded while the one before
                 // it is stored.
 #pragma unroll
@@ -1104,11 +1303,13 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
     hs::tc::fence_before_sync();
     __syncthreads();
     hs::tc::fence_after_sync();
-    if (warp == kMmaWarp) hs::tc::tmem_dealloc(tmem, kTmemCols);
+    if (warp == kQkWarp) hs::tc::tmem_dealloc(tmem, kTmemCols);
 }
 
 // Tensor map of a cache: dims (head dim, token of the page, KV head, page).
 int encode_map(CUtensorMap* m, const void* base, const PrefillArgs& a, int kv_dtype, int d, int bt);
+// Of the queries: dims (head dim, head, token), boxes of a query tile.
+int encode_q_map(CUtensorMap* m, const PrefillArgs& a, int dtype, int d);
 
 template <int KV, int D, bool TMA>
 int launch_one(const PrefillArgs& a, int bt, hs_stream_t stream) {
@@ -1134,13 +1335,14 @@ int launch_one(const PrefillArgs& a, int bt, hs_stream_t stream) {
         return -1;
     };
     if (hs_host::ask_once(&regs[dev], ask) != 65536 / kThreads) return HS_ERR_UNSUPPORTED;
-    CUtensorMap k{}, v{};
+    CUtensorMap q{}, k{}, v{};
     if (TMA) {
-        rc = encode_map(&k, a.k, a, KV, D, bt);
+        rc = encode_q_map(&q, a, KV, D);
+        if (rc == HS_OK) rc = encode_map(&k, a.k, a, KV, D, bt);
         if (rc == HS_OK) rc = encode_map(&v, a.v, a, KV, D, bt);
         if (rc != HS_OK) return rc;
     }
-    return hs_host::launch_pdl(kern, dim3(unsigned(a.ctas)), dim3(kThreads), smem, stream, t, k, v);
+    return hs_host::launch_pdl(kern, dim3(unsigned(a.ctas)), dim3(kThreads), smem, stream, t, q, k, v);
 }
 
 // bt: tokens of a TMA box, or 0: threads load.

@@ -280,3 +280,14 @@ def test_refusals():
         call(s, workspace=torch.empty(64, 64, device="cuda").t()[:, :3])
     with pytest.raises(ValueError):
         call(s, out=torch.empty(4, 8, 64, dtype=BF, device="cuda"))
+
+
+def test_cold_cache_loads_land_in_any_order():
+    s = setup([5] * 6, [4000 - 37 * i for i in range(6)], 16, 4, 128, 16)
+    flush = torch.empty(48 << 20, dtype=torch.int32, device="cuda")
+    want = call(s)
+    for _ in range(60):
+        flush.fill_(1)
+        got = call(s)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert s["status"].item() == 0
