@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
     for (int i = 0; i < kMergeDims; ++i) o[i] = 0.f;
     const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + j;
     const float4* po = reinterpret_cast<const float4*>(a.part_o) +
-                       int64_t(part * (kMergeDims / 4)) * a.unit_rows + j;
+                       (int64_t(part * (kMergeDims / 8)) * a.unit_rows + j) * 2;
     constexpr int kAhead = 4;  // parts in flight
     for (int p0 = 0; p0 < n; p0 += kAhead) {
         float2 s[kAhead];
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
             s[k] = __ldcg(ml + slot * a.unit_rows);
 #pragma unroll
             for (int i = 0; i < kMergeDims / 4; ++i)
-                x[k][i] = __ldcg(po + (slot * (D / 4) + i) * a.unit_rows);
+                x[k][i] = __ldcg(po + (slot * (D / 8) + i / 2) * a.unit_rows * 2 + i % 2);
         }
         float m = M;
 #pragma unroll
@@ -283,6 +283,7 @@ extern "C" int hs_paged_prefill(const void* q, int64_t q_stride, int32_t q_dtype
     a.max_len = max_len;
     a.scale_log2 = scale * kLog2e;
     a.out = out;
+    a.out_wide = al(out, 32);
     a.lse = lse;
     a.status = status;
     a.q_is_half = q_dtype == HS_FP16;

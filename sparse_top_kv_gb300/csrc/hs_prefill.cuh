@@ -43,6 +43,7 @@ struct PrefillArgs {
     int32_t q_is_half;   // E4M3 caches: the query is fp16 (else bf16)
     float scale_log2;    // scale * log2(e)
     void* out;           // [tokens, heads, D]
+    int32_t out_wide;    // out is 32-byte aligned
     float* lse;          // [tokens, heads] or nullptr
     int32_t tq;          // new tokens of a query tile: 128 / group
     int32_t tb;          // and of a unit: one or two query tiles
@@ -50,7 +51,7 @@ struct PrefillArgs {
     // Workspace: two partial states per CTA (of the units that its run begins
     // and ends in) and the shared units.
     float* part_ml;      // [2 * ctas][unit rows][2]
-    float* part_o;       // [2 * ctas][D / 4][unit rows][4]
+    float* part_o;       // [2 * ctas][D / 8][unit rows][8]
     SharedUnit* shared;  // [ctas]
     int32_t unit_rows;   // 128 or 256
     int32_t* status;

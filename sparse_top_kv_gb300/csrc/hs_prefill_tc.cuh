@@ -374,6 +374,12 @@ template <int N>
 __device__ __forceinline__ void set_max_regs_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
+// 32 bytes, 32-byte aligned.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
 // 2^x (PTX ex2.approx.ftz: within 2 ulp; 0 below -126, where a weight no longer
 // counts against the sum's 1).
 __device__ __forceinline__ float ex2(float x) {
@@ -786,59 +792,44 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
             if (!whole && live)
                 reinterpret_cast<float2*>(a.part_ml)[slot0 * a.unit_rows + w * kTile + r] =
                     make_float2(off, l);
-            // Lanes of the warp's rows that have a query, and where they go.
-            const int64_t to = live ? qh * D : -1;
+            // A row per thread: 32 bytes of each of 32 rows at a time.  (Pieces
+            // exchanged between lanes for whole lines: five times as long.)
+            uint16_t* to = static_cast<uint16_t*>(a.out) + qh * D;
+            float* po = a.part_o + ((slot0 * (D / 8)) * a.unit_rows + w * kTile + r) * 8;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float o[32];
                 tmem_ld32(o_addr + uint32_t(c), o);
                 hs::tc::tmem_wait_ld();
+                if (!live) continue;
                 if (!whole) {
-                    // [4 dims][row]: neighbouring lanes, neighbouring addresses.
-                    float4* po = reinterpret_cast<float4*>(a.part_o) +
-                                 ((slot0 * (D / 4) + c / 4) * a.unit_rows + w * kTile + r);
-                    if (live)
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            po[j * a.unit_rows] =
-                                make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    for (int j = 0; j < 32; j += 8) {
+                        uint32_t y[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] = __float_as_uint(o[j + e]);
+                        store32(po + int64_t((c + j) / 8) * a.unit_rows * 8, y);
+                    }
                     continue;
                 }
 #pragma unroll
                 for (int j = 0; j < 32; ++j) o[j] = l == 0.f ? 0.f : o[j] * f;
-                // Four lanes exchange 16-byte pieces of their rows, so that they
-                // write 64 neighbouring bytes of one row at a time (16 bytes of
-                // 32 rows at a time took 4 us a unit).
-                uint32_t y[4][4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < 32; j += 16) {
+                    uint32_t y[8];
+                    if (bf) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        y[j][e] = bf ? pack<kBf16>(o[8 * j + 2 * e], o[8 * j + 2 * e + 1])
-                                     : pack<kFp16>(o[8 * j + 2 * e], o[8 * j + 2 * e + 1]);
-                const int b = lane & 3;
-                // got[k]: piece b of the row of the quad's lane b ^ k.
-                uint32_t got[4][4];
+                        for (int e = 0; e < 8; ++e) y[e] = pack<kBf16>(o[j + 2 * e], o[j + 2 * e + 1]);
+                    } else {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int j = b ^ k;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t give = j == 0 ? y[0][e] : j == 1 ? y[1][e] : j == 2 ? y[2][e] : y[3][e];
-                        got[k][e] = k == 0 ? give : __shfl_xor_sync(0xffffffffu, give, k);
+                        for (int e = 0; e < 8; ++e) y[e] = pack<kFp16>(o[j + 2 * e], o[j + 2 * e + 1]);
                     }
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int j = b ^ k;
-                    const int64_t row = __shfl_sync(0xffffffffu, to, (lane & ~3) + k);
-                    uint32_t z[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        z[e] = j == 0 ? got[0][e] : j == 1 ? got[1][e] : j == 2 ? got[2][e] : got[3][e];
-                    if (row >= 0)
-                        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row + c + b * 8) =
-                            make_uint4(z[0], z[1], z[2], z[3]);
+                    if (a.out_wide) {
+                        store32(to + c + j, y);
+                    } else {
+                        reinterpret_cast<uint4*>(to + c + j)[0] = make_uint4(y[0], y[1], y[2], y[3]);
+                        reinterpret_cast<uint4*>(to + c + j)[1] = make_uint4(y[4], y[5], y[6], y[7]);
+                    }
                 }
             }
             hs::tc::fence_before_sync();
