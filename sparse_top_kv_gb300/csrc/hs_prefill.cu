@@ -11,8 +11,6 @@ namespace hs_paged {
 namespace tc {
 using Encode = decltype(&cuTensorMapEncodeTiled);
 Encode encoder();
-int encode_map(CUtensorMap* m, int kv, const void* base, const PagedArgs& a, int d, int bt,
-               int hs_box);
 }  // namespace tc
 }  // namespace hs_paged
 
@@ -23,41 +21,56 @@ int launch_fp16(const PrefillArgs& a, int d, int bt, hs_stream_t stream);
 int launch_e4m3(const PrefillArgs& a, int d, int bt, hs_stream_t stream);
 
 namespace tc {
-int encode_map(CUtensorMap* m, const void* base, const PrefillArgs& a, int kv_dtype, int d,
-               int bt) {
-    hs_paged::PagedArgs p{};  // what the decode's maps depend on
-    p.page_stride = a.page_stride;
-    p.row_stride = a.row_stride;
-    p.head_stride = a.head_stride;
-    p.num_pages = a.num_pages;
-    p.page_size = a.page_size;
-    p.kv_heads = a.kv_heads;
-    return hs_paged::tc::encode_map(m, kv_dtype, base, p, d, bt, 1);
-}
-int encode_q_map(CUtensorMap* m, const PrefillArgs& a, int dtype, int d) {
+int encode(CUtensorMap* m, int dtype, int dims, const void* base, const cuuint64_t* size,
+           const cuuint64_t* stride, const cuuint32_t* box) {
     const hs_paged::tc::Encode f = hs_paged::tc::encoder();
     if (f == nullptr) return HS_ERR_CUDA;
+    const cuuint32_t one[4] = {1u, 1u, 1u, 1u};
+    const CUtensorMapDataType type = dtype == HS_BF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                     : dtype == HS_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                        : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const CUresult r =
+        f(m, type, cuuint32_t(dims), const_cast<void*>(base), size, stride, box, one,
+          CU_TENSOR_MAP_INTERLEAVE_NONE,
+          // E4M3 rows are converted by threads, in their own order.
+          dtype == HS_E4M3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? HS_OK : HS_ERR_CUDA;
+}
+int encode_map(CUtensorMap* m, const void* base, const PrefillArgs& a, int kv_dtype, int d,
+               int bt) {
+    const cuuint64_t elt = kv_dtype == HS_E4M3 ? 1 : 2;
+    // A dimension of one entry may have any stride; the encoder wants a valid one.
+    const auto bytes = [&](int64_t stride, int64_t n) {
+        return n > 1 ? cuuint64_t(stride) * elt : cuuint64_t(d) * elt;
+    };
+    const cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(a.page_size), cuuint64_t(a.kv_heads),
+                                cuuint64_t(a.num_pages)};
+    const cuuint64_t strides[3] = {bytes(a.row_stride, a.page_size),
+                                   bytes(a.head_stride, a.kv_heads),
+                                   bytes(a.page_stride, a.num_pages)};
+    // E4M3: the dims of a ring unit; else one swizzled block's.
+    const int wide = kv_dtype != HS_E4M3 || d == 64 ? 64 : 128;
+    const cuuint32_t box[4] = {cuuint32_t(wide), cuuint32_t(bt), 1u, 1u};
+    return encode(m, kv_dtype, 4, base, dims, strides, box);
+}
+int encode_q_map(CUtensorMap* m, const PrefillArgs& a, int dtype, int d) {
     const cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(a.heads), cuuint64_t(a.tokens)};
     const cuuint64_t strides[2] = {
         cuuint64_t(d) * 2,
         a.tokens > 1 ? cuuint64_t(a.q_stride) * 2 : cuuint64_t(a.heads) * d * 2};
     const cuuint32_t box[3] = {64u, cuuint32_t(a.group), cuuint32_t(a.tq)};
-    const cuuint32_t one[3] = {1u, 1u, 1u};
-    const CUresult r = f(m, dtype == HS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                         3, const_cast<void*>(a.q), dims, strides, box, one,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? HS_OK : HS_ERR_CUDA;
+    return encode(m, dtype, 3, a.q, dims, strides, box);
 }
 }  // namespace tc
 
 namespace {
 
 // Tokens of a TMA box, or 0 where threads have to load: pages without runs of
-// 16 tokens, broadcast strides.  (E4M3 rows are converted by threads.)
+// 16 tokens, broadcast strides.
 int box_tokens(const PrefillArgs& a, int kv_dtype) {
     const int64_t most = int64_t(1) << 38;  // elements; the encoder takes strides below 2^40 bytes
-    if (kv_dtype == HS_E4M3 || a.page_size % 16 != 0 || a.num_pages <= 0 ||
+    if (a.page_size % 16 != 0 || a.num_pages <= 0 ||
         (a.kv_heads > 1 && (a.head_stride <= 0 || a.head_stride >= most)) ||
         (a.num_pages > 1 && (a.page_stride <= 0 || a.page_stride >= most)) || a.row_stride <= 0 ||
         a.row_stride >= most || (a.tokens > 1 && (a.q_stride <= 0 || a.q_stride >= most)))

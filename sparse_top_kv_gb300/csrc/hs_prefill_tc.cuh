@@ -48,15 +48,12 @@ enum Kind { kBf16 = 0, kFp16 = 1, kE4m3 = 2 };
 
 constexpr int kThreads = 512;
 constexpr int kQkWarp = 8, kPvWarp = 9;
-constexpr int kQWarp = 10;     // and 11: queries
-constexpr int kQWarps = 2;
-constexpr int kLoadWarp = 12;  // TMA: 13 to 15 check V; else all four load
-constexpr int kCheckWarps = 3;
+constexpr int kTmaWarp = 10;   // or, with 11, the queries
+constexpr int kQThreads = 64;
+constexpr int kLoadWarp = 12;  // to 15: V's rows or the loads, and the outputs
 constexpr int kLoadBar = 1;    // named barrier of the loading threads
 constexpr int kBlk = kTile * 128;  // 128 rows x 128 bytes
-constexpr int kRing = 16;      // tiles whose loaded tokens are remembered
 constexpr int kTmemCols = 512;
-constexpr int kSegRing = 4;    // units whose query scales are remembered
 
 struct TcArgs {
     PrefillArgs p;
@@ -64,60 +61,56 @@ struct TcArgs {
     uint64_t timeout_ns;
 };
 
-template <int KV, int D, bool TMA>
+// Who loads K and V.
+enum Loads { kTma = 0, kThreadsLoad = 1 };
+
+template <int KV, int D, int LD>
 struct Cfg {
-    static constexpr bool kE4 = KV == kE4m3;
+    static constexpr int kKind = KV, kD = D;
+    static constexpr bool kE4 = KV == kE4m3, kByTma = LD == kTma;
+    static constexpr bool kConvert = kE4 && kByTma;        // E4M3 units pass through a stage
     static constexpr int NQ = D == 256 ? 1 : 2;            // query tiles of a unit
-    static constexpr int NB = D == 256 ? 2 : 1;            // S buffers of each
     static constexpr int kDims = D < 128 ? D : 128;        // dims of a ring unit
     static constexpr int kSubs = D / kDims;                // ring units of a tile
     static constexpr int kUnit = kTile * kDims * 2;
     static constexpr int kQTile = kTile * D * 2;
-    static constexpr int NS = D == 64 ? 10 : TMA ? 5 : 4;  // ring units
-    static constexpr int kQOff = 0;
-    static constexpr int kRingOff = NQ * kQTile;
-    static constexpr int kBarOff = kRingOff + NS * kUnit;
+    static constexpr int NS = D == 64 ? 8 : kByTma && !kE4 ? 5 : 4;  // ring units
+    static constexpr int kStages = kConvert ? 2 : 0, kStage = kTile * kDims;
+    static constexpr int kRing = 8;        // tiles whose loaded tokens are remembered
+    static constexpr int kSegRing = D == 256 ? 4 : 2;  // units whose query scales are
+    static constexpr int kRingOff = NQ * kQTile;       // (queries first)
+    static constexpr int kStageOff = kRingOff + NS * kUnit;
+    static constexpr int kBarOff = kStageOff + kStages * kStage;
     // TMEM columns.  Two query tiles: one S for both, a P of each, an O of each.
     // One: two S buffers, whose first half P takes, and O.
     static constexpr uint32_t kPCol = 128, kOCol = 256;
     // Registers of a thread, by warpgroup: 2 * soft + products + loads = 512.
-    static constexpr int kSoftRegs = TMA ? 184 : 168, kMmaRegs = 72, kLoadRegs = TMA ? 72 : 104;
+    static constexpr int kSoftRegs = kByTma ? 176 : 168, kMmaRegs = kByTma ? 64 : 72,
+                         kLoadRegs = kByTma ? 96 : 104;
     static_assert(2 * kSoftRegs + kMmaRegs + kLoadRegs == 65536 / 128, "register shares");
+    // Log2 headroom before the reference moves, and what P is raised by.
     static constexpr float kThresh = KV == kBf16 ? 8.f : 4.f;
     static constexpr float kShift = KV == kBf16 ? 0.f : 11.f;
 };
 
+template <typename C>
 struct Bars {
-    uint64_t kfull[10], vfull[10], ready[10], empty[10];
-    uint64_t q_full, q_empty, s_full[2], s_free, p_full[2], pv_done[2], o_free[2], drain[2];
+    uint64_t kfull[C::NS], vfull[C::NS], ready[C::NS], empty[C::NS];
+    uint64_t sfull[2], sempty[2];
+    uint64_t q_full, q_empty, s_full[2], s_free, p_full[2], pv_done[2], l_full[2], o_free[2], drain[2];
     int64_t place0, place1, start;  // the run, and where its first unit starts
     int64_t per;                    // the call's places: per * ctas + rest
     int32_t rest;
     int32_t row, kvh, block;        // the run's first unit
     uint32_t tmem_base;
     volatile int32_t abort;
-    volatile int32_t keep[2];              // O holds something before the first product
-    alignas(16) uint32_t loaded[kRing][4]; // tokens of a tile that were loaded
-    int2 tile[kRing];                      // its first token; whether some query does not see all of it
-    alignas(16) uint32_t odd[kRing][2][4]; // rows of V that were taken out, by ring unit
-};
-struct BarsLdg : Bars {
-    int64_t offset[2][kTile];              // rows of a tile in the cache, -1: none
-};
-struct BarsE4 : BarsLdg {
-    float qscale[kSegRing][2 * kTile];
-};
-template <bool TMA, bool E4>
-struct BarsOf {
-    using T = Bars;
-};
-template <>
-struct BarsOf<false, false> {
-    using T = BarsLdg;
-};
-template <>
-struct BarsOf<false, true> {
-    using T = BarsE4;
+    volatile int32_t keep[2];                     // O holds something before the first product
+    alignas(16) uint32_t loaded[C::kRing][4];     // tokens of a tile that were loaded
+    int2 tile[C::kRing];                          // its first token; whether some query does not see all of it
+    alignas(16) uint32_t odd[C::kRing][C::kSubs][4];  // rows of V that were taken out, by ring unit
+    float factor[C::NQ][kTile];                   // of each row's output; 0: nothing was attended to
+    int8_t qexp[C::kE4 ? C::kSegRing : 1][C::kE4 ? C::NQ * kTile : 1];  // queries are raised by 2^qexp
+    int64_t offset[C::kByTma ? 1 : 2][C::kByTma ? 1 : kTile];  // rows of a tile in the cache, -1: none
 };
 
 // One unit's share of a run.
@@ -150,7 +143,8 @@ __device__ __forceinline__ void shape(const PrefillArgs& a, Seg& s, int64_t plac
     s.begins = place0 <= s.start;
 }
 // The run's first unit, or none (false).
-__device__ __forceinline__ bool first_seg(const PrefillArgs& a, const Bars& B, Seg& s) {
+template <typename B_>
+__device__ __forceinline__ bool first_seg(const PrefillArgs& a, const B_& B, Seg& s) {
     if (B.place0 >= B.place1) return false;
     s.row = B.row;
     s.kvh = B.kvh;
@@ -160,7 +154,8 @@ __device__ __forceinline__ bool first_seg(const PrefillArgs& a, const Bars& B, S
     shape(a, s, B.place0, B.place1);
     return true;
 }
-__device__ __forceinline__ bool next_seg(const PrefillArgs& a, const Bars& B, Seg& s) {
+template <typename B_>
+__device__ __forceinline__ bool next_seg(const PrefillArgs& a, const B_& B, Seg& s) {
     s.start += s.cost;
     if (s.start >= B.place1) return false;
     if (++s.block >= blocks_of(a, s.x.n)) {
@@ -192,7 +187,8 @@ __device__ __forceinline__ bool all_see(const PrefillArgs& a, const Seg& s, int 
 
 // The run of this CTA: its places, and the unit that they begin in.  All
 // threads; ends with a barrier.
-__device__ __forceinline__ void make_plan(const PrefillArgs& a, Bars& B, int64_t* sums) {
+template <typename B_>
+__device__ __forceinline__ void make_plan(const PrefillArgs& a, B_& B, int64_t* sums) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kWarps = kThreads / 32;
     // Inclusive sum over the block; *all receives the total.
@@ -457,46 +453,1038 @@ __device__ __forceinline__ float element(const void* row, int i) {
     else return float(static_cast<const __nv_fp8_e4m3*>(row)[i]);
 }
 
-template <int KV, int D, bool TMA>
+// Ring unit u of the CTA's tile t: first those of K, then those of V.
+template <typename C>
+__device__ __forceinline__ int unit_of(int t, bool v, int u) {
+    return (2 * t + (v ? 1 : 0)) * C::kSubs + u;
+}
+// The barriers of K's units and of V's count those alone: loads may land in
+// another order than they were issued in, and a parity tells only neighbouring
+// phases apart, so who waits has to have seen the phase before.
+template <typename C>
+__device__ __forceinline__ int turn_of(int t, int u) {
+    return t * C::kSubs + u;
+}
+
+// What every role of the CTA knows.
+template <typename C>
+struct Cta {
+    const TcArgs& ta;
+    const PrefillArgs& a;
+    Bars<C>& B;
+    unsigned char* smem;
+    uint32_t sb, tmem;
+    __device__ __forceinline__ bool wait(uint64_t* bar, int phase) const {
+        return hs::mbar_wait_bounded(bar, uint32_t(phase & 1), ta.timeout_ns, &B.abort);
+    }
+    // By all lanes of a warp.
+    __device__ __forceinline__ bool wait_all(uint64_t* bar, int phase) const {
+        return __all_sync(0xffffffffu, wait(bar, phase));
+    }
+    // The product of query tile w's n-th P is done.
+    __device__ __forceinline__ bool pv_wait(int w, int n) const {
+        return C::NQ == 2 ? wait_all(&B.pv_done[w], n) : wait_all(&B.pv_done[n & 1], n >> 1);
+    }
+    __device__ __forceinline__ void give_up() const {
+        hs::set_status(a.status, HS_ERR_TIMEOUT);
+        B.abort = 1;
+    }
+};
+
+// -------------------------------- softmax ---------------------------------
+// A warpgroup per query tile, a thread per row.
+template <typename C>
+__device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
+    constexpr int NQ = C::NQ, NS = C::NS, kSubs = C::kSubs, KV = C::kKind, D = C::kD;
+    constexpr bool E4 = C::kE4;
+    const PrefillArgs& a = cx.a;
+    Bars<C>& B = cx.B;
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const uint32_t tmem = cx.tmem;
+    const int w = warp >> 2;   // query tile
+    const int r = tid & 127;   // row of the tile, and TMEM lane
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+    const int tok = r / a.group, hd = r - tok * a.group;  // its new token and query head
+    const uint32_t o_addr = tmem + lanes + C::kOCol + uint32_t(NQ == 2 ? w * 128 : 0);
+    bool ok = true;
+    int t = 0, mine = 0, units = 0;  // the CTA's tiles, this tile's, units with tiles
+    int own = 0;                     // and those with this query tile
+    bool head = false;               // the run ends in the first part of a shared unit
+    Seg s;
+    for (bool more = first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
+        const int n = s.i1 - s.i0;
+        const bool live = tok < a.tq && w * a.tq + tok < s.m;
+        const int64_t qh = int64_t(s.x.first + s.block * a.tb + w * a.tq + tok) * a.heads +
+                           s.kvh * a.group + hd;
+        if (n == 0) {
+            if (s.nt == 0 && s.begins && live) {
+                // Nothing is attended to: zeros.
+                for (int i = 0; i < D / 8; ++i)
+                    reinterpret_cast<uint4*>(a.out)[qh * (D / 8) + i] = make_uint4(0u, 0u, 0u, 0u);
+                if (a.lse != nullptr) a.lse[qh] = -CUDART_INF_F;
+            }
+            continue;
+        }
+        const bool whole = s.i0 == 0 && s.i1 == s.nt;
+        if (w == 0 && tid == 0 && !whole && s.i0 == 0) {
+            head = true;
+            SharedUnit u;
+            u.start = s.start;
+            u.per = B.per;
+            u.rest = B.rest;
+            u.cost = s.cost;
+            u.tiles = s.nt;
+            u.first = s.x.first + s.block * a.tb;
+            u.tokens = s.m;
+            u.kvh = s.kvh;
+            u.valid = 1;
+            a.shared[blockIdx.x] = u;
+        }
+        const int useg = units++;
+        if (w * a.tq >= s.m) {  // the second tile of a unit that has one
+            t += n;
+            continue;
+        }
+        // The row's position; rows without a query see what the last does.
+        const int pos = s.p0 + min(w * a.tq + tok, s.m - 1);
+        float scl = a.scale_log2;
+        float off = -CUDART_INF_F;      // reference - kShift
+        uint64_t l0 = 0, l1 = 0;        // sums, in pairs
+        bool first = true;
+        const int last = mine + n;
+        for (; mine < last; ++t, ++mine, first = false) {
+            const int x = NQ == 2 ? w : mine & 1;
+            const int ph = NQ == 2 ? mine : mine >> 1;
+            const uint32_t s_addr = tmem + lanes + uint32_t(NQ == 2 ? 0 : x * 128);
+            const uint32_t p_addr = NQ == 2 ? tmem + lanes + C::kPCol + uint32_t(w * 64) : s_addr;
+            ok = cx.wait_all(&B.s_full[x], ph);
+            if (!ok) break;
+            hs::tc::fence_after_sync();
+            float v[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, v + c * 32);
+            if (first) {
+                // (0 would turn masked places into NaN; 2^-126 does not show.)
+                if constexpr (E4) {
+                    scl *= pow2(-B.qexp[useg & (C::kSegRing - 1)][w * kTile + r]);
+                    if (a.k_scale != nullptr) scl *= a.k_scale[s.kvh];
+                }
+                if (scl == 0.f) scl = 1.17549435e-38f;
+            }
+            const bool part = B.tile[t & (C::kRing - 1)].y != 0;
+            const float as = fabsf(scl);
+            uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+            hs::tc::tmem_wait_ld();
+            if (NQ == 2) {
+                hs::tc::fence_before_sync();
+                hs::mbar_arrive(&B.s_free);
+            }
+            if (scl < 0.f) {
+#pragma unroll
+                for (int c = 0; c < 128; ++c) v[c] = -v[c];
+            }
+            if (part) {
+                // What this row sees of the tile.
+                const uint4 ld = *reinterpret_cast<const uint4*>(B.loaded[t & (C::kRing - 1)]);
+                const int t0 = B.tile[t & (C::kRing - 1)].x;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int b = t0 + 32 * j;
+                    const uint32_t lw = j == 0 ? ld.x : j == 1 ? ld.y : j == 2 ? ld.z : ld.w;
+                    vis[j] = low_bits(pos + 1 - b) & lw;
+                    if (a.window > 0)
+                        vis[j] &= ~low_bits(pos - a.window + 1 - b) | low_bits(a.sinks - b);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        if (!((vis[j] >> c) & 1u)) v[32 * j + c] = -CUDART_INF_F;
+                }
+            }
+            uint64_t as2, ref2, s0 = 0, s1 = 0;
+            const auto refer = [&] {
+                // Without a finite logit so far: subtract 0, every weight is
+                // 0 (a NaN logit stays NaN).
+                const float ref = off == -CUDART_INF_F ? 0.f : off;
+                as2 = pair_of(as, as);
+                ref2 = pair_of(-ref, -ref);
+            };
+            const auto weigh = [&](int c) {  // columns [32 c, 32 c + 32)
+                uint32_t pk[16];
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) {
+                    const int e = 32 * c + 2 * j;
+                    const float2 y = split(fma2(pair_of(v[e], v[e + 1]), as2, ref2));
+                    const float2 z = split(fma2(pair_of(v[e + 2], v[e + 3]), as2, ref2));
+                    const float2 p = make_float2(ex2(y.x), ex2(y.y)), q = make_float2(ex2(z.x), ex2(z.y));
+                    s0 = add2(s0, pair_of(p.x, p.y));
+                    s1 = add2(s1, pair_of(q.x, q.y));
+                    pk[j] = pack<KV>(p.x, p.y);
+                    pk[j + 1] = pack<KV>(q.x, q.y);
+                }
+                tmem_st16u(p_addr + c * 16, pk);
+            };
+            // The reference moves up to the maximum where that is far above;
+            // what has been summed is scaled down.
+            const auto raise = [&] {
+                float mx[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+                for (int c = 4; c < 124; c += 8)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mx[j] = max3(mx[j], v[c + 2 * j], v[c + 2 * j + 1]);
+                mx[0] = max3(mx[0], v[124], v[125]);
+                mx[1] = max3(mx[1], v[126], v[127]);
+                const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * as - C::kShift;
+                const bool grow = top > off + C::kThresh || (off == -CUDART_INF_F && top > off);
+                if (first) {
+                    if (grow) off = top;
+                    return false;
+                }
+                if (!__any_sync(0xffffffffu, grow)) return false;
+                const float to = grow ? top : off;
+                const float al = grow ? (off == -CUDART_INF_F ? 0.f : ex2(off - to)) : 1.f;
+                off = to;
+                l0 = fma2(l0, pair_of(al, al), 0);
+                l1 = fma2(l1, pair_of(al, al), 0);
+                if (NQ == 1) {
+                    ok = cx.pv_wait(w, mine - 1);
+                    hs::tc::fence_after_sync();
+                }
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                    float o[16];
+                    hs::tc::tmem_ld16(o_addr + uint32_t(c), o);
+                    hs::tc::tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) o[j] *= al;
+                    hs::tc::tmem_st16(o_addr + uint32_t(c), o);
+                }
+                return true;
+            };
+            // The products of the tile before have read P and are in O.
+            if (NQ == 2 && mine > 0) {
+                ok = cx.pv_wait(w, mine - 1);
+                hs::tc::fence_after_sync();
+            }
+            // Mostly the reference stays: the weights are made while the
+            // maximum is found, and the first half again where it moved.
+            const bool ahead = !part && !first && scl > 0.f;
+            if (!ahead) raise();
+            refer();
+            weigh(0);
+            weigh(1);
+            if (ahead && raise()) {
+                refer();
+                s0 = s1 = 0;
+                weigh(0);
+                weigh(1);
+            }
+            if (!ok) break;
+            weigh(2);
+            weigh(3);
+            l0 = add2(l0, s0);
+            l1 = add2(l1, s1);
+            hs::tc::tmem_wait_st();
+            if (part) {
+                // Rows of V that were taken out.
+                uint32_t any = 0;
+                for (int u = 0; u < kSubs && ok; ++u) {
+                    const int q = turn_of<C>(t, u);
+                    ok = cx.wait_all(&B.ready[q % NS], q / NS);
+                    const uint4 o = *reinterpret_cast<const uint4*>(B.odd[t & (C::kRing - 1)][u]);
+                    any |= o.x | o.y | o.z | o.w;
+                }
+                if (!ok) break;
+                if (first) B.keep[w] = any != 0;
+                if (any != 0) {
+                    if (NQ == 1 && !first) {
+                        ok = cx.pv_wait(w, mine - 1);
+                        if (!ok) break;
+                        hs::tc::fence_after_sync();
+                    }
+                    // (The output before has been read.)
+                    if (first && own > 0) ok = cx.wait_all(&B.o_free[w], own - 1);
+                    if (!ok) break;
+                    hs::tc::fence_after_sync();
+                    const float zero[16] = {};
+                    if (first)
+                        for (int c = 0; c < D; c += 16) hs::tc::tmem_st16(o_addr + uint32_t(c), zero);
+                    hs::tc::tmem_wait_st();
+                    for (int j = 0; j < kTile; ++j) {
+                        const uint32_t pw = tmem_ld1(p_addr + uint32_t(j >> 1));
+                        hs::tc::tmem_wait_ld();
+                        const uint32_t h = (j & 1) ? pw >> 16 : pw & 0xffffu;
+                        const float p = KV == kBf16 ? __uint_as_float(h << 16)
+                                                    : __half2float(__ushort_as_half(uint16_t(h)));
+                        const uint32_t vw = j < 32 ? vis[0] : j < 64 ? vis[1] : j < 96 ? vis[2] : vis[3];
+                        const bool sees = (vw >> (j & 31)) & 1u;
+                        for (int u = 0; u < kSubs; ++u) {
+                            if (!((B.odd[t & (C::kRing - 1)][u][j >> 5] >> (j & 31)) & 1u)) continue;
+                            const int tk = B.tile[t & (C::kRing - 1)].x + j, b = block_of(a, tk);
+                            const int64_t page = a.block_table[s.row * a.bt_stride + b];
+                            const void* row = static_cast<const char*>(a.v) +
+                                (page * a.page_stride + int64_t(tk - b * a.page_size) * a.row_stride +
+                                 s.kvh * a.head_stride) * (E4 ? 1 : 2);
+                            for (int c = u * C::kDims; c < (u + 1) * C::kDims; c += 16) {
+                                float o[16];
+                                hs::tc::tmem_ld16(o_addr + uint32_t(c), o);
+                                hs::tc::tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    if (sees) o[e] = fmaf(p, element<KV>(row, c + e), o[e]);
+                                hs::tc::tmem_st16(o_addr + uint32_t(c), o);
+                                hs::tc::tmem_wait_st();
+                            }
+                        }
+                    }
+                }
+            } else if (first) {
+                B.keep[w] = 0;
+            }
+            hs::tc::fence_before_sync();
+            hs::mbar_arrive(&B.p_full[x]);
+        }
+        if (!ok) break;
+        // ---- The unit's state: its output is written by another warpgroup ----
+        if (own > 0) ok = cx.wait_all(&B.o_free[w], own - 1);
+        if (!ok) break;
+        ++own;
+        const float2 ls = split(add2(l0, l1));
+        const float l = ls.x + ls.y;
+        float f = 1.f;
+        if (whole) {
+            f = l == 0.f ? 0.f : 1.f / l;
+            if (a.v_scale != nullptr && l != 0.f) f *= a.v_scale[s.kvh];
+            if (live && a.lse != nullptr)
+                a.lse[qh] = l == 0.f ? -CUDART_INF_F : (off + log2f(l)) * kLn2;
+        } else if (live) {
+            const int64_t slot = 2 * int(blockIdx.x) + (s.start < B.place0 ? 0 : 1);
+            reinterpret_cast<float2*>(a.part_ml)[slot * a.unit_rows + w * kTile + r] =
+                make_float2(off, l);
+        }
+        B.factor[w][r] = f;
+        hs::mbar_arrive(&B.l_full[w]);
+    }
+    if (!ok) cx.give_up();
+    if (tid == 0 && !head) a.shared[blockIdx.x].valid = 0;
+}
+
+// -------------------------------- products --------------------------------
+// Products and commits are the bound of a warp that issues them all (3600 cycles
+// for a pair of tiles whose products take 2048): one issues QK, one PV.  Two
+// query tiles share S, whose softmax begins by taking it into registers, and
+// have a P each: the QK of one runs ahead of the PV of the other, and a tile has
+// the time of both tiles' products for its softmax.  (With S and P of a tile in
+// the same columns QK has to wait for PV and the softmax is on the products'
+// path.)
+template <typename C>
+__device__ __forceinline__ bool qk_role(const Cta<C>& cx) {
+    constexpr int NQ = C::NQ, NS = C::NS, kSubs = C::kSubs, KV = C::kKind;
+    const PrefillArgs& a = cx.a;
+    Bars<C>& B = cx.B;
+    const uint32_t tmem = cx.tmem, sb = cx.sb;
+    bool ok = true;
+    Seg s;
+    constexpr uint32_t id = idesc<KV>(kTile, 0);
+    const uint64_t q_desc = hs::tc::sdesc_sw128(sb, 16, 1024);
+    const uint64_t k_desc = hs::tc::sdesc_sw128(sb + C::kRingOff, 16, 1024);
+    int t = 0, segs = 0, n_qk = 0;
+    for (bool more = first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
+        const int n = s.i1 - s.i0;
+        if (n == 0) continue;
+        const int tiles = NQ == 2 && a.tq < s.m ? 2 : 1;
+        ok = ok && cx.wait_all(&B.q_full, segs++);
+        for (int i = 0; i < n && ok; ++i, ++t) {
+            uint32_t at[kSubs];
+#pragma unroll
+            for (int u = 0; u < kSubs; ++u) {
+                const int q = turn_of<C>(t, u);
+                at[u] = uint32_t(unit_of<C>(t, false, u) % NS * (C::kUnit >> 4));
+                ok = ok && cx.wait_all(&B.kfull[q % NS], q / NS);
+            }
+            for (int w = 0; w < tiles; ++w, ++n_qk) {
+                const int x = NQ == 2 ? 0 : t & 1;
+                // The last softmax has taken S, or the last product of
+                // this buffer's P is done.
+                if (NQ == 2) {
+                    if (n_qk > 0) ok = ok && cx.wait_all(&B.s_free, n_qk - 1);
+                } else if (t >= 2) {
+                    ok = ok && cx.wait_all(&B.pv_done[x], (t - 2) >> 1);
+                }
+                hs::tc::fence_after_sync();
+                if (!ok) break;
+#pragma unroll
+                for (int u = 0; u < kSubs; ++u)
+#pragma unroll
+                    for (int b = 0; b < C::kDims / 64; ++b)
+                        mma_ss4(tmem + uint32_t(x * 128),
+                                q_desc + uint32_t(w * (C::kQTile >> 4) +
+                                                  (u * (C::kDims / 64) + b) * (kBlk >> 4)),
+                                k_desc + at[u] + uint32_t(b * (kBlk >> 4)), id,
+                                (u | b) ? 1u : 0u);
+                commit(&B.s_full[NQ == 2 ? w : x]);
+            }
+            if (!ok) break;
+#pragma unroll
+            for (int u = 0; u < kSubs; ++u) commit(&B.empty[unit_of<C>(t, false, u) % NS]);
+            if (i + 1 == n) commit(&B.q_empty);
+        }
+    }
+    return ok;
+}
+template <typename C>
+__device__ __forceinline__ bool pv_role(const Cta<C>& cx) {
+    constexpr int NQ = C::NQ, NS = C::NS, kSubs = C::kSubs, KV = C::kKind;
+    const PrefillArgs& a = cx.a;
+    Bars<C>& B = cx.B;
+    const uint32_t tmem = cx.tmem, sb = cx.sb;
+    bool ok = true;
+    Seg s;
+    constexpr uint32_t id = idesc<KV>(C::kDims, 1);
+    const uint64_t v_desc = hs::tc::sdesc_sw128(sb + C::kRingOff, kBlk, 1024);
+    int t = 0, done0 = 0, done1 = 0, had0 = 0, had1 = 0;
+    for (bool more = first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
+        const int n = s.i1 - s.i0;
+        if (n == 0) continue;
+        const int tiles = NQ == 2 && a.tq < s.m ? 2 : 1;
+        // The outputs before have been read.
+        if (had0 > 0) ok = ok && cx.wait_all(&B.o_free[0], had0 - 1);
+        if (tiles == 2 && had1 > 0) ok = ok && cx.wait_all(&B.o_free[1], had1 - 1);
+        ++had0;
+        if (tiles == 2) ++had1;
+        for (int i = 0; i < n && ok; ++i, ++t) {
+            uint32_t at[kSubs];
+#pragma unroll
+            for (int u = 0; u < kSubs; ++u) {
+                const int q = turn_of<C>(t, u);
+                at[u] = uint32_t(unit_of<C>(t, true, u) % NS * (C::kUnit >> 4));
+                ok = ok && cx.wait_all(&B.ready[q % NS], q / NS);
+            }
+            for (int w = 0; w < tiles; ++w) {
+                const int x = NQ == 2 ? w : t & 1;
+                ok = ok && cx.wait_all(&B.p_full[x], NQ == 2 ? (w == 0 ? done0 : done1) : t >> 1);
+                hs::tc::fence_after_sync();
+                if (!ok) break;
+                const bool fresh = i == 0 && B.keep[w] == 0;
+                const uint32_t p_col =
+                    tmem + (NQ == 2 ? C::kPCol + uint32_t(w * 64) : uint32_t(x * 128));
+#pragma unroll
+                for (int u = 0; u < kSubs; ++u)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        mma_ts4(tmem + C::kOCol + uint32_t((w + u) * 128), p_col + uint32_t(h * 32),
+                                v_desc + at[u] + uint32_t(h * 512), id,
+                                fresh && h == 0 ? 0u : 1u);
+                commit(&B.pv_done[x]);
+                if (w == 0) ++done0;
+                else ++done1;
+            }
+            if (!ok) break;
+#pragma unroll
+            for (int u = 0; u < kSubs; ++u) commit(&B.empty[unit_of<C>(t, true, u) % NS]);
+        }
+    }
+    return ok;
+}
+
+// ------------------------------ loads by TMA ------------------------------
+// One warp: the queries of each unit (E4M3: made by the converting threads),
+// then the K and V units of its tiles, a lane per run of tokens in one page.
+template <typename C>
+__device__ __forceinline__ bool tma_role(const Cta<C>& cx, const CUtensorMap& qmap,
+                                         const CUtensorMap& kmap, const CUtensorMap& vmap) {
+    constexpr int kSubs = C::kSubs;
+    const PrefillArgs& a = cx.a;
+    Bars<C>& B = cx.B;
+    const int lane = threadIdx.x & 31, bt = cx.ta.bt;
+    const int runs = kTile / bt;  // a power of two up to 8
+    constexpr int kBoxes = C::kConvert ? 1 : C::kDims / 64;
+    const uint32_t row_bytes = C::kConvert ? C::kDims : 128;
+    const uint32_t box = uint32_t(bt) * row_bytes;
+    const uint32_t q_bytes = uint32_t(a.tq * a.group) * 128u * (C::kD / 64);
+    bool ok = true, bad = false;
+    int t = 0, seq = 0, segs = 0;
+    Seg s;
+    for (bool more = first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
+        if (s.i1 == s.i0) continue;
+        if constexpr (!C::kConvert) {
+            // A box takes the heads of a KV head for a tile's tokens: its rows are
+            // the tile's.  (Tokens of other requests behind a unit's own land in
+            // rows that are not written.)
+            if (segs > 0) ok = cx.wait_all(&B.q_empty, segs - 1);
+            if (!ok) break;
+            ++segs;
+            if (lane == 0) {
+                const int tiles = C::NQ == 2 && s.m > a.tq ? 2 : 1;
+                hs::mbar_arrive_expect_tx(&B.q_full, q_bytes * tiles);
+                for (int w = 0; w < tiles; ++w)
+                    for (int c = 0; c < C::kD / 64; ++c)
+                        tma_load_q(cx.sb + w * C::kQTile + c * kBlk, &qmap, c * 64, s.kvh * a.group,
+                                   s.x.first + s.block * a.tb + w * a.tq, &B.q_full);
+            }
+            __syncwarp();
+        }
+        for (int i = s.i0; i < s.i1 && ok; ++i, ++t) {
+            const int t0 = token_of(s, i), tok = t0 + lane * bt;
+            const int b = block_of(a, tok);
+            const bool wants = lane < runs && any_sees(a, s, tok, bt);
+            const int page = wants ? a.block_table[s.row * a.bt_stride + b] : -1;
+            const bool want = wants && page >= 0 && page < a.num_pages;
+            if (wants && !want) bad = true;
+            const uint32_t got = __ballot_sync(0xffffffffu, want);
+            // (Read by the softmax of this tile, which the ring's units keep less
+            // than kRing tiles behind.)
+            if (lane < 4) {
+                uint32_t bits = 0;
+                if (bt >= 32) {
+                    bits = (got >> (lane * 32 / bt)) & 1u ? 0xffffffffu : 0u;
+                } else {  // 16
+                    if ((got >> (2 * lane)) & 1u) bits |= 0xffffu;
+                    if ((got >> (2 * lane + 1)) & 1u) bits |= 0xffff0000u;
+                }
+                B.loaded[t & (C::kRing - 1)][lane] = bits;
+            }
+            if (lane == 4)
+                B.tile[t & (C::kRing - 1)] = make_int2(t0, !all_see(a, s, t0) || got != low_bits(runs));
+            __syncwarp();
+            const uint32_t bytes = uint32_t(__popc(got)) * box * kBoxes;
+            const int at = tok - b * a.page_size;
+            for (int u = 0; u < 2 * kSubs; ++u, ++seq) {
+                uint64_t* full;
+                uint32_t dst;
+                if constexpr (C::kConvert) {
+                    const int slot = seq % C::kStages;
+                    ok = cx.wait_all(&B.sempty[slot], seq / C::kStages + 1);
+                    full = &B.sfull[slot];
+                    dst = cx.sb + C::kStageOff + slot * C::kStage;
+                } else {
+                    const int slot = seq % C::NS, turn = turn_of<C>(t, u % kSubs) % C::NS;
+                    ok = cx.wait_all(&B.empty[slot], seq / C::NS + 1);
+                    full = u < kSubs ? &B.kfull[turn] : &B.vfull[turn];
+                    dst = cx.sb + C::kRingOff + slot * C::kUnit;
+                }
+                if (!ok) break;
+                if (lane == 0) hs::mbar_arrive_expect_tx(full, bytes);
+                __syncwarp();
+                if (want) {
+#pragma unroll
+                    for (int c = 0; c < kBoxes; ++c)
+                        tma_load(dst + lane * box + c * kBlk, u < kSubs ? &kmap : &vmap,
+                                 u % kSubs * C::kDims + c * 64, at, s.kvh, page, full);
+                }
+            }
+        }
+    }
+    // No copy may outlive the CTA (where all went well each has been waited for).
+    if (!ok) {
+        if constexpr (C::kConvert) {
+            for (int q = max(0, seq - C::kStages); q < seq; ++q)
+                hs::mbar_wait_bounded(&B.sfull[q % C::kStages], (q / C::kStages) & 1,
+                                      cx.ta.timeout_ns, nullptr);
+        } else {
+            if (segs > 0)
+                hs::mbar_wait_bounded(&B.q_full, (segs - 1) & 1, cx.ta.timeout_ns, nullptr);
+            for (int q = max(0, seq - C::NS); q < seq; ++q) {
+                const int u = q % (2 * kSubs), turn = turn_of<C>(q / (2 * kSubs), u % kSubs);
+                hs::mbar_wait_bounded(u < kSubs ? &B.kfull[turn % C::NS] : &B.vfull[turn % C::NS],
+                                      (turn / C::NS) & 1, cx.ta.timeout_ns, nullptr);
+            }
+        }
+    }
+    if (bad) hs::set_status(a.status, HS_ERR_BAD_INDEX);
+    return ok;
+}
+
+// --------------------------- queries by threads ---------------------------
+// The rows of a unit's queries, by THREADS threads (whole warps): 16-bit ones
+// copied, those of E4M3 caches made fp16.
+template <typename C, int THREADS>
+__device__ __forceinline__ void load_queries(const Cta<C>& cx, const Seg& s, int ti, int slot) {
+    constexpr int D = C::kD;
+    const PrefillArgs& a = cx.a;
+    const int lane = ti & 31;
+    constexpr int kCh = D / 8;  // 16-byte chunks of a row: a lane each
+    constexpr int kRowStep = THREADS / kCh;
+    const int ch = lane % kCh, row0 = ti / 32 * (32 / kCh) + lane / kCh;
+    // Token and head of a row without a division each.
+    const int hstep = kRowStep % a.group, tstep = kRowStep / a.group;
+    const int tok0 = row0 / a.group, hd0 = row0 - tok0 * a.group;
+    const char* q = static_cast<const char*>(a.q) +
+                    ((s.x.first + s.block * a.tb) * a.q_stride + int64_t(s.kvh) * a.group * D + ch * 8) * 2;
+#pragma unroll 1
+    for (int w = 0; w < C::NQ; ++w) {
+        int tok = tok0, hd = hd0;
+#pragma unroll 4
+        for (int r = row0; r < kTile; r += kRowStep) {
+            const bool in = tok < a.tq && w * a.tq + tok < s.m;
+            const int64_t at = in ? (w * a.tq + tok) * a.q_stride + hd * D : 0;
+            const uint32_t dst = w * C::kQTile + (ch >> 3) * kBlk + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+            if constexpr (!C::kE4) {
+                hs::tc::cp_async16(cx.sb + dst, q + at * 2, in ? 16u : 0u);
+            } else {
+                uint4 raw = in ? *reinterpret_cast<const uint4*>(q + at * 2) : make_uint4(0u, 0u, 0u, 0u);
+                int e = 0;
+                if (!a.q_is_half) {
+                    uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+                    float f[8], mx = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u[i]));
+                        f[2 * i] = y.x;
+                        f[2 * i + 1] = y.y;
+                        mx = fmaxf(mx, fmaxf(fabsf(y.x), fabsf(y.y)));
+                    }
+#pragma unroll
+                    for (int o = kCh / 2; o > 0; o >>= 1)
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    // Largest magnitude to [2^14, 2^15) (rows below 2^-112 not as
+                    // far).
+                    if (mx > 0.f && mx < CUDART_INF_F)
+                        e = min(14 - (int(__float_as_uint(mx) >> 23) - 127), 126);
+                    const float up = pow2(e);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) u[i] = pack<kFp16>(f[2 * i] * up, f[2 * i + 1] * up);
+                    raw = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+                *reinterpret_cast<uint4*>(cx.smem + dst) = raw;
+                if (ch == 0) cx.B.qexp[slot & (C::kSegRing - 1)][w * kTile + r] = int8_t(e);
+            }
+            hd += hstep;
+            tok += tstep;
+            if (hd >= a.group) {
+                hd -= a.group;
+                ++tok;
+            }
+        }
+    }
+    if constexpr (!C::kE4) hs::tc::cp_async_wait_all();
+    hs::fence_proxy_async_shared();
+    hs::mbar_arrive(&cx.B.q_full);
+}
+template <typename C>
+__device__ __forceinline__ bool query_role(const Cta<C>& cx) {
+    const int ti = threadIdx.x - kTmaWarp * 32;
+    int segs = 0;
+    Seg s;
+    for (bool more = first_seg(cx.a, cx.B, s); more; more = next_seg(cx.a, cx.B, s)) {
+        if (s.i1 == s.i0) continue;
+        if (segs > 0 && !cx.wait_all(&cx.B.q_empty, segs - 1)) return false;
+        load_queries<C, kQThreads>(cx, s, ti, segs++);
+    }
+    return true;
+}
+
+// --------------------------------- output ---------------------------------
+// The fourth warpgroup writes a unit's output (or partial state) while the
+// softmax is at the next unit's tiles.
+struct Written {
+    int n = 0;              // tiles of the unit; 0: none to write
+    int tiles, m, kvh;      // query tiles, tokens
+    int64_t first, slot;    // first token; slot of the partial state, -1: whole
+    int units[2] = {0, 0}, products[2] = {0, 0};  // of each query tile, up to this unit
+};
+__device__ __forceinline__ Written unit_to_write(const PrefillArgs& a, const Seg& s, int64_t place0,
+                                                 int tiles, const Written& before) {
+    Written d = before;
+    d.n = s.i1 - s.i0;
+    d.tiles = tiles;
+    d.m = s.m;
+    d.kvh = s.kvh;
+    d.first = s.x.first + s.block * a.tb;
+    d.slot = s.i0 == 0 && s.i1 == s.nt ? -1 : 2 * int(blockIdx.x) + (s.start < place0 ? 0 : 1);
+    for (int w = 0; w < 2; ++w)
+        if (w < tiles) {
+            ++d.units[w];
+            d.products[w] += d.n;
+        }
+    return d;
+}
+template <typename C>
+__device__ __forceinline__ bool write_unit(const Cta<C>& cx, const Written& d) {
+    constexpr int D = C::kD;
+    const PrefillArgs& a = cx.a;
+    Bars<C>& B = cx.B;
+    const int r = threadIdx.x & 127;
+    const uint32_t lanes = uint32_t((r >> 5) * 32) << 16;
+    const int tok = r / a.group, hd = r - tok * a.group;
+    const bool bf = C::kKind == kBf16 || (C::kE4 && !a.q_is_half);
+#pragma unroll 1
+    for (int w = 0; w < d.tiles; ++w) {
+        if (!cx.wait_all(&B.l_full[w], d.units[w] - 1) || !cx.pv_wait(w, d.products[w] - 1))
+            return false;
+        hs::tc::fence_after_sync();
+        const uint32_t o_addr = cx.tmem + lanes + C::kOCol + uint32_t(w * 128);
+        const bool live = tok < a.tq && w * a.tq + tok < d.m;
+        const float f = B.factor[w][r];
+        const int64_t qh = (d.first + w * a.tq + tok) * a.heads + d.kvh * a.group + hd;
+        uint16_t* to = static_cast<uint16_t*>(a.out) + qh * D;
+        float* po = a.part_o + ((d.slot * (D / 8)) * a.unit_rows + w * kTile + r) * 8;
+        // A row per thread: 32 bytes of each of 32 rows at a time.  (Pieces
+        // exchanged between lanes for whole lines: five times as long.)
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(o_addr + uint32_t(c), o);
+            hs::tc::tmem_wait_ld();
+            if (c + 32 == D) {
+                hs::tc::fence_before_sync();
+                hs::mbar_arrive(&B.o_free[w]);
+            }
+            if (!live) continue;
+            if (d.slot >= 0) {
+#pragma unroll
+                for (int j = 0; j < 32; j += 8) {
+                    uint32_t y[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = __float_as_uint(o[j + e]);
+                    store32(po + int64_t((c + j) / 8) * a.unit_rows * 8, y);
+                }
+                continue;
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = f == 0.f ? 0.f : o[j] * f;
+#pragma unroll
+            for (int j = 0; j < 32; j += 16) {
+                uint32_t y[8];
+                if (bf) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = pack<kBf16>(o[j + 2 * e], o[j + 2 * e + 1]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = pack<kFp16>(o[j + 2 * e], o[j + 2 * e + 1]);
+                }
+                if (a.out_wide) {
+                    store32(to + c + j, y);
+                } else {
+                    reinterpret_cast<uint4*>(to + c + j)[0] = make_uint4(y[0], y[1], y[2], y[3]);
+                    reinterpret_cast<uint4*>(to + c + j)[1] = make_uint4(y[4], y[5], y[6], y[7]);
+                }
+            }
+        }
+    }
+    return true;
+}
+
+// ------------------------------- rows of V --------------------------------
+// 16-bit caches by TMA: V's units pass through here, for the rows that have to
+// be cleared.
+template <typename C>
+__device__ __forceinline__ bool check_role(const Cta<C>& cx) {
+    constexpr int NS = C::NS;
+    const PrefillArgs& a = cx.a;
+    Bars<C>& B = cx.B;
+    const int lane = threadIdx.x & 31, j = (threadIdx.x >> 5) & 3;
+    bool ok = true;
+    int t = 0;
+    Written done;
+    Seg s;
+    for (bool more = first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
+        if (s.i1 == s.i0) continue;
+        for (int i = s.i0; i < s.i1 && ok; ++i, ++t) {
+            for (int u = 0; u < C::kSubs; ++u) {
+                const int q = unit_of<C>(t, true, u), turn = turn_of<C>(t, u);
+                ok = cx.wait_all(&B.vfull[turn % NS], turn / NS);
+                if (!ok) break;
+                const int2 tile = B.tile[t & (C::kRing - 1)];
+                if (tile.y != 0) {
+                    const int r = j * 32 + lane;
+                    const bool in = any_sees(a, s, tile.x + r) &&
+                                    ((B.loaded[t & (C::kRing - 1)][j] >> lane) & 1u);
+                    unsigned char* row = cx.smem + C::kRingOff + q % NS * C::kUnit + r * 128;
+                    bool odd = false;
+                    if (in)
+                        for (int c = 0; c < C::kDims / 8; ++c)
+                            odd |= not_finite<C::kKind>(*reinterpret_cast<const uint4*>(
+                                row + (c >> 3) * kBlk + (((c + lane) & 7) << 4)));
+                    const uint32_t all = __ballot_sync(0xffffffffu, odd);
+                    if (lane == 0) B.odd[t & (C::kRing - 1)][u][j] = all;
+                    if (!in || odd)
+                        for (int c = 0; c < C::kDims / 8; ++c)
+                            *reinterpret_cast<uint4*>(row + (c >> 3) * kBlk + (((c + lane) & 7) << 4)) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                    hs::fence_proxy_async_shared();
+                }
+                __syncwarp();
+                if (lane == 0) hs::mbar_arrive(&B.ready[turn % NS]);
+            }
+            // The unit before, while this one's first tile is in its softmax.
+            if (ok && i == s.i0 && done.n > 0) ok = write_unit(cx, done);
+        }
+        done = unit_to_write(a, s, B.place0, C::NQ == 2 && a.tq < s.m ? 2 : 1, done);
+    }
+    return ok && (done.n == 0 || write_unit(cx, done));
+}
+
+// Two 16-byte chunks of fp16 from 16 E4M3 codes.
+__device__ __forceinline__ void widen_codes(const uint4& x, uint4& y, uint4& z) {
+    y.x = e4m3x2_to_half2(x.x & 0xffffu);
+    y.y = e4m3x2_to_half2(x.x >> 16);
+    y.z = e4m3x2_to_half2(x.y & 0xffffu);
+    y.w = e4m3x2_to_half2(x.y >> 16);
+    z.x = e4m3x2_to_half2(x.z & 0xffffu);
+    z.y = e4m3x2_to_half2(x.z >> 16);
+    z.z = e4m3x2_to_half2(x.w & 0xffffu);
+    z.w = e4m3x2_to_half2(x.w >> 16);
+}
+// Lanes of a warp that hold the chunks of this lane's row.
+template <int CHUNKS>
+__device__ __forceinline__ uint32_t row_lanes(int lane) {
+    return CHUNKS >= 32 ? 0xffffffffu : ((1u << (CHUNKS & 31)) - 1u) << (lane / CHUNKS * CHUNKS);
+}
+
+// E4M3 caches by TMA: units from the stage to the ring as fp16.
+template <typename C>
+__device__ __forceinline__ bool convert_role(const Cta<C>& cx) {
+    constexpr int NS = C::NS, kCh = C::kDims / 16, kStep = kTile / kCh;  // chunks of a row, rows of a pass
+    const PrefillArgs& a = cx.a;
+    Bars<C>& B = cx.B;
+    const int lt = threadIdx.x & 127, lane = lt & 31, ch = lt % kCh, r0 = lt / kCh;
+    // Its two 16-byte chunks of fp16; half the lanes begin with the second one, for
+    // the banks.
+    const int c0 = 2 * ch + (ch >= 4 ? 1 : 0), c1 = 2 * ch + (ch >= 4 ? 0 : 1);
+    bool ok = true;
+    int t = 0, seq = 0, segs = 0;
+    Written done;
+    Seg s;
+    for (bool more = first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
+        if (s.i1 == s.i0) continue;
+        if (segs > 0) ok = cx.wait_all(&B.q_empty, segs - 1);
+        if (!ok) break;
+        load_queries<C, 128>(cx, s, lt, segs++);
+        for (int i = s.i0; i < s.i1 && ok; ++i, ++t) {
+            for (int u = 0; u < 2 * C::kSubs; ++u, ++seq) {
+                const bool v = u >= C::kSubs;
+                const int turn = turn_of<C>(t, u % C::kSubs), slot = seq % NS;
+                ok = cx.wait_all(&B.sfull[seq % C::kStages], seq / C::kStages) &&
+                     cx.wait_all(&B.empty[slot], seq / NS + 1);
+                if (!ok) break;
+                const unsigned char* from = cx.smem + C::kStageOff + seq % C::kStages * C::kStage + lt * 16;
+                unsigned char* to = cx.smem + C::kRingOff + slot * C::kUnit;
+                const int2 tile = B.tile[t & (C::kRing - 1)];
+                uint4 x[kCh];
+#pragma unroll
+                for (int p = 0; p < kCh; ++p)
+                    x[p] = *reinterpret_cast<const uint4*>(from + p * kStep * C::kDims);
+                hs::mbar_arrive(&B.sempty[seq % C::kStages]);
+                if (v && tile.y != 0) {
+                    // A warp has kStep / 4 rows of a pass.
+                    uint32_t odd[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                    for (int p = 0; p < kCh; ++p) {
+                        const int r = p * kStep + r0;
+                        const bool in = any_sees(a, s, tile.x + r) &&
+                                        ((B.loaded[t & (C::kRing - 1)][r >> 5] >> (r & 31)) & 1u);
+                        const uint32_t bad = __ballot_sync(0xffffffffu, in && not_finite<kE4m3>(x[p]));
+                        const bool out = (bad & row_lanes<kCh>(lane)) != 0;
+                        if (!in || out) x[p] = make_uint4(0u, 0u, 0u, 0u);
+                        if (out && ch == 0) odd[p * kStep >> 5] |= 1u << (r & 31);
+                    }
+                    // (Cleared two tiles ahead, below: the warps are at most two
+                    // units apart.)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const uint32_t all = __reduce_or_sync(0xffffffffu, odd[g]);
+                        if (lane == 0 && all != 0) atomicOr(&B.odd[t & (C::kRing - 1)][u - C::kSubs][g], all);
+                    }
+                }
+                if (u == C::kSubs && lt < 4 * C::kSubs)
+                    B.odd[(t + 2) & (C::kRing - 1)][lt >> 2][lt & 3] = 0;
+#pragma unroll
+                for (int p = 0; p < kCh; ++p) {
+                    const int r = p * kStep + r0;
+                    uint4 y, z;
+                    widen_codes(x[p], y, z);
+                    unsigned char* row = to + r * 128;
+                    *reinterpret_cast<uint4*>(row + (c0 >> 3) * kBlk + (((c0 & 7) ^ (r & 7)) << 4)) = ch >= 4 ? z : y;
+                    *reinterpret_cast<uint4*>(row + (c1 >> 3) * kBlk + (((c1 & 7) ^ (r & 7)) << 4)) = ch >= 4 ? y : z;
+                }
+                hs::fence_proxy_async_shared();
+                hs::mbar_arrive(v ? &B.ready[turn % NS] : &B.kfull[turn % NS]);
+            }
+            if (ok && i == s.i0 && done.n > 0) ok = write_unit(cx, done);
+        }
+        done = unit_to_write(a, s, B.place0, C::NQ == 2 && a.tq < s.m ? 2 : 1, done);
+    }
+    return ok && (done.n == 0 || write_unit(cx, done));
+}
+
+// Loads by 128 threads: pages without runs of 16 tokens, broadcast strides.
+template <typename C>
+__device__ __forceinline__ bool load_role(const Cta<C>& cx) {
+    constexpr bool E4 = C::kE4;
+    constexpr int D = C::kD;
+    const PrefillArgs& a = cx.a;
+    Bars<C>& B = cx.B;
+    unsigned char* smem = cx.smem;
+    const int lt = threadIdx.x & 127, lane = lt & 31;
+    Seg s;
+    constexpr int kElt = E4 ? 1 : 2, kPer = 16 / kElt;  // elements of 16 bytes
+    constexpr int kCh = D / kPer;                       // 16-byte chunks of a row
+    constexpr int kStep = kTile / kCh;                  // rows of a pass
+    constexpr int kPass = kCh < 8 ? kCh : 8;            // passes of a batch
+    constexpr int kBatch = kPass * kStep, kBatches = kTile / kBatch;
+    const int ch = lt % kCh, r0 = lt / kCh;
+    bool ok = true, bad = false;
+    int t = 0;
+    uint4 buf[2][kPass];
+    const auto rows_of = [&](int t, int i) {
+        // Row lt of the tile: where it lies in the cache.
+        const int tok = token_of(s, i) + lt, b = block_of(a, tok);
+        int64_t at = -1;
+        if (any_sees(a, s, tok)) {
+            const int64_t page = a.block_table[s.row * a.bt_stride + b];
+            if (page >= 0 && page < a.num_pages)
+                at = page * a.page_stride + int64_t(tok - b * a.page_size) * a.row_stride +
+                     s.kvh * a.head_stride;
+            else
+                bad = true;
+        }
+        B.offset[t & 1][lt] = at;
+        const uint32_t got = __ballot_sync(0xffffffffu, at >= 0);
+        if (lane == 0) {
+            B.loaded[t & (C::kRing - 1)][lt >> 5] = got;
+            for (int u = 0; u < C::kSubs; ++u) B.odd[t & (C::kRing - 1)][u][lt >> 5] = 0;
+        }
+        hs::pair::named_sync(kLoadBar, kTile);
+    };
+    const auto load = [&](int t, bool v, int batch, uint4 (&x)[kPass]) {
+        const char* base = static_cast<const char*>(v ? a.v : a.k) + ch * 16;
+#pragma unroll
+        for (int j = 0; j < kPass; ++j) {
+            const int64_t at = B.offset[t & 1][batch * kBatch + j * kStep + r0];
+            x[j] = at >= 0 ? *reinterpret_cast<const uint4*>(base + at * kElt)
+                           : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    const auto store = [&](int t, bool v, int batch, uint4 (&x)[kPass], bool part) {
+#pragma unroll
+        for (int j = 0; j < kPass; ++j) {
+            const int r = batch * kBatch + j * kStep + r0;
+            if (v && part) {
+                // A row's chunks lie in neighbouring lanes of one warp.
+                const uint32_t odd = __ballot_sync(0xffffffffu, not_finite<C::kKind>(x[j]));
+                const uint32_t mine = (kCh == 32 ? 0xffffffffu : ((1u << (kCh & 31)) - 1u) << (lane / kCh * kCh));
+                if (odd & mine) {
+                    x[j] = make_uint4(0u, 0u, 0u, 0u);
+                    if (ch == 0)
+                        for (int u = 0; u < C::kSubs; ++u)
+                            atomicOr(&B.odd[t & (C::kRing - 1)][u][r >> 5], 1u << (r & 31));
+                }
+            }
+            const int c0 = E4 ? 2 * ch : ch;  // its first chunk of eight 16-bit elements
+            const int u = c0 * 8 / C::kDims, cb = c0 - u * (C::kDims / 8);
+            unsigned char* dst = smem + C::kRingOff + unit_of<C>(t, v, u) % C::NS * C::kUnit +
+                                 (cb >> 3) * kBlk + r * 128;
+            if constexpr (E4) {
+                uint4 y, z;
+                y.x = e4m3x2_to_half2(x[j].x & 0xffffu);
+                y.y = e4m3x2_to_half2(x[j].x >> 16);
+                y.z = e4m3x2_to_half2(x[j].y & 0xffffu);
+                y.w = e4m3x2_to_half2(x[j].y >> 16);
+                z.x = e4m3x2_to_half2(x[j].z & 0xffffu);
+                z.y = e4m3x2_to_half2(x[j].z >> 16);
+                z.z = e4m3x2_to_half2(x[j].w & 0xffffu);
+                z.w = e4m3x2_to_half2(x[j].w >> 16);
+                *reinterpret_cast<uint4*>(dst + (((cb & 7) ^ (r & 7)) << 4)) = y;
+                *reinterpret_cast<uint4*>(dst + ((((cb & 7) + 1) ^ (r & 7)) << 4)) = z;
+            } else {
+                *reinterpret_cast<uint4*>(dst + (((cb & 7) ^ (r & 7)) << 4)) = x[j];
+            }
+        }
+    };
+    const auto wait_empty = [&](int t, bool v) {
+        bool fine = ok;
+        for (int u = 0; u < C::kSubs; ++u) {
+            const int q = unit_of<C>(t, v, u);
+            fine = fine && cx.wait(&B.empty[q % C::NS], q / C::NS + 1);
+        }
+        // All or none go on: they meet at a barrier.
+        return !hs::pair::named_sync_or(kLoadBar, kTile, !fine);
+    };
+    const auto arrive = [&](int t, bool v) {
+        hs::fence_proxy_async_shared();
+        for (int u = 0; u < C::kSubs; ++u) {
+            const int q = turn_of<C>(t, u) % C::NS;
+            hs::mbar_arrive(v ? &B.ready[q] : &B.kfull[q]);
+        }
+    };
+    Written done;
+    bool run = true;  // alike in all threads
+    for (bool more = first_seg(a, B, s); more && run; more = next_seg(a, B, s)) {
+        if (s.i0 == s.i1) continue;
+        rows_of(t, s.i0);
+        load(t, false, 0, buf[0]);
+        for (int i = s.i0; i < s.i1 && run; ++i, ++t) {
+            const uint4 ld = *reinterpret_cast<const uint4*>(B.loaded[t & (C::kRing - 1)]);
+            const bool part = !all_see(a, s, token_of(s, i)) ||
+                              (ld.x & ld.y & ld.z & ld.w) != 0xffffffffu;
+            if (lt == 0) B.tile[t & (C::kRing - 1)] = make_int2(token_of(s, i), part);
+            // Batches of K, then of V; each is loaded while the one before it is
+            // stored.
+#pragma unroll
+            for (int j = 0; j < 2 * kBatches; ++j) {
+                const bool v = j >= kBatches;
+                if (j % kBatches == 0 && run) run = wait_empty(t, v);
+                if (j + 1 < 2 * kBatches) {
+                    load(t, j + 1 >= kBatches, (j + 1) % kBatches, buf[(j + 1) & 1]);
+                } else if (i + 1 < s.i1) {
+                    rows_of(t + 1, i + 1);
+                    load(t + 1, false, 0, buf[0]);
+                }
+                if (run) {
+                    store(t, v, j % kBatches, buf[j & 1], part);
+                    if ((j + 1) % kBatches == 0) arrive(t, v);
+                }
+            }
+            // (A warp that gives up says so where all meet next.)
+            if (run && i == s.i0 && done.n > 0) ok = write_unit(cx, done) && ok;
+        }
+        done = unit_to_write(a, s, B.place0, C::NQ == 2 && a.tq < s.m ? 2 : 1, done);
+    }
+    ok = ok && run;
+    if (ok && done.n > 0) ok = write_unit(cx, done);
+    if (bad) hs::set_status(a.status, HS_ERR_BAD_INDEX);
+    return ok;
+}
+
+template <int KV, int D, int LD>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUtensorMap qmap,
                   const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap) {
-    using C = Cfg<KV, D, TMA>;
-    constexpr int NQ = C::NQ, NS = C::NS, kSubs = C::kSubs;
-    constexpr bool E4 = C::kE4;
-    using BarsT = typename BarsOf<TMA, E4>::T;
+    using C = Cfg<KV, D, LD>;
     const PrefillArgs& a = ta.p;
-    extern __shared__ __align__(1024) unsigned char smem_raw[];
-    unsigned char* smem = reinterpret_cast<unsigned char*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    BarsT& B = *reinterpret_cast<BarsT*>(smem + C::kBarOff);
-    const uint32_t sb = hs::smem_u32(smem);
+    extern __shared__ __align__(1024) unsigned char smem[];
+    Bars<C>& B = *reinterpret_cast<Bars<C>*>(smem + C::kBarOff);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint64_t tmo = ta.timeout_ns;
-    const volatile int* abort_flag = &B.abort;
-
+    // The swizzled tiles need it (and there is no room to round up).
+    if ((hs::smem_u32(smem) & 1023u) != 0) {
+        hs::set_status(a.status, HS_ERR_CUDA);
+        return;
+    }
     if (tid == 0) {
-        for (int i = 0; i < NS; ++i) {
-            hs::mbar_init(&B.kfull[i], TMA ? 1 : kTile);
+        for (int i = 0; i < C::NS; ++i) {
+            hs::mbar_init(&B.kfull[i], C::kByTma && !C::kE4 ? 1 : kTile);
             hs::mbar_init(&B.vfull[i], 1);
-            hs::mbar_init(&B.ready[i], TMA ? kCheckWarps : kTile);
+            hs::mbar_init(&B.ready[i], C::kByTma && !C::kE4 ? 4 : kTile);
             hs::mbar_init(&B.empty[i], 1);
         }
-        hs::mbar_init(&B.q_full, TMA ? 1 : kQWarps * 32);
+        hs::mbar_init(&B.q_full, C::kConvert ? kTile : C::kByTma ? 1 : kQThreads);
         hs::mbar_init(&B.q_empty, 1);
         hs::mbar_init(&B.s_free, kTile);
         for (int i = 0; i < 2; ++i) {
+            hs::mbar_init(&B.sfull[i], 1);
+            hs::mbar_init(&B.sempty[i], kTile);
             hs::mbar_init(&B.s_full[i], 1);
             hs::mbar_init(&B.p_full[i], kTile);
             hs::mbar_init(&B.pv_done[i], 1);
+            hs::mbar_init(&B.l_full[i], kTile);
             hs::mbar_init(&B.o_free[i], kTile);
             hs::mbar_init(&B.drain[i], 1);
         }
         B.abort = 0;
         hs::fence_mbar_init();
     }
-    if (TMA && warp == kLoadWarp && lane < 3)
+    for (int i = tid; i < C::kRing * C::kSubs * 4; i += kThreads) (&B.odd[0][0][0])[i] = 0;
+    if (C::kByTma && warp == kTmaWarp && lane < 3)
         asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &kmap : lane == 1 ? &vmap : &qmap)
                      : "memory");
     if (warp == kQkWarp) {
@@ -515,786 +1503,37 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
                 hs::set_status(a.status, HS_ERR_BAD_INDEX);
         }
     make_plan(a, B, reinterpret_cast<int64_t*>(smem));
-    const uint32_t tmem = B.tmem_base;
-    const auto give_up = [&] {
-        hs::set_status(a.status, HS_ERR_TIMEOUT);
-        B.abort = 1;
-    };
-    const auto wait = [&](uint64_t* bar, int parity) {
-        return hs::mbar_wait_bounded(bar, uint32_t(parity & 1), tmo, abort_flag);
-    };
-    // Ring unit s of the CTA's tile t: first those of K, then those of V.
-    const auto unit_of = [](int t, bool v, int s) { return (2 * t + (v ? 1 : 0)) * kSubs + s; };
-    // The barriers of K's units and of V's count those alone: loads may land in
-    // another order than they were issued in, and a parity tells only neighbouring
-    // phases apart, so who waits has to have seen the phase before.
-    const auto turn_of = [](int t, int s) { return t * kSubs + s; };
-    Seg s;
-
+    const Cta<C> cx{ta, a, B, smem, hs::smem_u32(smem), B.tmem_base};
+    bool ok = true;
     if (warp < 8) {
-        // ------------------------- softmax and output -------------------------
         set_max_regs_up<C::kSoftRegs>();
-        const int w = warp >> 2;   // query tile (NQ = 1: only 0 works)
-        const int r = tid & 127;   // row of the tile, and TMEM lane
-        const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-        const int tok = r / a.group, hd = r - tok * a.group;  // its new token and query head
-        const uint32_t o_addr = tmem + lanes + C::kOCol + uint32_t(NQ == 2 ? w * 128 : 0);
-        const bool bf = KV == kBf16 || (E4 && !a.q_is_half);
-        bool ok = w < NQ;
-        // The product of this tile's k-th P is done.
-        const auto pv_wait = [&](int k) {
-            return NQ == 2 ? wait(&B.pv_done[w], k) : wait(&B.pv_done[k & 1], k >> 1);
-        };
-        int t = 0, mine = 0, units = 0;  // the CTA's tiles, this tile's, units with tiles
-        bool head = false;               // the run ends in the first part of a shared unit
-        for (bool more = ok && first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
-            const int n = s.i1 - s.i0;
-            const bool live = tok < a.tq && w * a.tq + tok < s.m;
-            const int64_t qh = int64_t(s.x.first + s.block * a.tb + w * a.tq + tok) * a.heads +
-                               s.kvh * a.group + hd;
-            if (n == 0) {
-                if (s.nt == 0 && s.begins && live) {
-                    // Nothing is attended to: zeros.
-                    for (int i = 0; i < D / 8; ++i)
-                        reinterpret_cast<uint4*>(a.out)[qh * (D / 8) + i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (a.lse != nullptr) a.lse[qh] = -CUDART_INF_F;
-                }
-                continue;
-            }
-            const bool whole = s.i0 == 0 && s.i1 == s.nt;
-            if (w == 0 && tid == 0 && !whole && s.i0 == 0) {
-                head = true;
-                SharedUnit u;
-                u.start = s.start;
-                u.per = B.per;
-                u.rest = B.rest;
-                u.cost = s.cost;
-                u.tiles = s.nt;
-                u.first = s.x.first + s.block * a.tb;
-                u.tokens = s.m;
-                u.kvh = s.kvh;
-                u.valid = 1;
-                a.shared[blockIdx.x] = u;
-            }
-            const int useg = units++;
-            if (w * a.tq >= s.m) {  // the second tile of a unit that has one
-                t += n;
-                continue;
-            }
-            // The row's position; rows without a query see what the last does.
-            const int pos = s.p0 + min(w * a.tq + tok, s.m - 1);
-            float scl = a.scale_log2;
-            float off = -CUDART_INF_F;      // reference - kShift
-            uint64_t l0 = 0, l1 = 0;        // sums, in pairs
-            bool first = true;
-            const int last = mine + n;
-            for (; mine < last; ++t, ++mine, first = false) {
-                const int x = NQ == 2 ? w : mine & 1;
-                const int ph = NQ == 2 ? mine : mine >> 1;
-                const uint32_t s_addr = tmem + lanes + uint32_t(NQ == 2 ? 0 : x * 128);
-                const uint32_t p_addr = NQ == 2 ? tmem + lanes + C::kPCol + uint32_t(w * 64) : s_addr;
-                ok = __all_sync(0xffffffffu, wait(&B.s_full[x], ph));
-                if (!ok) break;
-                hs::tc::fence_after_sync();
-                float v[128];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, v + c * 32);
-                if (first) {
-                    // (0 would turn masked places into NaN; 2^-126 does not show.)
-                    if constexpr (E4) {
-                        scl *= B.qscale[useg & (kSegRing - 1)][w * kTile + r];
-                        if (a.k_scale != nullptr) scl *= a.k_scale[s.kvh];
-                    }
-                    if (scl == 0.f) scl = 1.17549435e-38f;
-                }
-                const bool part = B.tile[t & (kRing - 1)].y != 0;
-                const float as = fabsf(scl);
-                uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-                hs::tc::tmem_wait_ld();
-                if (NQ == 2) {
-                    hs::tc::fence_before_sync();
-                    hs::mbar_arrive(&B.s_free);
-                }
-                if (scl < 0.f) {
-#pragma unroll
-                    for (int c = 0; c < 128; ++c) v[c] = -v[c];
-                }
-                if (part) {
-                    // What this row sees of the tile.
-                    const uint4 ld = *reinterpret_cast<const uint4*>(B.loaded[t & (kRing - 1)]);
-                    const int t0 = B.tile[t & (kRing - 1)].x;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int b = t0 + 32 * j;
-                        const uint32_t lw = j == 0 ? ld.x : j == 1 ? ld.y : j == 2 ? ld.z : ld.w;
-                        vis[j] = low_bits(pos + 1 - b) & lw;
-                        if (a.window > 0)
-                            vis[j] &= ~low_bits(pos - a.window + 1 - b) | low_bits(a.sinks - b);
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (!((vis[j] >> c) & 1u)) v[32 * j + c] = -CUDART_INF_F;
-                    }
-                }
-                uint64_t as2, ref2, s0 = 0, s1 = 0;
-                const auto refer = [&] {
-                    // Without a finite logit so far: subtract 0, every weight is
-                    // 0 (a NaN logit stays NaN).
-                    const float ref = off == -CUDART_INF_F ? 0.f : off;
-                    as2 = pair_of(as, as);
-                    ref2 = pair_of(-ref, -ref);
-                };
-                const auto weigh = [&](int c) {  // columns [32 c, 32 c + 32)
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const int e = 32 * c + 2 * j;
-                        const float2 y = split(fma2(pair_of(v[e], v[e + 1]), as2, ref2));
-                        const float2 z = split(fma2(pair_of(v[e + 2], v[e + 3]), as2, ref2));
-                        const float2 p = make_float2(ex2(y.x), ex2(y.y)), q = make_float2(ex2(z.x), ex2(z.y));
-                        s0 = add2(s0, pair_of(p.x, p.y));
-                        s1 = add2(s1, pair_of(q.x, q.y));
-                        pk[j] = pack<KV>(p.x, p.y);
-                        pk[j + 1] = pack<KV>(q.x, q.y);
-                    }
-                    tmem_st16u(p_addr + c * 16, pk);
-                };
-                // The reference moves up to the maximum where that is far above;
-                // what has been summed is scaled down.
-                const auto raise = [&] {
-                    float mx[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-                    for (int c = 4; c < 124; c += 8)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) mx[j] = max3(mx[j], v[c + 2 * j], v[c + 2 * j + 1]);
-                    mx[0] = max3(mx[0], v[124], v[125]);
-                    mx[1] = max3(mx[1], v[126], v[127]);
-                    const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * as - C::kShift;
-                    const bool grow = top > off + C::kThresh || (off == -CUDART_INF_F && top > off);
-                    if (first) {
-                        if (grow) off = top;
-                        return false;
-                    }
-                    if (!__any_sync(0xffffffffu, grow)) return false;
-                    const float to = grow ? top : off;
-                    const float al = grow ? (off == -CUDART_INF_F ? 0.f : ex2(off - to)) : 1.f;
-                    off = to;
-                    l0 = fma2(l0, pair_of(al, al), 0);
-                    l1 = fma2(l1, pair_of(al, al), 0);
-                    if (NQ == 1) {
-                        ok = __all_sync(0xffffffffu, pv_wait(mine - 1));
-                        hs::tc::fence_after_sync();
-                    }
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
-                        float o[16];
-                        hs::tc::tmem_ld16(o_addr + uint32_t(c), o);
-                        hs::tc::tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) o[j] *= al;
-                        hs::tc::tmem_st16(o_addr + uint32_t(c), o);
-                    }
-                    return true;
-                };
-                // The products of the tile before have read P and are in O.
-                if (NQ == 2 && mine > 0) {
-                    ok = __all_sync(0xffffffffu, pv_wait(mine - 1));
-                    hs::tc::fence_after_sync();
-                }
-                // Mostly the reference stays: the weights are made while the
-                // maximum is found, and the first half again where it moved.
-                const bool ahead = !part && !first && scl > 0.f;
-                if (!ahead) raise();
-                refer();
-                weigh(0);
-                weigh(1);
-                if (ahead && raise()) {
-                    refer();
-                    s0 = s1 = 0;
-                    weigh(0);
-                    weigh(1);
-                }
-                if (!ok) break;
-                weigh(2);
-                weigh(3);
-                l0 = add2(l0, s0);
-                l1 = add2(l1, s1);
-                hs::tc::tmem_wait_st();
-                if (part) {
-                    // Rows of V that were taken out.
-                    uint32_t any = 0;
-                    for (int u = 0; u < kSubs && ok; ++u) {
-                        const int q = turn_of(t, u);
-                        ok = __all_sync(0xffffffffu, wait(&B.ready[q % NS], q / NS));
-                        const uint4 o = *reinterpret_cast<const uint4*>(B.odd[t & (kRing - 1)][u]);
-                        any |= o.x | o.y | o.z | o.w;
-                    }
-                    if (!ok) break;
-                    if (first) B.keep[w] = any != 0;
-                    if (any != 0) {
-                        if (NQ == 1 && !first) {
-                            ok = __all_sync(0xffffffffu, pv_wait(mine - 1));
-                            if (!ok) break;
-                            hs::tc::fence_after_sync();
-                        }
-                        const float zero[16] = {};
-                        if (first)
-                            for (int c = 0; c < D; c += 16) hs::tc::tmem_st16(o_addr + uint32_t(c), zero);
-                        hs::tc::tmem_wait_st();
-                        for (int j = 0; j < kTile; ++j) {
-                            const uint32_t pw = tmem_ld1(p_addr + uint32_t(j >> 1));
-                            hs::tc::tmem_wait_ld();
-                            const uint32_t h = (j & 1) ? pw >> 16 : pw & 0xffffu;
-                            const float p = KV == kBf16 ? __uint_as_float(h << 16)
-                                                        : __half2float(__ushort_as_half(uint16_t(h)));
-                            const uint32_t vw = j < 32 ? vis[0] : j < 64 ? vis[1] : j < 96 ? vis[2] : vis[3];
-                            const bool sees = (vw >> (j & 31)) & 1u;
-                            for (int u = 0; u < kSubs; ++u) {
-                                if (!((B.odd[t & (kRing - 1)][u][j >> 5] >> (j & 31)) & 1u)) continue;
-                                const int tk = B.tile[t & (kRing - 1)].x + j, b = block_of(a, tk);
-                                const int64_t page = a.block_table[s.row * a.bt_stride + b];
-                                const void* row = static_cast<const char*>(a.v) +
-                                    (page * a.page_stride + int64_t(tk - b * a.page_size) * a.row_stride +
-                                     s.kvh * a.head_stride) * (E4 ? 1 : 2);
-                                for (int c = u * C::kDims; c < (u + 1) * C::kDims; c += 16) {
-                                    float o[16];
-                                    hs::tc::tmem_ld16(o_addr + uint32_t(c), o);
-                                    hs::tc::tmem_wait_ld();
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e)
-                                        if (sees) o[e] = fmaf(p, element<KV>(row, c + e), o[e]);
-                                    hs::tc::tmem_st16(o_addr + uint32_t(c), o);
-                                    hs::tc::tmem_wait_st();
-                                }
-                            }
-                        }
-                    }
-                } else if (first) {
-                    B.keep[w] = 0;
-                }
-                hs::tc::fence_before_sync();
-                hs::mbar_arrive(&B.p_full[x]);
-            }
-            if (!ok) break;
-            // ---- The unit's state ---------------------------------------------
-            ok = __all_sync(0xffffffffu, pv_wait(mine - 1));
-            if (!ok) break;
-            hs::tc::fence_after_sync();
-            const float2 ls = split(add2(l0, l1));
-            const float l = ls.x + ls.y;
-            const float lg = l == 0.f ? -CUDART_INF_F : off + log2f(l);
-            float f = 1.f;
-            if (whole) {
-                f = l == 0.f ? 0.f : 1.f / l;
-                if (a.v_scale != nullptr && l != 0.f) f *= a.v_scale[s.kvh];
-                if (live && a.lse != nullptr) a.lse[qh] = lg * kLn2;
-            }
-            const int64_t slot0 = 2 * int(blockIdx.x) + (s.start < B.place0 ? 0 : 1);
-            if (!whole && live)
-                reinterpret_cast<float2*>(a.part_ml)[slot0 * a.unit_rows + w * kTile + r] =
-                    make_float2(off, l);
-            // A row per thread: 32 bytes of each of 32 rows at a time.  (Pieces
-            // exchanged between lanes for whole lines: five times as long.)
-            uint16_t* to = static_cast<uint16_t*>(a.out) + qh * D;
-            float* po = a.part_o + ((slot0 * (D / 8)) * a.unit_rows + w * kTile + r) * 8;
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                float o[32];
-                tmem_ld32(o_addr + uint32_t(c), o);
-                hs::tc::tmem_wait_ld();
-                if (!live) continue;
-                if (!whole) {
-#pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        uint32_t y[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = __float_as_uint(o[j + e]);
-                        store32(po + int64_t((c + j) / 8) * a.unit_rows * 8, y);
-                    }
-                    continue;
-                }
-#pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] = l == 0.f ? 0.f : o[j] * f;
-#pragma unroll
-                for (int j = 0; j < 32; j += 16) {
-                    uint32_t y[8];
-                    if (bf) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = pack<kBf16>(o[j + 2 * e], o[j + 2 * e + 1]);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = pack<kFp16>(o[j + 2 * e], o[j + 2 * e + 1]);
-                    }
-                    if (a.out_wide) {
-                        store32(to + c + j, y);
-                    } else {
-                        reinterpret_cast<uint4*>(to + c + j)[0] = make_uint4(y[0], y[1], y[2], y[3]);
-                        reinterpret_cast<uint4*>(to + c + j)[1] = make_uint4(y[4], y[5], y[6], y[7]);
-                    }
-                }
-            }
-            hs::tc::fence_before_sync();
-            hs::mbar_arrive(&B.o_free[w]);
-        }
-        if (w < NQ && !ok) give_up();
-        if (tid == 0 && !head) a.shared[blockIdx.x].valid = 0;
+        if (warp < 4 * C::NQ) softmax_role<C>(cx);
     } else if (warp < kLoadWarp) {
         set_max_regs_down<C::kMmaRegs>();
-        // Products and commits are the bound of a warp that issues them all (3600
-        // cycles for a pair of tiles whose products take 2048): one issues QK,
-        // one PV.  Two query tiles share S, whose softmax begins by taking it into
-        // registers, and have a P each: the QK of one runs ahead of the PV of the
-        // other, and a tile has the time of both tiles' products for its softmax.
-        // (With S and P of a tile in the same columns QK has to wait for PV and
-        // the softmax is on the products' path.)
-        bool ok = true;
-        const auto all_wait = [&](uint64_t* bar, int parity) {
-            ok = ok && __all_sync(0xffffffffu, wait(bar, parity));
-        };
-        if (warp == kQkWarp) {
-            // ------------------------------- S = Q K^T ---------------------------
-            constexpr uint32_t id = idesc<KV>(kTile, 0);
-            const uint64_t q_desc = hs::tc::sdesc_sw128(sb + C::kQOff, 16, 1024);
-            const uint64_t k_desc = hs::tc::sdesc_sw128(sb + C::kRingOff, 16, 1024);
-            int t = 0, segs = 0, n_qk = 0;
-            for (bool more = first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
-                const int n = s.i1 - s.i0;
-                if (n == 0) continue;
-                const int tiles = NQ == 2 && a.tq < s.m ? 2 : 1;
-                all_wait(&B.q_full, segs++);
-                for (int i = 0; i < n && ok; ++i, ++t) {
-                    uint32_t at[kSubs];
-#pragma unroll
-                    for (int u = 0; u < kSubs; ++u) {
-                        const int k = turn_of(t, u);
-                        at[u] = uint32_t(unit_of(t, false, u) % NS * (C::kUnit >> 4));
-                        all_wait(&B.kfull[k % NS], k / NS);
-                    }
-                    for (int w = 0; w < tiles; ++w, ++n_qk) {
-                        const int x = NQ == 2 ? 0 : t & 1;
-                        // The last softmax has taken S, or the last product of
-                        // this buffer's P is done.
-                        if (NQ == 2) {
-                            if (n_qk > 0) all_wait(&B.s_free, n_qk - 1);
-                        } else if (t >= 2) {
-                            all_wait(&B.pv_done[x], (t - 2) >> 1);
-                        }
-                        hs::tc::fence_after_sync();
-                        if (!ok) break;
-#pragma unroll
-                        for (int u = 0; u < kSubs; ++u)
-#pragma unroll
-                            for (int b = 0; b < C::kDims / 64; ++b)
-                                mma_ss4(tmem + uint32_t(x * 128),
-                                        q_desc + uint32_t(w * (C::kQTile >> 4) +
-                                                          (u * (C::kDims / 64) + b) * (kBlk >> 4)),
-                                        k_desc + at[u] + uint32_t(b * (kBlk >> 4)), id,
-                                        (u | b) ? 1u : 0u);
-                        commit(&B.s_full[NQ == 2 ? w : x]);
-                    }
-                    if (!ok) break;
-#pragma unroll
-                    for (int u = 0; u < kSubs; ++u) commit(&B.empty[unit_of(t, false, u) % NS]);
-                    if (i + 1 == n) commit(&B.q_empty);
-                }
-            }
-        } else if (warp == kPvWarp) {
-            // ------------------------------- O += P V ----------------------------
-            constexpr uint32_t id = idesc<KV>(C::kDims, 1);
-            const uint64_t v_desc = hs::tc::sdesc_sw128(sb + C::kRingOff, kBlk, 1024);
-            int t = 0, done0 = 0, done1 = 0, had0 = 0, had1 = 0;
-            for (bool more = first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
-                const int n = s.i1 - s.i0;
-                if (n == 0) continue;
-                const int tiles = NQ == 2 && a.tq < s.m ? 2 : 1;
-                // The outputs before have been read.
-                if (had0 > 0) all_wait(&B.o_free[0], had0 - 1);
-                if (tiles == 2 && had1 > 0) all_wait(&B.o_free[1], had1 - 1);
-                ++had0;
-                if (tiles == 2) ++had1;
-                for (int i = 0; i < n && ok; ++i, ++t) {
-                    uint32_t at[kSubs];
-#pragma unroll
-                    for (int u = 0; u < kSubs; ++u) {
-                        const int q = turn_of(t, u);
-                        at[u] = uint32_t(unit_of(t, true, u) % NS * (C::kUnit >> 4));
-                        all_wait(&B.ready[q % NS], q / NS);
-                    }
-                    for (int w = 0; w < tiles; ++w) {
-                        const int x = NQ == 2 ? w : t & 1;
-                        all_wait(&B.p_full[x], NQ == 2 ? (w == 0 ? done0 : done1) : t >> 1);
-                        hs::tc::fence_after_sync();
-                        if (!ok) break;
-                        const bool fresh = i == 0 && B.keep[w] == 0;
-                        const uint32_t p_col =
-                            tmem + (NQ == 2 ? C::kPCol + uint32_t(w * 64) : uint32_t(x * 128));
-#pragma unroll
-                        for (int u = 0; u < kSubs; ++u)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-                                mma_ts4(tmem + C::kOCol + uint32_t((w + u) * 128), p_col + uint32_t(h * 32),
-                                        v_desc + at[u] + uint32_t(h * 512), id,
-                                        fresh && h == 0 ? 0u : 1u);
-                        commit(&B.pv_done[x]);
-                        if (w == 0) ++done0;
-                        else ++done1;
-                    }
-                    if (!ok) break;
-#pragma unroll
-                    for (int u = 0; u < kSubs; ++u) commit(&B.empty[unit_of(t, true, u) % NS]);
-                }
-            }
-        } else if (TMA && warp == kQWarp) {
-            // ------------------------------- queries ----------------------------
-            // A box takes the heads of a KV head for a tile's tokens: its rows
-            // are the tile's.  (Tokens of other requests behind a unit's own
-            // land in rows that are not written.)
-            int segs = 0;
-            const uint32_t bytes = uint32_t(a.tq * a.group) * 128u;
-            for (bool more = first_seg(a, B, s); more; more = next_seg(a, B, s)) {
-                if (s.i1 == s.i0) continue;
-                ok = segs == 0 || __all_sync(0xffffffffu, wait(&B.q_empty, segs - 1));
-                if (!ok) break;
-                if (lane == 0) {
-                    const int tiles = s.m > a.tq ? 2 : 1;
-                    hs::mbar_arrive_expect_tx(&B.q_full, bytes * (D / 64) * tiles);
-                    for (int w = 0; w < tiles; ++w)
-                        for (int c = 0; c < D / 64; ++c)
-                            tma_load_q(sb + C::kQOff + w * C::kQTile + c * kBlk, &qmap, c * 64,
-                                       s.kvh * a.group, s.x.first + s.block * a.tb + w * a.tq,
-                                       &B.q_full);
-                }
-                __syncwarp();
-                ++segs;
-            }
-            // No copy may outlive the CTA.
-            if (segs > 0) hs::mbar_wait_bounded(&B.q_full, (segs - 1) & 1, tmo, nullptr);
-        } else if (!TMA && warp >= kQWarp) {
-            // ------------------------------- queries ----------------------------
-            const int qw = warp - kQWarp, qt = qw * 32 + lane;
-            int segs = 0;
-            for (bool more = first_seg(a, B, s); more; more = next_seg(a, B, s)) {
-                if (s.i1 == s.i0) continue;
-                if (segs > 0 && !__all_sync(0xffffffffu, wait(&B.q_empty, segs - 1))) {
-                    ok = false;
-                    break;
-                }
-                const int64_t first = s.x.first + s.block * a.tb;
-                const char* q = static_cast<const char*>(a.q) + int64_t(s.kvh) * a.group * D * 2;
-                constexpr int kCh = D / 8;  // 16-byte chunks of a row
-                // (A quotient by a division a row took 7 us a unit.)
-                constexpr int kRowStep = kQWarps * 32 / kCh;
-                const int hstep = kRowStep % a.group, tstep = kRowStep / a.group;
-                const int row0 = E4 ? qw * (32 / kCh) + lane / kCh : qt / kCh;
-                int tok = row0 / a.group, hd = row0 - tok * a.group;
-                const int tok0 = tok, hd0 = hd;
-                const auto next_row = [&](int n) {
-                    hd += hstep;
-                    tok += tstep;
-                    if (hd >= a.group) {
-                        hd -= a.group;
-                        ++tok;
-                    }
-                    if (NQ == 2 && n == kTile) {  // the second tile starts over
-                        tok = tok0;
-                        hd = hd0;
-                    }
-                };
-                if constexpr (!E4) {
-                    for (int n = row0; n < NQ * kTile; n += kRowStep, next_row(n - row0)) {
-                        const int ch = qt % kCh, w = n / kTile, r = n % kTile;
-                        const bool in = tok < a.tq && w * a.tq + tok < s.m;
-                        const int64_t at = in ? (first + w * a.tq + tok) * a.q_stride + hd * D + ch * 8 : 0;
-                        hs::tc::cp_async16(sb + C::kQOff + w * C::kQTile + (ch >> 3) * kBlk + r * 128 +
-                                               (((ch & 7) ^ (r & 7)) << 4),
-                                           q + at * 2, in ? 16u : 0u);
-                    }
-                    hs::tc::cp_async_wait_all();
-                } else {
-                    // A row per D / 8 lanes.
-                    const int ch = lane % kCh;
-#pragma unroll 4
-                    for (int n = row0; n < NQ * kTile; n += kRowStep, next_row(n - row0)) {
-                        const int w = n / kTile, r = n % kTile;
-                        const bool in = tok < a.tq && w * a.tq + tok < s.m;
-                        uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-                        if (in)
-                            raw = *reinterpret_cast<const uint4*>(
-                                q + ((first + w * a.tq + tok) * a.q_stride + hd * D + ch * 8) * 2);
-                        float scale = 1.f;
-                        if (!a.q_is_half) {
-                            uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
-                            float f[8], mx = 0.f;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u[i]));
-                                f[2 * i] = y.x;
-                                f[2 * i + 1] = y.y;
-                                mx = fmaxf(mx, fmaxf(fabsf(y.x), fabsf(y.y)));
-                            }
-#pragma unroll
-                            for (int o = kCh / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                            // Largest magnitude to [2^14, 2^15), by two factors
-                            // (their product may lie outside fp32's range).
-                            int e = 0;
-                            if (mx > 0.f && mx < CUDART_INF_F)
-                                e = max(14 - (int(__float_as_uint(mx) >> 23) - 127), -126);
-                            const int ea = e / 2, eb = e - ea;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                u[i] = pack<kFp16>(f[2 * i] * pow2(ea) * pow2(eb),
-                                                   f[2 * i + 1] * pow2(ea) * pow2(eb));
-                            raw = make_uint4(u[0], u[1], u[2], u[3]);
-                            scale = pow2(-ea) * pow2(-eb);
-                        }
-                        *reinterpret_cast<uint4*>(smem + C::kQOff + w * C::kQTile + (ch >> 3) * kBlk + r * 128 +
-                                                  (((ch & 7) ^ (r & 7)) << 4)) = raw;
-                        if (ch == 0) B.qscale[segs & (kSegRing - 1)][n] = scale;
-                    }
-                }
-                hs::fence_proxy_async_shared();
-                hs::mbar_arrive(&B.q_full);
-                ++segs;
-            }
-        }
-        if (!ok) give_up();
         if (warp <= kPvWarp) {
+            ok = warp == kQkWarp ? qk_role<C>(cx) : pv_role<C>(cx);
+            if (!ok) cx.give_up();
             // Every product issued has completed before TMEM is freed.
             __syncwarp();
             commit(&B.drain[warp - kQkWarp]);
-            hs::mbar_wait_bounded(&B.drain[warp - kQkWarp], 0, tmo, nullptr);
+            hs::mbar_wait_bounded(&B.drain[warp - kQkWarp], 0, ta.timeout_ns, nullptr);
             __syncwarp();
-        }
-    } else if constexpr (TMA) {
-        set_max_regs_down<C::kLoadRegs>();
-        const int runs = kTile / ta.bt;  // a power of two up to 8
-        if (warp == kLoadWarp) {
-            // -------------------------------- loads -----------------------------
-            bool ok = true, bad = false;
-            int t = 0, seq = 0;
-            const uint32_t box = uint32_t(ta.bt) * 128u;
-            for (bool more = first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
-                for (int i = s.i0; i < s.i1 && ok; ++i, ++t) {
-                    // Lane i: run i of the tile.
-                    const int tok = token_of(s, i) + lane * ta.bt;
-                    const int b = block_of(a, tok);
-                    const bool wants = lane < runs && any_sees(a, s, tok, ta.bt);
-                    const int page = wants ? a.block_table[s.row * a.bt_stride + b] : -1;
-                    const bool want = wants && page >= 0 && page < a.num_pages;
-                    if (wants && !want) bad = true;
-                    const uint32_t got = __ballot_sync(0xffffffffu, want);
-                    if (lane < 4) {
-                        uint32_t bits = 0;
-                        if (ta.bt >= 32) {
-                            bits = (got >> (lane * 32 / ta.bt)) & 1u ? 0xffffffffu : 0u;
-                        } else {  // 16
-                            if ((got >> (2 * lane)) & 1u) bits |= 0xffffu;
-                            if ((got >> (2 * lane + 1)) & 1u) bits |= 0xffff0000u;
-                        }
-                        B.loaded[t & (kRing - 1)][lane] = bits;
-                    }
-                    if (lane == 4) {
-                        const int t0 = token_of(s, i);
-                        B.tile[t & (kRing - 1)] = make_int2(t0, !all_see(a, s, t0) || got != low_bits(runs));
-                    }
-                    __syncwarp();
-                    const uint32_t bytes = uint32_t(__popc(got)) * box * (C::kDims / 64);
-                    const int at = tok - b * a.page_size;
-                    for (int u = 0; u < 2 * kSubs; ++u, ++seq) {
-                        const int slot = seq % NS;
-                        ok = __all_sync(0xffffffffu, wait(&B.empty[slot], seq / NS + 1));
-                        if (!ok) break;
-                        const int turn = turn_of(t, u % kSubs) % NS;
-                        uint64_t* full = u < kSubs ? &B.kfull[turn] : &B.vfull[turn];
-                        if (lane == 0) hs::mbar_arrive_expect_tx(full, bytes);
-                        __syncwarp();
-                        if (want) {
-                            const uint32_t dst = sb + C::kRingOff + slot * C::kUnit + lane * box;
-#pragma unroll
-                            for (int c = 0; c < C::kDims / 64; ++c)
-                                tma_load(dst + c * kBlk, u < kSubs ? &kmap : &vmap,
-                                         u % kSubs * C::kDims + c * 64, at, s.kvh, page, full);
-                        }
-                    }
-                }
-            }
-            if (!ok) {
-                give_up();
-                // No copy may outlive the CTA: wait for every unit in flight.
-                for (int q = max(0, seq - NS); q < seq; ++q) {
-                    const int u = q % (2 * kSubs), turn = turn_of(q / (2 * kSubs), u % kSubs);
-                    hs::mbar_wait_bounded(u < kSubs ? &B.kfull[turn % NS] : &B.vfull[turn % NS],
-                                          (turn / NS) & 1, tmo, nullptr);
-                }
-            }
-            if (bad) hs::set_status(a.status, HS_ERR_BAD_INDEX);
+        } else if constexpr (C::kByTma) {
+            if (warp == kTmaWarp && !tma_role<C>(cx, qmap, kmap, vmap)) cx.give_up();
         } else {
-            // ------------------------------ rows of V ---------------------------
-            const int cw = warp - kLoadWarp - 1;
-            bool ok = true;
-            int t = 0;
-            for (bool more = first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
-                for (int i = s.i0; i < s.i1 && ok; ++i, ++t) {
-                    const int t0 = token_of(s, i);
-                    for (int u = 0; u < kSubs; ++u) {
-                        const int q = unit_of(t, true, u), turn = turn_of(t, u);
-                        ok = __all_sync(0xffffffffu, wait(&B.vfull[turn % NS], turn / NS));
-                        if (!ok) break;
-                        if (B.tile[t & (kRing - 1)].y != 0) {
-                            for (int j = cw; j < 4; j += kCheckWarps) {
-                                const int r = j * 32 + lane;
-                                const bool in = any_sees(a, s, t0 + r) &&
-                                                ((B.loaded[t & (kRing - 1)][j] >> lane) & 1u);
-                                unsigned char* row = smem + C::kRingOff + q % NS * C::kUnit + r * 128;
-                                bool odd = false;
-                                if (in)
-                                    for (int c = 0; c < C::kDims / 8; ++c)
-                                        odd |= not_finite<KV>(*reinterpret_cast<const uint4*>(
-                                            row + (c >> 3) * kBlk + (((c + lane) & 7) << 4)));
-                                const uint32_t all = __ballot_sync(0xffffffffu, odd);
-                                if (lane == 0) B.odd[t & (kRing - 1)][u][j] = all;
-                                if (!in || odd)
-                                    for (int c = 0; c < C::kDims / 8; ++c)
-                                        *reinterpret_cast<uint4*>(row + (c >> 3) * kBlk + (((c + lane) & 7) << 4)) =
-                                            make_uint4(0u, 0u, 0u, 0u);
-                            }
-                            hs::fence_proxy_async_shared();
-                        }
-                        __syncwarp();
-                        if (lane == 0) hs::mbar_arrive(&B.ready[turn % NS]);
-                    }
-                }
-            }
-            if (!ok) give_up();
+            if (!query_role<C>(cx)) cx.give_up();
         }
     } else {
-        // ------------------- loads by threads, and rows of V --------------------
         set_max_regs_down<C::kLoadRegs>();
-        constexpr int kElt = E4 ? 1 : 2, kPer = 16 / kElt;  // elements of 16 bytes
-        constexpr int kCh = D / kPer;                       // 16-byte chunks of a row
-        constexpr int kStep = kTile / kCh;                  // rows of a pass
-        constexpr int kPass = kCh < 8 ? kCh : 8;            // passes of a batch
-        constexpr int kBatch = kPass * kStep, kBatches = kTile / kBatch;
-        const int lt = tid - kLoadWarp * 32, ch = lt % kCh, r0 = lt / kCh;
-        bool ok = true, bad = false;
-        int t = 0;
-        uint4 buf[2][kPass];
-        const auto rows_of = [&](int t, int i) {
-            // Row lt of the tile: where it lies in the cache.
-            const int tok = token_of(s, i) + lt, b = block_of(a, tok);
-            int64_t at = -1;
-            if (any_sees(a, s, tok)) {
-                const int64_t page = a.block_table[s.row * a.bt_stride + b];
-                if (page >= 0 && page < a.num_pages)
-                    at = page * a.page_stride + int64_t(tok - b * a.page_size) * a.row_stride +
-                         s.kvh * a.head_stride;
-                else
-                    bad = true;
-            }
-            B.offset[t & 1][lt] = at;
-            const uint32_t got = __ballot_sync(0xffffffffu, at >= 0);
-            if (lane == 0) {
-                B.loaded[t & (kRing - 1)][lt >> 5] = got;
-                B.odd[t & (kRing - 1)][0][lt >> 5] = 0;
-                B.odd[t & (kRing - 1)][1][lt >> 5] = 0;
-            }
-            hs::pair::named_sync(kLoadBar, kTile);
-        };
-        const auto load = [&](int t, bool v, int batch, uint4 (&x)[kPass]) {
-            const char* base = static_cast<const char*>(v ? a.v : a.k) + ch * 16;
-#pragma unroll
-            for (int j = 0; j < kPass; ++j) {
-                const int64_t at = B.offset[t & 1][batch * kBatch + j * kStep + r0];
-                x[j] = at >= 0 ? *reinterpret_cast<const uint4*>(base + at * kElt)
-                               : make_uint4(0u, 0u, 0u, 0u);
-            }
-        };
-        const auto store = [&](int t, bool v, int batch, uint4 (&x)[kPass], bool part) {
-#pragma unroll
-            for (int j = 0; j < kPass; ++j) {
-                const int r = batch * kBatch + j * kStep + r0;
-                if (v && part) {
-                    // A row's chunks lie in neighbouring lanes of one warp.
-                    const uint32_t odd = __ballot_sync(0xffffffffu, not_finite<KV>(x[j]));
-                    const uint32_t mine = (kCh == 32 ? 0xffffffffu : ((1u << (kCh & 31)) - 1u) << (lane / kCh * kCh));
-                    if (odd & mine) {
-                        x[j] = make_uint4(0u, 0u, 0u, 0u);
-                        if (ch == 0)
-                            for (int u = 0; u < kSubs; ++u)
-                                atomicOr(&B.odd[t & (kRing - 1)][u][r >> 5], 1u << (r & 31));
-                    }
-                }
-                const int c0 = E4 ? 2 * ch : ch;  // its first chunk of eight 16-bit elements
-                const int u = c0 * 8 / C::kDims, cb = c0 - u * (C::kDims / 8);
-                unsigned char* dst = smem + C::kRingOff + unit_of(t, v, u) % NS * C::kUnit +
-                                     (cb >> 3) * kBlk + r * 128;
-                if constexpr (E4) {
-                    uint4 y, z;
-                    y.x = e4m3x2_to_half2(x[j].x & 0xffffu);
-                    y.y = e4m3x2_to_half2(x[j].x >> 16);
-                    y.z = e4m3x2_to_half2(x[j].y & 0xffffu);
-                    y.w = e4m3x2_to_half2(x[j].y >> 16);
-                    z.x = e4m3x2_to_half2(x[j].z & 0xffffu);
-                    z.y = e4m3x2_to_half2(x[j].z >> 16);
-                    z.z = e4m3x2_to_half2(x[j].w & 0xffffu);
-                    z.w = e4m3x2_to_half2(x[j].w >> 16);
-                    *reinterpret_cast<uint4*>(dst + (((cb & 7) ^ (r & 7)) << 4)) = y;
-                    *reinterpret_cast<uint4*>(dst + ((((cb & 7) + 1) ^ (r & 7)) << 4)) = z;
-                } else {
-                    *reinterpret_cast<uint4*>(dst + (((cb & 7) ^ (r & 7)) << 4)) = x[j];
-                }
-            }
-        };
-        const auto wait_empty = [&](int t, bool v) {
-            bool fine = true;
-            for (int u = 0; u < kSubs; ++u) {
-                const int q = unit_of(t, v, u);
-                fine = fine && wait(&B.empty[q % NS], q / NS + 1);
-            }
-            // All or none go on: they meet at a barrier.
-            return !hs::pair::named_sync_or(kLoadBar, kTile, !fine);
-        };
-        const auto arrive = [&](int t, bool v) {
-            hs::fence_proxy_async_shared();
-            for (int u = 0; u < kSubs; ++u) {
-                const int q = turn_of(t, u);
-                hs::mbar_arrive(v ? &B.ready[q % NS] : &B.kfull[q % NS]);
-            }
-        };
-        for (bool more = first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
-            if (s.i0 == s.i1) continue;
-            rows_of(t, s.i0);
-            load(t, false, 0, buf[0]);
-            for (int i = s.i0; i < s.i1 && ok; ++i, ++t) {
-                const uint4 ld = *reinterpret_cast<const uint4*>(B.loaded[t & (kRing - 1)]);
-                const bool part = !all_see(a, s, token_of(s, i)) ||
-                                  (ld.x & ld.y & ld.z & ld.w) != 0xffffffffu;
-                if (lt == 0) B.tile[t & (kRing - 1)] = make_int2(token_of(s, i), part);
-                // Batches of K, then of V; each is loaded while the one before
-                // it is stored.
-#pragma unroll
-                for (int j = 0; j < 2 * kBatches; ++j) {
-                    const bool v = j >= kBatches;
-                    if (j % kBatches == 0 && ok) ok = wait_empty(t, v);
-                    if (j + 1 < 2 * kBatches) {
-                        load(t, j + 1 >= kBatches, (j + 1) % kBatches, buf[(j + 1) & 1]);
-                    } else if (i + 1 < s.i1) {
-                        rows_of(t + 1, i + 1);
-                        load(t + 1, false, 0, buf[0]);
-                    }
-                    if (ok) {
-                        store(t, v, j % kBatches, buf[j & 1], part);
-                        if ((j + 1) % kBatches == 0) arrive(t, v);
-                    }
-                }
-            }
-        }
-        if (!ok) give_up();
-        if (bad) hs::set_status(a.status, HS_ERR_BAD_INDEX);
+        if constexpr (C::kConvert) ok = convert_role<C>(cx);
+        else if constexpr (C::kByTma) ok = check_role<C>(cx);
+        else ok = load_role<C>(cx);
+        if (!ok) cx.give_up();
     }
     hs::tc::fence_before_sync();
     __syncthreads();
     hs::tc::fence_after_sync();
-    if (warp == kQkWarp) hs::tc::tmem_dealloc(tmem, kTmemCols);
+    if (warp == kQkWarp) hs::tc::tmem_dealloc(cx.tmem, kTmemCols);
 }
 
 // Tensor map of a cache: dims (head dim, token of the page, KV head, page).
@@ -1302,15 +1541,15 @@ int encode_map(CUtensorMap* m, const void* base, const PrefillArgs& a, int kv_dt
 // Of the queries: dims (head dim, head, token), boxes of a query tile.
 int encode_q_map(CUtensorMap* m, const PrefillArgs& a, int dtype, int d);
 
-template <int KV, int D, bool TMA>
+template <int KV, int D, int LD>
 int launch_one(const PrefillArgs& a, int bt, hs_stream_t stream) {
-    using C = Cfg<KV, D, TMA>;
+    using C = Cfg<KV, D, LD>;
     TcArgs t{};
     t.p = a;
     t.bt = bt;
     t.timeout_ns = hs::kWaitTimeoutNs;
-    auto kern = prefill_tc_kernel<KV, D, TMA>;
-    constexpr size_t smem = size_t(C::kBarOff) + sizeof(typename BarsOf<TMA, C::kE4>::T) + 1024;
+    auto kern = prefill_tc_kernel<KV, D, LD>;
+    constexpr size_t smem = size_t(C::kBarOff) + sizeof(Bars<C>);
     static_assert(smem <= 227 * 1024, "shared memory");
     static int smem_set[64] = {};
     int rc = hs_host::ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem, smem_set);
@@ -1327,8 +1566,8 @@ int launch_one(const PrefillArgs& a, int bt, hs_stream_t stream) {
     };
     if (hs_host::ask_once(&regs[dev], ask) != 65536 / kThreads) return HS_ERR_UNSUPPORTED;
     CUtensorMap q{}, k{}, v{};
-    if (TMA) {
-        rc = encode_q_map(&q, a, KV, D);
+    if (C::kByTma) {
+        if (!C::kE4) rc = encode_q_map(&q, a, KV, D);
         if (rc == HS_OK) rc = encode_map(&k, a.k, a, KV, D, bt);
         if (rc == HS_OK) rc = encode_map(&v, a.v, a, KV, D, bt);
         if (rc != HS_OK) return rc;
@@ -1339,16 +1578,14 @@ int launch_one(const PrefillArgs& a, int bt, hs_stream_t stream) {
 // bt: tokens of a TMA box, or 0: threads load.
 template <int KV>
 int launch_kind(const PrefillArgs& a, int d, int bt, hs_stream_t stream) {
-    if constexpr (KV != kE4m3) {
-        if (bt > 0) {
-            if (d == 64) return launch_one<KV, 64, true>(a, bt, stream);
-            if (d == 128) return launch_one<KV, 128, true>(a, bt, stream);
-            return launch_one<KV, 256, true>(a, bt, stream);
-        }
+    if (bt > 0) {
+        if (d == 64) return launch_one<KV, 64, kTma>(a, bt, stream);
+        if (d == 128) return launch_one<KV, 128, kTma>(a, bt, stream);
+        return launch_one<KV, 256, kTma>(a, bt, stream);
     }
-    if (d == 64) return launch_one<KV, 64, false>(a, 0, stream);
-    if (d == 128) return launch_one<KV, 128, false>(a, 0, stream);
-    return launch_one<KV, 256, false>(a, 0, stream);
+    if (d == 64) return launch_one<KV, 64, kThreadsLoad>(a, 0, stream);
+    if (d == 128) return launch_one<KV, 128, kThreadsLoad>(a, 0, stream);
+    return launch_one<KV, 256, kThreadsLoad>(a, 0, stream);
 }
 
 }  // namespace tc
