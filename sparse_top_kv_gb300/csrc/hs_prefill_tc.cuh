@@ -48,8 +48,10 @@ enum Kind { kBf16 = 0, kFp16 = 1, kE4m3 = 2 };
 
 constexpr int kThreads = 512;
 constexpr int kQkWarp = 8, kPvWarp = 9;
-constexpr int kTmaWarp = 10;   // or, with 11, the queries
-constexpr int kQThreads = 64;
+constexpr int kTmaWarp = 10;   // or the queries
+constexpr int kPlanWarp = 11;  // the run's units, one after another
+constexpr int kQThreads = 32;
+constexpr int kUnitRing = 4;   // units that the roles may be apart
 constexpr int kLoadWarp = 12;  // to 15: V's rows or the loads, and the outputs
 constexpr int kLoadBar = 1;    // named barrier of the loading threads
 constexpr int kBlk = kTile * 128;  // 128 rows x 128 bytes
@@ -93,11 +95,23 @@ struct Cfg {
     static constexpr float kShift = KV == kBf16 ? 0.f : 11.f;
 };
 
+// One unit's share of a run, as the roles of the CTA see it: written to a ring by
+// one warp (all of them finding it for themselves made 144 KB of code, more than
+// an SM's instruction cache, and 2 us of a unit's time).
+struct Seg {
+    int32_t n;               // this run's tiles; 0: no more units
+    int32_t row, kvh;
+    int32_t first, m;        // its first new token, and how many
+    int32_t p0;              // position of the first query
+    int32_t i0, ns, tw;      // first tile; tiles of the sinks; first tile of the rest
+    int32_t slot;            // of the partial state, -1: the unit is whole
+};
 template <typename C>
 struct Bars {
     uint64_t kfull[C::NS], vfull[C::NS], ready[C::NS], empty[C::NS];
-    uint64_t sfull[2], sempty[2];
+    uint64_t sfull[2], sempty[2], unit_full[kUnitRing], unit_free[kUnitRing];
     uint64_t q_full, q_empty, s_full[2], s_free, p_full[2], pv_done[2], l_full[2], o_free[2], drain[2];
+    Seg unit[kUnitRing];
     int64_t place0, place1, start;  // the run, and where its first unit starts
     int64_t per;                    // the call's places: per * ctas + rest
     int32_t rest;
@@ -113,63 +127,9 @@ struct Bars {
     int64_t offset[C::kByTma ? 1 : 2][C::kByTma ? 1 : kTile];  // rows of a tile in the cache, -1: none
 };
 
-// One unit's share of a run.
-struct Seg {
-    int row, kvh, block;
-    Request x;
-    int64_t start;   // its first place
-    int cost, nt;    // its places and tiles
-    int i0, i1;      // this run's tiles
-    int p0, m;       // position of its first query, and its tokens
-    int ns, tw;      // tiles of the sinks; the first tile of the rest
-    bool begins;     // the run holds the unit's first place
-};
 __device__ __forceinline__ int token_of(const Seg& s, int i) {
-    return (i < s.ns ? i : i - s.ns + s.tw) * kTile;
-}
-__device__ __forceinline__ void shape(const PrefillArgs& a, Seg& s, int64_t place0,
-                                      int64_t place1) {
-    s.m = min(a.tb, s.x.n - s.block * a.tb);
-    s.p0 = s.x.T - s.x.n + s.block * a.tb;
-    const int hi = max(0, s.p0 + s.m);  // tokens up to the last query's own
-    const int lo = a.window > 0 ? max(0, s.p0 + 1 - a.window) : 0;
-    s.tw = min(lo, hi) / kTile;
-    const int sc = a.window > 0 ? min(a.sinks, lo) : 0;
-    s.ns = min((sc + kTile - 1) / kTile, s.tw);
-    s.nt = s.ns + (hi + kTile - 1) / kTile - s.tw;
-    s.cost = cost_of(a, s.x, s.block);
-    s.i0 = tile_at(place0 - s.start, s.cost, s.nt);
-    s.i1 = tile_at(place1 - s.start, s.cost, s.nt);
-    s.begins = place0 <= s.start;
-}
-// The run's first unit, or none (false).
-template <typename B_>
-__device__ __forceinline__ bool first_seg(const PrefillArgs& a, const B_& B, Seg& s) {
-    if (B.place0 >= B.place1) return false;
-    s.row = B.row;
-    s.kvh = B.kvh;
-    s.block = B.block;
-    s.start = B.start;
-    s.x = request_of(a, s.row);
-    shape(a, s, B.place0, B.place1);
-    return true;
-}
-template <typename B_>
-__device__ __forceinline__ bool next_seg(const PrefillArgs& a, const B_& B, Seg& s) {
-    s.start += s.cost;
-    if (s.start >= B.place1) return false;
-    if (++s.block >= blocks_of(a, s.x.n)) {
-        s.block = 0;
-        if (++s.kvh >= a.kv_heads) {
-            s.kvh = 0;
-            do {  // the next request with a new token; there is one
-                if (++s.row >= a.rows) return false;
-                s.x = request_of(a, s.row);
-            } while (s.x.n == 0);
-        }
-    }
-    shape(a, s, B.place0, B.place1);
-    return true;
+    const int j = s.i0 + i;
+    return (j < s.ns ? j : j - s.ns + s.tw) * kTile;
 }
 // Whether any query of the unit sees token t.
 __device__ __forceinline__ bool any_sees(const PrefillArgs& a, const Seg& s, int t) {
@@ -466,6 +426,33 @@ __device__ __forceinline__ int turn_of(int t, int u) {
     return t * C::kSubs + u;
 }
 
+// As hs::mbar_wait_bounded, in a dozen instructions (there are many waits).
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, uint64_t timeout_ns,
+                                             uint32_t abort_flag) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 t0, t;\n\t.reg .b32 f;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE%=;\n\t"
+        "mov.u64 t0, %%globaltimer;\n"
+        "AGAIN%=:\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE%=;\n\t"
+        "ld.volatile.shared::cta.b32 f, [%4];\n\t"
+        "setp.ne.b32 q, f, 0;\n\t"
+        "@q bra DONE%=;\n\t"
+        "mov.u64 t, %%globaltimer;\n\t"
+        "sub.u64 t, t, t0;\n\t"
+        "setp.gt.u64 q, t, %3;\n\t"
+        "@!q bra AGAIN%=;\n"
+        "DONE%=:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "l"(timeout_ns), "r"(abort_flag)
+        : "memory");
+    return ok != 0;
+}
+
 // What every role of the CTA knows.
 template <typename C>
 struct Cta {
@@ -475,7 +462,8 @@ struct Cta {
     unsigned char* smem;
     uint32_t sb, tmem;
     __device__ __forceinline__ bool wait(uint64_t* bar, int phase) const {
-        return hs::mbar_wait_bounded(bar, uint32_t(phase & 1), ta.timeout_ns, &B.abort);
+        return wait_bounded(hs::smem_u32(bar), uint32_t(phase & 1), ta.timeout_ns,
+                            hs::smem_u32(const_cast<int32_t*>(&B.abort)));
     }
     // By all lanes of a warp.
     __device__ __forceinline__ bool wait_all(uint64_t* bar, int phase) const {
@@ -484,6 +472,16 @@ struct Cta {
     // The product of query tile w's n-th P is done.
     __device__ __forceinline__ bool pv_wait(int w, int n) const {
         return C::NQ == 2 ? wait_all(&B.pv_done[w], n) : wait_all(&B.pv_done[n & 1], n >> 1);
+    }
+    // The k-th unit of the run (all lanes); false: no more, or ok = false.
+    __device__ __forceinline__ bool next_unit(int k, Seg& s, bool& ok) const {
+        if (!ok) return false;
+        ok = wait_all(&B.unit_full[k % kUnitRing], k / kUnitRing);
+        if (!ok) return false;
+        s = B.unit[k % kUnitRing];
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) hs::mbar_arrive(&B.unit_free[k % kUnitRing]);
+        return s.n > 0;
     }
     __device__ __forceinline__ void give_up() const {
         hs::set_status(a.status, HS_ERR_TIMEOUT);
@@ -507,40 +505,11 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
     const int tok = r / a.group, hd = r - tok * a.group;  // its new token and query head
     const uint32_t o_addr = tmem + lanes + C::kOCol + uint32_t(NQ == 2 ? w * 128 : 0);
     bool ok = true;
-    int t = 0, mine = 0, units = 0;  // the CTA's tiles, this tile's, units with tiles
-    int own = 0;                     // and those with this query tile
-    bool head = false;               // the run ends in the first part of a shared unit
+    int t = 0, mine = 0;  // the CTA's tiles, this query tile's
+    int own = 0;          // units with this query tile
     Seg s;
-    for (bool more = first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
-        const int n = s.i1 - s.i0;
-        const bool live = tok < a.tq && w * a.tq + tok < s.m;
-        const int64_t qh = int64_t(s.x.first + s.block * a.tb + w * a.tq + tok) * a.heads +
-                           s.kvh * a.group + hd;
-        if (n == 0) {
-            if (s.nt == 0 && s.begins && live) {
-                // Nothing is attended to: zeros.
-                for (int i = 0; i < D / 8; ++i)
-                    reinterpret_cast<uint4*>(a.out)[qh * (D / 8) + i] = make_uint4(0u, 0u, 0u, 0u);
-                if (a.lse != nullptr) a.lse[qh] = -CUDART_INF_F;
-            }
-            continue;
-        }
-        const bool whole = s.i0 == 0 && s.i1 == s.nt;
-        if (w == 0 && tid == 0 && !whole && s.i0 == 0) {
-            head = true;
-            SharedUnit u;
-            u.start = s.start;
-            u.per = B.per;
-            u.rest = B.rest;
-            u.cost = s.cost;
-            u.tiles = s.nt;
-            u.first = s.x.first + s.block * a.tb;
-            u.tokens = s.m;
-            u.kvh = s.kvh;
-            u.valid = 1;
-            a.shared[blockIdx.x] = u;
-        }
-        const int useg = units++;
+    for (int unit = 0; cx.next_unit(unit, s, ok); ++unit) {
+        const int n = s.n;
         if (w * a.tq >= s.m) {  // the second tile of a unit that has one
             t += n;
             continue;
@@ -566,7 +535,7 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
             if (first) {
                 // (0 would turn masked places into NaN; 2^-126 does not show.)
                 if constexpr (E4) {
-                    scl *= pow2(-B.qexp[useg & (C::kSegRing - 1)][w * kTile + r]);
+                    scl *= pow2(-B.qexp[unit & (C::kSegRing - 1)][w * kTile + r]);
                     if (a.k_scale != nullptr) scl *= a.k_scale[s.kvh];
                 }
                 if (scl == 0.f) scl = 1.17549435e-38f;
@@ -666,16 +635,15 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
             }
             // Mostly the reference stays: the weights are made while the
             // maximum is found, and the first half again where it moved.
-            const bool ahead = !part && !first && scl > 0.f;
+            bool ahead = !part && !first && scl > 0.f;
             if (!ahead) raise();
-            refer();
-            weigh(0);
-            weigh(1);
-            if (ahead && raise()) {
+            for (;;) {
                 refer();
                 s0 = s1 = 0;
                 weigh(0);
                 weigh(1);
+                if (!ahead || !raise()) break;
+                ahead = false;
             }
             if (!ok) break;
             weigh(2);
@@ -723,6 +691,7 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
                             const void* row = static_cast<const char*>(a.v) +
                                 (page * a.page_stride + int64_t(tk - b * a.page_size) * a.row_stride +
                                  s.kvh * a.head_stride) * (E4 ? 1 : 2);
+#pragma unroll 1
                             for (int c = u * C::kDims; c < (u + 1) * C::kDims; c += 16) {
                                 float o[16];
                                 hs::tc::tmem_ld16(o_addr + uint32_t(c), o);
@@ -749,22 +718,22 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
         ++own;
         const float2 ls = split(add2(l0, l1));
         const float l = ls.x + ls.y;
+        const bool live = tok < a.tq && w * a.tq + tok < s.m;
         float f = 1.f;
-        if (whole) {
+        if (s.slot < 0) {
             f = l == 0.f ? 0.f : 1.f / l;
             if (a.v_scale != nullptr && l != 0.f) f *= a.v_scale[s.kvh];
             if (live && a.lse != nullptr)
-                a.lse[qh] = l == 0.f ? -CUDART_INF_F : (off + log2f(l)) * kLn2;
+                a.lse[int64_t(s.first + w * a.tq + tok) * a.heads + s.kvh * a.group + hd] =
+                    l == 0.f ? -CUDART_INF_F : (off + log2f(l)) * kLn2;
         } else if (live) {
-            const int64_t slot = 2 * int(blockIdx.x) + (s.start < B.place0 ? 0 : 1);
-            reinterpret_cast<float2*>(a.part_ml)[slot * a.unit_rows + w * kTile + r] =
+            reinterpret_cast<float2*>(a.part_ml)[int64_t(s.slot) * a.unit_rows + w * kTile + r] =
                 make_float2(off, l);
         }
         B.factor[w][r] = f;
         hs::mbar_arrive(&B.l_full[w]);
     }
     if (!ok) cx.give_up();
-    if (tid == 0 && !head) a.shared[blockIdx.x].valid = 0;
 }
 
 // -------------------------------- products --------------------------------
@@ -787,11 +756,10 @@ __device__ __forceinline__ bool qk_role(const Cta<C>& cx) {
     const uint64_t q_desc = hs::tc::sdesc_sw128(sb, 16, 1024);
     const uint64_t k_desc = hs::tc::sdesc_sw128(sb + C::kRingOff, 16, 1024);
     int t = 0, segs = 0, n_qk = 0;
-    for (bool more = first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
-        const int n = s.i1 - s.i0;
-        if (n == 0) continue;
+    for (; cx.next_unit(segs, s, ok); ++segs) {
+        const int n = s.n;
         const int tiles = NQ == 2 && a.tq < s.m ? 2 : 1;
-        ok = ok && cx.wait_all(&B.q_full, segs++);
+        ok = ok && cx.wait_all(&B.q_full, segs);
         for (int i = 0; i < n && ok; ++i, ++t) {
             uint32_t at[kSubs];
 #pragma unroll
@@ -841,9 +809,8 @@ __device__ __forceinline__ bool pv_role(const Cta<C>& cx) {
     constexpr uint32_t id = idesc<KV>(C::kDims, 1);
     const uint64_t v_desc = hs::tc::sdesc_sw128(sb + C::kRingOff, kBlk, 1024);
     int t = 0, done0 = 0, done1 = 0, had0 = 0, had1 = 0;
-    for (bool more = first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
-        const int n = s.i1 - s.i0;
-        if (n == 0) continue;
+    for (int unit = 0; cx.next_unit(unit, s, ok); ++unit) {
+        const int n = s.n;
         const int tiles = NQ == 2 && a.tq < s.m ? 2 : 1;
         // The outputs before have been read.
         if (had0 > 0) ok = ok && cx.wait_all(&B.o_free[0], had0 - 1);
@@ -903,8 +870,7 @@ __device__ __forceinline__ bool tma_role(const Cta<C>& cx, const CUtensorMap& qm
     bool ok = true, bad = false;
     int t = 0, seq = 0, segs = 0;
     Seg s;
-    for (bool more = first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
-        if (s.i1 == s.i0) continue;
+    for (int unit = 0; cx.next_unit(unit, s, ok); ++unit) {
         if constexpr (!C::kConvert) {
             // A box takes the heads of a KV head for a tile's tokens: its rows are
             // the tile's.  (Tokens of other requests behind a unit's own land in
@@ -918,11 +884,11 @@ __device__ __forceinline__ bool tma_role(const Cta<C>& cx, const CUtensorMap& qm
                 for (int w = 0; w < tiles; ++w)
                     for (int c = 0; c < C::kD / 64; ++c)
                         tma_load_q(cx.sb + w * C::kQTile + c * kBlk, &qmap, c * 64, s.kvh * a.group,
-                                   s.x.first + s.block * a.tb + w * a.tq, &B.q_full);
+                                   s.first + w * a.tq, &B.q_full);
             }
             __syncwarp();
         }
-        for (int i = s.i0; i < s.i1 && ok; ++i, ++t) {
+        for (int i = 0; i < s.n && ok; ++i, ++t) {
             const int t0 = token_of(s, i), tok = t0 + lane * bt;
             const int b = block_of(a, tok);
             const bool wants = lane < runs && any_sees(a, s, tok, bt);
@@ -1008,7 +974,7 @@ __device__ __forceinline__ void load_queries(const Cta<C>& cx, const Seg& s, int
     const int hstep = kRowStep % a.group, tstep = kRowStep / a.group;
     const int tok0 = row0 / a.group, hd0 = row0 - tok0 * a.group;
     const char* q = static_cast<const char*>(a.q) +
-                    ((s.x.first + s.block * a.tb) * a.q_stride + int64_t(s.kvh) * a.group * D + ch * 8) * 2;
+                    (s.first * a.q_stride + int64_t(s.kvh) * a.group * D + ch * 8) * 2;
 #pragma unroll 1
     for (int w = 0; w < C::NQ; ++w) {
         int tok = tok0, hd = hd0;
@@ -1062,14 +1028,13 @@ __device__ __forceinline__ void load_queries(const Cta<C>& cx, const Seg& s, int
 template <typename C>
 __device__ __forceinline__ bool query_role(const Cta<C>& cx) {
     const int ti = threadIdx.x - kTmaWarp * 32;
-    int segs = 0;
+    bool ok = true;
     Seg s;
-    for (bool more = first_seg(cx.a, cx.B, s); more; more = next_seg(cx.a, cx.B, s)) {
-        if (s.i1 == s.i0) continue;
-        if (segs > 0 && !cx.wait_all(&cx.B.q_empty, segs - 1)) return false;
-        load_queries<C, kQThreads>(cx, s, ti, segs++);
+    for (int unit = 0; cx.next_unit(unit, s, ok); ++unit) {
+        if (unit > 0) ok = cx.wait_all(&cx.B.q_empty, unit - 1);
+        if (ok) load_queries<C, kQThreads>(cx, s, ti, unit);
     }
-    return true;
+    return ok;
 }
 
 // --------------------------------- output ---------------------------------
@@ -1078,24 +1043,22 @@ __device__ __forceinline__ bool query_role(const Cta<C>& cx) {
 struct Written {
     int n = 0;              // tiles of the unit; 0: none to write
     int tiles, m, kvh;      // query tiles, tokens
-    int64_t first, slot;    // first token; slot of the partial state, -1: whole
+    int first, slot;        // first token; slot of the partial state, -1: whole
     int units[2] = {0, 0}, products[2] = {0, 0};  // of each query tile, up to this unit
 };
-__device__ __forceinline__ Written unit_to_write(const PrefillArgs& a, const Seg& s, int64_t place0,
-                                                 int tiles, const Written& before) {
-    Written d = before;
-    d.n = s.i1 - s.i0;
+__device__ __forceinline__ void unit_to_write(const Seg& s, int tiles, Written& d) {
+    d.n = s.n;
     d.tiles = tiles;
     d.m = s.m;
     d.kvh = s.kvh;
-    d.first = s.x.first + s.block * a.tb;
-    d.slot = s.i0 == 0 && s.i1 == s.nt ? -1 : 2 * int(blockIdx.x) + (s.start < place0 ? 0 : 1);
+    d.first = s.first;
+    d.slot = s.slot;
+#pragma unroll
     for (int w = 0; w < 2; ++w)
         if (w < tiles) {
             ++d.units[w];
-            d.products[w] += d.n;
+            d.products[w] += s.n;
         }
-    return d;
 }
 template <typename C>
 __device__ __forceinline__ bool write_unit(const Cta<C>& cx, const Written& d) {
@@ -1114,9 +1077,9 @@ __device__ __forceinline__ bool write_unit(const Cta<C>& cx, const Written& d) {
         const uint32_t o_addr = cx.tmem + lanes + C::kOCol + uint32_t(w * 128);
         const bool live = tok < a.tq && w * a.tq + tok < d.m;
         const float f = B.factor[w][r];
-        const int64_t qh = (d.first + w * a.tq + tok) * a.heads + d.kvh * a.group + hd;
+        const int64_t qh = int64_t(d.first + w * a.tq + tok) * a.heads + d.kvh * a.group + hd;
         uint16_t* to = static_cast<uint16_t*>(a.out) + qh * D;
-        float* po = a.part_o + ((d.slot * (D / 8)) * a.unit_rows + w * kTile + r) * 8;
+        float* po = a.part_o + (int64_t(d.slot) * (D / 8) * a.unit_rows + w * kTile + r) * 8;
         // A row per thread: 32 bytes of each of 32 rows at a time.  (Pieces
         // exchanged between lanes for whole lines: five times as long.)
 #pragma unroll 1
@@ -1176,9 +1139,8 @@ __device__ __forceinline__ bool check_role(const Cta<C>& cx) {
     int t = 0;
     Written done;
     Seg s;
-    for (bool more = first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
-        if (s.i1 == s.i0) continue;
-        for (int i = s.i0; i < s.i1 && ok; ++i, ++t) {
+    for (int unit = 0; cx.next_unit(unit, s, ok); ++unit) {
+        for (int i = 0; i < s.n && ok; ++i, ++t) {
             for (int u = 0; u < C::kSubs; ++u) {
                 const int q = unit_of<C>(t, true, u), turn = turn_of<C>(t, u);
                 ok = cx.wait_all(&B.vfull[turn % NS], turn / NS);
@@ -1206,9 +1168,9 @@ __device__ __forceinline__ bool check_role(const Cta<C>& cx) {
                 if (lane == 0) hs::mbar_arrive(&B.ready[turn % NS]);
             }
             // The unit before, while this one's first tile is in its softmax.
-            if (ok && i == s.i0 && done.n > 0) ok = write_unit(cx, done);
+            if (ok && i == 0 && done.n > 0) ok = write_unit(cx, done);
         }
-        done = unit_to_write(a, s, B.place0, C::NQ == 2 && a.tq < s.m ? 2 : 1, done);
+        unit_to_write(s, C::NQ == 2 && a.tq < s.m ? 2 : 1, done);
     }
     return ok && (done.n == 0 || write_unit(cx, done));
 }
@@ -1241,15 +1203,14 @@ __device__ __forceinline__ bool convert_role(const Cta<C>& cx) {
     // the banks.
     const int c0 = 2 * ch + (ch >= 4 ? 1 : 0), c1 = 2 * ch + (ch >= 4 ? 0 : 1);
     bool ok = true;
-    int t = 0, seq = 0, segs = 0;
+    int t = 0, seq = 0;
     Written done;
     Seg s;
-    for (bool more = first_seg(a, B, s); more && ok; more = next_seg(a, B, s)) {
-        if (s.i1 == s.i0) continue;
-        if (segs > 0) ok = cx.wait_all(&B.q_empty, segs - 1);
+    for (int unit = 0; cx.next_unit(unit, s, ok); ++unit) {
+        if (unit > 0) ok = cx.wait_all(&B.q_empty, unit - 1);
         if (!ok) break;
-        load_queries<C, 128>(cx, s, lt, segs++);
-        for (int i = s.i0; i < s.i1 && ok; ++i, ++t) {
+        load_queries<C, 128>(cx, s, lt, unit);
+        for (int i = 0; i < s.n && ok; ++i, ++t) {
             for (int u = 0; u < 2 * C::kSubs; ++u, ++seq) {
                 const bool v = u >= C::kSubs;
                 const int turn = turn_of<C>(t, u % C::kSubs), slot = seq % NS;
@@ -1299,9 +1260,9 @@ __device__ __forceinline__ bool convert_role(const Cta<C>& cx) {
                 hs::fence_proxy_async_shared();
                 hs::mbar_arrive(v ? &B.ready[turn % NS] : &B.kfull[turn % NS]);
             }
-            if (ok && i == s.i0 && done.n > 0) ok = write_unit(cx, done);
+            if (ok && i == 0 && done.n > 0) ok = write_unit(cx, done);
         }
-        done = unit_to_write(a, s, B.place0, C::NQ == 2 && a.tq < s.m ? 2 : 1, done);
+        unit_to_write(s, C::NQ == 2 && a.tq < s.m ? 2 : 1, done);
     }
     return ok && (done.n == 0 || write_unit(cx, done));
 }
@@ -1408,11 +1369,14 @@ __device__ __forceinline__ bool load_role(const Cta<C>& cx) {
     };
     Written done;
     bool run = true;  // alike in all threads
-    for (bool more = first_seg(a, B, s); more && run; more = next_seg(a, B, s)) {
-        if (s.i0 == s.i1) continue;
-        rows_of(t, s.i0);
+    for (int unit = 0; run; ++unit) {
+        // (All or none: they meet at barriers.)
+        bool more = cx.next_unit(unit, s, ok);
+        run = !hs::pair::named_sync_or(kLoadBar, kTile, !ok);
+        if (!run || !more) break;
+        rows_of(t, 0);
         load(t, false, 0, buf[0]);
-        for (int i = s.i0; i < s.i1 && run; ++i, ++t) {
+        for (int i = 0; i < s.n && run; ++i, ++t) {
             const uint4 ld = *reinterpret_cast<const uint4*>(B.loaded[t & (C::kRing - 1)]);
             const bool part = !all_see(a, s, token_of(s, i)) ||
                               (ld.x & ld.y & ld.z & ld.w) != 0xffffffffu;
@@ -1425,7 +1389,7 @@ __device__ __forceinline__ bool load_role(const Cta<C>& cx) {
                 if (j % kBatches == 0 && run) run = wait_empty(t, v);
                 if (j + 1 < 2 * kBatches) {
                     load(t, j + 1 >= kBatches, (j + 1) % kBatches, buf[(j + 1) & 1]);
-                } else if (i + 1 < s.i1) {
+                } else if (i + 1 < s.n) {
                     rows_of(t + 1, i + 1);
                     load(t + 1, false, 0, buf[0]);
                 }
@@ -1435,13 +1399,103 @@ __device__ __forceinline__ bool load_role(const Cta<C>& cx) {
                 }
             }
             // (A warp that gives up says so where all meet next.)
-            if (run && i == s.i0 && done.n > 0) ok = write_unit(cx, done) && ok;
+            if (run && i == 0 && done.n > 0) ok = write_unit(cx, done) && ok;
         }
-        done = unit_to_write(a, s, B.place0, C::NQ == 2 && a.tq < s.m ? 2 : 1, done);
+        unit_to_write(s, C::NQ == 2 && a.tq < s.m ? 2 : 1, done);
     }
     ok = ok && run;
     if (ok && done.n > 0) ok = write_unit(cx, done);
     if (bad) hs::set_status(a.status, HS_ERR_BAD_INDEX);
+    return ok;
+}
+
+// --------------------------------- units ----------------------------------
+// Walks the run's units; writes zeros where a unit's queries see nothing.
+template <typename C>
+__device__ __forceinline__ bool plan_role(const Cta<C>& cx) {
+    constexpr int D = C::kD;
+    const PrefillArgs& a = cx.a;
+    Bars<C>& B = cx.B;
+    const int lane = threadIdx.x & 31;
+    const int64_t place0 = B.place0, place1 = B.place1;
+    int64_t start = B.start;
+    int row = B.row, kvh = B.kvh, block = B.block, unit = 0;
+    bool ok = true, head = false;
+    const auto publish = [&](const Seg& s) {
+        if (unit >= kUnitRing)
+            ok = cx.wait_all(&B.unit_free[unit % kUnitRing], unit / kUnitRing - 1);
+        if (ok && lane == 0) {
+            B.unit[unit % kUnitRing] = s;
+            hs::mbar_arrive(&B.unit_full[unit % kUnitRing]);
+        }
+        __syncwarp();
+        ++unit;
+    };
+    if (place0 < place1) {
+        Request x = request_of(a, row);
+        int blocks = blocks_of(a, x.n);
+        while (ok) {
+            Seg s;
+            s.row = row;
+            s.kvh = kvh;
+            s.first = x.first + block * a.tb;
+            s.m = min(a.tb, x.n - block * a.tb);
+            s.p0 = x.T - x.n + block * a.tb;
+            const int hi = max(0, s.p0 + s.m);  // tokens up to the last query's own
+            const int lo = a.window > 0 ? max(0, s.p0 + 1 - a.window) : 0;
+            s.tw = min(lo, hi) / kTile;
+            const int sc = a.window > 0 ? min(a.sinks, lo) : 0;
+            s.ns = min((sc + kTile - 1) / kTile, s.tw);
+            const int nt = s.ns + (hi + kTile - 1) / kTile - s.tw;
+            const int cost = cost_of(a, x, block);
+            s.i0 = tile_at(place0 - start, cost, nt);
+            const int i1 = tile_at(place1 - start, cost, nt);
+            s.n = i1 - s.i0;
+            s.slot = s.i0 == 0 && i1 == nt ? -1 : 2 * int(blockIdx.x) + (start < place0 ? 0 : 1);
+            if (s.n > 0) {
+                if (s.slot >= 0 && s.i0 == 0) {
+                    head = true;
+                    SharedUnit u;
+                    u.start = start;
+                    u.per = B.per;
+                    u.rest = B.rest;
+                    u.cost = cost;
+                    u.tiles = nt;
+                    u.first = s.first;
+                    u.tokens = s.m;
+                    u.kvh = kvh;
+                    u.valid = 1;
+                    if (lane == 0) a.shared[blockIdx.x] = u;
+                }
+                publish(s);
+            } else if (nt == 0 && place0 <= start) {
+                // Nothing is attended to: zeros.
+                for (int r = lane; r < s.m * a.group; r += 32) {
+                    const int64_t qh = int64_t(s.first + r / a.group) * a.heads + kvh * a.group + r % a.group;
+                    for (int i = 0; i < D / 8; ++i)
+                        static_cast<uint4*>(a.out)[qh * (D / 8) + i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (a.lse != nullptr) a.lse[qh] = -CUDART_INF_F;
+                }
+            }
+            start += cost;
+            if (start >= place1) break;
+            if (++block < blocks) continue;
+            block = 0;
+            if (++kvh < a.kv_heads) continue;
+            kvh = 0;
+            do {  // the next request with a new token; there is one
+                if (++row >= a.rows) break;
+                x = request_of(a, row);
+            } while (x.n == 0);
+            if (row >= a.rows) break;
+            blocks = blocks_of(a, x.n);
+        }
+    }
+    if (ok) {
+        Seg end{};
+        publish(end);
+    }
+    if (!head && lane == 0) a.shared[blockIdx.x].valid = 0;
     return ok;
 }
 
@@ -1479,6 +1533,10 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
             hs::mbar_init(&B.l_full[i], kTile);
             hs::mbar_init(&B.o_free[i], kTile);
             hs::mbar_init(&B.drain[i], 1);
+        }
+        for (int i = 0; i < kUnitRing; ++i) {
+            hs::mbar_init(&B.unit_full[i], 1);
+            hs::mbar_init(&B.unit_free[i], 4 * C::NQ + 3 + 4);  // a warp each
         }
         B.abort = 0;
         hs::fence_mbar_init();
@@ -1518,8 +1576,10 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
             commit(&B.drain[warp - kQkWarp]);
             hs::mbar_wait_bounded(&B.drain[warp - kQkWarp], 0, ta.timeout_ns, nullptr);
             __syncwarp();
+        } else if (warp == kPlanWarp) {
+            if (!plan_role<C>(cx)) cx.give_up();
         } else if constexpr (C::kByTma) {
-            if (warp == kTmaWarp && !tma_role<C>(cx, qmap, kmap, vmap)) cx.give_up();
+            if (!tma_role<C>(cx, qmap, kmap, vmap)) cx.give_up();
         } else {
             if (!query_role<C>(cx)) cx.give_up();
         }
