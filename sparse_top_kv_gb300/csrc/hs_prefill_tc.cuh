@@ -76,8 +76,8 @@ struct Cfg {
     static constexpr int kSubs = D / kDims;                // ring units of a tile
     static constexpr int kUnit = kTile * kDims * 2;
     static constexpr int kQTile = kTile * D * 2;
-    static constexpr int NS = D == 64 ? 8 : kByTma && !kE4 ? 5 : 4;  // ring units
-    static constexpr int kStages = kConvert ? 2 : 0, kStage = kTile * kDims;
+    static constexpr int NS = D == 64 ? 8 : kConvert ? 3 : kByTma ? 5 : 4;  // ring units
+    static constexpr int kStages = kConvert ? 4 : 0, kStage = kTile * kDims;
     static constexpr int kRing = 8;        // tiles whose loaded tokens are remembered
     static constexpr int kSegRing = D == 256 ? 4 : 2;  // units whose query scales are
     static constexpr int kRingOff = NQ * kQTile;       // (queries first)
@@ -109,7 +109,7 @@ struct Seg {
 template <typename C>
 struct Bars {
     uint64_t kfull[C::NS], vfull[C::NS], ready[C::NS], empty[C::NS];
-    uint64_t sfull[2], sempty[2], unit_full[kUnitRing], unit_free[kUnitRing];
+    uint64_t sfull[4], sempty[4], unit_full[kUnitRing], unit_free[kUnitRing];
     uint64_t q_full, q_empty, s_full[2], s_free, p_full[2], pv_done[2], l_full[2], o_free[2], drain[2];
     Seg unit[kUnitRing];
     int64_t place0, place1, start;  // the run, and where its first unit starts
@@ -118,7 +118,6 @@ struct Bars {
     int32_t row, kvh, block;        // the run's first unit
     uint32_t tmem_base;
     volatile int32_t abort;
-    volatile int32_t keep[2];                     // O holds something before the first product
     alignas(16) uint32_t loaded[C::kRing][4];     // tokens of a tile that were loaded
     int2 tile[C::kRing];                          // its first token; whether some query does not see all of it
     alignas(16) uint32_t odd[C::kRing][C::kSubs][4];  // rows of V that were taken out, by ring unit
@@ -489,6 +488,47 @@ struct Cta {
     }
 };
 
+// Rows of V that were taken out of a tile, into a row's output: P stands until the
+// next one is written, O has the other rows' products.  Apart from the softmax's
+// code and registers: it hardly ever runs.
+template <int KV, int D>
+__device__ __noinline__ void add_odd_rows(const PrefillArgs* ap, const uint32_t* odd, uint4 vis,
+                                          int t0, int row, int kvh, uint32_t o_addr,
+                                          uint32_t p_addr) {
+    constexpr int kDims = D < 128 ? D : 128;
+    const PrefillArgs& a = *ap;
+#pragma unroll 1
+    for (int j = 0; j < kTile; ++j) {
+        const uint32_t pw = tmem_ld1(p_addr + uint32_t(j >> 1));
+        hs::tc::tmem_wait_ld();
+        const uint32_t h = (j & 1) ? pw >> 16 : pw & 0xffffu;
+        const float p = KV == kBf16 ? __uint_as_float(h << 16)
+                                    : __half2float(__ushort_as_half(uint16_t(h)));
+        const uint32_t vw = j < 32 ? vis.x : j < 64 ? vis.y : j < 96 ? vis.z : vis.w;
+        const bool sees = (vw >> (j & 31)) & 1u;
+#pragma unroll 1
+        for (int u = 0; u < D / kDims; ++u) {
+            if (!((odd[u * 4 + (j >> 5)] >> (j & 31)) & 1u)) continue;
+            const int tk = t0 + j, b = block_of(a, tk);
+            const int64_t page = a.block_table[row * a.bt_stride + b];
+            const void* from = static_cast<const char*>(a.v) +
+                               (page * a.page_stride + int64_t(tk - b * a.page_size) * a.row_stride +
+                                kvh * a.head_stride) * (KV == kE4m3 ? 1 : 2);
+#pragma unroll 1
+            for (int c = u * kDims; c < (u + 1) * kDims; c += 16) {
+                float o[16];
+                hs::tc::tmem_ld16(o_addr + uint32_t(c), o);
+                hs::tc::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (sees) o[e] = fmaf(p, element<KV>(from, c + e), o[e]);
+                hs::tc::tmem_st16(o_addr + uint32_t(c), o);
+                hs::tc::tmem_wait_st();
+            }
+        }
+    }
+}
+
 // -------------------------------- softmax ---------------------------------
 // A warpgroup per query tile, a thread per row.
 template <typename C>
@@ -507,10 +547,59 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
     bool ok = true;
     int t = 0, mine = 0;  // the CTA's tiles, this query tile's
     int own = 0;          // units with this query tile
+    bool pending = false;  // a unit's output waits for its last product
+    // Whether rows of the last tile's V may have been taken out; which tile it was,
+    // and the row's position, its request and KV head.
+    bool odd = false;
+    int odd_tile = 0, odd_pos = 0, odd_row = 0, odd_kvh = 0;
+    // Tokens of the CTA's tile t that a query at position pos sees.
+    const auto see = [&](int t, int pos, uint32_t (&vis)[4]) {
+        const uint4 ld = *reinterpret_cast<const uint4*>(B.loaded[t & (C::kRing - 1)]);
+        const int t0 = B.tile[t & (C::kRing - 1)].x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int b = t0 + 32 * j;
+            vis[j] = low_bits(pos + 1 - b) & (j == 0 ? ld.x : j == 1 ? ld.y : j == 2 ? ld.z : ld.w);
+            if (a.window > 0)
+                vis[j] &= ~low_bits(pos - a.window + 1 - b) | low_bits(a.sinks - b);
+        }
+    };
+    // Rows of the last tile's V that were taken out, into the queries that see
+    // them.
+    const auto clear_odd = [&] {
+        uint32_t any = 0;
+        for (int u = 0; u < kSubs && ok; ++u) {
+            const int q = turn_of<C>(odd_tile, u);
+            ok = cx.wait_all(&B.ready[q % NS], q / NS);
+            const uint4 o = *reinterpret_cast<const uint4*>(B.odd[odd_tile & (C::kRing - 1)][u]);
+            any |= o.x | o.y | o.z | o.w;
+        }
+        odd = false;
+        if (any == 0 || !ok) return;
+        ok = cx.pv_wait(w, mine - 1);
+        hs::tc::fence_after_sync();
+        uint32_t vis[4];
+        see(odd_tile, odd_pos, vis);
+        add_odd_rows<KV, D>(&a, &B.odd[odd_tile & (C::kRing - 1)][0][0], make_uint4(vis[0], vis[1], vis[2], vis[3]),
+                            B.tile[odd_tile & (C::kRing - 1)].x, odd_row, odd_kvh, o_addr,
+                            tmem + lanes + (NQ == 2 ? C::kPCol + uint32_t(w * 64)
+                                                    : uint32_t(((mine - 1) & 1) * 128)));
+    };
+    // The last tile's product has read P and is in O.
+    const auto finish = [&] {
+        ok = cx.pv_wait(w, mine - 1);
+        if (pending) {
+            hs::tc::fence_before_sync();
+            hs::mbar_arrive(&B.l_full[w]);
+        }
+        pending = false;
+    };
     Seg s;
     for (int unit = 0; cx.next_unit(unit, s, ok); ++unit) {
         const int n = s.n;
         if (w * a.tq >= s.m) {  // the second tile of a unit that has one
+            if (odd) clear_odd();
+            if (pending) finish();
             t += n;
             continue;
         }
@@ -526,7 +615,8 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
             const int ph = NQ == 2 ? mine : mine >> 1;
             const uint32_t s_addr = tmem + lanes + uint32_t(NQ == 2 ? 0 : x * 128);
             const uint32_t p_addr = NQ == 2 ? tmem + lanes + C::kPCol + uint32_t(w * 64) : s_addr;
-            ok = cx.wait_all(&B.s_full[x], ph);
+            if (odd) clear_odd();
+            ok = ok && cx.wait_all(&B.s_full[x], ph);
             if (!ok) break;
             hs::tc::fence_after_sync();
             float v[128];
@@ -542,7 +632,6 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
             }
             const bool part = B.tile[t & (C::kRing - 1)].y != 0;
             const float as = fabsf(scl);
-            uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
             hs::tc::tmem_wait_ld();
             if (NQ == 2) {
                 hs::tc::fence_before_sync();
@@ -553,20 +642,15 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
                 for (int c = 0; c < 128; ++c) v[c] = -v[c];
             }
             if (part) {
-                // What this row sees of the tile.
-                const uint4 ld = *reinterpret_cast<const uint4*>(B.loaded[t & (C::kRing - 1)]);
-                const int t0 = B.tile[t & (C::kRing - 1)].x;
+                // What this row sees of the tile, 32 tokens at a time.
+                uint32_t vis[4];
+                see(t, pos, vis);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int b = t0 + 32 * j;
-                    const uint32_t lw = j == 0 ? ld.x : j == 1 ? ld.y : j == 2 ? ld.z : ld.w;
-                    vis[j] = low_bits(pos + 1 - b) & lw;
-                    if (a.window > 0)
-                        vis[j] &= ~low_bits(pos - a.window + 1 - b) | low_bits(a.sinks - b);
+                for (int j = 0; j < 4; ++j)
+                    if (__any_sync(0xffffffffu, vis[j] != 0xffffffffu))
 #pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        if (!((vis[j] >> c) & 1u)) v[32 * j + c] = -CUDART_INF_F;
-                }
+                        for (int c = 0; c < 32; ++c)
+                            if (!((vis[j] >> c) & 1u)) v[32 * j + c] = -CUDART_INF_F;
             }
             uint64_t as2, ref2, s0 = 0, s1 = 0;
             const auto refer = [&] {
@@ -628,10 +712,16 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
                 }
                 return true;
             };
-            // The products of the tile before have read P and are in O.
-            if (NQ == 2 && mine > 0) {
-                ok = cx.pv_wait(w, mine - 1);
+            if (mine > 0 && (NQ == 2 || pending)) {
+                finish();
                 hs::tc::fence_after_sync();
+            }
+            if (part) {
+                odd = true;
+                odd_tile = t;
+                odd_pos = pos;
+                odd_row = s.row;
+                odd_kvh = s.kvh;
             }
             // Mostly the reference stays: the weights are made while the
             // maximum is found, and the first half again where it moved.
@@ -651,63 +741,6 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
             l0 = add2(l0, s0);
             l1 = add2(l1, s1);
             hs::tc::tmem_wait_st();
-            if (part) {
-                // Rows of V that were taken out.
-                uint32_t any = 0;
-                for (int u = 0; u < kSubs && ok; ++u) {
-                    const int q = turn_of<C>(t, u);
-                    ok = cx.wait_all(&B.ready[q % NS], q / NS);
-                    const uint4 o = *reinterpret_cast<const uint4*>(B.odd[t & (C::kRing - 1)][u]);
-                    any |= o.x | o.y | o.z | o.w;
-                }
-                if (!ok) break;
-                if (first) B.keep[w] = any != 0;
-                if (any != 0) {
-                    if (NQ == 1 && !first) {
-                        ok = cx.pv_wait(w, mine - 1);
-                        if (!ok) break;
-                        hs::tc::fence_after_sync();
-                    }
-                    // (The output before has been read.)
-                    if (first && own > 0) ok = cx.wait_all(&B.o_free[w], own - 1);
-                    if (!ok) break;
-                    hs::tc::fence_after_sync();
-                    const float zero[16] = {};
-                    if (first)
-                        for (int c = 0; c < D; c += 16) hs::tc::tmem_st16(o_addr + uint32_t(c), zero);
-                    hs::tc::tmem_wait_st();
-                    for (int j = 0; j < kTile; ++j) {
-                        const uint32_t pw = tmem_ld1(p_addr + uint32_t(j >> 1));
-                        hs::tc::tmem_wait_ld();
-                        const uint32_t h = (j & 1) ? pw >> 16 : pw & 0xffffu;
-                        const float p = KV == kBf16 ? __uint_as_float(h << 16)
-                                                    : __half2float(__ushort_as_half(uint16_t(h)));
-                        const uint32_t vw = j < 32 ? vis[0] : j < 64 ? vis[1] : j < 96 ? vis[2] : vis[3];
-                        const bool sees = (vw >> (j & 31)) & 1u;
-                        for (int u = 0; u < kSubs; ++u) {
-                            if (!((B.odd[t & (C::kRing - 1)][u][j >> 5] >> (j & 31)) & 1u)) continue;
-                            const int tk = B.tile[t & (C::kRing - 1)].x + j, b = block_of(a, tk);
-                            const int64_t page = a.block_table[s.row * a.bt_stride + b];
-                            const void* row = static_cast<const char*>(a.v) +
-                                (page * a.page_stride + int64_t(tk - b * a.page_size) * a.row_stride +
-                                 s.kvh * a.head_stride) * (E4 ? 1 : 2);
-#pragma unroll 1
-                            for (int c = u * C::kDims; c < (u + 1) * C::kDims; c += 16) {
-                                float o[16];
-                                hs::tc::tmem_ld16(o_addr + uint32_t(c), o);
-                                hs::tc::tmem_wait_ld();
-#pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    if (sees) o[e] = fmaf(p, element<KV>(row, c + e), o[e]);
-                                hs::tc::tmem_st16(o_addr + uint32_t(c), o);
-                                hs::tc::tmem_wait_st();
-                            }
-                        }
-                    }
-                }
-            } else if (first) {
-                B.keep[w] = 0;
-            }
             hs::tc::fence_before_sync();
             hs::mbar_arrive(&B.p_full[x]);
         }
@@ -731,8 +764,10 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
                 make_float2(off, l);
         }
         B.factor[w][r] = f;
-        hs::mbar_arrive(&B.l_full[w]);
+        pending = true;
     }
+    if (odd && ok) clear_odd();
+    if (pending && ok) finish();
     if (!ok) cx.give_up();
 }
 
@@ -830,7 +865,7 @@ __device__ __forceinline__ bool pv_role(const Cta<C>& cx) {
                 ok = ok && cx.wait_all(&B.p_full[x], NQ == 2 ? (w == 0 ? done0 : done1) : t >> 1);
                 hs::tc::fence_after_sync();
                 if (!ok) break;
-                const bool fresh = i == 0 && B.keep[w] == 0;
+                const bool fresh = i == 0;
                 const uint32_t p_col =
                     tmem + (NQ == 2 ? C::kPCol + uint32_t(w * 64) : uint32_t(x * 128));
 #pragma unroll
@@ -1139,9 +1174,12 @@ __device__ __forceinline__ bool check_role(const Cta<C>& cx) {
     int t = 0;
     Written done;
     Seg s;
-    for (int unit = 0; cx.next_unit(unit, s, ok); ++unit) {
-        for (int i = 0; i < s.n && ok; ++i, ++t) {
-            for (int u = 0; u < C::kSubs; ++u) {
+    bool more = true;
+    for (int unit = 0; more; ++unit) {
+        more = cx.next_unit(unit, s, ok);
+        const int n = more ? s.n : 1;  // (behind the last unit: its output)
+        for (int i = 0; i < n && ok; ++i, ++t) {
+            for (int u = 0; u < C::kSubs && more; ++u) {
                 const int q = unit_of<C>(t, true, u), turn = turn_of<C>(t, u);
                 ok = cx.wait_all(&B.vfull[turn % NS], turn / NS);
                 if (!ok) break;
@@ -1170,9 +1208,9 @@ __device__ __forceinline__ bool check_role(const Cta<C>& cx) {
             // The unit before, while this one's first tile is in its softmax.
             if (ok && i == 0 && done.n > 0) ok = write_unit(cx, done);
         }
-        unit_to_write(s, C::NQ == 2 && a.tq < s.m ? 2 : 1, done);
+        if (more) unit_to_write(s, C::NQ == 2 && a.tq < s.m ? 2 : 1, done);
     }
-    return ok && (done.n == 0 || write_unit(cx, done));
+    return ok;
 }
 
 // Two 16-byte chunks of fp16 from 16 E4M3 codes.
@@ -1206,12 +1244,15 @@ __device__ __forceinline__ bool convert_role(const Cta<C>& cx) {
     int t = 0, seq = 0;
     Written done;
     Seg s;
-    for (int unit = 0; cx.next_unit(unit, s, ok); ++unit) {
-        if (unit > 0) ok = cx.wait_all(&B.q_empty, unit - 1);
+    bool more = true;
+    for (int unit = 0; more; ++unit) {
+        more = cx.next_unit(unit, s, ok);
+        if (more && unit > 0) ok = cx.wait_all(&B.q_empty, unit - 1);
         if (!ok) break;
-        load_queries<C, 128>(cx, s, lt, unit);
-        for (int i = 0; i < s.n && ok; ++i, ++t) {
-            for (int u = 0; u < 2 * C::kSubs; ++u, ++seq) {
+        if (more) load_queries<C, 128>(cx, s, lt, unit);
+        const int n = more ? s.n : 1;  // (behind the last unit: its output)
+        for (int i = 0; i < n && ok; ++i, ++t) {
+            for (int u = 0; u < 2 * C::kSubs && more; ++u, ++seq) {
                 const bool v = u >= C::kSubs;
                 const int turn = turn_of<C>(t, u % C::kSubs), slot = seq % NS;
                 ok = cx.wait_all(&B.sfull[seq % C::kStages], seq / C::kStages) &&
@@ -1224,6 +1265,10 @@ __device__ __forceinline__ bool convert_role(const Cta<C>& cx) {
 #pragma unroll
                 for (int p = 0; p < kCh; ++p)
                     x[p] = *reinterpret_cast<const uint4*>(from + p * kStep * C::kDims);
+                // What later tiles find out about their rows of V begins at none;
+                // the warps are at most kStages units apart.
+                if (u == C::kSubs && lt < 4 * C::kSubs)
+                    B.odd[(t + 2) & (C::kRing - 1)][lt >> 2][lt & 3] = 0;
                 hs::mbar_arrive(&B.sempty[seq % C::kStages]);
                 if (v && tile.y != 0) {
                     // A warp has kStep / 4 rows of a pass.
@@ -1238,16 +1283,12 @@ __device__ __forceinline__ bool convert_role(const Cta<C>& cx) {
                         if (!in || out) x[p] = make_uint4(0u, 0u, 0u, 0u);
                         if (out && ch == 0) odd[p * kStep >> 5] |= 1u << (r & 31);
                     }
-                    // (Cleared two tiles ahead, below: the warps are at most two
-                    // units apart.)
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         const uint32_t all = __reduce_or_sync(0xffffffffu, odd[g]);
                         if (lane == 0 && all != 0) atomicOr(&B.odd[t & (C::kRing - 1)][u - C::kSubs][g], all);
                     }
                 }
-                if (u == C::kSubs && lt < 4 * C::kSubs)
-                    B.odd[(t + 2) & (C::kRing - 1)][lt >> 2][lt & 3] = 0;
 #pragma unroll
                 for (int p = 0; p < kCh; ++p) {
                     const int r = p * kStep + r0;
@@ -1262,9 +1303,9 @@ __device__ __forceinline__ bool convert_role(const Cta<C>& cx) {
             }
             if (ok && i == 0 && done.n > 0) ok = write_unit(cx, done);
         }
-        unit_to_write(s, C::NQ == 2 && a.tq < s.m ? 2 : 1, done);
+        if (more) unit_to_write(s, C::NQ == 2 && a.tq < s.m ? 2 : 1, done);
     }
-    return ok && (done.n == 0 || write_unit(cx, done));
+    return ok;
 }
 
 // Loads by 128 threads: pages without runs of 16 tokens, broadcast strides.
@@ -1525,14 +1566,16 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
         hs::mbar_init(&B.q_empty, 1);
         hs::mbar_init(&B.s_free, kTile);
         for (int i = 0; i < 2; ++i) {
-            hs::mbar_init(&B.sfull[i], 1);
-            hs::mbar_init(&B.sempty[i], kTile);
             hs::mbar_init(&B.s_full[i], 1);
             hs::mbar_init(&B.p_full[i], kTile);
             hs::mbar_init(&B.pv_done[i], 1);
             hs::mbar_init(&B.l_full[i], kTile);
             hs::mbar_init(&B.o_free[i], kTile);
             hs::mbar_init(&B.drain[i], 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            hs::mbar_init(&B.sfull[i], 1);
+            hs::mbar_init(&B.sempty[i], kTile);
         }
         for (int i = 0; i < kUnitRing; ++i) {
             hs::mbar_init(&B.unit_full[i], 1);
