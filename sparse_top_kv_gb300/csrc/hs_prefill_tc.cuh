@@ -76,8 +76,8 @@ struct Cfg {
     static constexpr int kSubs = D / kDims;                // ring units of a tile
     static constexpr int kUnit = kTile * kDims * 2;
     static constexpr int kQTile = kTile * D * 2;
-    static constexpr int NS = D == 64 ? 8 : kConvert ? 3 : kByTma ? 5 : 4;  // ring units
-    static constexpr int kStages = kConvert ? 4 : 0, kStage = kTile * kDims;
+    static constexpr int NS = D == 64 ? 8 : kByTma && !kConvert ? 5 : 4;  // ring units
+    static constexpr int kStages = kConvert ? 2 : 0, kStage = kTile * kDims;
     static constexpr int kRing = 8;        // tiles whose loaded tokens are remembered
     static constexpr int kSegRing = D == 256 ? 4 : 2;  // units whose query scales are
     static constexpr int kRingOff = NQ * kQTile;       // (queries first)
@@ -110,7 +110,7 @@ template <typename C>
 struct Bars {
     uint64_t kfull[C::NS], vfull[C::NS], ready[C::NS], empty[C::NS];
     uint64_t sfull[4], sempty[4], unit_full[kUnitRing], unit_free[kUnitRing];
-    uint64_t q_full, q_empty, s_full[2], s_free, p_full[2], pv_done[2], l_full[2], o_free[2], drain[2];
+    uint64_t q_raw, q_full, q_empty, s_full[2], s_free, p_full[2], pv_done[2], l_full[2], o_free[2], drain[2];
     Seg unit[kUnitRing];
     int64_t place0, place1, start;  // the run, and where its first unit starts
     int64_t per;                    // the call's places: per * ctas + rest
@@ -888,8 +888,7 @@ __device__ __forceinline__ bool pv_role(const Cta<C>& cx) {
 }
 
 // ------------------------------ loads by TMA ------------------------------
-// One warp: the queries of each unit (E4M3: made by the converting threads),
-// then the K and V units of its tiles, a lane per run of tokens in one page.
+// One warp: the queries of each unit, then the K and V units of its tiles, a lane per run of tokens in one page.
 template <typename C>
 __device__ __forceinline__ bool tma_role(const Cta<C>& cx, const CUtensorMap& qmap,
                                          const CUtensorMap& kmap, const CUtensorMap& vmap) {
@@ -902,27 +901,26 @@ __device__ __forceinline__ bool tma_role(const Cta<C>& cx, const CUtensorMap& qm
     const uint32_t row_bytes = C::kConvert ? C::kDims : 128;
     const uint32_t box = uint32_t(bt) * row_bytes;
     const uint32_t q_bytes = uint32_t(a.tq * a.group) * 128u * (C::kD / 64);
+    uint64_t* q_bar = C::kConvert ? &B.q_raw : &B.q_full;
     bool ok = true, bad = false;
     int t = 0, seq = 0, segs = 0;
     Seg s;
     for (int unit = 0; cx.next_unit(unit, s, ok); ++unit) {
-        if constexpr (!C::kConvert) {
-            // A box takes the heads of a KV head for a tile's tokens: its rows are
-            // the tile's.  (Tokens of other requests behind a unit's own land in
-            // rows that are not written.)
-            if (segs > 0) ok = cx.wait_all(&B.q_empty, segs - 1);
-            if (!ok) break;
-            ++segs;
-            if (lane == 0) {
-                const int tiles = C::NQ == 2 && s.m > a.tq ? 2 : 1;
-                hs::mbar_arrive_expect_tx(&B.q_full, q_bytes * tiles);
-                for (int w = 0; w < tiles; ++w)
-                    for (int c = 0; c < C::kD / 64; ++c)
-                        tma_load_q(cx.sb + w * C::kQTile + c * kBlk, &qmap, c * 64, s.kvh * a.group,
-                                   s.first + w * a.tq, &B.q_full);
-            }
-            __syncwarp();
+        // A box takes the heads of a KV head for a tile's tokens: its rows are the
+        // tile's.  (Tokens of other requests behind a unit's own land in rows that
+        // are not written.)
+        if (unit > 0) ok = cx.wait_all(&B.q_empty, unit - 1);
+        if (!ok) break;
+        segs = unit + 1;
+        if (lane == 0) {
+            const int tiles = C::NQ == 2 && s.m > a.tq ? 2 : 1;
+            hs::mbar_arrive_expect_tx(q_bar, q_bytes * tiles);
+            for (int w = 0; w < tiles; ++w)
+                for (int c = 0; c < C::kD / 64; ++c)
+                    tma_load_q(cx.sb + w * C::kQTile + c * kBlk, &qmap, c * 64, s.kvh * a.group,
+                               s.first + w * a.tq, q_bar);
         }
+        __syncwarp();
         for (int i = 0; i < s.n && ok; ++i, ++t) {
             const int t0 = token_of(s, i), tok = t0 + lane * bt;
             const int b = block_of(a, tok);
@@ -976,13 +974,12 @@ __device__ __forceinline__ bool tma_role(const Cta<C>& cx, const CUtensorMap& qm
     }
     // No copy may outlive the CTA (where all went well each has been waited for).
     if (!ok) {
+        if (segs > 0) hs::mbar_wait_bounded(q_bar, (segs - 1) & 1, cx.ta.timeout_ns, nullptr);
         if constexpr (C::kConvert) {
             for (int q = max(0, seq - C::kStages); q < seq; ++q)
                 hs::mbar_wait_bounded(&B.sfull[q % C::kStages], (q / C::kStages) & 1,
                                       cx.ta.timeout_ns, nullptr);
         } else {
-            if (segs > 0)
-                hs::mbar_wait_bounded(&B.q_full, (segs - 1) & 1, cx.ta.timeout_ns, nullptr);
             for (int q = max(0, seq - C::NS); q < seq; ++q) {
                 const int u = q % (2 * kSubs), turn = turn_of<C>(q / (2 * kSubs), u % kSubs);
                 hs::mbar_wait_bounded(u < kSubs ? &B.kfull[turn % C::NS] : &B.vfull[turn % C::NS],
@@ -995,8 +992,32 @@ __device__ __forceinline__ bool tma_role(const Cta<C>& cx, const CUtensorMap& qm
 }
 
 // --------------------------- queries by threads ---------------------------
+// Eight bf16 queries as fp16, raised so that their row's largest magnitude lies in
+// [2^14, 2^15) (rows below 2^-112 not as far); a row is CHUNKS neighbouring lanes.
+// *up: the power.
+template <int CHUNKS>
+__device__ __forceinline__ uint4 raise_queries(const uint4& raw, int* up) {
+    uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+    float f[8], mx = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u[i]));
+        f[2 * i] = y.x;
+        f[2 * i + 1] = y.y;
+        mx = max3(mx, fabsf(y.x), fabsf(y.y));
+    }
+#pragma unroll
+    for (int o = CHUNKS / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    int e = 0;
+    if (mx > 0.f && mx < CUDART_INF_F) e = min(14 - (int(__float_as_uint(mx) >> 23) - 127), 126);
+    const float m = pow2(e);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = pack<kFp16>(f[2 * i] * m, f[2 * i + 1] * m);
+    *up = e;
+    return make_uint4(u[0], u[1], u[2], u[3]);
+}
 // The rows of a unit's queries, by THREADS threads (whole warps): 16-bit ones
-// copied, those of E4M3 caches made fp16.
+// copied, bf16 ones of E4M3 caches made fp16.
 template <typename C, int THREADS>
 __device__ __forceinline__ void load_queries(const Cta<C>& cx, const Seg& s, int ti, int slot) {
     constexpr int D = C::kD;
@@ -1013,7 +1034,7 @@ __device__ __forceinline__ void load_queries(const Cta<C>& cx, const Seg& s, int
 #pragma unroll 1
     for (int w = 0; w < C::NQ; ++w) {
         int tok = tok0, hd = hd0;
-#pragma unroll 4
+#pragma unroll 1
         for (int r = row0; r < kTile; r += kRowStep) {
             const bool in = tok < a.tq && w * a.tq + tok < s.m;
             const int64_t at = in ? (w * a.tq + tok) * a.q_stride + hd * D : 0;
@@ -1023,28 +1044,7 @@ __device__ __forceinline__ void load_queries(const Cta<C>& cx, const Seg& s, int
             } else {
                 uint4 raw = in ? *reinterpret_cast<const uint4*>(q + at * 2) : make_uint4(0u, 0u, 0u, 0u);
                 int e = 0;
-                if (!a.q_is_half) {
-                    uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
-                    float f[8], mx = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u[i]));
-                        f[2 * i] = y.x;
-                        f[2 * i + 1] = y.y;
-                        mx = fmaxf(mx, fmaxf(fabsf(y.x), fabsf(y.y)));
-                    }
-#pragma unroll
-                    for (int o = kCh / 2; o > 0; o >>= 1)
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                    // Largest magnitude to [2^14, 2^15) (rows below 2^-112 not as
-                    // far).
-                    if (mx > 0.f && mx < CUDART_INF_F)
-                        e = min(14 - (int(__float_as_uint(mx) >> 23) - 127), 126);
-                    const float up = pow2(e);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) u[i] = pack<kFp16>(f[2 * i] * up, f[2 * i + 1] * up);
-                    raw = make_uint4(u[0], u[1], u[2], u[3]);
-                }
+                if (!a.q_is_half) raw = raise_queries<kCh>(raw, &e);
                 *reinterpret_cast<uint4*>(cx.smem + dst) = raw;
                 if (ch == 0) cx.B.qexp[slot & (C::kSegRing - 1)][w * kTile + r] = int8_t(e);
             }
@@ -1057,6 +1057,29 @@ __device__ __forceinline__ void load_queries(const Cta<C>& cx, const Seg& s, int
         }
     }
     if constexpr (!C::kE4) hs::tc::cp_async_wait_all();
+    hs::fence_proxy_async_shared();
+    hs::mbar_arrive(&cx.B.q_full);
+}
+// The same of queries that have landed in their place, by 128 threads.  (Loaded
+// by these: 40000 cycles a unit.)
+template <typename C>
+__device__ __forceinline__ void convert_queries(const Cta<C>& cx, int tiles, int ti, int slot) {
+    constexpr int kCh = C::kD / 8, kRowStep = 128 / kCh;
+    const int lane = ti & 31, ch = lane % kCh, row0 = ti / 32 * (32 / kCh) + lane / kCh;
+    int8_t* qexp = cx.B.qexp[slot & (C::kSegRing - 1)];
+    if (cx.a.q_is_half) {
+        for (int n = ti; n < C::NQ * kTile; n += 128) qexp[n] = 0;
+    } else {
+#pragma unroll 4
+        for (int n = row0; n < tiles * kTile; n += kRowStep) {
+            const int w = n / kTile, r = n % kTile;
+            uint4* at = reinterpret_cast<uint4*>(cx.smem + w * C::kQTile + (ch >> 3) * kBlk + r * 128 +
+                                                 (((ch & 7) ^ (r & 7)) << 4));
+            int e;
+            *at = raise_queries<kCh>(*at, &e);
+            if (ch == 0) qexp[n] = int8_t(e);
+        }
+    }
     hs::fence_proxy_async_shared();
     hs::mbar_arrive(&cx.B.q_full);
 }
@@ -1213,16 +1236,10 @@ __device__ __forceinline__ bool check_role(const Cta<C>& cx) {
     return ok;
 }
 
-// Two 16-byte chunks of fp16 from 16 E4M3 codes.
-__device__ __forceinline__ void widen_codes(const uint4& x, uint4& y, uint4& z) {
-    y.x = e4m3x2_to_half2(x.x & 0xffffu);
-    y.y = e4m3x2_to_half2(x.x >> 16);
-    y.z = e4m3x2_to_half2(x.y & 0xffffu);
-    y.w = e4m3x2_to_half2(x.y >> 16);
-    z.x = e4m3x2_to_half2(x.z & 0xffffu);
-    z.y = e4m3x2_to_half2(x.z >> 16);
-    z.z = e4m3x2_to_half2(x.w & 0xffffu);
-    z.w = e4m3x2_to_half2(x.w >> 16);
+// Eight E4M3 codes as fp16.
+__device__ __forceinline__ uint4 widen_codes(const uint2& x) {
+    return make_uint4(e4m3x2_to_half2(x.x & 0xffffu), e4m3x2_to_half2(x.x >> 16),
+                      e4m3x2_to_half2(x.y & 0xffffu), e4m3x2_to_half2(x.y >> 16));
 }
 // Lanes of a warp that hold the chunks of this lane's row.
 template <int CHUNKS>
@@ -1237,9 +1254,12 @@ __device__ __forceinline__ bool convert_role(const Cta<C>& cx) {
     const PrefillArgs& a = cx.a;
     Bars<C>& B = cx.B;
     const int lt = threadIdx.x & 127, lane = lt & 31, ch = lt % kCh, r0 = lt / kCh;
-    // Its two 16-byte chunks of fp16; half the lanes begin with the second one, for
-    // the banks.
-    const int c0 = 2 * ch + (ch >= 4 ? 1 : 0), c1 = 2 * ch + (ch >= 4 ? 0 : 1);
+    // Its 16 codes make two 16-byte chunks of fp16; half the lanes begin with the
+    // second one, for the banks.
+    const int swap = ch >= 4 ? 1 : 0, c0 = 2 * ch + swap, c1 = 2 * ch + 1 - swap;
+    const int to0 = r0 * 128 + (c0 >> 3) * kBlk + (((c0 & 7) ^ (r0 & 7)) << 4);
+    const int to1 = r0 * 128 + (c1 >> 3) * kBlk + (((c1 & 7) ^ (r0 & 7)) << 4);
+    static_assert(kStep % 8 == 0, "the swizzle is the same in every pass");
     bool ok = true;
     int t = 0, seq = 0;
     Written done;
@@ -1247,9 +1267,9 @@ __device__ __forceinline__ bool convert_role(const Cta<C>& cx) {
     bool more = true;
     for (int unit = 0; more; ++unit) {
         more = cx.next_unit(unit, s, ok);
-        if (more && unit > 0) ok = cx.wait_all(&B.q_empty, unit - 1);
+        if (more) ok = cx.wait_all(&B.q_raw, unit);
         if (!ok) break;
-        if (more) load_queries<C, 128>(cx, s, lt, unit);
+        if (more) convert_queries<C>(cx, C::NQ == 2 && a.tq < s.m ? 2 : 1, lt, unit);
         const int n = more ? s.n : 1;  // (behind the last unit: its output)
         for (int i = 0; i < n && ok; ++i, ++t) {
             for (int u = 0; u < 2 * C::kSubs && more; ++u, ++seq) {
@@ -1261,10 +1281,12 @@ __device__ __forceinline__ bool convert_role(const Cta<C>& cx) {
                 const unsigned char* from = cx.smem + C::kStageOff + seq % C::kStages * C::kStage + lt * 16;
                 unsigned char* to = cx.smem + C::kRingOff + slot * C::kUnit;
                 const int2 tile = B.tile[t & (C::kRing - 1)];
-                uint4 x[kCh];
+                uint2 x[kCh][2];
 #pragma unroll
-                for (int p = 0; p < kCh; ++p)
-                    x[p] = *reinterpret_cast<const uint4*>(from + p * kStep * C::kDims);
+                for (int p = 0; p < kCh; ++p) {
+                    x[p][0] = *reinterpret_cast<const uint2*>(from + p * kStep * C::kDims + swap * 8);
+                    x[p][1] = *reinterpret_cast<const uint2*>(from + p * kStep * C::kDims + 8 - swap * 8);
+                }
                 // What later tiles find out about their rows of V begins at none;
                 // the warps are at most kStages units apart.
                 if (u == C::kSubs && lt < 4 * C::kSubs)
@@ -1278,9 +1300,10 @@ __device__ __forceinline__ bool convert_role(const Cta<C>& cx) {
                         const int r = p * kStep + r0;
                         const bool in = any_sees(a, s, tile.x + r) &&
                                         ((B.loaded[t & (C::kRing - 1)][r >> 5] >> (r & 31)) & 1u);
-                        const uint32_t bad = __ballot_sync(0xffffffffu, in && not_finite<kE4m3>(x[p]));
+                        const uint32_t bad = __ballot_sync(0xffffffffu, in && not_finite<kE4m3>(make_uint4(x[p][0].x, x[p][0].y,
+                                                                                         x[p][1].x, x[p][1].y)));
                         const bool out = (bad & row_lanes<kCh>(lane)) != 0;
-                        if (!in || out) x[p] = make_uint4(0u, 0u, 0u, 0u);
+                        if (!in || out) x[p][0] = x[p][1] = make_uint2(0u, 0u);
                         if (out && ch == 0) odd[p * kStep >> 5] |= 1u << (r & 31);
                     }
 #pragma unroll
@@ -1291,12 +1314,8 @@ __device__ __forceinline__ bool convert_role(const Cta<C>& cx) {
                 }
 #pragma unroll
                 for (int p = 0; p < kCh; ++p) {
-                    const int r = p * kStep + r0;
-                    uint4 y, z;
-                    widen_codes(x[p], y, z);
-                    unsigned char* row = to + r * 128;
-                    *reinterpret_cast<uint4*>(row + (c0 >> 3) * kBlk + (((c0 & 7) ^ (r & 7)) << 4)) = ch >= 4 ? z : y;
-                    *reinterpret_cast<uint4*>(row + (c1 >> 3) * kBlk + (((c1 & 7) ^ (r & 7)) << 4)) = ch >= 4 ? y : z;
+                    *reinterpret_cast<uint4*>(to + to0 + p * kStep * 128) = widen_codes(x[p][0]);
+                    *reinterpret_cast<uint4*>(to + to1 + p * kStep * 128) = widen_codes(x[p][1]);
                 }
                 hs::fence_proxy_async_shared();
                 hs::mbar_arrive(v ? &B.ready[turn % NS] : &B.kfull[turn % NS]);
@@ -1376,15 +1395,7 @@ __device__ __forceinline__ bool load_role(const Cta<C>& cx) {
             unsigned char* dst = smem + C::kRingOff + unit_of<C>(t, v, u) % C::NS * C::kUnit +
                                  (cb >> 3) * kBlk + r * 128;
             if constexpr (E4) {
-                uint4 y, z;
-                y.x = e4m3x2_to_half2(x[j].x & 0xffffu);
-                y.y = e4m3x2_to_half2(x[j].x >> 16);
-                y.z = e4m3x2_to_half2(x[j].y & 0xffffu);
-                y.w = e4m3x2_to_half2(x[j].y >> 16);
-                z.x = e4m3x2_to_half2(x[j].z & 0xffffu);
-                z.y = e4m3x2_to_half2(x[j].z >> 16);
-                z.z = e4m3x2_to_half2(x[j].w & 0xffffu);
-                z.w = e4m3x2_to_half2(x[j].w >> 16);
+                const uint4 y = widen_codes(make_uint2(x[j].x, x[j].y)), z = widen_codes(make_uint2(x[j].z, x[j].w));
                 *reinterpret_cast<uint4*>(dst + (((cb & 7) ^ (r & 7)) << 4)) = y;
                 *reinterpret_cast<uint4*>(dst + ((((cb & 7) + 1) ^ (r & 7)) << 4)) = z;
             } else {
@@ -1563,6 +1574,7 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
             hs::mbar_init(&B.empty[i], 1);
         }
         hs::mbar_init(&B.q_full, C::kConvert ? kTile : C::kByTma ? 1 : kQThreads);
+        hs::mbar_init(&B.q_raw, 1);
         hs::mbar_init(&B.q_empty, 1);
         hs::mbar_init(&B.s_free, kTile);
         for (int i = 0; i < 2; ++i) {
@@ -1670,7 +1682,7 @@ int launch_one(const PrefillArgs& a, int bt, hs_stream_t stream) {
     if (hs_host::ask_once(&regs[dev], ask) != 65536 / kThreads) return HS_ERR_UNSUPPORTED;
     CUtensorMap q{}, k{}, v{};
     if (C::kByTma) {
-        if (!C::kE4) rc = encode_q_map(&q, a, KV, D);
+        rc = encode_q_map(&q, a, C::kE4 ? (a.q_is_half ? HS_FP16 : HS_BF16) : KV, D);
         if (rc == HS_OK) rc = encode_map(&k, a.k, a, KV, D, bt);
         if (rc == HS_OK) rc = encode_map(&v, a.v, a, KV, D, bt);
         if (rc != HS_OK) return rc;
