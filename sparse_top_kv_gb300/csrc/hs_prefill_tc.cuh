@@ -78,6 +78,7 @@ struct Cfg {
     static constexpr int kQTile = kTile * D * 2;
     static constexpr int NS = D == 64 ? 8 : kByTma && !kConvert ? 5 : 4;  // ring units
     static constexpr int kStages = kConvert ? 2 : 0, kStage = kTile * kDims;
+    static constexpr int kOddWords = kConvert ? 16 : 4;
     static constexpr int kRing = 8;        // tiles whose loaded tokens are remembered
     static constexpr int kSegRing = D == 256 ? 4 : 2;  // units whose query scales are
     static constexpr int kRingOff = NQ * kQTile;       // (queries first)
@@ -109,7 +110,7 @@ struct Seg {
 template <typename C>
 struct Bars {
     uint64_t kfull[C::NS], vfull[C::NS], ready[C::NS], empty[C::NS];
-    uint64_t sfull[4], sempty[4], unit_full[kUnitRing], unit_free[kUnitRing];
+    uint64_t sfull[2], sempty[2], unit_full[kUnitRing], unit_free[kUnitRing];
     uint64_t q_raw, q_full, q_empty, s_full[2], s_free, p_full[2], pv_done[2], l_full[2], o_free[2], drain[2];
     Seg unit[kUnitRing];
     int64_t place0, place1, start;  // the run, and where its first unit starts
@@ -120,7 +121,9 @@ struct Bars {
     volatile int32_t abort;
     alignas(16) uint32_t loaded[C::kRing][4];     // tokens of a tile that were loaded
     int2 tile[C::kRing];                          // its first token; whether some query does not see all of it
-    alignas(16) uint32_t odd[C::kRing][C::kSubs][4];  // rows of V that were taken out, by ring unit
+    // Rows of V that were taken out, by ring unit (where threads convert, what each
+    // of four warps has found, to be joined).
+    alignas(16) uint32_t odd[C::kRing][C::kSubs][C::kOddWords / 4][4];
     float factor[C::NQ][kTile];                   // of each row's output; 0: nothing was attended to
     int8_t qexp[C::kE4 ? C::kSegRing : 1][C::kE4 ? C::NQ * kTile : 1];  // queries are raised by 2^qexp
     int64_t offset[C::kByTma ? 1 : 2][C::kByTma ? 1 : kTile];  // rows of a tile in the cache, -1: none
@@ -491,7 +494,7 @@ struct Cta {
 // Rows of V that were taken out of a tile, into a row's output: P stands until the
 // next one is written, O has the other rows' products.  Apart from the softmax's
 // code and registers: it hardly ever runs.
-template <int KV, int D>
+template <int KV, int D, int WORDS>
 __device__ __noinline__ void add_odd_rows(const PrefillArgs* ap, const uint32_t* odd, uint4 vis,
                                           int t0, int row, int kvh, uint32_t o_addr,
                                           uint32_t p_addr) {
@@ -508,7 +511,9 @@ __device__ __noinline__ void add_odd_rows(const PrefillArgs* ap, const uint32_t*
         const bool sees = (vw >> (j & 31)) & 1u;
 #pragma unroll 1
         for (int u = 0; u < D / kDims; ++u) {
-            if (!((odd[u * 4 + (j >> 5)] >> (j & 31)) & 1u)) continue;
+            uint32_t word = 0;
+            for (int g = 0; g < WORDS; g += 4) word |= odd[u * WORDS + g + (j >> 5)];
+            if (!((word >> (j & 31)) & 1u)) continue;
             const int tk = t0 + j, b = block_of(a, tk);
             const int64_t page = a.block_table[row * a.bt_stride + b];
             const void* from = static_cast<const char*>(a.v) +
@@ -571,8 +576,9 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
         for (int u = 0; u < kSubs && ok; ++u) {
             const int q = turn_of<C>(odd_tile, u);
             ok = cx.wait_all(&B.ready[q % NS], q / NS);
-            const uint4 o = *reinterpret_cast<const uint4*>(B.odd[odd_tile & (C::kRing - 1)][u]);
-            any |= o.x | o.y | o.z | o.w;
+            const uint4* o = reinterpret_cast<const uint4*>(B.odd[odd_tile & (C::kRing - 1)][u]);
+#pragma unroll
+            for (int g = 0; g < C::kOddWords / 4; ++g) any |= o[g].x | o[g].y | o[g].z | o[g].w;
         }
         odd = false;
         if (any == 0 || !ok) return;
@@ -580,7 +586,7 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
         hs::tc::fence_after_sync();
         uint32_t vis[4];
         see(odd_tile, odd_pos, vis);
-        add_odd_rows<KV, D>(&a, &B.odd[odd_tile & (C::kRing - 1)][0][0], make_uint4(vis[0], vis[1], vis[2], vis[3]),
+        add_odd_rows<KV, D, C::kOddWords>(&a, &B.odd[odd_tile & (C::kRing - 1)][0][0][0], make_uint4(vis[0], vis[1], vis[2], vis[3]),
                             B.tile[odd_tile & (C::kRing - 1)].x, odd_row, odd_kvh, o_addr,
                             tmem + lanes + (NQ == 2 ? C::kPCol + uint32_t(w * 64)
                                                     : uint32_t(((mine - 1) & 1) * 128)));
@@ -950,8 +956,8 @@ __device__ __forceinline__ bool tma_role(const Cta<C>& cx, const CUtensorMap& qm
                 uint64_t* full;
                 uint32_t dst;
                 if constexpr (C::kConvert) {
-                    const int slot = seq % C::kStages;
-                    ok = cx.wait_all(&B.sempty[slot], seq / C::kStages + 1);
+                    const int slot = u / kSubs;  // one for K, one for V
+                    ok = cx.wait_all(&B.sempty[slot], turn_of<C>(t, u % kSubs) + 1);
                     full = &B.sfull[slot];
                     dst = cx.sb + C::kStageOff + slot * C::kStage;
                 } else {
@@ -976,9 +982,12 @@ __device__ __forceinline__ bool tma_role(const Cta<C>& cx, const CUtensorMap& qm
     if (!ok) {
         if (segs > 0) hs::mbar_wait_bounded(q_bar, (segs - 1) & 1, cx.ta.timeout_ns, nullptr);
         if constexpr (C::kConvert) {
-            for (int q = max(0, seq - C::kStages); q < seq; ++q)
-                hs::mbar_wait_bounded(&B.sfull[q % C::kStages], (q / C::kStages) & 1,
+            for (int q = max(0, seq - 2 * kSubs); q < seq; ++q) {
+                const int u = q % (2 * kSubs);
+                hs::mbar_wait_bounded(&B.sfull[u / kSubs],
+                                      turn_of<C>(q / (2 * kSubs), u % kSubs) & 1,
                                       cx.ta.timeout_ns, nullptr);
+            }
         } else {
             for (int q = max(0, seq - C::NS); q < seq; ++q) {
                 const int u = q % (2 * kSubs), turn = turn_of<C>(q / (2 * kSubs), u % kSubs);
@@ -1218,7 +1227,7 @@ __device__ __forceinline__ bool check_role(const Cta<C>& cx) {
                             odd |= not_finite<C::kKind>(*reinterpret_cast<const uint4*>(
                                 row + (c >> 3) * kBlk + (((c + lane) & 7) << 4)));
                     const uint32_t all = __ballot_sync(0xffffffffu, odd);
-                    if (lane == 0) B.odd[t & (C::kRing - 1)][u][j] = all;
+                    if (lane == 0) B.odd[t & (C::kRing - 1)][u][0][j] = all;
                     if (!in || odd)
                         for (int c = 0; c < C::kDims / 8; ++c)
                             *reinterpret_cast<uint4*>(row + (c >> 3) * kBlk + (((c + lane) & 7) << 4)) =
@@ -1247,10 +1256,13 @@ __device__ __forceinline__ uint32_t row_lanes(int lane) {
     return CHUNKS >= 32 ? 0xffffffffu : ((1u << (CHUNKS & 31)) - 1u) << (lane / CHUNKS * CHUNKS);
 }
 
-// E4M3 caches by TMA: units from the stage to the ring as fp16.
+// E4M3 caches by TMA: units from the stages (one for K, one for V) to the ring as
+// fp16.
 template <typename C>
 __device__ __forceinline__ bool convert_role(const Cta<C>& cx) {
-    constexpr int NS = C::NS, kCh = C::kDims / 16, kStep = kTile / kCh;  // chunks of a row, rows of a pass
+    constexpr int NS = C::NS, kCh = C::kDims / 16;  // chunks of a row
+    constexpr int kStep = kTile / kCh;              // rows of a pass
+    static_assert(kStep % 8 == 0, "the swizzle is the same in every pass");
     const PrefillArgs& a = cx.a;
     Bars<C>& B = cx.B;
     const int lt = threadIdx.x & 127, lane = lt & 31, ch = lt % kCh, r0 = lt / kCh;
@@ -1259,11 +1271,29 @@ __device__ __forceinline__ bool convert_role(const Cta<C>& cx) {
     const int swap = ch >= 4 ? 1 : 0, c0 = 2 * ch + swap, c1 = 2 * ch + 1 - swap;
     const int to0 = r0 * 128 + (c0 >> 3) * kBlk + (((c0 & 7) ^ (r0 & 7)) << 4);
     const int to1 = r0 * 128 + (c1 >> 3) * kBlk + (((c1 & 7) ^ (r0 & 7)) << 4);
-    static_assert(kStep % 8 == 0, "the swizzle is the same in every pass");
+    const unsigned char* from = cx.smem + C::kStageOff + lt * 16;
     bool ok = true;
-    int t = 0, seq = 0;
+    int t = 0;
     Written done;
     Seg s;
+    const auto take = [&](int side, uint2 (&x)[kCh][2]) {
+#pragma unroll
+        for (int p = 0; p < kCh; ++p) {
+            const unsigned char* at = from + side * C::kStage + p * kStep * C::kDims;
+            x[p][0] = *reinterpret_cast<const uint2*>(at + swap * 8);
+            x[p][1] = *reinterpret_cast<const uint2*>(at + 8 - swap * 8);
+        }
+        hs::mbar_arrive(&B.sempty[side]);
+    };
+    const auto put = [&](int slot, const uint2 (&x)[kCh][2]) {
+        unsigned char* to = cx.smem + C::kRingOff + slot * C::kUnit;
+#pragma unroll
+        for (int p = 0; p < kCh; ++p) {
+            *reinterpret_cast<uint4*>(to + to0 + p * kStep * 128) = widen_codes(x[p][0]);
+            *reinterpret_cast<uint4*>(to + to1 + p * kStep * 128) = widen_codes(x[p][1]);
+        }
+        hs::fence_proxy_async_shared();
+    };
     bool more = true;
     for (int unit = 0; more; ++unit) {
         more = cx.next_unit(unit, s, ok);
@@ -1272,53 +1302,55 @@ __device__ __forceinline__ bool convert_role(const Cta<C>& cx) {
         if (more) convert_queries<C>(cx, C::NQ == 2 && a.tq < s.m ? 2 : 1, lt, unit);
         const int n = more ? s.n : 1;  // (behind the last unit: its output)
         for (int i = 0; i < n && ok; ++i, ++t) {
-            for (int u = 0; u < 2 * C::kSubs && more; ++u, ++seq) {
-                const bool v = u >= C::kSubs;
-                const int turn = turn_of<C>(t, u % C::kSubs), slot = seq % NS;
-                ok = cx.wait_all(&B.sfull[seq % C::kStages], seq / C::kStages) &&
-                     cx.wait_all(&B.empty[slot], seq / NS + 1);
-                if (!ok) break;
-                const unsigned char* from = cx.smem + C::kStageOff + seq % C::kStages * C::kStage + lt * 16;
-                unsigned char* to = cx.smem + C::kRingOff + slot * C::kUnit;
-                const int2 tile = B.tile[t & (C::kRing - 1)];
-                uint2 x[kCh][2];
+            // K's units, then V's, whose codes are taken early where a tile has one.
+            uint2 x[kCh][2], y[kCh][2];
 #pragma unroll
-                for (int p = 0; p < kCh; ++p) {
-                    x[p][0] = *reinterpret_cast<const uint2*>(from + p * kStep * C::kDims + swap * 8);
-                    x[p][1] = *reinterpret_cast<const uint2*>(from + p * kStep * C::kDims + 8 - swap * 8);
+            for (int u = 0; u < C::kSubs && more; ++u) {
+                const int turn = turn_of<C>(t, u), seq = unit_of<C>(t, false, u);
+                ok = ok && cx.wait_all(&B.sfull[0], turn) &&
+                     cx.wait_all(&B.empty[seq % NS], seq / NS + 1);
+                if (!ok) break;
+                take(0, x);
+                if (C::kSubs == 1) {
+                    ok = cx.wait_all(&B.sfull[1], turn);
+                    take(1, y);
                 }
-                // What later tiles find out about their rows of V begins at none;
-                // the warps are at most kStages units apart.
-                if (u == C::kSubs && lt < 4 * C::kSubs)
-                    B.odd[(t + 2) & (C::kRing - 1)][lt >> 2][lt & 3] = 0;
-                hs::mbar_arrive(&B.sempty[seq % C::kStages]);
-                if (v && tile.y != 0) {
-                    // A warp has kStep / 4 rows of a pass.
+                put(seq % NS, x);
+                hs::mbar_arrive(&B.kfull[turn % NS]);
+            }
+#pragma unroll
+            for (int u = 0; u < C::kSubs && more; ++u) {
+                const int turn = turn_of<C>(t, u), seq = unit_of<C>(t, true, u);
+                if (C::kSubs > 1) {
+                    ok = ok && cx.wait_all(&B.sfull[1], turn);
+                    if (ok) take(1, y);
+                }
+                ok = ok && cx.wait_all(&B.empty[seq % NS], seq / NS + 1);
+                if (!ok) break;
+                const int2 tile = B.tile[t & (C::kRing - 1)];
+                if (tile.y != 0) {
                     uint32_t odd[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
                     for (int p = 0; p < kCh; ++p) {
                         const int r = p * kStep + r0;
                         const bool in = any_sees(a, s, tile.x + r) &&
                                         ((B.loaded[t & (C::kRing - 1)][r >> 5] >> (r & 31)) & 1u);
-                        const uint32_t bad = __ballot_sync(0xffffffffu, in && not_finite<kE4m3>(make_uint4(x[p][0].x, x[p][0].y,
-                                                                                         x[p][1].x, x[p][1].y)));
+                        const uint32_t bad = __ballot_sync(
+                            0xffffffffu, in && not_finite<kE4m3>(make_uint4(
+                                                   y[p][0].x, y[p][0].y, y[p][1].x, y[p][1].y)));
                         const bool out = (bad & row_lanes<kCh>(lane)) != 0;
-                        if (!in || out) x[p][0] = x[p][1] = make_uint2(0u, 0u);
+                        if (!in || out) y[p][0] = y[p][1] = make_uint2(0u, 0u);
                         if (out && ch == 0) odd[p * kStep >> 5] |= 1u << (r & 31);
                     }
+                    // What each warp has found of its rows: a quarter of every word.
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         const uint32_t all = __reduce_or_sync(0xffffffffu, odd[g]);
-                        if (lane == 0 && all != 0) atomicOr(&B.odd[t & (C::kRing - 1)][u - C::kSubs][g], all);
+                        if (lane == 0) B.odd[t & (C::kRing - 1)][u][lt >> 5][g] = all;
                     }
                 }
-#pragma unroll
-                for (int p = 0; p < kCh; ++p) {
-                    *reinterpret_cast<uint4*>(to + to0 + p * kStep * 128) = widen_codes(x[p][0]);
-                    *reinterpret_cast<uint4*>(to + to1 + p * kStep * 128) = widen_codes(x[p][1]);
-                }
-                hs::fence_proxy_async_shared();
-                hs::mbar_arrive(v ? &B.ready[turn % NS] : &B.kfull[turn % NS]);
+                put(seq % NS, y);
+                hs::mbar_arrive(&B.ready[turn % NS]);
             }
             if (ok && i == 0 && done.n > 0) ok = write_unit(cx, done);
         }
@@ -1362,7 +1394,7 @@ __device__ __forceinline__ bool load_role(const Cta<C>& cx) {
         const uint32_t got = __ballot_sync(0xffffffffu, at >= 0);
         if (lane == 0) {
             B.loaded[t & (C::kRing - 1)][lt >> 5] = got;
-            for (int u = 0; u < C::kSubs; ++u) B.odd[t & (C::kRing - 1)][u][lt >> 5] = 0;
+            for (int u = 0; u < C::kSubs; ++u) B.odd[t & (C::kRing - 1)][u][0][lt >> 5] = 0;
         }
         hs::pair::named_sync(kLoadBar, kTile);
     };
@@ -1387,7 +1419,7 @@ __device__ __forceinline__ bool load_role(const Cta<C>& cx) {
                     x[j] = make_uint4(0u, 0u, 0u, 0u);
                     if (ch == 0)
                         for (int u = 0; u < C::kSubs; ++u)
-                            atomicOr(&B.odd[t & (C::kRing - 1)][u][r >> 5], 1u << (r & 31));
+                            atomicOr(&B.odd[t & (C::kRing - 1)][u][0][r >> 5], 1u << (r & 31));
                 }
             }
             const int c0 = E4 ? 2 * ch : ch;  // its first chunk of eight 16-bit elements
@@ -1568,9 +1600,9 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
     }
     if (tid == 0) {
         for (int i = 0; i < C::NS; ++i) {
-            hs::mbar_init(&B.kfull[i], C::kByTma && !C::kE4 ? 1 : kTile);
+            hs::mbar_init(&B.kfull[i], C::kByTma && !C::kConvert ? 1 : kTile);
             hs::mbar_init(&B.vfull[i], 1);
-            hs::mbar_init(&B.ready[i], C::kByTma && !C::kE4 ? 4 : kTile);
+            hs::mbar_init(&B.ready[i], C::kByTma && !C::kConvert ? 4 : kTile);
             hs::mbar_init(&B.empty[i], 1);
         }
         hs::mbar_init(&B.q_full, C::kConvert ? kTile : C::kByTma ? 1 : kQThreads);
@@ -1584,8 +1616,6 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
             hs::mbar_init(&B.l_full[i], kTile);
             hs::mbar_init(&B.o_free[i], kTile);
             hs::mbar_init(&B.drain[i], 1);
-        }
-        for (int i = 0; i < 4; ++i) {
             hs::mbar_init(&B.sfull[i], 1);
             hs::mbar_init(&B.sempty[i], kTile);
         }
@@ -1596,7 +1626,6 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
         B.abort = 0;
         hs::fence_mbar_init();
     }
-    for (int i = tid; i < C::kRing * C::kSubs * 4; i += kThreads) (&B.odd[0][0][0])[i] = 0;
     if (C::kByTma && warp == kTmaWarp && lane < 3)
         asm volatile("prefetch.tensormap [%0];" ::"l"(lane == 0 ? &kmap : lane == 1 ? &vmap : &qmap)
                      : "memory");
