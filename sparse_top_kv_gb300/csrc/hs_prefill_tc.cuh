@@ -111,12 +111,8 @@ template <typename C>
 struct Bars {
     uint64_t kfull[C::NS], vfull[C::NS], ready[C::NS], empty[C::NS];
     uint64_t sfull[2], sempty[2], unit_full[kUnitRing], unit_free[kUnitRing];
-    uint64_t q_raw, q_full, q_empty, s_full[2], s_free, p_full[2], pv_done[2], l_full[2], o_free[2], drain[2];
+    uint64_t q_raw, q_full, q_empty, s_full[2], s_free[2], p_full[2], pv_done[2], l_full[2], o_free[2], drain[2];
     Seg unit[kUnitRing];
-    int64_t place0, place1, start;  // the run, and where its first unit starts
-    int64_t per;                    // the call's places: per * ctas + rest
-    int32_t rest;
-    int32_t row, kvh, block;        // the run's first unit
     uint32_t tmem_base;
     volatile int32_t abort;
     alignas(16) uint32_t loaded[C::kRing][4];     // tokens of a tile that were loaded
@@ -145,85 +141,6 @@ __device__ __forceinline__ bool any_sees(const PrefillArgs& a, const Seg& s, int
 __device__ __forceinline__ bool all_see(const PrefillArgs& a, const Seg& s, int t) {
     return t + kTile - 1 <= s.p0 &&
            (a.window == 0 || t > s.p0 + s.m - 1 - a.window || t + kTile <= a.sinks);
-}
-
-// The run of this CTA: its places, and the unit that they begin in.  All
-// threads; ends with a barrier.
-template <typename B_>
-__device__ __forceinline__ void make_plan(const PrefillArgs& a, B_& B, int64_t* sums) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int kWarps = kThreads / 32;
-    // Inclusive sum over the block; *all receives the total.
-    const auto scan = [&](int64_t v, int64_t* all) {
-        const int64_t own = v;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t o = __shfl_up_sync(0xffffffffu, v, d);
-            if (lane >= d) v += o;
-        }
-        __syncthreads();
-        if (lane == 31) sums[warp] = v;
-        __syncthreads();
-        int64_t before = 0, total = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) before += sums[w];
-            total += sums[w];
-        }
-        *all = total;
-        return before + v - own;
-    };
-    int64_t total = 0, at = 0, own = 0;
-    Request x{};
-    for (int r0 = 0; r0 < a.rows; r0 += kThreads) {
-        own = 0;
-        if (r0 + tid < a.rows) {
-            x = request_of(a, r0 + tid);
-            own = places_of(a, x);
-        }
-        int64_t all;
-        at = scan(own, &all);
-        total += all;
-    }
-    const int64_t per = total / a.ctas;
-    const int rest = int(total - per * a.ctas);
-    const int64_t p0 = run_begin(per, rest, a.ctas, blockIdx.x);
-    const int64_t p1 = run_begin(per, rest, a.ctas, blockIdx.x + 1);
-    int64_t base = 0;
-    for (int r0 = 0; r0 < a.rows; r0 += kThreads) {
-        if (a.rows > kThreads) {
-            own = 0;
-            if (r0 + tid < a.rows) {
-                x = request_of(a, r0 + tid);
-                own = places_of(a, x);
-            }
-            int64_t all;
-            at = base + scan(own, &all);
-            base += all;
-        }
-        if (own > 0 && p0 >= at && p0 < at + own) {
-            const int64_t each = own / a.kv_heads;
-            const int kvh = int((p0 - at) / each);
-            const int64_t rel = p0 - at - kvh * each;
-            int lo = 0, hi = blocks_of(a, x.n);
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (places(a, x, mid) <= rel) lo = mid;
-                else hi = mid;
-            }
-            B.row = r0 + tid;
-            B.kvh = kvh;
-            B.block = lo;
-            B.start = at + kvh * each + places(a, x, lo);
-        }
-    }
-    if (tid == 0) {
-        B.place0 = p0;
-        B.place1 = p1;
-        B.per = per;
-        B.rest = rest;
-    }
-    __syncthreads();
 }
 
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int tok,
@@ -382,6 +299,15 @@ __device__ __forceinline__ uint32_t pack(float x, float y) {
     }
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
+// x if `bit` is set in bits, else -inf.  (The compiler's own: ten instructions.)
+__device__ __forceinline__ float keep_if(float x, uint32_t bits, uint32_t bit) {
+    float r;
+    asm("{\n\t.reg .pred p;\n\t.reg .b32 t;\n\tand.b32 t, %2, %3;\n\tsetp.ne.u32 p, t, 0;\n\t"
+        "selp.f32 %0, %1, 0fFF800000, p;\n\t}"
+        : "=f"(r)
+        : "f"(x), "r"(bits), "r"(bit));
+    return r;
+}
 // The low n bits (n outside [0, 32] as the nearest).
 __device__ __forceinline__ uint32_t low_bits(int n) {
     return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
@@ -553,10 +479,6 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
     int t = 0, mine = 0;  // the CTA's tiles, this query tile's
     int own = 0;          // units with this query tile
     bool pending = false;  // a unit's output waits for its last product
-    // Whether rows of the last tile's V may have been taken out; which tile it was,
-    // and the row's position, its request and KV head.
-    bool odd = false;
-    int odd_tile = 0, odd_pos = 0, odd_row = 0, odd_kvh = 0;
     // Tokens of the CTA's tile t that a query at position pos sees.
     const auto see = [&](int t, int pos, uint32_t (&vis)[4]) {
         const uint4 ld = *reinterpret_cast<const uint4*>(B.loaded[t & (C::kRing - 1)]);
@@ -568,28 +490,6 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
             if (a.window > 0)
                 vis[j] &= ~low_bits(pos - a.window + 1 - b) | low_bits(a.sinks - b);
         }
-    };
-    // Rows of the last tile's V that were taken out, into the queries that see
-    // them.
-    const auto clear_odd = [&] {
-        uint32_t any = 0;
-        for (int u = 0; u < kSubs && ok; ++u) {
-            const int q = turn_of<C>(odd_tile, u);
-            ok = cx.wait_all(&B.ready[q % NS], q / NS);
-            const uint4* o = reinterpret_cast<const uint4*>(B.odd[odd_tile & (C::kRing - 1)][u]);
-#pragma unroll
-            for (int g = 0; g < C::kOddWords / 4; ++g) any |= o[g].x | o[g].y | o[g].z | o[g].w;
-        }
-        odd = false;
-        if (any == 0 || !ok) return;
-        ok = cx.pv_wait(w, mine - 1);
-        hs::tc::fence_after_sync();
-        uint32_t vis[4];
-        see(odd_tile, odd_pos, vis);
-        add_odd_rows<KV, D, C::kOddWords>(&a, &B.odd[odd_tile & (C::kRing - 1)][0][0][0], make_uint4(vis[0], vis[1], vis[2], vis[3]),
-                            B.tile[odd_tile & (C::kRing - 1)].x, odd_row, odd_kvh, o_addr,
-                            tmem + lanes + (NQ == 2 ? C::kPCol + uint32_t(w * 64)
-                                                    : uint32_t(((mine - 1) & 1) * 128)));
     };
     // The last tile's product has read P and is in O.
     const auto finish = [&] {
@@ -604,7 +504,6 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
     for (int unit = 0; cx.next_unit(unit, s, ok); ++unit) {
         const int n = s.n;
         if (w * a.tq >= s.m) {  // the second tile of a unit that has one
-            if (odd) clear_odd();
             if (pending) finish();
             t += n;
             continue;
@@ -621,7 +520,6 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
             const int ph = NQ == 2 ? mine : mine >> 1;
             const uint32_t s_addr = tmem + lanes + uint32_t(NQ == 2 ? 0 : x * 128);
             const uint32_t p_addr = NQ == 2 ? tmem + lanes + C::kPCol + uint32_t(w * 64) : s_addr;
-            if (odd) clear_odd();
             ok = ok && cx.wait_all(&B.s_full[x], ph);
             if (!ok) break;
             hs::tc::fence_after_sync();
@@ -641,8 +539,9 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
             hs::tc::tmem_wait_ld();
             if (NQ == 2) {
                 hs::tc::fence_before_sync();
-                hs::mbar_arrive(&B.s_free);
+                hs::mbar_arrive(&B.s_free[0]);
             }
+            if (pending) finish();
             if (scl < 0.f) {
 #pragma unroll
                 for (int c = 0; c < 128; ++c) v[c] = -v[c];
@@ -652,11 +551,11 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
                 uint32_t vis[4];
                 see(t, pos, vis);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (__any_sync(0xffffffffu, vis[j] != 0xffffffffu))
+                for (int j = 0; j < 4; ++j) {
+                    if (__all_sync(0xffffffffu, vis[j] == 0xffffffffu)) continue;
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (!((vis[j] >> c) & 1u)) v[32 * j + c] = -CUDART_INF_F;
+                    for (int c = 0; c < 32; ++c) v[32 * j + c] = keep_if(v[32 * j + c], vis[j], 1u << c);
+                }
             }
             uint64_t as2, ref2, s0 = 0, s1 = 0;
             const auto refer = [&] {
@@ -681,9 +580,8 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
                 }
                 tmem_st16u(p_addr + c * 16, pk);
             };
-            // The reference moves up to the maximum where that is far above;
-            // what has been summed is scaled down.
-            const auto raise = [&] {
+            // The largest logit, as a reference.
+            const auto highest = [&] {
                 float mx[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
                 for (int c = 4; c < 124; c += 8)
@@ -691,55 +589,54 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
                     for (int j = 0; j < 4; ++j) mx[j] = max3(mx[j], v[c + 2 * j], v[c + 2 * j + 1]);
                 mx[0] = max3(mx[0], v[124], v[125]);
                 mx[1] = max3(mx[1], v[126], v[127]);
-                const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * as - C::kShift;
-                const bool grow = top > off + C::kThresh || (off == -CUDART_INF_F && top > off);
-                if (first) {
-                    if (grow) off = top;
-                    return false;
-                }
-                if (!__any_sync(0xffffffffu, grow)) return false;
-                const float to = grow ? top : off;
-                const float al = grow ? (off == -CUDART_INF_F ? 0.f : ex2(off - to)) : 1.f;
-                off = to;
-                l0 = fma2(l0, pair_of(al, al), 0);
-                l1 = fma2(l1, pair_of(al, al), 0);
-                if (NQ == 1) {
-                    ok = cx.pv_wait(w, mine - 1);
-                    hs::tc::fence_after_sync();
-                }
-#pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                    float o[16];
-                    hs::tc::tmem_ld16(o_addr + uint32_t(c), o);
-                    hs::tc::tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) o[j] *= al;
-                    hs::tc::tmem_st16(o_addr + uint32_t(c), o);
-                }
-                return true;
+                return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * as - C::kShift;
             };
-            if (mine > 0 && (NQ == 2 || pending)) {
-                finish();
+            // Whether the reference has to move up to it.
+            const auto far_above = [&](float top) {
+                return top > off + C::kThresh || (off == -CUDART_INF_F && top > off);
+            };
+            if (NQ == 2 && mine > 0) {
+                ok = ok && cx.pv_wait(w, mine - 1);
                 hs::tc::fence_after_sync();
-            }
-            if (part) {
-                odd = true;
-                odd_tile = t;
-                odd_pos = pos;
-                odd_row = s.row;
-                odd_kvh = s.kvh;
             }
             // Mostly the reference stays: the weights are made while the
             // maximum is found, and the first half again where it moved.
-            bool ahead = !part && !first && scl > 0.f;
-            if (!ahead) raise();
+            bool sure = part || first || scl < 0.f;
             for (;;) {
+                if (sure) {
+                    const float top = highest();
+                    const bool grow = far_above(top);
+                    if (first) {
+                        if (grow) off = top;
+                    } else if (__any_sync(0xffffffffu, grow)) {
+                        // What has been summed is scaled down.
+                        const float to = grow ? top : off;
+                        const float al = grow ? (off == -CUDART_INF_F ? 0.f : ex2(off - to)) : 1.f;
+                        off = to;
+                        l0 = fma2(l0, pair_of(al, al), 0);
+                        l1 = fma2(l1, pair_of(al, al), 0);
+                        if (NQ == 1) {
+                            ok = cx.pv_wait(w, mine - 1);
+                            hs::tc::fence_after_sync();
+                        }
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            float o[16];
+                            hs::tc::tmem_ld16(o_addr + uint32_t(c), o);
+                            hs::tc::tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) o[j] *= al;
+                            hs::tc::tmem_st16(o_addr + uint32_t(c), o);
+                        }
+                    }
+                }
                 refer();
                 s0 = s1 = 0;
                 weigh(0);
                 weigh(1);
-                if (!ahead || !raise()) break;
-                ahead = false;
+                if (sure) break;
+                sure = true;
+                if (!__any_sync(0xffffffffu, far_above(highest()))) break;
             }
             if (!ok) break;
             weigh(2);
@@ -749,6 +646,29 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
             hs::tc::tmem_wait_st();
             hs::tc::fence_before_sync();
             hs::mbar_arrive(&B.p_full[x]);
+            if (part) {
+                // Rows of V that were taken out, into the queries that see them.
+                uint32_t any = 0;
+                for (int u = 0; u < kSubs && ok; ++u) {
+                    const int q = turn_of<C>(t, u);
+                    ok = cx.wait_all(&B.ready[q % NS], q / NS);
+                    const uint4* o = reinterpret_cast<const uint4*>(B.odd[t & (C::kRing - 1)][u]);
+#pragma unroll
+                    for (int g = 0; g < C::kOddWords / 4; ++g) any |= o[g].x | o[g].y | o[g].z | o[g].w;
+                }
+                if (any != 0 && ok) {
+                    ok = cx.pv_wait(w, mine);
+                    hs::tc::fence_after_sync();
+                    uint32_t vis[4];
+                    see(t, pos, vis);
+                    add_odd_rows<KV, D, C::kOddWords>(
+                        &a, &B.odd[t & (C::kRing - 1)][0][0][0],
+                        make_uint4(vis[0], vis[1], vis[2], vis[3]), B.tile[t & (C::kRing - 1)].x,
+                        s.row, s.kvh, o_addr, p_addr);
+                }
+                if (!ok) break;
+            }
+            if (NQ == 1) hs::mbar_arrive(&B.s_free[x]);
         }
         if (!ok) break;
         // ---- The unit's state: its output is written by another warpgroup ----
@@ -772,7 +692,6 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
         B.factor[w][r] = f;
         pending = true;
     }
-    if (odd && ok) clear_odd();
     if (pending && ok) finish();
     if (!ok) cx.give_up();
 }
@@ -811,12 +730,13 @@ __device__ __forceinline__ bool qk_role(const Cta<C>& cx) {
             }
             for (int w = 0; w < tiles; ++w, ++n_qk) {
                 const int x = NQ == 2 ? 0 : t & 1;
-                // The last softmax has taken S, or the last product of
-                // this buffer's P is done.
+                // The last softmax has taken S; or the last product of this
+                // buffer's P is done, and its softmax needs P no more.
                 if (NQ == 2) {
-                    if (n_qk > 0) ok = ok && cx.wait_all(&B.s_free, n_qk - 1);
+                    if (n_qk > 0) ok = ok && cx.wait_all(&B.s_free[0], n_qk - 1);
                 } else if (t >= 2) {
                     ok = ok && cx.wait_all(&B.pv_done[x], (t - 2) >> 1);
+                    ok = ok && cx.wait_all(&B.s_free[x], (t - 2) >> 1);
                 }
                 hs::tc::fence_after_sync();
                 if (!ok) break;
@@ -1501,9 +1421,53 @@ __device__ __forceinline__ bool plan_role(const Cta<C>& cx) {
     const PrefillArgs& a = cx.a;
     Bars<C>& B = cx.B;
     const int lane = threadIdx.x & 31;
-    const int64_t place0 = B.place0, place1 = B.place1;
-    int64_t start = B.start;
-    int row = B.row, kvh = B.kvh, block = B.block, unit = 0;
+    constexpr uint32_t kAll = 0xffffffffu;
+    // The run: the call's places, dealt to the CTAs, a lane per request.
+    int64_t total = 0;
+#pragma unroll 2
+    for (int r = lane; r < a.rows; r += 32) total += places_of(a, request_of(a, r));
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(kAll, total, d);
+    const int64_t per = total / a.ctas;
+    const int rest = int(total - per * a.ctas);
+    const int64_t place0 = run_begin(per, rest, a.ctas, blockIdx.x);
+    const int64_t place1 = run_begin(per, rest, a.ctas, blockIdx.x + 1);
+    // The unit that it begins in.
+    int64_t start = 0;
+    int row = 0, kvh = 0, block = 0, unit = 0;
+    if (place0 < place1) {
+        for (int64_t before = 0;; row += 32) {
+            const int r = row + lane;
+            const int64_t own = r < a.rows ? places_of(a, request_of(a, r)) : 0;
+            int64_t upto = own;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t o = __shfl_up_sync(kAll, upto, d);
+                if (lane >= d) upto += o;
+            }
+            upto += before;
+            const uint32_t past = __ballot_sync(kAll, upto > place0);
+            before = __shfl_sync(kAll, upto, 31);
+            if (past != 0) {
+                const int at = __ffs(past) - 1;
+                start = __shfl_sync(kAll, upto - own, at);
+                const int64_t each = __shfl_sync(kAll, own, at) / a.kv_heads;
+                row += at;
+                kvh = int((place0 - start) / each);
+                start += kvh * each;
+                break;
+            }
+            if (row + 32 >= a.rows) break;  // (cannot be)
+        }
+        const Request x = request_of(a, row);
+        int hi = blocks_of(a, x.n);
+        while (hi - block > 1) {
+            const int mid = (block + hi) >> 1;
+            if (places(a, x, mid) <= place0 - start) block = mid;
+            else hi = mid;
+        }
+        start += places(a, x, block);
+    }
     bool ok = true, head = false;
     const auto publish = [&](const Seg& s) {
         if (unit >= kUnitRing)
@@ -1541,8 +1505,8 @@ __device__ __forceinline__ bool plan_role(const Cta<C>& cx) {
                     head = true;
                     SharedUnit u;
                     u.start = start;
-                    u.per = B.per;
-                    u.rest = B.rest;
+                    u.per = per;
+                    u.rest = rest;
                     u.cost = cost;
                     u.tiles = nt;
                     u.first = s.first;
@@ -1608,7 +1572,7 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
         hs::mbar_init(&B.q_full, C::kConvert ? kTile : C::kByTma ? 1 : kQThreads);
         hs::mbar_init(&B.q_raw, 1);
         hs::mbar_init(&B.q_empty, 1);
-        hs::mbar_init(&B.s_free, kTile);
+        for (int w = 0; w < 2; ++w) hs::mbar_init(&B.s_free[w], kTile);
         for (int i = 0; i < 2; ++i) {
             hs::mbar_init(&B.s_full[i], 1);
             hs::mbar_init(&B.p_full[i], kTile);
@@ -1644,7 +1608,6 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
             if (a.seq_lens[r] > a.max_len || c0 < 0 || c1 < c0 || c1 > a.tokens)
                 hs::set_status(a.status, HS_ERR_BAD_INDEX);
         }
-    make_plan(a, B, reinterpret_cast<int64_t*>(smem));
     const Cta<C> cx{ta, a, B, smem, hs::smem_u32(smem), B.tmem_base};
     bool ok = true;
     if (warp < 8) {

@@ -132,6 +132,21 @@ def test_what_a_query_does_not_attend_to_has_no_effect(dtype, cache):
         check(s, window=window)
 
 
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (FP, E4)])
+@pytest.mark.parametrize("heads,d", [(16, 256), (16, 128)])
+def test_infinite_values_ahead_of_many_tiles(heads, d, dtype, cache):
+    """Where the window begins: rows that a part of the queries sees are added
+    apart, while the tiles behind them are under way."""
+    lens = [690 + i for i in range(160)]
+    s = setup([8] * 160, lens, heads, 1, d, 16, dtype, cache, seed=5)
+    for r, T in enumerate(lens):
+        for back, dim in ((563, 3), (565, d - 1)):
+            t = T - back
+            s["v"][s["table"][r, t // 16].item(), t % 16, 0, dim] = (
+                math.nan if cache == E4 or r % 2 else math.inf)
+    check(s, window=560)
+
+
 def test_queries_before_position_zero_and_empty_requests():
     s = setup([4, 3, 0, 5], [0, 2, 9, -3], 8, 2, 128, 16, pad=2)
     out, lse = check(s)
