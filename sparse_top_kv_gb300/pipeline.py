@@ -668,3 +668,185 @@ class BudgetedDecoder:
         self.graph_v.copy_(v_new, non_blocking=True)
         self.graph.replay()
         return self.out, self.lse
+
+
+class PagedBatch:
+    """Continuous batching over caches that stay on the device: in a step every
+    request gets any number of new tokens (a prompt or a chunk of one, drafted
+    tokens, a single one, none), or gives its last tokens up again.  `grow`
+    makes room for a step's tokens (hs_paged_extend) once for all `layers`;
+    `attend` rotates a layer's q and k, writes k and v into its cache
+    (hs_rope_append) and attends to all that is cached (hs_paged_prefill).
+
+    `num_reqs` fixed places for requests of at most `max_len` tokens that share
+    `num_pages` pages (default: enough for all); `max_tokens` bounds a step's
+    new tokens.  The requests' tokens lie one after another in q, k and v, in the
+    order of their places; rows behind the last one are not read.  No call
+    reads device memory on the host, so that a step can be captured; `check`
+    does, and raises what the steps so far have reported.
+
+    cache_dtype: dtype or torch.float8_e4m3fn (with k_scale, v_scale fp32
+    [layers, kv_heads]).  inv_freq, mscale: as hs.rope_frequencies gives them
+    (default: over all of d, base 10000)."""
+
+    def __init__(self, *, num_reqs, heads, kv_heads, d, page_size, max_len, max_tokens, scale,
+                 layers=1, num_pages=None, inv_freq=None, mscale=1.0, interleaved=False, window=0,
+                 num_sinks=0, dtype=torch.bfloat16, cache_dtype=None, k_scale=None, v_scale=None,
+                 device="cuda"):
+        cache_dtype = dtype if cache_dtype is None else cache_dtype
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"dtype: torch.bfloat16 or torch.float16, got {dtype}")
+        if cache_dtype not in (dtype, torch.float8_e4m3fn):
+            raise TypeError(f"cache_dtype: {dtype} or torch.float8_e4m3fn, got {cache_dtype}")
+        if d not in (64, 128, 256) or kv_heads < 1 or heads < 1 or heads % kv_heads:
+            raise ValueError("d: 64, 128 or 256; heads: a multiple of kv_heads")
+        if heads // kv_heads > 128:
+            raise ValueError("heads: at most 128 to a KV head")
+        if min(num_reqs, layers, page_size, max_len, max_tokens) < 1:
+            raise ValueError("num_reqs, layers, page_size, max_len, max_tokens: at least one")
+        if num_reqs > 4096:
+            raise ValueError("num_reqs: at most 4096")
+        if window < 0 or num_sinks < 0:
+            raise ValueError("window, num_sinks: not negative")
+        blocks = -(-max_len // page_size)
+        num_pages = num_reqs * blocks if num_pages is None else num_pages
+        if num_pages < 1 or num_pages * page_size >= 1 << 31:
+            raise ValueError("num_pages: at least one, fewer than 2^31 tokens in all")
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is not None and cache_dtype != torch.float8_e4m3fn:
+                raise ValueError(f"{name}: for E4M3 caches")
+            if t is not None and tuple(t.shape) != (layers, kv_heads):
+                raise ValueError(f"{name}: expected {(layers, kv_heads)}, got {tuple(t.shape)}")
+        if inv_freq is None:
+            inv_freq = hs.rope_frequencies(d)[0]
+        if inv_freq.dim() != 1 or 2 * inv_freq.shape[0] > d:
+            raise ValueError("inv_freq: [rot / 2], rot at most d")
+        self.device = torch.device(device)
+        dev = self.device
+        self.num_reqs, self.layers, self.heads, self.kv_heads, self.d = (num_reqs, layers, heads,
+                                                                         kv_heads, d)
+        self.page_size, self.max_len, self.max_tokens = page_size, max_len, max_tokens
+        self.scale, self.mscale, self.interleaved = scale, mscale, interleaved
+        self.window, self.num_sinks = window, num_sinks
+        self.turns = hs.rope_turns(inv_freq, dev)
+        self.k_scale, self.v_scale = (None if t is None else t.to(dev, torch.float32).contiguous()
+                                      for t in (k_scale, v_scale))
+        shape = (layers, num_pages, page_size, kv_heads, d)
+        self.k_cache = torch.zeros(shape, dtype=cache_dtype, device=dev)
+        self.v_cache = torch.zeros(shape, dtype=cache_dtype, device=dev)
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.block_table = torch.zeros(num_reqs, blocks, **i32)
+        self.seq_lens = torch.zeros(num_reqs, **i32)
+        self.attend_lens = torch.zeros(num_reqs, **i32)
+        self.free_ring = torch.arange(num_pages, **i32)
+        self.ring_pos = torch.tensor([0, num_pages], dtype=torch.int64, device=dev)
+        self.cu_new = torch.zeros(num_reqs + 1, **i32)
+        self.slot, self.row_req, self.positions = (torch.full((max_tokens,), -1, **i32)
+                                                   for _ in range(3))
+        self.status = torch.zeros(1, **i32)
+        opt = dict(dtype=dtype, device=dev)
+        self.q_rot = torch.zeros(max_tokens, heads, d, **opt)
+        self.out = torch.zeros(layers, max_tokens, heads, d, **opt)
+        self.lse = torch.zeros(layers, max_tokens, heads, dtype=torch.float32, device=dev)
+        self.workspace = torch.empty(max(1, hs.paged_prefill_workspace_bytes(
+            max_tokens, num_reqs, heads, kv_heads, d, max_len, window=window,
+            num_sinks=num_sinks)), dtype=torch.uint8, device=dev)
+        self.graph = None
+
+    def _check_rows(self, q, k, v):
+        for name, t, heads in (("q", q, self.heads), ("k", k, self.kv_heads),
+                               ("v", v, self.kv_heads)):
+            shape = (self.max_tokens, heads, self.d)
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name}: expected {shape}, got {tuple(t.shape)}")
+            if t.dtype != self.q_rot.dtype:
+                raise TypeError(f"{name}: expected {self.q_rot.dtype}, got {t.dtype}")
+
+    def grow(self, new_lens):
+        """Room for new_lens[r] more tokens of every request r (int32 [num_reqs] on
+        the device; negative: its last tokens are given up).  A request that there
+        is no room for keeps what it has, and none of its new tokens is computed
+        in this step (`attend_lens` 0)."""
+        hs.paged_extend(new_lens, self.seq_lens, self.block_table, self.free_ring, self.ring_pos,
+                        self.page_size, self.max_tokens, attend_lens=self.attend_lens,
+                        cu_new=self.cu_new, slot=self.slot, row_req=self.row_req,
+                        positions=self.positions, status=self.status)
+
+    def attend(self, layer, q, k, v):
+        """The new tokens' attention in one layer: q [max_tokens, heads, d], k and v
+        [max_tokens, kv_heads, d] as the model's projections give them (tokens may
+        be strided).  Returns (out [max_tokens, heads, d], lse fp32 [max_tokens,
+        heads]), the same tensors in every step; rows of tokens that are not
+        computed keep what an earlier step left there."""
+        if not 0 <= layer < self.layers:
+            raise ValueError(f"layer: 0 to {self.layers - 1}")
+        self._check_rows(q, k, v)
+        scales = dict(k_scale=None if self.k_scale is None else self.k_scale[layer],
+                      v_scale=None if self.v_scale is None else self.v_scale[layer])
+        hs.rope_append(q, k, v, self.positions, self.slot, self.turns, self.k_cache[layer],
+                       self.v_cache[layer], interleaved=self.interleaved, mscale=self.mscale,
+                       q_out=self.q_rot, status=self.status, **scales)
+        return hs.paged_prefill(self.q_rot, self.k_cache[layer], self.v_cache[layer],
+                                self.block_table, self.cu_new, self.attend_lens, self.scale,
+                                window=self.window, num_sinks=self.num_sinks,
+                                max_len=self.max_len, out=self.out[layer], lse=self.lse[layer],
+                                workspace=self.workspace, status=self.status, **scales)
+
+    def step(self, new_lens, qs, ks, vs):
+        """grow, then attend in every layer (qs, ks, vs: one tensor a layer).
+        Returns (out [layers, max_tokens, heads, d], lse)."""
+        if not len(qs) == len(ks) == len(vs) == self.layers:
+            raise ValueError(f"qs, ks, vs: {self.layers} layers")
+        for rows in zip(qs, ks, vs):
+            self._check_rows(*rows)
+        self.grow(new_lens)
+        for layer, rows in enumerate(zip(qs, ks, vs)):
+            self.attend(layer, *rows)
+        return self.out, self.lse
+
+    def stop(self, r):
+        """Free place r and its pages (between two steps)."""
+        if not 0 <= r < self.num_reqs:
+            raise ValueError(f"r: 0 to {self.num_reqs - 1}")
+        drop = torch.zeros_like(self.seq_lens)
+        drop[r] = -self.max_len
+        self.grow(drop)
+
+    def check(self):
+        """Raise what the steps have reported since the last check (synchronizes):
+        HS_ERR_CAPACITY where a request was not served."""
+        code = int(self.status)
+        if code:
+            self.status.zero_()
+            raise hs.HSError("PagedBatch", code)
+
+    def capture(self):
+        """Capture one step over static inputs (self.graph_new, graph_q, graph_k,
+        graph_v) as a CUDA graph, which `replay` fills and runs.  The state is left
+        as it is.  Run at least one eager step first."""
+        opt = dict(dtype=self.q_rot.dtype, device=self.device)
+        n = self.max_tokens
+        self.graph_new = torch.zeros_like(self.seq_lens)
+        self.graph_q = torch.zeros(self.layers, n, self.heads, self.d, **opt)
+        self.graph_k = torch.zeros(self.layers, n, self.kv_heads, self.d, **opt)
+        self.graph_v = torch.zeros_like(self.graph_k)
+        self.graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(self.graph):
+            self.step(self.graph_new, self.graph_q, self.graph_k, self.graph_v)
+        return self.graph
+
+    def replay(self, new_lens, qs, ks, vs):
+        """One step through the captured graph."""
+        if self.graph is None:
+            raise ValueError("replay: capture a step first")
+        if not len(qs) == len(ks) == len(vs) == self.layers:
+            raise ValueError(f"qs, ks, vs: {self.layers} layers")
+        for rows in zip(qs, ks, vs):
+            self._check_rows(*rows)
+        self.graph_new.copy_(new_lens, non_blocking=True)
+        for layer in range(self.layers):
+            self.graph_q[layer].copy_(qs[layer], non_blocking=True)
+            self.graph_k[layer].copy_(ks[layer], non_blocking=True)
+            self.graph_v[layer].copy_(vs[layer], non_blocking=True)
+        self.graph.replay()
+        return self.out, self.lse
