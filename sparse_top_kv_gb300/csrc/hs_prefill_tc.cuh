@@ -478,7 +478,6 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
     bool ok = true;
     int t = 0, mine = 0;  // the CTA's tiles, this query tile's
     int own = 0;          // units with this query tile
-    bool pending = false;  // a unit's output waits for its last product
     // Tokens of the CTA's tile t that a query at position pos sees.
     const auto see = [&](int t, int pos, uint32_t (&vis)[4]) {
         const uint4 ld = *reinterpret_cast<const uint4*>(B.loaded[t & (C::kRing - 1)]);
@@ -491,26 +490,16 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
                 vis[j] &= ~low_bits(pos - a.window + 1 - b) | low_bits(a.sinks - b);
         }
     };
-    // The last tile's product has read P and is in O.
-    const auto finish = [&] {
-        ok = cx.pv_wait(w, mine - 1);
-        if (pending) {
-            hs::tc::fence_before_sync();
-            hs::mbar_arrive(&B.l_full[w]);
-        }
-        pending = false;
-    };
     Seg s;
     for (int unit = 0; cx.next_unit(unit, s, ok); ++unit) {
         const int n = s.n;
         if (w * a.tq >= s.m) {  // the second tile of a unit that has one
-            if (pending) finish();
             t += n;
             continue;
         }
         // The row's position; rows without a query see what the last does.
         const int pos = s.p0 + min(w * a.tq + tok, s.m - 1);
-        float scl = a.scale_log2;
+        float as = a.scale_log2;        // its size: the product made the sign
         float off = -CUDART_INF_F;      // reference - kShift
         uint64_t l0 = 0, l1 = 0;        // sums, in pairs
         bool first = true;
@@ -529,22 +518,16 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
             if (first) {
                 // (0 would turn masked places into NaN; 2^-126 does not show.)
                 if constexpr (E4) {
-                    scl *= pow2(-B.qexp[unit & (C::kSegRing - 1)][w * kTile + r]);
-                    if (a.k_scale != nullptr) scl *= a.k_scale[s.kvh];
+                    as *= pow2(-B.qexp[unit & (C::kSegRing - 1)][w * kTile + r]);
+                    if (a.k_scale != nullptr) as *= a.k_scale[s.kvh];
                 }
-                if (scl == 0.f) scl = 1.17549435e-38f;
+                as = as == 0.f ? 1.17549435e-38f : fabsf(as);
             }
             const bool part = B.tile[t & (C::kRing - 1)].y != 0;
-            const float as = fabsf(scl);
             hs::tc::tmem_wait_ld();
             if (NQ == 2) {
                 hs::tc::fence_before_sync();
                 hs::mbar_arrive(&B.s_free[0]);
-            }
-            if (pending) finish();
-            if (scl < 0.f) {
-#pragma unroll
-                for (int c = 0; c < 128; ++c) v[c] = -v[c];
             }
             if (part) {
                 // What this row sees of the tile, 32 tokens at a time.
@@ -601,7 +584,7 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
             }
             // Mostly the reference stays: the weights are made while the
             // maximum is found, and the first half again where it moved.
-            bool sure = part || first || scl < 0.f;
+            bool sure = part || first;
             for (;;) {
                 if (sure) {
                     const float top = highest();
@@ -690,9 +673,9 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
                 make_float2(off, l);
         }
         B.factor[w][r] = f;
-        pending = true;
+        hs::tc::fence_before_sync();
+        hs::mbar_arrive(&B.l_full[w]);
     }
-    if (pending && ok) finish();
     if (!ok) cx.give_up();
 }
 
@@ -704,6 +687,7 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
 // the time of both tiles' products for its softmax.  (With S and P of a tile in
 // the same columns QK has to wait for PV and the softmax is on the products'
 // path.)
+constexpr uint32_t kNegateA = 1u << 13;  // of the instruction descriptor
 template <typename C>
 __device__ __forceinline__ bool qk_role(const Cta<C>& cx) {
     constexpr int NQ = C::NQ, NS = C::NS, kSubs = C::kSubs, KV = C::kKind;
@@ -712,7 +696,6 @@ __device__ __forceinline__ bool qk_role(const Cta<C>& cx) {
     const uint32_t tmem = cx.tmem, sb = cx.sb;
     bool ok = true;
     Seg s;
-    constexpr uint32_t id = idesc<KV>(kTile, 0);
     const uint64_t q_desc = hs::tc::sdesc_sw128(sb, 16, 1024);
     const uint64_t k_desc = hs::tc::sdesc_sw128(sb + C::kRingOff, 16, 1024);
     int t = 0, segs = 0, n_qk = 0;
@@ -720,6 +703,10 @@ __device__ __forceinline__ bool qk_role(const Cta<C>& cx) {
         const int n = s.n;
         const int tiles = NQ == 2 && a.tq < s.m ? 2 : 1;
         ok = ok && cx.wait_all(&B.q_full, segs);
+        // A negative scale: the products with -Q.
+        const bool neg = (a.scale_log2 < 0.f) !=
+                         (C::kE4 && a.k_scale != nullptr && a.k_scale[s.kvh] < 0.f);
+        const uint32_t id = idesc<KV>(kTile, 0) | (neg ? kNegateA : 0u);
         for (int i = 0; i < n && ok; ++i, ++t) {
             uint32_t at[kSubs];
 #pragma unroll
@@ -835,18 +822,25 @@ __device__ __forceinline__ bool tma_role(const Cta<C>& cx, const CUtensorMap& qm
         // A box takes the heads of a KV head for a tile's tokens: its rows are the
         // tile's.  (Tokens of other requests behind a unit's own land in rows that
         // are not written.)
-        if (unit > 0) ok = cx.wait_all(&B.q_empty, unit - 1);
-        if (!ok) break;
-        segs = unit + 1;
-        if (lane == 0) {
-            const int tiles = C::NQ == 2 && s.m > a.tq ? 2 : 1;
-            hs::mbar_arrive_expect_tx(q_bar, q_bytes * tiles);
-            for (int w = 0; w < tiles; ++w)
-                for (int c = 0; c < C::kD / 64; ++c)
-                    tma_load_q(cx.sb + w * C::kQTile + c * kBlk, &qmap, c * 64, s.kvh * a.group,
-                               s.first + w * a.tq, q_bar);
-        }
-        __syncwarp();
+        const auto load_q = [&] {
+            if (unit > 0) ok = cx.wait_all(&B.q_empty, unit - 1);
+            if (!ok) return;
+            segs = unit + 1;
+            if (lane == 0) {
+                const int tiles = C::NQ == 2 && s.m > a.tq ? 2 : 1;
+                hs::mbar_arrive_expect_tx(q_bar, q_bytes * tiles);
+                for (int w = 0; w < tiles; ++w)
+                    for (int c = 0; c < C::kD / 64; ++c)
+                        tma_load_q(cx.sb + w * C::kQTile + c * kBlk, &qmap, c * 64, s.kvh * a.group,
+                                   s.first + w * a.tq, q_bar);
+            }
+            __syncwarp();
+        };
+        // The first tile's units go ahead of the queries, whose place is free only
+        // when the unit before has made its last logits.  (Two ring units: the
+        // places of a tile's own are free by then.  More would wait for products
+        // behind those logits, or for the converter, which begins with the queries.)
+        constexpr int kAhead = kSubs == 1 ? 2 : 1;
         for (int i = 0; i < s.n && ok; ++i, ++t) {
             const int t0 = token_of(s, i), tok = t0 + lane * bt;
             const int b = block_of(a, tok);
@@ -894,6 +888,13 @@ __device__ __forceinline__ bool tma_role(const Cta<C>& cx, const CUtensorMap& qm
                     for (int c = 0; c < kBoxes; ++c)
                         tma_load(dst + lane * box + c * kBlk, u < kSubs ? &kmap : &vmap,
                                  u % kSubs * C::kDims + c * 64, at, s.kvh, page, full);
+                }
+                if (i == 0 && u == kAhead - 1) {
+                    load_q();
+                    if (!ok) {
+                        ++seq;
+                        break;
+                    }
                 }
             }
         }
@@ -1142,13 +1143,16 @@ __device__ __forceinline__ bool check_role(const Cta<C>& cx) {
                                     ((B.loaded[t & (C::kRing - 1)][j] >> lane) & 1u);
                     unsigned char* row = cx.smem + C::kRingOff + q % NS * C::kUnit + r * 128;
                     bool odd = false;
+                    // (Rolled: fetching the unrolled code took 4000 cycles a unit.)
                     if (in)
+#pragma unroll 2
                         for (int c = 0; c < C::kDims / 8; ++c)
                             odd |= not_finite<C::kKind>(*reinterpret_cast<const uint4*>(
                                 row + (c >> 3) * kBlk + (((c + lane) & 7) << 4)));
                     const uint32_t all = __ballot_sync(0xffffffffu, odd);
                     if (lane == 0) B.odd[t & (C::kRing - 1)][u][0][j] = all;
                     if (!in || odd)
+#pragma unroll 2
                         for (int c = 0; c < C::kDims / 8; ++c)
                             *reinterpret_cast<uint4*>(row + (c >> 3) * kBlk + (((c + lane) & 7) << 4)) =
                                 make_uint4(0u, 0u, 0u, 0u);

@@ -132,6 +132,17 @@ def test_what_a_query_does_not_attend_to_has_no_effect(dtype, cache):
         check(s, window=window)
 
 
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (FP, FP), (BF, E4)])
+@pytest.mark.parametrize("scale", [-0.07, 0.0])
+def test_scales_that_are_not_positive(dtype, cache, scale):
+    s = setup([70, 3], [500, 130], 8, 2, 128, 16, dtype, cache)
+    s["scale"] = scale
+    check(s)
+    if cache == E4:
+        s["k_scale"] = s["k_scale"] * torch.tensor([-1.0, 1.0], device="cuda")
+        check(s, window=100, sinks=2)
+
+
 @pytest.mark.parametrize("dtype,cache", [(BF, BF), (FP, E4)])
 @pytest.mark.parametrize("heads,d", [(16, 256), (16, 128)])
 def test_infinite_values_ahead_of_many_tiles(heads, d, dtype, cache):
