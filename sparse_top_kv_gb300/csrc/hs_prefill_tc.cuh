@@ -85,7 +85,7 @@ struct Cfg {
     static constexpr int kStageOff = kRingOff + NS * kUnit;
     static constexpr int kBarOff = kStageOff + kStages * kStage;
     // TMEM columns.  Two query tiles: one S for both, a P of each, an O of each.
-    // One: two S buffers, whose first half P takes, and O.
+    // One: two S buffers, P in the first half of each half of them, and O.
     static constexpr uint32_t kPCol = 128, kOCol = 256;
     // Registers of a thread, by warpgroup: 2 * soft + products + loads = 512.
     static constexpr int kSoftRegs = kByTma ? 176 : 168, kMmaRegs = kByTma ? 64 : 72,
@@ -112,6 +112,7 @@ struct Bars {
     uint64_t kfull[C::NS], vfull[C::NS], ready[C::NS], empty[C::NS];
     uint64_t sfull[2], sempty[2], unit_full[kUnitRing], unit_free[kUnitRing];
     uint64_t q_raw, q_full, q_empty, s_full[2], s_free[2], p_full[2], pv_done[2], l_full[2], o_free[2], drain[2];
+    uint64_t pair[C::NQ == 1 ? 4 : 1];  // of warps that share rows
     Seg unit[kUnitRing];
     uint32_t tmem_base;
     volatile int32_t abort;
@@ -236,6 +237,9 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[1
         "r"(v[15])
         : "memory");
 }
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, float x) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "f"(x) : "memory");
+}
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
     uint32_t r;
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
@@ -287,6 +291,17 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
+}
+template <int N>
+__device__ __forceinline__ float largest(const float (&v)[N]) {
+    float mx[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+    for (int c = 4; c < N - 4; c += 8)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx[j] = max3(mx[j], v[c + 2 * j], v[c + 2 * j + 1]);
+    mx[0] = max3(mx[0], v[N - 4], v[N - 3]);
+    mx[1] = max3(mx[1], v[N - 2], v[N - 1]);
+    return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
 }
 template <int KV>
 __device__ __forceinline__ uint32_t pack(float x, float y) {
@@ -411,6 +426,18 @@ struct Cta {
         if ((threadIdx.x & 31) == 0) hs::mbar_arrive(&B.unit_free[k % kUnitRing]);
         return s.n > 0;
     }
+    // Tokens of the CTA's tile t that a query at position pos sees.
+    __device__ __forceinline__ void see(int t, int pos, uint32_t (&vis)[4]) const {
+        const uint4 ld = *reinterpret_cast<const uint4*>(B.loaded[t & (C::kRing - 1)]);
+        const int t0 = B.tile[t & (C::kRing - 1)].x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int b = t0 + 32 * j;
+            vis[j] = low_bits(pos + 1 - b) & (j == 0 ? ld.x : j == 1 ? ld.y : j == 2 ? ld.z : ld.w);
+            if (a.window > 0)
+                vis[j] &= ~low_bits(pos - a.window + 1 - b) | low_bits(a.sinks - b);
+        }
+    }
     __device__ __forceinline__ void give_up() const {
         hs::set_status(a.status, HS_ERR_TIMEOUT);
         B.abort = 1;
@@ -423,48 +450,45 @@ struct Cta {
 template <int KV, int D, int WORDS>
 __device__ __noinline__ void add_odd_rows(const PrefillArgs* ap, const uint32_t* odd, uint4 vis,
                                           int t0, int row, int kvh, uint32_t o_addr,
-                                          uint32_t p_addr) {
+                                          uint32_t p_addr, int u) {
     constexpr int kDims = D < 128 ? D : 128;
     const PrefillArgs& a = *ap;
+    odd += u * WORDS;
 #pragma unroll 1
     for (int j = 0; j < kTile; ++j) {
-        const uint32_t pw = tmem_ld1(p_addr + uint32_t(j >> 1));
+        uint32_t word = 0;
+        for (int g = 0; g < WORDS; g += 4) word |= odd[g + (j >> 5)];
+        if (!((word >> (j & 31)) & 1u)) continue;
+        // (A head size of 256: the second half's weights are 32 columns further.)
+        const uint32_t pw = tmem_ld1(p_addr + uint32_t((j >> 1) + (D == 256 && j >= 64 ? 32 : 0)));
         hs::tc::tmem_wait_ld();
         const uint32_t h = (j & 1) ? pw >> 16 : pw & 0xffffu;
         const float p = KV == kBf16 ? __uint_as_float(h << 16)
                                     : __half2float(__ushort_as_half(uint16_t(h)));
         const uint32_t vw = j < 32 ? vis.x : j < 64 ? vis.y : j < 96 ? vis.z : vis.w;
         const bool sees = (vw >> (j & 31)) & 1u;
+        const int tk = t0 + j, b = block_of(a, tk);
+        const int64_t page = a.block_table[row * a.bt_stride + b];
+        const void* from = static_cast<const char*>(a.v) +
+                           (page * a.page_stride + int64_t(tk - b * a.page_size) * a.row_stride +
+                            kvh * a.head_stride) * (KV == kE4m3 ? 1 : 2);
 #pragma unroll 1
-        for (int u = 0; u < D / kDims; ++u) {
-            uint32_t word = 0;
-            for (int g = 0; g < WORDS; g += 4) word |= odd[u * WORDS + g + (j >> 5)];
-            if (!((word >> (j & 31)) & 1u)) continue;
-            const int tk = t0 + j, b = block_of(a, tk);
-            const int64_t page = a.block_table[row * a.bt_stride + b];
-            const void* from = static_cast<const char*>(a.v) +
-                               (page * a.page_stride + int64_t(tk - b * a.page_size) * a.row_stride +
-                                kvh * a.head_stride) * (KV == kE4m3 ? 1 : 2);
-#pragma unroll 1
-            for (int c = u * kDims; c < (u + 1) * kDims; c += 16) {
-                float o[16];
-                hs::tc::tmem_ld16(o_addr + uint32_t(c), o);
-                hs::tc::tmem_wait_ld();
+        for (int c = u * kDims; c < (u + 1) * kDims; c += 16) {
+            float o[16];
+            hs::tc::tmem_ld16(o_addr + uint32_t(c), o);
+            hs::tc::tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (sees) o[e] = fmaf(p, element<KV>(from, c + e), o[e]);
-                hs::tc::tmem_st16(o_addr + uint32_t(c), o);
-                hs::tc::tmem_wait_st();
-            }
+            for (int e = 0; e < 16; ++e)
+                if (sees) o[e] = fmaf(p, element<KV>(from, c + e), o[e]);
+            hs::tc::tmem_st16(o_addr + uint32_t(c), o);
+            hs::tc::tmem_wait_st();
         }
     }
 }
-
-// -------------------------------- softmax ---------------------------------
-// A warpgroup per query tile, a thread per row.
 template <typename C>
 __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
-    constexpr int NQ = C::NQ, NS = C::NS, kSubs = C::kSubs, KV = C::kKind, D = C::kD;
+    static_assert(C::NQ == 2 && C::kSubs == 1, "two query tiles");
+    constexpr int NS = C::NS, KV = C::kKind, D = C::kD;
     constexpr bool E4 = C::kE4;
     const PrefillArgs& a = cx.a;
     Bars<C>& B = cx.B;
@@ -474,22 +498,10 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
     const int r = tid & 127;   // row of the tile, and TMEM lane
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const int tok = r / a.group, hd = r - tok * a.group;  // its new token and query head
-    const uint32_t o_addr = tmem + lanes + C::kOCol + uint32_t(NQ == 2 ? w * 128 : 0);
+    const uint32_t o_addr = tmem + lanes + C::kOCol + uint32_t(w * 128);
     bool ok = true;
     int t = 0, mine = 0;  // the CTA's tiles, this query tile's
     int own = 0;          // units with this query tile
-    // Tokens of the CTA's tile t that a query at position pos sees.
-    const auto see = [&](int t, int pos, uint32_t (&vis)[4]) {
-        const uint4 ld = *reinterpret_cast<const uint4*>(B.loaded[t & (C::kRing - 1)]);
-        const int t0 = B.tile[t & (C::kRing - 1)].x;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int b = t0 + 32 * j;
-            vis[j] = low_bits(pos + 1 - b) & (j == 0 ? ld.x : j == 1 ? ld.y : j == 2 ? ld.z : ld.w);
-            if (a.window > 0)
-                vis[j] &= ~low_bits(pos - a.window + 1 - b) | low_bits(a.sinks - b);
-        }
-    };
     Seg s;
     for (int unit = 0; cx.next_unit(unit, s, ok); ++unit) {
         const int n = s.n;
@@ -505,11 +517,9 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
         bool first = true;
         const int last = mine + n;
         for (; mine < last; ++t, ++mine, first = false) {
-            const int x = NQ == 2 ? w : mine & 1;
-            const int ph = NQ == 2 ? mine : mine >> 1;
-            const uint32_t s_addr = tmem + lanes + uint32_t(NQ == 2 ? 0 : x * 128);
-            const uint32_t p_addr = NQ == 2 ? tmem + lanes + C::kPCol + uint32_t(w * 64) : s_addr;
-            ok = ok && cx.wait_all(&B.s_full[x], ph);
+            const uint32_t s_addr = tmem + lanes;
+            const uint32_t p_addr = tmem + lanes + C::kPCol + uint32_t(w * 64);
+            ok = ok && cx.wait_all(&B.s_full[w], mine);
             if (!ok) break;
             hs::tc::fence_after_sync();
             float v[128];
@@ -525,14 +535,12 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
             }
             const bool part = B.tile[t & (C::kRing - 1)].y != 0;
             hs::tc::tmem_wait_ld();
-            if (NQ == 2) {
-                hs::tc::fence_before_sync();
-                hs::mbar_arrive(&B.s_free[0]);
-            }
+            hs::tc::fence_before_sync();
+            hs::mbar_arrive(&B.s_free[0]);
             if (part) {
                 // What this row sees of the tile, 32 tokens at a time.
                 uint32_t vis[4];
-                see(t, pos, vis);
+                cx.see(t, pos, vis);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (__all_sync(0xffffffffu, vis[j] == 0xffffffffu)) continue;
@@ -564,21 +572,12 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
                 tmem_st16u(p_addr + c * 16, pk);
             };
             // The largest logit, as a reference.
-            const auto highest = [&] {
-                float mx[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-                for (int c = 4; c < 124; c += 8)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) mx[j] = max3(mx[j], v[c + 2 * j], v[c + 2 * j + 1]);
-                mx[0] = max3(mx[0], v[124], v[125]);
-                mx[1] = max3(mx[1], v[126], v[127]);
-                return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * as - C::kShift;
-            };
+            const auto highest = [&] { return largest(v) * as - C::kShift; };
             // Whether the reference has to move up to it.
             const auto far_above = [&](float top) {
                 return top > off + C::kThresh || (off == -CUDART_INF_F && top > off);
             };
-            if (NQ == 2 && mine > 0) {
+            if (mine > 0) {
                 ok = ok && cx.pv_wait(w, mine - 1);
                 hs::tc::fence_after_sync();
             }
@@ -598,10 +597,6 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
                         off = to;
                         l0 = fma2(l0, pair_of(al, al), 0);
                         l1 = fma2(l1, pair_of(al, al), 0);
-                        if (NQ == 1) {
-                            ok = cx.pv_wait(w, mine - 1);
-                            hs::tc::fence_after_sync();
-                        }
 #pragma unroll 1
                         for (int c = 0; c < D; c += 16) {
                             float o[16];
@@ -628,30 +623,26 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
             l1 = add2(l1, s1);
             hs::tc::tmem_wait_st();
             hs::tc::fence_before_sync();
-            hs::mbar_arrive(&B.p_full[x]);
+            hs::mbar_arrive(&B.p_full[w]);
             if (part) {
                 // Rows of V that were taken out, into the queries that see them.
+                ok = cx.wait_all(&B.ready[t % NS], t / NS);
+                const uint4* o = reinterpret_cast<const uint4*>(B.odd[t & (C::kRing - 1)][0]);
                 uint32_t any = 0;
-                for (int u = 0; u < kSubs && ok; ++u) {
-                    const int q = turn_of<C>(t, u);
-                    ok = cx.wait_all(&B.ready[q % NS], q / NS);
-                    const uint4* o = reinterpret_cast<const uint4*>(B.odd[t & (C::kRing - 1)][u]);
 #pragma unroll
-                    for (int g = 0; g < C::kOddWords / 4; ++g) any |= o[g].x | o[g].y | o[g].z | o[g].w;
-                }
+                for (int g = 0; g < C::kOddWords / 4; ++g) any |= o[g].x | o[g].y | o[g].z | o[g].w;
                 if (any != 0 && ok) {
                     ok = cx.pv_wait(w, mine);
                     hs::tc::fence_after_sync();
                     uint32_t vis[4];
-                    see(t, pos, vis);
+                    cx.see(t, pos, vis);
                     add_odd_rows<KV, D, C::kOddWords>(
                         &a, &B.odd[t & (C::kRing - 1)][0][0][0],
                         make_uint4(vis[0], vis[1], vis[2], vis[3]), B.tile[t & (C::kRing - 1)].x,
-                        s.row, s.kvh, o_addr, p_addr);
+                        s.row, s.kvh, o_addr, p_addr, 0);
                 }
                 if (!ok) break;
             }
-            if (NQ == 1) hs::mbar_arrive(&B.s_free[x]);
         }
         if (!ok) break;
         // ---- The unit's state: its output is written by another warpgroup ----
@@ -675,6 +666,194 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
         B.factor[w][r] = f;
         hs::tc::fence_before_sync();
         hs::mbar_arrive(&B.l_full[w]);
+    }
+    if (!ok) cx.give_up();
+}
+
+
+// A unit of one query tile (a head size of 256): each warpgroup has half of a
+// tile's tokens, and of the output's dims where it is changed, so that the rows'
+// softmax has all eight warps.  (By four, the other idle, it took longer than the
+// tile's products: 2048 tokens over 8 K of E4M3, 465 us, now 419.)  Two warps that share rows tell each other their
+// largest logits by a column of S, and so have one reference.
+template <typename C>
+__device__ __forceinline__ void softmax_split_role(const Cta<C>& cx) {
+    static_assert(C::NQ == 1 && C::kSubs == 2, "one query tile");
+    constexpr int NS = C::NS, KV = C::kKind, D = C::kD;
+    constexpr bool E4 = C::kE4;
+    const PrefillArgs& a = cx.a;
+    Bars<C>& B = cx.B;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int w = warp >> 2;   // half
+    const int r = tid & 127;   // row of the tile, and TMEM lane
+    const uint32_t rows = cx.tmem + (uint32_t((warp & 3) * 32) << 16);
+    const int tok = r / a.group, hd = r - tok * a.group;  // its new token and query head
+    const uint32_t o_addr = rows + C::kOCol;
+    uint64_t* pair = &B.pair[warp & 3];
+    bool ok = true;
+    int t = 0, met = 0;  // the CTA's tiles; exchanges with the other warp
+    // What was written before is the other warp's to read, and its own this one's.
+    const auto meet = [&] {
+        __syncwarp();
+        if (lane == 0) hs::mbar_arrive(pair);
+    };
+    Seg s;
+    for (int unit = 0; cx.next_unit(unit, s, ok); ++unit) {
+        // The row's position; rows without a query see what the last does.
+        const int pos = s.p0 + min(tok, s.m - 1);
+        float as = a.scale_log2;        // its size: the product made the sign
+        float off = -CUDART_INF_F;      // reference - kShift
+        uint64_t l0 = 0, l1 = 0;        // sums, in pairs
+        bool first = true;
+        const int last = t + s.n;
+        for (; t < last; ++t, first = false) {
+            const int x = t & 1;
+            const uint32_t s_addr = rows + uint32_t(x * 128 + w * 64);  // and P
+            ok = ok && cx.wait_all(&B.s_full[x], t >> 1);
+            if (!ok) break;
+            hs::tc::fence_after_sync();
+            float v[64];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) tmem_ld32(s_addr + c * 32, v + c * 32);
+            if (first) {
+                // (0 would turn masked places into NaN; 2^-126 does not show.)
+                if constexpr (E4) {
+                    as *= pow2(-B.qexp[unit & (C::kSegRing - 1)][r]);
+                    if (a.k_scale != nullptr) as *= a.k_scale[s.kvh];
+                }
+                as = as == 0.f ? 1.17549435e-38f : fabsf(as);
+            }
+            const bool part = B.tile[t & (C::kRing - 1)].y != 0;
+            hs::tc::tmem_wait_ld();
+            if (part) {
+                uint32_t vis[4];
+                cx.see(t, pos, vis);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t see = w == 0 ? vis[j] : vis[2 + j];
+                    if (__all_sync(0xffffffffu, see == 0xffffffffu)) continue;
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) v[32 * j + c] = keep_if(v[32 * j + c], see, 1u << c);
+                }
+            }
+            const float own = largest(v) * as - C::kShift;
+            tmem_st1(s_addr + 32, own);  // (behind P's columns)
+            hs::tc::tmem_wait_st();
+            hs::tc::fence_before_sync();
+            meet();
+            uint64_t s0 = 0, s1 = 0;
+            const auto weigh = [&] {
+                // Without a finite logit so far: subtract 0, every weight is
+                // 0 (a NaN logit stays NaN).
+                const float ref = off == -CUDART_INF_F ? 0.f : off;
+                const uint64_t as2 = pair_of(as, as), ref2 = pair_of(-ref, -ref);
+                s0 = s1 = 0;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        const int e = 32 * c + 2 * j;
+                        const float2 y = split(fma2(pair_of(v[e], v[e + 1]), as2, ref2));
+                        const float2 z = split(fma2(pair_of(v[e + 2], v[e + 3]), as2, ref2));
+                        const float2 p = make_float2(ex2(y.x), ex2(y.y)), q = make_float2(ex2(z.x), ex2(z.y));
+                        s0 = add2(s0, pair_of(p.x, p.y));
+                        s1 = add2(s1, pair_of(q.x, q.y));
+                        pk[j] = pack<KV>(p.x, p.y);
+                        pk[j + 1] = pack<KV>(q.x, q.y);
+                    }
+                    tmem_st16u(s_addr + c * 16, pk);
+                }
+            };
+            // Mostly the reference stays, and these weights stand.
+            if (!first) weigh();
+            ok = cx.wait_all(pair, met++);
+            if (!ok) break;
+            hs::tc::fence_after_sync();
+            const float other = __uint_as_float(tmem_ld1(rows + uint32_t(x * 128 + (1 - w) * 64 + 32)));
+            hs::tc::tmem_wait_ld();
+            const float top = fmaxf(own, other);
+            const bool grow = top > off + C::kThresh || (off == -CUDART_INF_F && top > off);
+            if (first) {
+                if (grow) off = top;
+                weigh();
+            } else if (__any_sync(0xffffffffu, grow)) {
+                // What has been summed is scaled down.
+                const float to = grow ? top : off;
+                const float al = grow ? (off == -CUDART_INF_F ? 0.f : ex2(off - to)) : 1.f;
+                off = to;
+                l0 = fma2(l0, pair_of(al, al), 0);
+                l1 = fma2(l1, pair_of(al, al), 0);
+                ok = cx.pv_wait(0, t - 1);
+                if (!ok) break;
+                hs::tc::fence_after_sync();
+#pragma unroll 1
+                for (int c = w * (D / 2); c < (w + 1) * (D / 2); c += 16) {
+                    float o[16];
+                    hs::tc::tmem_ld16(o_addr + uint32_t(c), o);
+                    hs::tc::tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) o[j] *= al;
+                    hs::tc::tmem_st16(o_addr + uint32_t(c), o);
+                }
+                weigh();
+            }
+            l0 = add2(l0, s0);
+            l1 = add2(l1, s1);
+            hs::tc::tmem_wait_st();
+            hs::tc::fence_before_sync();
+            hs::mbar_arrive(&B.p_full[x]);
+            if (part) {
+                // Rows of V that were taken out, into the queries that see them:
+                // a ring unit's dims each.
+                const int turn = turn_of<C>(t, w);
+                ok = cx.wait_all(&B.ready[turn % NS], turn / NS);
+                const uint4* o = reinterpret_cast<const uint4*>(B.odd[t & (C::kRing - 1)][w]);
+                uint32_t any = 0;
+#pragma unroll
+                for (int g = 0; g < C::kOddWords / 4; ++g) any |= o[g].x | o[g].y | o[g].z | o[g].w;
+                if (any != 0 && ok) {
+                    ok = cx.pv_wait(0, t);
+                    hs::tc::fence_after_sync();
+                    uint32_t vis[4];
+                    cx.see(t, pos, vis);
+                    add_odd_rows<KV, D, C::kOddWords>(
+                        &a, &B.odd[t & (C::kRing - 1)][0][0][0],
+                        make_uint4(vis[0], vis[1], vis[2], vis[3]), B.tile[t & (C::kRing - 1)].x,
+                        s.row, s.kvh, o_addr, rows + uint32_t(x * 128), w);
+                }
+                if (!ok) break;
+            }
+            hs::mbar_arrive(&B.s_free[x]);
+        }
+        if (!ok) break;
+        // ---- The unit's state: its output is written by another warpgroup ----
+        if (unit > 0) ok = cx.wait_all(&B.o_free[0], unit - 1);
+        if (!ok) break;
+        const float2 ls = split(add2(l0, l1));
+        float l = ls.x + ls.y;
+        if (w == 1) B.factor[0][r] = l;
+        meet();
+        ok = cx.wait_all(pair, met++);
+        if (!ok) break;
+        if (w == 0) {
+            l += B.factor[0][r];
+            const bool live = tok < a.tq && tok < s.m;
+            float f = 1.f;
+            if (s.slot < 0) {
+                f = l == 0.f ? 0.f : 1.f / l;
+                if (a.v_scale != nullptr && l != 0.f) f *= a.v_scale[s.kvh];
+                if (live && a.lse != nullptr)
+                    a.lse[int64_t(s.first + tok) * a.heads + s.kvh * a.group + hd] =
+                        l == 0.f ? -CUDART_INF_F : (off + log2f(l)) * kLn2;
+            } else if (live) {
+                reinterpret_cast<float2*>(a.part_ml)[int64_t(s.slot) * a.unit_rows + r] =
+                    make_float2(off, l);
+            }
+            B.factor[0][r] = f;
+        }
+        hs::tc::fence_before_sync();
+        hs::mbar_arrive(&B.l_full[0]);
     }
     if (!ok) cx.give_up();
 }
@@ -785,7 +964,8 @@ __device__ __forceinline__ bool pv_role(const Cta<C>& cx) {
                 for (int u = 0; u < kSubs; ++u)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        mma_ts4(tmem + C::kOCol + uint32_t((w + u) * 128), p_col + uint32_t(h * 32),
+                        mma_ts4(tmem + C::kOCol + uint32_t((w + u) * 128),
+                                p_col + uint32_t(h * (NQ == 2 ? 32 : 64)),
                                 v_desc + at[u] + uint32_t(h * 512), id,
                                 fresh && h == 0 ? 0u : 1u);
                 commit(&B.pv_done[x]);
@@ -1566,6 +1746,7 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
         hs::set_status(a.status, HS_ERR_CUDA);
         return;
     }
+    constexpr int kHalves = C::NQ == 1 ? 2 : 1;  // warpgroups of a query tile
     if (tid == 0) {
         for (int i = 0; i < C::NS; ++i) {
             hs::mbar_init(&B.kfull[i], C::kByTma && !C::kConvert ? 1 : kTile);
@@ -1576,12 +1757,13 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
         hs::mbar_init(&B.q_full, C::kConvert ? kTile : C::kByTma ? 1 : kQThreads);
         hs::mbar_init(&B.q_raw, 1);
         hs::mbar_init(&B.q_empty, 1);
-        for (int w = 0; w < 2; ++w) hs::mbar_init(&B.s_free[w], kTile);
+        for (uint64_t& b : B.pair) hs::mbar_init(&b, 2);
         for (int i = 0; i < 2; ++i) {
             hs::mbar_init(&B.s_full[i], 1);
-            hs::mbar_init(&B.p_full[i], kTile);
+            hs::mbar_init(&B.s_free[i], kHalves * kTile);
+            hs::mbar_init(&B.p_full[i], kHalves * kTile);
             hs::mbar_init(&B.pv_done[i], 1);
-            hs::mbar_init(&B.l_full[i], kTile);
+            hs::mbar_init(&B.l_full[i], kHalves * kTile);
             hs::mbar_init(&B.o_free[i], kTile);
             hs::mbar_init(&B.drain[i], 1);
             hs::mbar_init(&B.sfull[i], 1);
@@ -1589,7 +1771,7 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
         }
         for (int i = 0; i < kUnitRing; ++i) {
             hs::mbar_init(&B.unit_full[i], 1);
-            hs::mbar_init(&B.unit_free[i], 4 * C::NQ + 3 + 4);  // a warp each
+            hs::mbar_init(&B.unit_free[i], 8 + 3 + 4);  // a warp each
         }
         B.abort = 0;
         hs::fence_mbar_init();
@@ -1616,7 +1798,8 @@ prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUt
     bool ok = true;
     if (warp < 8) {
         set_max_regs_up<C::kSoftRegs>();
-        if (warp < 4 * C::NQ) softmax_role<C>(cx);
+        if constexpr (C::NQ == 2) softmax_role<C>(cx);
+        else softmax_split_role<C>(cx);
     } else if (warp < kLoadWarp) {
         set_max_regs_down<C::kMmaRegs>();
         if (warp <= kPvWarp) {
