@@ -80,6 +80,16 @@ int box_tokens(const PrefillArgs& a, int kv_dtype) {
     return bt;
 }
 
+// Whether units are of one query tile, whose softmax two warpgroups share, rather
+// than of two with one each (a head size of 256 has no other): E4M3 caches, whose
+// conversion leaves little time for anything else, where two tiles would mostly be
+// one.  Groups of 4, 64 requests over up to 4096 tokens: 4 new tokens each 180 ->
+// 154 us, up to 32 191 -> 168; 64, two tiles, 306 -> 425.  (16-bit caches: 3 % either
+// way.)  By half, so that a long prompt among single tokens has two.
+bool one_tile(const PrefillArgs& a, int kv_dtype, int bt) {
+    return kv_dtype == HS_E4M3 && bt > 0 && int64_t(a.tokens) * 2 <= int64_t(a.rows) * a.tq;
+}
+
 constexpr int kMergeThreads = 128;
 constexpr int kMergeDims = 16;  // dims of a block
 
@@ -100,22 +110,18 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
     // The slots of the unit's parts, in order; CTAs without a tile have none.
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
-        int n = 0;
-        for (int c0 = c;; c0 += 32) {
+        int n = 1;
+        for (int c0 = c + 1; c0 <= u.last; c0 += 32) {
             const int p = c0 + lane;
-            int slot = -1, i1 = 0;
-            if (p < a.ctas) {
-                const int64_t at = run_begin(u.per, u.rest, a.ctas, p) - u.start;
-                const int i0 = tile_at(at, u.cost, u.tiles);
-                i1 = tile_at(run_begin(u.per, u.rest, a.ctas, p + 1) - u.start, u.cost, u.tiles);
-                if (i1 > i0) slot = 2 * p + (at > 0 ? 0 : 1);
-            }
-            const uint32_t has = __ballot_sync(0xffffffffu, slot >= 0);
-            if (slot >= 0) slots[n + __popc(has & ((1u << lane) - 1u))] = slot;
-            n += __popc(has);
-            if (__any_sync(0xffffffffu, i1 == u.tiles || p + 1 >= a.ctas)) break;
+            const bool has = p <= u.last && a.shared[p].cont > 0;
+            const uint32_t all = __ballot_sync(0xffffffffu, has);
+            if (has) slots[n + __popc(all & ((1u << lane) - 1u))] = 2 * p;
+            n += __popc(all);
         }
-        if (lane == 0) count = n;
+        if (lane == 0) {
+            slots[0] = u.slot;
+            count = n;
+        }
     }
     __syncthreads();
     const int n = count, w = blockIdx.y / kParts, part = blockIdx.y % kParts, r = threadIdx.x;
@@ -303,17 +309,18 @@ extern "C" int hs_paged_prefill(const void* q, int64_t q_stride, int32_t q_dtype
     // Longer ones than any context see as much.
     a.window = int32_t(hs::min64(window, 1 << 30));
     a.sinks = int32_t(hs::min64(num_sinks, 1 << 30));
-    const Layout w = layout(d);
+    Layout w = layout(d);
     if (workspace == nullptr || workspace_bytes < w.total) return HS_ERR_CAPACITY;
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     a.tq = kTile / a.group;
+    const int bt = box_tokens(a, kv_dtype);
+    if (one_tile(a, kv_dtype, bt)) w.unit_rows = kTile;
     a.tb = a.tq * (w.unit_rows / kTile);
     a.ctas = w.ctas;
     a.part_ml = reinterpret_cast<float*>(ws + w.ml);
     a.part_o = reinterpret_cast<float*>(ws + w.o);
     a.shared = reinterpret_cast<SharedUnit*>(ws + w.shared);
     a.unit_rows = w.unit_rows;
-    const int bt = box_tokens(a, kv_dtype);
     const int rc = kv_dtype == HS_BF16   ? launch_bf16(a, d, bt, stream)
                    : kv_dtype == HS_FP16 ? launch_fp16(a, d, bt, stream)
                                          : launch_e4m3(a, d, bt, stream);

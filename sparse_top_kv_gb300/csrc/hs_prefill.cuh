@@ -20,11 +20,12 @@ constexpr int kExtra = 256;
 
 // A unit whose tokens several CTAs share, written by the CTA of its first part.
 struct SharedUnit {
-    int64_t start, per;     // its first place, and the places of a run
-    int32_t rest;           // (places left over)
-    int32_t cost, tiles;    // its places and tiles
-    int32_t first, tokens;  // its new tokens
-    int32_t kvh, valid;     // 0: this CTA has no first part
+    int32_t cont;   // tiles of this run's first unit where that began in an earlier one
+    // The unit whose first part this run has, if it is shared:
+    int32_t valid;
+    int32_t slot;   // of that part
+    int32_t last;   // the last run with a part of it
+    int32_t first, tokens, kvh;
 };
 
 struct PrefillArgs {
@@ -106,13 +107,18 @@ __device__ __forceinline__ int cost_of(const PrefillArgs& a, const Request& x, i
     const int lo = a.window > 0 ? max(0, base + b * a.tb + 1 - a.window) : 0;
     return kExtra + base + (b + 1) * a.tb - lo;
 }
-// First place of CTA c's run: floor(total c / ctas).
-__device__ __forceinline__ int64_t run_begin(int64_t per, int rest, int ctas, int c) {
-    return per * c + rest * c / ctas;
+// First place of CTA c's run: per = total / ctas each, and one more for the first
+// `rest` of them.
+__device__ __forceinline__ int64_t run_begin(int64_t per, int rest, int c) {
+    return per * c + min(c, rest);
+}
+// a / b, both positive.  (64-bit divisions were half the plan's time.)
+__device__ __forceinline__ int64_t quotient(int64_t a, int32_t b) {
+    return a >> 32 == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
 }
 // The tile that place `at` of a unit stands for.
 __device__ __forceinline__ int tile_at(int64_t at, int cost, int tiles) {
-    return at <= 0 ? 0 : at >= cost ? tiles : int(at * tiles / cost);
+    return at <= 0 ? 0 : at >= cost ? tiles : int(quotient(at * tiles, cost));
 }
 
 }  // namespace hs_prefill

@@ -66,21 +66,23 @@ struct TcArgs {
 // Who loads K and V.
 enum Loads { kTma = 0, kThreadsLoad = 1 };
 
-template <int KV, int D, int LD>
+template <int KV, int D, int LD, int QT>
 struct Cfg {
     static constexpr int kKind = KV, kD = D;
     static constexpr bool kE4 = KV == kE4m3, kByTma = LD == kTma;
     static constexpr bool kConvert = kE4 && kByTma;        // E4M3 units pass through a stage
-    static constexpr int NQ = D == 256 ? 1 : 2;            // query tiles of a unit
+    static constexpr int NQ = QT;                          // query tiles of a unit
+    static_assert(QT == 1 || D < 256, "two outputs of 256 dims do not fit TMEM");
     static constexpr int kDims = D < 128 ? D : 128;        // dims of a ring unit
     static constexpr int kSubs = D / kDims;                // ring units of a tile
     static constexpr int kUnit = kTile * kDims * 2;
     static constexpr int kQTile = kTile * D * 2;
-    static constexpr int NS = D == 64 ? 8 : kByTma && !kConvert ? 5 : 4;  // ring units
+    // Ring units: what shared memory holds.
+    static constexpr int NS = D == 64 ? 8 : (kByTma && !kConvert ? 5 : 4) + (D == 128 && QT == 1 ? 1 : 0);
     static constexpr int kStages = kConvert ? 2 : 0, kStage = kTile * kDims;
     static constexpr int kOddWords = kConvert ? 16 : 4;
     static constexpr int kRing = 8;        // tiles whose loaded tokens are remembered
-    static constexpr int kSegRing = D == 256 ? 4 : 2;  // units whose query scales are
+    static constexpr int kSegRing = QT == 1 ? 4 : 2;  // units whose query scales are
     static constexpr int kRingOff = NQ * kQTile;       // (queries first)
     static constexpr int kStageOff = kRingOff + NS * kUnit;
     static constexpr int kBarOff = kStageOff + kStages * kStage;
@@ -447,7 +449,7 @@ struct Cta {
 // Rows of V that were taken out of a tile, into a row's output: P stands until the
 // next one is written, O has the other rows' products.  Apart from the softmax's
 // code and registers: it hardly ever runs.
-template <int KV, int D, int WORDS>
+template <int KV, int D, int WORDS, bool SPLIT>
 __device__ __noinline__ void add_odd_rows(const PrefillArgs* ap, const uint32_t* odd, uint4 vis,
                                           int t0, int row, int kvh, uint32_t o_addr,
                                           uint32_t p_addr, int u) {
@@ -459,8 +461,8 @@ __device__ __noinline__ void add_odd_rows(const PrefillArgs* ap, const uint32_t*
         uint32_t word = 0;
         for (int g = 0; g < WORDS; g += 4) word |= odd[g + (j >> 5)];
         if (!((word >> (j & 31)) & 1u)) continue;
-        // (A head size of 256: the second half's weights are 32 columns further.)
-        const uint32_t pw = tmem_ld1(p_addr + uint32_t((j >> 1) + (D == 256 && j >= 64 ? 32 : 0)));
+        // (Split softmax: the second half's weights are 32 columns further.)
+        const uint32_t pw = tmem_ld1(p_addr + uint32_t((j >> 1) + (SPLIT && j >= 64 ? 32 : 0)));
         hs::tc::tmem_wait_ld();
         const uint32_t h = (j & 1) ? pw >> 16 : pw & 0xffffu;
         const float p = KV == kBf16 ? __uint_as_float(h << 16)
@@ -636,7 +638,7 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
                     hs::tc::fence_after_sync();
                     uint32_t vis[4];
                     cx.see(t, pos, vis);
-                    add_odd_rows<KV, D, C::kOddWords>(
+                    add_odd_rows<KV, D, C::kOddWords, false>(
                         &a, &B.odd[t & (C::kRing - 1)][0][0][0],
                         make_uint4(vis[0], vis[1], vis[2], vis[3]), B.tile[t & (C::kRing - 1)].x,
                         s.row, s.kvh, o_addr, p_addr, 0);
@@ -678,7 +680,7 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
 // largest logits by a column of S, and so have one reference.
 template <typename C>
 __device__ __forceinline__ void softmax_split_role(const Cta<C>& cx) {
-    static_assert(C::NQ == 1 && C::kSubs == 2, "one query tile");
+    static_assert(C::NQ == 1, "one query tile");
     constexpr int NS = C::NS, KV = C::kKind, D = C::kD;
     constexpr bool E4 = C::kE4;
     const PrefillArgs& a = cx.a;
@@ -803,7 +805,7 @@ __device__ __forceinline__ void softmax_split_role(const Cta<C>& cx) {
             hs::tc::tmem_wait_st();
             hs::tc::fence_before_sync();
             hs::mbar_arrive(&B.p_full[x]);
-            if (part) {
+            if (part && w < C::kSubs) {
                 // Rows of V that were taken out, into the queries that see them:
                 // a ring unit's dims each.
                 const int turn = turn_of<C>(t, w);
@@ -817,7 +819,7 @@ __device__ __forceinline__ void softmax_split_role(const Cta<C>& cx) {
                     hs::tc::fence_after_sync();
                     uint32_t vis[4];
                     cx.see(t, pos, vis);
-                    add_odd_rows<KV, D, C::kOddWords>(
+                    add_odd_rows<KV, D, C::kOddWords, true>(
                         &a, &B.odd[t & (C::kRing - 1)][0][0][0],
                         make_uint4(vis[0], vis[1], vis[2], vis[3]), B.tile[t & (C::kRing - 1)].x,
                         s.row, s.kvh, o_addr, rows + uint32_t(x * 128), w);
@@ -1021,6 +1023,7 @@ __device__ __forceinline__ bool tma_role(const Cta<C>& cx, const CUtensorMap& qm
         // places of a tile's own are free by then.  More would wait for products
         // behind those logits, or for the converter, which begins with the queries.)
         constexpr int kAhead = kSubs == 1 ? 2 : 1;
+        if (unit == 0) load_q();
         for (int i = 0; i < s.n && ok; ++i, ++t) {
             const int t0 = token_of(s, i), tok = t0 + lane * bt;
             const int b = block_of(a, tok);
@@ -1069,7 +1072,7 @@ __device__ __forceinline__ bool tma_role(const Cta<C>& cx, const CUtensorMap& qm
                         tma_load(dst + lane * box + c * kBlk, u < kSubs ? &kmap : &vmap,
                                  u % kSubs * C::kDims + c * 64, at, s.kvh, page, full);
                 }
-                if (i == 0 && u == kAhead - 1) {
+                if (i == 0 && u == kAhead - 1 && unit > 0) {
                     load_q();
                     if (!ok) {
                         ++seq;
@@ -1612,13 +1615,14 @@ __device__ __forceinline__ bool plan_role(const Cta<C>& cx) {
     for (int r = lane; r < a.rows; r += 32) total += places_of(a, request_of(a, r));
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(kAll, total, d);
-    const int64_t per = total / a.ctas;
+    const int64_t per = quotient(total, a.ctas);
     const int rest = int(total - per * a.ctas);
-    const int64_t place0 = run_begin(per, rest, a.ctas, blockIdx.x);
-    const int64_t place1 = run_begin(per, rest, a.ctas, blockIdx.x + 1);
+    const int64_t place0 = run_begin(per, rest, blockIdx.x);
+    const int64_t place1 = run_begin(per, rest, blockIdx.x + 1);
     // The unit that it begins in.
     int64_t start = 0;
     int row = 0, kvh = 0, block = 0, unit = 0;
+    SharedUnit shared{};
     if (place0 < place1) {
         for (int64_t before = 0;; row += 32) {
             const int r = row + lane;
@@ -1635,15 +1639,18 @@ __device__ __forceinline__ bool plan_role(const Cta<C>& cx) {
             if (past != 0) {
                 const int at = __ffs(past) - 1;
                 start = __shfl_sync(kAll, upto - own, at);
-                const int64_t each = __shfl_sync(kAll, own, at) / a.kv_heads;
                 row += at;
-                kvh = int((place0 - start) / each);
-                start += kvh * each;
                 break;
             }
             if (row + 32 >= a.rows) break;  // (cannot be)
         }
         const Request x = request_of(a, row);
+        const int64_t each = places(a, x, blocks_of(a, x.n));
+        for (; kvh + 32 < a.kv_heads; kvh += 32)
+            if (start + (kvh + 32) * each > place0) break;
+        kvh += __popc(__ballot_sync(kAll, kvh + lane + 1 < a.kv_heads &&
+                                              start + (kvh + lane + 1) * each <= place0));
+        start += kvh * each;
         int hi = blocks_of(a, x.n);
         while (hi - block > 1) {
             const int mid = (block + hi) >> 1;
@@ -1652,7 +1659,7 @@ __device__ __forceinline__ bool plan_role(const Cta<C>& cx) {
         }
         start += places(a, x, block);
     }
-    bool ok = true, head = false;
+    bool ok = true;
     const auto publish = [&](const Seg& s) {
         if (unit >= kUnitRing)
             ok = cx.wait_all(&B.unit_free[unit % kUnitRing], unit / kUnitRing - 1);
@@ -1685,19 +1692,19 @@ __device__ __forceinline__ bool plan_role(const Cta<C>& cx) {
             s.n = i1 - s.i0;
             s.slot = s.i0 == 0 && i1 == nt ? -1 : 2 * int(blockIdx.x) + (start < place0 ? 0 : 1);
             if (s.n > 0) {
+                if (start < place0) shared.cont = s.n;
                 if (s.slot >= 0 && s.i0 == 0) {
-                    head = true;
-                    SharedUnit u;
-                    u.start = start;
-                    u.per = per;
-                    u.rest = rest;
-                    u.cost = cost;
-                    u.tiles = nt;
-                    u.first = s.first;
-                    u.tokens = s.m;
-                    u.kvh = kvh;
-                    u.valid = 1;
-                    if (lane == 0) a.shared[blockIdx.x] = u;
+                    shared.valid = 1;
+                    shared.slot = s.slot;
+                    shared.first = s.first;
+                    shared.tokens = s.m;
+                    shared.kvh = kvh;
+                    for (int c = blockIdx.x + 1;; c += 32) {
+                        const uint32_t in = __ballot_sync(
+                            kAll, c + lane < a.ctas && run_begin(per, rest, c + lane) < start + cost);
+                        shared.last = c - 1 + __popc(in);
+                        if (in != kAll) break;
+                    }
                 }
                 publish(s);
             } else if (nt == 0 && place0 <= start) {
@@ -1727,16 +1734,16 @@ __device__ __forceinline__ bool plan_role(const Cta<C>& cx) {
         Seg end{};
         publish(end);
     }
-    if (!head && lane == 0) a.shared[blockIdx.x].valid = 0;
+    if (lane == 0) a.shared[blockIdx.x] = shared;
     return ok;
 }
 
-template <int KV, int D, int LD>
+template <int KV, int D, int LD, int QT>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_tc_kernel(const __grid_constant__ TcArgs ta, const __grid_constant__ CUtensorMap qmap,
                   const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap) {
-    using C = Cfg<KV, D, LD>;
+    using C = Cfg<KV, D, LD, QT>;
     const PrefillArgs& a = ta.p;
     extern __shared__ __align__(1024) unsigned char smem[];
     Bars<C>& B = *reinterpret_cast<Bars<C>*>(smem + C::kBarOff);
@@ -1835,14 +1842,14 @@ int encode_map(CUtensorMap* m, const void* base, const PrefillArgs& a, int kv_dt
 // Of the queries: dims (head dim, head, token), boxes of a query tile.
 int encode_q_map(CUtensorMap* m, const PrefillArgs& a, int dtype, int d);
 
-template <int KV, int D, int LD>
+template <int KV, int D, int LD, int QT>
 int launch_one(const PrefillArgs& a, int bt, hs_stream_t stream) {
-    using C = Cfg<KV, D, LD>;
+    using C = Cfg<KV, D, LD, QT>;
     TcArgs t{};
     t.p = a;
     t.bt = bt;
     t.timeout_ns = hs::kWaitTimeoutNs;
-    auto kern = prefill_tc_kernel<KV, D, LD>;
+    auto kern = prefill_tc_kernel<KV, D, LD, QT>;
     constexpr size_t smem = size_t(C::kBarOff) + sizeof(Bars<C>);
     static_assert(smem <= 227 * 1024, "shared memory");
     static int smem_set[64] = {};
@@ -1872,14 +1879,18 @@ int launch_one(const PrefillArgs& a, int bt, hs_stream_t stream) {
 // bt: tokens of a TMA box, or 0: threads load.
 template <int KV>
 int launch_kind(const PrefillArgs& a, int d, int bt, hs_stream_t stream) {
-    if (bt > 0) {
-        if (d == 64) return launch_one<KV, 64, kTma>(a, bt, stream);
-        if (d == 128) return launch_one<KV, 128, kTma>(a, bt, stream);
-        return launch_one<KV, 256, kTma>(a, bt, stream);
-    }
-    if (d == 64) return launch_one<KV, 64, kThreadsLoad>(a, 0, stream);
-    if (d == 128) return launch_one<KV, 128, kThreadsLoad>(a, 0, stream);
-    return launch_one<KV, 256, kThreadsLoad>(a, 0, stream);
+    if (d == 256)
+        return bt > 0 ? launch_one<KV, 256, kTma, 1>(a, bt, stream)
+                      : launch_one<KV, 256, kThreadsLoad, 1>(a, 0, stream);
+    if constexpr (KV == kE4m3)
+        if (a.unit_rows == kTile)
+            return d == 64 ? launch_one<KV, 64, kTma, 1>(a, bt, stream)
+                           : launch_one<KV, 128, kTma, 1>(a, bt, stream);
+    if (bt > 0)
+        return d == 64 ? launch_one<KV, 64, kTma, 2>(a, bt, stream)
+                       : launch_one<KV, 128, kTma, 2>(a, bt, stream);
+    return d == 64 ? launch_one<KV, 64, kThreadsLoad, 2>(a, 0, stream)
+                   : launch_one<KV, 128, kThreadsLoad, 2>(a, 0, stream);
 }
 
 }  // namespace tc

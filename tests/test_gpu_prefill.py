@@ -132,6 +132,23 @@ def test_what_a_query_does_not_attend_to_has_no_effect(dtype, cache):
         check(s, window=window)
 
 
+@pytest.mark.parametrize("dtype,heads,kv_heads,d,window,sinks,page", [
+    (BF, 8, 2, 128, 0, 0, 16), (FP, 8, 2, 128, 150, 3, 128), (BF, 16, 1, 64, 150, 3, 32),
+    (FP, 16, 1, 64, 0, 0, 16), (BF, 3, 3, 128, 150, 3, 16), (FP, 33, 1, 64, 150, 3, 16),
+    (BF, 80, 40, 64, 0, 0, 32)])
+def test_few_tokens_over_e4m3_caches(dtype, heads, kv_heads, d, window, sinks, page):
+    """Units of one query tile; rows that are not finite, some in part."""
+    new = [1, 0, 5, 2, 1, 3, 60, 1] + [1] * 60
+    lens = [700, 0, 5, 131, 1, 900, 400, 2500] + [1 + 29 * i for i in range(60)]
+    if heads // kv_heads > 32:
+        new[6] = 1
+    s = setup(new, lens, heads, kv_heads, d, page, dtype, E4, seed=d + heads)
+    for r, back in ((0, 151), (5, 150), (5, 2), (6, 400), (7, 1), (5, 152), (7, 152)):
+        t = lens[r] - back
+        s["v"][s["table"][r, t // page].item(), t % page, 0, d - 2] = math.nan
+    check(s, window=window, sinks=sinks)
+
+
 @pytest.mark.parametrize("dtype,cache", [(BF, BF), (FP, FP), (BF, E4)])
 @pytest.mark.parametrize("scale", [-0.07, 0.0])
 def test_scales_that_are_not_positive(dtype, cache, scale):
