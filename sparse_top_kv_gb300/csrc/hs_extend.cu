@@ -9,11 +9,13 @@
 //
 // Latency bounds it (a few KB to a few MB): one kernel of one CTA or one
 // cluster of CTAs.  Every CTA makes the prefix sums of all requests for itself
-// (at most 4096: four to a thread), then takes its share of the tokens and of
-// the pages that change hands, finding the request of each by bisection in
+// (at most 4096: one or four to a thread), then takes its share of the tokens
+// and of the pages that change hands, finding the request of each by bisection in
 // shared memory; a token in a fresh block reads its page from the ring, so
 // nothing waits for the table.  The cluster barrier between the two parts lets
-// lengths and ring be updated in place.
+// lengths and ring be updated in place.  Measured: 64 requests of one token 4.8
+// us (with a 64-bit remainder per token, four requests to a thread and a scan for
+// each sum 7.1), 512 requests of up to 1024 tokens 10.3 (15.9).
 #include "hs_common.cuh"
 #include "hs_pair.cuh"
 
@@ -21,7 +23,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kMaxRows = 4096;
-constexpr int kPer = kMaxRows / kThreads;  // requests of a thread
+constexpr int kAtOnce = 4;                 // tokens of a thread whose pages are read together
 constexpr int kMany = 1 << 30;             // prefix sums stop here (saturating)
 constexpr int kMaxCluster = 8;
 
@@ -34,7 +36,7 @@ struct ExtendArgs {
     int32_t* ring;
     int32_t pages;
     const int64_t* ring_pos;
-    int32_t page_size, max_tokens;
+    int32_t page_size, page_shift, max_tokens;  // page_shift: log2, -1: no power of two
     int32_t* lens_out;
     int32_t* attend_lens;
     int64_t* ring_out;
@@ -47,39 +49,53 @@ struct ExtendArgs {
 
 __device__ __forceinline__ int sat_add(int a, int b) { return min(a + b, kMany); }
 
-// Exclusive saturating prefix sum over the block of kPer consecutive values of
-// each thread (each in [0, kMany]); returns the block's total.
-__device__ __forceinline__ int scan_rows(int (&v)[kPer], int* scratch) {
-    int sum = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int x = v[i];
-        v[i] = sum;
-        sum = sat_add(sum, x);
-    }
+// Exclusive saturating prefix sums over the block of M lists of PER consecutive
+// values of each thread (each in [0, kMany]); total: the block's.
+template <int M, int PER>
+__device__ __forceinline__ void scan_rows(int (&v)[M][PER], int (&total)[M], int (*scratch)[32]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int incl = sum;
+    int incl[M], before[M];
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl = sat_add(incl, o);
+    for (int m = 0; m < M; ++m) {
+        incl[m] = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int x = v[m][i];
+            v[m][i] = incl[m];
+            incl[m] = sat_add(incl[m], x);
+        }
     }
-    const int before = __shfl_up_sync(0xffffffffu, incl, 1);
-    __syncthreads();  // scratch may still be read
-    if (lane == 31) scratch[warp] = incl;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1)
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            const int o = __shfl_up_sync(0xffffffffu, incl[m], d);
+            if (lane >= d) incl[m] = sat_add(incl[m], o);
+        }
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        before[m] = __shfl_up_sync(0xffffffffu, incl[m], 1);
+        if (lane == 31) scratch[m][warp] = incl[m];
+    }
     __syncthreads();
-    int w = scratch[lane];
+    int w[M];
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, w, d);
-        if (lane >= d) w = sat_add(w, o);
+    for (int m = 0; m < M; ++m) w[m] = scratch[m][lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1)
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            const int o = __shfl_up_sync(0xffffffffu, w[m], d);
+            if (lane >= d) w[m] = sat_add(w[m], o);
+        }
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        total[m] = __shfl_sync(0xffffffffu, w[m], 31);
+        const int base = warp == 0 ? 0 : __shfl_sync(0xffffffffu, w[m], warp - 1);
+        const int mine = sat_add(base, lane == 0 ? 0 : before[m]);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) v[m][i] = sat_add(mine, v[m][i]);
     }
-    const int total = __shfl_sync(0xffffffffu, w, 31);
-    const int base = warp == 0 ? 0 : __shfl_sync(0xffffffffu, w, warp - 1);
-    const int mine = sat_add(base, lane == 0 ? 0 : before);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) v[i] = sat_add(mine, v[i]);
-    return total;
 }
 
 // The last r of [0, rows) with start[r] <= i.
@@ -93,11 +109,8 @@ __device__ __forceinline__ int find(const int* start, int rows, int i) {
     return lo;
 }
 
-__device__ __forceinline__ int ring_at(int64_t first, int i, int pages) {
-    int x = int(first % pages) + i;
-    return x >= pages ? x - pages : x;
-}
-
+// PER: requests of a thread in the prefix sums.
+template <int PER>
 __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const ExtendArgs a) {
     extern __shared__ int shared[];
     int* cu = shared;                       // first token of each request
@@ -105,30 +118,46 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const ExtendArgs a)
     int* to = at + a.rows;                  // first page that it gives back
     int* lens = to + a.rows;                // tokens held before
     int* grow = lens + a.rows;              // tokens granted; < 0: given up
-    __shared__ int scratch[32];
+    __shared__ int scratch[4][32];          // (a row for each of the kernel's exchanges)
     const int tid = threadIdx.x, B = a.page_size;
     const int cl = gridDim.x, rank = blockIdx.x;
+    // Pages of n tokens, and the page of token n.
+    const auto page_of = [&](int n) { return a.page_shift >= 0 ? n >> a.page_shift : n / B; };
+    const auto pages_of = [&](int n) { return page_of(n + B - 1); };
     hs::pdl_wait();
     hs::pdl_trigger();
     const int64_t taken = a.ring_pos[0], returned = a.ring_pos[1];
-    // A ring that cannot be: nothing is taken or given back.
-    const bool odd = taken < 0 || returned < taken || returned - taken > a.pages;
-    const int avail = odd ? 0 : int(returned - taken);
-    const int64_t room = int64_t(a.max_blocks) * B;
-
-    int ask[kPer], need[kPer], back[kPer], held[kPer], n[kPer];
+    int held[PER], n[PER];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int r = tid * kPer + i;
+    for (int i = 0; i < PER; ++i) {
+        const int r = tid * PER + i;
         held[i] = n[i] = 0;
         if (r < a.rows) {
             held[i] = a.seq_lens[r];
             n[i] = a.new_lens[r];
         }
     }
+    // A ring that cannot be: nothing is taken or given back.
+    const bool odd = taken < 0 || returned < taken || returned - taken > a.pages;
+    const int avail = odd ? 0 : int(returned - taken);
+    const int64_t room = int64_t(a.max_blocks) * B;
+    // The ring's ends as places.  (A 64-bit remainder for every token took longer
+    // than the rest of the step.)
+    int take_at = 0, give_at = 0;
+    if (!odd && a.pages > 0) {
+        take_at = taken >> 32 == 0 ? int(uint32_t(taken) % uint32_t(a.pages)) : int(taken % a.pages);
+        give_at = take_at + avail;
+        if (give_at >= a.pages) give_at -= a.pages;
+    }
+    const auto ring_at = [&](int first, int i) {
+        const int x = first + i;
+        return x >= a.pages ? x - a.pages : x;
+    };
+
     bool bad = odd;
+    int asked[2][PER], own_ask[PER], own_back[PER];  // tokens asked for, pages given back
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
         // A length that the table cannot hold: the request is left alone.
         if (held[i] > room) {
             bad = true;
@@ -137,52 +166,46 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const ExtendArgs a)
         } else {
             held[i] = max(held[i], 0);
         }
-        ask[i] = min(max(n[i], 0), kMany);
-        back[i] = 0;
-        if (n[i] < 0 && held[i] > 0 && !odd) {
-            const int left = max(0, held[i] + max(n[i], -held[i]));
-            back[i] = (held[i] + B - 1) / B - (left + B - 1) / B;
-        }
+        own_ask[i] = min(max(n[i], 0), kMany);
+        own_back[i] = 0;
+        if (n[i] < 0 && held[i] > 0 && !odd)
+            own_back[i] = pages_of(held[i]) - pages_of(max(0, held[i] + max(n[i], -held[i])));
+        asked[0][i] = own_ask[i];
+        asked[1][i] = own_back[i];
     }
-    int own_ask[kPer], own_back[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        own_ask[i] = ask[i];
-        own_back[i] = back[i];
-    }
-    const int tokens = min(scan_rows(ask, scratch), a.max_tokens);
-    int given = scan_rows(back, scratch);
+    int totals[2];
+    scan_rows(asked, totals, scratch);
+    const int tokens = min(totals[0], a.max_tokens);
+    int given = totals[1];
     // More than the ring can hold: something else returned them already.
     if (given > a.pages - avail) {
         bad = true;
         given = 0;
     }
-    int own_need[kPer];
-    bool fits[kPer];
+    int need[1][PER], own_need[PER], all_need[1];
+    bool fits[PER];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
         fits[i] = held[i] >= 0 && int64_t(held[i]) + own_ask[i] <= room &&
-                  int64_t(ask[i]) + own_ask[i] <= a.max_tokens;
-        need[i] = fits[i] ? int((int64_t(held[i]) + own_ask[i] + B - 1) / B - (held[i] + B - 1) / B)
-                          : 0;
-        own_need[i] = need[i];
+                  int64_t(asked[0][i]) + own_ask[i] <= a.max_tokens;
+        own_need[i] = need[0][i] = fits[i] ? pages_of(held[i] + own_ask[i]) - pages_of(held[i]) : 0;
     }
-    scan_rows(need, scratch);
+    scan_rows(need, all_need, scratch + 2);
     bool refused = false;
     int last = 0;  // pages taken up to this thread's last served request
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int r = tid * kPer + i;
+    for (int i = 0; i < PER; ++i) {
+        const int r = tid * PER + i;
         if (r >= a.rows) continue;
-        const bool served = fits[i] && (own_need[i] == 0 || sat_add(need[i], own_need[i]) <= avail);
+        const bool served = fits[i] && (own_need[i] == 0 || sat_add(need[0][i], own_need[i]) <= avail);
         if (own_ask[i] > 0 && !served) refused = true;
-        cu[r] = min(ask[i], a.max_tokens);
-        at[r] = min(need[i], avail);
-        to[r] = back[i];
+        cu[r] = min(asked[0][i], a.max_tokens);
+        at[r] = min(need[0][i], avail);
+        to[r] = asked[1][i];
         lens[r] = held[i];
         grow[r] = n[i] > 0 ? (served ? n[i] : 0)
                            : (!odd && given >= own_back[i] ? max(n[i], -max(held[i], 0)) : 0);
-        if (served && own_need[i] > 0) last = max(last, need[i] + own_need[i]);
+        if (served && own_need[i] > 0) last = max(last, need[0][i] + own_need[i]);
     }
     if (rank == 0) {
         if (bad) hs::set_status(a.status, HS_ERR_BAD_INDEX);
@@ -190,10 +213,9 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const ExtendArgs a)
     }
     // Pages taken in all: what the last served request's share ends with.
     last = int(__reduce_max_sync(0xffffffffu, unsigned(last)));
+    if ((tid & 31) == 0) scratch[3][tid >> 5] = last;
     __syncthreads();
-    if ((tid & 31) == 0) scratch[tid >> 5] = last;
-    __syncthreads();
-    const int grown = int(__reduce_max_sync(0xffffffffu, unsigned(scratch[tid & 31])));
+    const int grown = int(__reduce_max_sync(0xffffffffu, unsigned(scratch[3][tid & 31])));
     // Every CTA has read the lengths and the ring's ends.
     if (cl > 1) hs::pair::cluster_sync();
 
@@ -212,32 +234,42 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const ExtendArgs a)
     }
     for (int i = first; i < grown; i += step) {
         const int r = find(at, a.rows, i);
-        a.table[r * a.bt_stride + (lens[r] + B - 1) / B + i - at[r]] =
-            a.ring[ring_at(taken, i, a.pages)];
+        a.table[r * a.bt_stride + pages_of(lens[r]) + i - at[r]] = a.ring[ring_at(take_at, i)];
     }
     for (int i = first; i < given; i += step) {
         const int r = find(to, a.rows, i);
-        a.ring[ring_at(returned, i, a.pages)] =
-            a.table[r * a.bt_stride + (lens[r] + grow[r] + B - 1) / B + i - to[r]];
+        a.ring[ring_at(give_at, i)] =
+            a.table[r * a.bt_stride + pages_of(lens[r] + grow[r]) + i - to[r]];
     }
-    for (int t = first; t < a.max_tokens; t += step) {
-        int r = -1, pos = -1, slot = -1;
-        if (t < tokens) {
-            r = find(cu, a.rows, t);
-            if (grow[r] > 0) {
-                pos = lens[r] + t - cu[r];
-                const int b = pos / B, have = (lens[r] + B - 1) / B;
-                const int page = b < have ? a.table[r * a.bt_stride + b]
-                                          : a.ring[ring_at(taken, at[r] + b - have, a.pages)];
-                slot = page >= 0 && page < a.pages ? page * B + pos - b * B : -1;
-                if (slot < 0) hs::set_status(a.status, HS_ERR_BAD_INDEX);
-            } else {
-                r = -1;
-            }
+    // The pages of kAtOnce tokens are read together.  (Four neighbouring tokens
+    // with one search and wide stores: no faster.)
+    for (int64_t t0 = first; t0 < a.max_tokens; t0 += int64_t(kAtOnce) * step) {
+        int req[kAtOnce], pos[kAtOnce], in[kAtOnce], page[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int64_t t = t0 + int64_t(k) * step;
+            req[k] = pos[k] = page[k] = -1;
+            in[k] = 0;
+            if (t >= tokens) continue;
+            const int r = find(cu, a.rows, int(t));
+            if (grow[r] <= 0) continue;
+            req[k] = r;
+            pos[k] = lens[r] + int(t) - cu[r];
+            const int b = page_of(pos[k]), have = pages_of(lens[r]);
+            in[k] = pos[k] - b * B;
+            page[k] = b < have ? a.table[r * a.bt_stride + b]
+                               : a.ring[ring_at(take_at, at[r] + b - have)];
         }
-        a.slot[t] = slot;
-        a.row_req[t] = r;
-        a.positions[t] = pos;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int64_t t = t0 + int64_t(k) * step;
+            if (t >= a.max_tokens) break;
+            const bool good = page[k] >= 0 && page[k] < a.pages;
+            if (req[k] >= 0 && !good) hs::set_status(a.status, HS_ERR_BAD_INDEX);
+            a.slot[t] = good ? page[k] * B + in[k] : -1;
+            a.row_req[t] = req[k];
+            a.positions[t] = pos[k];
+        }
     }
 }
 
@@ -282,6 +314,9 @@ extern "C" int hs_paged_extend(const int32_t* new_lens, const int32_t* seq_lens,
     a.pages = num_pages;
     a.ring_pos = ring_pos;
     a.page_size = page_size;
+    a.page_shift = -1;
+    for (int i = 0; i < 31; ++i)
+        if (page_size == (1 << i)) a.page_shift = i;
     a.max_tokens = max_tokens;
     a.lens_out = lens_out;
     a.attend_lens = attend_lens;
@@ -292,9 +327,13 @@ extern "C" int hs_paged_extend(const int32_t* new_lens, const int32_t* seq_lens,
     a.positions = positions;
     a.status = status;
     const size_t smem = size_t(rows) * 5 * 4;
-    static int smem_set[64] = {};
-    const int rc = hs_host::ensure_dynamic_smem(reinterpret_cast<const void*>(extend_kernel), smem,
-                                                smem_set);
+    // Four requests to a thread only where there are more than 1024: the chain of
+    // their sums is the call's time.
+    const bool one = rows <= kThreads;
+    auto kern = one ? extend_kernel<1> : extend_kernel<kMaxRows / kThreads>;
+    static int smem_set[2][64] = {};
+    const int rc = hs_host::ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem,
+                                                smem_set[one ? 0 : 1]);
     if (rc != HS_OK) return rc;
     const int cl = max_tokens > 2 * kThreads ? kMaxCluster : 1;
     cudaLaunchAttribute attr[2];
@@ -311,7 +350,7 @@ extern "C" int hs_paged_extend(const int32_t* new_lens, const int32_t* seq_lens,
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, extend_kernel, a) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) {
         cudaGetLastError();
         return HS_ERR_CUDA;
     }
