@@ -1023,13 +1023,22 @@ __device__ __forceinline__ bool tma_role(const Cta<C>& cx, const CUtensorMap& qm
         // places of a tile's own are free by then.  More would wait for products
         // behind those logits, or for the converter, which begins with the queries.)
         constexpr int kAhead = kSubs == 1 ? 2 : 1;
+        // Whether the lane's run of a tile is needed, and its page: looked up a tile
+        // ahead, for it takes as long as a small tile's copies.
+        bool next_wants = false;
+        int next_page = -1;
+        const auto look_up = [&](int i) {
+            const int tok = token_of(s, i) + lane * bt;
+            next_wants = lane < runs && any_sees(a, s, tok, bt);
+            if (next_wants) next_page = a.block_table[s.row * a.bt_stride + block_of(a, tok)];
+        };
+        look_up(0);
         if (unit == 0) load_q();
         for (int i = 0; i < s.n && ok; ++i, ++t) {
             const int t0 = token_of(s, i), tok = t0 + lane * bt;
-            const int b = block_of(a, tok);
-            const bool wants = lane < runs && any_sees(a, s, tok, bt);
-            const int page = wants ? a.block_table[s.row * a.bt_stride + b] : -1;
-            const bool want = wants && page >= 0 && page < a.num_pages;
+            const int b = block_of(a, tok), page = next_page;
+            const bool wants = next_wants, want = wants && page >= 0 && page < a.num_pages;
+            if (i + 1 < s.n) look_up(i + 1);
             if (wants && !want) bad = true;
             const uint32_t got = __ballot_sync(0xffffffffu, want);
             // (Read by the softmax of this tile, which the ring's units keep less
