@@ -67,10 +67,10 @@ int encode_q_map(CUtensorMap* m, const PrefillArgs& a, int dtype, int d) {
 namespace {
 
 // Tokens of a TMA box, or 0 where threads have to load: pages without runs of
-// 16 tokens, broadcast strides.
+// 8 tokens (a swizzle's rows), broadcast strides.
 int box_tokens(const PrefillArgs& a, int kv_dtype) {
     const int64_t most = int64_t(1) << 38;  // elements; the encoder takes strides below 2^40 bytes
-    if (a.page_size % 16 != 0 || a.num_pages <= 0 ||
+    if (a.page_size % 8 != 0 || a.num_pages <= 0 ||
         (a.kv_heads > 1 && (a.head_stride <= 0 || a.head_stride >= most)) ||
         (a.num_pages > 1 && (a.page_stride <= 0 || a.page_stride >= most)) || a.row_stride <= 0 ||
         a.row_stride >= most || (a.tokens > 1 && (a.q_stride <= 0 || a.q_stride >= most)))

@@ -12,12 +12,13 @@
 //  * A query tile is 128 rows of (new token, query head of the KV head), so that
 //    a K tile of 128 cached tokens serves every head that shares it, and the
 //    causal edge is 128 / group tokens wide.  Two query tiles share the K and V
-//    tiles (heads of 256: one), and the tensor cores work on one while the other
-//    is in its softmax.
+//    tiles, and the tensor cores work on one while the other is in its softmax;
+//    heads of 256 (whose two outputs TMEM does not hold) and few tokens over
+//    E4M3 caches have units of one, whose tokens two warpgroups share.
 //  * S[queries x tokens] = Q K^T from shared memory into TMEM; P goes back into
-//    the S columns as the A operand of O += P V, V an MN-major view of its tile.
-//    A thread per query row: no shuffle in the softmax, and P, O and the
-//    statistics of a row never leave their lane.
+//    TMEM as the A operand of O += P V, V an MN-major view of its tile.  A thread
+//    per query row: no shuffle in the softmax, and P, O and the statistics of a
+//    row never leave their lane.
 //  * Softmax against a reference maximum that moves only when a logit exceeds it
 //    by 2^kThresh, so that O is rescaled a few times a unit.
 //  * P is rounded once to the type of V's products: bf16, or fp16 raised by
@@ -25,12 +26,23 @@
 //    smaller ones 2^-36 of it.  The sums l are of unrounded weights, in fp32.
 //  * E4M3 caches become fp16 in shared memory (exact), bf16 queries fp16 of
 //    their row's largest magnitude 2^14 (elements down to 2^-28 of it exact).
-//  * Loads: 16-bit caches whose pages hold runs of 16 tokens by TMA; others and
-//    E4M3 by 128 threads, a batch of loads ahead of the stores.
+//  * Loads: caches whose pages hold runs of 8 tokens by TMA, E4M3 ones into a
+//    stage, from which four warps convert them; others by 128 threads, a batch of
+//    loads ahead of the stores.  K and V of a unit's first tile go ahead of its
+//    queries, and page numbers are looked up a tile ahead.
 //  * Entries of V that are not finite must not meet a weight of 0.  Where some
 //    query of the unit does not see some token of a tile, rows that no query
 //    sees become 0, and rows with entries that are not finite too; those are
 //    added to the queries that do see them, one by one.
+// Code is fetched like data: the kernel's is as large as the instruction cache,
+// and what a unit runs once (masks, plan, output) costs its fetch.  So whatever is
+// not a tile's main path is short, shared or rolled.
+//
+// Measured, 32/8 heads of 128 if nothing else is said: 2048 tokens over 32 K in
+// bf16 0.71 ms (1.5 PFLOP/s of 1.9 measured; the power cap lowers the clocks),
+// over 4 K 91 us, over 16 K of E4M3 432 us (1.2 PFLOP/s: the conversion), 16/2
+// heads of 256 over 8 K 225 us (1.07: rings of 1.25 tiles), 16 requests of 5
+// tokens over up to 8 K 63 us (4.5 TB/s of 6.8).
 // Every wait is bounded (HS_ERR_TIMEOUT in the status word on expiry).
 #pragma once
 
@@ -662,8 +674,9 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
 // A unit of one query tile (a head size of 256): each warpgroup has half of a
 // tile's tokens, and of the output's dims where it is changed, so that the rows'
 // softmax has all eight warps.  (By four, the other idle, it took longer than the
-// tile's products: 2048 tokens over 8 K of E4M3, 465 us, now 419.)  Two warps that share rows tell each other their
-// largest logits by a column of S, and so have one reference.
+// tile's products: 2048 tokens over 8 K of E4M3, 465 us, now 419.)  Two warps that
+// share rows tell each other their largest logits by a column of S, and so have
+// one reference.
 template <typename C>
 __device__ __forceinline__ void softmax_split_role(const Cta<C>& cx) {
     static_assert(C::NQ == 1, "one query tile");
@@ -977,7 +990,7 @@ __device__ __forceinline__ bool tma_role(const Cta<C>& cx, const CUtensorMap& qm
     const PrefillArgs& a = cx.a;
     Bars<C>& B = cx.B;
     const int lane = threadIdx.x & 31, bt = cx.ta.bt;
-    const int runs = kTile / bt;  // a power of two up to 8
+    const int bt_log = 31 - __clz(bt), runs = kTile >> bt_log;  // a power of two up to 16
     constexpr int kBoxes = C::kConvert ? 1 : C::kDims / 64;
     const uint32_t row_bytes = C::kConvert ? C::kDims : 128;
     const uint32_t box = uint32_t(bt) * row_bytes;
@@ -1030,13 +1043,11 @@ __device__ __forceinline__ bool tma_role(const Cta<C>& cx, const CUtensorMap& qm
             // (Read by the softmax of this tile, which the ring's units keep less
             // than kRing tiles behind.)
             if (lane < 4) {
-                uint32_t bits = 0;
-                if (bt >= 32) {
-                    bits = (got >> (lane * 32 / bt)) & 1u ? 0xffffffffu : 0u;
-                } else {  // 16
-                    if ((got >> (2 * lane)) & 1u) bits |= 0xffffu;
-                    if ((got >> (2 * lane + 1)) & 1u) bits |= 0xffff0000u;
-                }
+                // Runs as tokens, 32 of them a lane.
+                uint32_t bits = got >> ((lane * 32) >> bt_log);
+                if (bt >= 32) bits = 0u - (bits & 1u);
+                else if (bt == 16) bits = (bits & 1u) * 0xffffu + (bits >> 1 & 1u) * 0xffff0000u;
+                else bits = ((bits & 15u) * 0x00204081u & 0x01010101u) * 0xffu;
                 B.loaded[t & (C::kRing - 1)][lane] = bits;
             }
             if (lane == 4)
@@ -1461,7 +1472,7 @@ __device__ __forceinline__ bool convert_role(const Cta<C>& cx) {
     return ok;
 }
 
-// Loads by 128 threads: pages without runs of 16 tokens, broadcast strides.
+// Loads by 128 threads: pages without runs of 8 tokens, broadcast strides.
 template <typename C>
 __device__ __forceinline__ bool load_role(const Cta<C>& cx) {
     constexpr bool E4 = C::kE4;

@@ -678,8 +678,8 @@ class PagedBatch:
     `attend` rotates a layer's q and k, writes k and v into its cache
     (hs_rope_append) and attends to all that is cached (hs_paged_prefill).
 
-    `num_reqs` fixed places for requests of at most `max_len` tokens that share
-    `num_pages` pages (default: enough for all); `max_tokens` bounds a step's
+    `num_reqs` fixed places for requests of at most `max_len` tokens (made up to
+    whole pages) that share `num_pages` pages (default: enough for all); `max_tokens` bounds a step's
     new tokens.  The requests' tokens lie one after another in q, k and v, in the
     order of their places; rows behind the last one are not read.  No call
     reads device memory on the host, so that a step can be captured; `check`
@@ -712,6 +712,10 @@ class PagedBatch:
         num_pages = num_reqs * blocks if num_pages is None else num_pages
         if num_pages < 1 or num_pages * page_size >= 1 << 31:
             raise ValueError("num_pages: at least one, fewer than 2^31 tokens in all")
+        max_len = blocks * page_size
+        if max_len > 1 << 30 or max_tokens > 1 << 24 or (max_tokens + num_reqs) * heads >= 1 << 31:
+            raise ValueError("max_len: at most 2^30; max_tokens: at most 2^24, and with num_reqs "
+                             "fewer than 2^31 / heads")
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
             if t is not None and cache_dtype != torch.float8_e4m3fn:
                 raise ValueError(f"{name}: for E4M3 caches")

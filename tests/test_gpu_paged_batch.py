@@ -155,3 +155,23 @@ def test_drafts_taken_back_leave_no_trace():
 
     for a, c in zip(run(False), run(True)):
         assert torch.equal(a, c)
+
+
+def test_a_last_page_is_used_to_its_end():
+    """max_len 100 with pages of 16: 112 tokens are held and attended to."""
+    g = torch.Generator().manual_seed(1)
+    b = PagedBatch(num_reqs=1, heads=4, kv_heads=2, d=64, page_size=16, max_len=100,
+                   max_tokens=56, scale=0.125)
+    n = torch.tensor([56], dtype=torch.int32, device="cuda")
+    for _ in range(2):
+        x = torch.randn(1, 56, 8, 64, generator=g).to(BF).cuda()
+        b.step(n, x[:, :, :4], x[:, :, 4:6], x[:, :, 6:])
+    b.check()
+    ref, ref_lse, (tol, tol_lse), _ = step_ref.prefill(
+        b.q_rot, b.k_cache[0], b.v_cache[0], b.block_table, b.cu_new, b.attend_lens, b.scale)
+    assert b.seq_lens.tolist() == [112]
+    paged_ref.check(b.out[0].double(), ref, tol, "out")
+    paged_ref.check(b.lse[0].double(), ref_lse, tol_lse, "lse")
+    b.step(n.clamp(max=1), x[:, :, :4], x[:, :, 4:6], x[:, :, 6:])
+    with pytest.raises(hs.HSError):
+        b.check()

@@ -14,7 +14,8 @@ SHAPE = dict(num_reqs=3, heads=8, kv_heads=2, d=64, page_size=16, max_len=100, m
     dict(num_pages=0), dict(num_pages=1 << 27), dict(window=-1), dict(num_sinks=-1),
     dict(heads=258, kv_heads=2), dict(k_scale=torch.ones(1, 2)),
     dict(cache_dtype=torch.float8_e4m3fn, v_scale=torch.ones(2)),
-    dict(inv_freq=torch.ones(33)), dict(inv_freq=torch.ones(2, 2))])
+    dict(inv_freq=torch.ones(33)), dict(max_len=(1 << 30) + 1, num_pages=9),
+    dict(max_tokens=(1 << 24) + 1), dict(max_tokens=1 << 24, heads=128), dict(inv_freq=torch.ones(2, 2))])
 def test_bad_values(bad):
     with pytest.raises(ValueError):
         PagedBatch(**{**SHAPE, **bad})
@@ -44,3 +45,4 @@ def test_calls():
     with pytest.raises(ValueError):
         b.stop(3)
     b.check()
+    assert b.max_len == 112  # whole pages
