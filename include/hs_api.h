@@ -755,8 +755,8 @@ int hs_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_str
  *             elements apart.
  * cu_new      int32 [rows + 1]: not descending; entries outside [0, tokens] and
  *             descending ones are clipped and reported as HS_ERR_BAD_INDEX.
- *             q and out rows outside [cu_new[0], cu_new[rows]) are neither
- *             read nor written.
+ *             q rows outside [cu_new[0], cu_new[rows]) have no effect, whatever
+ *             they hold, and out rows there are not written.
  * seq_lens    int32 [rows]: T, the request's cached tokens with the new ones.
  *             Queries before position 0 (T < n) give out = 0, lse = -inf.
  * out         [tokens, heads, d] of q_dtype, packed; lse fp32 [tokens, heads]

@@ -1023,7 +1023,9 @@ __device__ __forceinline__ bool tma_role(const Cta<C>& cx, const CUtensorMap& qm
         // behind those logits, or for the converter, which begins with the queries.)
         constexpr int kAhead = kSubs == 1 ? 2 : 1;
         // Whether the lane's run of a tile is needed, and its page: looked up a tile
-        // ahead, for it takes as long as a small tile's copies.
+        // ahead, for it takes as long as a small tile's copies.  (Units that pass
+        // through a stage have the time, and were 5 to 10 % slower so.)
+        constexpr bool kLookAhead = !C::kConvert;
         bool next_wants = false;
         int next_page = -1;
         const auto look_up = [&](int i) {
@@ -1031,13 +1033,13 @@ __device__ __forceinline__ bool tma_role(const Cta<C>& cx, const CUtensorMap& qm
             next_wants = lane < runs && any_sees(a, s, tok, bt);
             if (next_wants) next_page = a.block_table[s.row * a.bt_stride + block_of(a, tok)];
         };
-        look_up(0);
+        if (kLookAhead) look_up(0);
         if (unit == 0) load_q();
         for (int i = 0; i < s.n && ok; ++i, ++t) {
+            if (!kLookAhead) look_up(i);
             const int t0 = token_of(s, i), tok = t0 + lane * bt;
             const int b = block_of(a, tok), page = next_page;
             const bool wants = next_wants, want = wants && page >= 0 && page < a.num_pages;
-            if (i + 1 < s.n) look_up(i + 1);
             if (wants && !want) bad = true;
             const uint32_t got = __ballot_sync(0xffffffffu, want);
             // (Read by the softmax of this tile, which the ring's units keep less
@@ -1078,6 +1080,7 @@ __device__ __forceinline__ bool tma_role(const Cta<C>& cx, const CUtensorMap& qm
                         tma_load(dst + lane * box + c * kBlk, u < kSubs ? &kmap : &vmap,
                                  u % kSubs * C::kDims + c * 64, at, s.kvh, page, full);
                 }
+                if (kLookAhead && u == 0 && i + 1 < s.n) look_up(i + 1);
                 if (i == 0 && u == kAhead - 1 && unit > 0) {
                     load_q();
                     if (!ok) {
