@@ -321,6 +321,9 @@ extern "C" int hs_paged_prefill(const void* q, int64_t q_stride, int32_t q_dtype
     a.part_o = reinterpret_cast<float*>(ws + w.o);
     a.shared = reinterpret_cast<SharedUnit*>(ws + w.shared);
     a.unit_rows = w.unit_rows;
+    // (E4M3: 64 requests of up to 48 tokens over up to 4 K 234 us with 256, 195 with
+    // 512; bf16: 8192 fresh tokens 382 us with 256, 392 with 512, 398 with 128.)
+    a.extra = kv_dtype == HS_E4M3 ? 512 : 256;
     const int rc = kv_dtype == HS_BF16   ? launch_bf16(a, d, bt, stream)
                    : kv_dtype == HS_FP16 ? launch_fp16(a, d, bt, stream)
                                          : launch_e4m3(a, d, bt, stream);

@@ -14,9 +14,6 @@ using hs_paged::kMaxRows;
 
 constexpr int kTile = 128;      // query rows and cached tokens of a tile
 constexpr int kMaxCtas = 1024;  // most CTAs of the attention kernel
-// Places (tokens' time) that a unit takes besides its tokens: its queries'
-// loads, the first product and the output.
-constexpr int kExtra = 256;
 
 // A unit whose tokens several CTAs share, written by the CTA of its first part.
 struct SharedUnit {
@@ -55,6 +52,9 @@ struct PrefillArgs {
     float* part_o;       // [2 * ctas][D / 8][unit rows][8]
     SharedUnit* shared;  // [ctas]
     int32_t unit_rows;   // 128 or 256
+    // Places (tokens' time) that a unit takes besides its tokens: its queries'
+    // loads, the first product and the output.
+    int32_t extra;
     int32_t* status;
 };
 
@@ -62,7 +62,7 @@ struct PrefillArgs {
 // request's new tokens: one or two query tiles, each 128 rows of (token, query
 // head of the KV head).  Units stand one after another (requests, their KV
 // heads, their blocks), each over as many places as cached tokens it sees and
-// kExtra more, and the places are dealt to the CTAs in equal contiguous runs;
+// a.extra more, and the places are dealt to the CTAs in equal contiguous runs;
 // a unit whose places several CTAs got is cut at tiles of 128 cached tokens
 // and merged.  So ragged batches, causal blocks of growing length and one
 // long context load every SM alike.
@@ -90,7 +90,7 @@ __device__ __forceinline__ int blocks_of(const PrefillArgs& a, int n) {
 // count).
 __device__ __forceinline__ int64_t places(const PrefillArgs& a, const Request& x, int b) {
     const int64_t base = max(x.T - x.n, 0), tb = a.tb, n = b;
-    int64_t sum = n * (kExtra + base) + tb * (n * (n + 1) / 2);
+    int64_t sum = n * (a.extra + base) + tb * (n * (n + 1) / 2);
     if (a.window > 0) {
         const int64_t c0 = base + 1 - a.window;
         const int64_t i0 = c0 > 0 ? 0 : int(-c0) / a.tb + 1;  // the first block that starts behind 0
@@ -105,7 +105,7 @@ __device__ __forceinline__ int64_t places_of(const PrefillArgs& a, const Request
 __device__ __forceinline__ int cost_of(const PrefillArgs& a, const Request& x, int b) {
     const int base = max(x.T - x.n, 0);
     const int lo = a.window > 0 ? max(0, base + b * a.tb + 1 - a.window) : 0;
-    return kExtra + base + (b + 1) * a.tb - lo;
+    return a.extra + base + (b + 1) * a.tb - lo;
 }
 // First place of CTA c's run: per = total / ctas each, and one more for the first
 // `rest` of them.
