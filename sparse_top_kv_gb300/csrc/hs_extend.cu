@@ -18,13 +18,14 @@
 // each sum 7.1), 512 requests of up to 1024 tokens 10.3 (15.9).
 #include "hs_common.cuh"
 #include "hs_pair.cuh"
+#include "hs_plan.h"
 
 namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kMaxRows = 4096;
 constexpr int kAtOnce = 4;                 // tokens of a thread whose pages are read together
-constexpr int kMany = 1 << 30;             // prefix sums stop here (saturating)
+constexpr int kMany = 1 << 30;             // most pages or tokens of a call
 constexpr int kMaxCluster = 8;
 
 struct ExtendArgs {
@@ -47,10 +48,11 @@ struct ExtendArgs {
     int32_t* status;
 };
 
-__device__ __forceinline__ int sat_add(int a, int b) { return min(a + b, kMany); }
+using hs_plan::kSatMax;
+using hs_plan::sat_add;
 
 // Exclusive saturating prefix sums over the block of M lists of PER consecutive
-// values of each thread (each in [0, kMany]); total: the block's.
+// values of each thread (each in [0, kSatMax]); total: the block's.
 template <int M, int PER>
 __device__ __forceinline__ void scan_rows(int (&v)[M][PER], int (&total)[M], int (*scratch)[32]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -166,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const ExtendArgs a)
         } else {
             held[i] = max(held[i], 0);
         }
-        own_ask[i] = min(max(n[i], 0), kMany);
+        own_ask[i] = min(max(n[i], 0), kSatMax);
         own_back[i] = 0;
         if (n[i] < 0 && held[i] > 0 && !odd)
             own_back[i] = pages_of(held[i]) - pages_of(max(0, held[i] + max(n[i], -held[i])));
