@@ -689,9 +689,13 @@ int hs_evict(const float* score, int64_t score_stride, const int32_t* positions,
  * slot, row_req, positions  int32 [max_tokens], by token: block_table[r][t /
  *             page_size] * page_size + t % page_size, r and t; -1 for tokens
  *             of requests that are not served and behind the last request.
- * A ring that cannot be (ends out of order, more pages than num_pages), a
- * length past the table and a page outside [0, num_pages) leave the request as
- * it is and are reported as HS_ERR_BAD_INDEX.  Out arrays must not overlap in
+ * A ring that cannot be (ends out of order, more pages than num_pages, less room
+ * than the pages given back need) and a length past the table leave the requests
+ * that they concern as they are and are reported as HS_ERR_BAD_INDEX.  Pages are
+ * passed on as they stand: one outside [0, num_pages), of the table or of the
+ * ring, does not keep a request from growing or giving up; a new token that lies
+ * in it has no slot (-1), and that, or giving it back, is reported as
+ * HS_ERR_BAD_INDEX.  Out arrays must not overlap in
  * arrays other than as stated.  Bit-exact and independent of thread scheduling.
  * HS_ERR_CAPACITY: rows > 4096, num_pages, max_tokens or max_blocks * page_size
  * > 2^30, num_pages * page_size >= 2^31.

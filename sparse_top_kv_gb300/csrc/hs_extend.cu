@@ -240,8 +240,9 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const ExtendArgs a)
     }
     for (int i = first; i < given; i += step) {
         const int r = find(to, a.rows, i);
-        a.ring[ring_at(give_at, i)] =
-            a.table[r * a.bt_stride + pages_of(lens[r] + grow[r]) + i - to[r]];
+        const int page = a.table[r * a.bt_stride + pages_of(lens[r] + grow[r]) + i - to[r]];
+        if (page < 0 || page >= a.pages) hs::set_status(a.status, HS_ERR_BAD_INDEX);
+        a.ring[ring_at(give_at, i)] = page;
     }
     // The pages of kAtOnce tokens are read together.  (Four neighbouring tokens
     // with one search and wide stores: no faster.)
