@@ -696,7 +696,9 @@ int hs_evict(const float* score, int64_t score_stride, const int32_t* positions,
  * ring, does not keep a request from growing or giving up; a new token that lies
  * in it has no slot (-1), and that, or giving it back, is reported as
  * HS_ERR_BAD_INDEX.  Out arrays must not overlap in
- * arrays other than as stated.  Bit-exact and independent of thread scheduling.
+ * arrays other than as stated.  Bit-exact and independent of thread scheduling;
+ * of several errors of a call *status reports HS_ERR_BAD_INDEX of a ring or a
+ * length, then HS_ERR_CAPACITY, then HS_ERR_BAD_INDEX of a page.
  * HS_ERR_CAPACITY: rows > 4096, num_pages, max_tokens or max_blocks * page_size
  * > 2^30, num_pages * page_size >= 2^31.
  * ------------------------------------------------------------------------- */

@@ -121,7 +121,9 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const ExtendArgs a)
     int* lens = to + a.rows;                // tokens held before
     int* grow = lens + a.rows;              // tokens granted; < 0: given up
     __shared__ int scratch[4][32];          // (a row for each of the kernel's exchanges)
+    __shared__ int found;                   // 1: a request was refused, 2: a state that cannot be
     const int tid = threadIdx.x, B = a.page_size;
+    if (tid == 0) found = 0;
     const int cl = gridDim.x, rank = blockIdx.x;
     // Pages of n tokens, and the page of token n.
     const auto page_of = [&](int n) { return a.page_shift >= 0 ? n >> a.page_shift : n / B; };
@@ -209,15 +211,19 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const ExtendArgs a)
                            : (!odd && given >= own_back[i] ? max(n[i], -max(held[i], 0)) : 0);
         if (served && own_need[i] > 0) last = max(last, need[0][i] + own_need[i]);
     }
-    if (rank == 0) {
-        if (bad) hs::set_status(a.status, HS_ERR_BAD_INDEX);
-        if (refused) hs::set_status(a.status, HS_ERR_CAPACITY);
-    }
     // Pages taken in all: what the last served request's share ends with.
     last = int(__reduce_max_sync(0xffffffffu, unsigned(last)));
+    if (bad || refused) atomicMax(&found, bad ? 2 : 1);
     if ((tid & 31) == 0) scratch[3][tid >> 5] = last;
     __syncthreads();
     const int grown = int(__reduce_max_sync(0xffffffffu, unsigned(scratch[3][tid & 31])));
+    // One code a call, whichever threads find what: that of the lengths and the ring,
+    // then refusals, then pages that are none.
+    if (rank == 0 && tid == 0 && found != 0)
+        hs::set_status(a.status, found == 2 ? HS_ERR_BAD_INDEX : HS_ERR_CAPACITY);
+    const auto no_page = [&] {
+        if (found == 0) hs::set_status(a.status, HS_ERR_BAD_INDEX);
+    };
     // Every CTA has read the lengths and the ring's ends.
     if (cl > 1) hs::pair::cluster_sync();
 
@@ -241,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const ExtendArgs a)
     for (int i = first; i < given; i += step) {
         const int r = find(to, a.rows, i);
         const int page = a.table[r * a.bt_stride + pages_of(lens[r] + grow[r]) + i - to[r]];
-        if (page < 0 || page >= a.pages) hs::set_status(a.status, HS_ERR_BAD_INDEX);
+        if (page < 0 || page >= a.pages) no_page();
         a.ring[ring_at(give_at, i)] = page;
     }
     // The pages of kAtOnce tokens are read together.  (Four neighbouring tokens
@@ -268,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const ExtendArgs a)
             const int64_t t = t0 + int64_t(k) * step;
             if (t >= a.max_tokens) break;
             const bool good = page[k] >= 0 && page[k] < a.pages;
-            if (req[k] >= 0 && !good) hs::set_status(a.status, HS_ERR_BAD_INDEX);
+            if (req[k] >= 0 && !good) no_page();
             a.slot[t] = good ? page[k] * B + in[k] : -1;
             a.row_req[t] = req[k];
             a.positions[t] = pos[k];

@@ -53,3 +53,29 @@ def test_many_pages_by_several_ctas():
     got, status = check(new, [32 if r % 2 else 31 for r in range(rows)], table, ring, [0, rows], page,
                         4000)
     assert status == 6 and got["ends"] == [0, rows + rows // 2 * 8]
+
+
+@pytest.mark.parametrize("first", [False, True])
+@pytest.mark.parametrize("rows", [2, 33, 1000, 4096])
+@pytest.mark.parametrize("max_tokens", [40, 4000])
+def test_one_code_for_several_errors(rows, first, max_tokens):
+    """A length past its table, a refused request and a bad page in one call: the
+    code does not depend on which thread finds which, or when."""
+    def call(at_length, at_refused, at_page):
+        table = [[r, -1] for r in range(rows)]
+        new, lens = [0] * rows, [1] * rows
+        if at_refused is not None:
+            new[at_refused] = 9
+        if at_page is not None:
+            new[at_page], table[at_page][0] = 1, -7
+        if at_length is not None:
+            lens[at_length] = 5
+        ring = [rows, rows + 1] + [-1] * rows
+        return extend(new, lens, table, ring, [0, 2], 2, max_tokens, True)[-1]
+
+    a, b = (0, rows - 1) if first else (rows - 1, 0)
+    for _ in range(20):
+        assert call(a, b, None) == 6 and call(None, a, b) == 3 and call(None, None, a) == 6
+        assert call(None, a, None) == 3 and call(None, None, None) == 0
+        if rows > 2:
+            assert call(a, b, rows // 2) == 6
