@@ -759,8 +759,9 @@ int hs_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_str
  *
  * q           [tokens, heads, d] of q_dtype, heads packed, tokens q_stride
  *             elements apart.
- * cu_new      int32 [rows + 1]: not descending; entries outside [0, tokens] and
- *             descending ones are clipped and reported as HS_ERR_BAD_INDEX.
+ * cu_new      int32 [rows + 1]: not descending; entries outside [0, tokens] are
+ *             clipped and reported as HS_ERR_BAD_INDEX.  A list that descends is
+ *             reported likewise, and out and lse stay as they were.
  *             q rows outside [cu_new[0], cu_new[rows]) have no effect, whatever
  *             they hold, and out rows there are not written.
  * seq_lens    int32 [rows]: T, the request's cached tokens with the new ones.

@@ -1620,10 +1620,16 @@ __device__ __forceinline__ bool plan_role(const Cta<C>& cx) {
     constexpr uint32_t kAll = 0xffffffffu;
     // The run: the call's places, dealt to the CTAs, a lane per request.
     int64_t total = 0;
+    bool falls = false;
 #pragma unroll 2
-    for (int r = lane; r < a.rows; r += 32) total += places_of(a, request_of(a, r));
+    for (int r = lane; r < a.rows; r += 32) {
+        total += places_of(a, request_of(a, r));
+        falls |= a.cu_new[r + 1] < a.cu_new[r];
+    }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(kAll, total, d);
+    // Requests that overlap would both write their rows: none does.
+    if (__any_sync(kAll, falls)) total = 0;
     const int64_t per = quotient(total, a.ctas);
     const int rest = int(total - per * a.ctas);
     const int64_t place0 = run_begin(per, rest, blockIdx.x);
