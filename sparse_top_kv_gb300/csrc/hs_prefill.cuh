@@ -4,6 +4,7 @@
 #pragma once
 
 #include "hs_paged.cuh"
+#include "hs_plan.h"
 
 namespace hs_prefill {
 
@@ -23,6 +24,7 @@ struct SharedUnit {
     int32_t slot;   // of that part
     int32_t last;   // the last run with a part of it
     int32_t first, tokens, kvh;
+    int32_t blind;  // whether the call has queries that attend to nothing (alike in all)
 };
 
 struct PrefillArgs {
@@ -65,18 +67,12 @@ struct PrefillArgs {
 // a.extra more, and the places are dealt to the CTAs in equal contiguous runs;
 // a unit whose places several CTAs got is cut at tiles of 128 cached tokens
 // and merged.  So ragged batches, causal blocks of growing length and one
-// long context load every SM alike.
+// long context load every SM alike.  Queries that attend to nothing are in no unit:
+// the kernel that merges writes their zeros.
 
-// Where request r's new tokens stand, and its cached tokens.
-struct Request {
-    int first, n, T;
-};
+using hs_plan::Request;
 __device__ __forceinline__ Request request_of(const PrefillArgs& a, int r) {
-    Request x;
-    x.first = min(max(a.cu_new[r], 0), a.tokens);
-    x.n = max(0, min(a.cu_new[r + 1], a.tokens) - x.first);
-    x.T = min(max(a.seq_lens[r], 0), a.max_len);
-    return x;
+    return hs_plan::request(a.cu_new[r], a.cu_new[r + 1], a.seq_lens[r], a.tokens, a.max_len);
 }
 __device__ __forceinline__ int block_of(const PrefillArgs& a, int t) {
     return a.page_shift >= 0 ? t >> a.page_shift : t / a.page_size;
@@ -84,28 +80,16 @@ __device__ __forceinline__ int block_of(const PrefillArgs& a, int t) {
 __device__ __forceinline__ int blocks_of(const PrefillArgs& a, int n) {
     return (n + a.tb - 1) / a.tb;
 }
-// Places of the first b blocks of a request, in closed form: block i sees up to
-// position base + (i + 1) tb and, with a window, from base + i tb + 1 - window
-// on (the grid of tiles, the sinks and a last block that is not full do not
-// count).
+// Places of the first b blocks of a request.
 __device__ __forceinline__ int64_t places(const PrefillArgs& a, const Request& x, int b) {
-    const int64_t base = max(x.T - x.n, 0), tb = a.tb, n = b;
-    int64_t sum = n * (a.extra + base) + tb * (n * (n + 1) / 2);
-    if (a.window > 0) {
-        const int64_t c0 = base + 1 - a.window;
-        const int64_t i0 = c0 > 0 ? 0 : int(-c0) / a.tb + 1;  // the first block that starts behind 0
-        if (n > i0) sum -= (n - i0) * c0 + tb * (n * (n - 1) / 2 - i0 * (i0 - 1) / 2);
-    }
-    return sum;
+    return hs_plan::places_of_blocks(x, a.tb, a.window, a.extra, b);
 }
 __device__ __forceinline__ int64_t places_of(const PrefillArgs& a, const Request& x) {
     return x.n > 0 ? places(a, x, blocks_of(a, x.n)) * a.kv_heads : 0;
 }
 // Places of one block.
 __device__ __forceinline__ int cost_of(const PrefillArgs& a, const Request& x, int b) {
-    const int base = max(x.T - x.n, 0);
-    const int lo = a.window > 0 ? max(0, base + b * a.tb + 1 - a.window) : 0;
-    return a.extra + base + (b + 1) * a.tb - lo;
+    return hs_plan::places_of_block(x, a.tb, a.window, a.extra, b);
 }
 // First place of CTA c's run: per = total / ctas each, and one more for the first
 // `rest` of them.

@@ -1610,26 +1610,28 @@ __device__ __forceinline__ bool load_role(const Cta<C>& cx) {
 }
 
 // --------------------------------- units ----------------------------------
-// Walks the run's units; writes zeros where a unit's queries see nothing.
+// Walks the run's units.
 template <typename C>
 __device__ __forceinline__ bool plan_role(const Cta<C>& cx) {
-    constexpr int D = C::kD;
     const PrefillArgs& a = cx.a;
     Bars<C>& B = cx.B;
     const int lane = threadIdx.x & 31;
     constexpr uint32_t kAll = 0xffffffffu;
     // The run: the call's places, dealt to the CTAs, a lane per request.
     int64_t total = 0;
-    bool falls = false;
+    bool falls = false, blind = false;
 #pragma unroll 2
     for (int r = lane; r < a.rows; r += 32) {
-        total += places_of(a, request_of(a, r));
+        const Request x = request_of(a, r);
+        total += places_of(a, x);
+        blind |= x.blind > 0;
         falls |= a.cu_new[r + 1] < a.cu_new[r];
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(kAll, total, d);
     // Requests that overlap would both write their rows: none does.
-    if (__any_sync(kAll, falls)) total = 0;
+    falls = __any_sync(kAll, falls);
+    if (falls) total = 0;
     const int64_t per = quotient(total, a.ctas);
     const int rest = int(total - per * a.ctas);
     const int64_t place0 = run_begin(per, rest, blockIdx.x);
@@ -1638,6 +1640,7 @@ __device__ __forceinline__ bool plan_role(const Cta<C>& cx) {
     int64_t start = 0;
     int row = 0, kvh = 0, block = 0, unit = 0;
     SharedUnit shared{};
+    shared.blind = __any_sync(kAll, blind) && !falls;
     if (place0 < place1) {
         for (int64_t before = 0;; row += 32) {
             const int r = row + lane;
@@ -1695,7 +1698,7 @@ __device__ __forceinline__ bool plan_role(const Cta<C>& cx) {
             s.first = x.first + block * a.tb;
             s.m = min(a.tb, x.n - block * a.tb);
             s.p0 = x.T - x.n + block * a.tb;
-            const int hi = max(0, s.p0 + s.m);  // tokens up to the last query's own
+            const int hi = s.p0 + s.m;  // tokens up to the last query's own
             const int lo = a.window > 0 ? max(0, s.p0 + 1 - a.window) : 0;
             s.tw = min(lo, hi) / kTile;
             const int sc = a.window > 0 ? min(a.sinks, lo) : 0;
@@ -1722,14 +1725,6 @@ __device__ __forceinline__ bool plan_role(const Cta<C>& cx) {
                     }
                 }
                 publish(s);
-            } else if (nt == 0 && place0 <= start) {
-                // Nothing is attended to: zeros.
-                for (int r = lane; r < s.m * a.group; r += 32) {
-                    const int64_t qh = int64_t(s.first + r / a.group) * a.heads + kvh * a.group + r % a.group;
-                    for (int i = 0; i < D / 8; ++i)
-                        static_cast<uint4*>(a.out)[qh * (D / 8) + i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (a.lse != nullptr) a.lse[qh] = -CUDART_INF_F;
-                }
             }
             start += cost;
             if (start >= place1) break;
@@ -1737,7 +1732,7 @@ __device__ __forceinline__ bool plan_role(const Cta<C>& cx) {
             block = 0;
             if (++kvh < a.kv_heads) continue;
             kvh = 0;
-            do {  // the next request with a new token; there is one
+            do {  // the next request with a query that attends; there is one
                 if (++row >= a.rows) break;
                 x = request_of(a, row);
             } while (x.n == 0);
