@@ -1036,9 +1036,11 @@ def rope_frequencies(rot, base=10000.0, *, scaling=None, factor=1.0, original_le
 
     scaling "linear": positions divided by `factor`; "ntk": the base grown so
     that the slowest pair turns `factor` times slower and the fastest stays;
-    "yarn": pairs that turn fewer than `slow_turns` times over `original_len`
-    tokens are slowed by `factor`, those that turn more than `fast_turns` times
-    not at all, linearly between, and attention sharpened by 0.1 ln(factor) + 1."""
+    "yarn": between the pairs that turn `fast_turns` and `slow_turns` times over
+    `original_len` tokens (rounded outwards to whole pairs) frequencies go over
+    from the unchanged ones to those divided by `factor`, linearly in the pair's
+    index, as checkpoints of that method are trained (its paper's text has the
+    ramp in turns); attention sharpened by 0.1 ln(factor) + 1."""
     if rot < 0 or rot % 2:
         raise ValueError("rot: even, not negative")
     if factor <= 0 or base <= 0:
@@ -1052,10 +1054,16 @@ def rope_frequencies(rot, base=10000.0, *, scaling=None, factor=1.0, original_le
         return inv / factor, 1.0
     if scaling != "yarn":
         raise ValueError(f"scaling: None, 'linear', 'ntk' or 'yarn', got {scaling!r}")
-    if original_len is None or original_len <= 0 or not slow_turns < fast_turns:
-        raise ValueError("yarn: needs original_len > 0 and slow_turns < fast_turns")
-    turns = original_len * inv / (2 * math.pi)
-    keep = ((turns - slow_turns) / (fast_turns - slow_turns)).clamp(0, 1)
+    if original_len is None or original_len <= 0 or not 0 < slow_turns < fast_turns or base <= 1:
+        raise ValueError("yarn: needs original_len > 0, 0 < slow_turns < fast_turns and base > 1")
+
+    def pair_of(turns):  # (not whole) that turns so often over original_len tokens
+        return rot / 2 * math.log(original_len / (2 * math.pi * turns)) / math.log(base)
+
+    low = max(math.floor(pair_of(fast_turns)), 0)
+    high = min(math.ceil(pair_of(slow_turns)), rot - 1)
+    ramp = (torch.arange(rot // 2, dtype=torch.float64) - low) / max(high - low, 1e-3)
+    keep = 1 - ramp.clamp(0, 1)
     return inv * keep + inv / factor * (1 - keep), max(1.0, 0.1 * math.log(factor) + 1.0)
 
 
