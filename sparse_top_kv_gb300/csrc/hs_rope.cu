@@ -5,8 +5,8 @@
 //   (a cos - b sin, a sin + b cos) * mscale,  angle = 2 pi frac(p * turns / 2^64),
 // with turns the pair's turns per position as a 64-bit binary fraction.  The
 // product wraps exactly at whole turns, so far positions lose nothing: an
-// angle is off by 2 pi (p 2^-65 + 2^-26) at most, by cospi / sinpi of its
-// fp32 rounding, whatever p.
+// angle is off by 2 pi (p 2^-65 + 2^-26) at most, of the table's rounding to the
+// nearest 2^-64 and of the angle's to fp32 for cospi / sinpi.
 //
 // Every element is read once and written once with a handful of operations,
 // so HBM bounds it.  A CTA takes a token: a thread keeps one place of 16 elements

@@ -1067,13 +1067,35 @@ def rope_frequencies(rot, base=10000.0, *, scaling=None, factor=1.0, original_le
     return inv * keep + inv / factor * (1 - keep), max(1.0, 0.1 * math.log(factor) + 1.0)
 
 
+def _inverse_tau():
+    """1 / (2 pi) times 2^192 (a float64 has 11 bits less than the table)."""
+    one = 1 << 256
+
+    def arctan(n):  # of 1 / n, times 2^256
+        total, term, k = 0, one // n, 1
+        while term:
+            total += term // k if k % 4 == 1 else -(term // k)
+            term, k = term // (n * n), k + 2
+        return total
+
+    pi = 4 * (4 * arctan(5) - arctan(239))  # off by less than 2^9 of 2^-256
+    return (one << 192) // (2 * pi)
+
+
 def rope_turns(inv_freq, device="cuda"):
     """The table that rope_append takes: frequencies [rot / 2] in radians per
-    position as int64 turns per position times 2^64."""
-    x = inv_freq.to("cpu", torch.float64) / (2 * math.pi)
-    x = x - torch.floor(x)
-    x = torch.where(x >= 0.5, x - 1.0, x)  # whole turns do not count; int64 is signed
-    return (x * 2.0 ** 64).to(torch.int64).to(device)
+    position as int64 turns per position times 2^64, rounded to the nearest (the
+    frequency is taken as the float64 that it is)."""
+    inv_freq = inv_freq.to("cpu", torch.float64)
+    if not torch.isfinite(inv_freq).all():
+        raise ValueError("inv_freq: finite")
+    inv_tau, table = _inverse_tau(), []
+    for f in inv_freq.tolist():
+        n, d = f.as_integer_ratio()
+        turns = ((n * inv_tau << 1) // (d << 128) + 1) >> 1  # times 2^64
+        turns &= (1 << 64) - 1  # whole turns do not count
+        table.append(turns - (1 << 64) if turns >> 63 else turns)  # int64 is signed
+    return torch.tensor(table, dtype=torch.int64, device=device)
 
 
 def rope_append(q, k, v, positions, slot, turns, k_cache, v_cache, *, interleaved=False,

@@ -1,6 +1,7 @@
 """The rotary tables (hs.rope_frequencies, hs.rope_turns) against their definitions
 (no GPU)."""
 import math
+from fractions import Fraction
 
 import pytest
 import torch
@@ -41,3 +42,33 @@ def test_yarn_refusals():
         with pytest.raises(ValueError):
             hs.rope_frequencies(**{**ok, **bad})
     assert hs.rope_frequencies(**{**ok, "rot": 0})[0].numel() == 0
+
+
+PI = Fraction(314159265358979323846264338327950288419716939937510582097494459230781640628620899,
+              10 ** 80)
+
+
+@pytest.mark.parametrize("inv", [
+    hs.rope_frequencies(128)[0], hs.rope_frequencies(64, 1e6)[0],
+    hs.rope_frequencies(64, scaling="linear", factor=32.0)[0],
+    torch.tensor([0.0, 1.0, -1.0, 3.0, 4.0, 6.0, 7.0, 100.0, 1e-300, 5e-324, 1e15, -0.3]),
+    torch.tensor([0.1, 2.5], dtype=torch.float32), torch.zeros(0)])
+def test_turns_are_rounded_at_64_bits(inv):
+    """Every entry is the nearest to its frequency's, so that the product with a
+    position, modulo whole turns, is off by half a unit of 2^-64 a position."""
+    table = hs.rope_turns(inv, "cpu")
+    assert table.dtype == torch.int64 and table.shape == inv.shape
+    for f, t in zip(inv.double().tolist(), table.tolist()):
+        exact = Fraction(f) / (2 * PI) * 2 ** 64
+        off = (t - exact) % 2 ** 64  # whole turns do not count
+        assert min(off, 2 ** 64 - off) <= Fraction(1, 2) + abs(exact) / 10 ** 60
+        for p in (1, 12345, 2 ** 30, 2 ** 31 - 1):
+            turns = Fraction(p * t, 2 ** 64) - Fraction(f) * p / (2 * PI)
+            off = turns % 1
+            assert min(off, 1 - off) <= Fraction(p, 2 ** 65) + p * abs(Fraction(f)) / 10 ** 60
+
+
+def test_turns_refuse_what_has_none():
+    for f in (math.inf, math.nan):
+        with pytest.raises(ValueError):
+            hs.rope_turns(torch.tensor([1.0, f]), "cpu")
