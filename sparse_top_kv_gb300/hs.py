@@ -688,12 +688,17 @@ def _check_i32(**values):
             raise ValueError(f"{name}: {v} is out of range")
 
 
-def _used_on(stream, *tensors):
-    """Tensors made here and used on a stream other than the current one: the
-    allocator must not hand their memory out before that stream is done."""
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(stream)
+def _empty(stream, *shape, returned=True, **opt):
+    """Memory made here for a call on `stream` (None: the current one): that stream's
+    own, as a block that the current stream has let go may still be in use there.  What
+    is returned is not handed out again before the current stream is done with it."""
+    if stream is None:
+        return torch.empty(*shape, **opt)
+    with torch.cuda.stream(stream):
+        t = torch.empty(*shape, **opt)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
 
 
 def _current_device(t, name):
@@ -782,14 +787,12 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, *, window=0,
     if v_scale is not None:
         v_scale_ptr = _vector(v_scale, _F, "v_scale", dev, kv_heads)
     if out is None:
-        out = torch.empty(rows, heads, d, dtype=qt, device=q.device)
-        _used_on(stream, out)
+        out = _empty(stream, rows, heads, d, dtype=qt, device=q.device)
     elif (out.dtype is not qt or out.get_device() != dev or out.shape != qshape
           or not out.is_contiguous()):
         _output(out, qt, "out", dev, qshape)
     if lse is None:
-        lse = torch.empty(rows, heads, dtype=_F, device=q.device)
-        _used_on(stream, lse)
+        lse = _empty(stream, rows, heads, dtype=_F, device=q.device)
     elif (lse.dtype is not _F or lse.get_device() != dev or lse.shape != (rows, heads)
           or not lse.is_contiguous()):
         _output(lse, _F, "lse", dev, (rows, heads))
@@ -819,8 +822,7 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale, *, window=0,
                                          num_sinks=num_sinks, with_score=score is not None)
         if n < 0:
             break
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
-        _used_on(stream, workspace)
+        workspace = _empty(stream, max(n, 1), returned=False, dtype=torch.uint8, device=q.device)
     if rc != HS_OK:
         raise HSError("hs_paged_decode", rc)
     return out, lse
@@ -856,9 +858,8 @@ def _evict_args(score, seq_lens, budget, max_len, recent, num_sinks, positions, 
     if moves is None:
         cap = max(0, min(budget, max_len - budget))
         i32 = dict(dtype=_I, device=score.device)
-        moves = (torch.empty(rows, cap, **i32), torch.empty(rows, cap, **i32),
-                 torch.empty(rows, **i32))
-        _used_on(stream, *moves)
+        moves = (_empty(stream, rows, cap, **i32), _empty(stream, rows, cap, **i32),
+                 _empty(stream, rows, **i32))
     src, dst, count = moves
     shape = src.shape
     if len(shape) != 2 or shape[0] != rows:
@@ -996,21 +997,17 @@ def paged_extend(new_lens, seq_lens, block_table, free_ring, ring_pos, page_size
         raise ValueError("new_lens: [rows]; block_table: [rows, blocks]; free_ring: [num_pages]")
     rows, pages = new_lens.shape[0], free_ring.shape[0]
     i64 = torch.int64
-    given = lens_out, attend_lens, ring_out, cu_new, slot, row_req, positions
     opt = dict(dtype=_I, device=new_lens.device)
     if lens_out is None:
         lens_out = seq_lens
     if ring_out is None:
         ring_out = ring_pos
     if attend_lens is None:
-        attend_lens = torch.empty(rows, **opt)
+        attend_lens = _empty(stream, rows, **opt)
     if cu_new is None:
-        cu_new = torch.empty(rows + 1, **opt)
-    slot, row_req, positions = (torch.empty(max_tokens, **opt) if t is None else t
+        cu_new = _empty(stream, rows + 1, **opt)
+    slot, row_req, positions = (_empty(stream, max_tokens, **opt) if t is None else t
                                 for t in (slot, row_req, positions))
-    _used_on(stream, *(t for t, g in zip((lens_out, attend_lens, ring_out, cu_new, slot, row_req,
-                                          positions), given)
-                       if g is None and t is not seq_lens and t is not ring_pos))
     table, table_stride = _matrix(block_table, _I, "block_table", dev, rows, 0)
     rc = lib().hs_paged_extend(
         _vector(new_lens, _I, "new_lens", dev, rows), _vector(seq_lens, _I, "seq_lens", dev, rows),
@@ -1134,8 +1131,7 @@ def rope_append(q, k, v, positions, slot, turns, k_cache, v_cache, *, interleave
     if q is not None:
         q_ptr, q_stride = _token_rows(q, "q", dev)
         if q_out is None:
-            q_out = torch.empty(n, heads, d, dtype=dtype, device=q.device)
-            _used_on(stream, q_out)
+            q_out = _empty(stream, n, heads, d, dtype=dtype, device=q.device)
         qo_ptr, qo_stride = _token_rows(q_out, "q_out", dev, dtype, q.shape)
     elif q_out is not None:
         raise ValueError("q_out: needs q")
@@ -1233,10 +1229,9 @@ def paged_prefill(q, k_cache, v_cache, block_table, cu_new, seq_lens, scale, *, 
               _vector(v_scale, _F, "v_scale", dev, kv_heads))
     made = []
     if out is None:
-        made.append(out := torch.empty(n, heads, d, dtype=q.dtype, device=q.device))
+        made.append(out := _empty(stream, n, heads, d, dtype=q.dtype, device=q.device))
     if lse is None:
-        made.append(lse := torch.empty(n, heads, dtype=_F, device=q.device))
-    _used_on(stream, *made)
+        made.append(lse := _empty(stream, n, heads, dtype=_F, device=q.device))
     with torch.cuda.stream(stream):  # the call's own: the kernel follows
         for t in made:
             t.zero_()
@@ -1262,8 +1257,8 @@ def paged_prefill(q, k_cache, v_cache, block_table, cu_new, seq_lens, scale, *, 
                                              num_sinks=num_sinks)
         if need < 0:
             break
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
-        _used_on(stream, workspace)
+        workspace = _empty(stream, max(need, 1), returned=False, dtype=torch.uint8,
+                           device=q.device)
     if rc != HS_OK:
         raise HSError("hs_paged_prefill", rc)
     return out, lse
