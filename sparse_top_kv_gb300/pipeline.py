@@ -757,7 +757,9 @@ class PagedBatch:
             num_sinks=num_sinks)), dtype=torch.uint8, device=dev)
         self.graph = None
 
-    def _check_rows(self, q, k, v):
+    def _check_rows(self, q, k, v, copied=False):
+        """Everything that the calls ask of a layer's rows (copied: of rows that are
+        copied first, from anywhere), so that a step has not grown when one refuses."""
         for name, t, heads in (("q", q, self.heads), ("k", k, self.kv_heads),
                                ("v", v, self.kv_heads)):
             shape = (self.max_tokens, heads, self.d)
@@ -765,6 +767,14 @@ class PagedBatch:
                 raise ValueError(f"{name}: expected {shape}, got {tuple(t.shape)}")
             if t.dtype != self.q_rot.dtype:
                 raise TypeError(f"{name}: expected {self.q_rot.dtype}, got {t.dtype}")
+            if copied:
+                continue
+            if t.device != self.q_rot.device:
+                raise ValueError(f"{name}: on {t.device}, expected {self.q_rot.device}")
+            if t.stride(2) != 1 or heads > 1 and t.stride(1) != self.d:
+                raise ValueError(f"{name}: heads must be packed")
+            if t.data_ptr() % 16 or self.max_tokens > 1 and t.stride(0) % 8:
+                raise ValueError(f"{name}: tokens must start on 16 bytes")
 
     def grow(self, new_lens):
         """Room for new_lens[r] more tokens of every request r (int32 [num_reqs] on
@@ -785,6 +795,9 @@ class PagedBatch:
         if not 0 <= layer < self.layers:
             raise ValueError(f"layer: 0 to {self.layers - 1}")
         self._check_rows(q, k, v)
+        return self._attend(layer, q, k, v)
+
+    def _attend(self, layer, q, k, v):
         scales = dict(k_scale=None if self.k_scale is None else self.k_scale[layer],
                       v_scale=None if self.v_scale is None else self.v_scale[layer])
         hs.rope_append(q, k, v, self.positions, self.slot, self.turns, self.k_cache[layer],
@@ -805,7 +818,7 @@ class PagedBatch:
             self._check_rows(*rows)
         self.grow(new_lens)
         for layer, rows in enumerate(zip(qs, ks, vs)):
-            self.attend(layer, *rows)
+            self._attend(layer, *rows)
         return self.out, self.lse
 
     def stop(self, r):
@@ -846,7 +859,11 @@ class PagedBatch:
         if not len(qs) == len(ks) == len(vs) == self.layers:
             raise ValueError(f"qs, ks, vs: {self.layers} layers")
         for rows in zip(qs, ks, vs):
-            self._check_rows(*rows)
+            self._check_rows(*rows, copied=True)
+        if tuple(new_lens.shape) != (self.num_reqs,):
+            raise ValueError(f"new_lens: expected {(self.num_reqs,)}, got {tuple(new_lens.shape)}")
+        if new_lens.is_floating_point() or new_lens.dtype == torch.bool:
+            raise TypeError(f"new_lens: expected torch.int32, got {new_lens.dtype}")
         self.graph_new.copy_(new_lens, non_blocking=True)
         for layer in range(self.layers):
             self.graph_q[layer].copy_(qs[layer], non_blocking=True)
