@@ -737,7 +737,8 @@ int hs_paged_extend(const int32_t* new_lens, const int32_t* seq_lens, int32_t* b
  * k_scale, v_scale  fp32 [kv_heads] or NULL (= 1); HS_E4M3 only: stored is the
  *             row divided by its head's scale, saturating at +-448 (NaN stays).
  * Computed in fp32 and rounded once, to nearest even.  16-byte aligned bases,
- * strides multiples of 16 bytes.  d a multiple of 8 up to 1024, rot even;
+ * strides multiples of 16 bytes; rows of q_out and of the caches that overlap are
+ * refused (HS_ERR_INVALID_ARG).  d a multiple of 8 up to 1024, rot even;
  * others HS_ERR_UNSUPPORTED.
  * ------------------------------------------------------------------------- */
 int hs_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,

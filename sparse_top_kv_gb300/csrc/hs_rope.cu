@@ -292,6 +292,11 @@ extern "C" int hs_rope_append(const void* q, int64_t q_stride, const void* k, in
         has_kv != (v != nullptr) ||
         (has_kv && (slot == nullptr || k_cache == nullptr || v_cache == nullptr || page_size <= 0)))
         return HS_ERR_INVALID_ARG;
+    // Rows that are written must not overlap.
+    if ((has_q && tokens > 1 && q_out_stride < int64_t(heads) * d) ||
+        (has_kv && ((num_pages > 1 && page_stride < d) || (page_size > 1 && row_stride < d) ||
+                    (kv_heads > 1 && head_stride < d))))
+        return HS_ERR_INVALID_ARG;
     const auto al = [](const void* p, uintptr_t n) {
         return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
     };
