@@ -772,16 +772,19 @@ int hs_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_str
  * The other arguments as for hs_paged_decode, workspace and status included;
  * a token counts as attended to where any query of the step attends to it.
  * What stands in places that a query does not attend to has no effect on it,
- * NaN and infinities included; attended entries that are not finite give
- * outputs of their own head that are not finite.
+ * NaN and infinities included.  Attended entries of V that are not finite, and
+ * of K where they make a logit NaN or +inf, give outputs of their own head that
+ * are not finite; a logit of -inf has no weight (out = 0, lse = -inf where a
+ * query has no other).
  * Weights are rounded to the type of the products: relative to a query's
  * largest weight, with 16-bit floats of 8 bits (bf16 caches) or of 11 bits
  * (fp16 and E4M3 caches, where those below 2^-24 keep 2^-35).  Results do not
  * depend on timing.
  * Supported: d 64, 128 or 256, at most 128 query heads on a KV head; others
- * HS_ERR_UNSUPPORTED.  rows <= 4096, heads <= 65536, max_len <= 2^30 and tokens
- * <= 2^24 (HS_ERR_CAPACITY above, or when the workspace is missing or too
- * small; the query gives -1 for sizes that are refused).
+ * HS_ERR_UNSUPPORTED.  rows <= 4096, heads <= 65536, max_len <= 2^30, tokens <=
+ * 2^24 and (tokens + rows) * heads < 2^31 (HS_ERR_CAPACITY above, or when the
+ * workspace is missing or too small; the query gives -1 for sizes that are
+ * refused).
  * ------------------------------------------------------------------------- */
 int64_t hs_paged_prefill_workspace_bytes(int32_t tokens, int32_t rows, int32_t heads,
                                          int32_t kv_heads, int32_t d, int32_t max_len,

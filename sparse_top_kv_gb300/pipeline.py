@@ -679,11 +679,11 @@ class PagedBatch:
     (hs_rope_append) and attends to all that is cached (hs_paged_prefill).
 
     `num_reqs` fixed places for requests of at most `max_len` tokens (made up to
-    whole pages) that share `num_pages` pages (default: enough for all); `max_tokens` bounds a step's
-    new tokens.  The requests' tokens lie one after another in q, k and v, in the
-    order of their places; rows behind the last one are not read.  No call
-    reads device memory on the host, so that a step can be captured; `check`
-    does, and raises what the steps so far have reported.
+    whole pages) that share `num_pages` pages (default: enough for all);
+    `max_tokens` bounds a step's new tokens.  The requests' tokens lie one after
+    another in q, k and v, in the order of their places; rows behind the last one
+    have no effect.  No call reads device memory on the host, so that a step can
+    be captured; `check` does, and raises what the steps so far have reported.
 
     cache_dtype: dtype or torch.float8_e4m3fn (with k_scale, v_scale fp32
     [layers, kv_heads]).  inv_freq, mscale: as hs.rope_frequencies gives them
@@ -790,8 +790,9 @@ class PagedBatch:
         """The new tokens' attention in one layer: q [max_tokens, heads, d], k and v
         [max_tokens, kv_heads, d] as the model's projections give them (tokens may
         be strided).  Returns (out [max_tokens, heads, d], lse fp32 [max_tokens,
-        heads]), the same tensors in every step; rows of tokens that are not
-        computed keep what an earlier step left there."""
+        heads]), the same tensors in every step; rows of a request that found no
+        room are 0 and -inf, those behind the last request's keep what an earlier
+        step left there."""
         if not 0 <= layer < self.layers:
             raise ValueError(f"layer: 0 to {self.layers - 1}")
         self._check_rows(q, k, v)
