@@ -16,10 +16,6 @@ Encode encoder();
 
 namespace hs_prefill {
 
-int launch_bf16(const PrefillArgs& a, int d, int bt, hs_stream_t stream);
-int launch_fp16(const PrefillArgs& a, int d, int bt, hs_stream_t stream);
-int launch_e4m3(const PrefillArgs& a, int d, int bt, hs_stream_t stream);
-
 namespace tc {
 int encode(CUtensorMap* m, int dtype, int dims, const void* base, const cuuint64_t* size,
            const cuuint64_t* stride, const cuuint32_t* box) {

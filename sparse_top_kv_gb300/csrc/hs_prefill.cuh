@@ -105,4 +105,10 @@ __device__ __forceinline__ int tile_at(int64_t at, int cost, int tiles) {
     return at <= 0 ? 0 : at >= cost ? tiles : int(quotient(at * tiles, cost));
 }
 
+// The attention kernel over a cache type; bt: tokens of a TMA box, or 0 where threads
+// load.
+int launch_bf16(const PrefillArgs& a, int d, int bt, hs_stream_t stream);
+int launch_fp16(const PrefillArgs& a, int d, int bt, hs_stream_t stream);
+int launch_e4m3(const PrefillArgs& a, int d, int bt, hs_stream_t stream);
+
 }  // namespace hs_prefill

@@ -671,10 +671,11 @@ __device__ __forceinline__ void softmax_role(const Cta<C>& cx) {
 }
 
 
-// A unit of one query tile (a head size of 256): each warpgroup has half of a
-// tile's tokens, and of the output's dims where it is changed, so that the rows'
-// softmax has all eight warps.  (By four, the other idle, it took longer than the
-// tile's products: 2048 tokens over 8 K of E4M3, 465 us, now 419.)  Two warps that
+// A unit of one query tile (a head size of 256, or few new tokens over an E4M3
+// cache): each warpgroup has half of a tile's tokens, and of the output's dims where
+// it is changed, so that the rows' softmax has all eight warps.  (By four, the other
+// idle, it took longer than the tile's products: 2048 tokens over 8 K of E4M3, heads
+// of 256, 465 us, now 419.)  Two warps that
 // share rows tell each other their largest logits by a column of S, and so have
 // one reference.
 template <typename C>
@@ -1904,9 +1905,5 @@ int launch_kind(const PrefillArgs& a, int d, int bt, hs_stream_t stream) {
 }
 
 }  // namespace tc
-
-int launch_bf16(const PrefillArgs& a, int d, int bt, hs_stream_t stream);
-int launch_fp16(const PrefillArgs& a, int d, int bt, hs_stream_t stream);
-int launch_e4m3(const PrefillArgs& a, int d, int bt, hs_stream_t stream);
 
 }  // namespace hs_prefill
