@@ -13,9 +13,9 @@
 // and of the pages that change hands, finding the request of each by bisection in
 // shared memory; a token in a fresh block reads its page from the ring, so
 // nothing waits for the table.  The cluster barrier between the two parts lets
-// lengths and ring be updated in place.  Measured: 64 requests of one token 4.8
+// lengths and ring be updated in place.  Measured: 64 requests of one token 4.7
 // us (with a 64-bit remainder per token, four requests to a thread and a scan for
-// each sum 7.1), 512 requests of up to 1024 tokens 10.3 (15.9).
+// each sum 7.1), 512 requests of up to 1024 tokens 10.4 (15.9).
 #include "hs_common.cuh"
 #include "hs_pair.cuh"
 #include "hs_plan.h"

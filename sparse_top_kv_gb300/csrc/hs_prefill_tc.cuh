@@ -38,11 +38,15 @@
 // and what a unit runs once (masks, plan, output) costs its fetch.  So whatever is
 // not a tile's main path is short, shared or rolled.
 //
-// Measured, 32/8 heads of 128 if nothing else is said: 2048 tokens over 32 K in
-// bf16 0.71 ms (1.5 PFLOP/s of 1.9 measured; the power cap lowers the clocks),
-// over 4 K 91 us, over 16 K of E4M3 432 us (1.2 PFLOP/s: the conversion), 16/2
-// heads of 256 over 8 K 225 us (1.07: rings of 1.25 tiles), 16 requests of 5
-// tokens over up to 8 K 63 us (4.5 TB/s of 6.8).
+// Measured, 32/8 heads of 128 if nothing else is said.  Over inputs that change from
+// call to call: 2048 tokens over 32 K in bf16 0.75 to 0.79 ms (1.4 PFLOP/s of 1.9
+// measured; the power cap lowers the clocks), 16 requests of 5 tokens over up to 8 K
+// 63 us (4.5 TB/s of 6.8), chunks of up to 512 tokens over up to 8 K of E4M3 200 us
+// (0.87 PFLOP/s: the conversion), 16/1 heads of 256 over up to 5 K 91 us (0.76: rings
+// of 1.25 tiles).  Replays of a captured graph over the same inputs: 2048 tokens over
+// 32 K 0.69 to 0.71 ms (1.5), over 4 K 91 us, over 16 K of E4M3 434 us (1.2), 16/2 heads
+// of 256 over 8 K 225 to 234 us (1.05).  (Here and below, figures of other sizes than the first four
+// are of replays.)
 // Every wait is bounded (HS_ERR_TIMEOUT in the status word on expiry).
 #pragma once
 

@@ -13,9 +13,11 @@
 // of the head for all its heads and moves 16-byte vectors, three rows of them
 // asked for before the token's position is known; meanwhile the threads make the
 // token's sines and cosines once, each for one pair, and pass them through shared
-// memory.  Measured: 8192 tokens of 32 + 8 heads of 128, 201 MB, 32.8 us (6.1
-// TB/s; without the rows ahead and with 128 threads 38.5), 4113 tokens of 16 + 4
-// heads over an E4M3 cache 11.1 us, one token 2.8 us.
+// memory.  Measured over inputs that change from call to call: 8192 tokens of 32 + 8
+// heads of 128, 201 MB, 33.4 us (6.0 TB/s), 4113 tokens of 16 + 4 heads over an E4M3
+// cache 14.5, one token 3.3; replays of a captured graph over the same inputs 32.8
+// (without the rows ahead and with 128 threads 38.5), 11.1 (46 MB: they stay in the
+// L2) and 2.8.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -27,7 +29,8 @@
 namespace {
 
 // Threads of a CTA: small CTAs keep more rows in flight on an SM; where there are
-// SMs to spare, a token has more of them (one token 2.8 us, by 64 threads 3.6).
+// SMs to spare, a token has more of them (one token 2.8 us, by 64 threads 3.6, the
+// same inputs again).
 constexpr int kThreads = 64, kManyThreads = 256;
 constexpr int kMaxDim = 1024;
 constexpr int kAhead = 3;  // rows of a thread in flight
